@@ -34,6 +34,15 @@ DSA_DEV_SMEM_LAYOUT = 8
 DSA_KEY_F32 = 0
 DSA_KEY_F16 = 1
 
+DSA_DT_F32 = 0
+DSA_DT_F16 = 1
+DSA_DT_BF16 = 2
+
+DSA_ROPE_NONE = 0
+DSA_ROPE_LINEAR = 1
+DSA_ROPE_NTK = 2
+DSA_ROPE_YARN = 3
+
 DSA_OP_K_APPEND = 0
 DSA_OP_INDEXER_SCORE = 1
 DSA_OP_TOPK = 2
@@ -43,6 +52,7 @@ DSA_OP_KPOOL = 5
 
 KPOOL = 4            # positions per pool of the kpool indexer
 KPOOL_ROW = 257      # fp16 values per packed indexer row: k | gate | valid
+Q8_ROW = 640         # codes per row of the 8-bit latent cache (512 without a tail)
 
 # Every symbol the header declares, with (restype, argtypes).
 _P = C.c_void_p
@@ -84,6 +94,12 @@ SIGNATURES = {
     "dsa_kpool_select": (_I, [_P, _P, _P, _P, _I64, _BP, _I, _I, _P, _P, _SZ, _P]),
     "dsa_decode_kpool": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _BP, _I, _I, _I, _F, _P, _P, _P, _P, _SZ,
                               _P]),
+    "dsa_rope_frequencies": (_I, [_I, C.c_double, _I, C.c_double, _I, C.c_double, C.c_double, _P, _P]),
+    "dsa_rope": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I, _I, _I, _I, _P, _P, _I, _P]),
+    "dsa_kv_append": (_I, [_P, _I64, _P, _I64, _I, _BP, _P, _P, _P, _P, _SZ, _P]),
+    "dsa_kv_append_q8": (_I, [_P, _I64, _P, _I64, _I, _BP, _P, _P, _P, _P, _P, _SZ, _P]),
+    "dsa_kv_read_q8": (_I, [_P, _P, _I, _BP, _P, _P, _I, _I64, _P, _SZ, _P]),
+    "dsa_sparse_mla_attn_q8": (_I, [_P, _P, _P, _P, _BP, _P, _P, _I, _I, _F, _P, _I, _P, _P, _SZ, _P]),
     "dsa_version": (_I, []),
 }
 
@@ -447,6 +463,221 @@ def dsa_decode_kpool(k_new, gate_new, ape, q_idx, w, q_lat, idx_rows, pool_keys,
                                   _ptr(idx_rows), _ptr(pool_keys), pool_keys.shape[0], _ptr(kv_latent), C.byref(d),
                                   q_idx.shape[1], q_lat.shape[1], top_k, sm_scale, _ptr(out), _ptr(lse),
                                   _ptr(idx_out), _ptr(ws), ws.numel(), _stream(stream)), "dsa_decode_kpool")
+
+
+class dsa_rope_t(C.Structure):
+    _fields_ = [("inv_freq", _P), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("scale", C.c_float)]
+
+
+_ROPE_SCALING = {"none": DSA_ROPE_NONE, "linear": DSA_ROPE_LINEAR, "ntk": DSA_ROPE_NTK, "yarn": DSA_ROPE_YARN}
+
+
+@dataclass
+class Rope:
+    """A rotation (dsa_rope_t): pair j of a token at position p turns by
+    p * inv_freq[j] and is multiplied by scale."""
+    inv_freq: object       # float64 CUDA [rot_dim / 2], radians per position
+    interleaved: bool      # pairs (2j, 2j+1), else (j, j + rot_dim / 2)
+    scale: float = 1.0
+
+    @classmethod
+    def make(cls, rot_dim: int, base: float = 10000.0, interleaved: bool = True, scaling: str = "none",
+             factor: float = 1.0, trained_ctx: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+             device="cuda"):
+        """Frequencies of dsa_rope_frequencies; scaling none, linear, ntk or yarn."""
+        import torch
+        f, scale = dsa_rope_frequencies(rot_dim, base, scaling, factor, trained_ctx, beta_fast, beta_slow)
+        return cls(torch.tensor(f, dtype=torch.float64).to(device), interleaved, scale)
+
+    @property
+    def rot_dim(self) -> int:
+        return 2 * self.inv_freq.numel()
+
+    def desc(self) -> dsa_rope_t:
+        import torch
+        _req(self.inv_freq, torch.float64, "inv_freq")
+        return dsa_rope_t(self.inv_freq.data_ptr(), self.rot_dim, bool(self.interleaved), self.scale)
+
+
+def dsa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                         trained_ctx: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(list of rot_dim / 2 float64 frequencies, scale) on the host."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling: expected one of {sorted(_ROPE_SCALING)}, got {scaling!r}")
+    f = (C.c_double * max(1, rot_dim // 2))()
+    scale = C.c_float(0.0)
+    _check(lib().dsa_rope_frequencies(rot_dim, base, _ROPE_SCALING[scaling], factor, trained_ctx, beta_fast,
+                                      beta_slow, f, C.byref(scale)), "dsa_rope_frequencies")
+    return list(f), scale.value
+
+
+def _dtypes():
+    import torch
+    return {torch.float32: DSA_DT_F32, torch.float16: DSA_DT_F16, torch.bfloat16: DSA_DT_BF16}
+
+
+_DT = None
+
+
+def _dt(t, name, allowed=(DSA_DT_F32, DSA_DT_F16, DSA_DT_BF16)):
+    global _DT
+    if _DT is None:
+        _DT = _dtypes()
+    d = _DT.get(t.dtype)
+    if d not in allowed:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return d
+
+
+def _shaped(t, name, dtype, *shape):
+    """A contiguous CUDA tensor of that dtype (None: any) and shape (-1: any extent)."""
+    got = t.shape
+    if not t.is_cuda or (dtype is not None and t.dtype != dtype) or not t.is_contiguous() or len(got) != len(shape) \
+            or any(w not in (-1, g) for w, g in zip(shape, got)):
+        raise TypeError(f"{name}: expected a contiguous CUDA {dtype or 'tensor'} of shape {shape}, "
+                        f"got {t.dtype} {tuple(got)} on {t.device}")
+
+
+def _run(name, tensors, call, stream):
+    """call(stream pointer) with the tensors' device current; they must share one."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise TypeError(f"{name}: tensors on {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        _check(call(_stream(stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(call(_stream(stream)), name)
+
+
+def _paging(block_table, block_size: int, batch: Batch):
+    """(dsa_paging_t pointer or None) of an optional block table [B, max_blocks]."""
+    import torch
+    if block_table is None:
+        return None
+    _shaped(block_table, "block_table", torch.int32, batch.B, -1)
+    return C.byref(dsa_paging_t(block_table.data_ptr(), block_table.shape[1], block_size))
+
+
+def dsa_rope(x, pos, rope: Rope, out, rot_off: int = 0, inverse: bool = False, stream=None):
+    """out = x with rope.rot_dim values of each head, from rot_off on, turned at
+    the tokens' positions.  x, out: [T, heads, dim] of one dtype (float32,
+    float16, bfloat16), any token and head strides, contiguous heads; out may
+    be x.  pos: int32 [T].  inverse: the gradient's direction."""
+    import torch
+    dt = _dt(x, "x")
+    if x.dim() != 3 or out.shape != x.shape or out.dtype != x.dtype or not x.is_cuda or not out.is_cuda \
+            or (x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1)):
+        raise TypeError(f"x, out: expected CUDA tensors [T, heads, dim] of one shape and dtype with contiguous heads, "
+                        f"got {x.dtype} {tuple(x.shape)} and {out.dtype} {tuple(out.shape)}")
+    T, heads, dim = x.shape
+    _shaped(pos, "pos", torch.int32, T)
+    r = rope.desc()
+    _run("dsa_rope", (x, out, pos, rope.inv_freq), lambda s: lib().dsa_rope(
+        x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0), out.stride(1), dt, T, heads, dim,
+        rot_off, pos.data_ptr(), C.byref(r), int(inverse), s), stream)
+
+
+def _new_rows(c_new, r_new, batch: Batch):
+    dt = _dt(c_new, "c_new")
+    for t, name, width in ((c_new, "c_new", 512), (r_new, "r_new", 64)):
+        if t is None:
+            continue
+        if not t.is_cuda or t.dtype != c_new.dtype or t.dim() != 2 or tuple(t.shape) != (batch.T, width) \
+                or t.stride(1) != 1:
+            raise TypeError(f"{name}: expected CUDA rows [{batch.T}, {width}] of {c_new.dtype}, "
+                            f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return dt
+
+
+def dsa_kv_append(c_new, r_new, batch: Batch, rope, kv_cache, ws, block_table=None, block_size: int = 0, stream=None):
+    """One bf16 latent row per token into kv_cache [rows, 576] ([rows, 512]
+    with r_new None).  c_new [T, 512] and r_new [T, 64] may be column slices;
+    the tail is turned at the token's position when rope (a Rope) is given."""
+    import torch
+    dt = _new_rows(c_new, r_new, batch)
+    _shaped(kv_cache, "kv_cache", torch.bfloat16, -1, 512 if r_new is None else 576)
+    if kv_cache.shape[0] < batch.cache_rows:
+        raise TypeError(f"kv_cache: {kv_cache.shape[0]} rows, the batch names {batch.cache_rows}")
+    d, pg = batch.desc(), _paging(block_table, block_size, batch)
+    r = C.byref(rope.desc()) if rope is not None else None
+    _run("dsa_kv_append", (c_new, r_new, batch.cu_q, batch.q_pos, batch.kv_off, block_table, kv_cache, ws,
+                           rope.inv_freq if rope is not None else None), lambda s: lib().dsa_kv_append(
+        c_new.data_ptr(), c_new.stride(0), r_new.data_ptr() if r_new is not None else None,
+        r_new.stride(0) if r_new is not None else 0, dt, C.byref(d), pg, r, kv_cache.data_ptr(), ws.data_ptr(),
+        ws.numel(), s), stream)
+
+
+def _q8_cache(codes, scale, tail: bool, batch: Batch):
+    import torch
+    _shaped(codes, "codes", torch.uint8, -1, Q8_ROW if tail else 512)
+    _shaped(scale, "scale", torch.float32, codes.shape[0])
+    if codes.shape[0] < batch.cache_rows:
+        raise TypeError(f"codes: {codes.shape[0]} rows, the batch names {batch.cache_rows}")
+
+
+def q8_cache(rows: int, tail: bool = True, device="cuda"):
+    """(codes, scale) of an 8-bit latent cache of `rows` rows, all zero."""
+    import torch
+    return (torch.zeros(rows, Q8_ROW if tail else 512, dtype=torch.uint8, device=device),
+            torch.zeros(rows, device=device))
+
+
+def dsa_kv_append_q8(c_new, r_new, batch: Batch, rope, codes, scale, ws, block_table=None, block_size: int = 0,
+                     stream=None):
+    """dsa_kv_append into an 8-bit cache: codes uint8 [rows, 640] ([rows, 512]
+    with r_new None), scale float32 [rows]."""
+    dt = _new_rows(c_new, r_new, batch)
+    _q8_cache(codes, scale, r_new is not None, batch)
+    d, pg = batch.desc(), _paging(block_table, block_size, batch)
+    r = C.byref(rope.desc()) if rope is not None else None
+    _run("dsa_kv_append_q8", (c_new, r_new, batch.cu_q, batch.q_pos, batch.kv_off, block_table, codes, scale, ws,
+                              rope.inv_freq if rope is not None else None), lambda s: lib().dsa_kv_append_q8(
+        c_new.data_ptr(), c_new.stride(0), r_new.data_ptr() if r_new is not None else None,
+        r_new.stride(0) if r_new is not None else 0, dt, C.byref(d), pg, r, codes.data_ptr(), scale.data_ptr(),
+        ws.data_ptr(), ws.numel(), s), stream)
+
+
+def dsa_kv_read_q8(codes, scale, batch: Batch, out, ws, block_table=None, block_size: int = 0, stream=None):
+    """The tokens' rows of an 8-bit cache as out [T, 576] ([T, 512] for codes
+    of 512), bfloat16 or float32; out may be a column slice of wider rows."""
+    import torch
+    tail = codes.dim() == 2 and codes.shape[1] == Q8_ROW
+    _q8_cache(codes, scale, tail, batch)
+    dt = _dt(out, "out", (DSA_DT_F32, DSA_DT_BF16))
+    width = 576 if tail else 512
+    if not out.is_cuda or out.dim() != 2 or tuple(out.shape) != (batch.T, width) or out.stride(1) != 1:
+        raise TypeError(f"out: expected CUDA rows [{batch.T}, {width}], got {tuple(out.shape)} on {out.device}")
+    stride = out.stride(0) if batch.T > 1 else width
+    d, pg = batch.desc(), _paging(block_table, block_size, batch)
+    _run("dsa_kv_read_q8", (codes, scale, batch.cu_q, batch.q_pos, batch.kv_off, block_table, out, ws),
+         lambda s: lib().dsa_kv_read_q8(codes.data_ptr(), scale.data_ptr(), int(tail), C.byref(d), pg, out.data_ptr(),
+                                        dt, stride, ws.data_ptr(), ws.numel(), s), stream)
+
+
+def dsa_sparse_mla_attn_q8(q_lat, q_rope, codes, scale, batch: Batch, idx, sm_scale: float, out, lse, ws,
+                           block_table=None, block_size: int = 0, stream=None):
+    """dsa_sparse_mla_attn over an 8-bit cache (q_rope None: codes of 512, no
+    tail); out [T, H, 512] float32 or bfloat16, lse [T, H] float32 or None."""
+    import torch
+    T, H = batch.T, q_lat.shape[1] if q_lat.dim() == 3 else -1
+    _shaped(q_lat, "q_lat", torch.bfloat16, T, H, 512)
+    if q_rope is not None:
+        _shaped(q_rope, "q_rope", torch.bfloat16, T, H, 64)
+    _q8_cache(codes, scale, q_rope is not None, batch)
+    _shaped(idx, "idx", torch.int32, T, -1)
+    dt = _dt(out, "out", (DSA_DT_F32, DSA_DT_BF16))
+    _shaped(out, "out", None, T, H, 512)
+    if lse is not None:
+        _shaped(lse, "lse", torch.float32, T, H)
+    d, pg = batch.desc(), _paging(block_table, block_size, batch)
+    _run("dsa_sparse_mla_attn_q8", (q_lat, q_rope, codes, scale, batch.cu_q, batch.q_pos, batch.kv_off, block_table,
+                                    idx, out, lse, ws), lambda s: lib().dsa_sparse_mla_attn_q8(
+        q_lat.data_ptr(), q_rope.data_ptr() if q_rope is not None else None, codes.data_ptr(), scale.data_ptr(),
+        C.byref(d), pg, idx.data_ptr(), idx.shape[1], H, sm_scale, out.data_ptr(), dt,
+        lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.numel(), s), stream)
 
 
 def dsa_set_trace_events(events):

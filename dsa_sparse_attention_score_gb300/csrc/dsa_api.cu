@@ -1,6 +1,7 @@
 // dsa_api.cu -- the C ABI declared in include/dsa.h: argument validation,
 // workspace layout, TMA tensor maps and the launch order of each call.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -23,6 +24,7 @@ int g_skip_copies = 0;
 
 constexpr int kMaxHeads = 128;        // query heads: one or two groups of 64 per token
 constexpr int kMaxSplit = 128;        // split partials the combine kernel merges
+constexpr int kMaxRotDim = 512;       // values of a head that rotary positions turn
 constexpr int kKpoolMaxTopK = 4096;   // kpool: 1024 pools per token (the expansion's slots)
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -680,6 +682,226 @@ dsa_status_t dsa_decode_kpool(const dsa_f16 *k_new, const dsa_f16 *gate_new, con
         return s;
     return run_attention(q_lat, nullptr, kv_latent, batch, idx, kpool_width(top_k), H, sm_scale, out, lse, ws, L,
                          stream, false, true, nullptr, false);
+}
+
+
+// ---------------------------------------------------------------- rotary positions and the 8-bit cache
+
+static bool float_dtype(int d) { return d == DSA_DT_F32 || d == DSA_DT_F16 || d == DSA_DT_BF16; }
+static int64_t dtype_bytes(int d) { return d == DSA_DT_F32 ? 4 : 2; }
+
+dsa_status_t dsa_rope_frequencies(int rot_dim, double base, int scaling, double factor, int trained_ctx,
+                                  double beta_fast, double beta_slow, double *inv_freq, float *scale) {
+    if (!inv_freq || !scale || rot_dim < 2 || rot_dim % 2 || !(base > 1.0) || !std::isfinite(base))
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (rot_dim > kMaxRotDim) return DSA_ERR_UNSUPPORTED;
+    if (scaling < DSA_ROPE_NONE || scaling > DSA_ROPE_YARN) return DSA_ERR_INVALID_ARGUMENT;
+    if (scaling != DSA_ROPE_NONE && !(factor >= 1.0 && std::isfinite(factor))) return DSA_ERR_INVALID_ARGUMENT;
+    if (scaling == DSA_ROPE_NTK) {
+        if (rot_dim < 4) return DSA_ERR_INVALID_ARGUMENT;
+        base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+    }
+    double low = 0.0, high = 1.0;
+    if (scaling == DSA_ROPE_YARN) {
+        if (trained_ctx < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast))
+            return DSA_ERR_INVALID_ARGUMENT;
+        // the (fractional) pair that makes beta turns over the trained context
+        const double two_pi = 6.283185307179586476925;
+        auto pair_of = [&](double beta) { return rot_dim * std::log(trained_ctx / (beta * two_pi)) / (2.0 * std::log(base)); };
+        low = std::max(0.0, std::floor(pair_of(beta_fast)));
+        high = std::min((double)rot_dim - 1.0, std::ceil(pair_of(beta_slow)));
+    }
+    *scale = scaling == DSA_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    for (int j = 0; j < rot_dim / 2; ++j) {
+        const double f = std::pow(base, -2.0 * j / rot_dim);
+        double slow = scaling == DSA_ROPE_LINEAR ? 1.0 : 0.0;      // share of f / factor
+        if (scaling == DSA_ROPE_YARN) slow = std::min(1.0, std::max(0.0, (j - low) / std::max(high - low, 1e-3)));
+        inv_freq[j] = slow == 0.0 ? f : f * (1.0 - slow) + f / factor * slow;
+    }
+    return DSA_OK;
+}
+
+static dsa_status_t check_rope(const dsa_rope_t *r) {
+    if (!r->inv_freq || r->rot_dim < 2 || r->rot_dim % 2) return DSA_ERR_INVALID_ARGUMENT;
+    if (r->rot_dim > kMaxRotDim) return DSA_ERR_UNSUPPORTED;
+    if (!aligned(r->inv_freq, 8)) return DSA_ERR_MISALIGNED;
+    return DSA_OK;
+}
+
+dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y, int64_t y_token_stride,
+                      int64_t y_head_stride, int dtype, int n_tokens, int heads, int head_dim, int rot_off,
+                      const int32_t *pos, const dsa_rope_t *rope, int inverse, cudaStream_t stream) {
+    if (!x || !y || !pos || !rope || !float_dtype(dtype)) return DSA_ERR_INVALID_ARGUMENT;
+    if (n_tokens < 1 || heads < 1 || head_dim < 2 || rot_off < 0) return DSA_ERR_INVALID_ARGUMENT;
+    dsa_status_t s = check_rope(rope);
+    if (s != DSA_OK) return s;
+    if ((int64_t)rot_off + rope->rot_dim > head_dim) return DSA_ERR_INVALID_ARGUMENT;
+    if ((int64_t)heads * head_dim > (int64_t(1) << 24)) return DSA_ERR_UNSUPPORTED;
+    constexpr int64_t kFar = int64_t(1) << 40;          // strides whose extents stay far from 64 bits
+    if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0 ||
+        std::max(std::max(x_token_stride, x_head_stride), std::max(y_token_stride, y_head_stride)) > kFar / n_tokens)
+        return DSA_ERR_INVALID_ARGUMENT;
+    const int64_t e = dtype_bytes(dtype);
+    if (!aligned(x, e) || !aligned(y, e) || !aligned(pos, 4)) return DSA_ERR_MISALIGNED;
+    // rows of y apart from one another: heads inside a token, or tokens inside a head
+    const int64_t head_span = (heads - 1) * y_head_stride + head_dim, token_span = (n_tokens - 1) * y_token_stride + head_dim;
+    const bool heads_apart = heads == 1 || y_head_stride >= head_dim, tokens_apart = n_tokens == 1 || y_token_stride >= head_dim;
+    if (!heads_apart || !tokens_apart ||
+        !(n_tokens == 1 || heads == 1 || y_token_stride >= head_span || y_head_stride >= token_span))
+        return DSA_ERR_INVALID_ARGUMENT;
+    const bool same_strides = x_token_stride == y_token_stride && x_head_stride == y_head_stride;
+    const bool in_place = x == y && same_strides;
+    if (!in_place) {
+        const uintptr_t xb = reinterpret_cast<uintptr_t>(x), yb = reinterpret_cast<uintptr_t>(y);
+        const uintptr_t xe = xb + (uintptr_t)(((n_tokens - 1) * x_token_stride + (heads - 1) * x_head_stride + head_dim) * e);
+        const uintptr_t ye = yb + (uintptr_t)(((n_tokens - 1) * y_token_stride + (heads - 1) * y_head_stride + head_dim) * e);
+        if (xb < ye && yb < xe) {
+            // disjoint slices of the same heads: the smaller of the strides
+            // in use leaves room for both
+            const int64_t gap = (int64_t)(xb > yb ? xb - yb : yb - xb);
+            int64_t step = INT64_MAX;
+            if (heads > 1) step = std::min(step, y_head_stride);
+            if (n_tokens > 1) step = std::min(step, y_token_stride);
+            if (!same_strides || gap < head_dim * e || step == INT64_MAX || gap + head_dim * e > step * e)
+                return DSA_ERR_INVALID_ARGUMENT;
+        }
+    }
+    RopeLaunch a;
+    a.x = x;
+    a.y = y;
+    a.x_token_stride = x_token_stride;
+    a.x_head_stride = x_head_stride;
+    a.y_token_stride = y_token_stride;
+    a.y_head_stride = y_head_stride;
+    a.dtype = dtype;
+    a.n_tokens = n_tokens;
+    a.heads = heads;
+    a.head_dim = head_dim;
+    a.rot_off = rot_off;
+    a.rot_dim = rope->rot_dim;
+    a.pos = pos;
+    a.inv_freq = rope->inv_freq;
+    a.interleaved = rope->interleaved != 0;
+    a.inverse = inverse != 0;
+    a.scale = rope->scale;
+    a.copy_rest = !in_place;
+    DSA_TRY_CUDA(launch_rope(a, stream));
+    return DSA_OK;
+}
+
+// Checks of the calls on the 8-bit cache (and dsa_kv_append): the batch, its
+// paging, and the device batch they give.
+static dsa_status_t cache_batch(const dsa_batch_t *batch, const dsa_paging_t *paging, DevBatch *db) {
+    dsa_status_t s = check_batch(batch, paging != nullptr);
+    if (s != DSA_OK) return s;
+    if (paging) {
+        if (!paging->block_table || paging->block_size < 1 || paging->max_blocks < 1 ||
+            (int64_t)paging->max_blocks * paging->block_size < batch->max_kv)
+            return DSA_ERR_INVALID_ARGUMENT;
+        if (!aligned(paging->block_table, 4)) return DSA_ERR_MISALIGNED;
+    }
+    *db = dev_batch(batch);
+    if (paging) {
+        db->block_table = paging->block_table;
+        db->max_blocks = paging->max_blocks;
+        db->block_size = paging->block_size;
+    }
+    return DSA_OK;
+}
+
+static dsa_status_t kv_append_impl(const void *c_new, int64_t c_stride, const void *r_new, int64_t r_stride, int dtype,
+                                   const dsa_batch_t *batch, const dsa_paging_t *paging, const dsa_rope_t *rope,
+                                   dsa_bf16 *kv, uint8_t *codes, float *scale, void *ws, size_t ws_bytes,
+                                   cudaStream_t stream) {
+    DevBatch db;
+    dsa_status_t s = cache_batch(batch, paging, &db);
+    if (s != DSA_OK) return s;
+    if (!c_new || (!kv && (!codes || !scale)) || !float_dtype(dtype)) return DSA_ERR_INVALID_ARGUMENT;
+    if (c_stride < 0 || (r_new && r_stride < 0) || (rope && !r_new)) return DSA_ERR_INVALID_ARGUMENT;
+    if (rope) {
+        if ((s = check_rope(rope)) != DSA_OK) return s;
+        if (rope->rot_dim != D_R) return DSA_ERR_UNSUPPORTED;
+    }
+    const size_t e = (size_t)dtype_bytes(dtype);
+    if (!aligned(c_new, e) || (r_new && !aligned(r_new, e)) || (kv && !aligned(kv, 16)) || (codes && !aligned(codes, 16)) ||
+        (scale && !aligned(scale, 4)))
+        return DSA_ERR_MISALIGNED;
+    if ((s = check_ws(ws, ws_bytes, kStatusBytes)) != DSA_OK) return s;
+    KvAppendLaunch a;
+    a.c_new = c_new;
+    a.r_new = r_new;
+    a.c_stride = c_stride;
+    a.r_stride = r_stride;
+    a.dtype = dtype;
+    a.inv_freq = rope ? rope->inv_freq : nullptr;
+    a.interleaved = rope ? rope->interleaved != 0 : 1;
+    a.rope_scale = rope ? rope->scale : 1.f;
+    a.kv = kv;
+    a.codes = codes;
+    a.scale = scale;
+    DSA_TRY_CUDA(launch_kv_append(a, db, status_ptr(ws), stream));
+    return DSA_OK;
+}
+
+dsa_status_t dsa_kv_append(const void *c_new, int64_t c_stride, const void *r_new, int64_t r_stride, int dtype,
+                           const dsa_batch_t *batch, const dsa_paging_t *paging, const dsa_rope_t *rope,
+                           dsa_bf16 *kv_cache, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!kv_cache) return DSA_ERR_INVALID_ARGUMENT;
+    return kv_append_impl(c_new, c_stride, r_new, r_stride, dtype, batch, paging, rope, kv_cache, nullptr, nullptr, ws,
+                          ws_bytes, stream);
+}
+
+dsa_status_t dsa_kv_append_q8(const void *c_new, int64_t c_stride, const void *r_new, int64_t r_stride, int dtype,
+                              const dsa_batch_t *batch, const dsa_paging_t *paging, const dsa_rope_t *rope,
+                              uint8_t *codes, float *scale, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    return kv_append_impl(c_new, c_stride, r_new, r_stride, dtype, batch, paging, rope, nullptr, codes, scale, ws,
+                          ws_bytes, stream);
+}
+
+dsa_status_t dsa_kv_read_q8(const uint8_t *codes, const float *scale, int tail, const dsa_batch_t *batch,
+                            const dsa_paging_t *paging, void *out, int out_dtype, int64_t out_stride, void *ws,
+                            size_t ws_bytes, cudaStream_t stream) {
+    DevBatch db;
+    dsa_status_t s = cache_batch(batch, paging, &db);
+    if (s != DSA_OK) return s;
+    if (!codes || !scale || !out || (out_dtype != DSA_DT_BF16 && out_dtype != DSA_DT_F32)) return DSA_ERR_INVALID_ARGUMENT;
+    if (out_stride < (tail ? D_ROW : D_L)) return DSA_ERR_INVALID_ARGUMENT;
+    if (!aligned(codes, 16) || !aligned(scale, 4) || !aligned(out, (size_t)dtype_bytes(out_dtype))) return DSA_ERR_MISALIGNED;
+    if ((s = check_ws(ws, ws_bytes, kStatusBytes)) != DSA_OK) return s;
+    DSA_TRY_CUDA(launch_kv_read(codes, scale, tail != 0, out, out_dtype, out_stride, db, status_ptr(ws), stream));
+    return DSA_OK;
+}
+
+dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const uint8_t *codes,
+                                    const float *scale, const dsa_batch_t *batch, const dsa_paging_t *paging,
+                                    const int32_t *idx, int k, int H, float sm_scale, void *out, int out_dtype,
+                                    float *lse, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    DevBatch db;
+    dsa_status_t s = cache_batch(batch, paging, &db);
+    if (s != DSA_OK) return s;
+    if (!q_lat || !codes || !scale || !idx || !out || (out_dtype != DSA_DT_BF16 && out_dtype != DSA_DT_F32))
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (H < 1 || H > kMaxHeads || k < 1 || k > 65536) return DSA_ERR_UNSUPPORTED;
+    if ((int64_t)batch->total_q * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+    if (!aligned(q_lat, 16) || (q_rope && !aligned(q_rope, 16)) || !aligned(codes, 16) || !aligned(scale, 4) ||
+        !aligned(out, 16) || !aligned(idx, 4) || (lse && !aligned(lse, 4)))
+        return DSA_ERR_MISALIGNED;
+    const Layout L = layout(DSA_OP_SPARSE_ATTN, batch, H, k);
+    if ((s = check_ws(ws, ws_bytes, L.total)) != DSA_OK) return s;
+    AttnQ8Launch a;
+    a.q_lat = q_lat;
+    a.q_rope = q_rope;
+    a.codes = codes;
+    a.scale = scale;
+    a.idx = idx;
+    a.H = H;
+    a.k = k;
+    a.sm_scale = sm_scale;
+    a.out = out;
+    a.out_bf16 = out_dtype == DSA_DT_BF16;
+    a.lse = lse;
+    DSA_TRY_CUDA(launch_sparse_attn_q8(a, db, status_ptr(ws), stream, false));
+    return DSA_OK;
 }
 
 }  // extern "C"

@@ -161,6 +161,54 @@ cudaError_t launch_sparse_attn(const AttnLaunch &a, const CUtensorMap &q_lat_map
                                const DevBatch &b, uint32_t *status, cudaStream_t stream, bool pdl);
 cudaError_t launch_attn_combine(const AttnLaunch &a, const DevBatch &b, cudaStream_t stream, bool pdl);
 
+// Rotary positions on [n_tokens, heads, head_dim] values (rope.cu).
+struct RopeLaunch {
+    const void *x;
+    void *y;
+    int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+    int dtype, n_tokens, heads, head_dim, rot_off, rot_dim;
+    const int32_t *pos;
+    const double *inv_freq;
+    int interleaved, inverse;
+    float scale;
+    int copy_rest;           // write the values that do not turn too (0: in place)
+};
+cudaError_t launch_rope(const RopeLaunch &a, cudaStream_t stream);
+
+// Latent rows of the 8-bit cache: 512 codes | 64 tail codes | 64 tail remainders.
+constexpr int kQ8Row = 640;
+
+// One latent row per token into the bf16 (kv) or the 8-bit cache (codes, scale).
+struct KvAppendLaunch {
+    const void *c_new, *r_new;        // r_new null: rows without a tail
+    int64_t c_stride, r_stride;       // values between tokens
+    int dtype;
+    const double *inv_freq;           // null: the tail is stored as it is
+    int interleaved;
+    float rope_scale;
+    uint16_t *kv;                     // bf16 cache, or null
+    uint8_t *codes;
+    float *scale;
+};
+cudaError_t launch_kv_append(const KvAppendLaunch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream);
+// The 8-bit rows of the batch's tokens as bf16 or float32 rows, `stride` values apart.
+cudaError_t launch_kv_read(const uint8_t *codes, const float *scale, int tail, void *out, int out_dtype, int64_t stride,
+                           const DevBatch &b, uint32_t *status, cudaStream_t stream);
+
+// Sparse attention over the 8-bit cache.
+struct AttnQ8Launch {
+    const uint16_t *q_lat, *q_rope;   // bf16 [T,H,512], [T,H,64]; q_rope null: rows without a tail
+    const uint8_t *codes;
+    const float *scale;
+    const int32_t *idx;               // [T, k]
+    int H, k;
+    float sm_scale;
+    void *out;                        // [T, H, 512] float32, or bf16 with out_bf16
+    int out_bf16;
+    float *lse;                       // [T, H] or null
+};
+cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream, bool pdl);
+
 // Sets a kernel's dynamic shared-memory limit once per device; `slot`
 // (0..kSmemAttrSlots-1) names the kernel instance.
 constexpr int kSmemAttrSlots = 11;

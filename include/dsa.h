@@ -392,6 +392,127 @@ dsa_status_t dsa_decode_kpool(const dsa_f16 *k_new, const dsa_f16 *gate_new, con
                               float *lse, int32_t *idx_out, void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Rotary positions.  DSA_DT_* are the element types of the calls below.
+ */
+enum { DSA_DT_F32 = 0, DSA_DT_F16 = 1, DSA_DT_BF16 = 2 };
+
+/* Frequency scalings of dsa_rope_frequencies. */
+enum {
+    DSA_ROPE_NONE = 0,        /* f_j = base^(-2j / rot_dim) */
+    DSA_ROPE_LINEAR = 1,      /* f_j / factor (positions interpolated) */
+    DSA_ROPE_NTK = 2,         /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+    DSA_ROPE_YARN = 3         /* per-pair blend of f_j and f_j / factor (Peng et al. 2023, "YaRN") */
+};
+
+/*
+ * A rotation: the value pair j of a token at position p turns by the angle
+ * p * inv_freq[j] and is multiplied by scale.
+ *   inv_freq     device float64 [rot_dim / 2], radians per position, 8-byte aligned
+ *   rot_dim      values that turn: even, 2..512
+ *   interleaved  nonzero: pair j is the values 2j and 2j + 1; 0: j and j + rot_dim / 2
+ *   scale        factor on the turned values (1, or a context scaling's attention factor)
+ */
+typedef struct {
+    const double *inv_freq;
+    int32_t rot_dim;
+    int32_t interleaved;
+    float scale;
+} dsa_rope_t;
+
+/*
+ * Fills HOST arrays: inv_freq [rot_dim / 2] and *scale, the factor that
+ * belongs to them (YaRN: 0.1 ln(factor) + 1; otherwise 1).  No device work.
+ *   base > 1; factor >= 1 (ignored by DSA_ROPE_NONE); DSA_ROPE_NTK needs rot_dim >= 4
+ *   trained_ctx, beta_fast, beta_slow: YaRN's trained context length (>= 1)
+ *   and the turns over it above which a pair keeps its frequency and below
+ *   which it is divided by factor (usually 32 and 1; beta_fast > beta_slow > 0)
+ */
+dsa_status_t dsa_rope_frequencies(int rot_dim, double base, int scaling, double factor, int trained_ctx,
+                                  double beta_fast, double beta_slow, double *inv_freq, float *scale);
+
+/*
+ * Rotary positions on (part of) each head of a token's row:
+ *   y[t,h,rot_off + i] = scale * (R(pos[t]) x[t,h,rot_off : rot_off + rot_dim])[i],
+ *   the other values of the head are copied.
+ * With `inverse` the angles are negated: the call that maps the gradient of
+ * y to the gradient of x.  Angles are formed in float64, the products in
+ * float32, and each result is rounded once to the element type.
+ *   x, y   [n_tokens, heads, head_dim] of dtype DSA_DT_*; a token's heads
+ *          and a head's rows are *_head_stride and *_token_stride values
+ *          apart (>= 0), a head's values are contiguous.  y may be x with the
+ *          same strides (in place; only the turned values are written then);
+ *          otherwise the two must not share memory, except as disjoint
+ *          slices of the heads of one buffer with the same strides.
+ *   pos    device int32 [n_tokens], any value
+ * Addresses and extents that are multiples of 16 bytes move 16 bytes at a time.
+ * Errors: DSA_ERR_INVALID_ARGUMENT for null pointers, sizes below 1, a
+ * rotated part outside the head, an odd rot_dim, negative strides, rows of y
+ * that overlap one another, or memory shared by x and y as above;
+ * DSA_ERR_UNSUPPORTED for rot_dim > 512 or heads * head_dim > 2^24;
+ * DSA_ERR_MISALIGNED for pointers not aligned to their elements.
+ */
+dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y, int64_t y_token_stride,
+                      int64_t y_head_stride, int dtype, int n_tokens, int heads, int head_dim, int rot_off,
+                      const int32_t *pos, const dsa_rope_t *rope, int inverse, cudaStream_t stream);
+
+/*
+ * The 8-bit latent cache.  A token's row x -- its kv latent (512) and, with a
+ * tail, its 64 rotary values -- is held under one power-of-two scale:
+ *   codes  uint8 [cache_rows, 640]: 512 e4m3 codes of the latent | 64 of the
+ *          tail | 64 of the tail's remainders; [cache_rows, 512] without a tail
+ *   scale  float32 [cache_rows]: 2^E, E the least integer in [-40, 119] with
+ *          max |x| <= 448 * 2^E
+ *   latent value = 2^E e4m3(x / 2^E)
+ *   tail value   = 2^E (hi + lo), hi = e4m3(x / 2^E), lo = e4m3(x / 2^E - hi)
+ * (round to nearest even; 644 bytes a token against 1152 in bf16).  A row
+ * with a NaN or infinite value gets the scale NaN and reads back as NaN.
+ * codes must be 16-byte aligned (128 keeps rows on cache lines).
+ *
+ * dsa_kv_append writes one bf16 row of the token per call argument below into
+ * a cache [cache_rows, 576] (or 512) as dsa_sparse_mla_attn reads it;
+ * dsa_kv_append_q8 into an 8-bit cache.  The tail is turned at the token's
+ * position first (rope, rot_dim 64), or stored as it is when rope is NULL.
+ *   c_new   [T,512], rows c_stride values apart; r_new [T,64], rows r_stride
+ *           values apart, or NULL for rows without a tail; both of dtype DSA_DT_*
+ *   paging  NULL for contiguous caches (row kv_off[b] + position); any
+ *           block_size >= 1 is accepted here and in the other calls on the
+ *           8-bit cache but dsa_decode_q8
+ *   ws      at least dsa_workspace_size(DSA_OP_K_APPEND) bytes (status word)
+ * Tokens of a batch must be at different rows.  A token whose position is out
+ * of bounds is skipped and flagged DSA_DEV_BAD_POSITION; no other row changes.
+ */
+dsa_status_t dsa_kv_append(const void *c_new, int64_t c_stride, const void *r_new, int64_t r_stride, int dtype,
+                           const dsa_batch_t *batch, const dsa_paging_t *paging, const dsa_rope_t *rope,
+                           dsa_bf16 *kv_cache, void *ws, size_t ws_bytes, cudaStream_t stream);
+dsa_status_t dsa_kv_append_q8(const void *c_new, int64_t c_stride, const void *r_new, int64_t r_stride, int dtype,
+                              const dsa_batch_t *batch, const dsa_paging_t *paging, const dsa_rope_t *rope,
+                              uint8_t *codes, float *scale, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Reads the rows of the batch's tokens (sequence b's position q_pos[t]) back
+ * from the 8-bit cache.
+ *   tail    nonzero: rows of 640 codes, out rows of 576 values; 0: 512 and 512
+ *   out     [T, 576] (or 512) of DSA_DT_BF16 or DSA_DT_F32, rows out_stride
+ *           values apart (>= the row's width)
+ * A token whose position is out of bounds gets zeros and is flagged.
+ */
+dsa_status_t dsa_kv_read_q8(const uint8_t *codes, const float *scale, int tail, const dsa_batch_t *batch,
+                            const dsa_paging_t *paging, void *out, int out_dtype, int64_t out_stride, void *ws,
+                            size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * dsa_sparse_mla_attn over the 8-bit cache (q_rope NULL: rows without a tail,
+ * as dsa_sparse_mla_attn_nope), contiguous or paged.
+ *   out        [T,H,512] of out_dtype DSA_DT_F32 or DSA_DT_BF16
+ *   the rest   as dsa_sparse_mla_attn, with its workspace (DSA_OP_SPARSE_ATTN)
+ * The codes are read as they are held, in float32 sums.
+ */
+dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const uint8_t *codes,
+                                    const float *scale, const dsa_batch_t *batch, const dsa_paging_t *paging,
+                                    const int32_t *idx, int k, int H, float sm_scale, void *out, int out_dtype,
+                                    float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Workspace bytes an operation needs for this batch (host only; batch
  * pointers are not read).  Every workspace starts with the 256-byte status
  * block; call dsa_workspace_init once on a new workspace.
