@@ -115,11 +115,13 @@ inline int head_groups(int H) { return (H + 63) / 64; }
 // group) pairs than SMs, up to one wave of CTAs (one per SM), each keeping at
 // least two tiles so that its gathers overlap its arithmetic, and never more
 // splits than the combine kernel merges.
-void attn_split(int T, int H, int k, int *n_split, int *tpc) {
-    const int n_tiles = (k + attn_tile_rows() - 1) / attn_tile_rows();
+// The 8-bit cache's kernel has tiles of 128 rows and one tile per CTA at the
+// least: never more splits than the 64-row kernel's, whose workspace it uses.
+void attn_split(int T, int H, int k, int *n_split, int *tpc, int tile_rows = attn_tile_rows(), int min_tiles = 2) {
+    const int n_tiles = (k + tile_rows - 1) / tile_rows;
     const int64_t units = (int64_t)T * head_groups(H);
     int ns = 1;
-    if (units < kSMs) ns = std::max(1, std::min((n_tiles + 1) / 2, (int)(kSMs / units)));
+    if (units < kSMs) ns = std::max(1, std::min((n_tiles + min_tiles - 1) / min_tiles, (int)(kSMs / units)));
     ns = std::min(ns, kMaxSplit);
     int t = (n_tiles + ns - 1) / ns;
     ns = (n_tiles + t - 1) / t;
@@ -809,6 +811,42 @@ static dsa_status_t cache_batch(const dsa_batch_t *batch, const dsa_paging_t *pa
     return DSA_OK;
 }
 
+// The attention over the 8-bit cache and its combine, with the split
+// partials where the 64-row kernel's would be.
+static dsa_status_t run_attention_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const uint8_t *codes,
+                                     const float *scale, const DevBatch &db, const int32_t *idx, int k, int H,
+                                     float sm_scale, void *out, int out_dtype, float *lse, void *ws, const Layout &L,
+                                     cudaStream_t stream, bool pdl) {
+    AttnQ8Launch a;
+    a.q_lat = q_lat;
+    a.q_rope = q_rope;
+    a.codes = codes;
+    a.scale = scale;
+    a.idx = idx;
+    a.H = H;
+    a.k = k;
+    a.sm_scale = sm_scale;
+    a.out = out;
+    a.out_bf16 = out_dtype == DSA_DT_BF16;
+    a.lse = lse;
+    attn_split(db.T, H, k, &a.n_split, &a.tiles_per_cta, attn_q8_tile_rows(), 1);
+    if (a.n_split > L.n_split) return DSA_ERR_WORKSPACE_TOO_SMALL;   // see attn_split: does not happen
+    uint8_t *w8 = static_cast<uint8_t *>(ws);
+    a.part_o = a.n_split > 1 ? reinterpret_cast<uint16_t *>(w8 + L.part_o) : nullptr;
+    a.part_ml = a.n_split > 1 ? reinterpret_cast<float *>(w8 + L.part_ml) : nullptr;
+    DSA_TRY_CUDA(launch_sparse_attn_q8(a, db, status_ptr(ws), stream, pdl));
+    AttnLaunch c{};
+    c.H = H;
+    c.out = a.out_bf16 ? nullptr : static_cast<float *>(out);
+    c.out16 = a.out_bf16 ? out : nullptr;
+    c.lse = lse;
+    c.n_split = a.n_split;
+    c.part_o = a.part_o;
+    c.part_ml = a.part_ml;
+    DSA_TRY_CUDA(launch_attn_combine(c, db, stream, true));
+    return DSA_OK;
+}
+
 static dsa_status_t kv_append_impl(const void *c_new, int64_t c_stride, const void *r_new, int64_t r_stride, int dtype,
                                    const dsa_batch_t *batch, const dsa_paging_t *paging, const dsa_rope_t *rope,
                                    dsa_bf16 *kv, uint8_t *codes, float *scale, void *ws, size_t ws_bytes,
@@ -888,20 +926,7 @@ dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rop
         return DSA_ERR_MISALIGNED;
     const Layout L = layout(DSA_OP_SPARSE_ATTN, batch, H, k);
     if ((s = check_ws(ws, ws_bytes, L.total)) != DSA_OK) return s;
-    AttnQ8Launch a;
-    a.q_lat = q_lat;
-    a.q_rope = q_rope;
-    a.codes = codes;
-    a.scale = scale;
-    a.idx = idx;
-    a.H = H;
-    a.k = k;
-    a.sm_scale = sm_scale;
-    a.out = out;
-    a.out_bf16 = out_dtype == DSA_DT_BF16;
-    a.lse = lse;
-    DSA_TRY_CUDA(launch_sparse_attn_q8(a, db, status_ptr(ws), stream, false));
-    return DSA_OK;
+    return run_attention_q8(q_lat, q_rope, codes, scale, db, idx, k, H, sm_scale, out, out_dtype, lse, ws, L, stream, false);
 }
 
 }  // extern "C"

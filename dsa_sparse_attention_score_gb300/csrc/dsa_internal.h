@@ -155,6 +155,7 @@ struct AttnLaunch {
     int n_split;             // CTAs per (token, head group)
     void *part_o;            // bf16 [T, n_split, groups*64, 512] when n_split > 1
     float *part_ml;          // [T, n_split, groups*64, 2]
+    void *out16 = nullptr;   // combine: bf16 output instead of `out`
 };
 cudaError_t launch_sparse_attn(const AttnLaunch &a, const CUtensorMap &q_lat_map,
                                const CUtensorMap &q_rope_map, const CUtensorMap &kv_map,
@@ -206,12 +207,16 @@ struct AttnQ8Launch {
     void *out;                        // [T, H, 512] float32, or bf16 with out_bf16
     int out_bf16;
     float *lse;                       // [T, H] or null
+    int tiles_per_cta, n_split;       // of attn_q8_tile_rows() rows; as AttnLaunch
+    uint16_t *part_o;
+    float *part_ml;
 };
+int attn_q8_tile_rows();
 cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream, bool pdl);
 
 // Sets a kernel's dynamic shared-memory limit once per device; `slot`
 // (0..kSmemAttrSlots-1) names the kernel instance.
-constexpr int kSmemAttrSlots = 11;
+constexpr int kSmemAttrSlots = 12;
 cudaError_t ensure_smem_attr(const void *func, int slot, size_t bytes);
 
 // Rows of one attention tile (the unit of the split across CTAs).

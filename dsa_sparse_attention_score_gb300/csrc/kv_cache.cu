@@ -76,7 +76,6 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
 
 template <typename T, bool kQ8>
 __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendParams p, const DevBatch b, uint32_t *status) {
-    pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= b.T) return;

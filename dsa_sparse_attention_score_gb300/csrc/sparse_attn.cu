@@ -636,12 +636,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // NF partial rows are loaded at a time.  With NF = 4 (up to four splits)
 // the kernel fits in 32 registers, so 16 CTAs share an SM and a grid of
 // thousands of (token, head) CTAs runs in one wave; NF = 16 keeps five CTAs
-// per SM.
-template <int NF>
+// per SM.  OutT: float, or bf16 (one more rounding) for the 8-bit cache's call.
+template <int NF, typename OutT>
 __global__ void __launch_bounds__(128, NF <= 4 ? 16 : 5) attn_combine_kernel(const uint16_t *__restrict__ part_o,
                                                                             const float *__restrict__ part_ml,
                                                                             int n_split, int H, int groups,
-                                                                            float *out, float *lse,
+                                                                            OutT *out, float *lse,
                                                                             unsigned long long *timeline) {
     __shared__ float wgt[128];
     __shared__ float ml[2][128];
@@ -685,7 +685,14 @@ __global__ void __launch_bounds__(128, NF <= 4 ? 16 : 5) attn_combine_kernel(con
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-    reinterpret_cast<float4 *>(out + ((int64_t)t * H + h) * D_L)[threadIdx.x] = acc;
+    OutT *dst = out + ((int64_t)t * H + h) * D_L;
+    if constexpr (sizeof(OutT) == 4) {
+        reinterpret_cast<float4 *>(dst)[threadIdx.x] = acc;
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), c = __floats2bfloat162_rn(acc.z, acc.w);
+        reinterpret_cast<uint2 *>(dst)[threadIdx.x] =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+    }
     if (lse && threadIdx.x == 0)
         lse[(int64_t)t * H + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     __syncthreads();
@@ -728,16 +735,26 @@ cudaError_t launch_sparse_attn(const AttnLaunch &a, const CUtensorMap &q_lat_map
     return launch_k(sparse_attn_kernel, grid, dim3(kThreads), smem, stream, pdl, p, q_lat_map, q_rope_map, kv_map);
 }
 
+namespace {
+
+template <int NF, typename OutT>
+cudaError_t launch_combine_as(const AttnLaunch &a, OutT *out, const DevBatch &b, cudaStream_t stream, bool pdl) {
+    const int groups = (a.H + kHeads - 1) / kHeads;
+    dim3 grid((unsigned)b.T, (unsigned)a.H);
+    return launch_k(attn_combine_kernel<NF, OutT>, grid, dim3(128), 0, stream, pdl, (const uint16_t *)a.part_o,
+                    (const float *)a.part_ml, a.n_split, a.H, groups, out, a.lse, b.timeline);
+}
+
+}  // namespace
+
 cudaError_t launch_attn_combine(const AttnLaunch &a, const DevBatch &b, cudaStream_t stream, bool pdl) {
     if (a.n_split <= 1) return cudaSuccess;
     if (a.n_split > 128) return cudaErrorInvalidConfiguration;
-    const int groups = (a.H + kHeads - 1) / kHeads;
-    dim3 grid((unsigned)b.T, (unsigned)a.H);
-    if (a.n_split <= 4)
-        return launch_k(attn_combine_kernel<4>, grid, dim3(128), 0, stream, pdl, (const uint16_t *)a.part_o,
-                        (const float *)a.part_ml, a.n_split, a.H, groups, a.out, a.lse, b.timeline);
-    return launch_k(attn_combine_kernel<16>, grid, dim3(128), 0, stream, pdl, (const uint16_t *)a.part_o,
-                    (const float *)a.part_ml, a.n_split, a.H, groups, a.out, a.lse, b.timeline);
+    if (a.out16) {
+        uint16_t *o = static_cast<uint16_t *>(a.out16);
+        return a.n_split <= 4 ? launch_combine_as<4>(a, o, b, stream, pdl) : launch_combine_as<16>(a, o, b, stream, pdl);
+    }
+    return a.n_split <= 4 ? launch_combine_as<4>(a, a.out, b, stream, pdl) : launch_combine_as<16>(a, a.out, b, stream, pdl);
 }
 
 }  // namespace dsa

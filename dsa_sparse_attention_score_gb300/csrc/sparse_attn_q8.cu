@@ -3,9 +3,43 @@
 //     z_j = sm_scale * (q_lat . c_j + q_rope . r_j),  o = sum_j softmax(z)_j c_j,
 // c_j = 2^E_j codes_j[0:512], r_j = 2^E_j (hi_j + lo_j).
 //
-// The plain kernel: a CTA takes one token and eight heads, one warp per head;
-// rows are decoded sixteen at a time into shared memory, and each warp keeps
-// its head's query, running maximum, sum and output in registers.
+// The tensor cores read the codes as they lie in the cache; no row is ever
+// decoded.  What makes that possible:
+//  - The row's scale leaves both contractions.  z_j = 2^E_j (codes_j . q), and
+//    with u_j = z_j log2(e) + E_j the output is sum_j 2^(u_j - M) codes_j over
+//    l = sum_j 2^(z_j log2(e) - M): the scale is folded into the weights (E_j = log2 of the scale: a power of two is not
+//    needed here).
+//  - A bf16 query is the sum of two e4m3 pieces: q 2^-e = hi + lo with
+//    hi = e4m3(q 2^-e), lo = e4m3(q 2^-e - hi).  Four significant bits each,
+//    the remainder signed, hold bf16's eight: the split is exact for values
+//    above 2^-10 of the head's largest, and off by 2^-19 of it below.
+//  - A weight is split the same way, in units where the largest lies in
+//    [2^5, 2^8]: each is off by at most 2^-8 of itself (half a bf16 step) or
+//    2^-15 of the largest.
+// So every product is 8-bit by 8-bit with float32 sums, at twice the rate of
+// bf16 products and half the bytes: the two pieces cost what one bf16 product
+// would, and the rows come in at 644 bytes instead of 1152.
+//
+// One CTA per (token, head group of 64, split) walks tiles of 128 selected
+// rows.  A tile is five 16 KB blocks of 128 rows x 128 bytes (SWIZZLE_128B):
+// four of latent codes, one of the tail (64 hi | 64 lo).
+//     S^T[row, piece*head]  = C[row, :] . Q[piece*head, :]^T   M=128, N=128, K=512 + 128
+//     O^T[dim, head]       += C[row, dim]^T . P^T[row, head]   4 x M=128, N=64, K=128, both pieces
+// The same bytes are the K-major A operand of S^T and the MN-major A operand
+// of O^T.  The tail's two halves multiply the same 64 query values, so its
+// four K steps read the two of q_rope twice.  S^T accumulates a head's two
+// pieces in columns h and 64 + h, which the softmax adds; O^T adds both pieces of
+// P^T in place.  The tail block is dead once S^T is computed and holds P^T.
+//
+// Shared memory: queries 72 KB and a ring of nine blocks (144 KB), one short
+// of two tiles: a tile's last block is gathered when the first value product of the
+// tile before has freed its slot.  One producer warp per block of the tile
+// gathers it with 16-byte cp.async copies (a row's 128 bytes are one cache
+// line; masked rows are filled with zeros and read nothing), so up to five
+// blocks are in flight.  The MMA thread issues score blocks and value
+// products as their inputs arrive; eight softmax warps (two per TMEM lane
+// quarter, 32 heads each) turn a tile's S^T into P^T.  The running maximum of
+// u is raised only when a tile exceeds it by 2^3.
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 #include "quant8.cuh"
@@ -14,94 +48,580 @@ namespace dsa {
 
 namespace {
 
-constexpr int kHeadsPerCta = 8;
-constexpr int kChunk = 16;              // rows decoded at a time
+constexpr int kHeads = 64;                    // heads per CTA (padded)
+constexpr int kRows = 128;                    // selected rows per tile
+constexpr int kBlockBytes = kRows * 128;      // 16 KB
+constexpr int kTileBlocks = 5;                // 4 latent + the tail (P^T)
+constexpr int kSlots = 9;
+constexpr int kQBlockBytes = 2 * kHeads * 128;        // hi and lo rows of 128 codes
+constexpr int kQTailBytes = 2 * kHeads * 64;          // hi and lo rows of 64 codes (SWIZZLE_64B)
+constexpr int kQBytes = 4 * kQBlockBytes + kQTailBytes;
+constexpr int kPieceBytes = kRows * 64;       // one piece of P^T (SWIZZLE_64B)
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kMmaWarp = 8;
+constexpr int kProducerWarps = kTileBlocks;   // warps 9..13
+constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kProducerWarps);
+constexpr float kTopLog2 = 5.0f;              // a new maximum's weight is 2^5 ...
+constexpr float kRaiseLog2 = 8.0f;            // ... and none exceeds 2^8
+constexpr float kMinScale = 0x1p-40f;
+constexpr uint32_t kTmemCols = 512;           // S^T: 2 x 128 columns, O^T: 4 x 64
+constexpr uint32_t kColS = 0;
+constexpr uint32_t kColO = 256;
+
+struct Params {
+    const uint16_t *q_lat, *q_rope;
+    const uint8_t *codes;
+    const float *scale;
+    const int32_t *idx;
+    void *out;
+    float *lse;
+    uint16_t *part_o;        // [T, n_split, groups, 64, 512] bf16, unnormalised
+    float *part_ml;          // [T, n_split, groups, 64, 2]
+    DevBatch b;
+    uint32_t *status;
+    int H, k, groups, out_bf16;
+    float scale_log2;        // sm_scale * log2(e)
+    int tiles_per_cta, n_split, n_tiles;
+};
+
+struct Ctl {
+    uint64_t q_full;
+    uint64_t full[kSlots];
+    uint64_t empty[kSlots];
+    uint64_t s_full[2];
+    uint64_t p_full[2];
+    uint64_t o_full;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    float qs[kHeads];        // 2^e of the head's query times scale_log2
+    float red[4][kHeads];
+    float m[kHeads];
+    float2 ma[kHeads];       // (m, alpha) of the current tile; m = 0 while there is none
+    int32_t resc[2];
+    float l[kHeads];
+    float inv_l[kHeads];
+    int32_t warp_alive[kSoftmaxWarps];
+};
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
+    if (*(volatile int32_t *)&c.abort_flag) return false;
+    if (mbar_wait(bar, parity, limit_ns)) return true;
+    *(volatile int32_t *)&c.abort_flag = 1;
+    flag(status, DSA_DEV_TIMEOUT);
+    return false;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Transposing butterfly: each lane holds 32 values, lane L ends up with the
+// reduction of value L over the warp.
+template <bool kMax>
+__device__ __forceinline__ float warp_reduce_32(const float (&x)[32], int lane) {
+    float a[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) a[i] = x[i];
+#pragma unroll
+    for (int half = 16; half >= 1; half >>= 1) {
+        const bool up = lane & half;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i < half) {
+                const float keep = up ? a[half + i] : a[i];
+                const float send = up ? a[i] : a[half + i];
+                const float o = __shfl_xor_sync(0xffffffffu, send, half);
+                a[i] = kMax ? fmaxf(keep, o) : keep + o;
+            }
+        }
+    }
+    return a[0];
+}
+
+// 16 bf16 values in two words of four.
+__device__ __forceinline__ void bf16x16(const uint4 &a, const uint4 &b, float (&v)[16]) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+// The two e4m3 pieces of sixteen values.
+__device__ __forceinline__ void split16(const float (&v)[16], float inv, uint4 &hi, uint4 &lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = v[4 * i] * inv, b = v[4 * i + 1] * inv, c = v[4 * i + 2] * inv, d = v[4 * i + 3] * inv;
+        const uint32_t h0 = e4m3x2(a, b), h1 = e4m3x2(c, d);
+        const float2 f0 = e4m3x2_to_float2(h0), f1 = e4m3x2_to_float2(h1);
+        h[i] = h0 | h1 << 16;
+        l[i] = e4m3x2(a - f0.x, b - f0.y) | e4m3x2(c - f1.x, d - f1.y) << 16;
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
 
 }  // namespace
 
-__global__ void __launch_bounds__(32 * kHeadsPerCta) sparse_attn_q8_kernel(const AttnQ8Launch p, const DevBatch b, uint32_t *status) {
-    __shared__ float rows[kChunk][D_ROW];
-    __shared__ int64_t at[kChunk];
-    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y * kHeadsPerCta + warp;
+__global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *ring = base;
+    uint8_t *q_s = base + kSlots * kBlockBytes;          // four latent blocks, then the tail's
+    Ctl &ctl = *reinterpret_cast<Ctl *>(q_s + kQBytes);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const DevBatch &b = p.b;
+    const int t = blockIdx.x / p.groups;
+    const int hg = blockIdx.x - t * p.groups;
+    const int h0 = hg * kHeads, nh = min(kHeads, p.H - h0);
+    const int split = blockIdx.y;
     const bool tail = p.q_rope != nullptr;
+    const int width = tail ? kQ8Row : D_L;               // bytes per cached row
+    const int64_t part_idx = ((int64_t)t * p.n_split + split) * p.groups + hg;
+    tl_start(b.timeline, kTlAttn);
     const int pos = __ldg(b.q_pos + t);
     const int seq = seq_of_warp(b.cu_q, b.B, t, lane);
     const int64_t kv0 = seq_base(b, seq);
-    int64_t own = -1;
-    if (pos >= 0 && pos < b.max_kv && kv0 >= 0) own = cache_row(b, seq, kv0, pos);
-    const bool ok = own >= 0 && own < b.cache_rows;
-    if (!ok && threadIdx.x == 0 && blockIdx.y == 0) flag(status, DSA_DEV_BAD_POSITION);
-    float q[18], acc[16], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    const int64_t qrow = (int64_t)t * p.H + h;
-    if (h < p.H) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = __bfloat162float(__ushort_as_bfloat16(p.q_lat[qrow * D_L + lane + 32 * i]));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) q[16 + i] = tail ? __bfloat162float(__ushort_as_bfloat16(p.q_rope[qrow * D_R + lane + 32 * i])) : 0.f;
-    }
-    const int width = tail ? kQ8Row : D_L;
-    for (int j0 = 0; ok && j0 < p.k; j0 += kChunk) {
-        const int n = min(kChunk, p.k - j0);
-        if (threadIdx.x < kChunk) {
-            int64_t row = -1;
-            const int v = (int)threadIdx.x < n ? __ldg(p.idx + (int64_t)t * p.k + j0 + threadIdx.x) : -1;
-            if (v >= 0 && v <= pos) row = cache_row(b, seq, kv0, v);
-            if (row >= b.cache_rows) row = -1;
-            if (row < 0 && v != -1 && blockIdx.y == 0) flag(status, DSA_DEV_BAD_INDEX);
-            at[threadIdx.x] = row;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < n * D_ROW; i += 32 * kHeadsPerCta) {
-            const int r = i / D_ROW, d = i - r * D_ROW;
-            const int64_t row = at[r];
-            float v = 0.f;
-            if (row >= 0 && (tail || d < D_L)) {
-                const uint8_t *src = p.codes + row * width;
-                v = e4m3x2_to_float2(src[d]).x;
-                if (d >= D_L) v += e4m3x2_to_float2(src[d + D_R]).x;
-                v *= p.scale[row];
+    const int tile_lo = split * p.tiles_per_cta;
+    const int tile_hi = min(p.n_tiles, tile_lo + p.tiles_per_cta);
+    int64_t own_row = -1;
+    if (pos >= 0 && pos < b.max_kv && kv0 >= 0) own_row = cache_row(b, seq, kv0, pos);
+    const bool pos_ok = own_row >= 0 && own_row < b.cache_rows;
+    if (!pos_ok || tile_lo >= tile_hi) {
+        if (!pos_ok && threadIdx.x == 0 && split == 0) flag(p.status, DSA_DEV_BAD_POSITION);
+        if (p.n_split > 1) {
+            for (int i = threadIdx.x; i < kHeads * D_L / 2; i += kThreads)
+                reinterpret_cast<uint32_t *>(p.part_o + part_idx * kHeads * D_L)[i] = 0u;
+            if (threadIdx.x < kHeads) {
+                float *ml = p.part_ml + (part_idx * kHeads + threadIdx.x) * 2;
+                ml[0] = -INFINITY;
+                ml[1] = 0.f;
             }
-            rows[r][d] = v;
+        } else {
+            const int64_t o = ((int64_t)t * p.H + h0) * D_L;
+            for (int i = threadIdx.x; i < nh * D_L; i += kThreads) {
+                if (p.out_bf16) static_cast<uint16_t *>(p.out)[o + i] = 0;
+                else static_cast<float *>(p.out)[o + i] = 0.f;
+            }
+            if (p.lse && threadIdx.x < nh) p.lse[(int64_t)t * p.H + h0 + threadIdx.x] = -INFINITY;
         }
-        __syncthreads();
-        if (h < p.H) {
-            for (int r = 0; r < n; ++r) {
-                if (at[r] < 0) continue;
-                float z = 0.f, c[16];
+        return;
+    }
+    const int n_my = tile_hi - tile_lo;
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&ctl.q_full), kSoftmaxWarps);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(smem_u32(&ctl.full[i]), 32);
+            mbar_init(smem_u32(&ctl.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl.s_full[i]), 1);
+            mbar_init(smem_u32(&ctl.p_full[i]), kSoftmaxWarps);
+        }
+        mbar_init(smem_u32(&ctl.o_full), 1);
+        ctl.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem_base;
+    const int32_t *idx_row = p.idx + (int64_t)t * p.k;
+    // Cache row of entry e of the token's selection: -1 for padding and for
+    // entries out of range (flagged by one thread per entry).
+    auto row_of = [&](int e, bool report) -> int32_t {
+        const int32_t v = e < p.k ? __ldg(idx_row + e) : -1;
+        int64_t row = -1;
+        if (v >= 0 && v <= pos) row = cache_row(b, seq, kv0, v);
+        if (row >= b.cache_rows) row = -1;
+        if (row < 0 && v != -1 && report) flag(p.status, DSA_DEV_BAD_INDEX);
+        return (int32_t)row;
+    };
+
+    if (warp > kMmaWarp) {
+        // ---------------- producers: warp j gathers block j of every tile.
+        // Rows without a tail have nothing to gather into the fifth: its warp
+        // only passes the free slot on to the softmax, which puts P^T there.
+        const int j = warp - kMmaWarp - 1;
+        const bool copy = (j < 4 || tail) && !b.skip_copies;
+        const uint8_t *src = p.codes + j * 128 + (lane & 7) * 16;
+        // lane's chunk of rows 4 g + lane / 8; g odd flips bit 2 of the swizzled chunk
+        const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
+        pdl_wait();                                  // the indices come from the preceding kernel
+        for (int it = 0; it < n_my; ++it) {
+            const uint32_t n = (uint32_t)(kTileBlocks * it + j), slot = n % kSlots, use = n / kSlots;
+            int32_t my_row[4] = {-1, -1, -1, -1};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) { c[i] = rows[r][lane + 32 * i]; z += c[i] * q[i]; }
-                z += rows[r][D_L + lane] * q[16] + rows[r][D_L + lane + 32] * q[17];
+            for (int q = 0; q < 4 && (j < 4 || tail); ++q) my_row[q] = row_of((tile_lo + it) * kRows + 32 * q + lane, j == 0);
+            if (!wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns)) break;
+            if (!copy) {
+                if (!b.skip_copies) mbar_arrive(smem_u32(&ctl.full[slot]));
+                continue;
+            }
+            const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                z *= p.sm_scale;
-                const float mn = fmaxf(m, z), al = __expf(m - mn), w = __expf(z - mn);
-                l = l * al + w;
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = acc[i] * al + w * c[i];
-                m = mn;
+                for (int g = 0; g < 8; ++g) {
+                    const int32_t row = __shfl_sync(0xffffffffu, my_row[q], 4 * g + (lane >> 3));
+                    cp_async16_or_zero((dst + (uint32_t)(8 * q + g) * 512u) ^ ((uint32_t)(g & 1) << 6),
+                                       src + (int64_t)max(row, 0) * width, row < 0 ? 0u : 16u);
+                }
+            cp_async_commit();
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&ctl.full[slot]));
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------- MMA issuer: value products first (they free slots),
+        // then the next score block whose codes have landed.
+        if (lane == 0 && wait_bar(smem_u32(&ctl.q_full), 0, ctl, p.status, b.wait_ns) &&
+            wait_bar(smem_u32(&ctl.full[0]), 0, ctl, p.status, b.wait_ns)) {
+            const uint32_t id_s = idesc_e4m3(kRows, 2 * kHeads, false, false);
+            const uint32_t id_o = idesc_e4m3(128, kHeads, true, true);
+            const uint32_t ra = smem_u32(ring), qa = smem_u32(q_s);
+            const uint64_t s_a0 = sdesc_sw128(ra, 16, 1024), s_b0 = sdesc_sw128(qa, 16, 1024);
+            const uint64_t s_bt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
+            const uint64_t o_a0 = sdesc_sw128(ra, 16, 1024), o_b0 = sdesc_sw64(ra, 16, 512);
+            const int s_blocks = tail ? kTileBlocks : kTileBlocks - 1;
+            int s_it = 0, s_j = 0, o_it = 0;
+            uint64_t t_last = global_ns();
+            while (o_it < n_my) {
+                bool progress = false;
+                if (o_it < s_it && mbar_test(smem_u32(&ctl.p_full[o_it & 1]), (uint32_t)(o_it >> 1) & 1u)) {
+                    tc_fence_after();
+                    const uint32_t n0 = (uint32_t)(kTileBlocks * o_it);
+                    const uint64_t bd = o_b0 + (uint64_t)(((n0 + 4) % kSlots) * (kBlockBytes >> 4));
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t slot = (n0 + c) % kSlots;
+                        const uint64_t ad = o_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+                        const uint32_t d_o = tmem + kColO + c * kHeads;
+#pragma unroll
+                        for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+                            for (int ks = 0; ks < kRows / 32; ++ks)
+                                umma_f8(d_o, ad + (uint64_t)(ks * (32 * 128 >> 4)),
+                                        bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), id_o,
+                                        (o_it > 0 || piece || ks) ? 1u : 0u);
+                        umma_commit(smem_u32(&ctl.empty[slot]));
+                    }
+                    umma_commit(smem_u32(&ctl.empty[(n0 + 4) % kSlots]));
+                    umma_commit(smem_u32(&ctl.o_full));
+                    ++o_it;
+                    progress = true;
+                } else if (s_it < n_my && s_it <= o_it + 1) {
+                    const uint32_t n = (uint32_t)(kTileBlocks * s_it + s_j), slot = n % kSlots;
+                    if (mbar_test(smem_u32(&ctl.full[slot]), (n / kSlots) & 1u)) {
+                        tc_fence_after();
+                        const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+                        const uint32_t d_s = tmem + kColS + (s_it & 1) * 2 * kHeads;
+                        if (s_j < 4) {
+                            const uint64_t bd = s_b0 + (uint64_t)(s_j * (kQBlockBytes >> 4));
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)(ks * 2), id_s, (s_j | ks) ? 1u : 0u);
+                        } else {
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                umma_f8(d_s, ad + (uint64_t)(ks * 2), s_bt + (uint64_t)((ks & 1) * 2), id_s, 1u);
+                        }
+                        if (++s_j == s_blocks) {
+                            umma_commit(smem_u32(&ctl.s_full[s_it & 1]));
+                            s_j = 0;
+                            ++s_it;
+                        }
+                        progress = true;
+                    }
+                }
+                if (progress) {
+                    t_last = global_ns();
+                } else if (*(volatile int32_t *)&ctl.abort_flag) {
+                    break;
+                } else if (global_ns() - t_last > b.wait_ns) {
+                    *(volatile int32_t *)&ctl.abort_flag = 1;
+                    flag(p.status, DSA_DEV_TIMEOUT);
+                    break;
+                }
             }
         }
-        __syncthreads();
-    }
-    if (h >= p.H) return;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    } else {
+        // ---------------- queries, softmax and epilogue (warps 0..7)
+        const int tx = (int)threadIdx.x;
+        const int quarter = warp & 3;                      // TMEM lanes 32*quarter ..
+        const int part = warp >> 2;                        // heads 32*part ..
+        const int hb = 32 * part;
+        const int r = quarter * 32 + lane;                 // row within the tile
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        if (tx < kHeads) ctl.m[tx] = -INFINITY;
+        // each warp splits eight heads' queries: lane l the values 16 l .. 16 l + 15
+#pragma unroll 2
+        for (int i = 0; i < kHeads / kSoftmaxWarps; ++i) {
+            const int h = warp * (kHeads / kSoftmaxWarps) + i;
+            uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a, ra = a, rc = a;
+            if (h < nh) {
+                const int64_t row = (int64_t)t * p.H + h0 + h;
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * D_L) + 2 * lane;
+                a = __ldg(src);
+                c = __ldg(src + 1);
+                if (tail && lane < 4) {
+                    const uint4 *rs = reinterpret_cast<const uint4 *>(p.q_rope + row * D_R) + 2 * lane;
+                    ra = __ldg(rs);
+                    rc = __ldg(rs + 1);
+                }
+            }
+            float v[16], w[16];
+            bf16x16(a, c, v);
+            bf16x16(ra, rc, w);
+            uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t o = qrow * D_L + lane + 32 * i;
-        if (p.out_bf16) static_cast<uint16_t *>(p.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i] * inv));
-        else static_cast<float *>(p.out)[o] = acc[i] * inv;
+            for (int k = 0; k < 16; ++k) top = max(top, max(__float_as_uint(v[k]) & 0x7FFFFFFFu, __float_as_uint(w[k]) & 0x7FFFFFFFu));
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int e = q8_exponent(__uint_as_float(top));
+            const float inv = exp2_int(-e);
+            uint4 hi, lo;
+            split16(v, inv, hi, lo);
+            uint8_t *blk = q_s + (lane >> 3) * kQBlockBytes;
+            *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)h, (uint32_t)(lane & 7))) = hi;
+            *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(kHeads + h), (uint32_t)(lane & 7))) = lo;
+            if (lane < 4) {
+                split16(w, inv, hi, lo);
+                uint8_t *tb = q_s + 4 * kQBlockBytes;
+                *reinterpret_cast<uint4 *>(tb + sw64_offset((uint32_t)h, (uint32_t)lane)) = hi;
+                *reinterpret_cast<uint4 *>(tb + sw64_offset((uint32_t)(kHeads + h), (uint32_t)lane)) = lo;
+            }
+            if (lane == 0) ctl.qs[h] = h < nh ? exp2_int(e) * p.scale_log2 : 0.f;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full));
+        pdl_wait();
+        bool alive = true;
+        named_barrier(1, kSoftmaxThreads);
+        float lpart[32];
+#pragma unroll
+        for (int h = 0; h < 32; ++h) lpart[h] = 0.f;
+        // Scale of this thread's row of a tile (0: masked), looked up a tile
+        // ahead.  Any positive scale will do; a row never written (scale 0)
+        // counts as zeros at the smallest one.
+        auto scale_of = [&](int it) -> float {
+            const int32_t row = row_of((tile_lo + it) * kRows + r, false);
+            if (row < 0) return 0.f;
+            const float s = __ldg(p.scale + row);
+            return s < kMinScale ? kMinScale : s;
+        };
+        float next_scale = scale_of(0);
+        // Every softmax thread runs the same sequence of named barriers whatever
+        // happens; `alive` (warp-uniform) only gates tensor-memory and shared
+        // memory work after a bounded wait gave up.
+        for (int it = 0; it < n_my; ++it) {
+            const int buf = it & 1;
+            const float rs = next_scale;
+            if (it + 1 < n_my) next_scale = scale_of(it + 1);
+            const bool valid = rs != 0.f;
+            const float ef = valid ? log2f(rs) : 0.f;
+            const float irs = valid ? 1.f / rs : 0.f;
+            if (alive) alive = wait_bar(smem_u32(&ctl.s_full[buf]), (uint32_t)(it >> 1) & 1u, ctl, p.status, b.wait_ns);
+            alive = __all_sync(0xffffffffu, alive);
+            float x[32];
+            if (alive) {
+                tc_fence_after();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t u[16], w[16];
+                    const uint32_t a = tmem + lane_addr + kColS + buf * 2 * kHeads + hb + 16 * half;
+                    tmem_ld16(a, u);
+                    tmem_ld16(a + kHeads, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < 16; ++h)
+                        x[16 * half + h] = valid ? (__uint_as_float(u[h]) + __uint_as_float(w[h])) * rs * ctl.qs[hb + 16 * half + h] + ef
+                                                 : -INFINITY;
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 32; ++h) x[h] = -INFINITY;
+            }
+            ctl.red[quarter][hb + lane] = warp_reduce_32<true>(x, lane);
+            named_barrier(1, kSoftmaxThreads);
+            if (tx < kHeads) {
+                const float tmax = fmaxf(fmaxf(ctl.red[0][tx], ctl.red[1][tx]), fmaxf(ctl.red[2][tx], ctl.red[3][tx]));
+                const float mo = ctl.m[tx];
+                float mn = mo, al = 1.f;
+                if (tmax != -INFINITY && (mo == -INFINITY || tmax > mo + kRaiseLog2)) {
+                    mn = tmax - kTopLog2;
+                    al = mo == -INFINITY ? 0.f : exp2f(mo - mn);
+                }
+                ctl.m[tx] = mn;
+                ctl.ma[tx] = make_float2(mn == -INFINITY ? 0.f : mn, al);
+                const bool any = __any_sync(0xffffffffu, al != 1.f);
+                if (lane == 0) ctl.resc[warp] = any ? 1 : 0;
+            }
+            named_barrier(1, kSoftmaxThreads);
+            const bool rescale = ctl.resc[0] | ctl.resc[1];
+            if (rescale) {
+#pragma unroll
+                for (int h = 0; h < 32; ++h) lpart[h] *= ctl.ma[hb + h].y;
+            }
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    w[q] = ex2(x[4 * i + q] - ctl.ma[hb + 4 * i + q].x);
+                    lpart[4 * i + q] = fmaf(w[q], irs, lpart[4 * i + q]);
+                }
+                const uint32_t a = e4m3x2(w[0], w[1]), c = e4m3x2(w[2], w[3]);
+                const float2 fa = e4m3x2_to_float2(a), fc = e4m3x2_to_float2(c);
+                hi[i] = a | c << 16;
+                lo[i] = e4m3x2(w[0] - fa.x, w[1] - fa.y) | e4m3x2(w[2] - fc.x, w[3] - fc.y) << 16;
+            }
+            const uint32_t pn = (uint32_t)(kTileBlocks * it + 4), pslot = pn % kSlots;
+            if (!tail && alive) {
+                // no score product has waited for this slot
+                alive = wait_bar(smem_u32(&ctl.full[pslot]), (pn / kSlots) & 1u, ctl, p.status, b.wait_ns);
+                alive = __all_sync(0xffffffffu, alive);
+            }
+            if (alive) {
+                uint8_t *pb = ring + pslot * kBlockBytes;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t o = sw64_offset((uint32_t)r, (uint32_t)(2 * part + i));
+                    *reinterpret_cast<uint4 *>(pb + o) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+                    *reinterpret_cast<uint4 *>(pb + kPieceBytes + o) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                }
+            }
+            if (rescale && it > 0) {
+                if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (uint32_t)(it - 1) & 1u, ctl, p.status, b.wait_ns);
+                alive = __all_sync(0xffffffffu, alive);
+                if (alive) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int cq = 0; cq < 8; ++cq) {             // 4 dim blocks x 2 groups of 16 heads
+                        uint32_t u[16];
+                        const int hq = hb + (cq & 1) * 16;
+                        const uint32_t addr = tmem + lane_addr + kColO + (cq >> 1) * kHeads + hq;
+                        tmem_ld16(addr, u);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) * ctl.ma[hq + q].y);
+                        tmem_st16(addr, u);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[buf]));
+        }
+        // ---- final: O^T of the last tile, row sums, outputs
+        if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (uint32_t)(n_my - 1) & 1u, ctl, p.status, b.wait_ns);
+        alive = __all_sync(0xffffffffu, alive);
+        ctl.red[quarter][hb + lane] = warp_reduce_32<false>(lpart, lane);
+        named_barrier(1, kSoftmaxThreads);
+        if (tx < kHeads) {
+            const float l = ctl.red[0][tx] + ctl.red[1][tx] + ctl.red[2][tx] + ctl.red[3][tx];
+            ctl.l[tx] = l;
+            ctl.inv_l[tx] = ctl.m[tx] == -INFINITY ? 0.f : 1.f / l;
+        }
+        if (lane == 0) ctl.warp_alive[warp] = alive ? 1 : 0;
+        named_barrier(1, kSoftmaxThreads);
+        bool all_alive = true;
+#pragma unroll
+        for (int w = 0; w < kSoftmaxWarps; ++w) all_alive = all_alive && ctl.warp_alive[w];
+        if (all_alive) {
+            // thread (quarter, lane) holds output dim 128 c + 32 quarter + lane
+            // of every head; the two warps of a quarter store 32 heads each
+            tc_fence_after();
+            const int rd = quarter * 32 + lane;
+            const int64_t o = ((int64_t)t * p.H + h0) * D_L;
+            uint16_t *po = p.n_split > 1 ? p.part_o + part_idx * kHeads * D_L : nullptr;
+#pragma unroll 1
+            for (int cq = 0; cq < 8; ++cq) {
+                const int hq = hb + (cq & 1) * 16, d = (cq >> 1) * 128 + rd;
+                uint32_t u[16];
+                tmem_ld16(tmem + lane_addr + kColO + (cq >> 1) * kHeads + hq, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const int h = hq + q;
+                    const float v = __uint_as_float(u[q]);
+                    if (po) {
+                        po[h * D_L + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                    } else if (h < nh) {
+                        if (p.out_bf16) static_cast<uint16_t *>(p.out)[o + h * D_L + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v * ctl.inv_l[h]));
+                        else static_cast<float *>(p.out)[o + h * D_L + d] = v * ctl.inv_l[h];
+                    }
+                }
+            }
+            if (tx < kHeads) {
+                const float l = ctl.l[tx], m = ctl.m[tx];
+                if (po) {
+                    float *ml = p.part_ml + (part_idx * kHeads + tx) * 2;
+                    ml[0] = m;
+                    ml[1] = l;
+                } else if (p.lse && tx < nh) {
+                    p.lse[(int64_t)t * p.H + h0 + tx] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                }
+            }
+        }
     }
-    if (p.lse && lane == 0) p.lse[qrow] = l > 0.f ? m + logf(l) : -INFINITY;
+
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    pdl_trigger();
+    tl_end(b.timeline, kTlAttn);
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
 }
 
+int attn_q8_tile_rows() { return kRows; }
+
 cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream, bool pdl) {
-    (void)pdl;
-    dim3 grid((unsigned)b.T, (unsigned)((a.H + kHeadsPerCta - 1) / kHeadsPerCta));
-    sparse_attn_q8_kernel<<<grid, 32 * kHeadsPerCta, 0, stream>>>(a, b, status);
-    return cudaGetLastError();
+    Params p{};
+    p.q_lat = a.q_lat;
+    p.q_rope = a.q_rope;
+    p.codes = a.codes;
+    p.scale = a.scale;
+    p.idx = a.idx;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.part_o = a.part_o;
+    p.part_ml = a.part_ml;
+    p.b = b;
+    p.status = status;
+    p.H = a.H;
+    p.k = a.k;
+    p.groups = (a.H + kHeads - 1) / kHeads;
+    p.out_bf16 = a.out_bf16;
+    p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+    p.tiles_per_cta = a.tiles_per_cta;
+    p.n_split = a.n_split;
+    p.n_tiles = (a.k + kRows - 1) / kRows;
+    const size_t smem = 1024 + kSlots * kBlockBytes + kQBytes + sizeof(Ctl);
+    static_assert(1024 + kSlots * kBlockBytes + kQBytes + sizeof(Ctl) <= 232448, "one CTA's shared memory");
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(sparse_attn_q8_kernel), 11, smem);
+    if (e != cudaSuccess) return e;
+    if (a.n_split > 65535 || p.groups < 1 || p.groups > 2 || (int64_t)b.T * p.groups > 0x7fffffff)
+        return cudaErrorInvalidConfiguration;
+    return launch_k(sparse_attn_q8_kernel, dim3((unsigned)(b.T * p.groups), (unsigned)a.n_split), dim3(kThreads), smem, stream,
+                    pdl, p);
 }
 
 }  // namespace dsa
