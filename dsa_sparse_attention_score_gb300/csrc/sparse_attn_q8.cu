@@ -64,6 +64,7 @@ constexpr int kProducerWarps = kTileBlocks;   // warps 9..13
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kProducerWarps);
 constexpr float kTopLog2 = 5.0f;              // a new maximum's weight is 2^5 ...
 constexpr float kRaiseLog2 = 8.0f;            // ... and none exceeds 2^8
+constexpr int kFewMoved = 6;                  // heads of 32 rescaled one by one
 constexpr float kMinScale = 0x1p-40f;
 constexpr uint32_t kTmemCols = 512;           // S^T: 2 x 128 columns, O^T: 4 x 64
 constexpr uint32_t kColS = 0;
@@ -98,7 +99,7 @@ struct Ctl {
     float red[4][kHeads];
     float m[kHeads];
     float2 ma[kHeads];       // (m, alpha) of the current tile; m = 0 while there is none
-    int32_t resc[2];
+    uint32_t resc[2];        // heads 0..31 / 32..63 whose maximum moved in this tile
     float l[kHeads];
     float inv_l[kHeads];
     int32_t warp_alive[kSoftmaxWarps];
@@ -285,71 +286,84 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
         }
     } else if (warp == kMmaWarp) {
         // ---------------- MMA issuer: value products first (they free slots),
-        // then the next score block whose codes have landed.
-        if (lane == 0 && wait_bar(smem_u32(&ctl.q_full), 0, ctl, p.status, b.wait_ns) &&
+        // then the next score block whose codes have landed.  The whole warp
+        // runs the loop (uniform descriptors); one elected lane issues.
+        if (wait_bar(smem_u32(&ctl.q_full), 0, ctl, p.status, b.wait_ns) &&
             wait_bar(smem_u32(&ctl.full[0]), 0, ctl, p.status, b.wait_ns)) {
+            __syncwarp();
             const uint32_t id_s = idesc_e4m3(kRows, 2 * kHeads, false, false);
             const uint32_t id_o = idesc_e4m3(128, kHeads, true, true);
             const uint32_t ra = smem_u32(ring), qa = smem_u32(q_s);
             const uint64_t s_a0 = sdesc_sw128(ra, 16, 1024), s_b0 = sdesc_sw128(qa, 16, 1024);
             const uint64_t s_bt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
-            const uint64_t o_a0 = sdesc_sw128(ra, 16, 1024), o_b0 = sdesc_sw64(ra, 16, 512);
+            const uint64_t o_b0 = sdesc_sw64(ra, 16, 512);
             const int s_blocks = tail ? kTileBlocks : kTileBlocks - 1;
             int s_it = 0, s_j = 0, o_it = 0;
             uint64_t t_last = global_ns();
             while (o_it < n_my) {
                 bool progress = false;
-                if (o_it < s_it && mbar_test(smem_u32(&ctl.p_full[o_it & 1]), (uint32_t)(o_it >> 1) & 1u)) {
+                if (o_it < s_it && __any_sync(0xffffffffu, mbar_test(smem_u32(&ctl.p_full[o_it & 1]), (uint32_t)(o_it >> 1) & 1u))) {
                     tc_fence_after();
                     const uint32_t n0 = (uint32_t)(kTileBlocks * o_it);
                     const uint64_t bd = o_b0 + (uint64_t)(((n0 + 4) % kSlots) * (kBlockBytes >> 4));
+                    const uint32_t acc0 = o_it > 0 ? 1u : 0u;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t slot = (n0 + c) % kSlots;
-                        const uint64_t ad = o_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+                        const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
                         const uint32_t d_o = tmem + kColO + c * kHeads;
+                        const uint32_t bar = smem_u32(&ctl.empty[slot]);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int piece = 0; piece < 2; ++piece)
+                            for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
-                            for (int ks = 0; ks < kRows / 32; ++ks)
-                                umma_f8(d_o, ad + (uint64_t)(ks * (32 * 128 >> 4)),
-                                        bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), id_o,
-                                        (o_it > 0 || piece || ks) ? 1u : 0u);
-                        umma_commit(smem_u32(&ctl.empty[slot]));
+                                for (int ks = 0; ks < kRows / 32; ++ks)
+                                    umma_f8(d_o, ad + (uint64_t)(ks * (32 * 128 >> 4)),
+                                            bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), id_o,
+                                            (piece || ks) ? 1u : acc0);
+                            umma_commit(bar);
+                        }
+                        __syncwarp();
                     }
-                    umma_commit(smem_u32(&ctl.empty[(n0 + 4) % kSlots]));
-                    umma_commit(smem_u32(&ctl.o_full));
+                    if (elect_one()) {
+                        umma_commit(smem_u32(&ctl.empty[(n0 + 4) % kSlots]));
+                        umma_commit(smem_u32(&ctl.o_full));
+                    }
+                    __syncwarp();
                     ++o_it;
                     progress = true;
                 } else if (s_it < n_my && s_it <= o_it + 1) {
                     const uint32_t n = (uint32_t)(kTileBlocks * s_it + s_j), slot = n % kSlots;
-                    if (mbar_test(smem_u32(&ctl.full[slot]), (n / kSlots) & 1u)) {
+                    if (__any_sync(0xffffffffu, mbar_test(smem_u32(&ctl.full[slot]), (n / kSlots) & 1u))) {
                         tc_fence_after();
                         const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
                         const uint32_t d_s = tmem + kColS + (s_it & 1) * 2 * kHeads;
-                        if (s_j < 4) {
-                            const uint64_t bd = s_b0 + (uint64_t)(s_j * (kQBlockBytes >> 4));
+                        const uint64_t bd = s_j < 4 ? s_b0 + (uint64_t)(s_j * (kQBlockBytes >> 4)) : s_bt;
+                        const uint64_t b2 = s_j < 4 ? 4 : 0;       // the tail's K steps 2, 3 read the query again
+                        const uint32_t acc0 = s_j > 0 ? 1u : 0u;
+                        const bool last = s_j + 1 == s_blocks;
+                        if (elect_one()) {
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)(ks * 2), id_s, (s_j | ks) ? 1u : 0u);
-                        } else {
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                umma_f8(d_s, ad + (uint64_t)(ks * 2), s_bt + (uint64_t)((ks & 1) * 2), id_s, 1u);
+                                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)((ks & 1) * 2) + (ks & 2 ? b2 : 0), id_s,
+                                        ks ? 1u : acc0);
+                            if (last) umma_commit(smem_u32(&ctl.s_full[s_it & 1]));
                         }
-                        if (++s_j == s_blocks) {
-                            umma_commit(smem_u32(&ctl.s_full[s_it & 1]));
+                        __syncwarp();
+                        if (last) {
                             s_j = 0;
                             ++s_it;
+                        } else {
+                            ++s_j;
                         }
                         progress = true;
                     }
                 }
                 if (progress) {
                     t_last = global_ns();
-                } else if (*(volatile int32_t *)&ctl.abort_flag) {
+                } else if (__any_sync(0xffffffffu, *(volatile int32_t *)&ctl.abort_flag)) {
                     break;
-                } else if (global_ns() - t_last > b.wait_ns) {
+                } else if (__any_sync(0xffffffffu, global_ns() - t_last > b.wait_ns)) {
                     *(volatile int32_t *)&ctl.abort_flag = 1;
                     flag(p.status, DSA_DEV_TIMEOUT);
                     break;
@@ -465,12 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                 }
                 ctl.m[tx] = mn;
                 ctl.ma[tx] = make_float2(mn == -INFINITY ? 0.f : mn, al);
-                const bool any = __any_sync(0xffffffffu, al != 1.f);
-                if (lane == 0) ctl.resc[warp] = any ? 1 : 0;
+                const uint32_t moved = __ballot_sync(0xffffffffu, al != 1.f);
+                if (lane == 0) ctl.resc[warp] = moved;
             }
             named_barrier(1, kSoftmaxThreads);
-            const bool rescale = ctl.resc[0] | ctl.resc[1];
-            if (rescale) {
+            uint32_t moved = ctl.resc[part];               // of this warp's heads
+            if (moved) {
 #pragma unroll
                 for (int h = 0; h < 32; ++h) lpart[h] *= ctl.ma[hb + h].y;
             }
@@ -503,21 +517,37 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                     *reinterpret_cast<uint4 *>(pb + kPieceBytes + o) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
                 }
             }
-            if (rescale && it > 0) {
+            if (moved && it > 0) {
+                // Columns of O^T whose maximum moved, once the previous tile's
+                // value product has landed: one by one while they are few
+                // (the usual tile moves one or two of 64 heads), else all.
                 if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (uint32_t)(it - 1) & 1u, ctl, p.status, b.wait_ns);
                 alive = __all_sync(0xffffffffu, alive);
                 if (alive) {
                     tc_fence_after();
-#pragma unroll 1
-                    for (int cq = 0; cq < 8; ++cq) {             // 4 dim blocks x 2 groups of 16 heads
-                        uint32_t u[16];
-                        const int hq = hb + (cq & 1) * 16;
-                        const uint32_t addr = tmem + lane_addr + kColO + (cq >> 1) * kHeads + hq;
-                        tmem_ld16(addr, u);
-                        tmem_wait_ld();
+                    const uint32_t o = tmem + lane_addr + kColO + hb;
+                    if (__popc(moved) <= kFewMoved) {
+                        while (moved) {
+                            const int h = __ffs(moved) - 1;
+                            moved &= moved - 1;
+                            const float al = ctl.ma[hb + h].y;
+                            uint32_t u[4];
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) * ctl.ma[hq + q].y);
-                        tmem_st16(addr, u);
+                            for (int c = 0; c < 4; ++c) tmem_ld1(o + c * kHeads + h, u[c]);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) tmem_st1(o + c * kHeads + h, __float_as_uint(__uint_as_float(u[c]) * al));
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t u[32];
+                            tmem_ld32(o + c * kHeads, u);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int h = 0; h < 32; ++h) u[h] = __float_as_uint(__uint_as_float(u[h]) * ctl.ma[hb + h].y);
+                            tmem_st32(o + c * kHeads, u);
+                        }
                     }
                     tmem_wait_st();
                 }
