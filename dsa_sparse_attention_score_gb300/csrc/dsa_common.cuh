@@ -299,6 +299,22 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
 __device__ __forceinline__ void tmem_wait_ld() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// Waits for this thread's tensor-memory loads and keeps the arithmetic on
+// what they loaded behind the wait: to the compiler the registers are the
+// load's outputs already, and it may move their uses up in front of a wait
+// that does not name them.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+template <int N, int M>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N], uint32_t (&q)[M]) {
+    tmem_wait_ld(r);
+#pragma unroll
+    for (int i = 0; i < M; ++i) asm volatile("" : "+r"(q[i]));
+}
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }

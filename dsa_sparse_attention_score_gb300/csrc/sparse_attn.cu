@@ -87,7 +87,7 @@ struct Ctl {
     uint64_t c_empty[kBufs];
     uint64_t s_full[kBufs];
     uint64_t p_full[kBufs];
-    uint64_t o_full;
+    uint64_t o_full[2];      // by tile parity: tile i's completes after tile i - 2's has been waited for
     uint32_t tmem_base;
     int32_t abort_flag;
     float red[4][kHeads];
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctl.s_full[i]), 1);
             mbar_init(smem_u32(&ctl.p_full[i]), kSoftmaxWarps);
         }
-        mbar_init(smem_u32(&ctl.o_full), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl.o_full[i]), 1);
         ctl.abort_flag = 0;
         fence_mbar_init();
     }
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ad += (uint64_t)((2 * kCBlockBytes) >> 4);
                     }
                     umma_commit(smem_u32(&ctl.c_empty[buf]));
-                    umma_commit(smem_u32(&ctl.o_full));
+                    umma_commit(smem_u32(&ctl.o_full[o_next & 1]));
                     ++o_next;
                     progress = true;
                 }
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // previous tile's PV product has landed.  O^T is an M=128
                 // accumulator: every lane of the warp owns one output dim; the
                 // two warps of a quarter take 32 heads each.
-                if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (uint32_t)(it - 1) & 1u, ctl, p.status, b.wait_ns);
+                if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(it - 1) & 1]), (uint32_t)((it - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
                 alive = __all_sync(0xffffffffu, alive);
                 if (alive) {
                     tc_fence_after();
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[buf]));
         }
         // ---- final: O^T of the last tile, row sums, outputs
-        if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (uint32_t)(n_my - 1) & 1u, ctl, p.status, b.wait_ns);
+        if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(n_my - 1) & 1]), (uint32_t)((n_my - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
         alive = __all_sync(0xffffffffu, alive);
         ctl.red[quarter][hl] = half_reduce_16<false>(lpart, lane);
         named_barrier(1, kSoftmaxThreads);

@@ -37,9 +37,11 @@
 // gathers it with 16-byte cp.async copies (a row's 128 bytes are one cache
 // line; masked rows are filled with zeros and read nothing), so up to five
 // blocks are in flight.  The MMA thread issues score blocks and value
-// products as their inputs arrive; eight softmax warps (two per TMEM lane
-// quarter, 32 heads each) turn a tile's S^T into P^T.  The running maximum of
+// products as their inputs arrive; sixteen softmax warps (four per TMEM lane
+// quarter, 16 heads each) turn a tile's S^T into P^T.  The running maximum of
 // u is raised only when a tile exceeds it by 2^3.
+#include <cstddef>
+
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 #include "quant8.cuh"
@@ -57,14 +59,16 @@ constexpr int kQBlockBytes = 2 * kHeads * 128;        // hi and lo rows of 128 c
 constexpr int kQTailBytes = 2 * kHeads * 64;          // hi and lo rows of 64 codes (SWIZZLE_64B)
 constexpr int kQBytes = 4 * kQBlockBytes + kQTailBytes;
 constexpr int kPieceBytes = kRows * 64;       // one piece of P^T (SWIZZLE_64B)
-constexpr int kSoftmaxWarps = 8;
+constexpr int kParts = 4;                     // groups of 16 heads
+constexpr int kPartHeads = kHeads / kParts;
+constexpr int kSoftmaxWarps = 4 * kParts;     // one per (TMEM lane quarter, part)
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kMmaWarp = 8;
-constexpr int kProducerWarps = kTileBlocks;   // warps 9..13
+constexpr int kMmaWarp = kSoftmaxWarps;
+constexpr int kProducerWarps = kTileBlocks;   // warps 17..21
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kProducerWarps);
 constexpr float kTopLog2 = 5.0f;              // a new maximum's weight is 2^5 ...
 constexpr float kRaiseLog2 = 8.0f;            // ... and none exceeds 2^8
-constexpr int kFewMoved = 6;                  // heads of 32 rescaled one by one
+constexpr int kFewMoved = 4;                  // heads of 16 rescaled one by one
 constexpr float kMinScale = 0x1p-40f;
 constexpr uint32_t kTmemCols = 512;           // S^T: 2 x 128 columns, O^T: 4 x 64
 constexpr uint32_t kColS = 0;
@@ -92,18 +96,18 @@ struct Ctl {
     uint64_t empty[kSlots];
     uint64_t s_full[2];
     uint64_t p_full[2];
-    uint64_t o_full;
+    uint64_t o_full[2];      // by tile parity: tile i's completes after tile i - 2's has been waited for
     uint32_t tmem_base;
     int32_t abort_flag;
-    float qs[kHeads];        // 2^e of the head's query times scale_log2
-    float red[4][kHeads];
-    float m[kHeads];
-    float2 ma[kHeads];       // (m, alpha) of the current tile; m = 0 while there is none
-    uint32_t resc[2];        // heads 0..31 / 32..63 whose maximum moved in this tile
-    float l[kHeads];
-    float inv_l[kHeads];
+    alignas(16) float qs[kHeads];   // 2^e of the head's query times scale_log2
+    float red[2][4][kHeads]; // a tile's maxima (by tile parity), the row sums at the end
+    alignas(16) float ma[kSoftmaxWarps][2 * kPartHeads];   // each warp's m (0 while there is none) and alpha
     int32_t warp_alive[kSoftmaxWarps];
 };
+
+// qs and ma are read four at a time
+static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
+                  (kSlots * kBlockBytes + kQBytes) % 16 == 0, "16-byte reads of shared memory");
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
     if (*(volatile int32_t *)&c.abort_flag) return false;
@@ -119,27 +123,31 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Transposing butterfly: each lane holds 32 values, lane L ends up with the
-// reduction of value L over the warp.
-template <bool kMax>
-__device__ __forceinline__ float warp_reduce_32(const float (&x)[32], int lane) {
-    float a[32];
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));   // volatile: stays where the warp is whole
+    return r;
+}
+
+// Transposing butterfly: each lane holds 16 values, lane L ends up with the
+// sum of value L mod 16 over the warp.
+__device__ __forceinline__ float warp_sum_16(const float (&x)[16], int lane) {
+    float a[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) a[i] = x[i];
+    for (int i = 0; i < 16; ++i) a[i] = x[i];
 #pragma unroll
-    for (int half = 16; half >= 1; half >>= 1) {
+    for (int half = 8; half >= 1; half >>= 1) {
         const bool up = lane & half;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
             if (i < half) {
                 const float keep = up ? a[half + i] : a[i];
                 const float send = up ? a[i] : a[half + i];
-                const float o = __shfl_xor_sync(0xffffffffu, send, half);
-                a[i] = kMax ? fmaxf(keep, o) : keep + o;
+                a[i] = keep + __shfl_xor_sync(0xffffffffu, send, half);
             }
         }
     }
-    return a[0];
+    return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 16);
 }
 
 // 16 bf16 values in two words of four.
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             mbar_init(smem_u32(&ctl.s_full[i]), 1);
             mbar_init(smem_u32(&ctl.p_full[i]), kSoftmaxWarps);
         }
-        mbar_init(smem_u32(&ctl.o_full), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl.o_full[i]), 1);
         ctl.abort_flag = 0;
         fence_mbar_init();
     }
@@ -285,9 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             mbar_arrive(smem_u32(&ctl.full[slot]));
         }
     } else if (warp == kMmaWarp) {
-        // ---------------- MMA issuer: value products first (they free slots),
-        // then the next score block whose codes have landed.  The whole warp
-        // runs the loop (uniform descriptors); one elected lane issues.
+        // ---------------- MMA issuer.  Score blocks go first as their codes
+        // land, value products block by block in between: a tile's last score
+        // block needs the slot that the first block of the value product
+        // before it frees, and the softmax waits for that block.  The whole warp runs
+        // the loop (uniform descriptors); one elected lane issues.
         if (wait_bar(smem_u32(&ctl.q_full), 0, ctl, p.status, b.wait_ns) &&
             wait_bar(smem_u32(&ctl.full[0]), 0, ctl, p.status, b.wait_ns)) {
             __syncwarp();
@@ -298,41 +308,13 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             const uint64_t s_bt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
             const uint64_t o_b0 = sdesc_sw64(ra, 16, 512);
             const int s_blocks = tail ? kTileBlocks : kTileBlocks - 1;
-            int s_it = 0, s_j = 0, o_it = 0;
+            int s_it = 0, s_j = 0, o_it = 0, o_c = 0;
+            bool p_ready = false;
             uint64_t t_last = global_ns();
             while (o_it < n_my) {
                 bool progress = false;
-                if (o_it < s_it && __any_sync(0xffffffffu, mbar_test(smem_u32(&ctl.p_full[o_it & 1]), (uint32_t)(o_it >> 1) & 1u))) {
-                    tc_fence_after();
-                    const uint32_t n0 = (uint32_t)(kTileBlocks * o_it);
-                    const uint64_t bd = o_b0 + (uint64_t)(((n0 + 4) % kSlots) * (kBlockBytes >> 4));
-                    const uint32_t acc0 = o_it > 0 ? 1u : 0u;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t slot = (n0 + c) % kSlots;
-                        const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
-                        const uint32_t d_o = tmem + kColO + c * kHeads;
-                        const uint32_t bar = smem_u32(&ctl.empty[slot]);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-                                for (int ks = 0; ks < kRows / 32; ++ks)
-                                    umma_f8(d_o, ad + (uint64_t)(ks * (32 * 128 >> 4)),
-                                            bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), id_o,
-                                            (piece || ks) ? 1u : acc0);
-                            umma_commit(bar);
-                        }
-                        __syncwarp();
-                    }
-                    if (elect_one()) {
-                        umma_commit(smem_u32(&ctl.empty[(n0 + 4) % kSlots]));
-                        umma_commit(smem_u32(&ctl.o_full));
-                    }
-                    __syncwarp();
-                    ++o_it;
-                    progress = true;
-                } else if (s_it < n_my && s_it <= o_it + 1) {
+                // the next score block, if its codes have landed ...
+                if (s_it < n_my && s_it <= o_it + 1) {
                     const uint32_t n = (uint32_t)(kTileBlocks * s_it + s_j), slot = n % kSlots;
                     if (__any_sync(0xffffffffu, mbar_test(smem_u32(&ctl.full[slot]), (n / kSlots) & 1u))) {
                         tc_fence_after();
@@ -350,12 +332,41 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                             if (last) umma_commit(smem_u32(&ctl.s_full[s_it & 1]));
                         }
                         __syncwarp();
-                        if (last) {
-                            s_j = 0;
-                            ++s_it;
-                        } else {
-                            ++s_j;
+                        s_j = last ? 0 : s_j + 1;
+                        s_it += last;
+                        progress = true;
+                    }
+                }
+                // ... then one block of the value product
+                if (!progress && o_it < s_it) {
+                    if (!p_ready)
+                        p_ready = __any_sync(0xffffffffu, mbar_test(smem_u32(&ctl.p_full[o_it & 1]), (uint32_t)(o_it >> 1) & 1u));
+                    if (p_ready) {
+                        tc_fence_after();
+                        const uint32_t n0 = (uint32_t)(kTileBlocks * o_it), slot = (n0 + o_c) % kSlots, pslot = (n0 + 4) % kSlots;
+                        const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+                        const uint64_t bd = o_b0 + (uint64_t)(pslot * (kBlockBytes >> 4));
+                        const uint32_t d_o = tmem + kColO + o_c * kHeads;
+                        const uint32_t acc0 = o_it > 0 ? 1u : 0u;
+                        const bool last = o_c == 3;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+                                for (int ks = 0; ks < kRows / 32; ++ks)
+                                    umma_f8(d_o, ad + (uint64_t)(ks * (32 * 128 >> 4)),
+                                            bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), id_o,
+                                            (piece || ks) ? 1u : acc0);
+                            umma_commit(smem_u32(&ctl.empty[slot]));
+                            if (last) {
+                                umma_commit(smem_u32(&ctl.empty[pslot]));
+                                umma_commit(smem_u32(&ctl.o_full[o_it & 1]));
+                            }
                         }
+                        __syncwarp();
+                        o_c = last ? 0 : o_c + 1;
+                        o_it += last;
+                        if (last) p_ready = false;
                         progress = true;
                     }
                 }
@@ -371,15 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             }
         }
     } else {
-        // ---------------- queries, softmax and epilogue (warps 0..7)
-        const int tx = (int)threadIdx.x;
+        // ---------------- queries, softmax and epilogue (warps 0..15)
         const int quarter = warp & 3;                      // TMEM lanes 32*quarter ..
-        const int part = warp >> 2;                        // heads 32*part ..
-        const int hb = 32 * part;
+        const int part = warp >> 2;                        // heads 16*part ..
+        const int hb = kPartHeads * part;
         const int r = quarter * 32 + lane;                 // row within the tile
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        if (tx < kHeads) ctl.m[tx] = -INFINITY;
-        // each warp splits eight heads' queries: lane l the values 16 l .. 16 l + 15
+        float *ma = ctl.ma[warp];
+        // each warp splits four heads' queries: lane l the values 16 l .. 16 l + 15
 #pragma unroll 2
         for (int i = 0; i < kHeads / kSoftmaxWarps; ++i) {
             const int h = warp * (kHeads / kSoftmaxWarps) + i;
@@ -423,9 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
         pdl_wait();
         bool alive = true;
         named_barrier(1, kSoftmaxThreads);
-        float lpart[32];
+        float lpart[16];
 #pragma unroll
-        for (int h = 0; h < 32; ++h) lpart[h] = 0.f;
+        for (int h = 0; h < 16; ++h) lpart[h] = 0.f;
+        // lane h < 16: the running maximum of head hb + h (the same in the
+        // four warps of the part)
+        float m = -INFINITY;
         // Scale of this thread's row of a tile (0: masked), looked up a tile
         // ahead.  Any positive scale will do; a row never written (scale 0)
         // counts as zeros at the smallest one.
@@ -448,55 +461,65 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             const float irs = valid ? 1.f / rs : 0.f;
             if (alive) alive = wait_bar(smem_u32(&ctl.s_full[buf]), (uint32_t)(it >> 1) & 1u, ctl, p.status, b.wait_ns);
             alive = __all_sync(0xffffffffu, alive);
-            float x[32];
+            float x[16];
             if (alive) {
                 tc_fence_after();
+                uint32_t u[16], w[16];
+                const uint32_t a = tmem + lane_addr + kColS + buf * 2 * kHeads + hb;
+                tmem_ld16(a, u);
+                tmem_ld16(a + kHeads, w);
+                tmem_wait_ld(u, w);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t u[16], w[16];
-                    const uint32_t a = tmem + lane_addr + kColS + buf * 2 * kHeads + hb + 16 * half;
-                    tmem_ld16(a, u);
-                    tmem_ld16(a + kHeads, w);
-                    tmem_wait_ld();
+                for (int i = 0; i < 4; ++i) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(ctl.qs + hb + 4 * i);
+                    const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-                    for (int h = 0; h < 16; ++h)
-                        x[16 * half + h] = valid ? (__uint_as_float(u[h]) + __uint_as_float(w[h])) * rs * ctl.qs[hb + 16 * half + h] + ef
-                                                 : -INFINITY;
+                    for (int j = 0; j < 4; ++j) {
+                        const float z = (__uint_as_float(u[4 * i + j]) + __uint_as_float(w[4 * i + j])) * rs;
+                        x[4 * i + j] = valid ? fmaf(z, qs[j], ef) : -INFINITY;
+                    }
                 }
             } else {
 #pragma unroll
-                for (int h = 0; h < 32; ++h) x[h] = -INFINITY;
+                for (int h = 0; h < 16; ++h) x[h] = -INFINITY;
             }
-            ctl.red[quarter][hb + lane] = warp_reduce_32<true>(x, lane);
-            named_barrier(1, kSoftmaxThreads);
-            if (tx < kHeads) {
-                const float tmax = fmaxf(fmaxf(ctl.red[0][tx], ctl.red[1][tx]), fmaxf(ctl.red[2][tx], ctl.red[3][tx]));
-                const float mo = ctl.m[tx];
-                float mn = mo, al = 1.f;
-                if (tmax != -INFINITY && (mo == -INFINITY || tmax > mo + kRaiseLog2)) {
-                    mn = tmax - kTopLog2;
-                    al = mo == -INFINITY ? 0.f : exp2f(mo - mn);
+            // maxima over the tile: warp by warp, then across the part's four warps
+            float wmax = 0.f;
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+                const float v = warp_max(x[h]);
+                wmax = (lane & 15) == h ? v : wmax;
+            }
+            if (lane < 16) ctl.red[buf][quarter][hb + lane] = wmax;
+            named_barrier(2 + part, 128);
+            uint32_t moved;                                // heads of the part whose maximum moves
+            {
+                const int h = hb + (lane & 15);
+                const float tmax = fmaxf(fmaxf(ctl.red[buf][0][h], ctl.red[buf][1][h]), fmaxf(ctl.red[buf][2][h], ctl.red[buf][3][h]));
+                float al = 1.f;
+                if (tmax != -INFINITY && (m == -INFINITY || tmax > m + kRaiseLog2)) {
+                    const float mn = tmax - kTopLog2;
+                    al = m == -INFINITY ? 0.f : exp2f(m - mn);
+                    m = mn;
                 }
-                ctl.m[tx] = mn;
-                ctl.ma[tx] = make_float2(mn == -INFINITY ? 0.f : mn, al);
-                const uint32_t moved = __ballot_sync(0xffffffffu, al != 1.f);
-                if (lane == 0) ctl.resc[warp] = moved;
+                if (lane < 16) {
+                    ma[lane] = m == -INFINITY ? 0.f : m;
+                    ma[kPartHeads + lane] = al;
+                }
+                moved = __ballot_sync(0xffffffffu, lane < 16 && al != 1.f);
+                __syncwarp();
             }
-            named_barrier(1, kSoftmaxThreads);
-            uint32_t moved = ctl.resc[part];               // of this warp's heads
             if (moved) {
 #pragma unroll
-                for (int h = 0; h < 32; ++h) lpart[h] *= ctl.ma[hb + h].y;
+                for (int h = 0; h < 16; ++h) lpart[h] *= ma[kPartHeads + h];
             }
-            uint32_t hi[8], lo[8];
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float w[4];
+            for (int i = 0; i < 4; ++i) {
+                const float4 m4 = *reinterpret_cast<const float4 *>(ma + 4 * i);
+                const float w[4] = {ex2(x[4 * i] - m4.x), ex2(x[4 * i + 1] - m4.y), ex2(x[4 * i + 2] - m4.z), ex2(x[4 * i + 3] - m4.w)};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    w[q] = ex2(x[4 * i + q] - ctl.ma[hb + 4 * i + q].x);
-                    lpart[4 * i + q] = fmaf(w[q], irs, lpart[4 * i + q]);
-                }
+                for (int j = 0; j < 4; ++j) lpart[4 * i + j] = fmaf(w[j], irs, lpart[4 * i + j]);
                 const uint32_t a = e4m3x2(w[0], w[1]), c = e4m3x2(w[2], w[3]);
                 const float2 fa = e4m3x2_to_float2(a), fc = e4m3x2_to_float2(c);
                 hi[i] = a | c << 16;
@@ -509,19 +532,15 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                 alive = __all_sync(0xffffffffu, alive);
             }
             if (alive) {
-                uint8_t *pb = ring + pslot * kBlockBytes;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t o = sw64_offset((uint32_t)r, (uint32_t)(2 * part + i));
-                    *reinterpret_cast<uint4 *>(pb + o) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                    *reinterpret_cast<uint4 *>(pb + kPieceBytes + o) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-                }
+                uint8_t *pb = ring + pslot * kBlockBytes + sw64_offset((uint32_t)r, (uint32_t)part);
+                *reinterpret_cast<uint4 *>(pb) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(pb + kPieceBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             if (moved && it > 0) {
                 // Columns of O^T whose maximum moved, once the previous tile's
                 // value product has landed: one by one while they are few
                 // (the usual tile moves one or two of 64 heads), else all.
-                if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (uint32_t)(it - 1) & 1u, ctl, p.status, b.wait_ns);
+                if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(it - 1) & 1]), (uint32_t)((it - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
                 alive = __all_sync(0xffffffffu, alive);
                 if (alive) {
                     tc_fence_after();
@@ -530,23 +549,23 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                         while (moved) {
                             const int h = __ffs(moved) - 1;
                             moved &= moved - 1;
-                            const float al = ctl.ma[hb + h].y;
+                            const float al = ma[kPartHeads + h];
                             uint32_t u[4];
 #pragma unroll
                             for (int c = 0; c < 4; ++c) tmem_ld1(o + c * kHeads + h, u[c]);
-                            tmem_wait_ld();
+                            tmem_wait_ld(u);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) tmem_st1(o + c * kHeads + h, __float_as_uint(__uint_as_float(u[c]) * al));
                         }
                     } else {
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            uint32_t u[32];
-                            tmem_ld32(o + c * kHeads, u);
-                            tmem_wait_ld();
+                            uint32_t u[16];
+                            tmem_ld16(o + c * kHeads, u);
+                            tmem_wait_ld(u);
 #pragma unroll
-                            for (int h = 0; h < 32; ++h) u[h] = __float_as_uint(__uint_as_float(u[h]) * ctl.ma[hb + h].y);
-                            tmem_st32(o + c * kHeads, u);
+                            for (int h = 0; h < 16; ++h) u[h] = __float_as_uint(__uint_as_float(u[h]) * ma[kPartHeads + h]);
+                            tmem_st16(o + c * kHeads, u);
                         }
                     }
                     tmem_wait_st();
@@ -558,53 +577,53 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[buf]));
         }
         // ---- final: O^T of the last tile, row sums, outputs
-        if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (uint32_t)(n_my - 1) & 1u, ctl, p.status, b.wait_ns);
+        if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(n_my - 1) & 1]), (uint32_t)((n_my - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
         alive = __all_sync(0xffffffffu, alive);
-        ctl.red[quarter][hb + lane] = warp_reduce_32<false>(lpart, lane);
-        named_barrier(1, kSoftmaxThreads);
-        if (tx < kHeads) {
-            const float l = ctl.red[0][tx] + ctl.red[1][tx] + ctl.red[2][tx] + ctl.red[3][tx];
-            ctl.l[tx] = l;
-            ctl.inv_l[tx] = ctl.m[tx] == -INFINITY ? 0.f : 1.f / l;
-        }
+        const float lsum = warp_sum_16(lpart, lane);
+        const int fin = n_my & 1;                          // the buffer the last tile did not use
+        if (lane < 16) ctl.red[fin][quarter][hb + lane] = lsum;
         if (lane == 0) ctl.warp_alive[warp] = alive ? 1 : 0;
         named_barrier(1, kSoftmaxThreads);
+        const int hl = hb + (lane & 15);
+        const float l = ctl.red[fin][0][hl] + ctl.red[fin][1][hl] + ctl.red[fin][2][hl] + ctl.red[fin][3][hl];
+        if (lane < 16) ma[lane] = m == -INFINITY ? 0.f : 1.f / l;
+        __syncwarp();
         bool all_alive = true;
 #pragma unroll
         for (int w = 0; w < kSoftmaxWarps; ++w) all_alive = all_alive && ctl.warp_alive[w];
         if (all_alive) {
             // thread (quarter, lane) holds output dim 128 c + 32 quarter + lane
-            // of every head; the two warps of a quarter store 32 heads each
+            // of the part's heads
             tc_fence_after();
             const int rd = quarter * 32 + lane;
             const int64_t o = ((int64_t)t * p.H + h0) * D_L;
             uint16_t *po = p.n_split > 1 ? p.part_o + part_idx * kHeads * D_L : nullptr;
 #pragma unroll 1
-            for (int cq = 0; cq < 8; ++cq) {
-                const int hq = hb + (cq & 1) * 16, d = (cq >> 1) * 128 + rd;
+            for (int c = 0; c < 4; ++c) {
+                const int d = c * 128 + rd;
                 uint32_t u[16];
-                tmem_ld16(tmem + lane_addr + kColO + (cq >> 1) * kHeads + hq, u);
-                tmem_wait_ld();
+                tmem_ld16(tmem + lane_addr + kColO + c * kHeads + hb, u);
+                tmem_wait_ld(u);
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
-                    const int h = hq + q;
+                    const int h = hb + q;
                     const float v = __uint_as_float(u[q]);
                     if (po) {
                         po[h * D_L + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
                     } else if (h < nh) {
-                        if (p.out_bf16) static_cast<uint16_t *>(p.out)[o + h * D_L + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v * ctl.inv_l[h]));
-                        else static_cast<float *>(p.out)[o + h * D_L + d] = v * ctl.inv_l[h];
+                        if (p.out_bf16) static_cast<uint16_t *>(p.out)[o + h * D_L + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v * ma[q]));
+                        else static_cast<float *>(p.out)[o + h * D_L + d] = v * ma[q];
                     }
                 }
             }
-            if (tx < kHeads) {
-                const float l = ctl.l[tx], m = ctl.m[tx];
+            if (quarter == 0 && lane < 16) {
+                const int h = hb + lane;
                 if (po) {
-                    float *ml = p.part_ml + (part_idx * kHeads + tx) * 2;
+                    float *ml = p.part_ml + (part_idx * kHeads + h) * 2;
                     ml[0] = m;
                     ml[1] = l;
-                } else if (p.lse && tx < nh) {
-                    p.lse[(int64_t)t * p.H + h0 + tx] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                } else if (p.lse && h < nh) {
+                    p.lse[(int64_t)t * p.H + h0 + h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                 }
             }
         }
