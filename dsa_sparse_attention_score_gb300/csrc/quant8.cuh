@@ -43,11 +43,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo_elem, float hi_elem) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi_elem), "f"(lo_elem));
     return r;
 }
+__device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&v)));
+    return r;
+}
 // The values of two codes (bits 0..7 first), exact in fp16.
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t codes) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return *reinterpret_cast<const __half2 *>(&h);
 }
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) { return __half22float2(e4m3x2_to_half2(codes)); }
 
 }  // namespace dsa

@@ -14,8 +14,8 @@
 //    the remainder signed, hold bf16's eight: the split is exact for values
 //    above 2^-10 of the head's largest, and off by 2^-19 of it below.
 //  - A weight is split the same way, in units where the largest lies in
-//    [2^5, 2^8]: each is off by at most 2^-8 of itself (half a bf16 step) or
-//    2^-15 of the largest.
+//    [2^3.5, 2^8]: each is off by at most 2^-8 of itself (half a bf16 step) or
+//    2^-13.5 of the largest.
 // So every product is 8-bit by 8-bit with float32 sums, at twice the rate of
 // bf16 products and half the bytes: the two pieces cost what one bf16 product
 // would, and the rows come in at 644 bytes instead of 1152.
@@ -32,14 +32,16 @@
 // P^T in place.  The tail block is dead once S^T is computed and holds P^T.
 //
 // Shared memory: queries 72 KB and a ring of nine blocks (144 KB), one short
-// of two tiles: a tile's last block is gathered when the first value product of the
-// tile before has freed its slot.  One producer warp per block of the tile
+// of two tiles: a tile's tail block goes in when the first value product of
+// the tile before has freed its slot.  One producer warp per latent block
 // gathers it with 16-byte cp.async copies (a row's 128 bytes are one cache
-// line; masked rows are filled with zeros and read nothing), so up to five
-// blocks are in flight.  The MMA thread issues score blocks and value
+// line; masked rows are filled with zeros and read nothing); four more hold
+// the tail block in registers until its slot is free.  The MMA thread issues score blocks and value
 // products as their inputs arrive; sixteen softmax warps (four per TMEM lane
-// quarter, 16 heads each) turn a tile's S^T into P^T.  The running maximum of
-// u is raised only when a tile exceeds it by 2^3.
+// quarter, 16 heads each) turn a tile's S^T into P^T.  The reference M of a
+// head's weights is set 2^3.5 below its first tile's maximum and moves only
+// when a weight would exceed 2^8, so most tiles need no maxima, only the
+// question whether any weight does.
 #include <cstddef>
 
 #include "dsa_common.cuh"
@@ -64,9 +66,10 @@ constexpr int kPartHeads = kHeads / kParts;
 constexpr int kSoftmaxWarps = 4 * kParts;     // one per (TMEM lane quarter, part)
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kMmaWarp = kSoftmaxWarps;
-constexpr int kProducerWarps = kTileBlocks;   // warps 17..21
+constexpr int kTailWarps = 4;                 // 32 rows of the tail block each
+constexpr int kProducerWarps = 4 + kTailWarps;   // warps 17..20: a latent block each; 21..24: the tail
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kProducerWarps);
-constexpr float kTopLog2 = 5.0f;              // a new maximum's weight is 2^5 ...
+constexpr float kTopLog2 = 3.5f;              // a new maximum's weight is 2^3.5 ...
 constexpr float kRaiseLog2 = 8.0f;            // ... and none exceeds 2^8
 constexpr int kFewMoved = 4;                  // heads of 16 rescaled one by one
 constexpr float kMinScale = 0x1p-40f;
@@ -100,8 +103,8 @@ struct Ctl {
     uint32_t tmem_base;
     int32_t abort_flag;
     alignas(16) float qs[kHeads];   // 2^e of the head's query times scale_log2
-    float red[2][4][kHeads]; // a tile's maxima (by tile parity), the row sums at the end
-    alignas(16) float ma[kSoftmaxWarps][2 * kPartHeads];   // each warp's m (0 while there is none) and alpha
+    float red[4][kHeads];    // a tile's maxima by lane quarter; the row sums at the end
+    alignas(16) float ma[kSoftmaxWarps][2 * kPartHeads];   // each warp's -m, and how far m moved
     int32_t warp_alive[kSoftmaxWarps];
 };
 
@@ -259,127 +262,153 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
     };
 
     if (warp > kMmaWarp) {
-        // ---------------- producers: warp j gathers block j of every tile.
-        // Rows without a tail have nothing to gather into the fifth: its warp
-        // only passes the free slot on to the softmax, which puts P^T there.
-        const int j = warp - kMmaWarp - 1;
-        const bool copy = (j < 4 || tail) && !b.skip_copies;
+        // ---------------- producers
+        const int pw = warp - kMmaWarp - 1;
+        const int j = min(pw, 4);                    // the warp's block of the tile
         const uint8_t *src = p.codes + j * 128 + (lane & 7) * 16;
         // lane's chunk of rows 4 g + lane / 8; g odd flips bit 2 of the swizzled chunk
         const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
         pdl_wait();                                  // the indices come from the preceding kernel
-        for (int it = 0; it < n_my; ++it) {
-            const uint32_t n = (uint32_t)(kTileBlocks * it + j), slot = n % kSlots, use = n / kSlots;
-            int32_t my_row[4] = {-1, -1, -1, -1};
+        if (pw < 4) {
+            // a latent block: asynchronous copies into its slot
+            for (int it = 0; it < n_my; ++it) {
+                const uint32_t n = (uint32_t)(kTileBlocks * it + j), slot = n % kSlots, use = n / kSlots;
+                int32_t my_row[4];
 #pragma unroll
-            for (int q = 0; q < 4 && (j < 4 || tail); ++q) my_row[q] = row_of((tile_lo + it) * kRows + 32 * q + lane, j == 0);
-            if (!wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns)) break;
-            if (!copy) {
-                if (!b.skip_copies) mbar_arrive(smem_u32(&ctl.full[slot]));
-                continue;
+                for (int q = 0; q < 4; ++q) my_row[q] = row_of((tile_lo + it) * kRows + 32 * q + lane, j == 0);
+                if (!wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns)) break;
+                if (b.skip_copies) continue;
+                const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const int32_t row = __shfl_sync(0xffffffffu, my_row[q], 4 * g + (lane >> 3));
+                        cp_async16_or_zero((dst + (uint32_t)(8 * q + g) * 512u) ^ ((uint32_t)(g & 1) << 6),
+                                           src + (int64_t)max(row, 0) * width, row < 0 ? 0u : 16u);
+                    }
+                cp_async_commit();
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&ctl.full[slot]));
             }
-            const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
+        } else {
+            // The tail block, whose slot frees last: its rows wait in
+            // registers, so that only the stores lie between the free slot
+            // and the score product.  Rows without a tail have nothing to
+            // gather: the warps only pass the free slot on to the softmax,
+            // which puts P^T there.
+            const int r0 = 32 * (pw - 4);
+            for (int it = 0; it < n_my; ++it) {
+                const uint32_t n = (uint32_t)(kTileBlocks * it + 4), slot = n % kSlots, use = n / kSlots;
+                uint4 v[8];
+                if (tail) {
+                    const int32_t my_row = row_of((tile_lo + it) * kRows + r0 + lane, false);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const int32_t row = __shfl_sync(0xffffffffu, my_row[q], 4 * g + (lane >> 3));
-                    cp_async16_or_zero((dst + (uint32_t)(8 * q + g) * 512u) ^ ((uint32_t)(g & 1) << 6),
-                                       src + (int64_t)max(row, 0) * width, row < 0 ? 0u : 16u);
+                    for (int g = 0; g < 8; ++g) {
+                        const int32_t row = __shfl_sync(0xffffffffu, my_row, 4 * g + (lane >> 3));
+                        v[g] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row >= 0) v[g] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * width));
+                    }
                 }
-            cp_async_commit();
-            cp_async_wait_all();
-            fence_proxy_async_smem();
-            mbar_arrive(smem_u32(&ctl.full[slot]));
+                if (!wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns)) break;
+                if (b.skip_copies) continue;
+                if (tail) {
+                    uint8_t *dst = ring + slot * kBlockBytes + r0 * 128;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        *reinterpret_cast<uint4 *>(dst + ((d0 + (uint32_t)g * 512u) ^ ((uint32_t)(g & 1) << 6))) = v[g];
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane < 32 / kTailWarps) mbar_arrive(smem_u32(&ctl.full[slot]));
+            }
         }
     } else if (warp == kMmaWarp) {
-        // ---------------- MMA issuer.  Score blocks go first as their codes
-        // land, value products block by block in between: a tile's last score
-        // block needs the slot that the first block of the value product
-        // before it frees, and the softmax waits for that block.  The whole warp runs
-        // the loop (uniform descriptors); one elected lane issues.
-        if (wait_bar(smem_u32(&ctl.q_full), 0, ctl, p.status, b.wait_ns) &&
-            wait_bar(smem_u32(&ctl.full[0]), 0, ctl, p.status, b.wait_ns)) {
-            __syncwarp();
-            const uint32_t id_s = idesc_e4m3(kRows, 2 * kHeads, false, false);
-            const uint32_t id_o = idesc_e4m3(128, kHeads, true, true);
-            const uint32_t ra = smem_u32(ring), qa = smem_u32(q_s);
-            const uint64_t s_a0 = sdesc_sw128(ra, 16, 1024), s_b0 = sdesc_sw128(qa, 16, 1024);
-            const uint64_t s_bt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
-            const uint64_t o_b0 = sdesc_sw64(ra, 16, 512);
-            const int s_blocks = tail ? kTileBlocks : kTileBlocks - 1;
-            int s_it = 0, s_j = 0, o_it = 0, o_c = 0;
-            bool p_ready = false;
-            uint64_t t_last = global_ns();
-            while (o_it < n_my) {
-                bool progress = false;
-                // the next score block, if its codes have landed ...
-                if (s_it < n_my && s_it <= o_it + 1) {
-                    const uint32_t n = (uint32_t)(kTileBlocks * s_it + s_j), slot = n % kSlots;
-                    if (__any_sync(0xffffffffu, mbar_test(smem_u32(&ctl.full[slot]), (n / kSlots) & 1u))) {
-                        tc_fence_after();
-                        const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
-                        const uint32_t d_s = tmem + kColS + (s_it & 1) * 2 * kHeads;
-                        const uint64_t bd = s_j < 4 ? s_b0 + (uint64_t)(s_j * (kQBlockBytes >> 4)) : s_bt;
-                        const uint64_t b2 = s_j < 4 ? 4 : 0;       // the tail's K steps 2, 3 read the query again
-                        const uint32_t acc0 = s_j > 0 ? 1u : 0u;
-                        const bool last = s_j + 1 == s_blocks;
-                        if (elect_one()) {
+        // ---------------- MMA issuer, in a fixed order per tile:
+        //   S(i + 1) latent blocks | P^T(i) | O(i) block 0 | S(i + 1) tail | O(i) blocks 1..3
+        // The first value-product block frees the slot that the next tile's
+        // tail needs; the rest of the value product runs beside the next
+        // softmax.  Polling for whichever input came first instead cost 360 to
+        // 600 cycles of bookkeeping per block against 300 to 460 of products.
+        // The whole warp runs the loop (uniform descriptors); one elected
+        // lane issues.
+        const uint32_t id_s = idesc_e4m3(kRows, 2 * kHeads, false, false);
+        const uint32_t id_o = idesc_e4m3(128, kHeads, true, true);
+        const uint32_t ra = smem_u32(ring), qa = smem_u32(q_s), full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
+        const uint64_t s_a0 = sdesc_sw128(ra, 16, 1024), s_b0 = sdesc_sw128(qa, 16, 1024);
+        const uint64_t s_bt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
+        const uint64_t o_b0 = sdesc_sw64(ra, 16, 512);
+        auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+            const bool ok = __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, p.status, b.wait_ns));
+            tc_fence_after();
+            return ok;
+        };
+        // Block j of tile i has number 5 i + j: slot and use follow from those
+        // of the tile's first block (base, use0).
+        auto score_block = [&](int j, uint32_t base, uint32_t use0, uint32_t d_s, uint64_t bd, uint32_t b2) -> bool {
+            const uint32_t wrap = base + j >= kSlots ? 1u : 0u, slot = base + j - (wrap ? kSlots : 0u);
+            if (!wait(full0 + 8 * slot, (use0 + wrap) & 1u)) return false;
+            const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+            if (elect_one()) {
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)((ks & 1) * 2) + (ks & 2 ? b2 : 0), id_s,
-                                        ks ? 1u : acc0);
-                            if (last) umma_commit(smem_u32(&ctl.s_full[s_it & 1]));
-                        }
-                        __syncwarp();
-                        s_j = last ? 0 : s_j + 1;
-                        s_it += last;
-                        progress = true;
-                    }
-                }
-                // ... then one block of the value product
-                if (!progress && o_it < s_it) {
-                    if (!p_ready)
-                        p_ready = __any_sync(0xffffffffu, mbar_test(smem_u32(&ctl.p_full[o_it & 1]), (uint32_t)(o_it >> 1) & 1u));
-                    if (p_ready) {
-                        tc_fence_after();
-                        const uint32_t n0 = (uint32_t)(kTileBlocks * o_it), slot = (n0 + o_c) % kSlots, pslot = (n0 + 4) % kSlots;
-                        const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
-                        const uint64_t bd = o_b0 + (uint64_t)(pslot * (kBlockBytes >> 4));
-                        const uint32_t d_o = tmem + kColO + o_c * kHeads;
-                        const uint32_t acc0 = o_it > 0 ? 1u : 0u;
-                        const bool last = o_c == 3;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-                                for (int ks = 0; ks < kRows / 32; ++ks)
-                                    umma_f8(d_o, ad + (uint64_t)(ks * (32 * 128 >> 4)),
-                                            bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), id_o,
-                                            (piece || ks) ? 1u : acc0);
-                            umma_commit(smem_u32(&ctl.empty[slot]));
-                            if (last) {
-                                umma_commit(smem_u32(&ctl.empty[pslot]));
-                                umma_commit(smem_u32(&ctl.o_full[o_it & 1]));
-                            }
-                        }
-                        __syncwarp();
-                        o_c = last ? 0 : o_c + 1;
-                        o_it += last;
-                        if (last) p_ready = false;
-                        progress = true;
-                    }
-                }
-                if (progress) {
-                    t_last = global_ns();
-                } else if (__any_sync(0xffffffffu, *(volatile int32_t *)&ctl.abort_flag)) {
-                    break;
-                } else if (__any_sync(0xffffffffu, global_ns() - t_last > b.wait_ns)) {
-                    *(volatile int32_t *)&ctl.abort_flag = 1;
-                    flag(p.status, DSA_DEV_TIMEOUT);
-                    break;
-                }
+                for (int ks = 0; ks < 4; ++ks)
+                    umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)((ks & 1) * 2) + (ks & 2 ? b2 : 0u), id_s, (j || ks) ? 1u : 0u);
             }
+            __syncwarp();
+            return true;
+        };
+        auto score_latent = [&](int it, uint32_t base, uint32_t use0) -> bool {
+            const uint32_t d_s = tmem + kColS + (it & 1) * 2 * kHeads;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (!score_block(j, base, use0, d_s, s_b0 + (uint64_t)(j * (kQBlockBytes >> 4)), 4)) return false;
+            if (!tail && elect_one()) umma_commit(smem_u32(&ctl.s_full[it & 1]));
+            __syncwarp();
+            return true;
+        };
+        auto score_tail = [&](int it, uint32_t base, uint32_t use0) -> bool {
+            if (!tail) return true;
+            // K steps 2 and 3, the remainders, read the query again
+            if (!score_block(4, base, use0, tmem + kColS + (it & 1) * 2 * kHeads, s_bt, 0)) return false;
+            if (elect_one()) umma_commit(smem_u32(&ctl.s_full[it & 1]));
+            __syncwarp();
+            return true;
+        };
+        bool go = wait(smem_u32(&ctl.q_full), 0) && score_latent(0, 0, 0) && score_tail(0, 0, 0);
+        uint32_t base = 0, use0 = 0;
+        for (int it = 0; go && it < n_my; ++it) {
+            const uint32_t wrap = base + kTileBlocks >= kSlots ? 1u : 0u;
+            const uint32_t next = base + kTileBlocks - (wrap ? kSlots : 0u), next_use = use0 + wrap;
+            const bool more = it + 1 < n_my;
+            if (more) go = score_latent(it + 1, next, next_use);
+            go = go && wait(smem_u32(&ctl.p_full[it & 1]), (uint32_t)(it >> 1) & 1u);
+            if (!go) break;
+            const uint32_t pslot = base + 4 - (base + 4 >= kSlots ? kSlots : 0u);
+            const uint64_t bd = o_b0 + (uint64_t)(pslot * (kBlockBytes >> 4));
+            const uint32_t acc0 = it > 0 ? 1u : 0u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t slot = base + c - (base + c >= kSlots ? kSlots : 0u);
+                const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+                if (elect_one()) {
+#pragma unroll
+                    for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+                        for (int ks = 0; ks < kRows / 32; ++ks)
+                            umma_f8(tmem + kColO + c * kHeads, ad + (uint64_t)(ks * (32 * 128 >> 4)),
+                                    bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), id_o, (piece || ks) ? 1u : acc0);
+                    umma_commit(empty0 + 8 * slot);
+                    if (c == 3) {
+                        umma_commit(empty0 + 8 * pslot);
+                        umma_commit(smem_u32(&ctl.o_full[it & 1]));
+                    }
+                }
+                __syncwarp();
+                if (c == 0 && more) go = score_tail(it + 1, next, next_use);
+            }
+            base = next;
+            use0 = next_use;
         }
     } else {
         // ---------------- queries, softmax and epilogue (warps 0..15)
@@ -433,12 +462,16 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
         pdl_wait();
         bool alive = true;
         named_barrier(1, kSoftmaxThreads);
-        float lpart[16];
+        uint64_t lpart[8];                                 // row sums of l, two heads each
 #pragma unroll
-        for (int h = 0; h < 16; ++h) lpart[h] = 0.f;
-        // lane h < 16: the running maximum of head hb + h (the same in the
-        // four warps of the part)
-        float m = -INFINITY;
+        for (int h = 0; h < 8; ++h) lpart[h] = f2(0.f, 0.f);
+        // lane h < 16: the reference m of head hb + h, 3.5 to 8 below its
+        // largest u so far (the same in the four warps of the part); 0 as long
+        // as every row was masked (fresh)
+        float m = 0.f;
+        bool fresh = true;
+        if (lane < 16) ma[lane] = 0.f;
+        __syncwarp();
         // Scale of this thread's row of a tile (0: masked), looked up a tile
         // ahead.  Any positive scale will do; a row never written (scale 0)
         // counts as zeros at the smallest one.
@@ -456,12 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             const int buf = it & 1;
             const float rs = next_scale;
             if (it + 1 < n_my) next_scale = scale_of(it + 1);
-            const bool valid = rs != 0.f;
-            const float ef = valid ? log2f(rs) : 0.f;
+            const bool valid = rs != 0.f;                  // a masked row's products are 0: u = -inf
+            const float ef = valid ? log2f(rs) : -INFINITY;
             const float irs = valid ? 1.f / rs : 0.f;
+            const uint64_t rs2 = f2(rs, rs), ef2 = f2(ef, ef), irs2 = f2(irs, irs);
             if (alive) alive = wait_bar(smem_u32(&ctl.s_full[buf]), (uint32_t)(it >> 1) & 1u, ctl, p.status, b.wait_ns);
             alive = __all_sync(0xffffffffu, alive);
-            float x[16];
+            float x[16], top = -INFINITY;                  // u, then u - m
             if (alive) {
                 tc_fence_after();
                 uint32_t u[16], w[16];
@@ -472,58 +506,66 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float4 q4 = *reinterpret_cast<const float4 *>(ctl.qs + hb + 4 * i);
-                    const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
+                    const float4 n4 = *reinterpret_cast<const float4 *>(ma + 4 * i);
+                    const uint64_t qs[2] = {f2(q4.x, q4.y), f2(q4.z, q4.w)}, nm[2] = {f2(n4.x, n4.y), f2(n4.z, n4.w)};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float z = (__uint_as_float(u[4 * i + j]) + __uint_as_float(w[4 * i + j])) * rs;
-                        x[4 * i + j] = valid ? fmaf(z, qs[j], ef) : -INFINITY;
+                    for (int j = 0; j < 2; ++j) {
+                        const int h = 4 * i + 2 * j;
+                        const uint64_t a2 = f2(__uint_as_float(u[h]), __uint_as_float(u[h + 1]));
+                        const uint64_t b2 = f2(__uint_as_float(w[h]), __uint_as_float(w[h + 1]));
+                        const float2 v = f2_get(f2_add(f2_fma(f2_mul(f2_add(a2, b2), rs2), qs[j], nm[j]), ef2));
+                        x[h] = v.x;
+                        x[h + 1] = v.y;
+                        top = fmaxf(top, fmaxf(v.x, v.y));
                     }
                 }
             } else {
 #pragma unroll
                 for (int h = 0; h < 16; ++h) x[h] = -INFINITY;
             }
-            // maxima over the tile: warp by warp, then across the part's four warps
-            float wmax = 0.f;
+            // Does any weight of the part exceed 2^8?  Then the heads' maxima
+            // are found and m moves where it has to; few tiles but a token's
+            // first come here.
+            uint32_t moved = 0;                            // heads of the part whose m moves
+            if (named_barrier_or(2 + part, 128, fresh || top > kRaiseLog2)) {
+                float wmax[16];
 #pragma unroll
-            for (int h = 0; h < 16; ++h) {
-                const float v = warp_max(x[h]);
-                wmax = (lane & 15) == h ? v : wmax;
-            }
-            if (lane < 16) ctl.red[buf][quarter][hb + lane] = wmax;
-            named_barrier(2 + part, 128);
-            uint32_t moved;                                // heads of the part whose maximum moves
-            {
-                const int h = hb + (lane & 15);
-                const float tmax = fmaxf(fmaxf(ctl.red[buf][0][h], ctl.red[buf][1][h]), fmaxf(ctl.red[buf][2][h], ctl.red[buf][3][h]));
-                float al = 1.f;
-                if (tmax != -INFINITY && (m == -INFINITY || tmax > m + kRaiseLog2)) {
-                    const float mn = tmax - kTopLog2;
-                    al = m == -INFINITY ? 0.f : exp2f(m - mn);
-                    m = mn;
-                }
+                for (int h = 0; h < 16; ++h) wmax[h] = warp_max(x[h]);
+                float over = wmax[0];
+#pragma unroll
+                for (int h = 1; h < 16; ++h) over = (lane & 15) == h ? wmax[h] : over;
+                if (lane < 16) ctl.red[quarter][hb + lane] = over;
+                named_barrier(2 + part, 128);
+                const int hl = hb + (lane & 15);
+                over = fmaxf(fmaxf(ctl.red[0][hl], ctl.red[1][hl]), fmaxf(ctl.red[2][hl], ctl.red[3][hl]));
+                const float up = (fresh ? over != -INFINITY : over > kRaiseLog2) ? over - kTopLog2 : 0.f;
+                m += up;
                 if (lane < 16) {
-                    ma[lane] = m == -INFINITY ? 0.f : m;
-                    ma[kPartHeads + lane] = al;
+                    ma[lane] = -m;
+                    ma[kPartHeads + lane] = up;
                 }
-                moved = __ballot_sync(0xffffffffu, lane < 16 && al != 1.f);
+                moved = fresh ? 0u : __ballot_sync(0xffffffffu, lane < 16 && up != 0.f);
+                fresh = __all_sync(0xffffffffu, over == -INFINITY) && fresh;
                 __syncwarp();
-            }
-            if (moved) {
 #pragma unroll
-                for (int h = 0; h < 16; ++h) lpart[h] *= ma[kPartHeads + h];
+                for (int h = 0; h < 16; ++h) x[h] -= ma[kPartHeads + h];
+                if (moved) {
+#pragma unroll
+                    for (int h = 0; h < 8; ++h)
+                        lpart[h] = f2_mul(lpart[h], f2(ex2(-ma[kPartHeads + 2 * h]), ex2(-ma[kPartHeads + 2 * h + 1])));
+                }
             }
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float4 m4 = *reinterpret_cast<const float4 *>(ma + 4 * i);
-                const float w[4] = {ex2(x[4 * i] - m4.x), ex2(x[4 * i + 1] - m4.y), ex2(x[4 * i + 2] - m4.z), ex2(x[4 * i + 3] - m4.w)};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) lpart[4 * i + j] = fmaf(w[j], irs, lpart[4 * i + j]);
-                const uint32_t a = e4m3x2(w[0], w[1]), c = e4m3x2(w[2], w[3]);
-                const float2 fa = e4m3x2_to_float2(a), fc = e4m3x2_to_float2(c);
-                hi[i] = a | c << 16;
-                lo[i] = e4m3x2(w[0] - fa.x, w[1] - fa.y) | e4m3x2(w[2] - fc.x, w[3] - fc.y) << 16;
+                const float w[4] = {ex2(x[4 * i]), ex2(x[4 * i + 1]), ex2(x[4 * i + 2]), ex2(x[4 * i + 3])};
+                lpart[2 * i] = f2_fma(f2(w[0], w[1]), irs2, lpart[2 * i]);
+                lpart[2 * i + 1] = f2_fma(f2(w[2], w[3]), irs2, lpart[2 * i + 1]);
+                // through fp16, whose 11 bits the two pieces cannot tell from 24
+                const __half2 a = __floats2half2_rn(w[0], w[1]), c = __floats2half2_rn(w[2], w[3]);
+                const uint32_t ha = e4m3x2(a), hc = e4m3x2(c);
+                hi[i] = ha | hc << 16;
+                lo[i] = e4m3x2(__hsub2(a, e4m3x2_to_half2(ha))) | e4m3x2(__hsub2(c, e4m3x2_to_half2(hc))) << 16;
             }
             const uint32_t pn = (uint32_t)(kTileBlocks * it + 4), pslot = pn % kSlots;
             if (!tail && alive) {
@@ -549,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                         while (moved) {
                             const int h = __ffs(moved) - 1;
                             moved &= moved - 1;
-                            const float al = ma[kPartHeads + h];
+                            const float al = ex2(-ma[kPartHeads + h]);
                             uint32_t u[4];
 #pragma unroll
                             for (int c = 0; c < 4; ++c) tmem_ld1(o + c * kHeads + h, u[c]);
@@ -564,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                             tmem_ld16(o + c * kHeads, u);
                             tmem_wait_ld(u);
 #pragma unroll
-                            for (int h = 0; h < 16; ++h) u[h] = __float_as_uint(__uint_as_float(u[h]) * ma[kPartHeads + h]);
+                            for (int h = 0; h < 16; ++h) u[h] = __float_as_uint(__uint_as_float(u[h]) * ex2(-ma[kPartHeads + h]));
                             tmem_st16(o + c * kHeads, u);
                         }
                     }
@@ -579,14 +621,21 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
         // ---- final: O^T of the last tile, row sums, outputs
         if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(n_my - 1) & 1]), (uint32_t)((n_my - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
         alive = __all_sync(0xffffffffu, alive);
-        const float lsum = warp_sum_16(lpart, lane);
-        const int fin = n_my & 1;                          // the buffer the last tile did not use
-        if (lane < 16) ctl.red[fin][quarter][hb + lane] = lsum;
+        float lrow[16];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            const float2 v = f2_get(lpart[h]);
+            lrow[2 * h] = v.x;
+            lrow[2 * h + 1] = v.y;
+        }
+        const float lsum = warp_sum_16(lrow, lane);
+        named_barrier(2 + part, 128);                      // red may still be read
+        if (lane < 16) ctl.red[quarter][hb + lane] = lsum;
         if (lane == 0) ctl.warp_alive[warp] = alive ? 1 : 0;
         named_barrier(1, kSoftmaxThreads);
         const int hl = hb + (lane & 15);
-        const float l = ctl.red[fin][0][hl] + ctl.red[fin][1][hl] + ctl.red[fin][2][hl] + ctl.red[fin][3][hl];
-        if (lane < 16) ma[lane] = m == -INFINITY ? 0.f : 1.f / l;
+        const float l = ctl.red[0][hl] + ctl.red[1][hl] + ctl.red[2][hl] + ctl.red[3][hl];
+        if (lane < 16) ma[lane] = fresh ? 0.f : 1.f / l;
         __syncwarp();
         bool all_alive = true;
 #pragma unroll
@@ -620,10 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                 const int h = hb + lane;
                 if (po) {
                     float *ml = p.part_ml + (part_idx * kHeads + h) * 2;
-                    ml[0] = m;
+                    ml[0] = fresh ? -INFINITY : m;
                     ml[1] = l;
                 } else if (p.lse && h < nh) {
-                    p.lse[(int64_t)t * p.H + h0 + h] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    p.lse[(int64_t)t * p.H + h0 + h] = fresh ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                 }
             }
         }
