@@ -459,9 +459,10 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool ab_bf16, boo
            | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
-// Instruction descriptor of tcgen05.mma kind::f8f6f4, e4m3 operands, f32 accumulator.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
-    return (1u << 4)                                   // D format f32; A and B formats 0: e4m3
+// Instruction descriptor of tcgen05.mma kind::f8f6f4, e4m3 A, e4m3 or e5m2 B, f32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn, bool b_e5m2 = false) {
+    return (1u << 4)                                   // D format f32; A format 0: e4m3
+           | ((b_e5m2 ? 1u : 0u) << 10)                // B format (0 e4m3, 1 e5m2)
            | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16)
            | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }

@@ -48,7 +48,13 @@ __device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&v)));
     return r;
 }
-// The values of two codes (bits 0..7 first), exact in fp16.
+// The same in e5m2, whose smallest step is 2^-16 against e4m3's 2^-9.
+__device__ __forceinline__ uint32_t e5m2x2(__half2 v) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&v)));
+    return r;
+}
+// The values of two e4m3 codes (bits 0..7 first), exact in fp16.
 __device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t codes) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));

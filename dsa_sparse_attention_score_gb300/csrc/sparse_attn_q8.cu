@@ -13,15 +13,18 @@
 //    hi = e4m3(q 2^-e), lo = e4m3(q 2^-e - hi).  Four significant bits each,
 //    the remainder signed, hold bf16's eight: the split is exact for values
 //    above 2^-10 of the head's largest, and off by 2^-19 of it below.
-//  - A weight is split the same way, in units where the largest lies in
-//    [2^3.5, 2^8]: each is off by at most 2^-8 of itself (half a bf16 step) or
-//    2^-13.5 of the largest.
+//  - A weight is an e4m3 piece and an e5m2 remainder, in units where the
+//    largest lies in [2^2, 2^8]: off by at most 2^-7 of itself (rms 2^-9.7, as
+//    for a rounding to bf16) or 2^-15 of the largest.  e5m2 keeps three
+//    significant bits of the remainder but reaches down to 2^-16, which buys
+//    six octaves of headroom before the units have to move; with e4m3
+//    remainders and 4.5 octaves 40% of the tiles moved some head's.
 // So every product is 8-bit by 8-bit with float32 sums, at twice the rate of
 // bf16 products and half the bytes: the two pieces cost what one bf16 product
 // would, and the rows come in at 644 bytes instead of 1152.
 //
-// One CTA per (token, head group of 64, split) walks tiles of 128 selected
-// rows.  A tile is five 16 KB blocks of 128 rows x 128 bytes (SWIZZLE_128B):
+// A unit of work is a (token, head group of 64, split); one CTA per SM takes
+// units in turn and walks their tiles of 128 selected rows.  A tile is five 16 KB blocks of 128 rows x 128 bytes (SWIZZLE_128B):
 // four of latent codes, one of the tail (64 hi | 64 lo).
 //     S^T[row, piece*head]  = C[row, :] . Q[piece*head, :]^T   M=128, N=128, K=512 + 128
 //     O^T[dim, head]       += C[row, dim]^T . P^T[row, head]   4 x M=128, N=64, K=128, both pieces
@@ -37,11 +40,12 @@
 // gathers it with 16-byte cp.async copies (a row's 128 bytes are one cache
 // line; masked rows are filled with zeros and read nothing); four more hold
 // the tail block in registers until its slot is free.  The MMA thread issues score blocks and value
-// products as their inputs arrive; sixteen softmax warps (four per TMEM lane
-// quarter, 16 heads each) turn a tile's S^T into P^T.  The reference M of a
-// head's weights is set 2^3.5 below its first tile's maximum and moves only
+// products as their inputs arrive; eight softmax warps (two per TMEM lane
+// quarter, 32 heads each) turn a tile's S^T into P^T.  The reference M of a
+// head's weights is set 2^2 below its first tile's maximum and moves only
 // when a weight would exceed 2^8, so most tiles need no maxima, only the
 // question whether any weight does.
+#include <algorithm>
 #include <cstddef>
 
 #include "dsa_common.cuh"
@@ -61,17 +65,20 @@ constexpr int kQBlockBytes = 2 * kHeads * 128;        // hi and lo rows of 128 c
 constexpr int kQTailBytes = 2 * kHeads * 64;          // hi and lo rows of 64 codes (SWIZZLE_64B)
 constexpr int kQBytes = 4 * kQBlockBytes + kQTailBytes;
 constexpr int kPieceBytes = kRows * 64;       // one piece of P^T (SWIZZLE_64B)
-constexpr int kParts = 4;                     // groups of 16 heads
+constexpr int kParts = 2;                     // groups of 32 heads
 constexpr int kPartHeads = kHeads / kParts;
 constexpr int kSoftmaxWarps = 4 * kParts;     // one per (TMEM lane quarter, part)
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kMmaWarp = kSoftmaxWarps;
-constexpr int kTailWarps = 4;                 // 32 rows of the tail block each
-constexpr int kProducerWarps = 4 + kTailWarps;   // warps 17..20: a latent block each; 21..24: the tail
-constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kProducerWarps);
-constexpr float kTopLog2 = 3.5f;              // a new maximum's weight is 2^3.5 ...
+// Warp 0 issues the MMAs, warps 1..3 gather latent blocks in turn, 4..11 do
+// the softmax, 12..15 hold 32 rows of the tail block each.
+constexpr int kLatentWarps = 3;
+constexpr int kFirstSoftmax = 1 + kLatentWarps;       // a multiple of 4: warp mod 4 is the lane quarter
+constexpr int kFirstTail = kFirstSoftmax + kSoftmaxWarps;
+constexpr int kTailWarps = 4;
+constexpr int kThreads = 32 * (kFirstTail + kTailWarps);
+constexpr float kTopLog2 = 2.0f;              // a new maximum's weight is 2^2 ...
 constexpr float kRaiseLog2 = 8.0f;            // ... and none exceeds 2^8
-constexpr int kFewMoved = 4;                  // heads of 16 rescaled one by one
+constexpr int kFewMoved = 6;                  // heads of 32 rescaled one by one
 constexpr float kMinScale = 0x1p-40f;
 constexpr uint32_t kTmemCols = 512;           // S^T: 2 x 128 columns, O^T: 4 x 64
 constexpr uint32_t kColS = 0;
@@ -91,6 +98,16 @@ struct Params {
     int H, k, groups, out_bf16;
     float scale_log2;        // sm_scale * log2(e)
     int tiles_per_cta, n_split, n_tiles;
+    int units;               // (token, head group, split) triples, shared out to the CTAs
+};
+
+// One unit of work: a head group of a token, a run of its tiles.
+struct Unit {
+    int t, h0, nh, split;
+    int pos, seq;
+    int64_t kv0;
+    int tile_lo, n;          // first tile and tiles; none when the position is out of bounds
+    bool bad;
 };
 
 struct Ctl {
@@ -99,20 +116,23 @@ struct Ctl {
     uint64_t empty[kSlots];
     uint64_t s_full[2];
     uint64_t p_full[2];
+    uint64_t o_empty;        // the unit's accumulator has been read out
     uint64_t o_full[2];      // by tile parity: tile i's completes after tile i - 2's has been waited for
     uint32_t tmem_base;
     int32_t abort_flag;
-    alignas(16) float qs[kHeads];   // 2^e of the head's query times scale_log2
+    alignas(16) float qs[2][kHeads];   // by unit parity: 2^e of the head's query times scale_log2
+    float4 row[2][kRows];    // by tile parity: a row's scale (0: masked), its log2 and its inverse
     float red[4][kHeads];    // a tile's maxima by lane quarter; the row sums at the end
     alignas(16) float ma[kSoftmaxWarps][2 * kPartHeads];   // each warp's -m, and how far m moved
-    int32_t warp_alive[kSoftmaxWarps];
+    Unit unit[kSoftmaxWarps][2];        // each warp's current and next unit, by unit parity
 };
 
 // qs and ma are read four at a time
-static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
+static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && offsetof(Ctl, row) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
                   (kSlots * kBlockBytes + kQBytes) % 16 == 0, "16-byte reads of shared memory");
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
     if (*(volatile int32_t *)&c.abort_flag) return false;
     if (mbar_wait(bar, parity, limit_ns)) return true;
     *(volatile int32_t *)&c.abort_flag = 1;
@@ -132,17 +152,14 @@ __device__ __forceinline__ float warp_max(float x) {
     return r;
 }
 
-// Transposing butterfly: each lane holds 16 values, lane L ends up with the
-// sum of value L mod 16 over the warp.
-__device__ __forceinline__ float warp_sum_16(const float (&x)[16], int lane) {
-    float a[16];
+// Transposing butterfly: each lane holds 32 values, lane L ends up with the
+// sum of value L over the warp.
+__device__ __forceinline__ float warp_sum_32(float (&a)[32], int lane) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a[i] = x[i];
-#pragma unroll
-    for (int half = 8; half >= 1; half >>= 1) {
+    for (int half = 16; half >= 1; half >>= 1) {
         const bool up = lane & half;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) {
             if (i < half) {
                 const float keep = up ? a[half + i] : a[i];
                 const float send = up ? a[i] : a[half + i];
@@ -150,32 +167,61 @@ __device__ __forceinline__ float warp_sum_16(const float (&x)[16], int lane) {
             }
         }
     }
-    return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 16);
+    return a[0];
 }
 
-// 16 bf16 values in two words of four.
-__device__ __forceinline__ void bf16x16(const uint4 &a, const uint4 &b, float (&v)[16]) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// The largest magnitude of eight bf16 values, as 15 bits.
+__device__ __forceinline__ uint32_t max_bf16(const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    return m;
 }
 
-// The two e4m3 pieces of sixteen values.
-__device__ __forceinline__ void split16(const float (&v)[16], float inv, uint4 &hi, uint4 &lo) {
+// The two e4m3 pieces of eight bf16 values times inv.  The product is exact in
+// float32, and fp16 holds it to 2^-24: far below the last piece's 2^-10.
+__device__ __forceinline__ void split8(const uint4 &v, float inv, uint2 &hi, uint2 &lo) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = v[4 * i] * inv, b = v[4 * i + 1] * inv, c = v[4 * i + 2] * inv, d = v[4 * i + 3] * inv;
-        const uint32_t h0 = e4m3x2(a, b), h1 = e4m3x2(c, d);
-        const float2 f0 = e4m3x2_to_float2(h0), f1 = e4m3x2_to_float2(h1);
-        h[i] = h0 | h1 << 16;
-        l[i] = e4m3x2(a - f0.x, b - f0.y) | e4m3x2(c - f1.x, d - f1.y) << 16;
+        const __half2 x = __floats2half2_rn(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xFFFF0000u) * inv);
+        h[i] = e4m3x2(x);
+        l[i] = e4m3x2(__hsub2(x, e4m3x2_to_half2(h[i])));
     }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
+    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
+__device__ __forceinline__ Unit load_unit(const Params &p, int u, int lane) {
+    const DevBatch &b = p.b;
+    Unit w;
+    const int g = u / p.n_split;
+    w.split = u - g * p.n_split;
+    w.t = g / p.groups;
+    w.h0 = (g - w.t * p.groups) * kHeads;
+    w.nh = min(kHeads, p.H - w.h0);
+    w.pos = __ldg(b.q_pos + w.t);
+    w.seq = seq_of_warp(b.cu_q, b.B, w.t, lane);
+    w.kv0 = seq_base(b, w.seq);
+    w.tile_lo = w.split * p.tiles_per_cta;
+    int64_t own = -1;
+    if (w.pos >= 0 && w.pos < b.max_kv && w.kv0 >= 0) own = cache_row(b, w.seq, w.kv0, w.pos);
+    w.bad = own < 0 || own >= b.cache_rows;
+    w.n = w.bad ? 0 : max(0, min(p.n_tiles, w.tile_lo + p.tiles_per_cta) - w.tile_lo);
+    return w;
+}
+
+// Cache row of entry e of a unit's selection: -1 for padding and for entries
+// out of range (flagged where `report` is set).
+__device__ __forceinline__ int32_t row_of(const Params &p, const Unit &w, int e, bool report) {
+    const int32_t v = e < p.k ? __ldg(p.idx + (int64_t)w.t * p.k + e) : -1;
+    int64_t row = -1;
+    if (v >= 0 && v <= w.pos) row = cache_row(p.b, w.seq, w.kv0, v);
+    if (row >= p.b.cache_rows) row = -1;
+    if (row < 0 && v != -1 && report) flag(p.status, DSA_DEV_BAD_INDEX);
+    return (int32_t)row;
 }
 
 }  // namespace
@@ -189,43 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const DevBatch &b = p.b;
-    const int t = blockIdx.x / p.groups;
-    const int hg = blockIdx.x - t * p.groups;
-    const int h0 = hg * kHeads, nh = min(kHeads, p.H - h0);
-    const int split = blockIdx.y;
     const bool tail = p.q_rope != nullptr;
     const int width = tail ? kQ8Row : D_L;               // bytes per cached row
-    const int64_t part_idx = ((int64_t)t * p.n_split + split) * p.groups + hg;
+    const int step = gridDim.x;
     tl_start(b.timeline, kTlAttn);
-    const int pos = __ldg(b.q_pos + t);
-    const int seq = seq_of_warp(b.cu_q, b.B, t, lane);
-    const int64_t kv0 = seq_base(b, seq);
-    const int tile_lo = split * p.tiles_per_cta;
-    const int tile_hi = min(p.n_tiles, tile_lo + p.tiles_per_cta);
-    int64_t own_row = -1;
-    if (pos >= 0 && pos < b.max_kv && kv0 >= 0) own_row = cache_row(b, seq, kv0, pos);
-    const bool pos_ok = own_row >= 0 && own_row < b.cache_rows;
-    if (!pos_ok || tile_lo >= tile_hi) {
-        if (!pos_ok && threadIdx.x == 0 && split == 0) flag(p.status, DSA_DEV_BAD_POSITION);
-        if (p.n_split > 1) {
-            for (int i = threadIdx.x; i < kHeads * D_L / 2; i += kThreads)
-                reinterpret_cast<uint32_t *>(p.part_o + part_idx * kHeads * D_L)[i] = 0u;
-            if (threadIdx.x < kHeads) {
-                float *ml = p.part_ml + (part_idx * kHeads + threadIdx.x) * 2;
-                ml[0] = -INFINITY;
-                ml[1] = 0.f;
-            }
-        } else {
-            const int64_t o = ((int64_t)t * p.H + h0) * D_L;
-            for (int i = threadIdx.x; i < nh * D_L; i += kThreads) {
-                if (p.out_bf16) static_cast<uint16_t *>(p.out)[o + i] = 0;
-                else static_cast<float *>(p.out)[o + i] = 0.f;
-            }
-            if (p.lse && threadIdx.x < nh) p.lse[(int64_t)t * p.H + h0 + threadIdx.x] = -INFINITY;
-        }
-        return;
-    }
-    const int n_my = tile_hi - tile_lo;
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&ctl.q_full), kSoftmaxWarps);
@@ -236,12 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl.s_full[i]), 1);
             mbar_init(smem_u32(&ctl.p_full[i]), kSoftmaxWarps);
+            mbar_init(smem_u32(&ctl.o_full[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl.o_full[i]), 1);
+        mbar_init(smem_u32(&ctl.o_empty), kSoftmaxWarps);
         ctl.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == 0) {
         tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
         tmem_relinquish();
     }
@@ -249,441 +263,594 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
-    const int32_t *idx_row = p.idx + (int64_t)t * p.k;
-    // Cache row of entry e of the token's selection: -1 for padding and for
-    // entries out of range (flagged by one thread per entry).
-    auto row_of = [&](int e, bool report) -> int32_t {
-        const int32_t v = e < p.k ? __ldg(idx_row + e) : -1;
-        int64_t row = -1;
-        if (v >= 0 && v <= pos) row = cache_row(b, seq, kv0, v);
-        if (row >= b.cache_rows) row = -1;
-        if (row < 0 && v != -1 && report) flag(p.status, DSA_DEV_BAD_INDEX);
-        return (int32_t)row;
-    };
+    // Every role walks the CTA's units and their tiles in the same order.  g
+    // counts tiles over all units: tile g has S^T buffer g & 1, the phase
+    // (g >> 1) & 1 of the barriers of that parity, and blocks 5 g .. 5 g + 4 of
+    // the ring (slot n % 9, use n / 9).  v counts the units that have tiles.
 
-    if (warp > kMmaWarp) {
-        // ---------------- producers
-        const int pw = warp - kMmaWarp - 1;
-        const int j = min(pw, 4);                    // the warp's block of the tile
-        const uint8_t *src = p.codes + j * 128 + (lane & 7) * 16;
-        // lane's chunk of rows 4 g + lane / 8; g odd flips bit 2 of the swizzled chunk
+    if (warp >= kFirstTail) {
+        // ---------------- tail block: its slot frees last, so its rows wait in
+        // registers and only the stores lie between the free slot and the
+        // score product.  Rows without a tail have nothing to gather: the
+        // warps only pass the free slot on to the softmax, which puts P^T
+        // there.  The rows' scales go with it.
+        const int r0 = 32 * (warp - kFirstTail);
+        const uint8_t *src = p.codes + 4 * 128 + (lane & 7) * 16;
         const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
-        pdl_wait();                                  // the indices come from the preceding kernel
-        if (pw < 4) {
-            // a latent block: asynchronous copies into its slot
-            for (int it = 0; it < n_my; ++it) {
-                const uint32_t n = (uint32_t)(kTileBlocks * it + j), slot = n % kSlots, use = n / kSlots;
-                int32_t my_row[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) my_row[q] = row_of((tile_lo + it) * kRows + 32 * q + lane, j == 0);
-                if (!wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns)) break;
-                if (b.skip_copies) continue;
-                const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        const int32_t row = __shfl_sync(0xffffffffu, my_row[q], 4 * g + (lane >> 3));
-                        cp_async16_or_zero((dst + (uint32_t)(8 * q + g) * 512u) ^ ((uint32_t)(g & 1) << 6),
-                                           src + (int64_t)max(row, 0) * width, row < 0 ? 0u : 16u);
-                    }
-                cp_async_commit();
-                cp_async_wait_all();
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(&ctl.full[slot]));
-            }
-        } else {
-            // The tail block, whose slot frees last: its rows wait in
-            // registers, so that only the stores lie between the free slot
-            // and the score product.  Rows without a tail have nothing to
-            // gather: the warps only pass the free slot on to the softmax,
-            // which puts P^T there.
-            const int r0 = 32 * (pw - 4);
-            for (int it = 0; it < n_my; ++it) {
-                const uint32_t n = (uint32_t)(kTileBlocks * it + 4), slot = n % kSlots, use = n / kSlots;
+        bool go = true;
+        int g = 0;
+        pdl_wait();                                      // the indices come from the preceding kernel
+        for (int u = blockIdx.x; go && u < p.units; u += step) {
+            const Unit w = load_unit(p, u, lane);
+            for (int it = 0; go && it < w.n; ++it, ++g) {
+                const uint32_t n = (uint32_t)(kTileBlocks * g + 4), slot = n % kSlots, use = n / kSlots;
+                const int32_t my_row = row_of(p, w, (w.tile_lo + it) * kRows + r0 + lane, false);
+                // The row's scale for the softmax.  Any positive one will do; a
+                // row never written (scale 0) counts as zeros at the smallest.
+                float s = my_row < 0 ? 0.f : __ldg(p.scale + my_row);
                 uint4 v[8];
                 if (tail) {
-                    const int32_t my_row = row_of((tile_lo + it) * kRows + r0 + lane, false);
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        const int32_t row = __shfl_sync(0xffffffffu, my_row, 4 * g + (lane >> 3));
-                        v[g] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row >= 0) v[g] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * width));
+                    for (int i = 0; i < 8; ++i) {
+                        const int32_t row = __shfl_sync(0xffffffffu, my_row, 4 * i + (lane >> 3));
+                        v[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (row >= 0) v[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * width));
                     }
                 }
-                if (!wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns)) break;
-                if (b.skip_copies) continue;
+                if (my_row >= 0 && s < kMinScale) s = kMinScale;
+                const float4 rv = my_row < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f) : make_float4(s, log2f(s), 1.f / s, 0.f);
+                go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
+                if (!go || b.skip_copies) continue;
+                // (tile g - 1's first value product freed the slot, after the
+                // softmax of tile g - 2 had read these row values)
+                ctl.row[g & 1][r0 + lane] = rv;
                 if (tail) {
                     uint8_t *dst = ring + slot * kBlockBytes + r0 * 128;
 #pragma unroll
-                    for (int g = 0; g < 8; ++g)
-                        *reinterpret_cast<uint4 *>(dst + ((d0 + (uint32_t)g * 512u) ^ ((uint32_t)(g & 1) << 6))) = v[g];
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(dst + ((d0 + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6))) = v[i];
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
                 if (lane < 32 / kTailWarps) mbar_arrive(smem_u32(&ctl.full[slot]));
             }
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp > 0 && warp < kFirstSoftmax) {
+        // ---------------- latent blocks: block k = 4 g + j of the sequence of
+        // all tiles goes to warp k mod 3, which copies its 128 rows x 128 bytes
+        // asynchronously.  Row offsets (in 128-byte lines) are looked up before
+        // the slot is free; masked rows become zeros.
+        const int lw = warp - 1;
+        const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
+        const uint32_t lines = (uint32_t)width / 128u;
+        bool go = true;
+        int g = 0;
+        pdl_wait();
+        for (int u = blockIdx.x; go && u < p.units; u += step) {
+            const Unit w = load_unit(p, u, lane);
+            for (int k = 0; go && k < 4 * w.n; ++k) {
+                if ((4 * g + k) % kLatentWarps != lw) continue;
+                const int it = k >> 2, j = k & 3;
+                const uint32_t n = (uint32_t)(kTileBlocks * (g + it) + j), slot = n % kSlots, use = n / kSlots;
+                uint32_t off[32];
+                bool masked = false;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int32_t my_row = row_of(p, w, (w.tile_lo + it) * kRows + 32 * q + lane, j == 0);
+                    masked |= my_row < 0;
+                    const uint32_t mine = my_row < 0 ? ~0u : (uint32_t)my_row * lines;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) off[8 * q + i] = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
+                }
+                masked = __any_sync(0xffffffffu, masked);
+                go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
+                if (!go || b.skip_copies) continue;
+                const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
+                const uint8_t *src = p.codes + j * 128 + (lane & 7) * 16;
+                if (!masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        cp_async16((dst + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6), src + (uint64_t)off[i] * 128u);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        cp_async16_or_zero((dst + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6),
+                                           src + (off[i] == ~0u ? 0u : (uint64_t)off[i] * 128u), off[i] == ~0u ? 0u : 16u);
+                }
+                cp_async_commit();
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&ctl.full[slot]));
+            }
+            g += w.n;
+        }
+    } else if (warp == 0) {
         // ---------------- MMA issuer, in a fixed order per tile:
-        //   S(i + 1) latent blocks | P^T(i) | O(i) block 0 | S(i + 1) tail | O(i) blocks 1..3
+        //   S(g + 1) blocks 0, 1 | P^T(g) | O(g) block 0 | S(g + 1) blocks 2, 3, tail | O(g) blocks 1..3
         // The first value-product block frees the slot that the next tile's
         // tail needs; the rest of the value product runs beside the next
-        // softmax.  Polling for whichever input came first instead cost 360 to
-        // 600 cycles of bookkeeping per block against 300 to 460 of products.
-        // The whole warp runs the loop (uniform descriptors); one elected
-        // lane issues.
-        const uint32_t id_s = idesc_e4m3(kRows, 2 * kHeads, false, false);
-        const uint32_t id_o = idesc_e4m3(128, kHeads, true, true);
+        // softmax.  A unit's last tile has its whole value product first, then
+        // the next unit's first scores.  Polling for whichever input came
+        // first instead cost 360 to 600 cycles of bookkeeping per block
+        // against 300 to 460 of products.  The whole warp runs the loop
+        // (uniform descriptors); one elected lane issues.
+        const uint32_t id_s = idesc_f8(kRows, 2 * kHeads, false, false);
+        const uint32_t id_hi = idesc_f8(128, kHeads, true, true), id_lo = idesc_f8(128, kHeads, true, true, true);
         const uint32_t ra = smem_u32(ring), qa = smem_u32(q_s), full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
         const uint64_t s_a0 = sdesc_sw128(ra, 16, 1024), s_b0 = sdesc_sw128(qa, 16, 1024);
         const uint64_t s_bt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
         const uint64_t o_b0 = sdesc_sw64(ra, 16, 512);
         auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-            const bool ok = __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, p.status, b.wait_ns));
+            bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+            if (!ok) ok = __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, p.status, b.wait_ns));
             tc_fence_after();
             return ok;
         };
-        // Block j of tile i has number 5 i + j: slot and use follow from those
+        // Block j of tile g has number 5 g + j: slot and use follow from those
         // of the tile's first block (base, use0).
-        auto score_block = [&](int j, uint32_t base, uint32_t use0, uint32_t d_s, uint64_t bd, uint32_t b2) -> bool {
-            const uint32_t wrap = base + j >= kSlots ? 1u : 0u, slot = base + j - (wrap ? kSlots : 0u);
-            if (!wait(full0 + 8 * slot, (use0 + wrap) & 1u)) return false;
+        auto slot_of = [&](int j, uint32_t base) -> uint32_t { return base + j - (base + j >= kSlots ? kSlots : 0u); };
+        auto landed = [&](int j, uint32_t base, uint32_t use0) -> bool {
+            const uint32_t bar = full0 + 8 * slot_of(j, base), parity = (use0 + (base + j >= kSlots ? 1u : 0u)) & 1u;
+            return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+                   __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, p.status, b.wait_ns));
+        };
+        // The products of score block j of a tile with S^T buffer d_s; the last
+        // one's commit completes the tile's scores.  Called by the elected lane.
+        auto score_block = [&](int j, int g, uint32_t base) {
+            const uint64_t ad = s_a0 + (uint64_t)(slot_of(j, base) * (kBlockBytes >> 4));
+            const uint64_t bd = j < 4 ? s_b0 + (uint64_t)(j * (kQBlockBytes >> 4)) : s_bt;
+            const uint32_t b2 = j < 4 ? 4u : 0u;         // the tail's K steps 2, 3 (remainders) read the query again
+            const uint32_t d_s = tmem + kColS + (g & 1) * 2 * kHeads;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)((ks & 1) * 2) + (ks & 2 ? b2 : 0u), id_s, (j || ks) ? 1u : 0u);
+            if (j == (tail ? 4 : 3)) umma_commit(smem_u32(&ctl.s_full[g & 1]));
+        };
+        // Value-product block c of tile g.
+        auto value_block = [&](int c, uint32_t base, uint64_t bd, uint32_t acc0) {
+            const uint32_t slot = slot_of(c, base);
             const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
-            if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)((ks & 1) * 2) + (ks & 2 ? b2 : 0u), id_s, (j || ks) ? 1u : 0u);
+            for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+                for (int ks = 0; ks < kRows / 32; ++ks)
+                    umma_f8(tmem + kColO + c * kHeads, ad + (uint64_t)(ks * (32 * 128 >> 4)),
+                            bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), piece ? id_lo : id_hi, (piece || ks) ? 1u : acc0);
+            umma_commit(empty0 + 8 * slot);
+        };
+        int u = blockIdx.x;
+        // the next unit that has tiles, from u on
+        auto tiles_from = [&]() -> int {
+            for (; u < p.units; u += step) {
+                const int n = load_unit(p, u, lane).n;
+                if (n > 0) return n;
             }
-            __syncwarp();
-            return true;
+            return 0;
         };
-        auto score_latent = [&](int it, uint32_t base, uint32_t use0) -> bool {
-            const uint32_t d_s = tmem + kColS + (it & 1) * 2 * kHeads;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (!score_block(j, base, use0, d_s, s_b0 + (uint64_t)(j * (kQBlockBytes >> 4)), 4)) return false;
-            if (!tail && elect_one()) umma_commit(smem_u32(&ctl.s_full[it & 1]));
-            __syncwarp();
-            return true;
-        };
-        auto score_tail = [&](int it, uint32_t base, uint32_t use0) -> bool {
-            if (!tail) return true;
-            // K steps 2 and 3, the remainders, read the query again
-            if (!score_block(4, base, use0, tmem + kColS + (it & 1) * 2 * kHeads, s_bt, 0)) return false;
-            if (elect_one()) umma_commit(smem_u32(&ctl.s_full[it & 1]));
-            __syncwarp();
-            return true;
-        };
-        bool go = wait(smem_u32(&ctl.q_full), 0) && score_latent(0, 0, 0) && score_tail(0, 0, 0);
+        int n = tiles_from();
         uint32_t base = 0, use0 = 0;
-        for (int it = 0; go && it < n_my; ++it) {
-            const uint32_t wrap = base + kTileBlocks >= kSlots ? 1u : 0u;
-            const uint32_t next = base + kTileBlocks - (wrap ? kSlots : 0u), next_use = use0 + wrap;
-            const bool more = it + 1 < n_my;
-            if (more) go = score_latent(it + 1, next, next_use);
-            go = go && wait(smem_u32(&ctl.p_full[it & 1]), (uint32_t)(it >> 1) & 1u);
-            if (!go) break;
-            const uint32_t pslot = base + 4 - (base + 4 >= kSlots ? kSlots : 0u);
-            const uint64_t bd = o_b0 + (uint64_t)(pslot * (kBlockBytes >> 4));
-            const uint32_t acc0 = it > 0 ? 1u : 0u;
+        int g = 0, v = 0;
+        bool go = n > 0;
+        while (go) {
+            // the unit's first scores
+            go = wait(smem_u32(&ctl.q_full), (uint32_t)v & 1u);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t slot = base + c - (base + c >= kSlots ? kSlots : 0u);
-                const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+            for (int j = 0; j < 5; ++j) {
+                if (j == 4 && !tail) break;
+                go = go && landed(j, base, use0);
+                if (go && elect_one()) score_block(j, g, base);
+                __syncwarp();
+            }
+            for (int it = 0; go && it < n; ++it, ++g) {
+                const uint32_t next = slot_of(kTileBlocks, base), next_use = use0 + (base + kTileBlocks >= kSlots ? 1u : 0u);
+                const bool more = it + 1 < n;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!more) break;
+                    go = go && landed(j, next, next_use);
+                    if (go && elect_one()) score_block(j, g + 1, next);
+                    __syncwarp();
+                }
+                const uint32_t pslot = slot_of(4, base);
+                const uint64_t bd = o_b0 + (uint64_t)(pslot * (kBlockBytes >> 4));
+                const uint32_t acc0 = it > 0 ? 1u : 0u;
+                go = go && wait(smem_u32(&ctl.p_full[g & 1]), (uint32_t)(g >> 1) & 1u);
+                // the accumulator of the unit before has been read
+                if (it == 0 && v > 0) go = go && wait(smem_u32(&ctl.o_empty), (uint32_t)(v - 1) & 1u);
+                if (!go) break;
+                if (elect_one()) value_block(0, base, bd, acc0);
+                __syncwarp();
+#pragma unroll
+                for (int j = 2; j < 5; ++j) {
+                    if (!more || (j == 4 && !tail)) break;
+                    go = go && landed(j, next, next_use);
+                    if (go && elect_one()) score_block(j, g + 1, next);
+                    __syncwarp();
+                }
                 if (elect_one()) {
 #pragma unroll
-                    for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-                        for (int ks = 0; ks < kRows / 32; ++ks)
-                            umma_f8(tmem + kColO + c * kHeads, ad + (uint64_t)(ks * (32 * 128 >> 4)),
-                                    bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), id_o, (piece || ks) ? 1u : acc0);
-                    umma_commit(empty0 + 8 * slot);
-                    if (c == 3) {
-                        umma_commit(empty0 + 8 * pslot);
-                        umma_commit(smem_u32(&ctl.o_full[it & 1]));
-                    }
+                    for (int c = 1; c < 4; ++c) value_block(c, base, bd, acc0);
+                    // a unit's last P^T slot goes to the epilogue, which frees it
+                    if (more) umma_commit(empty0 + 8 * pslot);
+                    umma_commit(smem_u32(&ctl.o_full[g & 1]));
                 }
                 __syncwarp();
-                if (c == 0 && more) go = score_tail(it + 1, next, next_use);
+                base = next;
+                use0 = next_use;
             }
-            base = next;
-            use0 = next_use;
+            if (!go) break;
+            u += step;
+            ++v;
+            n = tiles_from();
+            go = n > 0;
         }
     } else {
-        // ---------------- queries, softmax and epilogue (warps 0..15)
-        const int quarter = warp & 3;                      // TMEM lanes 32*quarter ..
-        const int part = warp >> 2;                        // heads 16*part ..
+        // ---------------- queries, softmax and epilogue
+        const int sw = warp - kFirstSoftmax, tx = (int)threadIdx.x - 32 * kFirstSoftmax;
+        const int quarter = sw & 3;                        // TMEM lanes 32*quarter ..
+        const int part = sw >> 2;                          // heads 16*part ..
         const int hb = kPartHeads * part;
         const int r = quarter * 32 + lane;                 // row within the tile
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-        float *ma = ctl.ma[warp];
-        // each warp splits four heads' queries: lane l the values 16 l .. 16 l + 15
-#pragma unroll 2
-        for (int i = 0; i < kHeads / kSoftmaxWarps; ++i) {
-            const int h = warp * (kHeads / kSoftmaxWarps) + i;
-            uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a, ra = a, rc = a;
-            if (h < nh) {
-                const int64_t row = (int64_t)t * p.H + h0 + h;
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * D_L) + 2 * lane;
-                a = __ldg(src);
-                c = __ldg(src + 1);
-                if (tail && lane < 4) {
-                    const uint4 *rs = reinterpret_cast<const uint4 *>(p.q_rope + row * D_R) + 2 * lane;
-                    ra = __ldg(rs);
-                    rc = __ldg(rs + 1);
-                }
-            }
-            float v[16], w[16];
-            bf16x16(a, c, v);
-            bf16x16(ra, rc, w);
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) top = max(top, max(__float_as_uint(v[k]) & 0x7FFFFFFFu, __float_as_uint(w[k]) & 0x7FFFFFFFu));
-            top = __reduce_max_sync(0xffffffffu, top);
-            const int e = q8_exponent(__uint_as_float(top));
-            const float inv = exp2_int(-e);
-            uint4 hi, lo;
-            split16(v, inv, hi, lo);
-            uint8_t *blk = q_s + (lane >> 3) * kQBlockBytes;
-            *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)h, (uint32_t)(lane & 7))) = hi;
-            *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(kHeads + h), (uint32_t)(lane & 7))) = lo;
-            if (lane < 4) {
-                split16(w, inv, hi, lo);
-                uint8_t *tb = q_s + 4 * kQBlockBytes;
-                *reinterpret_cast<uint4 *>(tb + sw64_offset((uint32_t)h, (uint32_t)lane)) = hi;
-                *reinterpret_cast<uint4 *>(tb + sw64_offset((uint32_t)(kHeads + h), (uint32_t)lane)) = lo;
-            }
-            if (lane == 0) ctl.qs[h] = h < nh ? exp2_int(e) * p.scale_log2 : 0.f;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full));
-        pdl_wait();
+        float *ma = ctl.ma[sw];
         bool alive = true;
-        named_barrier(1, kSoftmaxThreads);
-        uint64_t lpart[8];                                 // row sums of l, two heads each
-#pragma unroll
-        for (int h = 0; h < 8; ++h) lpart[h] = f2(0.f, 0.f);
-        // lane h < 16: the reference m of head hb + h, 3.5 to 8 below its
-        // largest u so far (the same in the four warps of the part); 0 as long
-        // as every row was masked (fresh)
-        float m = 0.f;
-        bool fresh = true;
-        if (lane < 16) ma[lane] = 0.f;
-        __syncwarp();
-        // Scale of this thread's row of a tile (0: masked), looked up a tile
-        // ahead.  Any positive scale will do; a row never written (scale 0)
-        // counts as zeros at the smallest one.
-        auto scale_of = [&](int it) -> float {
-            const int32_t row = row_of((tile_lo + it) * kRows + r, false);
-            if (row < 0) return 0.f;
-            const float s = __ldg(p.scale + row);
-            return s < kMinScale ? kMinScale : s;
+        int g = 0, v = 0;
+
+        // A unit without tiles: zeros (an empty partial of a split).
+        auto write_empty = [&](const Unit &w) {
+            if (w.bad && tx == 0 && w.split == 0) flag(p.status, DSA_DEV_BAD_POSITION);
+            if (p.n_split > 1) {
+                const int64_t part_row = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
+                for (int i = tx; i < kHeads * D_L / 2; i += kSoftmaxThreads)
+                    reinterpret_cast<uint32_t *>(p.part_o + part_row * D_L)[i] = 0u;
+                if (tx < kHeads) {
+                    p.part_ml[(part_row + tx) * 2] = -INFINITY;
+                    p.part_ml[(part_row + tx) * 2 + 1] = 0.f;
+                }
+            } else {
+                const int64_t row = (int64_t)w.t * p.H + w.h0;
+                for (int i = tx; i < w.nh * D_L; i += kSoftmaxThreads) {
+                    if (p.out_bf16) static_cast<uint16_t *>(p.out)[row * D_L + i] = 0;
+                    else static_cast<float *>(p.out)[row * D_L + i] = 0.f;
+                }
+                if (p.lse && tx < w.nh) p.lse[row + tx] = -INFINITY;
+            }
         };
-        float next_scale = scale_of(0);
+        // The unit's queries as two pieces.  Each warp splits eight heads, four
+        // at a time: of the latent values lane l takes 16 l .. 16 l + 15 of every
+        // head, of the tails eight values of head l / 8.
+        auto stage_queries = [&](const Unit &w, int parity) {
+            static_assert(kHeads / kSoftmaxWarps == 8, "two batches of four heads");
+#pragma unroll 1
+            for (int h0 = sw * 8; h0 < sw * 8 + 8; h0 += 4) {
+                const int64_t row0 = (int64_t)w.t * p.H + w.h0 + h0;
+                uint4 a[4], c[4], tv = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = c[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (h0 + i < w.nh) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + (row0 + i) * D_L) + 2 * lane;
+                        a[i] = __ldg(src);
+                        c[i] = __ldg(src + 1);
+                    }
+                }
+                const int ht = lane >> 3;                  // the lane's head of the tails
+                if (tail && h0 + ht < w.nh) tv = __ldg(reinterpret_cast<const uint4 *>(p.q_rope + (row0 + ht) * D_R) + (lane & 7));
+                float inv_t = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // the largest magnitude, by its bf16 bits
+                    uint32_t top = ht == i ? max_bf16(tv) : 0u;
+                    top = __reduce_max_sync(0xffffffffu, max(top, max(max_bf16(a[i]), max_bf16(c[i]))));
+                    const int e = q8_exponent(__uint_as_float(top << 16));
+                    const float inv = exp2_int(-e);
+                    if (ht == i) inv_t = inv;
+                    uint2 h2[2], l2[2];
+                    split8(a[i], inv, h2[0], l2[0]);
+                    split8(c[i], inv, h2[1], l2[1]);
+                    uint8_t *blk = q_s + (lane >> 3) * kQBlockBytes;
+                    *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(h0 + i), (uint32_t)(lane & 7))) =
+                        make_uint4(h2[0].x, h2[0].y, h2[1].x, h2[1].y);
+                    *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(kHeads + h0 + i), (uint32_t)(lane & 7))) =
+                        make_uint4(l2[0].x, l2[0].y, l2[1].x, l2[1].y);
+                    if (lane == 0) ctl.qs[parity][h0 + i] = h0 + i < w.nh ? exp2_int(e) * p.scale_log2 : 0.f;
+                }
+                uint2 h2, l2;
+                split8(tv, inv_t, h2, l2);
+                uint8_t *tb = q_s + 4 * kQBlockBytes + (lane & 1) * 8;
+                *reinterpret_cast<uint2 *>(tb + sw64_offset((uint32_t)(h0 + ht), (uint32_t)(lane & 7) >> 1)) = h2;
+                *reinterpret_cast<uint2 *>(tb + sw64_offset((uint32_t)(kHeads + h0 + ht), (uint32_t)(lane & 7) >> 1)) = l2;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full));
+        };
+        // Asks L2 for the warp's heads of a unit.
+        auto prefetch_queries = [&](const Unit &w) {
+            const int h = sw * (kHeads / kSoftmaxWarps) + lane;
+            if (lane < kHeads / kSoftmaxWarps && h < w.nh) {
+                prefetch_l2_bulk(p.q_lat + ((int64_t)w.t * p.H + w.h0 + h) * D_L, 2 * D_L);
+                if (tail) prefetch_l2_bulk(p.q_rope + ((int64_t)w.t * p.H + w.h0 + h) * D_R, 2 * D_R);
+            }
+        };
+        int u = blockIdx.x;
+        // The next unit that has tiles, from u on (n = 0: none is left); the
+        // empty ones on the way get their outputs.
+        auto next_unit = [&](int parity) {
+            Unit w;
+            w.n = 0;
+            for (; u < p.units; u += step) {
+                w = load_unit(p, u, lane);
+                if (w.n > 0) break;
+                write_empty(w);
+            }
+            if (lane == 0) ctl.unit[sw][parity] = w;
+            __syncwarp();
+        };
+
+        next_unit(0);
+        if (ctl.unit[sw][0].n > 0) stage_queries(ctl.unit[sw][0], 0);
+        pdl_wait();
         // Every softmax thread runs the same sequence of named barriers whatever
         // happens; `alive` (warp-uniform) only gates tensor-memory and shared
         // memory work after a bounded wait gave up.
-        for (int it = 0; it < n_my; ++it) {
-            const int buf = it & 1;
-            const float rs = next_scale;
-            if (it + 1 < n_my) next_scale = scale_of(it + 1);
-            const bool valid = rs != 0.f;                  // a masked row's products are 0: u = -inf
-            const float ef = valid ? log2f(rs) : -INFINITY;
-            const float irs = valid ? 1.f / rs : 0.f;
-            const uint64_t rs2 = f2(rs, rs), ef2 = f2(ef, ef), irs2 = f2(irs, irs);
-            if (alive) alive = wait_bar(smem_u32(&ctl.s_full[buf]), (uint32_t)(it >> 1) & 1u, ctl, p.status, b.wait_ns);
-            alive = __all_sync(0xffffffffu, alive);
-            float x[16], top = -INFINITY;                  // u, then u - m
-            if (alive) {
-                tc_fence_after();
-                uint32_t u[16], w[16];
-                const uint32_t a = tmem + lane_addr + kColS + buf * 2 * kHeads + hb;
-                tmem_ld16(a, u);
-                tmem_ld16(a + kHeads, w);
-                tmem_wait_ld(u, w);
+        while (ctl.unit[sw][v & 1].n > 0) {
+            const Unit &w = ctl.unit[sw][v & 1];
+            const int n_tiles = w.n;
+            uint64_t lpart[kPartHeads / 2];                // row sums of l, two heads each
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 q4 = *reinterpret_cast<const float4 *>(ctl.qs + hb + 4 * i);
-                    const float4 n4 = *reinterpret_cast<const float4 *>(ma + 4 * i);
-                    const uint64_t qs[2] = {f2(q4.x, q4.y), f2(q4.z, q4.w)}, nm[2] = {f2(n4.x, n4.y), f2(n4.z, n4.w)};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int h = 4 * i + 2 * j;
-                        const uint64_t a2 = f2(__uint_as_float(u[h]), __uint_as_float(u[h + 1]));
-                        const uint64_t b2 = f2(__uint_as_float(w[h]), __uint_as_float(w[h + 1]));
-                        const float2 v = f2_get(f2_add(f2_fma(f2_mul(f2_add(a2, b2), rs2), qs[j], nm[j]), ef2));
-                        x[h] = v.x;
-                        x[h + 1] = v.y;
-                        top = fmaxf(top, fmaxf(v.x, v.y));
-                    }
+            for (int h = 0; h < kPartHeads / 2; ++h) lpart[h] = f2(0.f, 0.f);
+            // lane h: the reference m of head hb + h, 2 to 8 below its largest
+            // u so far (the same in the four warps of the part); 0 as long as
+            // every row was masked (fresh)
+            float m = 0.f;
+            bool fresh = true;
+            ma[lane] = 0.f;
+            __syncwarp();
+            const float *qs_u = ctl.qs[v & 1] + hb;
+            if (alive) alive = wait_bar(smem_u32(&ctl.q_full), (uint32_t)v & 1u, ctl, p.status, b.wait_ns);   // everyone's qs
+            for (int it = 0; it < n_tiles; ++it, ++g) {
+                const int buf = g & 1;
+                if (it + 1 == n_tiles) {
+                    u += step;
+                    next_unit((v + 1) & 1);
+                    if (ctl.unit[sw][(v + 1) & 1].n > 0) prefetch_queries(ctl.unit[sw][(v + 1) & 1]);
                 }
-            } else {
-#pragma unroll
-                for (int h = 0; h < 16; ++h) x[h] = -INFINITY;
-            }
-            // Does any weight of the part exceed 2^8?  Then the heads' maxima
-            // are found and m moves where it has to; few tiles but a token's
-            // first come here.
-            uint32_t moved = 0;                            // heads of the part whose m moves
-            if (named_barrier_or(2 + part, 128, fresh || top > kRaiseLog2)) {
-                float wmax[16];
-#pragma unroll
-                for (int h = 0; h < 16; ++h) wmax[h] = warp_max(x[h]);
-                float over = wmax[0];
-#pragma unroll
-                for (int h = 1; h < 16; ++h) over = (lane & 15) == h ? wmax[h] : over;
-                if (lane < 16) ctl.red[quarter][hb + lane] = over;
-                named_barrier(2 + part, 128);
-                const int hl = hb + (lane & 15);
-                over = fmaxf(fmaxf(ctl.red[0][hl], ctl.red[1][hl]), fmaxf(ctl.red[2][hl], ctl.red[3][hl]));
-                const float up = (fresh ? over != -INFINITY : over > kRaiseLog2) ? over - kTopLog2 : 0.f;
-                m += up;
-                if (lane < 16) {
-                    ma[lane] = -m;
-                    ma[kPartHeads + lane] = up;
-                }
-                moved = fresh ? 0u : __ballot_sync(0xffffffffu, lane < 16 && up != 0.f);
-                fresh = __all_sync(0xffffffffu, over == -INFINITY) && fresh;
-                __syncwarp();
-#pragma unroll
-                for (int h = 0; h < 16; ++h) x[h] -= ma[kPartHeads + h];
-                if (moved) {
-#pragma unroll
-                    for (int h = 0; h < 8; ++h)
-                        lpart[h] = f2_mul(lpart[h], f2(ex2(-ma[kPartHeads + 2 * h]), ex2(-ma[kPartHeads + 2 * h + 1])));
-                }
-            }
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float w[4] = {ex2(x[4 * i]), ex2(x[4 * i + 1]), ex2(x[4 * i + 2]), ex2(x[4 * i + 3])};
-                lpart[2 * i] = f2_fma(f2(w[0], w[1]), irs2, lpart[2 * i]);
-                lpart[2 * i + 1] = f2_fma(f2(w[2], w[3]), irs2, lpart[2 * i + 1]);
-                // through fp16, whose 11 bits the two pieces cannot tell from 24
-                const __half2 a = __floats2half2_rn(w[0], w[1]), c = __floats2half2_rn(w[2], w[3]);
-                const uint32_t ha = e4m3x2(a), hc = e4m3x2(c);
-                hi[i] = ha | hc << 16;
-                lo[i] = e4m3x2(__hsub2(a, e4m3x2_to_half2(ha))) | e4m3x2(__hsub2(c, e4m3x2_to_half2(hc))) << 16;
-            }
-            const uint32_t pn = (uint32_t)(kTileBlocks * it + 4), pslot = pn % kSlots;
-            if (!tail && alive) {
-                // no score product has waited for this slot
-                alive = wait_bar(smem_u32(&ctl.full[pslot]), (pn / kSlots) & 1u, ctl, p.status, b.wait_ns);
+                // the row values and, without a tail, the free slot of P^T: no
+                // score product has waited for it
+                const uint32_t pn = (uint32_t)(kTileBlocks * g + 4), pslot = pn % kSlots;
+                if (alive) alive = wait_bar(smem_u32(&ctl.full[pslot]), (pn / kSlots) & 1u, ctl, p.status, b.wait_ns);
+                const float4 rv = ctl.row[buf][r];         // a masked row's products are 0: u = -inf
+                const uint64_t rs2 = f2(rv.x, rv.x), ef2 = f2(rv.y, rv.y), irs2 = f2(rv.z, rv.z);
+                if (alive) alive = wait_bar(smem_u32(&ctl.s_full[buf]), (uint32_t)(g >> 1) & 1u, ctl, p.status, b.wait_ns);
                 alive = __all_sync(0xffffffffu, alive);
-            }
-            if (alive) {
-                uint8_t *pb = ring + pslot * kBlockBytes + sw64_offset((uint32_t)r, (uint32_t)part);
-                *reinterpret_cast<uint4 *>(pb) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(pb + kPieceBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-            if (moved && it > 0) {
-                // Columns of O^T whose maximum moved, once the previous tile's
-                // value product has landed: one by one while they are few
-                // (the usual tile moves one or two of 64 heads), else all.
-                if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(it - 1) & 1]), (uint32_t)((it - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
-                alive = __all_sync(0xffffffffu, alive);
+                float x[kPartHeads], top = -INFINITY;      // u - m
                 if (alive) {
                     tc_fence_after();
-                    const uint32_t o = tmem + lane_addr + kColO + hb;
-                    if (__popc(moved) <= kFewMoved) {
-                        while (moved) {
-                            const int h = __ffs(moved) - 1;
-                            moved &= moved - 1;
-                            const float al = ex2(-ma[kPartHeads + h]);
-                            uint32_t u[4];
+                    const uint32_t a = tmem + lane_addr + kColS + buf * 2 * kHeads + hb;
+uint32_t a16[2][16], b16[2][16];
+                    tmem_ld16(a, a16[0]);
+                    tmem_ld16(a + kHeads, b16[0]);
+                    tmem_wait_ld(a16[0], b16[0]);
+                    tmem_ld16(a + 16, a16[1]);             // lands behind the first half's arithmetic
+                    tmem_ld16(a + kHeads + 16, b16[1]);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) tmem_ld1(o + c * kHeads + h, u[c]);
-                            tmem_wait_ld(u);
+                    for (int half = 0; half < 2; ++half) {
+                        if (half) tmem_wait_ld(a16[1], b16[1]);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) tmem_st1(o + c * kHeads + h, __float_as_uint(__uint_as_float(u[c]) * al));
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t u[16];
-                            tmem_ld16(o + c * kHeads, u);
-                            tmem_wait_ld(u);
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 q4 = *reinterpret_cast<const float4 *>(qs_u + 16 * half + 4 * i);
+                            const float4 n4 = *reinterpret_cast<const float4 *>(ma + 16 * half + 4 * i);
+                            const uint64_t qs[2] = {f2(q4.x, q4.y), f2(q4.z, q4.w)}, nm[2] = {f2(n4.x, n4.y), f2(n4.z, n4.w)};
 #pragma unroll
-                            for (int h = 0; h < 16; ++h) u[h] = __float_as_uint(__uint_as_float(u[h]) * ex2(-ma[kPartHeads + h]));
-                            tmem_st16(o + c * kHeads, u);
+                            for (int j = 0; j < 2; ++j) {
+                                const int h = 4 * i + 2 * j;
+                                const uint64_t a2 = f2(__uint_as_float(a16[half][h]), __uint_as_float(a16[half][h + 1]));
+                                const uint64_t b2 = f2(__uint_as_float(b16[half][h]), __uint_as_float(b16[half][h + 1]));
+                                const float2 d = f2_get(f2_add(f2_fma(f2_mul(f2_add(a2, b2), rs2), qs[j], nm[j]), ef2));
+                                x[16 * half + h] = d.x;
+                                x[16 * half + h + 1] = d.y;
+                                top = fmaxf(top, fmaxf(d.x, d.y));
+                            }
                         }
                     }
-                    tmem_wait_st();
+                } else {
+#pragma unroll
+                    for (int h = 0; h < kPartHeads; ++h) x[h] = -INFINITY;
+                }
+                // Does any weight of the part exceed 2^8?  Then the heads'
+                // maxima are found and m moves where it has to; few tiles but a
+                // unit's first come here.
+                uint32_t moved = 0;                        // heads of the part whose m moves
+                if (named_barrier_or(2 + part, 128, fresh || top > kRaiseLog2)) {
+                    float over = 0.f;
+#pragma unroll
+                    for (int h = 0; h < kPartHeads; ++h) {
+                        const float v32 = warp_max(x[h]);
+                        over = lane == h ? v32 : over;
+                    }
+                    ctl.red[quarter][hb + lane] = over;
+                    named_barrier(2 + part, 128);
+                    const int hl = hb + lane;
+                    over = fmaxf(fmaxf(ctl.red[0][hl], ctl.red[1][hl]), fmaxf(ctl.red[2][hl], ctl.red[3][hl]));
+                    const float up = (fresh ? over != -INFINITY : over > kRaiseLog2) ? over - kTopLog2 : 0.f;
+                    m += up;
+                    ma[lane] = -m;
+                    ma[kPartHeads + lane] = up;
+                    moved = fresh ? 0u : __ballot_sync(0xffffffffu, up != 0.f);
+                    fresh = __all_sync(0xffffffffu, over == -INFINITY) && fresh;
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < kPartHeads; ++h) x[h] -= ma[kPartHeads + h];
+                    if (moved) {
+#pragma unroll
+                        for (int h = 0; h < kPartHeads / 2; ++h)
+                            lpart[h] = f2_mul(lpart[h], f2(ex2(-ma[kPartHeads + 2 * h]), ex2(-ma[kPartHeads + 2 * h + 1])));
+                    }
+                }
+                // the weights' two pieces, 16 heads (16 bytes) at a time
+                uint8_t *pb = ring + pslot * kBlockBytes;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int h = 16 * half + 4 * i;
+                        const float e[4] = {ex2(x[h]), ex2(x[h + 1]), ex2(x[h + 2]), ex2(x[h + 3])};
+                        lpart[h / 2] = f2_fma(f2(e[0], e[1]), irs2, lpart[h / 2]);
+                        lpart[h / 2 + 1] = f2_fma(f2(e[2], e[3]), irs2, lpart[h / 2 + 1]);
+                        // through fp16, whose 11 bits the two pieces cannot tell from 24
+                        const __half2 a = __floats2half2_rn(e[0], e[1]), c = __floats2half2_rn(e[2], e[3]);
+                        const uint32_t ha = e4m3x2(a), hc = e4m3x2(c);
+                        hi[i] = ha | hc << 16;
+                        lo[i] = e5m2x2(__hsub2(a, e4m3x2_to_half2(ha))) | e5m2x2(__hsub2(c, e4m3x2_to_half2(hc))) << 16;
+                    }
+                    if (alive) {
+                        const uint32_t o = sw64_offset((uint32_t)r, (uint32_t)(2 * part + half));
+                        *reinterpret_cast<uint4 *>(pb + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(pb + kPieceBytes + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                if (moved && it > 0) {
+                    // Columns of O^T whose reference moved, once the previous
+                    // tile's value product has landed: one by one while they
+                    // are few, else all.
+                    if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(g - 1) & 1]), (uint32_t)((g - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
+                    alive = __all_sync(0xffffffffu, alive);
+                    if (alive) {
+                        tc_fence_after();
+                        const uint32_t o = tmem + lane_addr + kColO + hb;
+                        if (__popc(moved) <= kFewMoved) {
+                            while (moved) {
+                                const int h = __ffs(moved) - 1;
+                                moved &= moved - 1;
+                                const float al = ex2(-ma[kPartHeads + h]);
+                                uint32_t c4[4];
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) tmem_ld1(o + c * kHeads + h, c4[c]);
+                                tmem_wait_ld(c4);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) tmem_st1(o + c * kHeads + h, __float_as_uint(__uint_as_float(c4[c]) * al));
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t c16[16];
+                                const uint32_t at = o + (c >> 1) * kHeads + (c & 1) * 16;
+                                const float *up = ma + kPartHeads + (c & 1) * 16;
+                                tmem_ld16(at, c16);
+                                tmem_wait_ld(c16);
+#pragma unroll
+                                for (int h = 0; h < 16; ++h) c16[h] = __float_as_uint(__uint_as_float(c16[h]) * ex2(-up[h]));
+                                tmem_st16(at, c16);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[buf]));
+            }
+            // ---- While the last value product runs: the next unit's queries
+            // (the score products have read this one's).
+            const Unit &wn = ctl.unit[sw][(v + 1) & 1];
+            if (wn.n > 0) stage_queries(wn, (v + 1) & 1);
+            // ---- outputs
+            const int gl = g - 1;                          // the unit's last tile
+            if (alive) alive = wait_bar(smem_u32(&ctl.o_full[gl & 1]), (uint32_t)(gl >> 1) & 1u, ctl, p.status, b.wait_ns);
+            alive = __all_sync(0xffffffffu, alive);
+            float lrow[kPartHeads];
+#pragma unroll
+            for (int h = 0; h < kPartHeads / 2; ++h) {
+                const float2 d = f2_get(lpart[h]);
+                lrow[2 * h] = d.x;
+                lrow[2 * h + 1] = d.y;
+            }
+            const float lsum = warp_sum_32(lrow, lane);
+            named_barrier(2 + part, 128);                  // red may still be read
+            ctl.red[quarter][hb + lane] = lsum;
+            named_barrier(2 + part, 128);
+            const int hl = hb + lane;
+            const float l = ctl.red[0][hl] + ctl.red[1][hl] + ctl.red[2][hl] + ctl.red[3][hl];
+            ma[lane] = p.n_split > 1 ? 1.f : fresh ? 0.f : 1.f / l;
+            __syncwarp();
+            const int64_t row0 = (int64_t)w.t * p.H + w.h0;
+            const int64_t part0 = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
+            const uint32_t eslot = (uint32_t)(kTileBlocks * gl + 4) % kSlots;
+            if (alive) {
+                // Thread (quarter, lane) holds output dim 128 c + 32 quarter +
+                // lane of the part's heads.  16-bit results go through 2 KB of
+                // the tile's P^T slot per warp, head pairs side by side, and leave
+                // as 16 bytes (eight dims) per lane; float32 ones go straight out.
+                tc_fence_after();
+                const bool half = p.n_split > 1 || p.out_bf16;
+                uint16_t *dst = p.n_split > 1 ? p.part_o + part0 * D_L : static_cast<uint16_t *>(p.out) + row0 * D_L;
+                const int live = p.n_split > 1 ? kHeads : w.nh;
+                uint32_t *stage = reinterpret_cast<uint32_t *>(ring + eslot * kBlockBytes + sw * 2048);
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {              // 4 dim blocks x 2 groups of 16 heads
+                    const int d = (c >> 1) * 128 + quarter * 32, hq = (c & 1) * 16;
+                    uint32_t *st = stage + (c & 1) * 256;
+                    const float *il = ma + hq;
+                    uint32_t c16[16];
+                    tmem_ld16(tmem + lane_addr + kColO + (c >> 1) * kHeads + hb + hq, c16);
+                    tmem_wait_ld(c16);
+                    if (half) {
+                        __syncwarp();                      // st was read two turns ago
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 f = *reinterpret_cast<const float2 *>(il + 2 * i);
+                            const __nv_bfloat162 o2 = __floats2bfloat162_rn(__uint_as_float(c16[2 * i]) * f.x, __uint_as_float(c16[2 * i + 1]) * f.y);
+                            st[32 * i + lane] = *reinterpret_cast<const uint32_t *>(&o2);
+                        }
+                        __syncwarp();
+                        // lane: heads 2 i and 2 i + 1 with i = lane / 4, dims 8 (lane % 4) ..
+                        const uint4 e0 = *reinterpret_cast<const uint4 *>(st + 8 * lane), e1 = *reinterpret_cast<const uint4 *>(st + 8 * lane + 4);
+                        const int h = hb + hq + 2 * (lane >> 2), dd = d + 8 * (lane & 3);
+                        if (h < live)
+                            *reinterpret_cast<uint4 *>(dst + (int64_t)h * D_L + dd) =
+                                make_uint4(__byte_perm(e0.x, e0.y, 0x5410), __byte_perm(e0.z, e0.w, 0x5410),
+                                           __byte_perm(e1.x, e1.y, 0x5410), __byte_perm(e1.z, e1.w, 0x5410));
+                        if (h + 1 < live)
+                            *reinterpret_cast<uint4 *>(dst + (int64_t)(h + 1) * D_L + dd) =
+                                make_uint4(__byte_perm(e0.x, e0.y, 0x7632), __byte_perm(e0.z, e0.w, 0x7632),
+                                           __byte_perm(e1.x, e1.y, 0x7632), __byte_perm(e1.z, e1.w, 0x7632));
+                    } else {
+                        float *of = static_cast<float *>(p.out) + row0 * D_L + d + lane;
+#pragma unroll
+                        for (int h = 0; h < 16; ++h)
+                            if (hb + hq + h < live) of[(int64_t)(hb + hq + h) * D_L] = __uint_as_float(c16[h]) * il[h];
+                    }
+                }
+                if (quarter == 0) {
+                    const int h = hb + lane;
+                    if (p.n_split > 1) {
+                        p.part_ml[(part0 + h) * 2] = fresh ? -INFINITY : m;
+                        p.part_ml[(part0 + h) * 2 + 1] = l;
+                    } else if (p.lse && h < w.nh) {
+                        p.lse[row0 + h] = fresh ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    }
                 }
             }
-            fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[buf]));
-        }
-        // ---- final: O^T of the last tile, row sums, outputs
-        if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(n_my - 1) & 1]), (uint32_t)((n_my - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
-        alive = __all_sync(0xffffffffu, alive);
-        float lrow[16];
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-            const float2 v = f2_get(lpart[h]);
-            lrow[2 * h] = v.x;
-            lrow[2 * h + 1] = v.y;
-        }
-        const float lsum = warp_sum_16(lrow, lane);
-        named_barrier(2 + part, 128);                      // red may still be read
-        if (lane < 16) ctl.red[quarter][hb + lane] = lsum;
-        if (lane == 0) ctl.warp_alive[warp] = alive ? 1 : 0;
-        named_barrier(1, kSoftmaxThreads);
-        const int hl = hb + (lane & 15);
-        const float l = ctl.red[0][hl] + ctl.red[1][hl] + ctl.red[2][hl] + ctl.red[3][hl];
-        if (lane < 16) ma[lane] = fresh ? 0.f : 1.f / l;
-        __syncwarp();
-        bool all_alive = true;
-#pragma unroll
-        for (int w = 0; w < kSoftmaxWarps; ++w) all_alive = all_alive && ctl.warp_alive[w];
-        if (all_alive) {
-            // thread (quarter, lane) holds output dim 128 c + 32 quarter + lane
-            // of the part's heads
-            tc_fence_after();
-            const int rd = quarter * 32 + lane;
-            const int64_t o = ((int64_t)t * p.H + h0) * D_L;
-            uint16_t *po = p.n_split > 1 ? p.part_o + part_idx * kHeads * D_L : nullptr;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                const int d = c * 128 + rd;
-                uint32_t u[16];
-                tmem_ld16(tmem + lane_addr + kColO + c * kHeads + hb, u);
-                tmem_wait_ld(u);
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int h = hb + q;
-                    const float v = __uint_as_float(u[q]);
-                    if (po) {
-                        po[h * D_L + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-                    } else if (h < nh) {
-                        if (p.out_bf16) static_cast<uint16_t *>(p.out)[o + h * D_L + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v * ma[q]));
-                        else static_cast<float *>(p.out)[o + h * D_L + d] = v * ma[q];
-                    }
-                }
-            }
-            if (quarter == 0 && lane < 16) {
-                const int h = hb + lane;
-                if (po) {
-                    float *ml = p.part_ml + (part_idx * kHeads + h) * 2;
-                    ml[0] = fresh ? -INFINITY : m;
-                    ml[1] = l;
-                } else if (p.lse && h < nh) {
-                    p.lse[(int64_t)t * p.H + h0 + h] = fresh ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-                }
-            }
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.o_empty));
+            named_barrier(1, kSoftmaxThreads);
+            if (tx == 0) mbar_arrive(smem_u32(&ctl.empty[eslot]));
+            ++v;
         }
     }
 
     tc_fence_before();
     __syncwarp();
     __syncthreads();
+    // Dependents launch only now: CTAs of the next grid waiting on this one
+    // would share the SMs and slow it down.
     pdl_trigger();
     tl_end(b.timeline, kTlAttn);
-    if (warp == kMmaWarp) {
+    if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -716,10 +883,10 @@ cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint
     static_assert(1024 + kSlots * kBlockBytes + kQBytes + sizeof(Ctl) <= 232448, "one CTA's shared memory");
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(sparse_attn_q8_kernel), 11, smem);
     if (e != cudaSuccess) return e;
-    if (a.n_split > 65535 || p.groups < 1 || p.groups > 2 || (int64_t)b.T * p.groups > 0x7fffffff)
-        return cudaErrorInvalidConfiguration;
-    return launch_k(sparse_attn_q8_kernel, dim3((unsigned)(b.T * p.groups), (unsigned)a.n_split), dim3(kThreads), smem, stream,
-                    pdl, p);
+    const int64_t units = (int64_t)b.T * p.groups * a.n_split;
+    if (p.groups < 1 || p.groups > 2 || units > 0x7fffffff - kSMs) return cudaErrorInvalidConfiguration;
+    p.units = (int)units;
+    return launch_k(sparse_attn_q8_kernel, dim3((unsigned)std::min<int64_t>(units, kSMs)), dim3(kThreads), smem, stream, pdl, p);
 }
 
 }  // namespace dsa

@@ -90,10 +90,11 @@ def attention(q_lat, q_rope, codes, scale, rows, sm):
       largest value: off by at most max(2^-8 |q|, 2^-10 2^e), 2^e <= top / 224
       (and 2^e >= 2^-40);
       sums of 640 products in 32 bits: under 2^-18 of the sum of magnitudes;
-      a weight w_j 2^E_j is rounded to fp16 (2^-11) and split into two e4m3
-      pieces, in units where the largest lies in [2^3.5, 2^8]: off by at most
-      2^-8 + 2^-11 of itself or half the last piece's step, 2^-10, which is
-      2^-13.5 of the largest;
+      a weight w_j 2^E_j is rounded to fp16 (2^-11) and split into an e4m3
+      piece (off by 2^-4 of it, or 2^-10) and an e5m2 remainder (2^-3 of the
+      remainder, or 2^-17), in units where the largest lies in [2^2, 2^8]: off
+      by at most 2^-7 + 2^-11 of itself or 2^-13 + 2^-17, under 2^-14.9 of the
+      largest;
       partial outputs of splits are bf16 (half step of at most sum w |c|);
       exponentials and their sums in 32 bits: 2^-18."""
     H = q_lat.shape[0]
@@ -118,6 +119,6 @@ def attention(q_lat, q_rope, codes, scale, rows, sm):
     s = np.asarray(scale, np.float64)[rows]
     top = (w * s).max(1, keepdims=True)
     code_sum = np.abs(e4m3_decode(codes[rows])[:, :512]).sum(0)[None, :]
-    d_out = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -18 + 2 * dz) * A + 2.0 ** -13.5 * top * code_sum
+    d_out = (2.0 ** -7 + 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -18 + 2 * dz) * A + 2.0 ** -14.9 * top * code_sum
     d_lse = dz[:, 0] + 2.0 ** -18 * (1 + np.abs(lse))
     return out, lse, d_out, d_lse
