@@ -495,8 +495,9 @@ class Rope:
 
     def desc(self) -> dsa_rope_t:
         import torch
-        _req(self.inv_freq, torch.float64, "inv_freq")
-        return dsa_rope_t(self.inv_freq.data_ptr(), self.rot_dim, bool(self.interleaved), self.scale)
+        f = self.inv_freq
+        _shaped(f, "inv_freq", torch.float64, (f.numel(),), f.get_device())
+        return dsa_rope_t(f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0, self.scale)
 
 
 def dsa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -517,9 +518,11 @@ def _dtypes():
 
 
 _DT = None
+_ANY_FLOAT = (DSA_DT_F32, DSA_DT_F16, DSA_DT_BF16)
+_OUT_FLOAT = (DSA_DT_F32, DSA_DT_BF16)
 
 
-def _dt(t, name, allowed=(DSA_DT_F32, DSA_DT_F16, DSA_DT_BF16)):
+def _dt(t, name, allowed=_ANY_FLOAT):
     global _DT
     if _DT is None:
         _DT = _dtypes()
@@ -529,36 +532,63 @@ def _dt(t, name, allowed=(DSA_DT_F32, DSA_DT_F16, DSA_DT_BF16)):
     return d
 
 
-def _shaped(t, name, dtype, *shape):
-    """A contiguous CUDA tensor of that dtype (None: any) and shape (-1: any extent)."""
-    got = t.shape
-    if not t.is_cuda or (dtype is not None and t.dtype != dtype) or not t.is_contiguous() or len(got) != len(shape) \
-            or any(w not in (-1, g) for w, g in zip(shape, got)):
-        raise TypeError(f"{name}: expected a contiguous CUDA {dtype or 'tensor'} of shape {shape}, "
-                        f"got {t.dtype} {tuple(got)} on {t.device}")
+# The calls below take microseconds on the device, so their checks are kept to
+# a few attribute reads per tensor.
+
+def _shaped(t, name, dtype, shape, dev):
+    """A contiguous tensor of that dtype and shape on device `dev` (a CUDA index)."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on cuda:{max(dev, 0)}, "
+                        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _run(name, tensors, call, stream):
-    """call(stream pointer) with the tensors' device current; they must share one."""
+def _rows(t, name, dtype, shape, dev):
+    """The same for a matrix of contiguous rows any stride apart."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or dev < 0 or t.stride(1) != 1:
+        raise TypeError(f"{name}: expected {dtype} rows {tuple(shape)} on cuda:{max(dev, 0)}, "
+                        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _q8_cache(codes, scale, tail: bool, batch: Batch, dev):
     import torch
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise TypeError(f"{name}: tensors on {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        _check(call(_stream(stream)), name)
-    else:
-        with torch.cuda.device(dev):
-            _check(call(_stream(stream)), name)
+    rows = codes.shape[0]
+    _shaped(codes, "codes", torch.uint8, (rows, Q8_ROW if tail else 512), dev)
+    _shaped(scale, "scale", torch.float32, (rows,), dev)
+    if rows < batch.cache_rows:
+        raise TypeError(f"codes: {rows} rows, the batch names {batch.cache_rows}")
 
 
-def _paging(block_table, block_size: int, batch: Batch):
+def _batch_desc(batch: Batch, dev) -> dsa_batch_t:
+    """Batch.desc with its tensors' device checked as well."""
+    import torch
+    cu, pos, off = batch.cu_q, batch.q_pos, batch.kv_off
+    B, T = cu.numel() - 1, pos.numel()
+    _shaped(cu, "cu_q", torch.int32, (B + 1,), dev)
+    _shaped(pos, "q_pos", torch.int32, (T,), dev)
+    _shaped(off, "kv_off", torch.int64, (B,), dev)
+    return dsa_batch_t(B, T, batch.max_q_per_seq, batch.max_kv, batch.cache_rows, cu.data_ptr(), pos.data_ptr(),
+                       off.data_ptr())
+
+
+def _paging(block_table, block_size: int, batch: Batch, dev):
     """(dsa_paging_t pointer or None) of an optional block table [B, max_blocks]."""
     import torch
     if block_table is None:
         return None
-    _shaped(block_table, "block_table", torch.int32, batch.B, -1)
+    _shaped(block_table, "block_table", torch.int32, (batch.B, block_table.shape[-1]), dev)
     return C.byref(dsa_paging_t(block_table.data_ptr(), block_table.shape[1], block_size))
+
+
+def _call(name, dev, stream, fn, *args):
+    """fn(*args, stream) on device dev; the current stream of dev unless one is given."""
+    import torch
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, fn, *args)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    code = fn(*args, s)
+    if code != DSA_OK:
+        raise DsaError(code, name)
 
 
 def dsa_rope(x, pos, rope: Rope, out, rot_off: int = 0, inverse: bool = False, stream=None):
@@ -567,29 +597,39 @@ def dsa_rope(x, pos, rope: Rope, out, rot_off: int = 0, inverse: bool = False, s
     float16, bfloat16), any token and head strides, contiguous heads; out may
     be x.  pos: int32 [T].  inverse: the gradient's direction."""
     import torch
-    dt = _dt(x, "x")
-    if x.dim() != 3 or out.shape != x.shape or out.dtype != x.dtype or not x.is_cuda or not out.is_cuda \
-            or (x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1)):
+    dt, dev, shape = _dt(x, "x"), x.get_device(), x.shape
+    xs, ys = x.stride(), out.stride()
+    if len(shape) != 3 or out.shape != shape or out.dtype != x.dtype or dev < 0 or out.get_device() != dev \
+            or (shape[2] > 1 and (xs[2] != 1 or ys[2] != 1)):
         raise TypeError(f"x, out: expected CUDA tensors [T, heads, dim] of one shape and dtype with contiguous heads, "
-                        f"got {x.dtype} {tuple(x.shape)} and {out.dtype} {tuple(out.shape)}")
-    T, heads, dim = x.shape
-    _shaped(pos, "pos", torch.int32, T)
+                        f"got {x.dtype} {tuple(shape)} on {x.device} and {out.dtype} {tuple(out.shape)} on {out.device}")
+    T, heads, dim = shape
+    _shaped(pos, "pos", torch.int32, (T,), dev)
     r = rope.desc()
-    _run("dsa_rope", (x, out, pos, rope.inv_freq), lambda s: lib().dsa_rope(
-        x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0), out.stride(1), dt, T, heads, dim,
-        rot_off, pos.data_ptr(), C.byref(r), int(inverse), s), stream)
+    if rope.inv_freq.get_device() != dev:
+        raise TypeError(f"inv_freq: on {rope.inv_freq.device}, x on {x.device}")
+    _call("dsa_rope", dev, stream, lib().dsa_rope, x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1], dt, T,
+          heads, dim, rot_off, pos.data_ptr(), C.byref(r), 1 if inverse else 0)
 
 
-def _new_rows(c_new, r_new, batch: Batch):
-    dt = _dt(c_new, "c_new")
-    for t, name, width in ((c_new, "c_new", 512), (r_new, "r_new", 64)):
-        if t is None:
-            continue
-        if not t.is_cuda or t.dtype != c_new.dtype or t.dim() != 2 or tuple(t.shape) != (batch.T, width) \
-                or t.stride(1) != 1:
-            raise TypeError(f"{name}: expected CUDA rows [{batch.T}, {width}] of {c_new.dtype}, "
-                            f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return dt
+def _append_args(c_new, r_new, batch: Batch, rope, block_table, block_size, dev):
+    """The arguments the two append calls share, up to the cache."""
+    T, dt = batch.q_pos.numel(), _dt(c_new, "c_new")
+    _rows(c_new, "c_new", c_new.dtype, (T, 512), dev)
+    rp, rs = None, 0
+    if r_new is not None:
+        _rows(r_new, "r_new", c_new.dtype, (T, 64), dev)
+        rp, rs = r_new.data_ptr(), r_new.stride(0)
+    if rope is not None and rope.inv_freq.get_device() != dev:
+        raise TypeError(f"inv_freq: on {rope.inv_freq.device}, c_new on {c_new.device}")
+    return (c_new.data_ptr(), c_new.stride(0), rp, rs, dt, C.byref(_batch_desc(batch, dev)),
+            _paging(block_table, block_size, batch, dev), C.byref(rope.desc()) if rope is not None else None)
+
+
+def _workspace_arg(ws, dev):
+    if ws.get_device() != dev:
+        raise TypeError(f"ws: expected on cuda:{dev}, got {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def dsa_kv_append(c_new, r_new, batch: Batch, rope, kv_cache, ws, block_table=None, block_size: int = 0, stream=None):
@@ -597,25 +637,12 @@ def dsa_kv_append(c_new, r_new, batch: Batch, rope, kv_cache, ws, block_table=No
     with r_new None).  c_new [T, 512] and r_new [T, 64] may be column slices;
     the tail is turned at the token's position when rope (a Rope) is given."""
     import torch
-    dt = _new_rows(c_new, r_new, batch)
-    _shaped(kv_cache, "kv_cache", torch.bfloat16, -1, 512 if r_new is None else 576)
-    if kv_cache.shape[0] < batch.cache_rows:
-        raise TypeError(f"kv_cache: {kv_cache.shape[0]} rows, the batch names {batch.cache_rows}")
-    d, pg = batch.desc(), _paging(block_table, block_size, batch)
-    r = C.byref(rope.desc()) if rope is not None else None
-    _run("dsa_kv_append", (c_new, r_new, batch.cu_q, batch.q_pos, batch.kv_off, block_table, kv_cache, ws,
-                           rope.inv_freq if rope is not None else None), lambda s: lib().dsa_kv_append(
-        c_new.data_ptr(), c_new.stride(0), r_new.data_ptr() if r_new is not None else None,
-        r_new.stride(0) if r_new is not None else 0, dt, C.byref(d), pg, r, kv_cache.data_ptr(), ws.data_ptr(),
-        ws.numel(), s), stream)
-
-
-def _q8_cache(codes, scale, tail: bool, batch: Batch):
-    import torch
-    _shaped(codes, "codes", torch.uint8, -1, Q8_ROW if tail else 512)
-    _shaped(scale, "scale", torch.float32, codes.shape[0])
-    if codes.shape[0] < batch.cache_rows:
-        raise TypeError(f"codes: {codes.shape[0]} rows, the batch names {batch.cache_rows}")
+    dev, rows = c_new.get_device(), kv_cache.shape[0]
+    args = _append_args(c_new, r_new, batch, rope, block_table, block_size, dev)
+    _shaped(kv_cache, "kv_cache", torch.bfloat16, (rows, 512 if r_new is None else 576), dev)
+    if rows < batch.cache_rows:
+        raise TypeError(f"kv_cache: {rows} rows, the batch names {batch.cache_rows}")
+    _call("dsa_kv_append", dev, stream, lib().dsa_kv_append, *args, kv_cache.data_ptr(), *_workspace_arg(ws, dev))
 
 
 def q8_cache(rows: int, tail: bool = True, device="cuda"):
@@ -629,32 +656,24 @@ def dsa_kv_append_q8(c_new, r_new, batch: Batch, rope, codes, scale, ws, block_t
                      stream=None):
     """dsa_kv_append into an 8-bit cache: codes uint8 [rows, 640] ([rows, 512]
     with r_new None), scale float32 [rows]."""
-    dt = _new_rows(c_new, r_new, batch)
-    _q8_cache(codes, scale, r_new is not None, batch)
-    d, pg = batch.desc(), _paging(block_table, block_size, batch)
-    r = C.byref(rope.desc()) if rope is not None else None
-    _run("dsa_kv_append_q8", (c_new, r_new, batch.cu_q, batch.q_pos, batch.kv_off, block_table, codes, scale, ws,
-                              rope.inv_freq if rope is not None else None), lambda s: lib().dsa_kv_append_q8(
-        c_new.data_ptr(), c_new.stride(0), r_new.data_ptr() if r_new is not None else None,
-        r_new.stride(0) if r_new is not None else 0, dt, C.byref(d), pg, r, codes.data_ptr(), scale.data_ptr(),
-        ws.data_ptr(), ws.numel(), s), stream)
+    dev = c_new.get_device()
+    args = _append_args(c_new, r_new, batch, rope, block_table, block_size, dev)
+    _q8_cache(codes, scale, r_new is not None, batch, dev)
+    _call("dsa_kv_append_q8", dev, stream, lib().dsa_kv_append_q8, *args, codes.data_ptr(), scale.data_ptr(),
+          *_workspace_arg(ws, dev))
 
 
 def dsa_kv_read_q8(codes, scale, batch: Batch, out, ws, block_table=None, block_size: int = 0, stream=None):
     """The tokens' rows of an 8-bit cache as out [T, 576] ([T, 512] for codes
     of 512), bfloat16 or float32; out may be a column slice of wider rows."""
-    import torch
-    tail = codes.dim() == 2 and codes.shape[1] == Q8_ROW
-    _q8_cache(codes, scale, tail, batch)
-    dt = _dt(out, "out", (DSA_DT_F32, DSA_DT_BF16))
-    width = 576 if tail else 512
-    if not out.is_cuda or out.dim() != 2 or tuple(out.shape) != (batch.T, width) or out.stride(1) != 1:
-        raise TypeError(f"out: expected CUDA rows [{batch.T}, {width}], got {tuple(out.shape)} on {out.device}")
-    stride = out.stride(0) if batch.T > 1 else width
-    d, pg = batch.desc(), _paging(block_table, block_size, batch)
-    _run("dsa_kv_read_q8", (codes, scale, batch.cu_q, batch.q_pos, batch.kv_off, block_table, out, ws),
-         lambda s: lib().dsa_kv_read_q8(codes.data_ptr(), scale.data_ptr(), int(tail), C.byref(d), pg, out.data_ptr(),
-                                        dt, stride, ws.data_ptr(), ws.numel(), s), stream)
+    dev, T = codes.get_device(), batch.q_pos.numel()
+    tail = codes.shape[-1] == Q8_ROW
+    _q8_cache(codes, scale, tail, batch, dev)
+    dt, width = _dt(out, "out", _OUT_FLOAT), 576 if tail else 512
+    _rows(out, "out", out.dtype, (T, width), dev)
+    _call("dsa_kv_read_q8", dev, stream, lib().dsa_kv_read_q8, codes.data_ptr(), scale.data_ptr(), 1 if tail else 0,
+          C.byref(_batch_desc(batch, dev)), _paging(block_table, block_size, batch, dev), out.data_ptr(), dt,
+          out.stride(0) if T > 1 else width, *_workspace_arg(ws, dev))
 
 
 def dsa_sparse_mla_attn_q8(q_lat, q_rope, codes, scale, batch: Batch, idx, sm_scale: float, out, lse, ws,
@@ -662,22 +681,21 @@ def dsa_sparse_mla_attn_q8(q_lat, q_rope, codes, scale, batch: Batch, idx, sm_sc
     """dsa_sparse_mla_attn over an 8-bit cache (q_rope None: codes of 512, no
     tail); out [T, H, 512] float32 or bfloat16, lse [T, H] float32 or None."""
     import torch
-    T, H = batch.T, q_lat.shape[1] if q_lat.dim() == 3 else -1
-    _shaped(q_lat, "q_lat", torch.bfloat16, T, H, 512)
+    dev, T, H = q_lat.get_device(), batch.q_pos.numel(), q_lat.shape[1]
+    _shaped(q_lat, "q_lat", torch.bfloat16, (T, H, 512), dev)
     if q_rope is not None:
-        _shaped(q_rope, "q_rope", torch.bfloat16, T, H, 64)
-    _q8_cache(codes, scale, q_rope is not None, batch)
-    _shaped(idx, "idx", torch.int32, T, -1)
-    dt = _dt(out, "out", (DSA_DT_F32, DSA_DT_BF16))
-    _shaped(out, "out", None, T, H, 512)
+        _shaped(q_rope, "q_rope", torch.bfloat16, (T, H, 64), dev)
+    _q8_cache(codes, scale, q_rope is not None, batch, dev)
+    k = idx.shape[-1]
+    _shaped(idx, "idx", torch.int32, (T, k), dev)
+    dt = _dt(out, "out", _OUT_FLOAT)
+    _shaped(out, "out", out.dtype, (T, H, 512), dev)
     if lse is not None:
-        _shaped(lse, "lse", torch.float32, T, H)
-    d, pg = batch.desc(), _paging(block_table, block_size, batch)
-    _run("dsa_sparse_mla_attn_q8", (q_lat, q_rope, codes, scale, batch.cu_q, batch.q_pos, batch.kv_off, block_table,
-                                    idx, out, lse, ws), lambda s: lib().dsa_sparse_mla_attn_q8(
-        q_lat.data_ptr(), q_rope.data_ptr() if q_rope is not None else None, codes.data_ptr(), scale.data_ptr(),
-        C.byref(d), pg, idx.data_ptr(), idx.shape[1], H, sm_scale, out.data_ptr(), dt,
-        lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.numel(), s), stream)
+        _shaped(lse, "lse", torch.float32, (T, H), dev)
+    _call("dsa_sparse_mla_attn_q8", dev, stream, lib().dsa_sparse_mla_attn_q8, q_lat.data_ptr(),
+          q_rope.data_ptr() if q_rope is not None else None, codes.data_ptr(), scale.data_ptr(),
+          C.byref(_batch_desc(batch, dev)), _paging(block_table, block_size, batch, dev), idx.data_ptr(), k, H, sm_scale,
+          out.data_ptr(), dt, lse.data_ptr() if lse is not None else None, *_workspace_arg(ws, dev))
 
 
 def dsa_set_trace_events(events):

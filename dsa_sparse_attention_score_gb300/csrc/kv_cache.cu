@@ -8,7 +8,10 @@
 // warp per row: lane l holds latent values 16 l .. 16 l + 15, so that its
 // codes are one 16-byte word and the row's largest magnitude is one warp
 // reduction; and tail pair l, so that a lane forms one angle.  Nothing is
-// staged in shared memory.
+// staged in shared memory.  The chain position -> sequence -> block table ->
+// row is three dependent loads long, so with many tokens a warp takes four at
+// a time, their lookups side by side in four lanes and their rows in flight
+// together.
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 #include "quant8.cuh"
@@ -55,14 +58,26 @@ struct AppendParams {
     float *scale;
 };
 
-// Cache row of token t, -1 (flagged by lane 0) when it is out of bounds.
-__device__ __forceinline__ int64_t token_row(const DevBatch &b, int t, int lane, int32_t *pos_out, uint32_t *status) {
-    const int32_t pos = __ldg(b.q_pos + t);
-    const int seq = seq_of_warp(b.cu_q, b.B, t, lane);
-    const int64_t kv0 = seq_base(b, seq);
-    int64_t row = (pos >= 0 && pos < b.max_kv && kv0 >= 0) ? cache_row(b, seq, kv0, pos) : -1;
-    if (row >= b.cache_rows) row = -1;
-    if (row < 0 && lane == 0) flag(status, DSA_DEV_BAD_POSITION);
+// Cache rows of tokens t0 .. t0 + R - 1: lane i < R gets token t0 + i's position
+// and row, -1 past the last token (not flagged) or out of bounds (flagged).
+template <int R>
+__device__ __forceinline__ int64_t token_rows(const DevBatch &b, int t0, int lane, int32_t *pos_out, uint32_t *status) {
+    const int t = t0 + lane;
+    const bool mine = lane < R && t < b.T;
+    const int32_t pos = mine ? __ldg(b.q_pos + t) : -1;
+    int seq = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int s = seq_of_warp(b.cu_q, b.B, min(t0 + i, b.T - 1), lane);
+        seq = lane == i ? s : seq;
+    }
+    int64_t row = -1;
+    if (mine) {
+        const int64_t kv0 = seq_base(b, seq);
+        if (pos >= 0 && pos < b.max_kv && kv0 >= 0) row = cache_row(b, seq, kv0, pos);
+        if (row >= b.cache_rows) row = -1;
+        if (row < 0) flag(status, DSA_DEV_BAD_POSITION);
+    }
     *pos_out = pos;
     return row;
 }
@@ -74,26 +89,14 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
 
 }  // namespace
 
-template <typename T, bool kQ8>
-__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendParams p, const DevBatch b, uint32_t *status) {
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= b.T) return;
-    float v[16];
-    load16(static_cast<const T *>(p.c_new) + (int64_t)t * p.c_stride + lane * 16, p.vec, v);
+// The row of one token, held by the warp: its latent values v and tail pair.
+template <bool kQ8>
+__device__ __forceinline__ void store_row(const AppendParams &p, const float (&v)[16], float ra, float rb, int32_t pos,
+                                          int64_t row, int lane) {
     const bool tail = p.r_new != nullptr;
     // tail pair of this lane: values i0 and i1 of the 64
     const bool inter = p.rope.interleaved;
     const int i0 = inter ? 2 * lane : lane, i1 = inter ? 2 * lane + 1 : lane + 32;
-    float ra = 0.f, rb = 0.f;
-    if (tail) {
-        const T *r = static_cast<const T *>(p.r_new) + (int64_t)t * p.r_stride;
-        ra = as_f(r[i0]);
-        rb = as_f(r[i1]);
-    }
-    int32_t pos;
-    const int64_t row = token_row(b, t, lane, &pos, status);
-    if (row < 0) return;
     if (tail && p.rotate) {
         const float2 w = rope_cos_sin(pos, __ldg(p.rope.inv_freq + lane), p.rope.scale, p.rope.inverse);
         const float x = ra * w.x - rb * w.y;
@@ -151,6 +154,34 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendPara
     if (lane == 0) p.scale[row] = finite ? exp2_int(e) : __int_as_float(0x7FC00000);
 }
 
+template <typename T, bool kQ8, int R>
+__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendParams p, const DevBatch b, uint32_t *status) {
+    const int lane = threadIdx.x & 31;
+    const int t0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * R;
+    if (t0 >= b.T) return;
+    float v[R][16], ra[R], rb[R];
+    const int i0 = p.rope.interleaved ? 2 * lane : lane, i1 = p.rope.interleaved ? 2 * lane + 1 : lane + 32;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t t = min(t0 + i, b.T - 1);
+        load16(static_cast<const T *>(p.c_new) + t * p.c_stride + lane * 16, p.vec, v[i]);
+        ra[i] = rb[i] = 0.f;
+        if (p.r_new) {
+            const T *r = static_cast<const T *>(p.r_new) + t * p.r_stride;
+            ra[i] = as_f(r[i0]);
+            rb[i] = as_f(r[i1]);
+        }
+    }
+    int32_t pos;
+    const int64_t row = token_rows<R>(b, t0, lane, &pos, status);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t row_i = __shfl_sync(0xffffffffu, row, i);
+        const int32_t pos_i = __shfl_sync(0xffffffffu, pos, i);
+        if (row_i >= 0) store_row<kQ8>(p, v[i], ra[i], rb[i], pos_i, row_i, lane);
+    }
+}
+
 struct ReadParams {
     const uint8_t *codes;
     const float *scale;
@@ -160,78 +191,106 @@ struct ReadParams {
     int vec;                            // output rows are 16-byte aligned
 };
 
-// One warp per row.  A code times a power of two is exact in bf16, so only
-// the tail's sum rounds.  A token out of bounds gets a row of zeros.
-template <bool kBf16>
+// A code times a power of two is exact in bf16, so only the tail's sum rounds.
+// A token out of bounds gets a row of zeros.
+template <bool kBf16, int R>
 __global__ void __launch_bounds__(32 * kWarps) kv_read_kernel(const ReadParams p, const DevBatch b, uint32_t *status) {
     const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= b.T) return;
+    const int t0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * R;
+    if (t0 >= b.T) return;
     int32_t pos;
-    const int64_t row = token_row(b, t, lane, &pos, status);
-    uint4 c = make_uint4(0u, 0u, 0u, 0u);
-    uint32_t hi = 0, lo = 0;
-    float s = 0.f;
-    if (row >= 0) {
-        const uint8_t *src = p.codes + row * (p.tail ? kQ8Row : D_L);
-        c = __ldg(reinterpret_cast<const uint4 *>(src) + lane);
-        if (p.tail) {
-            hi = __ldg(reinterpret_cast<const uint16_t *>(src + D_L) + lane);
-            lo = __ldg(reinterpret_cast<const uint16_t *>(src + D_L + D_R) + lane);
+    const int64_t row = token_rows<R>(b, t0, lane, &pos, status);
+    uint4 c[R];
+    uint32_t hi[R], lo[R];
+    float s[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t row_i = __shfl_sync(0xffffffffu, row, i);
+        c[i] = make_uint4(0u, 0u, 0u, 0u);
+        hi[i] = lo[i] = 0;
+        s[i] = 0.f;
+        if (row_i >= 0) {
+            const uint8_t *src = p.codes + row_i * (p.tail ? kQ8Row : D_L);
+            c[i] = __ldg(reinterpret_cast<const uint4 *>(src) + lane);
+            if (p.tail) {
+                hi[i] = __ldg(reinterpret_cast<const uint16_t *>(src + D_L) + lane);
+                lo[i] = __ldg(reinterpret_cast<const uint16_t *>(src + D_L + D_R) + lane);
+            }
+            s[i] = __ldg(p.scale + row_i);
         }
-        s = __ldg(p.scale + row);
     }
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    float v[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = e4m3x2_to_float2(w[i] & 0xFFFFu), d = e4m3x2_to_float2(w[i] >> 16);
-        v[4 * i] = a.x * s; v[4 * i + 1] = a.y * s; v[4 * i + 2] = d.x * s; v[4 * i + 3] = d.y * s;
-    }
-    const float2 h = e4m3x2_to_float2(hi), l = e4m3x2_to_float2(lo);
-    const float ta = (h.x + l.x) * s, tb = (h.y + l.y) * s;
-    if (kBf16) {
-        uint16_t *dst = static_cast<uint16_t *>(p.out) + (int64_t)t * p.stride;
-        uint4 o[2];
-        uint32_t *u = reinterpret_cast<uint32_t *>(o);
+    for (int i = 0; i < R; ++i) {
+        if (t0 + i >= b.T) break;
+        const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = bf16x2(v[2 * i], v[2 * i + 1]);
-        if (p.vec) {
-            reinterpret_cast<uint4 *>(dst)[2 * lane] = o[0];
-            reinterpret_cast<uint4 *>(dst)[2 * lane + 1] = o[1];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dst[16 * lane + i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
+        for (int j = 0; j < 4; ++j) {
+            const float2 x = e4m3x2_to_float2(w[j] & 0xFFFFu), y = e4m3x2_to_float2(w[j] >> 16);
+            v[4 * j] = x.x * s[i]; v[4 * j + 1] = x.y * s[i]; v[4 * j + 2] = y.x * s[i]; v[4 * j + 3] = y.y * s[i];
         }
-        if (p.tail) {
+        const float2 h = e4m3x2_to_float2(hi[i]), l = e4m3x2_to_float2(lo[i]);
+        const float ta = (h.x + l.x) * s[i], tb = (h.y + l.y) * s[i];
+        if (kBf16) {
+            uint16_t *dst = static_cast<uint16_t *>(p.out) + (int64_t)(t0 + i) * p.stride;
+            uint32_t u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = bf16x2(v[2 * j], v[2 * j + 1]);
             const uint32_t o2 = bf16x2(ta, tb);
-            dst[D_L + 2 * lane] = (uint16_t)o2;
-            dst[D_L + 2 * lane + 1] = (uint16_t)(o2 >> 16);
-        }
-    } else {
-        float *dst = static_cast<float *>(p.out) + (int64_t)t * p.stride;
-        if (p.vec) {
+            if (p.vec) {
+                reinterpret_cast<uint4 *>(dst)[2 * lane] = make_uint4(u[0], u[1], u[2], u[3]);
+                reinterpret_cast<uint4 *>(dst)[2 * lane + 1] = make_uint4(u[4], u[5], u[6], u[7]);
+                if (p.tail) reinterpret_cast<uint32_t *>(dst + D_L)[lane] = o2;
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<float4 *>(dst)[4 * lane + i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                for (int j = 0; j < 16; ++j) dst[16 * lane + j] = (uint16_t)(u[j >> 1] >> (16 * (j & 1)));
+                if (p.tail) {
+                    dst[D_L + 2 * lane] = (uint16_t)o2;
+                    dst[D_L + 2 * lane + 1] = (uint16_t)(o2 >> 16);
+                }
+            }
         } else {
+            float *dst = static_cast<float *>(p.out) + (int64_t)(t0 + i) * p.stride;
+            if (p.vec) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dst[16 * lane + i] = v[i];
-        }
-        if (p.tail) {
-            dst[D_L + 2 * lane] = ta;
-            dst[D_L + 2 * lane + 1] = tb;
+                for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<float4 *>(dst)[4 * lane + j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) dst[16 * lane + j] = v[j];
+            }
+            if (p.tail) {
+                dst[D_L + 2 * lane] = ta;
+                dst[D_L + 2 * lane + 1] = tb;
+            }
         }
     }
 }
 
 namespace {
 
+// Four tokens per warp once there are enough to give every SM several warps;
+// one below that, where the latency of a single row counts.
+constexpr int kBatchTokens = 2;
+inline bool batched(const DevBatch &b) { return b.T >= 16 * kSMs * kBatchTokens; }
+inline unsigned grid_of(const DevBatch &b, int per_warp) {
+    return (unsigned)(((int64_t)b.T + kWarps * per_warp - 1) / (kWarps * per_warp));
+}
+
+template <typename T, bool kQ8>
+cudaError_t launch_append_as(const AppendParams &p, const DevBatch &b, uint32_t *status, cudaStream_t stream) {
+    if (batched(b)) kv_append_kernel<T, kQ8, kBatchTokens><<<grid_of(b, kBatchTokens), 32 * kWarps, 0, stream>>>(p, b, status);
+    else kv_append_kernel<T, kQ8, 1><<<grid_of(b, 1), 32 * kWarps, 0, stream>>>(p, b, status);
+    return cudaGetLastError();
+}
 template <typename T>
 cudaError_t launch_append_t(const AppendParams &p, const DevBatch &b, uint32_t *status, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(((int64_t)b.T + kWarps - 1) / kWarps);
-    if (p.kv) kv_append_kernel<T, false><<<grid, 32 * kWarps, 0, stream>>>(p, b, status);
-    else kv_append_kernel<T, true><<<grid, 32 * kWarps, 0, stream>>>(p, b, status);
+    return p.kv ? launch_append_as<T, false>(p, b, status, stream) : launch_append_as<T, true>(p, b, status, stream);
+}
+template <bool kBf16>
+cudaError_t launch_read_as(const ReadParams &p, const DevBatch &b, uint32_t *status, cudaStream_t stream) {
+    if (batched(b)) kv_read_kernel<kBf16, kBatchTokens><<<grid_of(b, kBatchTokens), 32 * kWarps, 0, stream>>>(p, b, status);
+    else kv_read_kernel<kBf16, 1><<<grid_of(b, 1), 32 * kWarps, 0, stream>>>(p, b, status);
     return cudaGetLastError();
 }
 
@@ -262,10 +321,7 @@ cudaError_t launch_kv_read(const uint8_t *codes, const float *scale, int tail, v
     const int64_t size = out_dtype == DSA_DT_F32 ? 4 : 2;
     ReadParams p{codes, scale, tail, out, stride,
                  ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(stride * size)) & 15) == 0};
-    const unsigned grid = (unsigned)(((int64_t)b.T + kWarps - 1) / kWarps);
-    if (out_dtype == DSA_DT_F32) kv_read_kernel<false><<<grid, 32 * kWarps, 0, stream>>>(p, b, status);
-    else kv_read_kernel<true><<<grid, 32 * kWarps, 0, stream>>>(p, b, status);
-    return cudaGetLastError();
+    return out_dtype == DSA_DT_F32 ? launch_read_as<false>(p, b, status, stream) : launch_read_as<true>(p, b, status, stream);
 }
 
 }  // namespace dsa

@@ -7,11 +7,13 @@
 // same with the angle negated.
 //
 // One pass over memory and three flops a value: bound by HBM, or by launch
-// latency for a few tokens.  A CTA takes one token and up to 256 * kUnits
-// 16-byte units of its heads; the units are loaded before the angles are
-// formed (rot_dim / 2 of them, once per CTA, in 64 bits), so that the trig
-// hides behind the loads.  Rows whose addresses or extents are not multiples of 16
-// bytes take the same kernel with units of one value.
+// latency for a few tokens.  A CTA takes one token; a thread takes the same
+// unit of 16 bytes of kUnits heads, so that its place in a head and its angles
+// are found once, and its loads are out before the angles are formed (rot_dim
+// / 2 of them, once per CTA).  Rows whose addresses or extents are not
+// multiples of 16 bytes take the same kernel with units of one value.
+#include <algorithm>
+
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 #include "rope.cuh"
@@ -21,7 +23,7 @@ namespace dsa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kUnits = 4;              // units in flight per thread
+constexpr int kUnits = 4;              // heads per thread
 constexpr int kMaxPairs = 256;         // rot_dim <= 512
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
@@ -43,91 +45,93 @@ struct RopeParams {
     DevRope r;
     int heads, dim, off;       // values per head; first rotated one
     int copy;                  // write the values that do not turn
+    int per_head, lanes;       // units of a head; those a CTA takes of each head
+    int rows;                  // heads a CTA takes at a time
 };
 
 }  // namespace
 
 // V values per unit.  Interleaved: a unit is V neighbouring values, pairs
 // inside it (V = 1 stands for one pair, or one copied value).  Halves: a unit
-// is V values of the first half and their V partners.
+// is V values of the first half and their V partners.  grid: token, block of
+// heads, block of a head's units.
 template <typename T, bool kInter, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
     __shared__ float2 cs[kMaxPairs];
     using VT = Vec<T, V>;
     constexpr int S = kInter && V == 1 ? 2 : V;          // values a rotated unit spans (per part)
     constexpr int kParts = (!kInter || V == 1) ? 2 : 1;  // loads of a rotated unit
+    constexpr int kPairs = V > 1 && kInter ? V / 2 : V;  // angles of a rotated unit
     const int t = blockIdx.x, tid = threadIdx.x;
     const int half = p.r.rot_dim >> 1;
     const int rot_units = (kInter ? p.r.rot_dim : half) / S;
-    const int copy_units = p.copy ? (p.dim - p.r.rot_dim) / V : 0;
-    const int per_head = rot_units + copy_units;
-    const int total = p.heads * per_head;
-    const int first = blockIdx.y * (kRopeThreads * kUnits) + tid;
-    const T *x = static_cast<const T *>(p.x) + (int64_t)t * p.xt;
-    T *y = static_cast<T *>(p.y) + (int64_t)t * p.yt;
+    const int row = tid / p.lanes, r = blockIdx.z * p.lanes + tid - row * p.lanes;
+    const int h0 = blockIdx.y * (p.rows * kUnits) + row;
+    const bool live = row < p.rows && r < p.per_head, turns = r < rot_units;
+    const int c = (r - rot_units) * V;                   // a copied unit's place among the copied values
+    const int v = turns ? p.off + r * S : c < p.off ? c : c + p.r.rot_dim;
+    const int partner = kInter ? 1 : half;
+    const T *x = static_cast<const T *>(p.x) + (int64_t)t * p.xt + v;
+    T *y = static_cast<T *>(p.y) + (int64_t)t * p.yt + v;
     VT a[kUnits], b[kUnits];
-    int head[kUnits], at[kUnits], part2[kUnits], pair[kUnits];   // pair < 0: copied
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-        const int i = first + u * kRopeThreads;
-        head[u] = -1;
-        if (i >= total) continue;
-        const int h = i / per_head, r = i - h * per_head;
-        head[u] = h;
-        if (r < rot_units) {
-            at[u] = p.off + r * S;
-            part2[u] = at[u] + (kInter ? 1 : half);
-            pair[u] = kInter ? r * S / 2 : r * S;
-        } else {
-            const int c = (r - rot_units) * V;
-            at[u] = c < p.off ? c : c + p.r.rot_dim;
-            pair[u] = -1;
+        const int h = h0 + u * p.rows;
+        if (live && h < p.heads) {
+            a[u] = *reinterpret_cast<const VT *>(x + (int64_t)h * p.xh);
+            if (kParts == 2 && turns) b[u] = *reinterpret_cast<const VT *>(x + (int64_t)h * p.xh + partner);
         }
-        const T *src = x + (int64_t)h * p.xh;
-        a[u] = *reinterpret_cast<const VT *>(src + at[u]);
-        if (kParts == 2 && pair[u] >= 0) b[u] = *reinterpret_cast<const VT *>(src + part2[u]);
     }
     const int32_t pos = __ldg(p.pos + t);
-    for (int j = tid; j < half; j += kRopeThreads) cs[j] = rope_cos_sin(pos, __ldg(p.r.inv_freq + j), p.r.scale, p.r.inverse);
+    for (int j = tid; j < half; j += blockDim.x) cs[j] = rope_cos_sin(pos, __ldg(p.r.inv_freq + j), p.r.scale, p.r.inverse);
     __syncthreads();
+    if (!live) return;
+    float2 w[kPairs];
+    if (turns) {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) w[e] = cs[r * kPairs + e];
+    }
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-        if (head[u] < 0) continue;
-        T *dst = y + (int64_t)head[u] * p.yh;
-        if (pair[u] >= 0) {
+        const int h = h0 + u * p.rows;
+        if (h >= p.heads) break;
+        T *dst = y + (int64_t)h * p.yh;
+        if (turns) {
             if (kParts == 1) {
 #pragma unroll
                 for (int e = 0; e + 1 < V; e += 2) {
-                    const float2 w = cs[pair[u] + e / 2];
+                    const float2 f = w[e / 2];
                     const float va = to_f(a[u].v[e]), vb = to_f(a[u].v[e + 1]);
-                    a[u].v[e] = from_f<T>(va * w.x - vb * w.y);
-                    a[u].v[e + 1] = from_f<T>(va * w.y + vb * w.x);
+                    a[u].v[e] = from_f<T>(va * f.x - vb * f.y);
+                    a[u].v[e + 1] = from_f<T>(va * f.y + vb * f.x);
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float2 w = cs[pair[u] + e];
+                    const float2 f = w[e];
                     const float va = to_f(a[u].v[e]), vb = to_f(b[u].v[e]);
-                    a[u].v[e] = from_f<T>(va * w.x - vb * w.y);
-                    b[u].v[e] = from_f<T>(va * w.y + vb * w.x);
+                    a[u].v[e] = from_f<T>(va * f.x - vb * f.y);
+                    b[u].v[e] = from_f<T>(va * f.y + vb * f.x);
                 }
-                *reinterpret_cast<VT *>(dst + part2[u]) = b[u];
+                *reinterpret_cast<VT *>(dst + partner) = b[u];
             }
         }
-        *reinterpret_cast<VT *>(dst + at[u]) = a[u];
+        *reinterpret_cast<VT *>(dst) = a[u];
     }
 }
 
 namespace {
 
 template <typename T, bool kInter, int V>
-cudaError_t launch_rope_as(const RopeParams &p, int n_tokens, cudaStream_t stream) {
-    const int units = (kInter && V > 1 ? p.r.rot_dim / V : p.r.rot_dim / 2 / V) + (p.copy ? (p.dim - p.r.rot_dim) / V : 0);
-    const int64_t total = (int64_t)units * p.heads;
-    const int64_t ny = (total + kRopeThreads * kUnits - 1) / (kRopeThreads * kUnits);
-    if (ny > 65535) return cudaErrorInvalidConfiguration;
-    if (ny == 0) return cudaSuccess;
-    rope_kernel<T, kInter, V><<<dim3((unsigned)n_tokens, (unsigned)ny), kRopeThreads, 0, stream>>>(p);
+cudaError_t launch_rope_as(RopeParams p, int n_tokens, cudaStream_t stream) {
+    p.per_head = (kInter && V > 1 ? p.r.rot_dim / V : p.r.rot_dim / 2 / V) + (p.copy ? (p.dim - p.r.rot_dim) / V : 0);
+    p.lanes = std::min(p.per_head, kRopeThreads);
+    // as many heads at a time as threads allow, fewer when the token is short
+    p.rows = std::max(1, std::min(kRopeThreads / p.lanes, (p.heads + kUnits - 1) / kUnits));
+    const int threads = (p.rows * p.lanes + 31) / 32 * 32;
+    const int ny = (p.heads + p.rows * kUnits - 1) / (p.rows * kUnits), nz = (p.per_head + p.lanes - 1) / p.lanes;
+    if (ny > 65535 || nz > 65535) return cudaErrorInvalidConfiguration;
+    rope_kernel<T, kInter, V><<<dim3((unsigned)n_tokens, (unsigned)ny, (unsigned)nz), threads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -13,14 +13,33 @@ struct DevRope {
     int inverse;              // turn by -angle
 };
 
-// scale * (cos, sin) of pos * inv_freq.  The angle is formed and reduced to a
-// fraction of a turn in 64 bits -- at position 10^6 a 32-bit product would be
-// off by 0.03 radians -- and the fraction, below 1/2, rounded once to 32.
+// scale * (cos, sin) of pos * inv_freq.
+//
+// A 32-bit angle would be off by 0.03 radians at position 10^6, and 64-bit
+// floating point runs at a sixteenth of a lane per cycle and SM partition here
+// (one row per warp spent more time on its angle than on its bytes), so the
+// angle is formed in integers, as a fraction of a turn in units of 2^-64:
+//     inv_freq = m 2^(e - 1075), m of 53 bits
+//     F        = frac(inv_freq / 2 pi) 2^64 = m C 2^(e - 1075) mod 2^64,  C = 2^64 / 2 pi
+//     turn     = pos F mod 2^64.
+// Whole turns drop out by wrapping.  F is off by at most 2 units (and C's
+// truncation, 2^-62 of it), so a turn by 2^-31 at the largest position; the
+// fraction, in [-1/2, 1/2), is rounded once to 32 bits.  Frequencies from 2^-60 on,
+// either sign.
 __device__ __forceinline__ float2 rope_cos_sin(int32_t pos, double inv_freq, float scale, int inverse) {
-    double turns = (double)pos * inv_freq * 0.15915494309189533576888;   // 1 / (2 pi)
-    turns -= rint(turns);
+    const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
+    const int shift = 1075 - (int)((bits >> 52) & 0x7FF);
+    const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
+    constexpr uint64_t C = 0x28BE60DB9391054Aull;             // floor(2^64 / (2 pi))
+    const uint64_t lo = m * C, hi = __umul64hi(m, C);
+    uint64_t F = 0;
+    if (shift <= 0) F = shift > -64 ? lo << -shift : 0;
+    else if (shift < 64) F = (lo >> shift) | (hi << (64 - shift));
+    else if (shift < 128) F = hi >> (shift - 64);
+    if (bits >> 63) F = ~F + 1;
+    const uint64_t turn = F * (uint64_t)(int64_t)pos;
     float s, c;
-    sincospif(2.f * (float)turns, &s, &c);
+    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
     return make_float2(c * scale, inverse ? -s * scale : s * scale);
 }
 

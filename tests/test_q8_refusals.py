@@ -168,25 +168,28 @@ def test_binding_checks_shapes_before_the_call():
     import torch
 
     class Fake:                                # stands in for a CUDA tensor; no GPU needed
-        is_cuda, device = True, "cuda:0"
+        device = "cuda:0"
 
         def __init__(self, dtype, *shape):
-            self.dtype, self.shape = dtype, shape
+            self.dtype, self.shape = dtype, torch.Size(shape)
+
+        def get_device(self):
+            return 0
 
         def is_contiguous(self):
             return True
 
-        def dim(self):
-            return len(self.shape)
+        def numel(self):
+            return self.shape.numel()
 
-        def stride(self, i):
-            n = 1
-            for s in self.shape[i + 1:]:
-                n *= s
-            return n
+        def data_ptr(self):
+            return 0x1000
 
-    b = dsa.Batch(None, Fake(torch.int32, 3), None, 1, 100, 200)
-    b.__class__ = type("B", (dsa.Batch,), {"T": 3, "B": 3})
+        def stride(self, i=None):
+            st = [self.shape[j + 1:].numel() for j in range(len(self.shape))]
+            return st if i is None else st[i]
+
+    b = dsa.Batch(Fake(torch.int32, 4), Fake(torch.int32, 3), Fake(torch.int64, 3), 1, 100, 200)
     bf, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
     codes, scale = Fake(u8, 200, 640), Fake(f32, 200)
     with pytest.raises(TypeError, match="codes"):          # a cache of rows without a tail, and a tail
@@ -211,6 +214,11 @@ def test_binding_checks_shapes_before_the_call():
     with pytest.raises(TypeError, match="codes"):
         dsa.dsa_sparse_mla_attn_q8(Fake(bf, 3, 8, 512), None, codes, scale, b, Fake(torch.int32, 3, 4), 1.0,
                                    Fake(bf, 3, 8, 512), None, None)
+    with pytest.raises(TypeError, match="kv_off"):
+        wrong = dsa.Batch(b.cu_q, b.q_pos, Fake(torch.int32, 3), 1, 100, 200)
+        dsa.dsa_kv_read_q8(codes, scale, wrong, Fake(bf, 3, 576), None)
+    with pytest.raises(TypeError, match="block_table"):
+        dsa.dsa_kv_read_q8(codes, scale, b, Fake(bf, 3, 576), None, Fake(torch.int32, 2, 4), 64)
     with pytest.raises(TypeError, match="x, out"):
         dsa.dsa_rope(Fake(bf, 3, 8, 64), Fake(torch.int32, 3), None, Fake(f32, 3, 8, 64))
     with pytest.raises(TypeError, match="pos"):
