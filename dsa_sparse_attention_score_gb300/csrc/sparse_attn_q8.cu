@@ -785,43 +785,60 @@ uint32_t a16[2][16], b16[2][16];
                 // the tile's P^T slot per warp, head pairs side by side, and leave
                 // as 16 bytes (eight dims) per lane; float32 ones go straight out.
                 tc_fence_after();
-                const bool half = p.n_split > 1 || p.out_bf16;
-                uint16_t *dst = p.n_split > 1 ? p.part_o + part0 * D_L : static_cast<uint16_t *>(p.out) + row0 * D_L;
-                const int live = p.n_split > 1 ? kHeads : w.nh;
-                uint32_t *stage = reinterpret_cast<uint32_t *>(ring + eslot * kBlockBytes + sw * 2048);
-#pragma unroll 1
-                for (int c = 0; c < 8; ++c) {              // 4 dim blocks x 2 groups of 16 heads
-                    const int d = (c >> 1) * 128 + quarter * 32, hq = (c & 1) * 16;
-                    uint32_t *st = stage + (c & 1) * 256;
-                    const float *il = ma + hq;
-                    uint32_t c16[16];
-                    tmem_ld16(tmem + lane_addr + kColO + (c >> 1) * kHeads + hb + hq, c16);
-                    tmem_wait_ld(c16);
-                    if (half) {
-                        __syncwarp();                      // st was read two turns ago
+                const int live = (p.n_split > 1 ? kHeads : w.nh) - hb;     // heads of the part that are stored
+                const uint32_t o_t = tmem + lane_addr + kColO + hb;
+                // (the factors in registers first: between shared stores their
+                // loads would wait for one another)
+                float f[kPartHeads];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 f = *reinterpret_cast<const float2 *>(il + 2 * i);
-                            const __nv_bfloat162 o2 = __floats2bfloat162_rn(__uint_as_float(c16[2 * i]) * f.x, __uint_as_float(c16[2 * i + 1]) * f.y);
+                for (int h = 0; h < kPartHeads; h += 4) {
+                    const float4 f4 = *reinterpret_cast<const float4 *>(ma + h);
+                    f[h] = f4.x; f[h + 1] = f4.y; f[h + 2] = f4.z; f[h + 3] = f4.w;
+                }
+                if (p.n_split > 1 || p.out_bf16) {
+                    uint16_t *dst = (p.n_split > 1 ? p.part_o + part0 * D_L : static_cast<uint16_t *>(p.out) + row0 * D_L) +
+                                    (int64_t)hb * D_L + quarter * 32;
+                    uint32_t *st = reinterpret_cast<uint32_t *>(ring + eslot * kBlockBytes + sw * 2048);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t c32[32];
+                        tmem_ld32(o_t + c * kHeads, c32);
+                        tmem_wait_ld(c32);
+                        __syncwarp();                      // the block before has been read
+#pragma unroll
+                        for (int i = 0; i < kPartHeads / 2; ++i) {
+                            const __nv_bfloat162 o2 =
+                                __floats2bfloat162_rn(__uint_as_float(c32[2 * i]) * f[2 * i], __uint_as_float(c32[2 * i + 1]) * f[2 * i + 1]);
                             st[32 * i + lane] = *reinterpret_cast<const uint32_t *>(&o2);
                         }
                         __syncwarp();
-                        // lane: heads 2 i and 2 i + 1 with i = lane / 4, dims 8 (lane % 4) ..
-                        const uint4 e0 = *reinterpret_cast<const uint4 *>(st + 8 * lane), e1 = *reinterpret_cast<const uint4 *>(st + 8 * lane + 4);
-                        const int h = hb + hq + 2 * (lane >> 2), dd = d + 8 * (lane & 3);
-                        if (h < live)
-                            *reinterpret_cast<uint4 *>(dst + (int64_t)h * D_L + dd) =
-                                make_uint4(__byte_perm(e0.x, e0.y, 0x5410), __byte_perm(e0.z, e0.w, 0x5410),
-                                           __byte_perm(e1.x, e1.y, 0x5410), __byte_perm(e1.z, e1.w, 0x5410));
-                        if (h + 1 < live)
-                            *reinterpret_cast<uint4 *>(dst + (int64_t)(h + 1) * D_L + dd) =
-                                make_uint4(__byte_perm(e0.x, e0.y, 0x7632), __byte_perm(e0.z, e0.w, 0x7632),
-                                           __byte_perm(e1.x, e1.y, 0x7632), __byte_perm(e1.z, e1.w, 0x7632));
-                    } else {
-                        float *of = static_cast<float *>(p.out) + row0 * D_L + d + lane;
+                        // lane: heads 2 i and 2 i + 1 with i = lane / 4 (+ 8), dims 8 (lane % 4) ..
+                        uint4 e[4];
 #pragma unroll
-                        for (int h = 0; h < 16; ++h)
-                            if (hb + hq + h < live) of[(int64_t)(hb + hq + h) * D_L] = __uint_as_float(c16[h]) * il[h];
+                        for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const uint4 *>(st + (i >> 1) * 256 + 8 * lane + 4 * (i & 1));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 e0 = e[2 * i], e1 = e[2 * i + 1];
+                            const int h = 16 * i + 2 * (lane >> 2);
+                            uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)h * D_L + c * 128 + 8 * (lane & 3));
+                            if (h < live)
+                                to[0] = make_uint4(__byte_perm(e0.x, e0.y, 0x5410), __byte_perm(e0.z, e0.w, 0x5410),
+                                                   __byte_perm(e1.x, e1.y, 0x5410), __byte_perm(e1.z, e1.w, 0x5410));
+                            if (h + 1 < live)
+                                to[D_L / 8] = make_uint4(__byte_perm(e0.x, e0.y, 0x7632), __byte_perm(e0.z, e0.w, 0x7632),
+                                                         __byte_perm(e1.x, e1.y, 0x7632), __byte_perm(e1.z, e1.w, 0x7632));
+                        }
+                    }
+                } else {
+                    float *of = static_cast<float *>(p.out) + (row0 + hb) * D_L + quarter * 32 + lane;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t c32[32];
+                        tmem_ld32(o_t + c * kHeads, c32);
+                        tmem_wait_ld(c32);
+#pragma unroll
+                        for (int h = 0; h < kPartHeads; ++h)
+                            if (h < live) of[(int64_t)h * D_L + c * 128] = __uint_as_float(c32[h]) * f[h];
                     }
                 }
                 if (quarter == 0) {
