@@ -39,8 +39,8 @@
 // the tile before has freed its slot.  One producer warp per latent block
 // gathers it with 16-byte cp.async copies (a row's 128 bytes are one cache
 // line; masked rows are filled with zeros and read nothing); four more hold
-// the tail block in registers until its slot is free.  The MMA thread issues score blocks and value
-// products as their inputs arrive; eight softmax warps (two per TMEM lane
+// the tail block in registers until its slot is free.  Two warps issue the
+// score and the value products as their inputs arrive; eight softmax warps (two per TMEM lane
 // quarter, 32 heads each) turn a tile's S^T into P^T.  The reference M of a
 // head's weights is set 2^2 below its first tile's maximum and moves only
 // when a weight would exceed 2^8, so most tiles need no maxima, only the
@@ -69,10 +69,11 @@ constexpr int kParts = 2;                     // groups of 32 heads
 constexpr int kPartHeads = kHeads / kParts;
 constexpr int kSoftmaxWarps = 4 * kParts;     // one per (TMEM lane quarter, part)
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-// Warp 0 issues the MMAs, warps 1..3 gather latent blocks in turn, 4..11 do
-// the softmax, 12..15 hold 32 rows of the tail block each.
-constexpr int kLatentWarps = 3;
-constexpr int kFirstSoftmax = 1 + kLatentWarps;       // a multiple of 4: warp mod 4 is the lane quarter
+// Warp 0 issues the score products, warp 1 the value products, warps 2 and 3
+// gather latent blocks in turn, 4..11 do the softmax, 12..15 hold 32 rows of
+// the tail block each.
+constexpr int kLatentWarps = 2;
+constexpr int kFirstSoftmax = 2 + kLatentWarps;       // a multiple of 4: warp mod 4 is the lane quarter
 constexpr int kFirstTail = kFirstSoftmax + kSoftmaxWarps;
 constexpr int kTailWarps = 4;
 constexpr int kThreads = 32 * (kFirstTail + kTailWarps);
@@ -116,12 +117,14 @@ struct Ctl {
     uint64_t empty[kSlots];
     uint64_t s_full[2];
     uint64_t p_full[2];
+    uint64_t rows_full[3];   // by tile mod 3: the tile's row offsets are there
     uint64_t o_empty;        // the unit's accumulator has been read out
     uint64_t o_full[2];      // by tile parity: tile i's completes after tile i - 2's has been waited for
     uint32_t tmem_base;
     int32_t abort_flag;
     alignas(16) float qs[2][kHeads];   // by unit parity: 2^e of the head's query times scale_log2
     float4 row[2][kRows];    // by tile parity: a row's scale (0: masked), its log2 and its inverse
+    uint32_t off[3][kRows];  // by tile mod 3: a row's first line in the cache (~0: masked)
     float red[4][kHeads];    // a tile's maxima by lane quarter; the row sums at the end
     alignas(16) float ma[kSoftmaxWarps][2 * kPartHeads];   // each warp's -m, and how far m moved
     Unit unit[kSoftmaxWarps][2];        // each warp's current and next unit, by unit parity
@@ -251,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             mbar_init(smem_u32(&ctl.p_full[i]), kSoftmaxWarps);
             mbar_init(smem_u32(&ctl.o_full[i]), 1);
         }
+        for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctl.rows_full[i]), kTailWarps);
         mbar_init(smem_u32(&ctl.o_empty), kSoftmaxWarps);
         ctl.abort_flag = 0;
         fence_mbar_init();
@@ -269,24 +273,36 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
     // the ring (slot n % 9, use n / 9).  v counts the units that have tiles.
 
     if (warp >= kFirstTail) {
-        // ---------------- tail block: its slot frees last, so its rows wait in
+        // ---------------- rows and tail blocks.  These warps look up the cache
+        // row of every selected position, one tile ahead: its offset (in
+        // 128-byte lines; masked: ~0) for the latent warps, its scale for
+        // the softmax.  The tail block's slot frees last, so its rows wait in
         // registers and only the stores lie between the free slot and the
         // score product.  Rows without a tail have nothing to gather: the
-        // warps only pass the free slot on to the softmax, which puts P^T
-        // there.  The rows' scales go with it.
+        // warps only pass the free slot on to the softmax, which puts P^T there.
         const int r0 = 32 * (warp - kFirstTail);
+        const uint32_t lines = (uint32_t)width / 128u;
         const uint8_t *src = p.codes + 4 * 128 + (lane & 7) * 16;
         const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
         bool go = true;
         int g = 0;
+        // (tile g - 1's offsets were the buffer's last use: tile g - 3's blocks
+        // had all landed before these warps got past the tail of tile g - 2)
+        auto publish = [&](int32_t row, int tile) {
+            ctl.off[tile % 3][r0 + lane] = row < 0 ? ~0u : (uint32_t)row * lines;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.rows_full[tile % 3]));
+        };
         pdl_wait();                                      // the indices come from the preceding kernel
         for (int u = blockIdx.x; go && u < p.units; u += step) {
             const Unit w = load_unit(p, u, lane);
+            int32_t next_row = -1;
+            if (w.n > 0) publish(next_row = row_of(p, w, w.tile_lo * kRows + r0 + lane, true), g);
             for (int it = 0; go && it < w.n; ++it, ++g) {
                 const uint32_t n = (uint32_t)(kTileBlocks * g + 4), slot = n % kSlots, use = n / kSlots;
-                const int32_t my_row = row_of(p, w, (w.tile_lo + it) * kRows + r0 + lane, false);
-                // The row's scale for the softmax.  Any positive one will do; a
-                // row never written (scale 0) counts as zeros at the smallest.
+                const int32_t my_row = next_row;
+                // The row's scale.  Any positive one will do; a row never
+                // written (scale 0) counts as zeros at the smallest.
                 float s = my_row < 0 ? 0.f : __ldg(p.scale + my_row);
                 uint4 v[8];
                 if (tail) {
@@ -297,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                         if (row >= 0) v[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * width));
                     }
                 }
+                if (it + 1 < w.n) publish(next_row = row_of(p, w, (w.tile_lo + it + 1) * kRows + r0 + lane, true), g + 1);
                 if (my_row >= 0 && s < kMinScale) s = kMinScale;
                 const float4 rv = my_row < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f) : make_float4(s, log2f(s), 1.f / s, 0.f);
                 go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
@@ -315,174 +332,143 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                 if (lane < 32 / kTailWarps) mbar_arrive(smem_u32(&ctl.full[slot]));
             }
         }
-    } else if (warp > 0 && warp < kFirstSoftmax) {
+    } else if (warp >= 2 && warp < kFirstSoftmax) {
         // ---------------- latent blocks: block k = 4 g + j of the sequence of
-        // all tiles goes to warp k mod 3, which copies its 128 rows x 128 bytes
-        // asynchronously.  Row offsets (in 128-byte lines) are looked up before
-        // the slot is free; masked rows become zeros.
-        const int lw = warp - 1;
+        // all tiles goes to warp k mod 2, which copies its 128 rows x 128 bytes
+        // asynchronously; masked rows become zeros.
+        const int lw = warp - 2;
         const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
-        const uint32_t lines = (uint32_t)width / 128u;
         bool go = true;
         int g = 0;
-        pdl_wait();
         for (int u = blockIdx.x; go && u < p.units; u += step) {
-            const Unit w = load_unit(p, u, lane);
-            for (int k = 0; go && k < 4 * w.n; ++k) {
-                if ((4 * g + k) % kLatentWarps != lw) continue;
-                const int it = k >> 2, j = k & 3;
-                const uint32_t n = (uint32_t)(kTileBlocks * (g + it) + j), slot = n % kSlots, use = n / kSlots;
+            const int n_tiles = load_unit(p, u, lane).n;
+            for (int it = 0; go && it < n_tiles; ++it, ++g) {
+                go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.rows_full[g % 3]), (uint32_t)(g / 3) & 1u, ctl, p.status, b.wait_ns));
+                if (!go) break;
+                // lane's chunk of rows 4 i + lane / 8
                 uint32_t off[32];
                 bool masked = false;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int32_t my_row = row_of(p, w, (w.tile_lo + it) * kRows + 32 * q + lane, j == 0);
-                    masked |= my_row < 0;
-                    const uint32_t mine = my_row < 0 ? ~0u : (uint32_t)my_row * lines;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) off[8 * q + i] = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
+                for (int i = 0; i < 32; ++i) {
+                    off[i] = ctl.off[g % 3][4 * i + (lane >> 3)];
+                    masked |= off[i] == ~0u;
                 }
                 masked = __any_sync(0xffffffffu, masked);
-                go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
-                if (!go || b.skip_copies) continue;
-                const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
-                const uint8_t *src = p.codes + j * 128 + (lane & 7) * 16;
-                if (!masked) {
+#pragma unroll 1
+                for (int j = lw; go && j < 4; j += kLatentWarps) {
+                    const uint32_t n = (uint32_t)(kTileBlocks * g + j), slot = n % kSlots, use = n / kSlots;
+                    go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
+                    if (!go || b.skip_copies) continue;
+                    const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
+                    const uint8_t *src = p.codes + j * 128 + (lane & 7) * 16;
+                    if (!masked) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        cp_async16((dst + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6), src + (uint64_t)off[i] * 128u);
-                } else {
+                        for (int i = 0; i < 32; ++i)
+                            cp_async16((dst + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6), src + (uint64_t)off[i] * 128u);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        cp_async16_or_zero((dst + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6),
-                                           src + (off[i] == ~0u ? 0u : (uint64_t)off[i] * 128u), off[i] == ~0u ? 0u : 16u);
+                        for (int i = 0; i < 32; ++i)
+                            cp_async16_or_zero((dst + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6),
+                                               src + (off[i] == ~0u ? 0u : (uint64_t)off[i] * 128u), off[i] == ~0u ? 0u : 16u);
+                    }
+                    cp_async_commit();
+                    cp_async_wait_all();
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&ctl.full[slot]));
                 }
-                cp_async_commit();
-                cp_async_wait_all();
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(&ctl.full[slot]));
             }
-            g += w.n;
         }
-    } else if (warp == 0) {
-        // ---------------- MMA issuer, in a fixed order per tile:
-        //   S(g + 1) blocks 0, 1 | P^T(g) | O(g) block 0 | S(g + 1) blocks 2, 3, tail | O(g) blocks 1..3
-        // The first value-product block frees the slot that the next tile's
-        // tail needs; the rest of the value product runs beside the next
-        // softmax.  A unit's last tile has its whole value product first, then
-        // the next unit's first scores.  Polling for whichever input came
-        // first instead cost 360 to 600 cycles of bookkeeping per block
-        // against 300 to 460 of products.  The whole warp runs the loop
-        // (uniform descriptors); one elected lane issues.
-        const uint32_t id_s = idesc_f8(kRows, 2 * kHeads, false, false);
-        const uint32_t id_hi = idesc_f8(128, kHeads, true, true), id_lo = idesc_f8(128, kHeads, true, true, true);
-        const uint32_t ra = smem_u32(ring), qa = smem_u32(q_s), full0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
-        const uint64_t s_a0 = sdesc_sw128(ra, 16, 1024), s_b0 = sdesc_sw128(qa, 16, 1024);
-        const uint64_t s_bt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
-        const uint64_t o_b0 = sdesc_sw64(ra, 16, 512);
+    } else if (warp < 2) {
+        // ---------------- MMA issuers: warp 0 the score products, warp 1 the
+        // value products, each block as its inputs arrive.  With one warp for
+        // both, its waits for one stream held up the other and their
+        // bookkeeping (200 to 400 cycles per block) lay between the products.
+        // The tensor core takes the two streams' products as they come; they meet in no
+        // accumulator and every reuse of memory goes through a barrier:
+        //  - scores of tile g overwrite those of tile g - 2, whose softmax was
+        //    over before its value product freed the slot of g's first block;
+        //  - the value product of tile g reads blocks its scores have read.
+        // The whole warp runs the loop (uniform descriptors); one elected
+        // lane issues.
+        const uint32_t ra = smem_u32(ring);
+        const uint64_t a0 = sdesc_sw128(ra, 16, 1024);
         auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-            bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
-            if (!ok) ok = __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, p.status, b.wait_ns));
-            tc_fence_after();
-            return ok;
+            return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+                   __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, p.status, b.wait_ns));
         };
         // Block j of tile g has number 5 g + j: slot and use follow from those
         // of the tile's first block (base, use0).
         auto slot_of = [&](int j, uint32_t base) -> uint32_t { return base + j - (base + j >= kSlots ? kSlots : 0u); };
-        auto landed = [&](int j, uint32_t base, uint32_t use0) -> bool {
-            const uint32_t bar = full0 + 8 * slot_of(j, base), parity = (use0 + (base + j >= kSlots ? 1u : 0u)) & 1u;
-            return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
-                   __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, p.status, b.wait_ns));
-        };
-        // The products of score block j of a tile with S^T buffer d_s; the last
-        // one's commit completes the tile's scores.  Called by the elected lane.
-        auto score_block = [&](int j, int g, uint32_t base) {
-            const uint64_t ad = s_a0 + (uint64_t)(slot_of(j, base) * (kBlockBytes >> 4));
-            const uint64_t bd = j < 4 ? s_b0 + (uint64_t)(j * (kQBlockBytes >> 4)) : s_bt;
-            const uint32_t b2 = j < 4 ? 4u : 0u;         // the tail's K steps 2, 3 (remainders) read the query again
-            const uint32_t d_s = tmem + kColS + (g & 1) * 2 * kHeads;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)((ks & 1) * 2) + (ks & 2 ? b2 : 0u), id_s, (j || ks) ? 1u : 0u);
-            if (j == (tail ? 4 : 3)) umma_commit(smem_u32(&ctl.s_full[g & 1]));
-        };
-        // Value-product block c of tile g.
-        auto value_block = [&](int c, uint32_t base, uint64_t bd, uint32_t acc0) {
-            const uint32_t slot = slot_of(c, base);
-            const uint64_t ad = s_a0 + (uint64_t)(slot * (kBlockBytes >> 4));
-#pragma unroll
-            for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-                for (int ks = 0; ks < kRows / 32; ++ks)
-                    umma_f8(tmem + kColO + c * kHeads, ad + (uint64_t)(ks * (32 * 128 >> 4)),
-                            bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), piece ? id_lo : id_hi, (piece || ks) ? 1u : acc0);
-            umma_commit(empty0 + 8 * slot);
-        };
-        int u = blockIdx.x;
-        // the next unit that has tiles, from u on
-        auto tiles_from = [&]() -> int {
-            for (; u < p.units; u += step) {
-                const int n = load_unit(p, u, lane).n;
-                if (n > 0) return n;
-            }
-            return 0;
-        };
-        int n = tiles_from();
         uint32_t base = 0, use0 = 0;
         int g = 0, v = 0;
-        bool go = n > 0;
-        while (go) {
-            // the unit's first scores
-            go = wait(smem_u32(&ctl.q_full), (uint32_t)v & 1u);
+        bool go = true;
+        for (int u = blockIdx.x; go && u < p.units; u += step) {
+            const int n = load_unit(p, u, lane).n;
+            if (n == 0) continue;
+            if (warp == 0) {
+                const uint32_t id_s = idesc_f8(kRows, 2 * kHeads, false, false);
+                const uint32_t qa = smem_u32(q_s);
+                const uint64_t q0 = sdesc_sw128(qa, 16, 1024), qt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
+                const uint32_t full0 = smem_u32(&ctl.full[0]);
+                go = wait(smem_u32(&ctl.q_full), (uint32_t)v & 1u);
+                for (int it = 0; go && it < n; ++it, ++g) {
+                    const uint32_t d_s = tmem + kColS + (g & 1) * 2 * kHeads;
 #pragma unroll
-            for (int j = 0; j < 5; ++j) {
-                if (j == 4 && !tail) break;
-                go = go && landed(j, base, use0);
-                if (go && elect_one()) score_block(j, g, base);
-                __syncwarp();
-            }
-            for (int it = 0; go && it < n; ++it, ++g) {
-                const uint32_t next = slot_of(kTileBlocks, base), next_use = use0 + (base + kTileBlocks >= kSlots ? 1u : 0u);
-                const bool more = it + 1 < n;
+                    for (int j = 0; j < kTileBlocks; ++j) {
+                        if (j == 4 && !tail) break;
+                        const uint32_t slot = slot_of(j, base);
+                        go = go && wait(full0 + 8 * slot, (use0 + (base + j >= kSlots ? 1u : 0u)) & 1u);
+                        if (j == 0) tc_fence_after();    // the accumulator's last readers
+                        if (go && elect_one()) {
+                            const uint64_t ad = a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+                            const uint64_t bd = j < 4 ? q0 + (uint64_t)(j * (kQBlockBytes >> 4)) : qt;
+                            const uint32_t b2 = j < 4 ? 4u : 0u;     // the tail's K steps 2, 3 (remainders) read the query again
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (!more) break;
-                    go = go && landed(j, next, next_use);
-                    if (go && elect_one()) score_block(j, g + 1, next);
-                    __syncwarp();
+                            for (int ks = 0; ks < 4; ++ks)
+                                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)((ks & 1) * 2) + (ks & 2 ? b2 : 0u), id_s,
+                                        (j || ks) ? 1u : 0u);
+                            if (j == (tail ? 4 : 3)) umma_commit(smem_u32(&ctl.s_full[g & 1]));
+                        }
+                        __syncwarp();
+                    }
+                    use0 += base + kTileBlocks >= kSlots ? 1u : 0u;
+                    base = slot_of(kTileBlocks, base);
                 }
-                const uint32_t pslot = slot_of(4, base);
-                const uint64_t bd = o_b0 + (uint64_t)(pslot * (kBlockBytes >> 4));
-                const uint32_t acc0 = it > 0 ? 1u : 0u;
-                go = go && wait(smem_u32(&ctl.p_full[g & 1]), (uint32_t)(g >> 1) & 1u);
+            } else {
+                const uint32_t id_hi = idesc_f8(128, kHeads, true, true), id_lo = idesc_f8(128, kHeads, true, true, true);
+                const uint64_t p0 = sdesc_sw64(ra, 16, 512);
+                const uint32_t empty0 = smem_u32(&ctl.empty[0]);
                 // the accumulator of the unit before has been read
-                if (it == 0 && v > 0) go = go && wait(smem_u32(&ctl.o_empty), (uint32_t)(v - 1) & 1u);
-                if (!go) break;
-                if (elect_one()) value_block(0, base, bd, acc0);
-                __syncwarp();
+                if (v > 0) go = wait(smem_u32(&ctl.o_empty), (uint32_t)(v - 1) & 1u);
+                for (int it = 0; go && it < n; ++it, ++g) {
+                    const uint32_t pslot = slot_of(4, base);
+                    const uint64_t bd = p0 + (uint64_t)(pslot * (kBlockBytes >> 4));
+                    const uint32_t acc0 = it > 0 ? 1u : 0u;
+                    go = wait(smem_u32(&ctl.p_full[g & 1]), (uint32_t)(g >> 1) & 1u);
+                    tc_fence_after();
+                    if (go && elect_one()) {
 #pragma unroll
-                for (int j = 2; j < 5; ++j) {
-                    if (!more || (j == 4 && !tail)) break;
-                    go = go && landed(j, next, next_use);
-                    if (go && elect_one()) score_block(j, g + 1, next);
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t slot = slot_of(c, base);
+                            const uint64_t ad = a0 + (uint64_t)(slot * (kBlockBytes >> 4));
+#pragma unroll
+                            for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+                                for (int ks = 0; ks < kRows / 32; ++ks)
+                                    umma_f8(tmem + kColO + c * kHeads, ad + (uint64_t)(ks * (32 * 128 >> 4)),
+                                            bd + (uint64_t)(piece * (kPieceBytes >> 4) + ks * (32 * 64 >> 4)), piece ? id_lo : id_hi,
+                                            (piece || ks) ? 1u : acc0);
+                            umma_commit(empty0 + 8 * slot);
+                        }
+                        // a unit's last P^T slot goes to the epilogue, which frees it
+                        if (it + 1 < n) umma_commit(empty0 + 8 * pslot);
+                        umma_commit(smem_u32(&ctl.o_full[g & 1]));
+                    }
                     __syncwarp();
+                    base = slot_of(kTileBlocks, base);
                 }
-                if (elect_one()) {
-#pragma unroll
-                    for (int c = 1; c < 4; ++c) value_block(c, base, bd, acc0);
-                    // a unit's last P^T slot goes to the epilogue, which frees it
-                    if (more) umma_commit(empty0 + 8 * pslot);
-                    umma_commit(smem_u32(&ctl.o_full[g & 1]));
-                }
-                __syncwarp();
-                base = next;
-                use0 = next_use;
             }
-            if (!go) break;
-            u += step;
             ++v;
-            n = tiles_from();
-            go = n > 0;
         }
     } else {
         // ---------------- queries, softmax and epilogue
