@@ -228,6 +228,33 @@ __device__ __forceinline__ float dsmem_ld_f32(uint32_t addr) {
     return v;
 }
 
+// ---------------------------------------------------------------- taking over pending CTAs
+// Cluster launch control: a running CTA cancels one of the grid's CTAs that
+// have not started and does its work itself.  The 16-byte answer at dst (shared
+// memory) completes on bar.  After an answer without a CTA no further request
+// may be made.
+__device__ __forceinline__ void clc_request(uint32_t dst, uint32_t bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+// blockIdx.x of the CTA taken over, -1 when none was left.
+__device__ __forceinline__ int clc_answer(uint32_t src) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(src)
+        : "memory");
+    return ok ? (int)x : -1;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");

@@ -23,8 +23,9 @@
 // bf16 products and half the bytes: the two pieces cost what one bf16 product
 // would, and the rows come in at 644 bytes instead of 1152.
 //
-// A unit of work is a (token, head group of 64, split); one CTA per SM takes
-// units in turn and walks their tiles of 128 selected rows.  A tile is five 16 KB blocks of 128 rows x 128 bytes (SWIZZLE_128B):
+// A unit of work is a (token, head group of 64, split), one per CTA of the
+// grid; the CTAs that run take over those that have not started and walk
+// their tiles of 128 selected rows.  A tile is five 16 KB blocks of 128 rows x 128 bytes (SWIZZLE_128B):
 // four of latent codes, one of the tail (64 hi | 64 lo).
 //     S^T[row, piece*head]  = C[row, :] . Q[piece*head, :]^T   M=128, N=128, K=512 + 128
 //     O^T[dim, head]       += C[row, dim]^T . P^T[row, head]   4 x M=128, N=64, K=128, both pieces
@@ -99,7 +100,6 @@ struct Params {
     int H, k, groups, out_bf16;
     float scale_log2;        // sm_scale * log2(e)
     int tiles_per_cta, n_split, n_tiles;
-    int units;               // (token, head group, split) triples, shared out to the CTAs
 };
 
 // One unit of work: a head group of a token, a run of its tiles.
@@ -117,13 +117,16 @@ struct Ctl {
     uint64_t empty[kSlots];
     uint64_t s_full[2];
     uint64_t p_full[2];
+    uint64_t next_full[2];   // the answer to a request for another unit, in turn
+    uint64_t next_empty[2];
     uint64_t rows_full[3];   // by tile mod 3: the tile's row offsets are there
     uint64_t o_empty;        // the unit's accumulator has been read out
     uint64_t o_full[2];      // by tile parity: tile i's completes after tile i - 2's has been waited for
     uint32_t tmem_base;
     int32_t abort_flag;
+    alignas(16) uint4 next[2];          // the answers
     alignas(16) float qs[2][kHeads];   // by unit parity: 2^e of the head's query times scale_log2
-    float4 row[2][kRows];    // by tile parity: a row's scale (0: masked), its log2 and its inverse
+    float2 row[2][kRows];    // by tile parity: a row's scale (0: masked) and its log2
     uint32_t off[3][kRows];  // by tile mod 3: a row's first line in the cache (~0: masked)
     float red[4][kHeads];    // a tile's maxima by lane quarter; the row sums at the end
     alignas(16) float ma[kSoftmaxWarps][2 * kPartHeads];   // each warp's -m, and how far m moved
@@ -131,7 +134,7 @@ struct Ctl {
 };
 
 // qs and ma are read four at a time
-static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && offsetof(Ctl, row) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
+static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && offsetof(Ctl, row) % 8 == 0 && offsetof(Ctl, next) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
                   (kSlots * kBlockBytes + kQBytes) % 16 == 0, "16-byte reads of shared memory");
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
@@ -240,7 +243,6 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
     const DevBatch &b = p.b;
     const bool tail = p.q_rope != nullptr;
     const int width = tail ? kQ8Row : D_L;               // bytes per cached row
-    const int step = gridDim.x;
     tl_start(b.timeline, kTlAttn);
 
     if (threadIdx.x == 0) {
@@ -253,6 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             mbar_init(smem_u32(&ctl.s_full[i]), 1);
             mbar_init(smem_u32(&ctl.p_full[i]), kSoftmaxWarps);
             mbar_init(smem_u32(&ctl.o_full[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl.next_full[i]), 1);
+            mbar_init(smem_u32(&ctl.next_empty[i]), kThreads / 32);
         }
         for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctl.rows_full[i]), kTailWarps);
         mbar_init(smem_u32(&ctl.o_empty), kSoftmaxWarps);
@@ -267,6 +273,24 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
+    // The CTA's units: its own, then those of CTAs that have not started, taken
+    // over one at a time (SMs differ by 20% in speed here: 13 or 14 equal
+    // units per CTA left the slowest 793 us against a mean of 685).  The first
+    // tail warp asks shortly before its last tile of a unit; every warp reads
+    // answer c when it is through with its unit c: a unit, or -1 for the end.
+    // A grid of one wave has nothing to take over (asking would cost it 2 us).
+    const bool one_wave = gridDim.x <= kSMs;
+    auto next_unit_id = [&](int c) -> int {
+        if (one_wave) return -1;
+        const int i = c & 1;
+        int u = -1;
+        if (__all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.next_full[i]), (uint32_t)(c >> 1) & 1u, ctl, p.status, b.wait_ns)))
+            u = clc_answer(smem_u32(&ctl.next[i]));
+        fence_proxy_async_smem();                        // read before the next answer is written
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.next_empty[i]));
+        return __shfl_sync(0xffffffffu, u, 0);
+    };
     // Every role walks the CTA's units and their tiles in the same order.  g
     // counts tiles over all units: tile g has S^T buffer g & 1, the phase
     // (g >> 1) & 1 of the barriers of that parity, and blocks 5 g .. 5 g + 4 of
@@ -293,14 +317,27 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.rows_full[tile % 3]));
         };
+        int asked = 0;                                   // answers requested
+        auto request = [&](int c) {                      // answer c
+            const int i = c & 1;
+            if (one_wave || warp != kFirstTail || lane != 0) return;
+            if (wait_bar(smem_u32(&ctl.next_empty[i]), ((uint32_t)(c >> 1) & 1u) ^ 1u, ctl, p.status, b.wait_ns)) {
+                clc_request(smem_u32(&ctl.next[i]), smem_u32(&ctl.next_full[i]));
+                asked = c + 1;
+            }
+        };
         pdl_wait();                                      // the indices come from the preceding kernel
-        for (int u = blockIdx.x; go && u < p.units; u += step) {
+        for (int u = blockIdx.x, c = 0; u >= 0; u = next_unit_id(c++)) {
             const Unit w = load_unit(p, u, lane);
             int32_t next_row = -1;
+            if (w.n <= 2) request(c);
+            __syncwarp();
             if (w.n > 0) publish(next_row = row_of(p, w, w.tile_lo * kRows + r0 + lane, true), g);
             for (int it = 0; go && it < w.n; ++it, ++g) {
                 const uint32_t n = (uint32_t)(kTileBlocks * g + 4), slot = n % kSlots, use = n / kSlots;
                 const int32_t my_row = next_row;
+                if (it == w.n - 2 && w.n > 2) request(c);
+                __syncwarp();
                 // The row's scale.  Any positive one will do; a row never
                 // written (scale 0) counts as zeros at the smallest.
                 float s = my_row < 0 ? 0.f : __ldg(p.scale + my_row);
@@ -315,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                 }
                 if (it + 1 < w.n) publish(next_row = row_of(p, w, (w.tile_lo + it + 1) * kRows + r0 + lane, true), g + 1);
                 if (my_row >= 0 && s < kMinScale) s = kMinScale;
-                const float4 rv = my_row < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f) : make_float4(s, log2f(s), 1.f / s, 0.f);
+                const float2 rv = my_row < 0 ? make_float2(0.f, -INFINITY) : make_float2(s, log2f(s));
                 go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
                 if (!go || b.skip_copies) continue;
                 // (tile g - 1's first value product freed the slot, after the
@@ -332,6 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                 if (lane < 32 / kTailWarps) mbar_arrive(smem_u32(&ctl.full[slot]));
             }
         }
+        // (after a wait that gave up the last answer may still be on its way)
+        if (asked) mbar_wait(smem_u32(&ctl.next_full[(asked - 1) & 1]), (uint32_t)((asked - 1) >> 1) & 1u, b.wait_ns);
+        __syncwarp();
     } else if (warp >= 2 && warp < kFirstSoftmax) {
         // ---------------- latent blocks: block k = 4 g + j of the sequence of
         // all tiles goes to warp k mod 2, which copies its 128 rows x 128 bytes
@@ -340,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
         const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
         bool go = true;
         int g = 0;
-        for (int u = blockIdx.x; go && u < p.units; u += step) {
+        for (int u = blockIdx.x, c = 0; u >= 0; u = next_unit_id(c++)) {
             const int n_tiles = load_unit(p, u, lane).n;
             for (int it = 0; go && it < n_tiles; ++it, ++g) {
                 go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.rows_full[g % 3]), (uint32_t)(g / 3) & 1u, ctl, p.status, b.wait_ns));
@@ -402,9 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
         uint32_t base = 0, use0 = 0;
         int g = 0, v = 0;
         bool go = true;
-        for (int u = blockIdx.x; go && u < p.units; u += step) {
+        for (int u = blockIdx.x, c = 0; u >= 0; u = next_unit_id(c++)) {
             const int n = load_unit(p, u, lane).n;
-            if (n == 0) continue;
+            if (!go || n == 0) continue;
             if (warp == 0) {
                 const uint32_t id_s = idesc_f8(kRows, 2 * kHeads, false, false);
                 const uint32_t qa = smem_u32(q_s);
@@ -559,23 +599,29 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                 if (tail) prefetch_l2_bulk(p.q_rope + ((int64_t)w.t * p.H + w.h0 + h) * D_R, 2 * D_R);
             }
         };
-        int u = blockIdx.x;
-        // The next unit that has tiles, from u on (n = 0: none is left); the
-        // empty ones on the way get their outputs.
-        auto next_unit = [&](int parity) {
+        int claims = 0;
+        // Puts unit u into the warp's slot (n = -1: there is none).
+        auto set_unit = [&](int u, int parity) {
             Unit w;
-            w.n = 0;
-            for (; u < p.units; u += step) {
-                w = load_unit(p, u, lane);
-                if (w.n > 0) break;
-                write_empty(w);
-            }
+            w.n = -1;
+            if (u >= 0) w = load_unit(p, u, lane);
             if (lane == 0) ctl.unit[sw][parity] = w;
             __syncwarp();
         };
-
-        next_unit(0);
-        if (ctl.unit[sw][0].n > 0) stage_queries(ctl.unit[sw][0], 0);
+        // Gives empty units their outputs until one with tiles, or the end, is
+        // in the slot; then splits its queries.  Only between units: the
+        // answers asked for here need every warp to be through with the unit
+        // before.
+        auto skip_empty = [&](int parity) {
+            while (ctl.unit[sw][parity].n == 0) {
+                write_empty(ctl.unit[sw][parity]);
+                __syncwarp();
+                set_unit(next_unit_id(claims++), parity);
+            }
+            if (ctl.unit[sw][parity].n > 0) stage_queries(ctl.unit[sw][parity], parity);
+        };
+        set_unit(blockIdx.x, 0);
+        skip_empty(0);
         pdl_wait();
         // Every softmax thread runs the same sequence of named barriers whatever
         // happens; `alive` (warp-uniform) only gates tensor-memory and shared
@@ -598,16 +644,16 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             for (int it = 0; it < n_tiles; ++it, ++g) {
                 const int buf = g & 1;
                 if (it + 1 == n_tiles) {
-                    u += step;
-                    next_unit((v + 1) & 1);
+                    set_unit(next_unit_id(claims++), (v + 1) & 1);
                     if (ctl.unit[sw][(v + 1) & 1].n > 0) prefetch_queries(ctl.unit[sw][(v + 1) & 1]);
                 }
                 // the row values and, without a tail, the free slot of P^T: no
                 // score product has waited for it
                 const uint32_t pn = (uint32_t)(kTileBlocks * g + 4), pslot = pn % kSlots;
                 if (alive) alive = wait_bar(smem_u32(&ctl.full[pslot]), (pn / kSlots) & 1u, ctl, p.status, b.wait_ns);
-                const float4 rv = ctl.row[buf][r];         // a masked row's products are 0: u = -inf
-                const uint64_t rs2 = f2(rv.x, rv.x), ef2 = f2(rv.y, rv.y), irs2 = f2(rv.z, rv.z);
+                const float2 rv = ctl.row[buf][r];         // a masked row's products are 0: u = -inf
+                const float irs = rv.x == 0.f ? 0.f : 1.f / rv.x;
+                const uint64_t rs2 = f2(rv.x, rv.x), ef2 = f2(rv.y, rv.y), irs2 = f2(irs, irs);
                 if (alive) alive = wait_bar(smem_u32(&ctl.s_full[buf]), (uint32_t)(g >> 1) & 1u, ctl, p.status, b.wait_ns);
                 alive = __all_sync(0xffffffffu, alive);
                 float x[kPartHeads], top = -INFINITY;      // u - m
@@ -742,7 +788,8 @@ uint32_t a16[2][16], b16[2][16];
             // ---- While the last value product runs: the next unit's queries
             // (the score products have read this one's).
             const Unit &wn = ctl.unit[sw][(v + 1) & 1];
-            if (wn.n > 0) stage_queries(wn, (v + 1) & 1);
+            const bool staged = wn.n > 0;
+            if (staged) stage_queries(wn, (v + 1) & 1);
             // ---- outputs
             const int gl = g - 1;                          // the unit's last tile
             if (alive) alive = wait_bar(smem_u32(&ctl.o_full[gl & 1]), (uint32_t)(gl >> 1) & 1u, ctl, p.status, b.wait_ns);
@@ -842,6 +889,7 @@ uint32_t a16[2][16], b16[2][16];
             if (lane == 0) mbar_arrive(smem_u32(&ctl.o_empty));
             named_barrier(1, kSoftmaxThreads);
             if (tx == 0) mbar_arrive(smem_u32(&ctl.empty[eslot]));
+            if (!staged) skip_empty((v + 1) & 1);
             ++v;
         }
     }
@@ -887,9 +935,8 @@ cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(sparse_attn_q8_kernel), 11, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)b.T * p.groups * a.n_split;
-    if (p.groups < 1 || p.groups > 2 || units > 0x7fffffff - kSMs) return cudaErrorInvalidConfiguration;
-    p.units = (int)units;
-    return launch_k(sparse_attn_q8_kernel, dim3((unsigned)std::min<int64_t>(units, kSMs)), dim3(kThreads), smem, stream, pdl, p);
+    if (p.groups < 1 || p.groups > 2 || units > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_k(sparse_attn_q8_kernel, dim3((unsigned)units), dim3(kThreads), smem, stream, pdl, p);
 }
 
 }  // namespace dsa

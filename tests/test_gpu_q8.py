@@ -585,3 +585,56 @@ def test_tensors_on_the_host_are_refused(dsa, torch):
         dsa.dsa_kv_read_q8(codes.cpu(), scale, s.batch, x.cuda(), s.ws)
     with pytest.raises(TypeError):
         dsa.dsa_rope(x[None], torch.zeros(1, dtype=torch.int32), dsa.Rope.make(64), x[None])
+
+
+@pytest.mark.parametrize("lens,per,k", [([700], [400], 600), ([3000, 2500], [1, 1], 2048)])
+def test_attention_waits_that_run_out(dsa, torch, lens, per, k):
+    """Producers that copy nothing (the failure-path hook): the call reports
+    DSA_DEV_TIMEOUT, and the next one is right again."""
+    s = Seqs(dsa, torch, lens, per)
+    idx = selections(s, k)
+    codes, scale = fill_cache(dsa, torch, s, True)
+    T = s.batch.T
+    q = torch.randn(T, 8, 512, device="cuda").to(torch.bfloat16)
+    qr = torch.randn(T, 8, 64, device="cuda").to(torch.bfloat16)
+    ws = dsa.workspace(dsa.DSA_OP_SPARSE_ATTN, s.batch, H=8, k=k)
+    out = torch.empty(T, 8, 512, device="cuda")
+    args = (q, qr, codes, scale, s.batch, torch.from_numpy(idx).cuda(), 0.1, out, None, ws)
+    try:
+        dsa.dsa_set_test_faults(wait_limit_ns=2_000_000, skip_copies=True)
+        dsa.dsa_sparse_mla_attn_q8(*args)
+        assert dsa.dsa_read_device_status(ws) & dsa.DSA_DEV_TIMEOUT
+    finally:
+        dsa.dsa_set_test_faults()
+    attend(dsa, torch, s, 8, k, idx, check=[0, T - 1])
+
+
+def test_attention_many_units(dsa, torch):
+    """Several thousand units of different lengths, bad positions among them:
+    CTAs take over units of CTAs that have not started."""
+    s = Seqs(dsa, torch, [3000, 900], [2900, 850])
+    k = 200
+    idx = selections(s, k)
+    idx[::7] = -1
+    codes, scale = fill_cache(dsa, torch, s, True)
+    pos = s.batch.q_pos.clone()
+    pos[5::11] = -1
+    s.batch.q_pos = pos
+    H = 3
+    q = torch.randn(s.batch.T, H, 512, device="cuda").to(torch.bfloat16)
+    qr = torch.randn(s.batch.T, H, 64, device="cuda").to(torch.bfloat16)
+    ws = dsa.workspace(dsa.DSA_OP_SPARSE_ATTN, s.batch, H=H, k=k)
+    out = torch.full((s.batch.T, H, 512), float("nan"), device="cuda")
+    lse = torch.full((s.batch.T, H), float("nan"), device="cuda")
+    dsa.dsa_sparse_mla_attn_q8(q, qr, codes, scale, s.batch, torch.from_numpy(idx).cuda(), 0.1, out, lse, ws)
+    assert dsa.dsa_read_device_status(ws) == dsa.DSA_DEV_BAD_POSITION
+    go, gl, c, sc = f64(out), f64(lse), codes.cpu().numpy(), f64(scale)
+    empty = np.zeros(len(s.pos), bool)
+    empty[::7] = True
+    empty[5::11] = True
+    assert np.all(go[empty] == 0) and np.all(np.isneginf(gl[empty]))
+    assert np.all(np.isfinite(go[~empty])) and np.all(np.isfinite(gl[~empty]))
+    for t in np.nonzero(~empty)[0][::97]:
+        rows = np.asarray(s.row(int(s.seq[t]), idx[t][idx[t] >= 0]))
+        ref, rl, tol, tl = R.attention(f64(q[t]), f64(qr[t]), c, sc, rows, 0.1)
+        assert np.all(np.abs(go[t] - ref) <= tol * (1 + 2.0 ** -7) + 2.0 ** -24) and np.all(np.abs(gl[t] - rl) <= tl)
