@@ -137,13 +137,18 @@ struct Ctl {
 static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && offsetof(Ctl, row) % 8 == 0 && offsetof(Ctl, next) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
                   (kSlots * kBlockBytes + kQBytes) % 16 == 0, "16-byte reads of shared memory");
 
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*(volatile int32_t *)&c.abort_flag) return false;
+// What lies off the usual path is called, not inlined: the kernel's code has to
+// stay in the SM's instruction cache (inlined everywhere it was 175 KB, and
+// warps of a decode grid spent half their time waiting for instructions).
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t *abort_flag, uint32_t *status, uint64_t limit_ns) {
+    if (*(volatile int32_t *)abort_flag) return false;
     if (mbar_wait(bar, parity, limit_ns)) return true;
-    *(volatile int32_t *)&c.abort_flag = 1;
+    *(volatile int32_t *)abort_flag = 1;
     flag(status, DSA_DEV_TIMEOUT);
     return false;
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, &c.abort_flag, status, limit_ns);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -200,7 +205,67 @@ __device__ __forceinline__ void split8(const uint4 &v, float inv, uint2 &hi, uin
     lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
-__device__ __forceinline__ Unit load_unit(const Params &p, int u, int lane) {
+// Answer c to the CTA's requests for units (see the kernel).
+__device__ __noinline__ int read_answer(Ctl &ctl, int c, uint32_t *status, uint64_t limit_ns, int lane) {
+    const int i = c & 1;
+    int u = -1;
+    if (__all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.next_full[i]), (uint32_t)(c >> 1) & 1u, ctl, status, limit_ns)))
+        u = clc_answer(smem_u32(&ctl.next[i]));
+    fence_proxy_async_smem();                            // read before the next answer is written
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ctl.next_empty[i]));
+    return __shfl_sync(0xffffffffu, u, 0);
+}
+
+// Heads first .. first + 7 of a unit as two e4m3 pieces in shared memory, and
+// their scales in qs; q_lat and q_rope at the unit's first of nh heads (zeros
+// beyond).  Four heads at a time: of the latent values lane l takes 16 l ..
+// 16 l + 15 of every head, of the tails eight values of head l / 8.
+__device__ __noinline__ void split_queries(const uint16_t *q_lat, const uint16_t *q_rope, int nh, int first, float scale_log2,
+                                           uint8_t *q_s, float *qs, int lane) {
+    static_assert(kHeads / kSoftmaxWarps == 8, "two batches of four heads");
+#pragma unroll 1
+    for (int h0 = first; h0 < first + 8; h0 += 4) {
+        uint4 a[4], c[4], tv = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = c[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h0 + i < nh) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(q_lat + (int64_t)(h0 + i) * D_L) + 2 * lane;
+                a[i] = __ldg(src);
+                c[i] = __ldg(src + 1);
+            }
+        }
+        const int ht = lane >> 3;                        // the lane's head of the tails
+        if (q_rope && h0 + ht < nh) tv = __ldg(reinterpret_cast<const uint4 *>(q_rope + (int64_t)(h0 + ht) * D_R) + (lane & 7));
+        float inv_t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // the largest magnitude, by its bf16 bits
+            uint32_t top = ht == i ? max_bf16(tv) : 0u;
+            top = __reduce_max_sync(0xffffffffu, max(top, max(max_bf16(a[i]), max_bf16(c[i]))));
+            const int e = q8_exponent(__uint_as_float(top << 16));
+            const float inv = exp2_int(-e);
+            if (ht == i) inv_t = inv;
+            uint2 h2[2], l2[2];
+            split8(a[i], inv, h2[0], l2[0]);
+            split8(c[i], inv, h2[1], l2[1]);
+            uint8_t *blk = q_s + (lane >> 3) * kQBlockBytes;
+            *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(h0 + i), (uint32_t)(lane & 7))) =
+                make_uint4(h2[0].x, h2[0].y, h2[1].x, h2[1].y);
+            *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(kHeads + h0 + i), (uint32_t)(lane & 7))) =
+                make_uint4(l2[0].x, l2[0].y, l2[1].x, l2[1].y);
+            if (lane == 0) qs[h0 + i] = h0 + i < nh ? exp2_int(e) * scale_log2 : 0.f;
+        }
+        uint2 h2, l2;
+        split8(tv, inv_t, h2, l2);
+        uint8_t *tb = q_s + 4 * kQBlockBytes + (lane & 1) * 8;
+        *reinterpret_cast<uint2 *>(tb + sw64_offset((uint32_t)(h0 + ht), (uint32_t)(lane & 7) >> 1)) = h2;
+        *reinterpret_cast<uint2 *>(tb + sw64_offset((uint32_t)(kHeads + h0 + ht), (uint32_t)(lane & 7) >> 1)) = l2;
+    }
+}
+
+__device__ __noinline__ Unit load_unit(const Params &p, int u, int lane) {
     const DevBatch &b = p.b;
     Unit w;
     const int g = u / p.n_split;
@@ -219,20 +284,20 @@ __device__ __forceinline__ Unit load_unit(const Params &p, int u, int lane) {
     return w;
 }
 
-// Cache row of entry e of a unit's selection: -1 for padding and for entries
-// out of range (flagged where `report` is set).
-__device__ __forceinline__ int32_t row_of(const Params &p, const Unit &w, int e, bool report) {
-    const int32_t v = e < p.k ? __ldg(p.idx + (int64_t)w.t * p.k + e) : -1;
+// Cache row of entry e of a token's selection: -1 for padding and for entries
+// out of range (flagged).
+__device__ __noinline__ int32_t row_of(const Params &p, int t, int seq, int64_t kv0, int pos, int e) {
+    const int32_t v = e < p.k ? __ldg(p.idx + (int64_t)t * p.k + e) : -1;
     int64_t row = -1;
-    if (v >= 0 && v <= w.pos) row = cache_row(p.b, w.seq, w.kv0, v);
+    if (v >= 0 && v <= pos) row = cache_row(p.b, seq, kv0, v);
     if (row >= p.b.cache_rows) row = -1;
-    if (row < 0 && v != -1 && report) flag(p.status, DSA_DEV_BAD_INDEX);
+    if (row < 0 && v != -1) flag(p.status, DSA_DEV_BAD_INDEX);
     return (int32_t)row;
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *ring = base;
@@ -280,17 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
     // answer c when it is through with its unit c: a unit, or -1 for the end.
     // A grid of one wave has nothing to take over (asking would cost it 2 us).
     const bool one_wave = gridDim.x <= kSMs;
-    auto next_unit_id = [&](int c) -> int {
-        if (one_wave) return -1;
-        const int i = c & 1;
-        int u = -1;
-        if (__all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.next_full[i]), (uint32_t)(c >> 1) & 1u, ctl, p.status, b.wait_ns)))
-            u = clc_answer(smem_u32(&ctl.next[i]));
-        fence_proxy_async_smem();                        // read before the next answer is written
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.next_empty[i]));
-        return __shfl_sync(0xffffffffu, u, 0);
-    };
+    auto next_unit_id = [&](int c) -> int { return one_wave ? -1 : read_answer(ctl, c, p.status, b.wait_ns, lane); };
     // Every role walks the CTA's units and their tiles in the same order.  g
     // counts tiles over all units: tile g has S^T buffer g & 1, the phase
     // (g >> 1) & 1 of the barriers of that parity, and blocks 5 g .. 5 g + 4 of
@@ -332,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             int32_t next_row = -1;
             if (w.n <= 2) request(c);
             __syncwarp();
-            if (w.n > 0) publish(next_row = row_of(p, w, w.tile_lo * kRows + r0 + lane, true), g);
+            if (w.n > 0) publish(next_row = row_of(p, w.t, w.seq, w.kv0, w.pos, w.tile_lo * kRows + r0 + lane), g);
             for (int it = 0; go && it < w.n; ++it, ++g) {
                 const uint32_t n = (uint32_t)(kTileBlocks * g + 4), slot = n % kSlots, use = n / kSlots;
                 const int32_t my_row = next_row;
@@ -350,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                         if (row >= 0) v[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * width));
                     }
                 }
-                if (it + 1 < w.n) publish(next_row = row_of(p, w, (w.tile_lo + it + 1) * kRows + r0 + lane, true), g + 1);
+                if (it + 1 < w.n) publish(next_row = row_of(p, w.t, w.seq, w.kv0, w.pos, (w.tile_lo + it + 1) * kRows + r0 + lane), g + 1);
                 if (my_row >= 0 && s < kMinScale) s = kMinScale;
                 const float2 rv = my_row < 0 ? make_float2(0.f, -INFINITY) : make_float2(s, log2f(s));
                 go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
@@ -385,15 +440,6 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
             for (int it = 0; go && it < n_tiles; ++it, ++g) {
                 go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.rows_full[g % 3]), (uint32_t)(g / 3) & 1u, ctl, p.status, b.wait_ns));
                 if (!go) break;
-                // lane's chunk of rows 4 i + lane / 8
-                uint32_t off[32];
-                bool masked = false;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    off[i] = ctl.off[g % 3][4 * i + (lane >> 3)];
-                    masked |= off[i] == ~0u;
-                }
-                masked = __any_sync(0xffffffffu, masked);
 #pragma unroll 1
                 for (int j = lw; go && j < 4; j += kLatentWarps) {
                     const uint32_t n = (uint32_t)(kTileBlocks * g + j), slot = n % kSlots, use = n / kSlots;
@@ -401,15 +447,16 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                     if (!go || b.skip_copies) continue;
                     const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
                     const uint8_t *src = p.codes + j * 128 + (lane & 7) * 16;
-                    if (!masked) {
+                    const uint32_t *off = ctl.off[g % 3] + (lane >> 3);      // lane's chunk of rows 4 i + lane / 8
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 32; i0 += 8) {
+                        uint32_t o[8];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            cp_async16((dst + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6), src + (uint64_t)off[i] * 128u);
-                    } else {
+                        for (int i = 0; i < 8; ++i) o[i] = off[4 * (i0 + i)];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            cp_async16_or_zero((dst + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6),
-                                               src + (off[i] == ~0u ? 0u : (uint64_t)off[i] * 128u), off[i] == ~0u ? 0u : 16u);
+                        for (int i = 0; i < 8; ++i)
+                            cp_async16_or_zero((dst + (uint32_t)(i0 + i) * 512u) ^ ((uint32_t)(i & 1) << 6),
+                                               src + (o[i] == ~0u ? 0u : (uint64_t)o[i] * 128u), o[i] == ~0u ? 0u : 16u);
                     }
                     cp_async_commit();
                     cp_async_wait_all();
@@ -542,51 +589,11 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const Param
                 if (p.lse && tx < w.nh) p.lse[row + tx] = -INFINITY;
             }
         };
-        // The unit's queries as two pieces.  Each warp splits eight heads, four
-        // at a time: of the latent values lane l takes 16 l .. 16 l + 15 of every
-        // head, of the tails eight values of head l / 8.
+        // The unit's queries as two pieces, eight heads per warp.
         auto stage_queries = [&](const Unit &w, int parity) {
-            static_assert(kHeads / kSoftmaxWarps == 8, "two batches of four heads");
-#pragma unroll 1
-            for (int h0 = sw * 8; h0 < sw * 8 + 8; h0 += 4) {
-                const int64_t row0 = (int64_t)w.t * p.H + w.h0 + h0;
-                uint4 a[4], c[4], tv = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[i] = c[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (h0 + i < w.nh) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + (row0 + i) * D_L) + 2 * lane;
-                        a[i] = __ldg(src);
-                        c[i] = __ldg(src + 1);
-                    }
-                }
-                const int ht = lane >> 3;                  // the lane's head of the tails
-                if (tail && h0 + ht < w.nh) tv = __ldg(reinterpret_cast<const uint4 *>(p.q_rope + (row0 + ht) * D_R) + (lane & 7));
-                float inv_t = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // the largest magnitude, by its bf16 bits
-                    uint32_t top = ht == i ? max_bf16(tv) : 0u;
-                    top = __reduce_max_sync(0xffffffffu, max(top, max(max_bf16(a[i]), max_bf16(c[i]))));
-                    const int e = q8_exponent(__uint_as_float(top << 16));
-                    const float inv = exp2_int(-e);
-                    if (ht == i) inv_t = inv;
-                    uint2 h2[2], l2[2];
-                    split8(a[i], inv, h2[0], l2[0]);
-                    split8(c[i], inv, h2[1], l2[1]);
-                    uint8_t *blk = q_s + (lane >> 3) * kQBlockBytes;
-                    *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(h0 + i), (uint32_t)(lane & 7))) =
-                        make_uint4(h2[0].x, h2[0].y, h2[1].x, h2[1].y);
-                    *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(kHeads + h0 + i), (uint32_t)(lane & 7))) =
-                        make_uint4(l2[0].x, l2[0].y, l2[1].x, l2[1].y);
-                    if (lane == 0) ctl.qs[parity][h0 + i] = h0 + i < w.nh ? exp2_int(e) * p.scale_log2 : 0.f;
-                }
-                uint2 h2, l2;
-                split8(tv, inv_t, h2, l2);
-                uint8_t *tb = q_s + 4 * kQBlockBytes + (lane & 1) * 8;
-                *reinterpret_cast<uint2 *>(tb + sw64_offset((uint32_t)(h0 + ht), (uint32_t)(lane & 7) >> 1)) = h2;
-                *reinterpret_cast<uint2 *>(tb + sw64_offset((uint32_t)(kHeads + h0 + ht), (uint32_t)(lane & 7) >> 1)) = l2;
-            }
+            const int64_t row0 = (int64_t)w.t * p.H + w.h0;
+            split_queries(p.q_lat + row0 * D_L, tail ? p.q_rope + row0 * D_R : nullptr, w.nh, sw * (kHeads / kSoftmaxWarps),
+                          p.scale_log2, q_s, ctl.qs[parity], lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full));
@@ -713,11 +720,13 @@ uint32_t a16[2][16], b16[2][16];
                     fresh = __all_sync(0xffffffffu, over == -INFINITY) && fresh;
                     __syncwarp();
 #pragma unroll
-                    for (int h = 0; h < kPartHeads; ++h) x[h] -= ma[kPartHeads + h];
-                    if (moved) {
-#pragma unroll
-                        for (int h = 0; h < kPartHeads / 2; ++h)
-                            lpart[h] = f2_mul(lpart[h], f2(ex2(-ma[kPartHeads + 2 * h]), ex2(-ma[kPartHeads + 2 * h + 1])));
+                    for (int h = 0; h < kPartHeads; h += 4) {
+                        const float4 up4 = *reinterpret_cast<const float4 *>(ma + kPartHeads + h);
+                        x[h] -= up4.x; x[h + 1] -= up4.y; x[h + 2] -= up4.z; x[h + 3] -= up4.w;
+                        if (moved) {
+                            lpart[h / 2] = f2_mul(lpart[h / 2], f2(ex2(-up4.x), ex2(-up4.y)));
+                            lpart[h / 2 + 1] = f2_mul(lpart[h / 2 + 1], f2(ex2(-up4.z), ex2(-up4.w)));
+                        }
                     }
                 }
                 // the weights' two pieces, 16 heads (16 bytes) at a time
