@@ -494,10 +494,12 @@ class Rope:
         return 2 * self.inv_freq.numel()
 
     def desc(self) -> dsa_rope_t:
-        import torch
+        if not _DT:
+            _bind()
         f = self.inv_freq
-        _shaped(f, "inv_freq", torch.float64, (f.numel(),), f.get_device())
-        return dsa_rope_t(f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0, self.scale)
+        n = f.numel()
+        _shaped(f, "inv_freq", _t_f64, (n,), _cuda(f, "inv_freq"))
+        return dsa_rope_t(f.data_ptr(), 2 * n, 1 if self.interleaved else 0, self.scale)
 
 
 def dsa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -512,81 +514,87 @@ def dsa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "no
     return list(f), scale.value
 
 
-def _dtypes():
-    import torch
-    return {torch.float32: DSA_DT_F32, torch.float16: DSA_DT_F16, torch.bfloat16: DSA_DT_BF16}
-
-
-_DT = None
+# The calls below take microseconds on the device, so their checks are kept to
+# a few attribute reads per tensor, on names bound by the first call.
+_DT = {}
 _ANY_FLOAT = (DSA_DT_F32, DSA_DT_F16, DSA_DT_BF16)
 _OUT_FLOAT = (DSA_DT_F32, DSA_DT_BF16)
 
 
+def _bind():
+    global _DT, _t_u8, _t_i32, _t_i64, _t_f32, _t_f64, _t_bf16, _get_device, _raw_stream, _on_device
+    import torch
+    _t_u8, _t_i32, _t_i64 = torch.uint8, torch.int32, torch.int64
+    _t_f32, _t_f64, _t_bf16 = torch.float32, torch.float64, torch.bfloat16
+    _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _on_device = torch.cuda.device
+    _DT = {torch.float32: DSA_DT_F32, torch.float16: DSA_DT_F16, torch.bfloat16: DSA_DT_BF16}
+
+
+def _cuda(t, name):
+    """The CUDA index of t's device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise TypeError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return dev
+
+
 def _dt(t, name, allowed=_ANY_FLOAT):
-    global _DT
-    if _DT is None:
-        _DT = _dtypes()
     d = _DT.get(t.dtype)
     if d not in allowed:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     return d
 
 
-# The calls below take microseconds on the device, so their checks are kept to
-# a few attribute reads per tensor.
-
 def _shaped(t, name, dtype, shape, dev):
     """A contiguous tensor of that dtype and shape on device `dev` (a CUDA index)."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or dev < 0 or not t.is_contiguous():
-        raise TypeError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on cuda:{max(dev, 0)}, "
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}, "
                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows(t, name, dtype, shape, dev):
-    """The same for a matrix of contiguous rows any stride apart."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or dev < 0 or t.stride(1) != 1:
-        raise TypeError(f"{name}: expected {dtype} rows {tuple(shape)} on cuda:{max(dev, 0)}, "
+    """A matrix of contiguous rows any stride apart; returns that stride."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or t.stride(1) != 1:
+        raise TypeError(f"{name}: expected {dtype} rows {tuple(shape)} on cuda:{dev}, "
                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.stride(0)
 
 
 def _q8_cache(codes, scale, tail: bool, batch: Batch, dev):
-    import torch
     rows = codes.shape[0]
-    _shaped(codes, "codes", torch.uint8, (rows, Q8_ROW if tail else 512), dev)
-    _shaped(scale, "scale", torch.float32, (rows,), dev)
+    _shaped(codes, "codes", _t_u8, (rows, Q8_ROW if tail else 512), dev)
+    _shaped(scale, "scale", _t_f32, (rows,), dev)
     if rows < batch.cache_rows:
         raise TypeError(f"codes: {rows} rows, the batch names {batch.cache_rows}")
 
 
 def _batch_desc(batch: Batch, dev) -> dsa_batch_t:
     """Batch.desc with its tensors' device checked as well."""
-    import torch
     cu, pos, off = batch.cu_q, batch.q_pos, batch.kv_off
     B, T = cu.numel() - 1, pos.numel()
-    _shaped(cu, "cu_q", torch.int32, (B + 1,), dev)
-    _shaped(pos, "q_pos", torch.int32, (T,), dev)
-    _shaped(off, "kv_off", torch.int64, (B,), dev)
+    _shaped(cu, "cu_q", _t_i32, (B + 1,), dev)
+    _shaped(pos, "q_pos", _t_i32, (T,), dev)
+    _shaped(off, "kv_off", _t_i64, (B,), dev)
     return dsa_batch_t(B, T, batch.max_q_per_seq, batch.max_kv, batch.cache_rows, cu.data_ptr(), pos.data_ptr(),
                        off.data_ptr())
 
 
 def _paging(block_table, block_size: int, batch: Batch, dev):
     """(dsa_paging_t pointer or None) of an optional block table [B, max_blocks]."""
-    import torch
     if block_table is None:
         return None
-    _shaped(block_table, "block_table", torch.int32, (batch.B, block_table.shape[-1]), dev)
-    return C.byref(dsa_paging_t(block_table.data_ptr(), block_table.shape[1], block_size))
+    blocks = block_table.shape[-1]
+    _shaped(block_table, "block_table", _t_i32, (batch.B, blocks), dev)
+    return C.byref(dsa_paging_t(block_table.data_ptr(), blocks, block_size))
 
 
 def _call(name, dev, stream, fn, *args):
     """fn(*args, stream) on device dev; the current stream of dev unless one is given."""
-    import torch
-    if torch._C._cuda_getDevice() != dev:
-        with torch.cuda.device(dev):
+    if _get_device() != dev:
+        with _on_device(dev):
             return _call(name, dev, stream, fn, *args)
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    code = fn(*args, s)
+    code = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if code != DSA_OK:
         raise DsaError(code, name)
 
@@ -596,15 +604,16 @@ def dsa_rope(x, pos, rope: Rope, out, rot_off: int = 0, inverse: bool = False, s
     the tokens' positions.  x, out: [T, heads, dim] of one dtype (float32,
     float16, bfloat16), any token and head strides, contiguous heads; out may
     be x.  pos: int32 [T].  inverse: the gradient's direction."""
-    import torch
-    dt, dev, shape = _dt(x, "x"), x.get_device(), x.shape
+    if not _DT:
+        _bind()
+    dt, dev, shape = _dt(x, "x"), _cuda(x, "x"), x.shape
     xs, ys = x.stride(), out.stride()
-    if len(shape) != 3 or out.shape != shape or out.dtype != x.dtype or dev < 0 or out.get_device() != dev \
+    if len(shape) != 3 or out.shape != shape or out.dtype is not x.dtype or out.get_device() != dev \
             or (shape[2] > 1 and (xs[2] != 1 or ys[2] != 1)):
         raise TypeError(f"x, out: expected CUDA tensors [T, heads, dim] of one shape and dtype with contiguous heads, "
                         f"got {x.dtype} {tuple(shape)} on {x.device} and {out.dtype} {tuple(out.shape)} on {out.device}")
     T, heads, dim = shape
-    _shaped(pos, "pos", torch.int32, (T,), dev)
+    _shaped(pos, "pos", _t_i32, (T,), dev)
     r = rope.desc()
     if rope.inv_freq.get_device() != dev:
         raise TypeError(f"inv_freq: on {rope.inv_freq.device}, x on {x.device}")
@@ -614,32 +623,35 @@ def dsa_rope(x, pos, rope: Rope, out, rot_off: int = 0, inverse: bool = False, s
 
 def _append_args(c_new, r_new, batch: Batch, rope, block_table, block_size, dev):
     """The arguments the two append calls share, up to the cache."""
-    T, dt = batch.q_pos.numel(), _dt(c_new, "c_new")
-    _rows(c_new, "c_new", c_new.dtype, (T, 512), dev)
-    rp, rs = None, 0
+    T, dt, kind = batch.q_pos.numel(), _dt(c_new, "c_new"), c_new.dtype
+    cs = _rows(c_new, "c_new", kind, (T, 512), dev)
+    rp, rs, turn = None, 0, None
     if r_new is not None:
-        _rows(r_new, "r_new", c_new.dtype, (T, 64), dev)
-        rp, rs = r_new.data_ptr(), r_new.stride(0)
-    if rope is not None and rope.inv_freq.get_device() != dev:
-        raise TypeError(f"inv_freq: on {rope.inv_freq.device}, c_new on {c_new.device}")
-    return (c_new.data_ptr(), c_new.stride(0), rp, rs, dt, C.byref(_batch_desc(batch, dev)),
-            _paging(block_table, block_size, batch, dev), C.byref(rope.desc()) if rope is not None else None)
+        rs = _rows(r_new, "r_new", kind, (T, 64), dev)
+        rp = r_new.data_ptr()
+    if rope is not None:
+        turn = C.byref(rope.desc())
+        if rope.inv_freq.get_device() != dev:
+            raise TypeError(f"inv_freq: on {rope.inv_freq.device}, c_new on {c_new.device}")
+    return (c_new.data_ptr(), cs, rp, rs, dt, C.byref(_batch_desc(batch, dev)),
+            _paging(block_table, block_size, batch, dev), turn)
 
 
 def _workspace_arg(ws, dev):
     if ws.get_device() != dev:
         raise TypeError(f"ws: expected on cuda:{dev}, got {ws.device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def dsa_kv_append(c_new, r_new, batch: Batch, rope, kv_cache, ws, block_table=None, block_size: int = 0, stream=None):
     """One bf16 latent row per token into kv_cache [rows, 576] ([rows, 512]
     with r_new None).  c_new [T, 512] and r_new [T, 64] may be column slices;
     the tail is turned at the token's position when rope (a Rope) is given."""
-    import torch
-    dev, rows = c_new.get_device(), kv_cache.shape[0]
+    if not _DT:
+        _bind()
+    dev, rows = _cuda(c_new, "c_new"), kv_cache.shape[0]
     args = _append_args(c_new, r_new, batch, rope, block_table, block_size, dev)
-    _shaped(kv_cache, "kv_cache", torch.bfloat16, (rows, 512 if r_new is None else 576), dev)
+    _shaped(kv_cache, "kv_cache", _t_bf16, (rows, 512 if r_new is None else 576), dev)
     if rows < batch.cache_rows:
         raise TypeError(f"kv_cache: {rows} rows, the batch names {batch.cache_rows}")
     _call("dsa_kv_append", dev, stream, lib().dsa_kv_append, *args, kv_cache.data_ptr(), *_workspace_arg(ws, dev))
@@ -656,7 +668,9 @@ def dsa_kv_append_q8(c_new, r_new, batch: Batch, rope, codes, scale, ws, block_t
                      stream=None):
     """dsa_kv_append into an 8-bit cache: codes uint8 [rows, 640] ([rows, 512]
     with r_new None), scale float32 [rows]."""
-    dev = c_new.get_device()
+    if not _DT:
+        _bind()
+    dev = _cuda(c_new, "c_new")
     args = _append_args(c_new, r_new, batch, rope, block_table, block_size, dev)
     _q8_cache(codes, scale, r_new is not None, batch, dev)
     _call("dsa_kv_append_q8", dev, stream, lib().dsa_kv_append_q8, *args, codes.data_ptr(), scale.data_ptr(),
@@ -666,32 +680,35 @@ def dsa_kv_append_q8(c_new, r_new, batch: Batch, rope, codes, scale, ws, block_t
 def dsa_kv_read_q8(codes, scale, batch: Batch, out, ws, block_table=None, block_size: int = 0, stream=None):
     """The tokens' rows of an 8-bit cache as out [T, 576] ([T, 512] for codes
     of 512), bfloat16 or float32; out may be a column slice of wider rows."""
-    dev, T = codes.get_device(), batch.q_pos.numel()
+    if not _DT:
+        _bind()
+    dev, T = _cuda(codes, "codes"), batch.q_pos.numel()
     tail = codes.shape[-1] == Q8_ROW
     _q8_cache(codes, scale, tail, batch, dev)
     dt, width = _dt(out, "out", _OUT_FLOAT), 576 if tail else 512
-    _rows(out, "out", out.dtype, (T, width), dev)
+    stride = _rows(out, "out", out.dtype, (T, width), dev)
     _call("dsa_kv_read_q8", dev, stream, lib().dsa_kv_read_q8, codes.data_ptr(), scale.data_ptr(), 1 if tail else 0,
           C.byref(_batch_desc(batch, dev)), _paging(block_table, block_size, batch, dev), out.data_ptr(), dt,
-          out.stride(0) if T > 1 else width, *_workspace_arg(ws, dev))
+          stride if T > 1 else width, *_workspace_arg(ws, dev))
 
 
 def dsa_sparse_mla_attn_q8(q_lat, q_rope, codes, scale, batch: Batch, idx, sm_scale: float, out, lse, ws,
                            block_table=None, block_size: int = 0, stream=None):
     """dsa_sparse_mla_attn over an 8-bit cache (q_rope None: codes of 512, no
     tail); out [T, H, 512] float32 or bfloat16, lse [T, H] float32 or None."""
-    import torch
-    dev, T, H = q_lat.get_device(), batch.q_pos.numel(), q_lat.shape[1]
-    _shaped(q_lat, "q_lat", torch.bfloat16, (T, H, 512), dev)
+    if not _DT:
+        _bind()
+    dev, T, H = _cuda(q_lat, "q_lat"), batch.q_pos.numel(), q_lat.shape[1]
+    _shaped(q_lat, "q_lat", _t_bf16, (T, H, 512), dev)
     if q_rope is not None:
-        _shaped(q_rope, "q_rope", torch.bfloat16, (T, H, 64), dev)
+        _shaped(q_rope, "q_rope", _t_bf16, (T, H, 64), dev)
     _q8_cache(codes, scale, q_rope is not None, batch, dev)
     k = idx.shape[-1]
-    _shaped(idx, "idx", torch.int32, (T, k), dev)
+    _shaped(idx, "idx", _t_i32, (T, k), dev)
     dt = _dt(out, "out", _OUT_FLOAT)
     _shaped(out, "out", out.dtype, (T, H, 512), dev)
     if lse is not None:
-        _shaped(lse, "lse", torch.float32, (T, H), dev)
+        _shaped(lse, "lse", _t_f32, (T, H), dev)
     _call("dsa_sparse_mla_attn_q8", dev, stream, lib().dsa_sparse_mla_attn_q8, q_lat.data_ptr(),
           q_rope.data_ptr() if q_rope is not None else None, codes.data_ptr(), scale.data_ptr(),
           C.byref(_batch_desc(batch, dev)), _paging(block_table, block_size, batch, dev), idx.data_ptr(), k, H, sm_scale,
