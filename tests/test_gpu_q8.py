@@ -638,3 +638,80 @@ def test_attention_many_units(dsa, torch):
         rows = np.asarray(s.row(int(s.seq[t]), idx[t][idx[t] >= 0]))
         ref, rl, tol, tl = R.attention(f64(q[t]), f64(qr[t]), c, sc, rows, 0.1)
         assert np.all(np.abs(go[t] - ref) <= tol * (1 + 2.0 ** -7) + 2.0 ** -24) and np.all(np.abs(gl[t] - rl) <= tl)
+
+
+def test_decode_step_over_the_8_bit_cache(dsa, torch):
+    """A whole step as a server runs it: the indexer's keys, scores and top-k,
+    the new tokens' rows turned and appended, their queries turned, attention
+    over the selection; against 64 bits over the cache and selection it left."""
+    lens, H, H_I, k = [2900, 1200, 300], 64, 32, 512
+    s = Seqs(dsa, torch, lens, [1, 1, 1])
+    codes, scale = fill_cache(dsa, torch, s, True)
+    before = codes.clone()
+    g = gen(torch, 21)
+    keys = torch.randn(s.rows, 128, generator=g, device="cuda").half()
+    k_new = torch.randn(3, 128, generator=g, device="cuda").half()
+    q_idx = torch.randn(3, H_I, 128, generator=g, device="cuda").half()
+    w = torch.rand(3, H_I, generator=g, device="cuda")
+    c_new = torch.randn(3, 512, generator=g, device="cuda").to(torch.bfloat16)
+    r_new = torch.randn(3, 64, generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn(3, H, 576, generator=g, device="cuda").to(torch.bfloat16)
+    rope = dsa.Rope.make(64, 1e4, True, "yarn", 4.0, 1024)
+    idx = torch.empty(3, k, dtype=torch.int32, device="cuda")
+    width = (max(lens) + 127) // 128 * 128
+    scores = torch.empty(3, width, device="cuda")
+    out, lse = torch.empty(3, H, 512, device="cuda"), torch.empty(3, H, device="cuda")
+    ws = {op: dsa.workspace(op, s.batch, H_I, H, k) for op in (dsa.DSA_OP_K_APPEND, dsa.DSA_OP_INDEXER_SCORE,
+                                                               dsa.DSA_OP_TOPK, dsa.DSA_OP_SPARSE_ATTN)}
+    dsa.dsa_indexer_k_append(k_new, s.batch, keys, False, ws[dsa.DSA_OP_K_APPEND])
+    dsa.dsa_kv_append_q8(c_new, r_new, s.batch, rope, codes, scale, ws[dsa.DSA_OP_K_APPEND])
+    dsa.dsa_indexer_score(q_idx, w, keys, s.batch, False, scores, ws[dsa.DSA_OP_INDEXER_SCORE])
+    dsa.dsa_topk(scores, s.batch, k, idx, ws[dsa.DSA_OP_TOPK])
+    dsa.dsa_rope(q, s.batch.q_pos, rope, q, 512)
+    q_lat, q_rope = q[:, :, :512].contiguous(), q[:, :, 512:].contiguous()
+    dsa.dsa_sparse_mla_attn_q8(q_lat, q_rope, codes, scale, s.batch, idx, 0.07, out, lse, ws[dsa.DSA_OP_SPARSE_ATTN])
+    assert all(dsa.dsa_read_device_status(v) == 0 for v in ws.values())
+    at = torch.from_numpy(s.token_rows()).cuda()
+    others = torch.ones(s.rows, dtype=torch.bool, device="cuda")
+    others[at] = False
+    assert torch.equal(codes[others], before[others]) and not torch.equal(codes[at], before[at])
+    c, sc, sel = codes.cpu().numpy(), f64(scale), idx.cpu().numpy()
+    for t in range(3):
+        mine = sel[t][sel[t] >= 0]
+        assert len(mine) == min(k, lens[t])
+        ref, rl, tol, tl = R.attention(f64(q_lat[t]), f64(q_rope[t]), c, sc, np.asarray(s.row(t, mine)), 0.07)
+        assert np.all(np.abs(f64(out[t]) - ref) <= tol) and np.all(np.abs(f64(lse[t]) - rl) <= tl)
+
+
+def test_two_streams_at_once(dsa, torch):
+    """Two attention calls side by side, each with its own workspace, give what
+    they give alone: split decodes and a grid of several waves."""
+    def setup(s, H, k, seed):
+        codes, scale = fill_cache(dsa, torch, s, True, seed=seed)
+        g = gen(torch, seed + 1)
+        T = s.batch.T
+        q = torch.randn(T, H, 512, generator=g, device="cuda").to(torch.bfloat16)
+        r = torch.randn(T, H, 64, generator=g, device="cuda").to(torch.bfloat16)
+        idx = torch.from_numpy(selections(s, k, seed)).cuda()
+        ws = dsa.workspace(dsa.DSA_OP_SPARSE_ATTN, s.batch, H=H, k=k)
+
+        def call():
+            out, lse = torch.empty(T, H, 512, device="cuda"), torch.empty(T, H, device="cuda")
+            dsa.dsa_sparse_mla_attn_q8(q, r, codes, scale, s.batch, idx, 0.06, out, lse, ws, *s.paging)
+            return out, lse
+        return call, ws
+
+    calls = [setup(Seqs(dsa, torch, [3000, 2500, 600], [1, 1, 1]), 64, 2048, 31),
+             setup(Seqs(dsa, torch, [900, 500], [200, 150], 16), 128, 300, 41)]
+    alone = [c() for c, _ in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(4):
+        got = []
+        for (c, _), st in zip(calls, streams):
+            with torch.cuda.stream(st):
+                got.append(c())
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert all(dsa.dsa_read_device_status(ws) == 0 for _, ws in calls)
