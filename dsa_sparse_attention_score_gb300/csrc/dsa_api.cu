@@ -816,7 +816,7 @@ static dsa_status_t cache_batch(const dsa_batch_t *batch, const dsa_paging_t *pa
 static dsa_status_t run_attention_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const uint8_t *codes,
                                      const float *scale, const DevBatch &db, const int32_t *idx, int k, int H,
                                      float sm_scale, void *out, int out_dtype, float *lse, void *ws, const Layout &L,
-                                     cudaStream_t stream, bool pdl) {
+                                     cudaStream_t stream) {
     AttnQ8Launch a;
     a.q_lat = q_lat;
     a.q_rope = q_rope;
@@ -834,7 +834,7 @@ static dsa_status_t run_attention_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_ro
     uint8_t *w8 = static_cast<uint8_t *>(ws);
     a.part_o = a.n_split > 1 ? reinterpret_cast<uint16_t *>(w8 + L.part_o) : nullptr;
     a.part_ml = a.n_split > 1 ? reinterpret_cast<float *>(w8 + L.part_ml) : nullptr;
-    DSA_TRY_CUDA(launch_sparse_attn_q8(a, db, status_ptr(ws), stream, pdl));
+    DSA_TRY_CUDA(launch_sparse_attn_q8(a, db, status_ptr(ws), stream));
     AttnLaunch c{};
     c.H = H;
     c.out = a.out_bf16 ? nullptr : static_cast<float *>(out);
@@ -926,7 +926,7 @@ dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rop
         return DSA_ERR_MISALIGNED;
     const Layout L = layout(DSA_OP_SPARSE_ATTN, batch, H, k);
     if ((s = check_ws(ws, ws_bytes, L.total)) != DSA_OK) return s;
-    return run_attention_q8(q_lat, q_rope, codes, scale, db, idx, k, H, sm_scale, out, out_dtype, lse, ws, L, stream, false);
+    return run_attention_q8(q_lat, q_rope, codes, scale, db, idx, k, H, sm_scale, out, out_dtype, lse, ws, L, stream);
 }
 
 }  // extern "C"

@@ -212,7 +212,7 @@ struct AttnQ8Launch {
     float *part_ml;
 };
 int attn_q8_tile_rows();
-cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream, bool pdl);
+cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream);
 
 // Sets a kernel's dynamic shared-memory limit once per device; `slot`
 // (0..kSmemAttrSlots-1) names the kernel instance.

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams 
     using W = Two<T>;
     constexpr bool kBoth = !kInter || V == 1;            // a rotated unit needs two loads
     constexpr int kPairs = kInter && V > 1 ? V / 2 : V;  // angles of a rotated unit
+    pdl_wait();
     const int t = blockIdx.x, tid = threadIdx.x;
     const int half = p.r.rot_dim >> 1;
     const int rot_units = V > 1 ? p.r.rot_dim / V : half;
@@ -159,8 +160,8 @@ cudaError_t launch_rope_as(RopeParams p, int n_tokens, cudaStream_t stream) {
     const int threads = (p.rows * p.lanes + 31) / 32 * 32;
     const int ny = (p.heads + p.rows * kUnits - 1) / (p.rows * kUnits), nz = (p.per_head + p.lanes - 1) / p.lanes;
     if (ny > 65535 || nz > 65535) return cudaErrorInvalidConfiguration;
-    rope_kernel<T, kInter, V><<<dim3((unsigned)n_tokens, (unsigned)ny, (unsigned)nz), threads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_k(rope_kernel<T, kInter, V>, dim3((unsigned)n_tokens, (unsigned)ny, (unsigned)nz), dim3((unsigned)threads), 0,
+                    stream, true, p);
 }
 
 template <typename T>

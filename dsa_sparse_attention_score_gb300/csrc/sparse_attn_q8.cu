@@ -7,8 +7,8 @@
 // decoded.  What makes that possible:
 //  - The row's scale leaves both contractions.  z_j = 2^E_j (codes_j . q), and
 //    with u_j = z_j log2(e) + E_j the output is sum_j 2^(u_j - M) codes_j over
-//    l = sum_j 2^(z_j log2(e) - M): the scale is folded into the weights (E_j = log2 of the scale: a power of two is not
-//    needed here).
+//    l = sum_j 2^(z_j log2(e) - M): the scale is folded into the weights (E_j =
+//    log2 of the scale: a power of two is not needed here).
 //  - A bf16 query is the sum of two e4m3 pieces: q 2^-e = hi + lo with
 //    hi = e4m3(q 2^-e), lo = e4m3(q 2^-e - hi).  Four significant bits each,
 //    the remainder signed, hold bf16's eight: the split is exact for values
@@ -25,27 +25,48 @@
 //
 // A unit of work is a (token, head group of 64, split), one per CTA of the
 // grid; the CTAs that run take over those that have not started and walk
-// their tiles of 128 selected rows.  A tile is five 16 KB blocks of 128 rows x 128 bytes (SWIZZLE_128B):
-// four of latent codes, one of the tail (64 hi | 64 lo).
+// their tiles of 128 selected rows.  A tile is five 16 KB blocks of 128 rows x
+// 128 bytes (SWIZZLE_128B): four of latent codes, one of the tail (64 hi | 64
+// lo).
 //     S^T[row, piece*head]  = C[row, :] . Q[piece*head, :]^T   M=128, N=128, K=512 + 128
 //     O^T[dim, head]       += C[row, dim]^T . P^T[row, head]   4 x M=128, N=64, K=128, both pieces
 // The same bytes are the K-major A operand of S^T and the MN-major A operand
 // of O^T.  The tail's two halves multiply the same 64 query values, so its
 // four K steps read the two of q_rope twice.  S^T accumulates a head's two
-// pieces in columns h and 64 + h, which the softmax adds; O^T adds both pieces of
-// P^T in place.  The tail block is dead once S^T is computed and holds P^T.
+// pieces in columns h and 64 + h, which the softmax adds; O^T adds both pieces
+// of P^T in place.  The tail block is dead once S^T is computed and holds P^T.
 //
 // Shared memory: queries 72 KB and a ring of nine blocks (144 KB), one short
 // of two tiles: a tile's tail block goes in when the first value product of
-// the tile before has freed its slot.  One producer warp per latent block
-// gathers it with 16-byte cp.async copies (a row's 128 bytes are one cache
+// the tile before has freed its slot.  Two producer warps gather the latent
+// blocks in turn with 16-byte cp.async copies (a row's 128 bytes are one cache
 // line; masked rows are filled with zeros and read nothing); four more hold
 // the tail block in registers until its slot is free.  Two warps issue the
-// score and the value products as their inputs arrive; eight softmax warps (two per TMEM lane
-// quarter, 32 heads each) turn a tile's S^T into P^T.  The reference M of a
-// head's weights is set 2^2 below its first tile's maximum and moves only
-// when a weight would exceed 2^8, so most tiles need no maxima, only the
-// question whether any weight does.
+// score and the value products as their inputs arrive; eight softmax warps (two
+// per TMEM lane quarter, 32 heads each) turn a tile's S^T into P^T.  The
+// reference M of a head's weights is set 2^2 below its first tile's maximum and
+// moves only when a weight would exceed 2^8, so most tiles need no maxima, only
+// the question whether any weight does.
+//
+// Measured on the device, 64 heads: a prefill chunk of 2048 tokens over 2048
+// rows each 674 us (866 TFLOP/s counted as for bf16, 45% of what the tensor
+// cores do on one large bf16 product); a decode step of 8 sequences over 2048
+// rows 17.9 us and of 32 sequences 27.5 us, the join of the splits included
+// (3.5 us).  What bounds it:
+//  - A tile takes about 5000 cycles, 16 of them and the change of units (13700
+//    cycles: queries split, outputs written) a unit.  The products read their
+//    operands from shared memory at its full rate, S^T 160 KB and O^T 192 KB a
+//    tile, and with the gather's 80 KB and P^T's 16 KB that is 3500 cycles at
+//    128 bytes each.  The rest is the chain: the first value product frees the
+//    slot of the next tile's tail, whose scores then stand behind the other
+//    three in the tensor core's queue, and its softmax (2700 cycles) has to
+//    wait for them.  Holding those three back until the scores are queued
+//    starves the gather instead (682 to 718 us); a ring of ten blocks does not
+//    fit; eight blocks with the tail passed through 4 KB a K step at a time
+//    took 663 to 709 us and made decode slower.
+//  - A decode step's CTA runs one or two tiles: 4000 cycles to the queries' two
+//    pieces, 2000 to the first scores, 3000 of softmax, 2000 of value products,
+//    5000 of epilogue, each once, with the code coming in from L2.
 #include <algorithm>
 #include <cstddef>
 
@@ -134,7 +155,8 @@ struct Ctl {
 };
 
 // qs and ma are read four at a time
-static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && offsetof(Ctl, row) % 8 == 0 && offsetof(Ctl, next) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
+static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && offsetof(Ctl, row) % 8 == 0 &&
+                  offsetof(Ctl, next) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
                   (kSlots * kBlockBytes + kQBytes) % 16 == 0, "16-byte reads of shared memory");
 
 // What lies off the usual path is called, not inlined: the kernel's code has to
@@ -338,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
+    pdl_wait();
     // The CTA's units: its own, then those of CTAs that have not started, taken
     // over one at a time (SMs differ by 20% in speed here: 13 or 14 equal
     // units per CTA left the slowest 793 us against a mean of 685).  The first
@@ -381,7 +404,6 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                 asked = c + 1;
             }
         };
-        pdl_wait();                                      // the indices come from the preceding kernel
         for (int u = blockIdx.x, c = 0; u >= 0; u = next_unit_id(c++)) {
             const Unit w = load_unit(p, u, lane);
             int32_t next_row = -1;
@@ -629,7 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
         };
         set_unit(blockIdx.x, 0);
         skip_empty(0);
-        pdl_wait();
         // Every softmax thread runs the same sequence of named barriers whatever
         // happens; `alive` (warp-uniform) only gates tensor-memory and shared
         // memory work after a bounded wait gave up.
@@ -799,10 +820,8 @@ uint32_t a16[2][16], b16[2][16];
             const Unit &wn = ctl.unit[sw][(v + 1) & 1];
             const bool staged = wn.n > 0;
             if (staged) stage_queries(wn, (v + 1) & 1);
-            // ---- outputs
+            // ---- outputs: the row sums behind the last value product as well
             const int gl = g - 1;                          // the unit's last tile
-            if (alive) alive = wait_bar(smem_u32(&ctl.o_full[gl & 1]), (uint32_t)(gl >> 1) & 1u, ctl, p.status, b.wait_ns);
-            alive = __all_sync(0xffffffffu, alive);
             float lrow[kPartHeads];
 #pragma unroll
             for (int h = 0; h < kPartHeads / 2; ++h) {
@@ -818,6 +837,8 @@ uint32_t a16[2][16], b16[2][16];
             const float l = ctl.red[0][hl] + ctl.red[1][hl] + ctl.red[2][hl] + ctl.red[3][hl];
             ma[lane] = p.n_split > 1 ? 1.f : fresh ? 0.f : 1.f / l;
             __syncwarp();
+            if (alive) alive = wait_bar(smem_u32(&ctl.o_full[gl & 1]), (uint32_t)(gl >> 1) & 1u, ctl, p.status, b.wait_ns);
+            alive = __all_sync(0xffffffffu, alive);
             const int64_t row0 = (int64_t)w.t * p.H + w.h0;
             const int64_t part0 = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
             const uint32_t eslot = (uint32_t)(kTileBlocks * gl + 4) % kSlots;
@@ -918,7 +939,7 @@ uint32_t a16[2][16], b16[2][16];
 
 int attn_q8_tile_rows() { return kRows; }
 
-cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream, bool pdl) {
+cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream) {
     Params p{};
     p.q_lat = a.q_lat;
     p.q_rope = a.q_rope;
@@ -945,7 +966,7 @@ cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)b.T * p.groups * a.n_split;
     if (p.groups < 1 || p.groups > 2 || units > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_k(sparse_attn_q8_kernel, dim3((unsigned)units), dim3(kThreads), smem, stream, pdl, p);
+    return launch_k(sparse_attn_q8_kernel, dim3((unsigned)units), dim3(kThreads), smem, stream, true, p);
 }
 
 }  // namespace dsa

@@ -468,15 +468,14 @@ dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stri
  * with a NaN or infinite value gets the scale NaN and reads back as NaN.
  * codes must be 16-byte aligned (128 keeps rows on cache lines).
  *
- * dsa_kv_append writes one bf16 row of the token per call argument below into
- * a cache [cache_rows, 576] (or 512) as dsa_sparse_mla_attn reads it;
- * dsa_kv_append_q8 into an 8-bit cache.  The tail is turned at the token's
- * position first (rope, rot_dim 64), or stored as it is when rope is NULL.
+ * dsa_kv_append writes each token's row into a bf16 cache [cache_rows, 576]
+ * (512 without a tail) as dsa_sparse_mla_attn reads it, dsa_kv_append_q8 into
+ * an 8-bit cache.  The tail is turned at the token's position first (rope,
+ * rot_dim 64), or stored as it is when rope is NULL.
  *   c_new   [T,512], rows c_stride values apart; r_new [T,64], rows r_stride
  *           values apart, or NULL for rows without a tail; both of dtype DSA_DT_*
  *   paging  NULL for contiguous caches (row kv_off[b] + position); any
- *           block_size >= 1 is accepted here and in the other calls on the
- *           8-bit cache but dsa_decode_q8
+ *           block_size >= 1, here and in the other calls on the 8-bit cache
  *   ws      at least dsa_workspace_size(DSA_OP_K_APPEND) bytes (status word)
  * Tokens of a batch must be at different rows.  A token whose position is out
  * of bounds is skipped and flagged DSA_DEV_BAD_POSITION; no other row changes.
@@ -505,7 +504,12 @@ dsa_status_t dsa_kv_read_q8(const uint8_t *codes, const float *scale, int tail, 
  * as dsa_sparse_mla_attn_nope), contiguous or paged.
  *   out        [T,H,512] of out_dtype DSA_DT_F32 or DSA_DT_BF16
  *   the rest   as dsa_sparse_mla_attn, with its workspace (DSA_OP_SPARSE_ATTN)
- * The codes are read as they are held, in float32 sums.
+ *              and dsa_decode_paged's meaning of paging
+ * Products are of 8-bit values with float32 sums.  Queries count to eight
+ * significant bits (all of a bf16 value's) down to 2^-10 of their head's largest
+ * value, weights to 2^-7 of themselves or 2^-15 of the largest; the partial
+ * outputs of a token that several CTAs share are joined in bf16.  Any positive
+ * scale serves, power of two or not; below 2^-40 it counts as 2^-40.
  */
 dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const uint8_t *codes,
                                     const float *scale, const dsa_batch_t *batch, const dsa_paging_t *paging,
