@@ -509,7 +509,9 @@ dsa_status_t dsa_kv_read_q8(const uint8_t *codes, const float *scale, int tail, 
  * significant bits (all of a bf16 value's) down to 2^-10 of their head's largest
  * value, weights to 2^-7 of themselves or 2^-15 of the largest; the partial
  * outputs of a token that several CTAs share are joined in bf16.  Any positive
- * scale serves, power of two or not; below 2^-40 it counts as 2^-40.
+ * scale serves, power of two or not; below 2^-40 it counts as 2^-40.  Scales
+ * of a token's selected rows that lie further than 2^90 apart cost the rows
+ * with the smaller ones their weight.
  */
 dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const uint8_t *codes,
                                     const float *scale, const dsa_batch_t *batch, const dsa_paging_t *paging,

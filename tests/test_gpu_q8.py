@@ -715,3 +715,72 @@ def test_two_streams_at_once(dsa, torch):
         for a, b in zip(alone, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert all(dsa.dsa_read_device_status(ws) == 0 for _, ws in calls)
+
+
+def test_calls_in_a_row_see_what_the_one_before_wrote(dsa, torch):
+    """The calls start while what precedes them ends: a hundred rounds without a
+    pause of torch kernel -> append -> read -> rotation in place and back ->
+    attention over the row just written, eager and from a graph in which
+    copies, a memset and a joined side stream precede them."""
+    B, H = 5, 16
+    s = Seqs(dsa, torch, [40] * B, [1] * B)
+    codes, scale = dsa.q8_cache(s.rows)
+    ws = dsa.workspace(dsa.DSA_OP_SPARSE_ATTN, s.batch, H=H, k=1)
+    idx = torch.full((B, 1), 39, dtype=torch.int32, device="cuda")        # its own row: the output is that row
+    c_new, r_new = (torch.zeros(B, n, dtype=torch.bfloat16, device="cuda") for n in (512, 64))
+    q, qr = (torch.ones(B, H, n, dtype=torch.bfloat16, device="cuda") for n in (512, 64))
+    back = torch.empty(B, 576, device="cuda")
+    out = torch.empty(B, H, 512, device="cuda")
+    rope = dsa.Rope.make(64, 1e4, False)
+    x = torch.empty(B, H, 64, device="cuda")
+    rounds = [(-1) ** i * 2.0 ** (i % 13) for i in range(100)]           # e4m3 holds them exactly
+    got = torch.empty(len(rounds), 3, device="cuda")
+
+    def calls():
+        dsa.dsa_kv_append_q8(c_new, r_new, s.batch, None, codes, scale, ws)
+        dsa.dsa_kv_read_q8(codes, scale, s.batch, back, ws)
+        dsa.dsa_rope(x, s.batch.q_pos, rope, x)
+        dsa.dsa_rope(x, s.batch.q_pos, rope, x, inverse=True)
+        dsa.dsa_sparse_mla_attn_q8(q, qr, codes, scale, s.batch, idx, 0.01, out, None, ws)
+
+    def check(tol=2.0 ** -20):
+        g = got.cpu().numpy()
+        for i, v in enumerate(rounds):
+            assert g[i, 0] == v and g[i, 1] == v, (i, v, g[i])
+            assert abs(g[i, 2] - v) <= tol * 4 * abs(v), (i, v, g[i])
+
+    def note(i):
+        got[i, 0], got[i, 1] = back.amin(), out.amin()
+        got[i, 2] = x.amin() if rounds[i] > 0 else x.amax()
+
+    for i, v in enumerate(rounds):
+        c_new.fill_(v)
+        r_new.fill_(v)
+        x.fill_(v)
+        calls()
+        note(i)
+    torch.cuda.synchronize()
+    check()
+    src = torch.zeros(B, 512, dtype=torch.bfloat16, device="cuda")
+    val = torch.zeros((), device="cuda")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            r_new.copy_(src[:, :64])
+            x.copy_(val.expand(B, H, 64))
+        codes.zero_()                                                     # a memset
+        main.wait_stream(side)
+        c_new.copy_(src)                                                  # a copy
+        calls()
+    got.zero_()
+    for i, v in enumerate(rounds):
+        src.fill_(v)
+        val.fill_(v)
+        graph.replay()
+        note(i)
+    torch.cuda.synchronize()
+    check()
+    assert dsa.dsa_read_device_status(ws) == 0
