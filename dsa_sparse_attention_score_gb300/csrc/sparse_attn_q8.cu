@@ -25,47 +25,45 @@
 //
 // A unit of work is a (token, head group of 64, split), one per CTA of the
 // grid; the CTAs that run take over those that have not started and walk
-// their tiles of 128 selected rows.  A tile is five 16 KB blocks of 128 rows x
-// 128 bytes (SWIZZLE_128B): four of latent codes, one of the tail (64 hi | 64
-// lo).
+// their tiles of 128 selected rows.  A tile's latent codes are four 16 KB
+// blocks of 128 rows x 128 bytes (SWIZZLE_128B) in shared memory, its tails
+// (64 hi | 64 lo) 32 columns of tensor memory, a row a lane.
 //     S^T[row, piece*head]  = C[row, :] . Q[piece*head, :]^T   M=128, N=128, K=512 + 128
 //     O^T[dim, head]       += C[row, dim]^T . P^T[row, head]   4 x M=128, N=64, K=128, both pieces
 // The same bytes are the K-major A operand of S^T and the MN-major A operand
 // of O^T.  The tail's two halves multiply the same 64 query values, so its
 // four K steps read the two of q_rope twice.  S^T accumulates a head's two
 // pieces in columns h and 64 + h, which the softmax adds; O^T adds both pieces
-// of P^T in place.  The tail block is dead once S^T is computed and holds P^T.
+// of P^T in place.
 //
-// Shared memory: queries 72 KB and a ring of nine blocks (144 KB), one short
-// of two tiles: a tile's tail block goes in when the first value product of
-// the tile before has freed its slot.  Two producer warps gather the latent
-// blocks in turn with 16-byte cp.async copies (a row's 128 bytes are one cache
-// line; masked rows are filled with zeros and read nothing); four more hold
-// the tail block in registers until its slot is free.  Two warps issue the
-// score and the value products as their inputs arrive; eight softmax warps (two
-// per TMEM lane quarter, 32 heads each) turn a tile's S^T into P^T.  The
+// Shared memory: queries 72 KB, a ring of two tiles' latent blocks 128 KB, P^T
+// 16 KB.  Tensor memory: S^T 128 columns, two tiles' tails 64, O^T 256.  Four
+// warps bring in 32 rows of every tile each, the latent codes with 16-byte
+// cp.async copies, the tails through registers; two issue the score and the
+// value products as their inputs arrive; eight softmax warps (two per TMEM lane
+// quarter, 32 heads each) turn a tile's S^T into P^T, and write a unit's
+// outputs; they and two more split the next unit's queries meanwhile.  The
 // reference M of a head's weights is set 2^2 below its first tile's maximum and
 // moves only when a weight would exceed 2^8, so most tiles need no maxima, only
 // the question whether any weight does.
 //
-// Measured on the device, 64 heads: a prefill chunk of 2048 tokens over 2048
-// rows each 674 us (866 TFLOP/s counted as for bf16, 45% of what the tensor
-// cores do on one large bf16 product); a decode step of 8 sequences over 2048
-// rows 17.9 us and of 32 sequences 27.5 us, the join of the splits included
-// (3.5 us).  What bounds it:
-//  - A tile takes about 5000 cycles, 16 of them and the change of units (13700
-//    cycles: queries split, outputs written) a unit.  The products read their
-//    operands from shared memory at its full rate, S^T 160 KB and O^T 192 KB a
-//    tile, and with the gather's 80 KB and P^T's 16 KB that is 3500 cycles at
-//    128 bytes each.  The rest is the chain: the first value product frees the
-//    slot of the next tile's tail, whose scores then stand behind the other
-//    three in the tensor core's queue, and its softmax (2700 cycles) has to
-//    wait for them.  Holding those three back until the scores are queued
-//    starves the gather instead (682 to 718 us); a ring of ten blocks does not
-//    fit; eight blocks with the tail passed through 4 KB a K step at a time
-//    took 663 to 709 us and made decode slower.
+// Measured, one call after the other over three sets of inputs, 64 heads: a
+// prefill chunk of 2048 tokens over 2048 rows each 659 us (886 TFLOP/s counted as
+// for bf16, 46% of what the tensor cores do on one large bf16 product); a decode
+// step of 8 sequences over 2048 rows 17.2 us and of 32 sequences 30.6 us, the join
+// of the splits included (3.5 us).  What bounds it:
+//  - A tile takes about 4600 cycles, and a unit 16 of them and some 13000 for
+//    its outputs and the next one's queries.  The products read their operands
+//    from shared memory at its full rate, S^T 144 KB and O^T 192 KB a tile, and
+//    with the gather's 64 KB and P^T's 16 KB that is 3300 cycles at 128 bytes
+//    each.  The rest is the chain of every other tile: value product (1900
+//    cycles, which frees the ring's blocks), gather (1500), scores (1300),
+//    softmax (2700); the two chains take turns on the tensor core.
+//  - With the tail as a fifth block, whose slot P^T took over, the next tile's
+//    scores waited for the value product: 5000 cycles, a ragged decode of 32 in
+//    33.2 instead of 30.6 us.
 //  - A decode step's CTA runs one or two tiles: 4000 cycles to the queries' two
-//    pieces, 2000 to the first scores, 3000 of softmax, 2000 of value products,
+//    pieces, 1000 to the first scores, 3000 of softmax, 2000 of value products,
 //    5000 of epilogue, each once, with the code coming in from L2.
 #include <algorithm>
 #include <cstddef>
@@ -81,8 +79,8 @@ namespace {
 constexpr int kHeads = 64;                    // heads per CTA (padded)
 constexpr int kRows = 128;                    // selected rows per tile
 constexpr int kBlockBytes = kRows * 128;      // 16 KB
-constexpr int kTileBlocks = 5;                // 4 latent + the tail (P^T)
-constexpr int kSlots = 9;
+constexpr int kTileBlocks = 4;                // of latent codes
+constexpr int kSlots = 2 * kTileBlocks;
 constexpr int kQBlockBytes = 2 * kHeads * 128;        // hi and lo rows of 128 codes
 constexpr int kQTailBytes = 2 * kHeads * 64;          // hi and lo rows of 64 codes (SWIZZLE_64B)
 constexpr int kQBytes = 4 * kQBlockBytes + kQTailBytes;
@@ -91,21 +89,26 @@ constexpr int kParts = 2;                     // groups of 32 heads
 constexpr int kPartHeads = kHeads / kParts;
 constexpr int kSoftmaxWarps = 4 * kParts;     // one per (TMEM lane quarter, part)
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-// Warp 0 issues the score products, warp 1 the value products, warps 2 and 3
-// gather latent blocks in turn, 4..11 do the softmax, 12..15 hold 32 rows of
-// the tail block each.
-constexpr int kLatentWarps = 2;
-constexpr int kFirstSoftmax = 2 + kLatentWarps;       // a multiple of 4: warp mod 4 is the lane quarter
-constexpr int kFirstTail = kFirstSoftmax + kSoftmaxWarps;
-constexpr int kTailWarps = 4;
-constexpr int kThreads = 32 * (kFirstTail + kTailWarps);
+// Warps 0..3 bring in 32 rows of a tile each, 4..11 do the softmax, 12 issues
+// the score products, 13 the value products, 14 and 15 split half of the
+// queries of the CTA's second and later units.
+constexpr int kRowWarps = 4;                  // one per TMEM lane quarter
+constexpr int kFirstSoftmax = kRowWarps;      // a multiple of 4: warp mod 4 is the lane quarter
+constexpr int kFirstIssuer = kFirstSoftmax + kSoftmaxWarps;
+constexpr int kFirstSplit = kFirstIssuer + 2;
+constexpr int kSplitWarps = 2;
+// heads of a later unit's queries that a softmax and a split warp take
+constexpr int kSoftmaxSplit = 4, kOwnSplit = (kHeads - kSoftmaxWarps * kSoftmaxSplit) / kSplitWarps;
+constexpr int kThreads = 32 * (kFirstSplit + kSplitWarps);
 constexpr float kTopLog2 = 2.0f;              // a new maximum's weight is 2^2 ...
 constexpr float kRaiseLog2 = 8.0f;            // ... and none exceeds 2^8
 constexpr int kFewMoved = 6;                  // heads of 32 rescaled one by one
 constexpr float kMinScale = 0x1p-40f;
-constexpr uint32_t kTmemCols = 512;           // S^T: 2 x 128 columns, O^T: 4 x 64
+constexpr uint32_t kTmemCols = 512;           // S^T: 128 columns, the tails of two tiles: 2 x 32, O^T: 4 x 64
 constexpr uint32_t kColS = 0;
+constexpr uint32_t kColT = 2 * kHeads;
 constexpr uint32_t kColO = 256;
+constexpr int kRingBytes = kSlots * kBlockBytes + kBlockBytes;    // latent blocks of two tiles, P^T
 
 struct Params {
     const uint16_t *q_lat, *q_rope;
@@ -134,21 +137,24 @@ struct Unit {
 
 struct Ctl {
     uint64_t q_full;
+    uint64_t q_empty;        // the unit's scores have read its queries
     uint64_t full[kSlots];
     uint64_t empty[kSlots];
-    uint64_t s_full[2];
-    uint64_t p_full[2];
+    uint64_t t_full[2];      // by tile parity: the tile's tails are in tensor memory
+    uint64_t t_empty[2];     // ... and have been read
+    uint64_t s_full;
+    uint64_t s_empty;        // S^T has been read
+    uint64_t p_full;
     uint64_t next_full[2];   // the answer to a request for another unit, in turn
     uint64_t next_empty[2];
-    uint64_t rows_full[3];   // by tile mod 3: the tile's row offsets are there
+    uint64_t row_full[3];    // by tile mod 3: the tile's row scales are there
     uint64_t o_empty;        // the unit's accumulator has been read out
     uint64_t o_full[2];      // by tile parity: tile i's completes after tile i - 2's has been waited for
     uint32_t tmem_base;
     int32_t abort_flag;
     alignas(16) uint4 next[2];          // the answers
     alignas(16) float qs[2][kHeads];   // by unit parity: 2^e of the head's query times scale_log2
-    float2 row[2][kRows];    // by tile parity: a row's scale (0: masked) and its log2
-    uint32_t off[3][kRows];  // by tile mod 3: a row's first line in the cache (~0: masked)
+    float2 row[3][kRows];    // by tile mod 3: a row's scale (0: masked) and its log2
     float red[4][kHeads];    // a tile's maxima by lane quarter; the row sums at the end
     alignas(16) float ma[kSoftmaxWarps][2 * kPartHeads];   // each warp's -m, and how far m moved
     Unit unit[kSoftmaxWarps][2];        // each warp's current and next unit, by unit parity
@@ -157,7 +163,7 @@ struct Ctl {
 // qs and ma are read four at a time
 static_assert(offsetof(Ctl, qs) % 16 == 0 && offsetof(Ctl, ma) % 16 == 0 && offsetof(Ctl, row) % 8 == 0 &&
                   offsetof(Ctl, next) % 16 == 0 && (2 * kPartHeads * 4) % 16 == 0 &&
-                  (kSlots * kBlockBytes + kQBytes) % 16 == 0, "16-byte reads of shared memory");
+                  (kRingBytes + kQBytes) % 16 == 0, "16-byte reads of shared memory");
 
 // What lies off the usual path is called, not inlined: the kernel's code has to
 // stay in the SM's instruction cache (inlined everywhere it was 175 KB, and
@@ -203,23 +209,25 @@ __device__ __forceinline__ float warp_sum_32(float (&a)[32], int lane) {
     return a[0];
 }
 
-// The largest magnitude of eight bf16 values, as 15 bits.
+// The largest magnitudes of eight bf16 values' upper and lower halves, as 15 bits each.
 __device__ __forceinline__ uint32_t max_bf16(const uint4 &v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-    return m;
+    constexpr uint32_t M = 0x7FFF7FFFu;
+    return __vmaxu2(__vmaxu2(v.x & M, v.y & M), __vmaxu2(v.z & M, v.w & M));
 }
 
-// The two e4m3 pieces of eight bf16 values times inv.  The product is exact in
-// float32, and fp16 holds it to 2^-24: far below the last piece's 2^-10.
-__device__ __forceinline__ void split8(const uint4 &v, float inv, uint2 &hi, uint2 &lo) {
+// The two e4m3 pieces of eight bf16 values times 2^-e, none above 448.  fp16
+// holds the products to 2^-24, far below the last piece's 2^-10, and they get
+// there in integers, two at a time: bf16's exponent field less 112 + e is
+// fp16's (drop: that times 2^7, negated, in both halves); what falls below
+// 2^-14 goes to a value below it or to 0.
+__device__ __forceinline__ void split8(const uint4 &v, uint32_t drop, uint2 &hi, uint2 &lo) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2 x = __floats2half2_rn(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xFFFF0000u) * inv);
+        const uint32_t u = __viaddmax_s16x2_relu(w[i] & 0x7FFF7FFFu, drop, 0u);
+        const uint32_t bits = u << 3 | (w[i] & 0x80008000u);
+        const __half2 x = *reinterpret_cast<const __half2 *>(&bits);
         h[i] = e4m3x2(x);
         l[i] = e4m3x2(__hsub2(x, e4m3x2_to_half2(h[i])));
     }
@@ -239,15 +247,14 @@ __device__ __noinline__ int read_answer(Ctl &ctl, int c, uint32_t *status, uint6
     return __shfl_sync(0xffffffffu, u, 0);
 }
 
-// Heads first .. first + 7 of a unit as two e4m3 pieces in shared memory, and
-// their scales in qs; q_lat and q_rope at the unit's first of nh heads (zeros
-// beyond).  Four heads at a time: of the latent values lane l takes 16 l ..
+// Heads first .. end - 1 (a multiple of four) of a unit as two e4m3 pieces in
+// shared memory, and their scales in qs; q_lat and q_rope at the unit's first
+// of nh heads (zeros beyond).  Four heads at a time: of the latent values lane l takes 16 l ..
 // 16 l + 15 of every head, of the tails eight values of head l / 8.
-__device__ __noinline__ void split_queries(const uint16_t *q_lat, const uint16_t *q_rope, int nh, int first, float scale_log2,
-                                           uint8_t *q_s, float *qs, int lane) {
-    static_assert(kHeads / kSoftmaxWarps == 8, "two batches of four heads");
+__device__ __noinline__ void split_queries(const uint16_t *q_lat, const uint16_t *q_rope, int nh, int first, int end,
+                                           float scale_log2, uint8_t *q_s, float *qs, int lane) {
 #pragma unroll 1
-    for (int h0 = first; h0 < first + 8; h0 += 4) {
+    for (int h0 = first; h0 < end; h0 += 4) {
         uint4 a[4], c[4], tv = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -260,27 +267,27 @@ __device__ __noinline__ void split_queries(const uint16_t *q_lat, const uint16_t
         }
         const int ht = lane >> 3;                        // the lane's head of the tails
         if (q_rope && h0 + ht < nh) tv = __ldg(reinterpret_cast<const uint4 *>(q_rope + (int64_t)(h0 + ht) * D_R) + (lane & 7));
-        float inv_t = 0.f;
+        uint32_t drop_t = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // the largest magnitude, by its bf16 bits
-            uint32_t top = ht == i ? max_bf16(tv) : 0u;
-            top = __reduce_max_sync(0xffffffffu, max(top, max(max_bf16(a[i]), max_bf16(c[i]))));
+            // the largest magnitude by its bf16 bits
+            const uint32_t both = __vmaxu2(ht == i ? max_bf16(tv) : 0u, __vmaxu2(max_bf16(a[i]), max_bf16(c[i])));
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(both & 0xFFFFu, both >> 16));
             const int e = q8_exponent(__uint_as_float(top << 16));
-            const float inv = exp2_int(-e);
-            if (ht == i) inv_t = inv;
+            const uint32_t drop = (uint32_t)(-(112 + e) * 128 & 0xFFFF) * 0x10001u;
+            if (ht == i) drop_t = drop;
+            if (lane == i) qs[h0 + i] = h0 + i >= nh ? 0.f : top < 0x7F80u ? exp2_int(e) * scale_log2 : __int_as_float(0x7FC00000);
             uint2 h2[2], l2[2];
-            split8(a[i], inv, h2[0], l2[0]);
-            split8(c[i], inv, h2[1], l2[1]);
+            split8(a[i], drop, h2[0], l2[0]);
+            split8(c[i], drop, h2[1], l2[1]);
             uint8_t *blk = q_s + (lane >> 3) * kQBlockBytes;
             *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(h0 + i), (uint32_t)(lane & 7))) =
                 make_uint4(h2[0].x, h2[0].y, h2[1].x, h2[1].y);
             *reinterpret_cast<uint4 *>(blk + sw128_offset((uint32_t)(kHeads + h0 + i), (uint32_t)(lane & 7))) =
                 make_uint4(l2[0].x, l2[0].y, l2[1].x, l2[1].y);
-            if (lane == 0) qs[h0 + i] = h0 + i < nh ? exp2_int(e) * scale_log2 : 0.f;
         }
         uint2 h2, l2;
-        split8(tv, inv_t, h2, l2);
+        split8(tv, drop_t, h2, l2);
         uint8_t *tb = q_s + 4 * kQBlockBytes + (lane & 1) * 8;
         *reinterpret_cast<uint2 *>(tb + sw64_offset((uint32_t)(h0 + ht), (uint32_t)(lane & 7) >> 1)) = h2;
         *reinterpret_cast<uint2 *>(tb + sw64_offset((uint32_t)(kHeads + h0 + ht), (uint32_t)(lane & 7) >> 1)) = l2;
@@ -306,24 +313,14 @@ __device__ __noinline__ Unit load_unit(const Params &p, int u, int lane) {
     return w;
 }
 
-// Cache row of entry e of a token's selection: -1 for padding and for entries
-// out of range (flagged).
-__device__ __noinline__ int32_t row_of(const Params &p, int t, int seq, int64_t kv0, int pos, int e) {
-    const int32_t v = e < p.k ? __ldg(p.idx + (int64_t)t * p.k + e) : -1;
-    int64_t row = -1;
-    if (v >= 0 && v <= pos) row = cache_row(p.b, seq, kv0, v);
-    if (row >= p.b.cache_rows) row = -1;
-    if (row < 0 && v != -1) flag(p.status, DSA_DEV_BAD_INDEX);
-    return (int32_t)row;
-}
-
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *ring = base;
-    uint8_t *q_s = base + kSlots * kBlockBytes;          // four latent blocks, then the tail's
+    uint8_t *p_s = base + kSlots * kBlockBytes;          // P^T
+    uint8_t *q_s = base + kRingBytes;                    // four latent blocks, then the tail's
     Ctl &ctl = *reinterpret_cast<Ctl *>(q_s + kQBytes);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -333,21 +330,25 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
     tl_start(b.timeline, kTlAttn);
 
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&ctl.q_full), kSoftmaxWarps);
+        mbar_init(smem_u32(&ctl.q_full), kSoftmaxWarps + kSplitWarps);
+        mbar_init(smem_u32(&ctl.q_empty), 1);
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(smem_u32(&ctl.full[i]), 32);
+            mbar_init(smem_u32(&ctl.full[i]), kRowWarps);
             mbar_init(smem_u32(&ctl.empty[i]), 1);
         }
+        mbar_init(smem_u32(&ctl.s_full), 1);
+        mbar_init(smem_u32(&ctl.s_empty), kSoftmaxWarps);
+        mbar_init(smem_u32(&ctl.p_full), kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&ctl.s_full[i]), 1);
-            mbar_init(smem_u32(&ctl.p_full[i]), kSoftmaxWarps);
+            mbar_init(smem_u32(&ctl.t_full[i]), kRowWarps);
+            mbar_init(smem_u32(&ctl.t_empty[i]), 1);
             mbar_init(smem_u32(&ctl.o_full[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl.next_full[i]), 1);
             mbar_init(smem_u32(&ctl.next_empty[i]), kThreads / 32);
         }
-        for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctl.rows_full[i]), kTailWarps);
+        for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctl.row_full[i]), kRowWarps);
         mbar_init(smem_u32(&ctl.o_empty), kSoftmaxWarps);
         ctl.abort_flag = 0;
         fence_mbar_init();
@@ -360,45 +361,37 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
-    pdl_wait();
+    pdl_wait();                                          // no input is read before this
     // The CTA's units: its own, then those of CTAs that have not started, taken
     // over one at a time (SMs differ by 20% in speed here: 13 or 14 equal
     // units per CTA left the slowest 793 us against a mean of 685).  The first
-    // tail warp asks shortly before its last tile of a unit; every warp reads
+    // row warp asks shortly before its last tile of a unit; every warp reads
     // answer c when it is through with its unit c: a unit, or -1 for the end.
     // A grid of one wave has nothing to take over (asking would cost it 2 us).
     const bool one_wave = gridDim.x <= kSMs;
     auto next_unit_id = [&](int c) -> int { return one_wave ? -1 : read_answer(ctl, c, p.status, b.wait_ns, lane); };
     // Every role walks the CTA's units and their tiles in the same order.  g
-    // counts tiles over all units: tile g has S^T buffer g & 1, the phase
-    // (g >> 1) & 1 of the barriers of that parity, and blocks 5 g .. 5 g + 4 of
-    // the ring (slot n % 9, use n / 9).  v counts the units that have tiles.
+    // counts tiles over all units: tile g has slots 4 (g & 1) .. of the ring, tail
+    // columns g & 1, and the phase (g >> 1) & 1 of their barriers.  v counts the
+    // units that have tiles.
 
-    if (warp >= kFirstTail) {
-        // ---------------- rows and tail blocks.  These warps look up the cache
-        // row of every selected position, one tile ahead: its offset (in
-        // 128-byte lines; masked: ~0) for the latent warps, its scale for
-        // the softmax.  The tail block's slot frees last, so its rows wait in
-        // registers and only the stores lie between the free slot and the
-        // score product.  Rows without a tail have nothing to gather: the
-        // warps only pass the free slot on to the softmax, which puts P^T there.
-        const int r0 = 32 * (warp - kFirstTail);
-        const uint32_t lines = (uint32_t)width / 128u;
-        const uint8_t *src = p.codes + 4 * 128 + (lane & 7) * 16;
-        const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
+    if (warp < kRowWarps) {
+        // ---------------- rows.  Lane l looks up the cache row of position l of
+        // its warp's quarter, one tile ahead.  The latent codes of the quarter's
+        // rows go to the ring with asynchronous copies (a row's 128 bytes of a
+        // block are one cache line; masked rows are filled with zeros and read
+        // nothing); the tail codes go through registers to the rows' lanes of
+        // tensor memory, where the score products take them as their first
+        // operand; the scales go to the softmax.
+        const int r0 = 32 * warp;
+        const uint32_t tails = tmem + ((uint32_t)r0 << 16) + kColT;
+        const uint32_t d0 = smem_u32(ring) + r0 * 128 + sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
         bool go = true;
         int g = 0;
-        // (tile g - 1's offsets were the buffer's last use: tile g - 3's blocks
-        // had all landed before these warps got past the tail of tile g - 2)
-        auto publish = [&](int32_t row, int tile) {
-            ctl.off[tile % 3][r0 + lane] = row < 0 ? ~0u : (uint32_t)row * lines;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl.rows_full[tile % 3]));
-        };
         int asked = 0;                                   // answers requested
         auto request = [&](int c) {                      // answer c
             const int i = c & 1;
-            if (one_wave || warp != kFirstTail || lane != 0) return;
+            if (one_wave || warp != 0 || lane != 0) return;
             if (wait_bar(smem_u32(&ctl.next_empty[i]), ((uint32_t)(c >> 1) & 1u) ^ 1u, ctl, p.status, b.wait_ns)) {
                 clc_request(smem_u32(&ctl.next[i]), smem_u32(&ctl.next_full[i]));
                 asked = c + 1;
@@ -406,96 +399,141 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
         };
         for (int u = blockIdx.x, c = 0; u >= 0; u = next_unit_id(c++)) {
             const Unit w = load_unit(p, u, lane);
-            int32_t next_row = -1;
             if (w.n <= 2) request(c);
             __syncwarp();
-            if (w.n > 0) publish(next_row = row_of(p, w.t, w.seq, w.kv0, w.pos, w.tile_lo * kRows + r0 + lane), g);
-            for (int it = 0; go && it < w.n; ++it, ++g) {
-                const uint32_t n = (uint32_t)(kTileBlocks * g + 4), slot = n % kSlots, use = n / kSlots;
-                const int32_t my_row = next_row;
-                if (it == w.n - 2 && w.n > 2) request(c);
-                __syncwarp();
-                // The row's scale.  Any positive one will do; a row never
-                // written (scale 0) counts as zeros at the smallest.
-                float s = my_row < 0 ? 0.f : __ldg(p.scale + my_row);
-                uint4 v[8];
+            auto index = [&](int it) -> int32_t {            // the lane's entry of a tile
+                const int e = (w.tile_lo + it) * kRows + r0 + lane;
+                return it < w.n && e < p.k ? __ldg(p.idx + (int64_t)w.t * p.k + e) : -1;
+            };
+            auto row_at = [&](int32_t v) -> int32_t {        // its cache row: -1 for padding and out of range (flagged)
+                int64_t row = -1;
+                if (v >= 0 && v <= w.pos) row = cache_row(b, w.seq, w.kv0, v);
+                if (row >= b.cache_rows) row = -1;
+                if (row < 0 && v != -1) flag(p.status, DSA_DEV_BAD_INDEX);
+                return (int32_t)row;
+            };
+            int32_t row = -1;
+            float s = 0.f;
+            uint32_t v[32];
+            auto load = [&]() {                              // the row's scale and tail
+                s = row < 0 ? 0.f : __ldg(p.scale + row);
                 if (tail) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(p.codes + (int64_t)row * width + 4 * 128);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int32_t row = __shfl_sync(0xffffffffu, my_row, 4 * i + (lane >> 3));
-                        v[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (row >= 0) v[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * width));
+                        const uint4 x = row < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(src + i);
+                        v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
                     }
                 }
-                if (it + 1 < w.n) publish(next_row = row_of(p, w.t, w.seq, w.kv0, w.pos, (w.tile_lo + it + 1) * kRows + r0 + lane), g + 1);
-                if (my_row >= 0 && s < kMinScale) s = kMinScale;
-                const float2 rv = my_row < 0 ? make_float2(0.f, -INFINITY) : make_float2(s, log2f(s));
-                go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
-                if (!go || b.skip_copies) continue;
-                // (tile g - 1's first value product freed the slot, after the
-                // softmax of tile g - 2 had read these row values)
-                ctl.row[g & 1][r0 + lane] = rv;
-                if (tail) {
-                    uint8_t *dst = ring + slot * kBlockBytes + r0 * 128;
+            };
+            if (w.n > 0) {
+                row = row_at(index(0));
+                load();
+            }
+#pragma unroll 1
+            for (int it = 0; go && it < w.n; ++it, ++g) {
+                const int buf = g & 1, i3 = g % 3;
+                const uint32_t phase = (uint32_t)(g >> 1) & 1u;
+                if (it == w.n - 2 && w.n > 2) request(c);
+                __syncwarp();
+                const int32_t ahead = index(it + 1);
+                const bool whole = __all_sync(0xffffffffu, row >= 0);
+                const uint8_t *src[8];                       // lane's chunk of rows 4 i + lane / 8
+                uint32_t live = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4 *>(dst + ((d0 + (uint32_t)i * 512u) ^ ((uint32_t)(i & 1) << 6))) = v[i];
-                    fence_proxy_async_smem();
+                for (int i = 0; i < 8; ++i) {
+                    const int32_t x = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
+                    live |= (x >= 0 ? 1u : 0u) << i;
+                    src[i] = p.codes + (int64_t)max(x, 0) * width + (lane & 7) * 16;
+                }
+#pragma unroll
+                for (int j = 0; j < kTileBlocks; ++j) {
+                    const int slot = kTileBlocks * buf + j;
+                    go = go && __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), phase ^ 1u, ctl, p.status, b.wait_ns));
+                    if (go && !b.skip_copies) {
+                        const uint32_t dst = d0 + slot * kBlockBytes;
+                        if (whole) {                         // (few instructions a copy: they compete with the softmax)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) cp_async16((i & 1 ? dst ^ 64u : dst) + i * 512u, src[i] + j * 128);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                cp_async16_or_zero((i & 1 ? dst ^ 64u : dst) + i * 512u, src[i] + j * 128, live >> i & 1u ? 16u : 0u);
+                        }
+                    }
+                    cp_async_commit();
+                }
+                // Tile g - 2's tails have been read, so its scores had begun and
+                // tile g - 3's scales have served.
+                go = go && __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.t_empty[buf]), phase ^ 1u, ctl, p.status, b.wait_ns));
+                if (!go || b.skip_copies) continue;
+                // The row's scale.  Any positive one will do; a row never
+                // written (scale 0) counts as zeros at the smallest.
+                if (row >= 0 && s < kMinScale) s = kMinScale;
+                ctl.row[i3][r0 + lane] = row < 0 ? make_float2(0.f, -INFINITY) : make_float2(s, log2f(s));
+                if (tail) {
+                    tmem_st32(tails + 32 * buf, v);
+                    tmem_wait_st();
+                    tc_fence_before();
                 }
                 __syncwarp();
-                if (lane < 32 / kTailWarps) mbar_arrive(smem_u32(&ctl.full[slot]));
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&ctl.row_full[i3]));
+                    if (tail) mbar_arrive(smem_u32(&ctl.t_full[buf]));
+                }
+                auto landed = [&](int j) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctl.full[kTileBlocks * buf + j]));
+                };
+                cp_async_wait<3>(); landed(0);
+                cp_async_wait<2>(); landed(1);
+                cp_async_wait<1>(); landed(2);
+                cp_async_wait<0>(); landed(3);
+                if (it + 1 < w.n) {
+                    row = row_at(ahead);
+                    load();
+                }
             }
         }
+        cp_async_wait<0>();                                // (a wait may have given up behind copies)
         // (after a wait that gave up the last answer may still be on its way)
         if (asked) mbar_wait(smem_u32(&ctl.next_full[(asked - 1) & 1]), (uint32_t)((asked - 1) >> 1) & 1u, b.wait_ns);
         __syncwarp();
-    } else if (warp >= 2 && warp < kFirstSoftmax) {
-        // ---------------- latent blocks: block k = 4 g + j of the sequence of
-        // all tiles goes to warp k mod 2, which copies its 128 rows x 128 bytes
-        // asynchronously; masked rows become zeros.
-        const int lw = warp - 2;
-        const uint32_t d0 = sw128_offset((uint32_t)(lane >> 3), (uint32_t)(lane & 7));
+    } else if (warp >= kFirstSplit) {
+        // ---------------- half of the queries of every unit but the first, while
+        // the softmax warps finish the unit before
+        const int first = kSoftmaxWarps * kSoftmaxSplit + kOwnSplit * (warp - kFirstSplit);
         bool go = true;
-        int g = 0;
+        int v = 0;
         for (int u = blockIdx.x, c = 0; u >= 0; u = next_unit_id(c++)) {
-            const int n_tiles = load_unit(p, u, lane).n;
-            for (int it = 0; go && it < n_tiles; ++it, ++g) {
-                go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.rows_full[g % 3]), (uint32_t)(g / 3) & 1u, ctl, p.status, b.wait_ns));
-                if (!go) break;
-#pragma unroll 1
-                for (int j = lw; go && j < 4; j += kLatentWarps) {
-                    const uint32_t n = (uint32_t)(kTileBlocks * g + j), slot = n % kSlots, use = n / kSlots;
-                    go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.empty[slot]), (use & 1u) ^ 1u, ctl, p.status, b.wait_ns));
-                    if (!go || b.skip_copies) continue;
-                    const uint32_t dst = smem_u32(ring + slot * kBlockBytes) + d0;
-                    const uint8_t *src = p.codes + j * 128 + (lane & 7) * 16;
-                    const uint32_t *off = ctl.off[g % 3] + (lane >> 3);      // lane's chunk of rows 4 i + lane / 8
-#pragma unroll 1
-                    for (int i0 = 0; i0 < 32; i0 += 8) {
-                        uint32_t o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = off[4 * (i0 + i)];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            cp_async16_or_zero((dst + (uint32_t)(i0 + i) * 512u) ^ ((uint32_t)(i & 1) << 6),
-                                               src + (o[i] == ~0u ? 0u : (uint64_t)o[i] * 128u), o[i] == ~0u ? 0u : 16u);
-                    }
-                    cp_async_commit();
-                    cp_async_wait_all();
-                    fence_proxy_async_smem();
-                    mbar_arrive(smem_u32(&ctl.full[slot]));
+            const Unit w = load_unit(p, u, lane);
+            if (!go || w.n == 0) continue;
+            if (v > 0) {
+                const int64_t row0 = (int64_t)w.t * p.H + w.h0;
+                for (int h = lane + 32 * (warp - kFirstSplit); h < w.nh; h += 32 * kSplitWarps) {
+                    prefetch_l2_bulk(p.q_lat + (row0 + h) * D_L, 2 * D_L);
+                    if (tail) prefetch_l2_bulk(p.q_rope + (row0 + h) * D_R, 2 * D_R);
                 }
+                go = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.q_empty), (uint32_t)(v - 1) & 1u, ctl, p.status, b.wait_ns));
+                if (!go) continue;
+                split_queries(p.q_lat + row0 * D_L, tail ? p.q_rope + row0 * D_R : nullptr, w.nh, first, first + kOwnSplit,
+                              p.scale_log2, q_s, ctl.qs[v & 1], lane);
+                fence_proxy_async_smem();
+                __syncwarp();
             }
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full));
+            ++v;
         }
-    } else if (warp < 2) {
-        // ---------------- MMA issuers: warp 0 the score products, warp 1 the
+    } else if (warp >= kFirstIssuer) {
+        // ---------------- MMA issuers: warp 12 the score products, warp 13 the
         // value products, each block as its inputs arrive.  With one warp for
         // both, its waits for one stream held up the other and their
         // bookkeeping (200 to 400 cycles per block) lay between the products.
         // The tensor core takes the two streams' products as they come; they meet in no
         // accumulator and every reuse of memory goes through a barrier:
-        //  - scores of tile g overwrite those of tile g - 2, whose softmax was
-        //    over before its value product freed the slot of g's first block;
+        //  - scores of tile g overwrite those of tile g - 1 once its softmax has
+        //    read them;
         //  - the value product of tile g reads blocks its scores have read.
         // The whole warp runs the loop (uniform descriptors); one elected
         // lane issues.
@@ -505,60 +543,66 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
             return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
                    __all_sync(0xffffffffu, wait_bar(bar, parity, ctl, p.status, b.wait_ns));
         };
-        // Block j of tile g has number 5 g + j: slot and use follow from those
-        // of the tile's first block (base, use0).
-        auto slot_of = [&](int j, uint32_t base) -> uint32_t { return base + j - (base + j >= kSlots ? kSlots : 0u); };
-        uint32_t base = 0, use0 = 0;
         int g = 0, v = 0;
         bool go = true;
         for (int u = blockIdx.x, c = 0; u >= 0; u = next_unit_id(c++)) {
             const int n = load_unit(p, u, lane).n;
             if (!go || n == 0) continue;
-            if (warp == 0) {
+            if (warp == kFirstIssuer) {
                 const uint32_t id_s = idesc_f8(kRows, 2 * kHeads, false, false);
                 const uint32_t qa = smem_u32(q_s);
                 const uint64_t q0 = sdesc_sw128(qa, 16, 1024), qt = sdesc_sw64(qa + 4 * kQBlockBytes, 16, 512);
                 const uint32_t full0 = smem_u32(&ctl.full[0]);
                 go = wait(smem_u32(&ctl.q_full), (uint32_t)v & 1u);
                 for (int it = 0; go && it < n; ++it, ++g) {
-                    const uint32_t d_s = tmem + kColS + (g & 1) * 2 * kHeads;
+                    const uint32_t buf = g & 1, phase = (uint32_t)(g >> 1) & 1u, d_s = tmem + kColS;
+                    go = wait(smem_u32(&ctl.s_empty), buf ^ 1u);
+                    tc_fence_after();
+                    if (tail) {                          // K steps 2 and 3 (remainders) read the query again
+                        go = go && wait(smem_u32(&ctl.t_full[buf]), phase);
+                        tc_fence_after();
+                    }
+                    if (go && tail && elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_f8_ts(d_s, tmem + kColT + 32 * buf + 8 * ks, qt + (uint64_t)((ks & 1) * 2), id_s, ks ? 1u : 0u);
+                    }
+                    __syncwarp();
 #pragma unroll
                     for (int j = 0; j < kTileBlocks; ++j) {
-                        if (j == 4 && !tail) break;
-                        const uint32_t slot = slot_of(j, base);
-                        go = go && wait(full0 + 8 * slot, (use0 + (base + j >= kSlots ? 1u : 0u)) & 1u);
-                        if (j == 0) tc_fence_after();    // the accumulator's last readers
+                        const uint32_t slot = kTileBlocks * buf + j;
+                        go = go && wait(full0 + 8 * slot, phase);
                         if (go && elect_one()) {
                             const uint64_t ad = a0 + (uint64_t)(slot * (kBlockBytes >> 4));
-                            const uint64_t bd = j < 4 ? q0 + (uint64_t)(j * (kQBlockBytes >> 4)) : qt;
-                            const uint32_t b2 = j < 4 ? 4u : 0u;     // the tail's K steps 2, 3 (remainders) read the query again
+                            const uint64_t bd = q0 + (uint64_t)(j * (kQBlockBytes >> 4));
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)((ks & 1) * 2) + (ks & 2 ? b2 : 0u), id_s,
-                                        (j || ks) ? 1u : 0u);
-                            if (j == (tail ? 4 : 3)) umma_commit(smem_u32(&ctl.s_full[g & 1]));
+                                umma_f8(d_s, ad + (uint64_t)(ks * 2), bd + (uint64_t)(ks * 2), id_s, (tail || j || ks) ? 1u : 0u);
+                            // (with the first block, which every row warp lands after its wait
+                            // for tile g - 2's: no phase goes by unseen)
+                            if (j == 0) umma_commit(smem_u32(&ctl.t_empty[buf]));
+                            if (j == kTileBlocks - 1) {
+                                umma_commit(smem_u32(&ctl.s_full));
+                                if (it + 1 == n) umma_commit(smem_u32(&ctl.q_empty));
+                            }
                         }
                         __syncwarp();
                     }
-                    use0 += base + kTileBlocks >= kSlots ? 1u : 0u;
-                    base = slot_of(kTileBlocks, base);
                 }
             } else {
                 const uint32_t id_hi = idesc_f8(128, kHeads, true, true), id_lo = idesc_f8(128, kHeads, true, true, true);
-                const uint64_t p0 = sdesc_sw64(ra, 16, 512);
+                const uint64_t bd = sdesc_sw64(smem_u32(p_s), 16, 512);
                 const uint32_t empty0 = smem_u32(&ctl.empty[0]);
                 // the accumulator of the unit before has been read
                 if (v > 0) go = wait(smem_u32(&ctl.o_empty), (uint32_t)(v - 1) & 1u);
                 for (int it = 0; go && it < n; ++it, ++g) {
-                    const uint32_t pslot = slot_of(4, base);
-                    const uint64_t bd = p0 + (uint64_t)(pslot * (kBlockBytes >> 4));
                     const uint32_t acc0 = it > 0 ? 1u : 0u;
-                    go = wait(smem_u32(&ctl.p_full[g & 1]), (uint32_t)(g >> 1) & 1u);
+                    go = wait(smem_u32(&ctl.p_full), (uint32_t)g & 1u);
                     tc_fence_after();
                     if (go && elect_one()) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const uint32_t slot = slot_of(c, base);
+                            const uint32_t slot = kTileBlocks * (g & 1) + c;
                             const uint64_t ad = a0 + (uint64_t)(slot * (kBlockBytes >> 4));
 #pragma unroll
                             for (int piece = 0; piece < 2; ++piece)
@@ -569,12 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                                             (piece || ks) ? 1u : acc0);
                             umma_commit(empty0 + 8 * slot);
                         }
-                        // a unit's last P^T slot goes to the epilogue, which frees it
-                        if (it + 1 < n) umma_commit(empty0 + 8 * pslot);
                         umma_commit(smem_u32(&ctl.o_full[g & 1]));
                     }
                     __syncwarp();
-                    base = slot_of(kTileBlocks, base);
                 }
             }
             ++v;
@@ -611,22 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                 if (p.lse && tx < w.nh) p.lse[row + tx] = -INFINITY;
             }
         };
-        // The unit's queries as two pieces, eight heads per warp.
-        auto stage_queries = [&](const Unit &w, int parity) {
+        // `heads` heads per warp of the unit's queries as two pieces.
+        auto stage_queries = [&](const Unit &w, int parity, int heads) {
             const int64_t row0 = (int64_t)w.t * p.H + w.h0;
-            split_queries(p.q_lat + row0 * D_L, tail ? p.q_rope + row0 * D_R : nullptr, w.nh, sw * (kHeads / kSoftmaxWarps),
-                          p.scale_log2, q_s, ctl.qs[parity], lane);
+            split_queries(p.q_lat + row0 * D_L, tail ? p.q_rope + row0 * D_R : nullptr, w.nh, sw * heads,
+                          (sw + 1) * heads, p.scale_log2, q_s, ctl.qs[parity], lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.q_full));
-        };
-        // Asks L2 for the warp's heads of a unit.
-        auto prefetch_queries = [&](const Unit &w) {
-            const int h = sw * (kHeads / kSoftmaxWarps) + lane;
-            if (lane < kHeads / kSoftmaxWarps && h < w.nh) {
-                prefetch_l2_bulk(p.q_lat + ((int64_t)w.t * p.H + w.h0 + h) * D_L, 2 * D_L);
-                if (tail) prefetch_l2_bulk(p.q_rope + ((int64_t)w.t * p.H + w.h0 + h) * D_R, 2 * D_R);
-            }
         };
         int claims = 0;
         // Puts unit u into the warp's slot (n = -1: there is none).
@@ -638,19 +671,18 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
             __syncwarp();
         };
         // Gives empty units their outputs until one with tiles, or the end, is
-        // in the slot; then splits its queries.  Only between units: the
-        // answers asked for here need every warp to be through with the unit
-        // before.
-        auto skip_empty = [&](int parity) {
+        // in the slot.  Only between units: the answers asked for here need
+        // every warp to be through with the unit before.
+        auto skip_empty = [&](int parity, int heads) {
             while (ctl.unit[sw][parity].n == 0) {
                 write_empty(ctl.unit[sw][parity]);
                 __syncwarp();
                 set_unit(next_unit_id(claims++), parity);
             }
-            if (ctl.unit[sw][parity].n > 0) stage_queries(ctl.unit[sw][parity], parity);
+            if (ctl.unit[sw][parity].n > 0) stage_queries(ctl.unit[sw][parity], parity, heads);
         };
         set_unit(blockIdx.x, 0);
-        skip_empty(0);
+        skip_empty(0, kHeads / kSoftmaxWarps);
         // Every softmax thread runs the same sequence of named barriers whatever
         // happens; `alive` (warp-uniform) only gates tensor-memory and shared
         // memory work after a bounded wait gave up.
@@ -670,24 +702,17 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
             const float *qs_u = ctl.qs[v & 1] + hb;
             if (alive) alive = wait_bar(smem_u32(&ctl.q_full), (uint32_t)v & 1u, ctl, p.status, b.wait_ns);   // everyone's qs
             for (int it = 0; it < n_tiles; ++it, ++g) {
-                const int buf = g & 1;
-                if (it + 1 == n_tiles) {
-                    set_unit(next_unit_id(claims++), (v + 1) & 1);
-                    if (ctl.unit[sw][(v + 1) & 1].n > 0) prefetch_queries(ctl.unit[sw][(v + 1) & 1]);
-                }
-                // the row values and, without a tail, the free slot of P^T: no
-                // score product has waited for it
-                const uint32_t pn = (uint32_t)(kTileBlocks * g + 4), pslot = pn % kSlots;
-                if (alive) alive = wait_bar(smem_u32(&ctl.full[pslot]), (pn / kSlots) & 1u, ctl, p.status, b.wait_ns);
-                const float2 rv = ctl.row[buf][r];         // a masked row's products are 0: u = -inf
+                if (it + 1 == n_tiles) set_unit(next_unit_id(claims++), (v + 1) & 1);
+                if (alive) alive = wait_bar(smem_u32(&ctl.row_full[g % 3]), (uint32_t)(g / 3) & 1u, ctl, p.status, b.wait_ns);
+                const float2 rv = ctl.row[g % 3][r];       // a masked row's products are 0: u = -inf
                 const float irs = rv.x == 0.f ? 0.f : 1.f / rv.x;
                 const uint64_t rs2 = f2(rv.x, rv.x), ef2 = f2(rv.y, rv.y), irs2 = f2(irs, irs);
-                if (alive) alive = wait_bar(smem_u32(&ctl.s_full[buf]), (uint32_t)(g >> 1) & 1u, ctl, p.status, b.wait_ns);
+                if (alive) alive = wait_bar(smem_u32(&ctl.s_full), (uint32_t)g & 1u, ctl, p.status, b.wait_ns);
                 alive = __all_sync(0xffffffffu, alive);
                 float x[kPartHeads], top = -INFINITY;      // u - m
                 if (alive) {
                     tc_fence_after();
-                    const uint32_t a = tmem + lane_addr + kColS + buf * 2 * kHeads + hb;
+                    const uint32_t a = tmem + lane_addr + kColS + hb;
 uint32_t a16[2][16], b16[2][16];
                     tmem_ld16(a, a16[0]);
                     tmem_ld16(a + kHeads, b16[0]);
@@ -696,7 +721,12 @@ uint32_t a16[2][16], b16[2][16];
                     tmem_ld16(a + kHeads + 16, b16[1]);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        if (half) tmem_wait_ld(a16[1], b16[1]);
+                        if (half) {
+                            tmem_wait_ld(a16[1], b16[1]);
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty));
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float4 q4 = *reinterpret_cast<const float4 *>(qs_u + 16 * half + 4 * i);
@@ -751,7 +781,6 @@ uint32_t a16[2][16], b16[2][16];
                     }
                 }
                 // the weights' two pieces, 16 heads (16 bytes) at a time
-                uint8_t *pb = ring + pslot * kBlockBytes;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t hi[4], lo[4];
@@ -767,18 +796,19 @@ uint32_t a16[2][16], b16[2][16];
                         hi[i] = ha | hc << 16;
                         lo[i] = e5m2x2(__hsub2(a, e4m3x2_to_half2(ha))) | e5m2x2(__hsub2(c, e4m3x2_to_half2(hc))) << 16;
                     }
+                    if (half == 0 && g > 0) {              // P^T of tile g - 1 has been read
+                        if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(g - 1) & 1]), (uint32_t)((g - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
+                        alive = __all_sync(0xffffffffu, alive);
+                    }
                     if (alive) {
                         const uint32_t o = sw64_offset((uint32_t)r, (uint32_t)(2 * part + half));
-                        *reinterpret_cast<uint4 *>(pb + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(pb + kPieceBytes + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4 *>(p_s + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(p_s + kPieceBytes + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
                 if (moved && it > 0) {
-                    // Columns of O^T whose reference moved, once the previous
-                    // tile's value product has landed: one by one while they
-                    // are few, else all.
-                    if (alive) alive = wait_bar(smem_u32(&ctl.o_full[(g - 1) & 1]), (uint32_t)((g - 1) >> 1) & 1u, ctl, p.status, b.wait_ns);
-                    alive = __all_sync(0xffffffffu, alive);
+                    // Columns of O^T whose reference moved: one by one while
+                    // they are few, else all.
                     if (alive) {
                         tc_fence_after();
                         const uint32_t o = tmem + lane_addr + kColO + hb;
@@ -813,13 +843,8 @@ uint32_t a16[2][16], b16[2][16];
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full[buf]));
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.p_full));
             }
-            // ---- While the last value product runs: the next unit's queries
-            // (the score products have read this one's).
-            const Unit &wn = ctl.unit[sw][(v + 1) & 1];
-            const bool staged = wn.n > 0;
-            if (staged) stage_queries(wn, (v + 1) & 1);
             // ---- outputs: the row sums behind the last value product as well
             const int gl = g - 1;                          // the unit's last tile
             float lrow[kPartHeads];
@@ -837,15 +862,18 @@ uint32_t a16[2][16], b16[2][16];
             const float l = ctl.red[0][hl] + ctl.red[1][hl] + ctl.red[2][hl] + ctl.red[3][hl];
             ma[lane] = p.n_split > 1 ? 1.f : fresh ? 0.f : 1.f / l;
             __syncwarp();
+            // ---- While the last value product runs: its share of the next unit's
+            // queries (the score products have read this one's).
+            const bool staged = ctl.unit[sw][(v + 1) & 1].n > 0;
+            if (staged) stage_queries(ctl.unit[sw][(v + 1) & 1], (v + 1) & 1, kSoftmaxSplit);
             if (alive) alive = wait_bar(smem_u32(&ctl.o_full[gl & 1]), (uint32_t)(gl >> 1) & 1u, ctl, p.status, b.wait_ns);
             alive = __all_sync(0xffffffffu, alive);
             const int64_t row0 = (int64_t)w.t * p.H + w.h0;
             const int64_t part0 = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
-            const uint32_t eslot = (uint32_t)(kTileBlocks * gl + 4) % kSlots;
             if (alive) {
                 // Thread (quarter, lane) holds output dim 128 c + 32 quarter +
                 // lane of the part's heads.  16-bit results go through 2 KB of
-                // the tile's P^T slot per warp, head pairs side by side, and leave
+                // P^T's place per warp, head pairs side by side, and leave
                 // as 16 bytes (eight dims) per lane; float32 ones go straight out.
                 tc_fence_after();
                 const int live = (p.n_split > 1 ? kHeads : w.nh) - hb;     // heads of the part that are stored
@@ -861,7 +889,7 @@ uint32_t a16[2][16], b16[2][16];
                 if (p.n_split > 1 || p.out_bf16) {
                     uint16_t *dst = (p.n_split > 1 ? p.part_o + part0 * D_L : static_cast<uint16_t *>(p.out) + row0 * D_L) +
                                     (int64_t)hb * D_L + quarter * 32;
-                    uint32_t *st = reinterpret_cast<uint32_t *>(ring + eslot * kBlockBytes + sw * 2048);
+                    uint32_t *st = reinterpret_cast<uint32_t *>(p_s + sw * 2048);
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         uint32_t c32[32];
@@ -918,8 +946,7 @@ uint32_t a16[2][16], b16[2][16];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.o_empty));
             named_barrier(1, kSoftmaxThreads);
-            if (tx == 0) mbar_arrive(smem_u32(&ctl.empty[eslot]));
-            if (!staged) skip_empty((v + 1) & 1);
+            if (!staged) skip_empty((v + 1) & 1, kSoftmaxSplit);
             ++v;
         }
     }
@@ -960,8 +987,8 @@ cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint
     p.tiles_per_cta = a.tiles_per_cta;
     p.n_split = a.n_split;
     p.n_tiles = (a.k + kRows - 1) / kRows;
-    const size_t smem = 1024 + kSlots * kBlockBytes + kQBytes + sizeof(Ctl);
-    static_assert(1024 + kSlots * kBlockBytes + kQBytes + sizeof(Ctl) <= 232448, "one CTA's shared memory");
+    const size_t smem = 1024 + kRingBytes + kQBytes + sizeof(Ctl);
+    static_assert(1024 + kRingBytes + kQBytes + sizeof(Ctl) <= 232448, "one CTA's shared memory");
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(sparse_attn_q8_kernel), 11, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)b.T * p.groups * a.n_split;

@@ -415,6 +415,9 @@ ATTN = [
     ([700, 300], [130, 100], 0, 16, 384, True, "f32"),       # prefill: one CTA walks a token's tiles
     ([700, 300], [130, 100], 1, 65, 300, False, "bf16"),
     ([2100] * 20, [1] * 20, 64, 33, 2051, False, "bf16"),
+    ([700, 300], [290, 200], 0, 70, 100, True, "bf16"),      # units of one tile, several per CTA
+    ([700, 300], [290, 200], 4, 64, 128, False, "f32"),
+    ([900, 300], [400, 200], 0, 64, 256, True, "f32"),       # of two
 ]
 
 
