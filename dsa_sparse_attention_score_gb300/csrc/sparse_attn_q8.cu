@@ -155,7 +155,8 @@ struct Ctl {
     alignas(16) uint4 next[2];          // the answers
     alignas(16) float qs[2][kHeads];   // by unit parity: 2^e of the head's query times scale_log2
     float2 row[3][kRows];    // by tile mod 3: a row's scale (0: masked) and its log2
-    float red[4][kHeads];    // a tile's maxima by lane quarter; the row sums at the end
+    float red[4][kHeads];    // a tile's maxima by lane quarter
+    float sum[4][kHeads];    // a unit's row sums
     alignas(16) float ma[kSoftmaxWarps][2 * kPartHeads];   // each warp's -m, and how far m moved
     Unit unit[kSoftmaxWarps][2];        // each warp's current and next unit, by unit parity
 };
@@ -855,11 +856,10 @@ uint32_t a16[2][16], b16[2][16];
                 lrow[2 * h + 1] = d.y;
             }
             const float lsum = warp_sum_32(lrow, lane);
-            named_barrier(2 + part, 128);                  // red may still be read
-            ctl.red[quarter][hb + lane] = lsum;
+            ctl.sum[quarter][hb + lane] = lsum;
             named_barrier(2 + part, 128);
             const int hl = hb + lane;
-            const float l = ctl.red[0][hl] + ctl.red[1][hl] + ctl.red[2][hl] + ctl.red[3][hl];
+            const float l = ctl.sum[0][hl] + ctl.sum[1][hl] + ctl.sum[2][hl] + ctl.sum[3][hl];
             ma[lane] = p.n_split > 1 ? 1.f : fresh ? 0.f : 1.f / l;
             __syncwarp();
             // ---- While the last value product runs: its share of the next unit's
@@ -872,9 +872,9 @@ uint32_t a16[2][16], b16[2][16];
             const int64_t part0 = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
             if (alive) {
                 // Thread (quarter, lane) holds output dim 128 c + 32 quarter +
-                // lane of the part's heads.  16-bit results go through 2 KB of
-                // P^T's place per warp, head pairs side by side, and leave
-                // as 16 bytes (eight dims) per lane; float32 ones go straight out.
+                // lane of the part's heads.  Of 16-bit results neighbouring lanes
+                // swap halves, so that the even one stores two dims of head 2 i
+                // and the odd one of head 2 i + 1.
                 tc_fence_after();
                 const int live = (p.n_split > 1 ? kHeads : w.nh) - hb;     // heads of the part that are stored
                 const uint32_t o_t = tmem + lane_addr + kColO + hb;
@@ -888,36 +888,20 @@ uint32_t a16[2][16], b16[2][16];
                 }
                 if (p.n_split > 1 || p.out_bf16) {
                     uint16_t *dst = (p.n_split > 1 ? p.part_o + part0 * D_L : static_cast<uint16_t *>(p.out) + row0 * D_L) +
-                                    (int64_t)hb * D_L + quarter * 32;
-                    uint32_t *st = reinterpret_cast<uint32_t *>(p_s + sw * 2048);
-#pragma unroll 1
+                                    (int64_t)(hb + (lane & 1)) * D_L + quarter * 32 + (lane & 30);
+                    const uint32_t take = lane & 1 ? 0x3276u : 0x5410u;
+#pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t c32[32];
                         tmem_ld32(o_t + c * kHeads, c32);
                         tmem_wait_ld(c32);
-                        __syncwarp();                      // the block before has been read
 #pragma unroll
                         for (int i = 0; i < kPartHeads / 2; ++i) {
-                            const __nv_bfloat162 o2 =
-                                __floats2bfloat162_rn(__uint_as_float(c32[2 * i]) * f[2 * i], __uint_as_float(c32[2 * i + 1]) * f[2 * i + 1]);
-                            st[32 * i + lane] = *reinterpret_cast<const uint32_t *>(&o2);
-                        }
-                        __syncwarp();
-                        // lane: heads 2 i and 2 i + 1 with i = lane / 4 (+ 8), dims 8 (lane % 4) ..
-                        uint4 e[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const uint4 *>(st + (i >> 1) * 256 + 8 * lane + 4 * (i & 1));
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 e0 = e[2 * i], e1 = e[2 * i + 1];
-                            const int h = 16 * i + 2 * (lane >> 2);
-                            uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)h * D_L + c * 128 + 8 * (lane & 3));
-                            if (h < live)
-                                to[0] = make_uint4(__byte_perm(e0.x, e0.y, 0x5410), __byte_perm(e0.z, e0.w, 0x5410),
-                                                   __byte_perm(e1.x, e1.y, 0x5410), __byte_perm(e1.z, e1.w, 0x5410));
-                            if (h + 1 < live)
-                                to[D_L / 8] = make_uint4(__byte_perm(e0.x, e0.y, 0x7632), __byte_perm(e0.z, e0.w, 0x7632),
-                                                         __byte_perm(e1.x, e1.y, 0x7632), __byte_perm(e1.z, e1.w, 0x7632));
+                            const __nv_bfloat162 o2 = __floats2bfloat162_rn(__uint_as_float(c32[2 * i]) * f[2 * i],
+                                                                            __uint_as_float(c32[2 * i + 1]) * f[2 * i + 1]);
+                            const uint32_t mine = *reinterpret_cast<const uint32_t *>(&o2);
+                            const uint32_t both = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), take);
+                            if (2 * i + (lane & 1) < live) *reinterpret_cast<uint32_t *>(dst + (int64_t)(2 * i) * D_L + c * 128) = both;
                         }
                     }
                 } else {
@@ -945,7 +929,6 @@ uint32_t a16[2][16], b16[2][16];
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.o_empty));
-            named_barrier(1, kSoftmaxThreads);
             if (!staged) skip_empty((v + 1) & 1, kSoftmaxSplit);
             ++v;
         }
