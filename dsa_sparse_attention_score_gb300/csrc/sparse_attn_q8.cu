@@ -48,11 +48,11 @@
 // the question whether any weight does.
 //
 // Measured, one call after the other over three sets of inputs, 64 heads: a
-// prefill chunk of 2048 tokens over 2048 rows each 657 us (889 TFLOP/s counted as
-// for bf16, 46% of what the tensor cores do on one large bf16 product); a decode
-// step of 8 sequences over 2048 rows 17.2 us and of 32 sequences 30.3 us, the join
+// prefill chunk of 2048 tokens over 2048 rows each 634 us (921 TFLOP/s counted as
+// for bf16, 48% of what the tensor cores do on one large bf16 product); a decode
+// step of 8 sequences over 2048 rows 16.5 us and of 32 sequences 29.4 us, the join
 // of the splits included (3.5 us).  What bounds it:
-//  - A tile takes about 4600 cycles, and a unit 16 of them and some 13000 for
+//  - A tile takes about 4600 cycles, and a unit 16 of them and some 11000 for
 //    its outputs and the next one's queries.  The products read their operands
 //    from shared memory at its full rate, S^T 144 KB and O^T 192 KB a tile, and
 //    with the gather's 64 KB and P^T's 16 KB that is 3300 cycles at 128 bytes
@@ -61,10 +61,10 @@
 //    softmax (2700); the two chains take turns on the tensor core.
 //  - With the tail as a fifth block, whose slot P^T took over, the next tile's
 //    scores waited for the value product: 5000 cycles, a ragged decode of 32 in
-//    33.2 instead of 30.3 us.
+//    33.2 us where the other form took 30.3.
 //  - A decode step's CTA runs one or two tiles: 4000 cycles to the queries' two
 //    pieces, 1000 to the first scores, 3000 of softmax, 2000 of value products,
-//    5000 of epilogue, each once, with the code coming in from L2.
+//    4000 of outputs, each once, with the code coming in from L2.
 #include <algorithm>
 #include <cstddef>
 
