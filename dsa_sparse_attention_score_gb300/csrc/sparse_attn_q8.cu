@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                 if (alive) {
                     tc_fence_after();
                     const uint32_t a = tmem + lane_addr + kColS + hb;
-uint32_t a16[2][16], b16[2][16];
+                    uint32_t a16[2][16], b16[2][16];
                     tmem_ld16(a, a16[0]);
                     tmem_ld16(a + kHeads, b16[0]);
                     tmem_wait_ld(a16[0], b16[0]);

@@ -787,3 +787,21 @@ def test_calls_in_a_row_see_what_the_one_before_wrote(dsa, torch):
     torch.cuda.synchronize()
     check()
     assert dsa.dsa_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_attention_shapes_drawn(dsa, torch, seed):
+    """Lengths, new tokens, pages, heads, selections, masks and orders drawn at random."""
+    rng = np.random.default_rng(900 + seed)
+    for _ in range(12):
+        B = int(rng.choice([1, 2, 5]))
+        lens = [int(n) for n in rng.choice([1, 2, 127, 128, 129, 500, 1500], B)]
+        per = [min(n, int(rng.choice([1, 3, 130, 260]))) for n in lens]
+        k, H = int(rng.choice([1, 100, 128, 129, 256, 385, 1000])), int(rng.choice([1, 8, 33, 64, 65, 128]))
+        s = Seqs(dsa, torch, lens, per, int(rng.choice([0, 1, 16, 64])), seed=int(rng.integers(1000)))
+        idx = selections(s, k, seed=int(rng.integers(1000)))
+        idx[rng.random(idx.shape) < rng.choice([0.0, 0.3, 0.95])] = -1
+        idx = np.ascontiguousarray(idx[:, rng.permutation(k)])
+        T = len(s.pos)
+        attend(dsa, torch, s, H, k, idx, bool(rng.random() < 0.6), out_dt=["f32", "bf16"][int(rng.integers(2))],
+               check=sorted({0, T - 1, int(rng.integers(T))}))
