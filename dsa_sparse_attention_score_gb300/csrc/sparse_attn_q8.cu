@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                 if (row >= 0 && s < kMinScale) s = kMinScale;
                 ctl.row[i3][r0 + lane] = row < 0 ? make_float2(0.f, -INFINITY) : make_float2(s, log2f(s));
                 if (tail) {
+                    tc_fence_after();                    // behind the products that read tile g - 2's tails
                     tmem_st32(tails + 32 * buf, v);
                     tmem_wait_st();
                     tc_fence_before();

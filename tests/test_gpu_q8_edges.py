@@ -1,0 +1,45 @@
+"""The 8-bit attention, its cache and the rotation where they can go wrong:
+tails alone deciding the scores, rows and queries that are not finite, far
+scales, the spread of the errors; against float64 (tests/_q8_ref.py, which
+derives the bounds that are not derived here)."""
+import numpy as np
+import pytest
+
+import _q8_ref as R
+from test_gpu_q8 import Seqs, dsa, f64, fill_cache, gen, selections, torch  # noqa: F401  (two fixtures among them)
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(dsa, torch, s, q, qr, codes, scale, idx, sm, out_dt=None):
+    """(out, lse) of one call, its status checked."""
+    T, H, k = q.shape[0], q.shape[1], idx.shape[1]
+    ws = dsa.workspace(dsa.DSA_OP_SPARSE_ATTN, s.batch, H=H, k=k)
+    out = torch.full((T, H, 512), -7.0, dtype=out_dt or torch.float32, device="cuda")
+    lse = torch.full((T, H), -7.0, device="cuda")
+    ix = torch.from_numpy(idx).cuda() if isinstance(idx, np.ndarray) else idx
+    dsa.dsa_sparse_mla_attn_q8(q, qr, codes, scale, s.batch, ix, sm, out, lse, ws, *s.paging)
+    assert dsa.dsa_read_device_status(ws) == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("lens,per,k", [([2300], [160], 2048), ([1500, 900], [200, 140], 700)])
+def test_scores_of_the_tails_alone(dsa, torch, lens, per, k):
+    """Latent queries of zero: every score is its row's tail, whose place in
+    tensor memory is written again two tiles later (6 to 16 tiles a token,
+    several tokens a CTA)."""
+    s = Seqs(dsa, torch, lens, per)
+    codes, scale = fill_cache(dsa, torch, s, True, 0.0)
+    T, H, sm = s.batch.T, 64, 0.5
+    q = torch.zeros(T, H, 512, dtype=torch.bfloat16, device="cuda")
+    qr = torch.randn(T, H, 64, generator=gen(torch, 3), device="cuda").to(torch.bfloat16)
+    idx = selections(s, k)
+    first = attend(dsa, torch, s, q, qr, codes, scale, idx, sm)
+    c, sc = codes.cpu().numpy(), f64(scale)
+    for t in range(0, T, 23):
+        rows = np.asarray(s.row(int(s.seq[t]), idx[t][idx[t] >= 0]))
+        ref, rl, tol, tl = R.attention(f64(q[t]), f64(qr[t]), c, sc, rows, sm)
+        assert np.all(np.abs(f64(first[0][t]) - ref) <= tol) and np.all(np.abs(f64(first[1][t]) - rl) <= tl)
+    for _ in range(20):
+        again = attend(dsa, torch, s, q, qr, codes, scale, idx, sm)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
