@@ -730,6 +730,19 @@ static dsa_status_t check_rope(const dsa_rope_t *r) {
     return DSA_OK;
 }
 
+// Do two sets of rows of dim values, n1 by n2 of them at strides s1 and s2, the
+// second set `gap` values behind the first, share no value?  So they do where
+// the second's rows lie between the first's (gap + dim within the smaller
+// stride) or behind a whole run of them, and the run of both ends before the
+// next run begins.
+static bool slices_apart(int64_t gap, int64_t dim, int64_t n1, int64_t s1, int64_t n2, int64_t s2) {
+    const bool first = n2 == 1 || (n1 > 1 && s1 <= s2);              // the first axis runs inside
+    const int64_t n_in = first ? n1 : n2, s_in = first ? s1 : s2, n_out = first ? n2 : n1, s_out = first ? s2 : s1;
+    const int64_t run = (n_in - 1) * s_in + dim;                     // of one of the sets
+    if (n_out > 1 && gap + run > s_out) return false;
+    return gap >= run || (gap >= dim && n_in > 1 && gap + dim <= s_in);
+}
+
 dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y, int64_t y_token_stride,
                       int64_t y_head_stride, int dtype, int n_tokens, int heads, int head_dim, int rot_off,
                       const int32_t *pos, const dsa_rope_t *rope, int inverse, cudaStream_t stream) {
@@ -744,7 +757,6 @@ dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stri
         std::max(std::max(x_token_stride, x_head_stride), std::max(y_token_stride, y_head_stride)) > kFar / n_tokens)
         return DSA_ERR_INVALID_ARGUMENT;
     const int64_t e = dtype_bytes(dtype);
-    if (!aligned(x, e) || !aligned(y, e) || !aligned(pos, 4)) return DSA_ERR_MISALIGNED;
     // rows of y apart from one another: heads inside a token, or tokens inside a head
     const int64_t head_span = (heads - 1) * y_head_stride + head_dim, token_span = (n_tokens - 1) * y_token_stride + head_dim;
     const bool heads_apart = heads == 1 || y_head_stride >= head_dim, tokens_apart = n_tokens == 1 || y_token_stride >= head_dim;
@@ -758,16 +770,12 @@ dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stri
         const uintptr_t xe = xb + (uintptr_t)(((n_tokens - 1) * x_token_stride + (heads - 1) * x_head_stride + head_dim) * e);
         const uintptr_t ye = yb + (uintptr_t)(((n_tokens - 1) * y_token_stride + (heads - 1) * y_head_stride + head_dim) * e);
         if (xb < ye && yb < xe) {
-            // disjoint slices of the same heads: the smaller of the strides
-            // in use leaves room for both
-            const int64_t gap = (int64_t)(xb > yb ? xb - yb : yb - xb);
-            int64_t step = INT64_MAX;
-            if (heads > 1) step = std::min(step, y_head_stride);
-            if (n_tokens > 1) step = std::min(step, y_token_stride);
-            if (!same_strides || gap < head_dim * e || step == INT64_MAX || gap + head_dim * e > step * e)
+            const int64_t gap = (int64_t)(xb > yb ? xb - yb : yb - xb) / e;
+            if (!same_strides || !slices_apart(gap, head_dim, n_tokens, y_token_stride, heads, y_head_stride))
                 return DSA_ERR_INVALID_ARGUMENT;
         }
     }
+    if (!aligned(x, e) || !aligned(y, e) || !aligned(pos, 4)) return DSA_ERR_MISALIGNED;
     RopeLaunch a;
     a.x = x;
     a.y = y;

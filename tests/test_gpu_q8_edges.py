@@ -43,3 +43,24 @@ def test_scores_of_the_tails_alone(dsa, torch, lens, per, k):
     for _ in range(20):
         again = attend(dsa, torch, s, q, qr, codes, scale, idx, sm)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_rotation_between_slices_of_one_buffer(dsa, torch, heads_first):
+    """Parts of the same heads and groups of heads, packed as tightly as they are taken."""
+    T, H = 5, 6
+    rope = dsa.Rope.make(64, 1e4, False)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 1000
+    for parts in (True, False):
+        shape = (T, H, 2, 64) if parts else (T, 2, H, 64)
+        buf = torch.randn(shape, generator=gen(torch, 4), device="cuda").to(torch.bfloat16)
+        if heads_first:
+            buf = torch.randn((H,) + ((T, 2, 64) if parts else (2, T, 64)), generator=gen(torch, 4), device="cuda").to(torch.bfloat16)
+        a, b = (buf.select(2 if parts else 1, i) for i in (0, 1))
+        if heads_first:
+            a, b = a.transpose(0, 1), b.transpose(0, 1)
+        for x, y in ((a, b), (b, a)):
+            keep, want = x.clone(), torch.empty_like(x, memory_format=torch.contiguous_format)
+            dsa.dsa_rope(keep, pos, rope, want)
+            dsa.dsa_rope(x, pos, rope, y)
+            assert torch.equal(y, want) and torch.equal(x, keep)
