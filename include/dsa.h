@@ -447,8 +447,9 @@ dsa_status_t dsa_rope_frequencies(int rot_dim, double base, int scaling, double 
  *   pos    device int32 [n_tokens], any value
  * Addresses and extents that are multiples of 16 bytes move 16 bytes at a time.
  * Errors: DSA_ERR_INVALID_ARGUMENT for null pointers, sizes below 1, a
- * rotated part outside the head, an odd rot_dim, negative strides, rows of y
- * that overlap one another, or memory shared by x and y as above;
+ * rotated part outside the head, an odd rot_dim, negative strides, strides
+ * times tokens or heads above 2^40 values, rows of y that overlap one another,
+ * or memory shared by x and y as above;
  * DSA_ERR_UNSUPPORTED for rot_dim > 512 or heads * head_dim > 2^24;
  * DSA_ERR_MISALIGNED for pointers not aligned to their elements.
  */

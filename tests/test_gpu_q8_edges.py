@@ -64,3 +64,15 @@ def test_rotation_between_slices_of_one_buffer(dsa, torch, heads_first):
             dsa.dsa_rope(keep, pos, rope, want)
             dsa.dsa_rope(x, pos, rope, y)
             assert torch.equal(y, want) and torch.equal(x, keep)
+
+
+def test_rotation_of_a_long_head_major_view(dsa, torch):
+    """Heads 131072 tokens of 128 values apart, in place: the bits of the packed call."""
+    T, H, D = 131072, 2, 128
+    x = torch.randn(H, T, D, generator=gen(torch, 6), device="cuda").to(torch.bfloat16).transpose(0, 1)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    rope = dsa.Rope.make(64, 1e6, True, "yarn", 4.0, 32768)
+    want = torch.empty(T, H, D, dtype=x.dtype, device="cuda")
+    dsa.dsa_rope(x.contiguous(), pos, rope, want, 64)
+    dsa.dsa_rope(x, pos, rope, x, 64)
+    assert torch.equal(x, want)

@@ -72,3 +72,18 @@ def test_what_is_taken_shares_nothing(L):
                     x = cells(T, H, D, *other)
                     assert x == y or not set(x) & set(y), (T, H, D, other, st, sh, gap)
     assert n > 500
+
+
+def test_strides_as_far_as_a_head_major_view_has_them(L):
+    # [H, T, D] passed as [T, H, D]: head stride T * D
+    assert taken(L, 131072, 32, 128, 128, 131072 * 128, 128, 131072 * 128, 32 * 131072 * 128)
+    assert taken(L, 131072, 32, 128, 128, 131072 * 128, 128, 131072 * 128, 0)
+    assert taken(L, 1 << 20, 8, 64, 8 * 64, 64, 64, 64 << 20, 1 << 34)
+    # an axis may reach over 2^40 values, no further
+    far = 1 << 40
+    assert taken(L, 4, 2, 64, 64, far // 2, 64, 256, 1 << 42) and not taken(L, 4, 2, 64, 64, far // 2 + 1, 64, 256, 1 << 42)
+    assert taken(L, 4, 2, 64, 64, 256, 64, far // 2, 1 << 42) and not taken(L, 4, 2, 64, 64, 256, 64, far // 2 + 1, 1 << 42)
+    assert taken(L, 4, 2, 64, far // 4, 64, 128, 64, 1 << 42) and not taken(L, 4, 2, 64, far // 4 + 1, 64, 128, 64, 1 << 42)
+    assert taken(L, 4, 2, 64, 128, 64, far // 4, 64, 1 << 42) and not taken(L, 4, 2, 64, 128, 64, far // 4 + 1, 64, 1 << 42)
+    # heads times stride beyond 64 bits is refused, not wrapped around
+    assert not taken(L, 1, 1 << 23, 2, 0, far, 0, 2, 1 << 42) and not taken(L, 1, 1 << 23, 2, 0, 2, 0, far, 1 << 42)
