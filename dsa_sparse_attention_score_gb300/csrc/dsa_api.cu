@@ -753,6 +753,8 @@ dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stri
     if ((int64_t)rot_off + rope->rot_dim > head_dim) return DSA_ERR_INVALID_ARGUMENT;
     if ((int64_t)heads * head_dim > (int64_t(1) << 24)) return DSA_ERR_UNSUPPORTED;
     if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0) return DSA_ERR_INVALID_ARGUMENT;
+    if (n_tokens == 1) x_token_stride = y_token_stride = 0;          // addresses nothing
+    if (heads == 1) x_head_stride = y_head_stride = 0;
     constexpr int64_t kFar = int64_t(1) << 40;          // an axis's reach: addresses stay far from 64 bits
     if (std::max(x_token_stride, y_token_stride) > kFar / n_tokens || std::max(x_head_stride, y_head_stride) > kFar / heads)
         return DSA_ERR_INVALID_ARGUMENT;

@@ -439,11 +439,12 @@ dsa_status_t dsa_rope_frequencies(int rot_dim, double base, int scaling, double 
  * float32, and each result is rounded once to the element type.
  *   x, y   [n_tokens, heads, head_dim] of dtype DSA_DT_*; a token's heads
  *          and a head's rows are *_head_stride and *_token_stride values
- *          apart (>= 0), a head's values are contiguous.  y may be x with the
- *          same strides (in place; only the turned values are written then);
- *          otherwise the two must not share memory, except as slices of one
- *          buffer with the same strides and no value in common: different
- *          parts of the same heads, or different groups of heads.
+ *          apart (>= 0; that of an axis of one does not count), a head's
+ *          values are contiguous.  y may be x with the same strides (in place;
+ *          only the turned values are written then); otherwise the two must
+ *          not share memory, except as slices of one buffer with the same
+ *          strides and no value in common: different parts of the same heads,
+ *          or different groups of heads.
  *   pos    device int32 [n_tokens], any value
  * Addresses and extents that are multiples of 16 bytes move 16 bytes at a time.
  * Errors: DSA_ERR_INVALID_ARGUMENT for null pointers, sizes below 1, a

@@ -76,3 +76,13 @@ def test_rotation_of_a_long_head_major_view(dsa, torch):
     dsa.dsa_rope(x.contiguous(), pos, rope, want, 64)
     dsa.dsa_rope(x, pos, rope, x, 64)
     assert torch.equal(x, want)
+
+
+def test_rotation_in_place_of_one_token_whatever_its_stride(dsa, torch):
+    rope = dsa.Rope.make(64, 1e4, True)
+    pos = torch.tensor([77], dtype=torch.int32, device="cuda")
+    x = torch.randn(1, 8, 64, generator=gen(torch, 6), device="cuda")
+    want = torch.empty_like(x)
+    dsa.dsa_rope(x, pos, rope, want)
+    dsa.dsa_rope(x, pos, rope, x.as_strided((1, 8, 64), (3, 64, 1)))
+    assert torch.equal(x, want)

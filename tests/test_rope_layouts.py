@@ -87,3 +87,16 @@ def test_strides_as_far_as_a_head_major_view_has_them(L):
     assert taken(L, 4, 2, 64, 128, 64, far // 4, 64, 1 << 42) and not taken(L, 4, 2, 64, 128, 64, far // 4 + 1, 64, 1 << 42)
     # heads times stride beyond 64 bits is refused, not wrapped around
     assert not taken(L, 1, 1 << 23, 2, 0, far, 0, 2, 1 << 42) and not taken(L, 1, 1 << 23, 2, 0, 2, 0, far, 1 << 42)
+
+
+def test_strides_of_an_axis_of_one_do_not_count(L):
+    """What a tensor library gives as the stride of an axis of size one is anything."""
+    assert taken(L, 1, 4, 64, 256, 64, 9999, 64, 0)                  # in place, one token
+    assert taken(L, 4, 1, 64, 64, 64, 64, 7, 0)                      # ... one head
+    assert taken(L, 1, 1, 64, 0, 5, 1 << 50, 1 << 60, 0)
+    assert taken(L, 1, 4, 64, 1 << 50, 128, 1 << 52, 128, 64)        # slices of one token's heads
+    assert taken(L, 4, 1, 64, 128, 1, 128, 2, -64)
+    assert not taken(L, 1, 4, 64, 256, 64, 256, 65, 0)
+    assert not taken(L, 4, 1, 64, 64, 64, 65, 64, 0)
+    assert not taken(L, 1, 4, 64, 1, 128, 2, 128, 63)
+    assert not taken(L, 1, 4, 64, -1, 64, 0, 64, 1 << 20) and not taken(L, 4, 1, 64, 64, 0, 64, -1, 1 << 20)
