@@ -683,7 +683,8 @@ __global__ void __launch_bounds__(128, NF <= 4 ? 16 : 5) attn_combine_kernel(con
             }
         }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    // Nothing selected leaves L = 0; a NaN among the partials has to reach both results.
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
     OutT *dst = out + ((int64_t)t * H + h) * D_L;
     if constexpr (sizeof(OutT) == 4) {
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(128, NF <= 4 ? 16 : 5) attn_combine_kernel(con
             make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
     }
     if (lse && threadIdx.x == 0)
-        lse[(int64_t)t * H + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        lse[(int64_t)t * H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
     __syncthreads();
     tl_end(timeline, kTlCombine);
 }

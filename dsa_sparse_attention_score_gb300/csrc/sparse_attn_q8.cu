@@ -314,6 +314,28 @@ __device__ __noinline__ Unit load_unit(const Params &p, int u, int lane) {
     return w;
 }
 
+// A unit without tiles or without a selected row: zeros (an empty partial of a
+// split).
+__device__ __noinline__ void write_empty(const Params &p, const Unit &w, int tx) {
+    if (w.bad && tx == 0 && w.split == 0) flag(p.status, DSA_DEV_BAD_POSITION);
+    if (p.n_split > 1) {
+        const int64_t part_row = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
+        for (int i = tx; i < kHeads * D_L / 2; i += kSoftmaxThreads)
+            reinterpret_cast<uint32_t *>(p.part_o + part_row * D_L)[i] = 0u;
+        if (tx < kHeads) {
+            p.part_ml[(part_row + tx) * 2] = -INFINITY;
+            p.part_ml[(part_row + tx) * 2 + 1] = 0.f;
+        }
+    } else {
+        const int64_t row = (int64_t)w.t * p.H + w.h0;
+        for (int i = tx; i < w.nh * D_L; i += kSoftmaxThreads) {
+            if (p.out_bf16) static_cast<uint16_t *>(p.out)[row * D_L + i] = 0;
+            else static_cast<float *>(p.out)[row * D_L + i] = 0.f;
+        }
+        if (p.lse && tx < w.nh) p.lse[row + tx] = -INFINITY;
+    }
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __grid_constant__ Params p) {
@@ -634,26 +656,6 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
         bool alive = true;
         int g = 0, v = 0;
 
-        // A unit without tiles: zeros (an empty partial of a split).
-        auto write_empty = [&](const Unit &w) {
-            if (w.bad && tx == 0 && w.split == 0) flag(p.status, DSA_DEV_BAD_POSITION);
-            if (p.n_split > 1) {
-                const int64_t part_row = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
-                for (int i = tx; i < kHeads * D_L / 2; i += kSoftmaxThreads)
-                    reinterpret_cast<uint32_t *>(p.part_o + part_row * D_L)[i] = 0u;
-                if (tx < kHeads) {
-                    p.part_ml[(part_row + tx) * 2] = -INFINITY;
-                    p.part_ml[(part_row + tx) * 2 + 1] = 0.f;
-                }
-            } else {
-                const int64_t row = (int64_t)w.t * p.H + w.h0;
-                for (int i = tx; i < w.nh * D_L; i += kSoftmaxThreads) {
-                    if (p.out_bf16) static_cast<uint16_t *>(p.out)[row * D_L + i] = 0;
-                    else static_cast<float *>(p.out)[row * D_L + i] = 0.f;
-                }
-                if (p.lse && tx < w.nh) p.lse[row + tx] = -INFINITY;
-            }
-        };
         // `heads` heads per warp of the unit's queries as two pieces.
         auto stage_queries = [&](const Unit &w, int parity, int heads) {
             const int64_t row0 = (int64_t)w.t * p.H + w.h0;
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
         // every warp to be through with the unit before.
         auto skip_empty = [&](int parity, int heads) {
             while (ctl.unit[sw][parity].n == 0) {
-                write_empty(ctl.unit[sw][parity]);
+                write_empty(p, ctl.unit[sw][parity], tx);
                 __syncwarp();
                 set_unit(next_unit_id(claims++), parity);
             }
@@ -696,9 +698,10 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
             for (int h = 0; h < kPartHeads / 2; ++h) lpart[h] = f2(0.f, 0.f);
             // lane h: the reference m of head hb + h, 2 to 8 below its largest
             // u so far (the same in the four warps of the part); 0 as long as
-            // every row was masked (fresh)
+            // every row was masked or NaN (fresh)
             float m = 0.f;
             bool fresh = true;
+            bool seen = false;                             // this thread had a row that is not masked
             ma[lane] = 0.f;
             __syncwarp();
             const float *qs_u = ctl.qs[v & 1] + hb;
@@ -707,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                 if (it + 1 == n_tiles) set_unit(next_unit_id(claims++), (v + 1) & 1);
                 if (alive) alive = wait_bar(smem_u32(&ctl.row_full[g % 3]), (uint32_t)(g / 3) & 1u, ctl, p.status, b.wait_ns);
                 const float2 rv = ctl.row[g % 3][r];       // a masked row's products are 0: u = -inf
+                seen = seen || rv.x != 0.f;
                 const float irs = rv.x == 0.f ? 0.f : 1.f / rv.x;
                 const uint64_t rs2 = f2(rv.x, rv.x), ef2 = f2(rv.y, rv.y), irs2 = f2(irs, irs);
                 if (alive) alive = wait_bar(smem_u32(&ctl.s_full), (uint32_t)g & 1u, ctl, p.status, b.wait_ns);
@@ -765,12 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                     named_barrier(2 + part, 128);
                     const int hl = hb + lane;
                     over = fmaxf(fmaxf(ctl.red[0][hl], ctl.red[1][hl]), fmaxf(ctl.red[2][hl], ctl.red[3][hl]));
-                    const float up = (fresh ? over != -INFINITY : over > kRaiseLog2) ? over - kTopLog2 : 0.f;
+                    // (NaN moves nothing: it gets through to l and the products by itself)
+                    const float up = over > (fresh ? -INFINITY : kRaiseLog2) ? over - kTopLog2 : 0.f;
                     m += up;
                     ma[lane] = -m;
                     ma[kPartHeads + lane] = up;
                     moved = fresh ? 0u : __ballot_sync(0xffffffffu, up != 0.f);
-                    fresh = __all_sync(0xffffffffu, over == -INFINITY) && fresh;
+                    fresh = __all_sync(0xffffffffu, !(over > -INFINITY)) && fresh;
                     __syncwarp();
 #pragma unroll
                     for (int h = 0; h < kPartHeads; h += 4) {
@@ -858,10 +863,10 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
             }
             const float lsum = warp_sum_32(lrow, lane);
             ctl.sum[quarter][hb + lane] = lsum;
-            named_barrier(2 + part, 128);
+            const bool none = !named_barrier_or(2 + part, 128, seen);      // every row of the unit was masked
             const int hl = hb + lane;
             const float l = ctl.sum[0][hl] + ctl.sum[1][hl] + ctl.sum[2][hl] + ctl.sum[3][hl];
-            ma[lane] = p.n_split > 1 ? 1.f : fresh ? 0.f : 1.f / l;
+            ma[lane] = p.n_split > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
             __syncwarp();
             // ---- While the last value product runs: its share of the next unit's
             // queries (the score products have read this one's).
@@ -871,7 +876,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
             alive = __all_sync(0xffffffffu, alive);
             const int64_t row0 = (int64_t)w.t * p.H + w.h0;
             const int64_t part0 = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
-            if (alive) {
+            if (alive && none) {
+                write_empty(p, w, tx);                            // whatever the queries are, NaN among them
+            } else if (alive) {
                 // Thread (quarter, lane) holds output dim 128 c + 32 quarter +
                 // lane of the part's heads.  Of 16-bit results neighbouring lanes
                 // swap halves, so that the even one stores two dims of head 2 i
@@ -920,10 +927,10 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                 if (quarter == 0) {
                     const int h = hb + lane;
                     if (p.n_split > 1) {
-                        p.part_ml[(part0 + h) * 2] = fresh ? -INFINITY : m;
+                        p.part_ml[(part0 + h) * 2] = l == 0.f ? -INFINITY : m;
                         p.part_ml[(part0 + h) * 2 + 1] = l;
                     } else if (p.lse && h < w.nh) {
-                        p.lse[row0 + h] = fresh ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                        p.lse[row0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                     }
                 }
             }

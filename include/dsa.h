@@ -56,7 +56,8 @@
  *    skips the offending work, ORs a DSA_DEV_* bit into the status word at
  *    the start of the workspace and carries on.  dsa_read_device_status
  *    reads and clears it.
- *  - Inputs must be finite; NaN or Inf inputs give unspecified results.
+ *  - Inputs must be finite; NaN or Inf inputs give unspecified results, except
+ *    where a call on the 8-bit cache says what they give.
  */
 #ifndef DSA_H
 #define DSA_H
@@ -514,7 +515,9 @@ dsa_status_t dsa_kv_read_q8(const uint8_t *codes, const float *scale, int tail, 
  * outputs of a token that several CTAs share are joined in bf16.  Any positive
  * scale serves, power of two or not; below 2^-40 it counts as 2^-40.  Scales
  * of a token's selected rows that lie further than 2^90 apart cost the rows
- * with the smaller ones their weight.
+ * with the smaller ones their weight.  A selected row whose scale is NaN makes
+ * out and lse of its token NaN, a query value that is not finite those of its
+ * head; without a valid entry they are 0 and -INFINITY all the same.
  */
 dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const uint8_t *codes,
                                     const float *scale, const dsa_batch_t *batch, const dsa_paging_t *paging,

@@ -86,3 +86,77 @@ def test_rotation_in_place_of_one_token_whatever_its_stride(dsa, torch):
     dsa.dsa_rope(x, pos, rope, want)
     dsa.dsa_rope(x, pos, rope, x.as_strided((1, 8, 64), (3, 64, 1)))
     assert torch.equal(x, want)
+
+
+NOT_FINITE = [
+    # lens, per, k: split (one token each of two sequences) and one CTA per token
+    ([2600, 1300], [1, 1], 1024),
+    ([1300], [160], 300),
+]
+
+
+def not_finite_case(dsa, torch, lens, per, k, tail, seed=13):
+    s = Seqs(dsa, torch, lens, per)
+    codes, scale = fill_cache(dsa, torch, s, tail)
+    g = gen(torch, seed)
+    q = torch.randn(s.batch.T, 70, 512, generator=g, device="cuda").to(torch.bfloat16)
+    qr = torch.randn(s.batch.T, 70, 64, generator=g, device="cuda").to(torch.bfloat16) if tail else None
+    return s, codes, scale, q, qr
+
+
+@pytest.mark.parametrize("lens,per,k", NOT_FINITE)
+@pytest.mark.parametrize("tail", [True, False])
+def test_selected_rows_that_are_not_finite(dsa, torch, lens, per, k, tail):
+    """Rows with the scale NaN, as the append leaves them: among finite ones,
+    alone, alone in a tile, beside masked ones.  Out and lse are NaN where one
+    is selected and untouched where none is."""
+    s, codes, scale, q, qr = not_finite_case(dsa, torch, lens, per, k, tail)
+    idx = selections(s, k)
+    good = attend(dsa, torch, s, q, qr, codes, scale, idx, 0.05)
+    last = s.batch.T - 1                                   # the first tokens stay as they are
+    at = int(idx[last][k // 3])
+    x = torch.full((1, 576 if tail else 512), float("inf"), device="cuda")
+    one = dsa.Batch.from_host([0, 1], [at], [s.off[int(s.seq[last])]], s.rows)
+    dsa.dsa_kv_append_q8(x[:, :512], x[:, 512:] if tail else None, one, None, codes, scale, s.ws)
+    only = np.full_like(idx[last], -1)
+    for how in range(5):
+        ix = idx.copy()
+        if how == 1:
+            ix[last], ix[last, 0] = -1, at                 # alone, first
+        elif how == 2:
+            ix[last], ix[last, -1] = -1, at                # alone, in the last tile
+        elif how == 3:
+            ix[last] = at                                  # nothing else, all through
+        elif how == 4:
+            ix[last] = only                                # none
+        hit = (ix == at).any(1) & (s.seq == s.seq[last])
+        for dt in (torch.float32, torch.bfloat16):
+            out, lse = attend(dsa, torch, s, q, qr, codes, scale, ix, 0.05, dt)
+            for t in range(s.batch.T):
+                if hit[t]:
+                    assert torch.isnan(out[t]).all() and torch.isnan(lse[t]).all(), (how, t)
+                elif t == last:
+                    assert (out[t] == 0).all() and torch.isneginf(lse[t]).all(), (how, t)
+                else:
+                    assert torch.equal(out[t], good[0][t].to(dt)) and torch.equal(lse[t], good[1][t]), (how, t)
+
+
+@pytest.mark.parametrize("lens,per,k", NOT_FINITE)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_queries_that_are_not_finite(dsa, torch, lens, per, k, bad):
+    """One head's query: that head alone is lost, and only where rows are
+    selected; the first tiles of a token fully masked as well."""
+    s, codes, scale, q, qr = not_finite_case(dsa, torch, lens, per, k, True)
+    idx = selections(s, k)
+    idx[0, :k // 2] = -1
+    idx[-1] = -1
+    sm = 4.0                                               # (references far from the first tile's)
+    good = attend(dsa, torch, s, q, qr, codes, scale, idx, sm)
+    assert (good[0][-1] == 0).all() and torch.isneginf(good[1][-1]).all()
+    q[:, 5, 100] = bad
+    qr[:, 67, 3] = bad
+    out, lse = attend(dsa, torch, s, q, qr, codes, scale, idx, sm)
+    lost = torch.zeros(s.batch.T, 70, dtype=torch.bool, device="cuda")
+    lost[:-1, 5] = lost[:-1, 67] = True
+    assert torch.isnan(out[lost]).all() and torch.isnan(lse[lost]).all()
+    assert torch.equal(out[~lost], good[0][~lost]) and torch.equal(lse[~lost], good[1][~lost])
