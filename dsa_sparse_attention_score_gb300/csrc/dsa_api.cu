@@ -61,6 +61,15 @@ DevBatch dev_batch(const dsa_batch_t *b) {
     return d;
 }
 
+// Rows through a block table when `paging` is given; kv_off is then not read.
+void set_paging(DevBatch *d, const dsa_paging_t *paging) {
+    if (!paging) return;
+    d->kv_off = nullptr;
+    d->block_table = paging->block_table;
+    d->max_blocks = paging->max_blocks;
+    d->block_size = paging->block_size;
+}
+
 // ---------------------------------------------------------------- tensor maps
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -211,11 +220,7 @@ dsa_status_t run_attention(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const 
                            float *out, float *lse, void *ws, const Layout &L, cudaStream_t stream,
                            bool traced, bool pdl, const dsa_paging_t *paging = nullptr, bool rope = true) {
     DevBatch db = dev_batch(batch);
-    if (paging) {
-        db.block_table = paging->block_table;
-        db.max_blocks = paging->max_blocks;
-        db.block_size = paging->block_size;
-    }
+    set_paging(&db, paging);
     CUtensorMap ql, qr, kv;
     const uint64_t qrows = (uint64_t)batch->total_q * H;
     // without the rope tail the latent rows are D_L wide and the kernel never
@@ -476,11 +481,7 @@ static dsa_status_t decode_impl(const void *k_new, int k_dtype, const dsa_f16 *q
     if ((s = check_ws(ws, ws_bytes, L.total)) != DSA_OK) return s;
 
     DevBatch db = dev_batch(batch);
-    if (paging) {
-        db.block_table = paging->block_table;
-        db.max_blocks = paging->max_blocks;
-        db.block_size = paging->block_size;
-    }
+    set_paging(&db, paging);
     uint8_t *w8 = static_cast<uint8_t *>(ws);
     uint32_t *st = status_ptr(ws);
     float *slab = reinterpret_cast<float *>(w8 + L.scores);
@@ -813,11 +814,7 @@ static dsa_status_t cache_batch(const dsa_batch_t *batch, const dsa_paging_t *pa
         if (!aligned(paging->block_table, 4)) return DSA_ERR_MISALIGNED;
     }
     *db = dev_batch(batch);
-    if (paging) {
-        db->block_table = paging->block_table;
-        db->max_blocks = paging->max_blocks;
-        db->block_size = paging->block_size;
-    }
+    set_paging(db, paging);
     return DSA_OK;
 }
 

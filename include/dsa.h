@@ -480,6 +480,7 @@ dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stri
  *           values apart, or NULL for rows without a tail; both of dtype DSA_DT_*
  *   paging  NULL for contiguous caches (row kv_off[b] + position); any
  *           block_size >= 1, here and in the other calls on the 8-bit cache
+ *           (with paging batch->kv_off is not read and may be NULL)
  *   ws      at least dsa_workspace_size(DSA_OP_K_APPEND) bytes (status word)
  * Tokens of a batch must be at different rows.  A token whose position is out
  * of bounds is skipped and flagged DSA_DEV_BAD_POSITION; no other row changes.

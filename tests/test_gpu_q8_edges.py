@@ -160,3 +160,37 @@ def test_queries_that_are_not_finite(dsa, torch, lens, per, k, bad):
     lost[:-1, 5] = lost[:-1, 67] = True
     assert torch.isnan(out[lost]).all() and torch.isnan(lse[lost]).all()
     assert torch.equal(out[~lost], good[0][~lost]) and torch.equal(lse[~lost], good[1][~lost])
+
+
+def test_paged_calls_do_not_read_the_sequences_offsets(dsa, torch):
+    """With a block table kv_off may hold anything: every paged call gives what
+    it gives over zeros."""
+    s = Seqs(dsa, torch, [700, 300], [3, 2], 64)
+    codes0, scale0 = fill_cache(dsa, torch, s, True)
+    idx = torch.from_numpy(selections(s, 200)).cuda()
+    g = gen(torch, 8)
+    q = torch.randn(5, 16, 512, generator=g, device="cuda").to(torch.bfloat16)
+    qr = torch.randn(5, 16, 64, generator=g, device="cuda").to(torch.bfloat16)
+    x = torch.randn(5, 576, generator=g, device="cuda").to(torch.bfloat16)
+    keys0 = torch.randn(s.rows, 128, generator=g, device="cuda").half()
+    k_new = torch.randn(5, 128, generator=g, device="cuda").half()
+    q_idx = torch.randn(5, 32, 128, generator=g, device="cuda").half()
+    w = torch.rand(5, 32, generator=g, device="cuda")
+    kv = torch.randn(s.rows, 576, generator=g, device="cuda").to(torch.bfloat16)
+    got = []
+    for off in ([0, 0], [-7, 1 << 40]):
+        s.batch.kv_off = torch.tensor(off, dtype=torch.int64, device="cuda")
+        codes, scale, keys, cache = codes0.clone(), scale0.clone(), keys0.clone(), kv.clone()
+        dsa.dsa_kv_append_q8(x[:, :512], x[:, 512:], s.batch, None, codes, scale, s.ws, *s.paging)
+        dsa.dsa_kv_append(x[:, :512], x[:, 512:], s.batch, None, cache, s.ws, *s.paging)
+        back = torch.empty(5, 576, device="cuda")
+        dsa.dsa_kv_read_q8(codes, scale, s.batch, back, s.ws, *s.paging)
+        assert dsa.dsa_read_device_status(s.ws) == 0
+        o8 = attend(dsa, torch, s, q, qr, codes, scale, idx, 0.07)
+        ws = dsa.workspace(dsa.DSA_OP_DECODE, s.batch, 32, 16, 200)
+        out, lse = torch.empty(5, 16, 512, device="cuda"), torch.empty(5, 16, device="cuda")
+        sel = torch.empty(5, 200, dtype=torch.int32, device="cuda")
+        dsa.dsa_decode_paged(k_new, q_idx, w, q, qr, keys, cache, s.batch, s.block, 64, 200, 0.07, False, out, lse, sel, ws)
+        assert dsa.dsa_read_device_status(ws) == 0
+        got.append((codes, scale, cache, back, *o8, keys, out, lse, sel))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
