@@ -22,13 +22,15 @@ struct DevRope {
 //     inv_freq = m 2^(e - 1075), m of 53 bits
 //     F        = frac(inv_freq / 2 pi) 2^64 = m C 2^(e - 1075) mod 2^64,  C = 2^64 / 2 pi
 //     turn     = pos F mod 2^64.
-// Whole turns drop out by wrapping.  F is off by at most 2 units (and C's
-// truncation, 2^-62 of it), so a turn by 2^-31 at the largest position; the
-// fraction, in [-1/2, 1/2), is rounded once to 32 bits.  Frequencies from 2^-60 on,
-// either sign.
+// Whole turns drop out by wrapping.  C and F are cut to their units, so F is
+// off by less than |inv_freq| + 1 of them and the turn by less than
+// (|inv_freq| + 1) |pos| 2^-64; the fraction, in [-1/2, 1/2), is cut to 2^-32
+// and rounded to 24 bits (2^-25 at most).  Either sign; a frequency that is NaN
+// or infinite gives NaN.
 __device__ __forceinline__ float2 rope_cos_sin(int32_t pos, double inv_freq, float scale, int inverse) {
     const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
-    const int shift = 1075 - (int)((bits >> 52) & 0x7FF);
+    const int exponent = (int)((bits >> 52) & 0x7FF), shift = 1075 - exponent;
+    if (exponent == 0x7FF) scale = __int_as_float(0x7FC00000);
     const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
     constexpr uint64_t C = 0x28BE60DB9391054Aull;             // floor(2^64 / (2 pi))
     const uint64_t lo = m * C, hi = __umul64hi(m, C);

@@ -408,7 +408,9 @@ enum {
 /*
  * A rotation: the value pair j of a token at position p turns by the angle
  * p * inv_freq[j] and is multiplied by scale.
- *   inv_freq     device float64 [rot_dim / 2], radians per position, 8-byte aligned
+ *   inv_freq     device float64 [rot_dim / 2], radians per position, 8-byte
+ *                aligned; either sign (a pair whose frequency is NaN or infinite
+ *                becomes NaN)
  *   rot_dim      values that turn: even, 2..512
  *   interleaved  nonzero: pair j is the values 2j and 2j + 1; 0: j and j + rot_dim / 2
  *   scale        factor on the turned values (1, or a context scaling's attention factor)
@@ -436,8 +438,10 @@ dsa_status_t dsa_rope_frequencies(int rot_dim, double base, int scaling, double 
  *   y[t,h,rot_off + i] = scale * (R(pos[t]) x[t,h,rot_off : rot_off + rot_dim])[i],
  *   the other values of the head are copied.
  * With `inverse` the angles are negated: the call that maps the gradient of
- * y to the gradient of x.  Angles are formed in float64, the products in
- * float32, and each result is rounded once to the element type.
+ * y to the gradient of x.  Angles are formed in 64-bit integers as fractions of
+ * a turn, off by less than (|inv_freq| + 1) |pos| 2^-64 turns, which are rounded
+ * to float32 (2^-25 turns at most); sine, cosine and products are float32, and
+ * each result is rounded once to the element type.
  *   x, y   [n_tokens, heads, head_dim] of dtype DSA_DT_*; a token's heads
  *          and a head's rows are *_head_stride and *_token_stride values
  *          apart (>= 0; that of an axis of one does not count), a head's

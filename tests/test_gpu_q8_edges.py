@@ -194,3 +194,63 @@ def test_paged_calls_do_not_read_the_sequences_offsets(dsa, torch):
         assert dsa.dsa_read_device_status(ws) == 0
         got.append((codes, scale, cache, back, *o8, keys, out, lse, sel))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def pi(digits=60):
+    """pi by Machin's formula."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = digits + 10
+
+    def arctan_inv(n):
+        total = term = Decimal(1) / n
+        k = 1
+        while abs(term) > Decimal(10) ** -(digits + 5):
+            term /= -n * n
+            k += 2
+            total += term / k
+        return total
+    return 16 * arctan_inv(5) - 4 * arctan_inv(239)
+
+
+def test_angles_of_far_positions_and_of_any_frequency(dsa, torch):
+    """Against exact products: the turn is off by less than (|f| + 1) |p| 2^-64
+    and the 2^-32 its fraction is cut to, then rounded (2^-25 of a turn); the
+    sine and cosine add two units of 2^-24."""
+    from decimal import Decimal
+    f = [0.0, 1e-30, 2.0 ** -60, 1e-12, 1e-4, 0.7, 1.0, -1.0, -3.1, 1000.0, 2.0 ** 20, 12345.678]
+    two_pi = 2 * pi()
+    pos = [0, 1, -1, 4097, 1 << 20, 2 ** 31 - 1, -2 ** 31]
+    rope = dsa.Rope(torch.tensor(f, dtype=torch.float64, device="cuda"), True)
+    x = torch.zeros(len(pos), 1, 2 * len(f), device="cuda")
+    x[:, :, 0::2] = 1.0
+    y = torch.empty_like(x)
+    dsa.dsa_rope(x, torch.tensor(pos, dtype=torch.int32, device="cuda"), rope, y)
+    got = f64(y)[:, 0]
+    for i, p in enumerate(pos):
+        for j, v in enumerate(f):
+            turn = float((Decimal(p) * Decimal(v) / two_pi) % 1)
+            tol = 2 * np.pi * ((abs(v) + 1) * abs(p) * 2.0 ** -64 + 2.0 ** -32 + 2.0 ** -25) + 2.0 ** -23
+            assert abs(got[i, 2 * j] - np.cos(2 * np.pi * turn)) <= tol, (p, v)
+            assert abs(got[i, 2 * j + 1] - np.sin(2 * np.pi * turn)) <= tol, (p, v)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("inter", [True, False])
+def test_frequencies_that_are_not_finite_give_nan(dsa, torch, bad, inter):
+    s = Seqs(dsa, torch, [50], [4])
+    rope, wrong = dsa.Rope.make(64, 1e4, inter), dsa.Rope.make(64, 1e4, inter)
+    wrong.inv_freq[5] = bad
+    x = torch.randn(4, 576, generator=gen(torch, 8), device="cuda")
+    hit = torch.zeros(64, dtype=torch.bool, device="cuda")
+    hit[[10, 11] if inter else [5, 37]] = True
+    want, got = torch.empty(4, 1, 64, device="cuda"), torch.empty(4, 1, 64, device="cuda")
+    dsa.dsa_rope(x[:, None, 512:], s.batch.q_pos, rope, want)
+    dsa.dsa_rope(x[:, None, 512:], s.batch.q_pos, wrong, got)
+    assert torch.isnan(got[..., hit]).all() and torch.equal(got[..., ~hit], want[..., ~hit])
+    kv = torch.zeros(s.rows, 576, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_kv_append(x[:, :512], x[:, 512:], s.batch, wrong, kv, s.ws)
+    new = kv[torch.from_numpy(s.token_rows()).cuda()]
+    assert torch.isnan(new[:, 512:][:, hit]).all() and torch.isfinite(new[:, 512:][:, ~hit]).all()
+    codes, scale = dsa.q8_cache(s.rows)
+    dsa.dsa_kv_append_q8(x[:, :512], x[:, 512:], s.batch, wrong, codes, scale, s.ws)
+    assert torch.isnan(scale[torch.from_numpy(s.token_rows()).cuda()]).all()
