@@ -24,9 +24,10 @@ struct DevRope {
 //     turn     = pos F mod 2^64.
 // Whole turns drop out by wrapping.  C and F are cut to their units, so F is
 // off by less than |inv_freq| + 1 of them and the turn by less than
-// (|inv_freq| + 1) |pos| 2^-64; the fraction, in [-1/2, 1/2), is cut to 2^-32
-// and rounded to 24 bits (2^-25 at most).  Either sign; a frequency that is NaN
-// or infinite gives NaN.
+// (|inv_freq| + 1) |pos| 2^-64; the fraction, in [-1/2, 1/2), is cut to 2^-32.
+// float32 holds 24 bits of it, and a turn by the rest follows the sine and
+// cosine: they are off by 8e-8 at most, 1.1e-7 without it.  Either sign; a
+// frequency that is NaN or infinite gives NaN.
 __device__ __forceinline__ float2 rope_cos_sin(int32_t pos, double inv_freq, float scale, int inverse) {
     const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
     const int exponent = (int)((bits >> 52) & 0x7FF), shift = 1075 - exponent;
@@ -40,8 +41,14 @@ __device__ __forceinline__ float2 rope_cos_sin(int32_t pos, double inv_freq, flo
     else if (shift < 128) F = hi >> (shift - 64);
     if (bits >> 63) F = ~F + 1;
     const uint64_t turn = F * (uint64_t)(int64_t)pos;
+    const int32_t frac = (int32_t)(turn >> 32);
+    const float near = (float)frac;
     float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+    sincospif(near * 0x1p-31f, &s, &c);
+    // what the conversion left out, at most 2^6 units: sin(a + d) = sin a + d cos a
+    const float d = (float)(frac - __float2int_rz(near)) * (6.2831853f * 0x1p-32f), s0 = s;
+    s = fmaf(c, d, s);
+    c = fmaf(-s0, d, c);
     return make_float2(c * scale, inverse ? -s * scale : s * scale);
 }
 

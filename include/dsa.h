@@ -439,9 +439,9 @@ dsa_status_t dsa_rope_frequencies(int rot_dim, double base, int scaling, double 
  *   the other values of the head are copied.
  * With `inverse` the angles are negated: the call that maps the gradient of
  * y to the gradient of x.  Angles are formed in 64-bit integers as fractions of
- * a turn, off by less than (|inv_freq| + 1) |pos| 2^-64 turns, which are rounded
- * to float32 (2^-25 turns at most); sine, cosine and products are float32, and
- * each result is rounded once to the element type.
+ * a turn, off by less than (|inv_freq| + 1) |pos| 2^-64 + 2^-32 turns; sine,
+ * cosine and products are float32, and each result is rounded once to the
+ * element type.
  *   x, y   [n_tokens, heads, head_dim] of dtype DSA_DT_*; a token's heads
  *          and a head's rows are *_head_stride and *_token_stride values
  *          apart (>= 0; that of an axis of one does not count), a head's

@@ -254,3 +254,23 @@ def test_frequencies_that_are_not_finite_give_nan(dsa, torch, bad, inter):
     codes, scale = dsa.q8_cache(s.rows)
     dsa.dsa_kv_append_q8(x[:, :512], x[:, 512:], s.batch, wrong, codes, scale, s.ws)
     assert torch.isnan(scale[torch.from_numpy(s.token_rows()).cuda()]).all()
+
+
+def test_sines_and_cosines_to_their_last_bit(dsa, torch):
+    """x = (1, 0) turned: float32 sine and cosine of pi times the fraction are
+    good to a unit of 2^-24, what the rounded fraction left out is put back to
+    2^-32 of a turn (and C, F and their product to less), and that sum is
+    rounded once more.  A fraction rounded to 24 bits alone would be off by up
+    to 2 pi 2^-26 by itself, as much as all of that."""
+    T = 3000
+    f, _ = dsa.dsa_rope_frequencies(64, 10000.0)
+    rope = dsa.Rope(torch.tensor(f, dtype=torch.float64, device="cuda"), True)
+    pos = torch.randint(0, 1 << 18, (T,), generator=gen(torch, 5), device="cuda", dtype=torch.int32)
+    x = torch.zeros(T, 1, 64, device="cuda")
+    x[:, :, 0::2] = 1.0
+    y = torch.empty_like(x)
+    dsa.dsa_rope(x, pos, rope, y)
+    # 64 bits hold angles below 2^18 to 2^-36
+    ang = pos.double()[:, None] * rope.inv_freq
+    err = torch.maximum((y[:, 0, 0::2].double() - ang.cos()).abs(), (y[:, 0, 1::2].double() - ang.sin()).abs())
+    assert float(err.max()) <= 2.0 ** -24 + 2.0 ** -25 + 2 * np.pi * 2.0 ** -31.9, float(err.max())
