@@ -30,11 +30,11 @@ constexpr int kQ8MinExp = -40, kQ8MaxExp = 119;
 // 2^n for -126 <= n <= 127.
 __device__ __forceinline__ float exp2_int(int n) { return __int_as_float((n + 127) << 23); }
 
-// E of a row whose largest magnitude is top (finite): 448 = 1.75 * 2^8.
-__device__ __forceinline__ int q8_exponent(float top) {
+// E of values whose largest magnitude is top (finite): 448 = 1.75 * 2^8.
+__device__ __forceinline__ int q8_exponent(float top, int least = kQ8MinExp) {
     const uint32_t b = __float_as_uint(top);
     const int e = (int)(b >> 23) - 127 - ((b & 0x7FFFFFu) > 0x600000u ? 7 : 8);
-    return min(max(e, kQ8MinExp), kQ8MaxExp);
+    return min(max(e, least), kQ8MaxExp);
 }
 
 // Two e4m3 codes, lo_elem in bits 0..7.

@@ -104,6 +104,9 @@ constexpr float kTopLog2 = 2.0f;              // a new maximum's weight is 2^2 .
 constexpr float kRaiseLog2 = 8.0f;            // ... and none exceeds 2^8
 constexpr int kFewMoved = 6;                  // heads of 32 rescaled one by one
 constexpr float kMinScale = 0x1p-40f;
+// Least e of a head's queries: under it split8 would add to their exponents,
+// zeros' among them.
+constexpr int kQueryMinExp = -112;
 constexpr uint32_t kTmemCols = 512;           // S^T: 128 columns, the tails of two tiles: 2 x 32, O^T: 4 x 64
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColT = 2 * kHeads;
@@ -274,7 +277,7 @@ __device__ __noinline__ void split_queries(const uint16_t *q_lat, const uint16_t
             // the largest magnitude by its bf16 bits
             const uint32_t both = __vmaxu2(ht == i ? max_bf16(tv) : 0u, __vmaxu2(max_bf16(a[i]), max_bf16(c[i])));
             const uint32_t top = __reduce_max_sync(0xffffffffu, max(both & 0xFFFFu, both >> 16));
-            const int e = q8_exponent(__uint_as_float(top << 16));
+            const int e = q8_exponent(__uint_as_float(top << 16), kQueryMinExp);
             const uint32_t drop = (uint32_t)(-(112 + e) * 128 & 0xFFFF) * 0x10001u;
             if (ht == i) drop_t = drop;
             if (lane == i) qs[h0 + i] = h0 + i >= nh ? 0.f : top < 0x7F80u ? exp2_int(e) * scale_log2 : __int_as_float(0x7FC00000);
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                             if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty));
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 4; ++i) {        // (the two scales first: one of them alone could overflow)
                             const float4 q4 = *reinterpret_cast<const float4 *>(qs_u + 16 * half + 4 * i);
                             const float4 n4 = *reinterpret_cast<const float4 *>(ma + 16 * half + 4 * i);
                             const uint64_t qs[2] = {f2(q4.x, q4.y), f2(q4.z, q4.w)}, nm[2] = {f2(n4.x, n4.y), f2(n4.z, n4.w)};
@@ -743,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                                 const int h = 4 * i + 2 * j;
                                 const uint64_t a2 = f2(__uint_as_float(a16[half][h]), __uint_as_float(a16[half][h + 1]));
                                 const uint64_t b2 = f2(__uint_as_float(b16[half][h]), __uint_as_float(b16[half][h + 1]));
-                                const float2 d = f2_get(f2_add(f2_fma(f2_mul(f2_add(a2, b2), rs2), qs[j], nm[j]), ef2));
+                                const float2 d = f2_get(f2_add(f2_fma(f2_add(a2, b2), f2_mul(qs[j], rs2), nm[j]), ef2));
                                 x[16 * half + h] = d.x;
                                 x[16 * half + h + 1] = d.y;
                                 top = fmaxf(top, fmaxf(d.x, d.y));

@@ -274,3 +274,34 @@ def test_sines_and_cosines_to_their_last_bit(dsa, torch):
     ang = pos.double()[:, None] * rope.inv_freq
     err = torch.maximum((y[:, 0, 0::2].double() - ang.cos()).abs(), (y[:, 0, 1::2].double() - ang.sin()).abs())
     assert float(err.max()) <= 2.0 ** -24 + 2.0 ** -25 + 2 * np.pi * 2.0 ** -31.9, float(err.max())
+
+
+@pytest.mark.parametrize("lens,per,k", [([2600, 1300], [1, 1], 1024), ([900], [160], 300)])
+@pytest.mark.parametrize("dq,drow,dsm", [(-60, 60, 0), (-100, 100, 0), (-100, 120, -20), (60, -25, -35)])
+def test_small_queries_over_large_rows(dsa, torch, lens, per, k, dq, drow, dsm):
+    """Queries times 2^dq, row scales times 2^drow, sm_scale times 2^dsm, summing
+    to nothing: the same weights, outputs times 2^drow.  The pieces of the
+    queries are the same; u = z log2 e + log2 scale is rounded twice at up to
+    2^8 (2^-17 each, on both sides: 2^-15), and the weights anew, where their
+    units lie otherwise: 2^-7 + 2^-11 of each on both sides, and 2^-14.9 of the
+    largest; split partials by 2^-8."""
+    s = Seqs(dsa, torch, lens, per)
+    codes, scale = fill_cache(dsa, torch, s, True)
+    g = gen(torch, 17)
+    T, H, sm = s.batch.T, 33, 1 / 13.86
+    q = torch.randn(T, H, 512, generator=g, device="cuda").to(torch.bfloat16)
+    qr = torch.randn(T, H, 64, generator=g, device="cuda").to(torch.bfloat16)
+    idx = selections(s, k)
+    out0, lse0 = attend(dsa, torch, s, q, qr, codes, scale, idx, sm)
+    out, lse = attend(dsa, torch, s, q * 2.0 ** dq, qr * 2.0 ** dq, codes, scale * 2.0 ** drow, idx, sm * 2.0 ** dsm)
+    assert ((lse - lse0).abs() <= 2.0 ** -15 * (1 + lse0.abs())).all(), float((lse - lse0).abs().max())
+    c, sc = codes.cpu().numpy(), f64(scale)
+    for t in range(0, T, 13):
+        rows = np.asarray(s.row(int(s.seq[t]), idx[t][idx[t] >= 0]))
+        lat, tail = R.decode_rows(c[rows], sc[rows])
+        z = sm * (f64(q[t]) @ lat.T + f64(qr[t]) @ tail.T)
+        w = np.exp(z - f64(lse0[t])[:, None])
+        top = (w * sc[rows]).max(1, keepdims=True)
+        tol = (2 * (2.0 ** -7 + 2.0 ** -11) + 2 * 2.0 ** -8 + 2.0 ** -14) * (w @ np.abs(lat)) + \
+            2 * 2.0 ** -14.9 * top * np.abs(lat / sc[rows][:, None]).sum(0)
+        assert np.all(np.abs(f64(out[t]) * 2.0 ** -drow - f64(out0[t])) <= tol), t
