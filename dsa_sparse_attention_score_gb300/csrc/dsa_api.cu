@@ -180,7 +180,7 @@ Layout layout(int op, const dsa_batch_t *b, int H, int k) {
         if (L.n_split > 1) {
             const size_t rows = (size_t)b->total_q * L.n_split * head_groups(H) * 64;
             L.part_o = off;
-            L.part_o_bytes = rows * D_L * 2;           // bf16
+            L.part_o_bytes = rows * D_L * 2;           // 16 bits each
             off = align_up(off + L.part_o_bytes, kAlign);
             L.part_ml = off;
             L.part_ml_bytes = rows * 2 * 4;
@@ -848,6 +848,7 @@ static dsa_status_t run_attention_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_ro
     c.out16 = a.out_bf16 ? out : nullptr;
     c.lse = lse;
     c.n_split = a.n_split;
+    c.part_unit = attn_q8_part_unit(a.tiles_per_cta);
     c.part_o = a.part_o;
     c.part_ml = a.part_ml;
     DSA_TRY_CUDA(launch_attn_combine(c, db, stream, true));

@@ -153,9 +153,10 @@ struct AttnLaunch {
     float *lse;              // [T, H] or null
     int tiles_per_cta;       // attention row tiles handled by one CTA
     int n_split;             // CTAs per (token, head group)
-    void *part_o;            // bf16 [T, n_split, groups*64, 512] when n_split > 1
+    void *part_o;            // bf16 [T, n_split, groups*64, 512] when n_split > 1 (fp16 with part_unit)
     float *part_ml;          // [T, n_split, groups*64, 2]
     void *out16 = nullptr;   // combine: bf16 output instead of `out`
+    float part_unit = 0.f;   // combine: partials are fp16, times this; 0: bf16
 };
 cudaError_t launch_sparse_attn(const AttnLaunch &a, const CUtensorMap &q_lat_map,
                                const CUtensorMap &q_rope_map, const CUtensorMap &kv_map,
@@ -212,6 +213,7 @@ struct AttnQ8Launch {
     float *part_ml;
 };
 int attn_q8_tile_rows();
+float attn_q8_part_unit(int tiles_per_cta);   // factor on the fp16 split partials, a power of two
 cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream);
 
 // Sets a kernel's dynamic shared-memory limit once per device; `slot`

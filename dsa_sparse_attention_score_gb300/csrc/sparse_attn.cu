@@ -632,16 +632,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Two partial outputs of a 32-bit word.
+template <typename Part> __device__ __forceinline__ float2 part_values(uint32_t v);
+template <> __device__ __forceinline__ float2 part_values<__nv_bfloat16>(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
+}
+template <> __device__ __forceinline__ float2 part_values<__half>(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+
 // Merge split partials: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
 // NF partial rows are loaded at a time.  With NF = 4 (up to four splits)
 // the kernel fits in 32 registers, so 16 CTAs share an SM and a grid of
 // thousands of (token, head) CTAs runs in one wave; NF = 16 keeps five CTAs
-// per SM.  OutT: float, or bf16 (one more rounding) for the 8-bit cache's call.
-template <int NF, typename OutT>
+// per SM.  Part: bf16 partials, or the 8-bit cache's fp16 ones times 1 / unit (a
+// power of two).  OutT: float, or bf16 (one more rounding) for the 8-bit cache.
+template <int NF, typename Part, typename OutT>
 __global__ void __launch_bounds__(128, NF <= 4 ? 16 : 5) attn_combine_kernel(const uint16_t *__restrict__ part_o,
                                                                             const float *__restrict__ part_ml,
                                                                             int n_split, int H, int groups,
-                                                                            OutT *out, float *lse,
+                                                                            float unit, OutT *out, float *lse,
                                                                             unsigned long long *timeline) {
     __shared__ float wgt[128];
     __shared__ float ml[2][128];
@@ -663,7 +673,7 @@ __global__ void __launch_bounds__(128, NF <= 4 ? 16 : 5) attn_combine_kernel(con
     for (int s = 0; s < n_split; ++s) {
         const float w = ml[0][s] == -INFINITY ? 0.f : exp2f(ml[0][s] - M);
         L += w * ml[1][s];
-        if (threadIdx.x == 0) wgt[s] = w;
+        if (threadIdx.x == 0) wgt[s] = w * unit;
     }
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -677,8 +687,7 @@ __global__ void __launch_bounds__(128, NF <= 4 ? 16 : 5) attn_combine_kernel(con
         for (int u = 0; u < NF; ++u) {
             if (s0 + u < n_split) {
                 const float w = wgt[s0 + u];
-                const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&o[u].x));
-                const float2 c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&o[u].y));
+                const float2 a = part_values<Part>(o[u].x), c = part_values<Part>(o[u].y);
                 acc.x += w * a.x; acc.y += w * a.y; acc.z += w * c.x; acc.w += w * c.y;
             }
         }
@@ -738,12 +747,13 @@ cudaError_t launch_sparse_attn(const AttnLaunch &a, const CUtensorMap &q_lat_map
 
 namespace {
 
-template <int NF, typename OutT>
-cudaError_t launch_combine_as(const AttnLaunch &a, OutT *out, const DevBatch &b, cudaStream_t stream, bool pdl) {
+template <typename Part, typename OutT>
+cudaError_t launch_combine_as(const AttnLaunch &a, float unit, OutT *out, const DevBatch &b, cudaStream_t stream, bool pdl) {
     const int groups = (a.H + kHeads - 1) / kHeads;
     dim3 grid((unsigned)b.T, (unsigned)a.H);
-    return launch_k(attn_combine_kernel<NF, OutT>, grid, dim3(128), 0, stream, pdl, (const uint16_t *)a.part_o,
-                    (const float *)a.part_ml, a.n_split, a.H, groups, out, a.lse, b.timeline);
+    return launch_k(a.n_split <= 4 ? attn_combine_kernel<4, Part, OutT> : attn_combine_kernel<16, Part, OutT>, grid, dim3(128), 0,
+                    stream, pdl, (const uint16_t *)a.part_o, (const float *)a.part_ml, a.n_split, a.H, groups, unit, out, a.lse,
+                    b.timeline);
 }
 
 }  // namespace
@@ -751,11 +761,9 @@ cudaError_t launch_combine_as(const AttnLaunch &a, OutT *out, const DevBatch &b,
 cudaError_t launch_attn_combine(const AttnLaunch &a, const DevBatch &b, cudaStream_t stream, bool pdl) {
     if (a.n_split <= 1) return cudaSuccess;
     if (a.n_split > 128) return cudaErrorInvalidConfiguration;
-    if (a.out16) {
-        uint16_t *o = static_cast<uint16_t *>(a.out16);
-        return a.n_split <= 4 ? launch_combine_as<4>(a, o, b, stream, pdl) : launch_combine_as<16>(a, o, b, stream, pdl);
-    }
-    return a.n_split <= 4 ? launch_combine_as<4>(a, a.out, b, stream, pdl) : launch_combine_as<16>(a, a.out, b, stream, pdl);
+    if (a.out16) return launch_combine_as<__half>(a, 1.f / a.part_unit, static_cast<uint16_t *>(a.out16), b, stream, pdl);
+    if (a.part_unit != 0.f) return launch_combine_as<__half>(a, 1.f / a.part_unit, a.out, b, stream, pdl);
+    return launch_combine_as<__nv_bfloat16>(a, 1.f, a.out, b, stream, pdl);
 }
 
 }  // namespace dsa

@@ -120,12 +120,13 @@ struct Params {
     const int32_t *idx;
     void *out;
     float *lse;
-    uint16_t *part_o;        // [T, n_split, groups, 64, 512] bf16, unnormalised
+    uint16_t *part_o;        // [T, n_split, groups, 64, 512] fp16, unnormalised, times part_unit
     float *part_ml;          // [T, n_split, groups, 64, 2]
     DevBatch b;
     uint32_t *status;
     int H, k, groups, out_bf16;
     float scale_log2;        // sm_scale * log2(e)
+    float part_unit;
     int tiles_per_cta, n_split, n_tiles;
 };
 
@@ -869,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
             const bool none = !named_barrier_or(2 + part, 128, seen);      // every row of the unit was masked
             const int hl = hb + lane;
             const float l = ctl.sum[0][hl] + ctl.sum[1][hl] + ctl.sum[2][hl] + ctl.sum[3][hl];
-            ma[lane] = p.n_split > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            ma[lane] = p.n_split > 1 ? p.part_unit : l == 0.f ? 0.f : 1.f / l;
             __syncwarp();
             // ---- While the last value product runs: its share of the next unit's
             // queries (the score products have read this one's).
@@ -906,12 +907,25 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
                         uint32_t c32[32];
                         tmem_ld32(o_t + c * kHeads, c32);
                         tmem_wait_ld(c32);
+                        uint32_t o16[kPartHeads / 2];
+                        if (p.n_split > 1) {
+#pragma unroll
+                            for (int i = 0; i < kPartHeads / 2; ++i) {
+                                const __half2 o2 = __floats2half2_rn(__uint_as_float(c32[2 * i]) * f[2 * i],
+                                                                     __uint_as_float(c32[2 * i + 1]) * f[2 * i + 1]);
+                                o16[i] = *reinterpret_cast<const uint32_t *>(&o2);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kPartHeads / 2; ++i) {
+                                const __nv_bfloat162 o2 = __floats2bfloat162_rn(__uint_as_float(c32[2 * i]) * f[2 * i],
+                                                                                __uint_as_float(c32[2 * i + 1]) * f[2 * i + 1]);
+                                o16[i] = *reinterpret_cast<const uint32_t *>(&o2);
+                            }
+                        }
 #pragma unroll
                         for (int i = 0; i < kPartHeads / 2; ++i) {
-                            const __nv_bfloat162 o2 = __floats2bfloat162_rn(__uint_as_float(c32[2 * i]) * f[2 * i],
-                                                                            __uint_as_float(c32[2 * i + 1]) * f[2 * i + 1]);
-                            const uint32_t mine = *reinterpret_cast<const uint32_t *>(&o2);
-                            const uint32_t both = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), take);
+                            const uint32_t both = __byte_perm(o16[i], __shfl_xor_sync(0xffffffffu, o16[i], 1), take);
                             if (2 * i + (lane & 1) < live) *reinterpret_cast<uint32_t *>(dst + (int64_t)(2 * i) * D_L + c * 128) = both;
                         }
                     }
@@ -960,6 +974,18 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
 
 int attn_q8_tile_rows() { return kRows; }
 
+// The partial outputs of splits are sums of up to tiles * 128 weights of at
+// most 2^8 times codes of at most 448: times 2^-8 / tiles (rounded down to a
+// power of two) they stay under 57344, inside fp16.  Its eleven bits reach down to
+// 2^-14, a product of the unit weight and the smallest code at one tile, so a
+// partial is rounded to 2^-11 of itself; in bf16, with the same bytes, to 2^-8,
+// which was most of a split decode's error (1.6e-3 of its size).
+float attn_q8_part_unit(int tiles_per_cta) {
+    float unit = 0x1p-8f;
+    for (int t = 1; t < tiles_per_cta; t *= 2) unit *= 0.5f;
+    return unit;
+}
+
 cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream) {
     Params p{};
     p.q_lat = a.q_lat;
@@ -977,6 +1003,7 @@ cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint
     p.k = a.k;
     p.groups = (a.H + kHeads - 1) / kHeads;
     p.out_bf16 = a.out_bf16;
+    p.part_unit = attn_q8_part_unit(a.tiles_per_cta);
     p.scale_log2 = a.sm_scale * 1.4426950408889634f;
     p.tiles_per_cta = a.tiles_per_cta;
     p.n_split = a.n_split;

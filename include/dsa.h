@@ -517,7 +517,8 @@ dsa_status_t dsa_kv_read_q8(const uint8_t *codes, const float *scale, int tail, 
  * Products are of 8-bit values with float32 sums.  Queries count to eight
  * significant bits (all of a bf16 value's) down to 2^-10 of their head's largest
  * value (or to 2^-122), weights to 2^-7 of themselves or 2^-15 of the largest;
- * the partial outputs of a token that several CTAs share are joined in bf16.
+ * the partial outputs of a token that several CTAs share are joined from eleven
+ * bits each (fp16, scaled).
  * Any positive scale serves, power of two or not; below 2^-40 it counts as
  * 2^-40.  Scales of a token's selected rows that lie further than 2^90 apart
  * cost the rows with the smaller ones their weight.  A selected row whose scale

@@ -305,3 +305,74 @@ def test_small_queries_over_large_rows(dsa, torch, lens, per, k, dq, drow, dsm):
         tol = (2 * (2.0 ** -7 + 2.0 ** -11) + 2 * 2.0 ** -8 + 2.0 ** -14) * (w @ np.abs(lat)) + \
             2 * 2.0 ** -14.9 * top * np.abs(lat / sc[rows][:, None]).sum(0)
         assert np.all(np.abs(f64(out[t]) * 2.0 ** -drow - f64(out0[t])) <= tol), t
+
+
+RMS = [
+    # lens, per, k, H: split decodes, then one CTA per token
+    ([4000] * 3, [1] * 3, 2048, 64),
+    ([4000, 3000], [1, 1], 600, 128),
+    ([4000], [1], 100, 64),
+    ([2500], [160], 2048, 16),
+    ([1500], [160], 300, 16),
+    ([1500], [160], 100, 16),
+]
+
+
+@pytest.mark.parametrize("lens,per,k,H", RMS)
+@pytest.mark.parametrize("out_dt", ["f32", "bf16"])
+def test_rms_error_of_the_outputs(dsa, torch, lens, per, k, H, out_dt):
+    """Worst cases over all rows say little about errors that average out, so
+    here their root mean square over everything, against the sum of squares of
+    the outputs.  Rounding v in [1, 2) of a binade is off by
+      an e4m3 piece and an e5m2 remainder: the first leaves an error uniform in
+        +-2^-4, whose rounding is uniform in +-2^-3 of its own binade: a mean
+        square of 2^-16 / 3 (1/2 + 1/16 + 1/128 ..) = 2^-16 / 3 * 4/7;
+      bf16: 2^-16 / 3;  fp16 (weights before their pieces, split partials): 2^-22 / 3.
+    v^2 is 3 / (2 ln 2) = 2.16 on average over weights spread over several
+    octaves, and at least 1.8 over normal outputs whatever their size.  Rows of
+    random signs add up in squares, so weights off by r leave outputs off by r.
+    A tenth is allowed on top for the drawn sizes.  Without the weights' remainder
+    the error is 4 to 16 times as large; partials in bf16 alone are off by
+    2^-8 / sqrt(3 * 1.85) = 1.66e-3, the float32 bound is 1.32e-3."""
+    s = Seqs(dsa, torch, lens, per)
+    codes, scale = fill_cache(dsa, torch, s, True, 0.3)
+    g = gen(torch, 19)
+    T, sm = s.batch.T, 1 / 16.0
+    q = torch.randn(T, H, 512, generator=g, device="cuda").to(torch.bfloat16)
+    qr = torch.randn(T, H, 64, generator=g, device="cuda").to(torch.bfloat16)
+    idx = selections(s, k)
+    out, _ = attend(dsa, torch, s, q, qr, codes, scale, idx, sm, {"f32": torch.float32, "bf16": torch.bfloat16}[out_dt])
+    c, sc = codes.cpu().numpy(), f64(scale)
+    err = size = 0.0
+    for t in range(0, T, 7 if T > 7 else 1):
+        rows = np.asarray(s.row(int(s.seq[t]), idx[t][idx[t] >= 0]))
+        ref = R.attention(f64(q[t]), f64(qr[t]), c, sc, rows, sm)[0]
+        err += ((f64(out[t]) - ref) ** 2).sum()
+        size += (ref ** 2).sum()
+    weights, half, bf16 = 2.0 ** -16 / 3 * 4 / 7, 2.0 ** -22 / 3, 2.0 ** -16 / 3
+    square = weights / 2.16 + 2 * half / 1.8 + (bf16 / 1.8 if out_dt == "bf16" else 0.0)
+    print(f"\nrms {lens[0]} {T} {k} {out_dt}: {np.sqrt(err / size):.3e} of {np.sqrt(square):.3e}")
+    assert np.sqrt(err / size) <= 1.1 * np.sqrt(square)
+
+
+def test_split_partials_at_their_largest(dsa, torch):
+    """Rows of the largest code throughout, and weights of nearly 2^8 in all but
+    the first tile of each split (which sets the reference): the partial sums
+    come as near to fp16's range as they can (six tiles of 128 rows a split), and
+    the output is those rows' value, off by the weights' 2^-7 + 2^-11 and the
+    partials' 2^-11."""
+    T, k, sm = 40, 2048, 0.01                              # 3 splits a token
+    s = Seqs(dsa, torch, [2100], [T])
+    x = torch.full((s.rows, 576), 448.0, device="cuda")
+    x[:, 512:] = 0.0
+    at = torch.arange(s.rows, device="cuda")
+    x[at // 128 % 6 > 0, 512] = 415.0                      # 2^5.987 times the first tile's weight, 2^2
+    b = dsa.Batch.from_host([0, s.rows], range(s.rows), [0], s.rows)
+    codes, scale = dsa.q8_cache(s.rows)
+    dsa.dsa_kv_append_q8(x[:, :512], x[:, 512:], b, None, codes, scale, s.ws)
+    q = torch.zeros(T, 64, 512, dtype=torch.bfloat16, device="cuda")
+    qr = torch.zeros(T, 64, 64, dtype=torch.bfloat16, device="cuda")
+    qr[:, :, 0] = 1.0
+    idx = np.tile(np.arange(k, dtype=np.int32), (T, 1))
+    out, _ = attend(dsa, torch, s, q, qr, codes, scale, idx, sm)
+    assert ((out - 448.0).abs() <= 448.0 * (2.0 ** -7 + 2.0 ** -10)).all(), (float(out.min()), float(out.max()))
