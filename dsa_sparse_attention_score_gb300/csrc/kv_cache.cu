@@ -12,10 +12,10 @@
 // row is three dependent loads long, so with many tokens a warp takes two at a
 // time, their lookups side by side in two lanes and their rows in flight
 // together.
-// Device times: appending 32 tokens, 8-bit and paged, 2.9 us (launch latency);
-// 16384 tokens 8.4 us (3.5 TB/s: under two rows per warp that can be resident, so half
-// the time is the chain of lookups); reading back 2048 tokens 3.0 us, 128k
-// tokens 38 us (6.0 TB/s, 88% of a plain copy's rate).
+// Device times: appending 32 tokens, 8-bit and paged, 2.6 us (launch latency);
+// 16384 tokens 8.2 us (3.6 TB/s: under two rows per warp that can be resident, so half
+// the time is the chain of lookups); reading back 2048 tokens 2.6 us, 128k
+// tokens 37.5 us (6.1 TB/s, 90% of a plain copy's rate).
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 #include "quant8.cuh"

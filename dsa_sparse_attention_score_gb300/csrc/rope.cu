@@ -12,8 +12,9 @@
 // are found once, and its loads are out before the angles are formed (rot_dim
 // / 2 of them, once per CTA).  Rows whose addresses or extents are not
 // multiples of 16 bytes take the same kernel with units of one value.
-// 4096 tokens x 128 heads x 64 values, in and out of HBM: 25 us (5.3 TB/s) for
-// pairs of neighbours, 30 us for halves.
+// In and out of HBM, on the device: 4096 tokens x 128 heads x 64 values, pairs of
+// neighbours, 22.3 us (6.0 TB/s); 4093 x 64 heads of 128, halves of the first 64
+// turned and the rest copied, 25.2 us (5.3 TB/s).
 #include <algorithm>
 
 #include "dsa_common.cuh"
@@ -79,8 +80,9 @@ constexpr __host__ __device__ int padded(int j) { return j + (j >> 3); }
 // inside it.  Halves: a unit is V values of either half, and its partner's
 // values are read a second time (from L1), so that a head's loads and stores
 // stay whole lines; with units of both halves, whose loads are half lines for
-// 64 16-bit values, the same tokens took 37 us against 30.  V = 1: a pair, or
-// one copied value.  grid: token, block of heads, block of a head's units.
+// 64 16-bit values, the same tokens took a quarter longer (37 us against 30,
+// both before later steps).  V = 1: a pair, or one copied value.  grid: token,
+// block of heads, block of a head's units.
 template <typename T, bool kInter, int V>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams p) {
     __shared__ float2 cs[padded(kMaxPairs)];

@@ -12,13 +12,15 @@
 //  - A bf16 query is the sum of two e4m3 pieces: q 2^-e = hi + lo with
 //    hi = e4m3(q 2^-e), lo = e4m3(q 2^-e - hi).  Four significant bits each,
 //    the remainder signed, hold bf16's eight: the split is exact for values
-//    above 2^-10 of the head's largest, and off by 2^-19 of it below.
+//    above 2^-9.8 of the head's largest, and off by at most 2^-17.8 of it below.
 //  - A weight is an e4m3 piece and an e5m2 remainder, in units where the
 //    largest lies in [2^2, 2^8]: off by at most 2^-7 of itself (rms 2^-9.7, as
 //    for a rounding to bf16) or 2^-15 of the largest.  e5m2 keeps three
 //    significant bits of the remainder but reaches down to 2^-16, which buys
 //    six octaves of headroom before the units have to move; with e4m3
 //    remainders and 4.5 octaves 40% of the tiles moved some head's.
+//  - A split's partial output is fp16 times a power of two that keeps its
+//    largest sum in range (attn_q8_part_unit).
 // So every product is 8-bit by 8-bit with float32 sums, at twice the rate of
 // bf16 products and half the bytes: the two pieces cost what one bf16 product
 // would, and the rows come in at 644 bytes instead of 1152.
@@ -48,9 +50,9 @@
 // the question whether any weight does.
 //
 // Measured, one call after the other over three sets of inputs, 64 heads: a
-// prefill chunk of 2048 tokens over 2048 rows each 634 us (921 TFLOP/s counted as
+// prefill chunk of 2048 tokens over 2048 rows each 638 us (915 TFLOP/s counted as
 // for bf16, 48% of what the tensor cores do on one large bf16 product); a decode
-// step of 8 sequences over 2048 rows 16.5 us and of 32 sequences 29.4 us, the join
+// step of 8 sequences over 2048 rows 16.7 us and of 32 sequences 29.6 us, the join
 // of the splits included (3.5 us).  What bounds it:
 //  - A tile takes about 4600 cycles, and a unit 16 of them and some 11000 for
 //    its outputs and the next one's queries.  The products read their operands
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
         // ---------------- queries, softmax and epilogue
         const int sw = warp - kFirstSoftmax, tx = (int)threadIdx.x - 32 * kFirstSoftmax;
         const int quarter = sw & 3;                        // TMEM lanes 32*quarter ..
-        const int part = sw >> 2;                          // heads 16*part ..
+        const int part = sw >> 2;                          // heads 32*part ..
         const int hb = kPartHeads * part;
         const int r = quarter * 32 + lane;                 // row within the tile
         const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
@@ -881,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_attn_q8_kernel(const __gri
             const int64_t row0 = (int64_t)w.t * p.H + w.h0;
             const int64_t part0 = (((int64_t)w.t * p.n_split + w.split) * p.groups + w.h0 / kHeads) * kHeads;
             if (alive && none) {
-                write_empty(p, w, tx);                            // whatever the queries are, NaN among them
+                write_empty(p, w, tx);                     // whatever the queries are, NaN among them
             } else if (alive) {
                 // Thread (quarter, lane) holds output dim 128 c + 32 quarter +
                 // lane of the part's heads.  Of 16-bit results neighbouring lanes

@@ -469,7 +469,7 @@ dsa_status_t dsa_rope(const void *x, int64_t x_token_stride, int64_t x_head_stri
  *   codes  uint8 [cache_rows, 640]: 512 e4m3 codes of the latent | 64 of the
  *          tail | 64 of the tail's remainders; [cache_rows, 512] without a tail
  *   scale  float32 [cache_rows]: 2^E, E the least integer in [-40, 119] with
- *          max |x| <= 448 * 2^E
+ *          max |x| <= 448 * 2^E (larger values are held as 448 * 2^119)
  *   latent value = 2^E e4m3(x / 2^E)
  *   tail value   = 2^E (hi + lo), hi = e4m3(x / 2^E), lo = e4m3(x / 2^E - hi)
  * (round to nearest even; 644 bytes a token against 1152 in bf16).  A row
@@ -515,7 +515,7 @@ dsa_status_t dsa_kv_read_q8(const uint8_t *codes, const float *scale, int tail, 
  *   the rest   as dsa_sparse_mla_attn, with its workspace (DSA_OP_SPARSE_ATTN)
  *              and dsa_decode_paged's meaning of paging
  * Products are of 8-bit values with float32 sums.  Queries count to eight
- * significant bits (all of a bf16 value's) down to 2^-10 of their head's largest
+ * significant bits (all of a bf16 value's) down to 2^-9 of their head's largest
  * value (or to 2^-122), weights to 2^-7 of themselves or 2^-15 of the largest;
  * the partial outputs of a token that several CTAs share are joined from eleven
  * bits each (fp16, scaled).
