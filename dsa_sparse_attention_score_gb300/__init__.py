@@ -49,6 +49,7 @@ DSA_OP_TOPK = 2
 DSA_OP_SPARSE_ATTN = 3
 DSA_OP_DECODE = 4
 DSA_OP_KPOOL = 5
+DSA_OP_MLA_ATTN = 6
 
 KPOOL = 4            # positions per pool of the kpool indexer
 KPOOL_ROW = 257      # fp16 values per packed indexer row: k | gate | valid
@@ -100,6 +101,8 @@ SIGNATURES = {
     "dsa_kv_append_q8": (_I, [_P, _I64, _P, _I64, _I, _BP, _P, _P, _P, _P, _P, _SZ, _P]),
     "dsa_kv_read_q8": (_I, [_P, _P, _I, _BP, _P, _P, _I, _I64, _P, _SZ, _P]),
     "dsa_sparse_mla_attn_q8": (_I, [_P, _P, _P, _P, _BP, _P, _P, _I, _I, _F, _P, _I, _P, _P, _SZ, _P]),
+    "dsa_mla_attn": (_I, [_P, _P, _P, _BP, _P, _I, _F, _P, _I, _P, _P, _SZ, _P]),
+    "dsa_mla_attn_window": (_I, [_P, _P, _P, _BP, _P, _I, _I, _I, _P, _F, _P, _I, _P, _P, _SZ, _P]),
     "dsa_version": (_I, []),
 }
 
@@ -713,6 +716,51 @@ def dsa_sparse_mla_attn_q8(q_lat, q_rope, codes, scale, batch: Batch, idx, sm_sc
           q_rope.data_ptr() if q_rope is not None else None, codes.data_ptr(), scale.data_ptr(),
           C.byref(_batch_desc(batch, dev)), _paging(block_table, block_size, batch, dev), idx.data_ptr(), k, H, sm_scale,
           out.data_ptr(), dt, lse.data_ptr() if lse is not None else None, *_workspace_arg(ws, dev))
+
+
+def _mla_args(q_lat, q_rope, kv_cache, batch: Batch, out, lse, ws, block_table, block_size, dev):
+    """Checked arguments of the calls over all visible rows: up to H, and from out on."""
+    T, H = batch.q_pos.numel(), q_lat.shape[1]
+    _shaped(q_lat, "q_lat", _t_bf16, (T, H, 512), dev)
+    if q_rope is not None:
+        _shaped(q_rope, "q_rope", _t_bf16, (T, H, 64), dev)
+    rows = kv_cache.shape[0]
+    _shaped(kv_cache, "kv_cache", _t_bf16, (rows, 512 if q_rope is None else 576), dev)
+    if rows < batch.cache_rows:
+        raise TypeError(f"kv_cache: {rows} rows, the batch names {batch.cache_rows}")
+    dt = _dt(out, "out", _OUT_FLOAT)
+    _shaped(out, "out", out.dtype, (T, H, 512), dev)
+    if lse is not None:
+        _shaped(lse, "lse", _t_f32, (T, H), dev)
+    return ((q_lat.data_ptr(), q_rope.data_ptr() if q_rope is not None else None, kv_cache.data_ptr(),
+             C.byref(_batch_desc(batch, dev)), _paging(block_table, block_size, batch, dev), H),
+            (out.data_ptr(), dt, lse.data_ptr() if lse is not None else None, *_workspace_arg(ws, dev)))
+
+
+def dsa_mla_attn(q_lat, q_rope, kv_cache, batch: Batch, sm_scale: float, out, lse, ws, block_table=None,
+                 block_size: int = 0, stream=None):
+    """Attention of q_lat [T, H, 512] (and tails q_rope [T, H, 64], or None) over
+    all the cached rows each token sees; kv_cache [rows, 576] ([rows, 512] without
+    tails), out [T, H, 512] float32 or bfloat16, lse [T, H] float32 or None."""
+    if not _DT:
+        _bind()
+    dev = _cuda(q_lat, "q_lat")
+    a, z = _mla_args(q_lat, q_rope, kv_cache, batch, out, lse, ws, block_table, block_size, dev)
+    _call("dsa_mla_attn", dev, stream, lib().dsa_mla_attn, *a, sm_scale, *z)
+
+
+def dsa_mla_attn_window(q_lat, q_rope, kv_cache, batch: Batch, window: int, n_sink: int, sink_pos0, sm_scale: float, out,
+                        lse, ws, block_table=None, block_size: int = 0, stream=None):
+    """dsa_mla_attn over the last `window` positions of each token and the first
+    n_sink of its sequence (from sink_pos0[b], int32 [B], or 0 when None)."""
+    if not _DT:
+        _bind()
+    dev = _cuda(q_lat, "q_lat")
+    a, z = _mla_args(q_lat, q_rope, kv_cache, batch, out, lse, ws, block_table, block_size, dev)
+    if sink_pos0 is not None:
+        _shaped(sink_pos0, "sink_pos0", _t_i32, (batch.B,), dev)
+    _call("dsa_mla_attn_window", dev, stream, lib().dsa_mla_attn_window, *a, window, n_sink,
+          sink_pos0.data_ptr() if sink_pos0 is not None else None, sm_scale, *z)
 
 
 def dsa_set_trace_events(events):

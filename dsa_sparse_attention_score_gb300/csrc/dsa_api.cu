@@ -145,6 +145,10 @@ inline int kpool_width(int top_k) { return kpool_pools(top_k) * kKpool + kKpool 
 Layout layout(int op, const dsa_batch_t *b, int H, int k) {
     Layout L;
     size_t off = kStatusBytes;
+    if (op == DSA_OP_MLA_ATTN) {
+        L.total = mla_attn_workspace(b->total_q, b->batch, H);
+        return L;
+    }
     if (op == DSA_OP_KPOOL) {
         // score slab over pools, the selected pools, the expanded positions,
         // then the attention's split partials over those positions
@@ -305,13 +309,14 @@ dsa_status_t dsa_set_test_faults(uint64_t wait_limit_ns, int skip_copies) {
 
 dsa_status_t dsa_workspace_size(int op, const dsa_batch_t *batch, int H_I, int H, int k, size_t *bytes) {
     (void)H_I;
-    if (!bytes || op < DSA_OP_K_APPEND || op > DSA_OP_KPOOL) return DSA_ERR_INVALID_ARGUMENT;
+    if (!bytes || op < DSA_OP_K_APPEND || op > DSA_OP_MLA_ATTN) return DSA_ERR_INVALID_ARGUMENT;
     if (!batch || batch->batch < 1 || batch->total_q < 1 || batch->max_q_per_seq < 1 || batch->max_kv < 1)
         return DSA_ERR_INVALID_ARGUMENT;
     if ((op == DSA_OP_TOPK || op == DSA_OP_SPARSE_ATTN || op == DSA_OP_DECODE) && (k < 1 || k > 65536))
         return DSA_ERR_UNSUPPORTED;
     if (op == DSA_OP_KPOOL && (k < 1 || k > kKpoolMaxTopK)) return DSA_ERR_UNSUPPORTED;
-    if ((op == DSA_OP_SPARSE_ATTN || op == DSA_OP_DECODE || op == DSA_OP_KPOOL) && (H < 1 || H > kMaxHeads))
+    if ((op == DSA_OP_SPARSE_ATTN || op == DSA_OP_DECODE || op == DSA_OP_KPOOL || op == DSA_OP_MLA_ATTN) &&
+        (H < 1 || H > kMaxHeads))
         return DSA_ERR_UNSUPPORTED;
     *bytes = layout(op, batch, H, k).total;
     return DSA_OK;
@@ -935,6 +940,64 @@ dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rop
     const Layout L = layout(DSA_OP_SPARSE_ATTN, batch, H, k);
     if ((s = check_ws(ws, ws_bytes, L.total)) != DSA_OK) return s;
     return run_attention_q8(q_lat, q_rope, codes, scale, db, idx, k, H, sm_scale, out, out_dtype, lse, ws, L, stream);
+}
+
+// ---------------------------------------------------------------- attention over all visible rows
+
+static dsa_status_t mla_attn_impl(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const dsa_bf16 *kv_cache,
+                                  const dsa_batch_t *batch, const dsa_paging_t *paging, int H, int window, int n_sink,
+                                  const int32_t *sink_pos0, float sm_scale, void *out, int out_dtype, float *lse, void *ws,
+                                  size_t ws_bytes, cudaStream_t stream) {
+    DevBatch db;
+    dsa_status_t s = cache_batch(batch, paging, &db);
+    if (s != DSA_OK) return s;
+    if (!q_lat || !kv_cache || !out || (out_dtype != DSA_DT_BF16 && out_dtype != DSA_DT_F32)) return DSA_ERR_INVALID_ARGUMENT;
+    if (H < 1 || H > kMaxHeads) return DSA_ERR_UNSUPPORTED;
+    if ((int64_t)batch->total_q * H > INT32_MAX - 256 ||
+        !mla_attn_countable(batch->total_q, batch->batch, H, batch->max_kv))
+        return DSA_ERR_UNSUPPORTED;
+    if (!aligned(q_lat, 16) || (q_rope && !aligned(q_rope, 16)) || !aligned(kv_cache, 16) || !aligned(out, 16) ||
+        (lse && !aligned(lse, 4)) || (sink_pos0 && !aligned(sink_pos0, 4)))
+        return DSA_ERR_MISALIGNED;
+    if ((s = check_ws(ws, ws_bytes, layout(DSA_OP_MLA_ATTN, batch, H, 1).total)) != DSA_OK) return s;
+    const int tail = q_rope ? 1 : 0;
+    const uint64_t qrows = (uint64_t)batch->total_q * H, rows = (uint64_t)batch->cache_rows, width = tail ? D_ROW : D_L;
+    const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    MlaMaps m;
+    // without a tail the kernel never reads the tail queries' map (it gets the latent one)
+    if (!make_map(&m.q_lat, bf16, q_lat, D_L, qrows, 64, 64) ||
+        !make_map(&m.q_rope, bf16, tail ? q_rope : q_lat, tail ? D_R : D_L, qrows, 64, 64) ||
+        !make_map(&m.kv64, bf16, kv_cache, width, rows, 64, 64) || !make_map(&m.kv16, bf16, kv_cache, width, rows, 64, 16) ||
+        !make_map(&m.kv1, bf16, kv_cache, width, rows, 64, 1))
+        return DSA_ERR_CUDA;
+    MlaLaunch a;
+    a.H = H;
+    a.tail = tail;
+    a.window = window;
+    a.n_sink = n_sink;
+    a.sink_pos0 = sink_pos0;
+    a.sm_scale = sm_scale;
+    a.out = out;
+    a.out_bf16 = out_dtype == DSA_DT_BF16;
+    a.lse = lse;
+    DSA_TRY_CUDA(launch_mla_attn(a, m, db, ws, stream));
+    return DSA_OK;
+}
+
+dsa_status_t dsa_mla_attn(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const dsa_bf16 *kv_cache, const dsa_batch_t *batch,
+                          const dsa_paging_t *paging, int H, float sm_scale, void *out, int out_dtype, float *lse, void *ws,
+                          size_t ws_bytes, cudaStream_t stream) {
+    return mla_attn_impl(q_lat, q_rope, kv_cache, batch, paging, H, INT32_MAX, 0, nullptr, sm_scale, out, out_dtype, lse, ws,
+                         ws_bytes, stream);
+}
+
+dsa_status_t dsa_mla_attn_window(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const dsa_bf16 *kv_cache,
+                                 const dsa_batch_t *batch, const dsa_paging_t *paging, int H, int window, int n_sink,
+                                 const int32_t *sink_pos0, float sm_scale, void *out, int out_dtype, float *lse, void *ws,
+                                 size_t ws_bytes, cudaStream_t stream) {
+    if (window < 1 || n_sink < 0) return DSA_ERR_INVALID_ARGUMENT;
+    return mla_attn_impl(q_lat, q_rope, kv_cache, batch, paging, H, window, n_sink, sink_pos0, sm_scale, out, out_dtype, lse,
+                         ws, ws_bytes, stream);
 }
 
 }  // extern "C"

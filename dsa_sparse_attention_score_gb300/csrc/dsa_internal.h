@@ -216,9 +216,29 @@ int attn_q8_tile_rows();
 float attn_q8_part_unit(int tiles_per_cta);   // factor on the fp16 split partials, a power of two
 cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint32_t *status, cudaStream_t stream);
 
+// Attention over all visible rows of the latent cache, or those of a window and
+// the first ones (mla_attn.cu): two or three launches.
+struct MlaLaunch {
+    int H, tail;                      // tail 0: 512-wide rows
+    int window;                       // INT32_MAX: every position up to the token's
+    int n_sink;
+    const int32_t *sink_pos0;         // [B] or null
+    float sm_scale;
+    void *out;                        // [T, H, 512] float32, or bf16 with out_bf16
+    int out_bf16;
+    float *lse;                       // [T, H] or null
+};
+struct MlaMaps {
+    CUtensorMap q_lat, q_rope;        // 64-row boxes of the query rows [T * H, 512] and [T * H, 64]
+    CUtensorMap kv64, kv16, kv1;      // the cache in boxes of 64, 16 and 1 rows
+};
+size_t mla_attn_workspace(int T, int B, int H);
+bool mla_attn_countable(int T, int B, int H, int max_kv);   // do the plan's counts fit
+cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBatch &b, void *ws, cudaStream_t stream);
+
 // Sets a kernel's dynamic shared-memory limit once per device; `slot`
 // (0..kSmemAttrSlots-1) names the kernel instance.
-constexpr int kSmemAttrSlots = 12;
+constexpr int kSmemAttrSlots = 13;
 cudaError_t ensure_smem_attr(const void *func, int slot, size_t bytes);
 
 // Rows of one attention tile (the unit of the split across CTAs).

@@ -1,0 +1,1016 @@
+// mla_attn.cu -- attention of every query head over all the cached latent
+// rows that its token sees (or those in a sliding window and the first ones):
+//     z_s = sm_scale * (q_lat . c_s[0:512] + q_rope . c_s[512:576]),
+//     o   = sum_s softmax(z)_s c_s[0:512],   lse = log(sum_s exp(z_s)).
+//
+// The query rows (token, head) of a sequence are taken 128 at a time, whatever
+// the head count; such an item meets its visible rows in tiles of 128
+// positions.  A cluster of two CTAs works on an item with cta_group::2 MMAs:
+//     S[row, s]   = Q[row, 0:576] . C[s, 0:576]^T     (M=128, N=128, K=576)
+//     O[row, dim] += P[row, s] . C[s, dim]             (M=128, N=2x256, K=128)
+// An O of 128 rows and 512 dims would fill the tensor memory of one SM.  With
+// M=128 over a pair of SMs each holds 64 rows, a row's first N / 2 columns in
+// lane r and the rest in lane r + 64: O takes 256 columns, two S buffers take 128.
+// Measured on GB300, this form runs at 4093 multiply-adds a clock and SM (all
+// the tensor core has), also while 64 bytes a clock come in through TMA.
+// Each CTA's shared memory holds
+//   its 64 query rows                                  72 KB
+//   its 64 of the tile's keys, nine 64-column blocks   72 KB   (B of S)
+//   all 128 rows of its 256 of the output dims         64 KB   (B of O)
+//   P of its 64 rows                                   16 KB
+// The value rows are read a second time from L2 because a pair's B operand lies
+// at one address in both CTAs: S wants a CTA's own keys there, O all keys.
+//
+// Per tile S takes 1152 clocks and O 1024.  The tensor core runs S(i+1), O(i),
+// S(i+2), O(i+1)...: the softmax of tile i+1 has the time of O(i) and S(i+2).
+// Keys are refilled in three groups of blocks and values in two halves, each as
+// soon as the product that read it is done, which leaves every copy more than
+// 1600 clocks to land.
+//
+// The work is cut by tiles, not by items: the tiles of all items in a row are
+// divided evenly among the clusters.  An item that several clusters share gets
+// its parts (unnormalised O, running maximum, sum) into the workspace, and
+// mla_combine_kernel joins them.
+#include "dsa_common.cuh"
+#include "dsa_internal.h"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kRows = 128;                    // query rows of an item
+constexpr int kHalf = 64;                     // rows and keys of one CTA
+constexpr int kKeys = 128;                    // positions of a tile
+constexpr int kGroup = 16;                    // keys of one MMA step of O
+constexpr int kBlock = kHalf * 128;           // 64 rows x 64 bf16: 8 KB
+constexpr int kQOff = 0;                      // nine blocks
+constexpr int kKOff = 9 * kBlock;             // nine blocks
+constexpr int kVOff = 18 * kBlock;            // [half j][64-dim block][128 keys]: eight blocks
+constexpr int kPOff = 26 * kBlock;            // two blocks
+constexpr int kCtlOff = 28 * kBlock;
+constexpr int kVHalf = 4 * kBlock;
+constexpr int kSoftmaxWarps = 4;
+constexpr int kMmaWarp = 4, kKWarp = 5, kVWarp = 6, kQWarp = 7;
+constexpr int kThreads = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColS = 256;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kItemCost = 1;                  // what an item costs beside its tiles, in tiles
+
+struct Ctl {
+    uint64_t k_full[3], k_empty[3];
+    uint64_t v_full[2], v_empty[2];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full, o_full;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    float red[2][kRows];
+};
+constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+
+// ---------------------------------------------------------------- pairs of CTAs
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t n) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(n) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t n) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(n) : "memory");
+}
+__device__ __forceinline__ void umma2_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// One arrival at the same barrier of both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void commit2(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// TMA copies into this CTA that complete on a barrier of either CTA.
+__device__ __forceinline__ void tma2_load(uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t col, int32_t row) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(col), "r"(row), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma2_gather4(uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t col, int4 r) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(col), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_remote(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// ---------------------------------------------------------------- work
+
+// What a call attends over, in device terms.
+struct Problem {
+    DevBatch b;
+    int H;
+    int window;                   // INT32_MAX: every position
+    int n_sink;
+    const int32_t *sink_pos0;     // null: 0
+};
+
+// Up to 128 query rows of one sequence and the positions some of them see:
+// [lo, hi] and the first ones [s_lo, s_hi), as tiles of the grid of 128.
+struct Item {
+    int seq, row0, nrows;         // flat rows (token * H + head)
+    int lo, hi, s_lo, s_hi;       // hi < 0: nothing
+    int min_pos;                  // the least position of its tokens (those that see anything)
+    int first_tile, n_first;      // tiles of the first positions before those of [lo, hi]
+    int tile0, n;                 // first tile of [lo, hi]; all tiles
+};
+
+__device__ __forceinline__ int item_cost(int n) { return n + kItemCost; }
+
+__device__ __forceinline__ void item_tiles(const Problem &p, Item &it) {
+    it.n = it.n_first = 0;
+    it.s_lo = it.s_hi = 0;
+    it.lo = 0;
+    it.tile0 = it.first_tile = 0;
+    if (it.hi < 0) return;
+    // 64 bits: a window near 2^31 must not wrap
+    it.lo = (int)max((int64_t)0, (int64_t)it.min_pos - p.window + 1);
+    it.tile0 = it.lo / kKeys;
+    it.n = it.hi / kKeys - it.tile0 + 1;
+    if (p.n_sink > 0) {
+        const int a = p.sink_pos0 ? max(0, __ldg(p.sink_pos0 + it.seq)) : 0;
+        const int e = (int)min((int64_t)a + p.n_sink, (int64_t)it.hi + 1);
+        if (a < e) {
+            it.s_lo = a;
+            it.s_hi = e;
+            it.first_tile = a / kKeys;
+            it.n_first = max(0, min((e - 1) / kKeys + 1, it.tile0) - it.first_tile);
+            it.n += it.n_first;
+        }
+    }
+}
+// Position of tile i's first key.
+__device__ __forceinline__ int tile_pos(const Item &it, int i) {
+    return (i < it.n_first ? it.first_tile + i : it.tile0 + i - it.n_first) * kKeys;
+}
+__device__ __forceinline__ bool seen_by_some(const Item &it, int pos) {
+    return (pos >= it.lo && pos <= it.hi) || (pos >= it.s_lo && pos < it.s_hi);
+}
+// The tile's groups of 16 keys with a position that some row sees, one bit each.
+__device__ __forceinline__ uint32_t tile_groups(const Item &it, int p0) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int g = 0; g < kKeys / kGroup; ++g) {
+        const int a = p0 + g * kGroup, e = a + kGroup - 1;
+        if ((e >= it.lo && a <= it.hi) || (e >= it.s_lo && a < it.s_hi)) m |= 1u << g;
+    }
+    return m;
+}
+
+// The plan of a call, in the workspace.
+struct PlanHead {
+    int32_t total;                // costs of all items
+    int32_t clusters;             // clusters with work: every one has some
+};
+struct PlanItem { int32_t seq, row, cost0, pad; };   // row within the sequence; costs before it
+struct Start { int32_t item, off; };                 // a cluster's first item and the costs of it done before
+struct Split { int32_t row0, nrows, first, parts; }; // an item that begins in a cluster and ends in a later one
+
+struct MlaParams {
+    Problem pr;
+    uint32_t *status;
+    const PlanHead *head;
+    const PlanItem *items;
+    const Start *start;
+    Split *split;                 // [clusters]
+    float *part_o;                // [2 * clusters, 128, 512]
+    float *part_ml;               // [2 * clusters, 128, 2]
+    void *out;
+    int out_bf16;
+    float *lse;
+    float scale_log2;
+    int tail;                     // rows of 576 (1) or 512 (0)
+    int rows_per_box;             // 64, 16 or 0: rows that lie together for certain (pages)
+};
+
+// Token position if the token is in order, else -1 (flagged unless it is padding).
+__device__ __forceinline__ int token_pos(const DevBatch &b, int t, uint32_t *status) {
+    const int p = __ldg(b.q_pos + t);
+    if (p >= 0 && p < b.max_kv) return p;
+    if (p != -1) flag(status, DSA_DEV_BAD_POSITION);
+    return -1;
+}
+// The row of a position that a token holds, -1 if there is none.
+__device__ __forceinline__ int64_t own_row(const DevBatch &b, int seq, int64_t kv0, int pos) {
+    const int64_t r = kv0 < 0 ? -1 : cache_row(b, seq, kv0, pos);
+    return r >= 0 && r < b.cache_rows ? r : -1;
+}
+
+// Loads an item with a whole warp.
+__device__ __forceinline__ Item load_item(const MlaParams &p, int index, int lane) {
+    const DevBatch &b = p.pr.b;
+    Item it;
+    const PlanItem pi = p.items[index];
+    it.seq = pi.seq;
+    const int t0 = __ldg(b.cu_q + pi.seq), t1 = __ldg(b.cu_q + pi.seq + 1);
+    it.row0 = t0 * p.pr.H + pi.row;
+    it.nrows = min(kRows, t1 * p.pr.H - it.row0);
+    const int ta = it.row0 / p.pr.H, tb = (it.row0 + it.nrows - 1) / p.pr.H;
+    int lo = INT32_MAX, hi = -1;
+    for (int t = ta + lane; t <= tb; t += 32) {
+        const int pos = __ldg(b.q_pos + t);
+        if (pos >= 0 && pos < b.max_kv) {
+            lo = min(lo, pos);
+            hi = max(hi, pos);
+        }
+    }
+    it.min_pos = __reduce_min_sync(0xffffffffu, lo);
+    it.hi = __reduce_max_sync(0xffffffffu, hi);
+    item_tiles(p.pr, it);
+    return it;
+}
+
+// The pieces of items that a cluster works on, in order.
+struct Pieces {
+    int item, off, left;          // next item, costs of it done, costs left to this cluster
+    int t0, t1;                   // tiles of the current piece
+    bool whole, first;            // all tiles of the item; the item's first tile is among them
+    Item it;
+    __device__ Pieces(const MlaParams &p, int cluster) {
+        const int64_t total = p.head->total;
+        const int n = p.head->clusters;
+        item = off = left = 0;
+        if (cluster >= n) return;
+        const Start s = p.start[cluster];
+        item = s.item;
+        off = s.off;
+        left = (int)(total * (cluster + 1) / n - total * cluster / n);
+    }
+    __device__ bool next(const MlaParams &p, int lane) {
+        while (left > 0) {
+            it = load_item(p, item, lane);
+            const int cost = item_cost(it.n), take = min(left, cost - off);
+            t0 = min(off, it.n);
+            t1 = min(off + take, it.n);
+            whole = t0 == 0 && t1 == it.n;
+            first = off == 0;
+            left -= take;
+            off += take;
+            if (off == cost) {
+                ++item;
+                off = 0;
+            }
+            if (t1 > t0 || (it.n == 0 && first)) return true;
+        }
+        return false;
+    }
+};
+
+// Bounded wait of a whole warp; the same answer in every lane.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
+    bool ok = try_wait_cluster(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = global_ns();
+        while (!ok && !*(volatile int32_t *)&c.abort_flag) {
+            ok = try_wait_cluster(bar, parity);
+            if (!ok && global_ns() - t0 > limit_ns) {
+                *(volatile int32_t *)&c.abort_flag = 1;
+                flag(status, DSA_DEV_TIMEOUT);
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// Cache row of a position that some row of the item sees; `spare` (a row that is
+// there) for any other position, and for one in an unmapped block.
+__device__ __forceinline__ int32_t row_or_spare(const MlaParams &p, const Item &it, int64_t kv0, int pos, int32_t spare,
+                                                bool report) {
+    if (!seen_by_some(it, pos)) return spare;
+    const int64_t r = own_row(p.pr.b, it.seq, kv0, pos);
+    if (r >= 0) return (int32_t)r;
+    if (report) flag(p.status, DSA_DEV_BAD_INDEX);
+    return spare;
+}
+
+// A row of the cache that may be read for positions that no row sees: the one of
+// the item's last position, row 0 if that has none (no row sees anything then).
+__device__ __forceinline__ int32_t spare_row(const MlaParams &p, const Item &it, int64_t kv0) {
+    const int64_t r = it.hi < 0 ? -1 : own_row(p.pr.b, it.seq, kv0, it.hi);
+    return r < 0 ? 0 : (int32_t)r;
+}
+
+}  // namespace
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mla_attn_kernel(const MlaParams p, const __grid_constant__ CUtensorMap q_lat_map,
+                    const __grid_constant__ CUtensorMap q_rope_map, const __grid_constant__ CUtensorMap kv64_map,
+                    const __grid_constant__ CUtensorMap kv16_map, const __grid_constant__ CUtensorMap kv1_map) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctl &ctl = *reinterpret_cast<Ctl *>(smem + kCtlOff);
+    const uint32_t s0 = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int cluster = blockIdx.x >> 1;
+    const DevBatch &b = p.pr.b;
+    if (s0 & 1023u) {             // the same in every CTA of the grid
+        if (threadIdx.x == 0) flag(p.status, DSA_DEV_SMEM_LAYOUT);
+        return;
+    }
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(smem_u32(&ctl.k_full[i]), 2);       // both CTAs' producers, and their bytes
+            mbar_init(smem_u32(&ctl.k_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl.v_full[i]), 2);
+            mbar_init(smem_u32(&ctl.v_empty[i]), 1);
+            mbar_init(smem_u32(&ctl.s_full[i]), 1);
+        }
+        mbar_init(smem_u32(&ctl.q_full), 2);
+        mbar_init(smem_u32(&ctl.q_empty), 1);
+        mbar_init(smem_u32(&ctl.p_full), 2 * kSoftmaxWarps);
+        mbar_init(smem_u32(&ctl.o_full), 1);
+        ctl.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc2(smem_u32(&ctl.tmem_base), kTmemCols);
+    if (warp == kKWarp && lane == 0) {
+        tma_prefetch_desc(&kv64_map);
+        tma_prefetch_desc(&q_lat_map);
+        tma_prefetch_desc(&q_rope_map);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem_base;
+    pdl_wait();
+    const uint64_t limit = b.wait_ns;
+    const int n_blocks = p.tail ? 9 : 8;
+
+    if (warp == kKWarp) {
+        // ---------------- keys: this CTA's 64 of each tile, in three groups of blocks
+        uint32_t g = 0;                                       // tiles so far
+        Pieces pc(p, cluster);
+        bool alive = true;
+        while (alive && pc.next(p, lane)) {
+            const int64_t kv0 = seq_base(b, pc.it.seq);
+            const int32_t spare = spare_row(p, pc.it, kv0);
+            for (int i = pc.t0; alive && i < pc.t1; ++i, ++g) {
+                const int pos = tile_pos(pc.it, i) + kHalf * (int)rank;
+                // rows of this lane's copies: one box of 64, four of 16, or quads of single
+                // rows.  Keys that nobody sees may be anything: their scores are masked.
+                int4 r = make_int4(0, 0, 0, 0);
+                const int step = p.rows_per_box ? p.rows_per_box : 4;   // keys of one copy
+                const int copies = kHalf / step;                       // of one block
+                const int mine = lane % copies;
+                if (p.rows_per_box) {
+                    // the box's first position; the rest of the box follows it
+                    const int a = pos + mine * step;
+                    int first = a;
+                    while (first < a + step && !seen_by_some(pc.it, first)) ++first;
+                    r.x = first < a + step ? row_or_spare(p, pc.it, kv0, first, spare + (first - a), true) - (first - a) : spare;
+                    r.x = max(r.x, 0);
+                } else {
+                    const int a = pos + mine * 4;
+                    r.x = row_or_spare(p, pc.it, kv0, a, spare, true);
+                    r.y = row_or_spare(p, pc.it, kv0, a + 1, spare, true);
+                    r.z = row_or_spare(p, pc.it, kv0, a + 2, spare, true);
+                    r.w = row_or_spare(p, pc.it, kv0, a + 3, spare, true);
+                }
+                for (int q = 0; q < 3; ++q) {
+                    if (!wait_bar(smem_u32(&ctl.k_empty[q]), (g & 1u) ^ 1u, ctl, p.status, limit)) {
+                        alive = false;
+                        break;
+                    }
+                    if (b.skip_copies) continue;
+                    const int nb = min(3, n_blocks - 3 * q);
+                    const uint32_t full = dsmem_map(smem_u32(&ctl.k_full[q]), 0);
+                    if (lane == 0) arrive_expect_remote(full, (uint32_t)(nb * kBlock));
+                    __syncwarp();
+                    for (int c = lane; c < nb * copies; c += 32) {
+                        // c % copies is lane % copies: copies divides 32
+                        const int kb = 3 * q + c / copies;
+                        const uint32_t dst = s0 + kKOff + kb * kBlock + mine * step * 128;
+                        if (p.rows_per_box == 64) tma2_load(dst, &kv64_map, full, kb * 64, r.x);
+                        else if (p.rows_per_box) tma2_load(dst, &kv16_map, full, kb * 64, r.x);
+                        else tma2_gather4(dst, &kv1_map, full, kb * 64, r);
+                    }
+                }
+            }
+        }
+    } else if (warp == kVWarp) {
+        // ---------------- values: all keys of a tile, this CTA's 256 dims in two halves.
+        // Groups of 16 keys that nobody sees are neither read nor multiplied; in a
+        // group that is seen in part the other rows are the spare one's copies
+        // (P is 0 there, and 0 times what an unused row may hold is not).
+        uint32_t g = 0;
+        Pieces pc(p, cluster);
+        bool alive = true;
+        while (alive && pc.next(p, lane)) {
+            const int64_t kv0 = seq_base(b, pc.it.seq);
+            const int32_t spare = spare_row(p, pc.it, kv0);
+            for (int i = pc.t0; alive && i < pc.t1; ++i, ++g) {
+                const int pos = tile_pos(pc.it, i), a = pos + 4 * lane;     // this lane's four keys
+                const uint32_t groups = tile_groups(pc.it, pos);
+                int4 r;
+                r.x = row_or_spare(p, pc.it, kv0, a, spare, false);
+                r.y = row_or_spare(p, pc.it, kv0, a + 1, spare, false);
+                r.z = row_or_spare(p, pc.it, kv0, a + 2, spare, false);
+                r.w = row_or_spare(p, pc.it, kv0, a + 3, spare, false);
+                // groups whose 16 rows are all seen and lie together
+                const int32_t group_row = __shfl_sync(0xffffffffu, r.x, lane & ~3);
+                const bool run = r.y == r.x + 1 && r.z == r.x + 2 && r.w == r.x + 3 && r.x == group_row + 4 * (lane & 3);
+                const uint32_t runs = __ballot_sync(0xffffffffu, run);
+                const bool box16 = ((runs >> (lane & ~3)) & 0xfu) == 0xfu;
+                const int32_t half_row = __shfl_sync(0xffffffffu, r.x, lane & 16);
+                const bool in_half = box16 && r.x == half_row + 4 * (lane & 15);
+                const uint32_t halves = __ballot_sync(0xffffffffu, in_half);
+                const bool box64 = ((halves >> (lane & 16)) & 0xffffu) == 0xffffu;
+                const bool on = (groups >> (lane >> 2)) & 1u;
+                const uint32_t bytes = (uint32_t)__popc(groups) * (kGroup * 128u) * 2u;
+                for (int j = 0; j < 2; ++j) {
+                    if (!wait_bar(smem_u32(&ctl.v_empty[j]), (g & 1u) ^ 1u, ctl, p.status, limit)) {
+                        alive = false;
+                        break;
+                    }
+                    if (b.skip_copies) continue;
+                    const uint32_t full = dsmem_map(smem_u32(&ctl.v_full[j]), 0);
+                    if (lane == 0) arrive_expect_remote(full, bytes);
+                    __syncwarp();
+                    for (int d = 0; d < 2; ++d) {
+                        const uint32_t dst = s0 + kVOff + j * kVHalf + d * (kVHalf / 2) + lane * 4 * 128;
+                        const int32_t col = 256 * (int)rank + 128 * j + 64 * d;
+                        if (box64) {
+                            if ((lane & 15) == 0) tma2_load(dst, &kv64_map, full, col, r.x);
+                        } else if (box16) {
+                            if ((lane & 3) == 0 && on) tma2_load(dst, &kv16_map, full, col, r.x);
+                        } else if (on) {
+                            tma2_gather4(dst, &kv1_map, full, col, r);
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp == kQWarp) {
+        // ---------------- queries: this CTA's 64 rows of each piece's item
+        uint32_t n = 0;
+        Pieces pc(p, cluster);
+        while (pc.next(p, lane)) {
+            if (pc.t1 == pc.t0) continue;
+            if (!wait_bar(smem_u32(&ctl.q_empty), (n & 1u) ^ 1u, ctl, p.status, limit)) break;
+            ++n;
+            if (b.skip_copies) continue;
+            const uint32_t full = dsmem_map(smem_u32(&ctl.q_full), 0);
+            if (lane == 0) arrive_expect_remote(full, (uint32_t)(n_blocks * kBlock));
+            __syncwarp();
+            // rows past the sequence's are some other token's (or zero past the
+            // tensor): they only feed accumulator rows that are never stored
+            const int row = pc.it.row0 + kHalf * (int)rank;
+            if (lane < 8) tma2_load(s0 + kQOff + lane * kBlock, &q_lat_map, full, lane * 64, row);
+            else if (lane < n_blocks) tma2_load(s0 + kQOff + lane * kBlock, &q_rope_map, full, 0, row);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------- MMA issuer: the even CTA's for both
+        if (rank == 0) {
+            constexpr uint32_t id_s = idesc_f16(kRows, kKeys, true, false, false);
+            constexpr uint32_t id_o = idesc_f16(kRows, 256, true, false, true);
+            const uint64_t qd = sdesc_sw128(s0 + kQOff, 16, 1024), kd = sdesc_sw128(s0 + kKOff, 16, 1024);
+            const uint64_t pd = sdesc_sw128(s0 + kPOff, 16, 1024), vd = sdesc_sw128(s0 + kVOff, kVHalf / 2, 1024);
+            uint32_t gs = 0, go = 0, n = 0;                   // tiles scored and summed, pieces
+            Pieces pc(p, cluster);
+            bool alive = true;
+            while (alive && pc.next(p, lane)) {
+                if (pc.t1 == pc.t0) continue;
+                if (!wait_bar(smem_u32(&ctl.q_full), n & 1u, ctl, p.status, limit)) break;
+                ++n;
+                for (int i = pc.t0; alive && i <= pc.t1; ++i) {
+                    if (i < pc.t1) {
+                        const uint32_t d_s = tmem + kColS + (gs & 1u) * (kKeys / 2);
+                        for (int q = 0; q < 3; ++q) {
+                            if (!wait_bar(smem_u32(&ctl.k_full[q]), gs & 1u, ctl, p.status, limit)) {
+                                alive = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const int nb = min(3, n_blocks - 3 * q);
+                            if (elect_one()) {
+                                for (int kb = 3 * q; kb < 3 * q + nb; ++kb) {
+                                    const uint64_t o = (uint64_t)(kb * (kBlock >> 4));
+#pragma unroll
+                                    for (int ks = 0; ks < 4; ++ks)
+                                        umma2_f16(d_s, qd + o + 2 * ks, kd + o + 2 * ks, id_s, (kb | ks) != 0);
+                                }
+                                commit2(smem_u32(&ctl.k_empty[q]));
+                                if (q == 2) commit2(smem_u32(&ctl.s_full[gs & 1u]));
+                                if (q == 2 && i == pc.t1 - 1) commit2(smem_u32(&ctl.q_empty));
+                            }
+                            __syncwarp();
+                        }
+                        ++gs;
+                    }
+                    if (!alive) break;
+                    if (i > pc.t0) {
+                        const uint32_t groups = tile_groups(pc.it, tile_pos(pc.it, i - 1));
+                        if (!wait_bar(smem_u32(&ctl.p_full), go & 1u, ctl, p.status, limit)) {
+                            alive = false;
+                            break;
+                        }
+                        for (int j = 0; j < 2; ++j) {
+                            if (!wait_bar(smem_u32(&ctl.v_full[j]), go & 1u, ctl, p.status, limit)) {
+                                alive = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            if (elect_one()) {
+                                uint32_t acc = i - 1 > pc.t0 ? 1u : 0u;
+                                const uint64_t vj = vd + (uint64_t)(j * (kVHalf >> 4));
+#pragma unroll
+                                for (int ks = 0; ks < kKeys / kGroup; ++ks) {
+                                    if (groups >> ks & 1u) {
+                                        umma2_f16(tmem + kColO + j * 128, pd + (ks >> 2) * (kBlock >> 4) + 2 * (ks & 3),
+                                                  vj + ks * (kGroup * 128 >> 4), id_o, acc);
+                                        acc = 1u;
+                                    }
+                                }
+                                commit2(smem_u32(&ctl.v_empty[j]));
+                                if (j == 1) commit2(smem_u32(&ctl.o_full));
+                            }
+                            __syncwarp();
+                        }
+                        ++go;
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------- softmax and output: TMEM lane tx holds row tx % 64 of
+        // this CTA's rows, keys (of S) or dims (of O) of half tx / 64
+        const int tx = (int)threadIdx.x;
+        const int half = tx >> 6, r = tx & 63;
+        const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
+        const uint32_t p_bar = dsmem_map(smem_u32(&ctl.p_full), 0);
+        uint8_t *prow = smem + kPOff + half * kBlock;
+        if (rank == 0 && tx == 0) p.split[cluster] = Split{0, 0, 0, 0};
+        uint32_t g = 0;                                       // tiles so far
+        Pieces pc(p, cluster);
+        // Every softmax thread runs the same sequence of named barriers whatever
+        // happens; `alive` (the same in a warp) only gates work on tensor memory
+        // and shared memory after a bounded wait gave up.
+        bool alive = true;
+        while (pc.next(p, lane)) {
+            const Item &it = pc.it;
+            const int row = kHalf * (int)rank + r;
+            const bool mine = row < it.nrows;
+            const int64_t kv0 = seq_base(b, it.seq);
+            int pos = -1;
+            if (mine) {
+                pos = token_pos(b, (it.row0 + row) / p.pr.H, p.status);
+                if (pos >= 0 && own_row(b, it.seq, kv0, pos) < 0) {
+                    flag(p.status, DSA_DEV_BAD_POSITION);
+                    pos = -1;
+                }
+            }
+            const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);   // first of the window
+            float m = -INFINITY, l = 0.f;
+            for (int i = pc.t0; i < pc.t1; ++i, ++g) {
+                const int p0 = tile_pos(it, i), kp = p0 + kHalf * half;
+                if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 1u]), (g >> 1) & 1u, ctl, p.status, limit);
+                float x[64];
+                if (alive) {
+                    tc_fence_after();
+                    uint32_t u[32], v[32];
+                    const uint32_t at = tmem + lane_addr + kColS + (g & 1u) * (kKeys / 2);
+                    tmem_ld32(at, u);
+                    tmem_ld32(at + 32, v);
+                    tmem_wait_ld(u, v);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        x[c] = __uint_as_float(u[c]) * p.scale_log2;
+                        x[32 + c] = __uint_as_float(v[c]) * p.scale_log2;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c] = -INFINITY;
+                }
+                // every row of the item sees every key of the tile?
+                if (!(p0 + kKeys - 1 <= it.min_pos && (int64_t)p0 > (int64_t)it.hi - p.pr.window)) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        const int s = kp + c;
+                        const bool see = s <= pos && (s >= from || (s >= it.s_lo && s < it.s_hi));
+                        x[c] = see ? x[c] : -INFINITY;
+                    }
+                }
+                float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 64; c += 4) {
+                    t0 = fmaxf(t0, x[c]);
+                    t1 = fmaxf(t1, x[c + 1]);
+                    t2 = fmaxf(t2, x[c + 2]);
+                    t3 = fmaxf(t3, x[c + 3]);
+                }
+                const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+                float *red = ctl.red[g & 1u];
+                red[tx] = top;
+                named_barrier(1 + (warp & 1), 64);            // the two warps that share these rows
+                const float mx = fmaxf(top, red[tx ^ 64]);
+                // The maximum is only raised by more than 2^8 at a time (the result
+                // is the same either way): O is rescaled seldom.
+                float al = 1.f;
+                if (mx > m + kRescaleLog2 || (m == -INFINITY && mx != -INFINITY)) {
+                    al = m == -INFINITY ? 0.f : ex2(m - mx);
+                    m = mx;
+                }
+                const float mm = m == -INFINITY ? 0.f : m;
+                float l0 = 0.f, l1 = 0.f;
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                    const float a = ex2(x[c] - mm), e = ex2(x[c + 1] - mm);
+                    l0 += a;
+                    l1 += e;
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, e);
+                    pk[c / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                l = l * al + (l0 + l1);
+                // P's buffer and O are free once the product of the tile before is done
+                if (i > pc.t0) {
+                    if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (g - 1) & 1u, ctl, p.status, limit);
+                        if (__any_sync(0xffffffffu, al != 1.f) && alive) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 256; c += 32) {
+                            uint32_t u[32];
+                            tmem_ld32(tmem + lane_addr + kColO + c, u);
+                            tmem_wait_ld(u);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * al);
+                            tmem_st32(tmem + lane_addr + kColO + c, u);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                if (alive) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(prow + sw128_offset((uint32_t)r, (uint32_t)c)) =
+                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(p_bar);
+                }
+            }
+            // ---- the piece's output
+            const bool empty = pc.t1 == pc.t0;
+            if (!empty) {
+                if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (g - 1) & 1u, ctl, p.status, limit);
+                tc_fence_after();
+                named_barrier(1 + (warp & 1), 64);            // the last tile's maxima have been read
+                ctl.red[0][tx] = l;
+                named_barrier(1 + (warp & 1), 64);
+                l += ctl.red[0][tx ^ 64];
+                named_barrier(1 + (warp & 1), 64);
+            }
+            const bool none = pos < 0 || l == 0.f;            // a sum of NaN is not none
+            if (alive && pc.whole) {
+                const float inv = 1.f / l;
+                const int64_t at = ((int64_t)it.row0 + row) * D_L + 256 * half;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 32) {
+                    uint32_t u[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) u[e] = 0u;
+                    if (!empty) {
+                        tmem_ld32(tmem + lane_addr + kColO + c, u);
+                        tmem_wait_ld(u);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) u[e] = none ? 0u : __float_as_uint(__uint_as_float(u[e]) * inv);
+                    if (mine && p.out_bf16) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at + c);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u[8 * q + 2 * e]),
+                                                                               __uint_as_float(u[8 * q + 2 * e + 1]));
+                                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                            dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (mine) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at + c);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) dst[q] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (p.lse && mine && half == 0) p.lse[(int64_t)it.row0 + row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+            } else if (alive) {
+                // a part: to slot 2c where the item began in an earlier cluster, else 2c + 1
+                const int64_t at = ((int64_t)2 * cluster + (pc.t0 == 0 ? 1 : 0)) * kRows + row;
+                float *dst = p.part_o + at * D_L + 256 * half;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 32) {
+                    uint32_t u[32];
+                    tmem_ld32(tmem + lane_addr + kColO + c, u);
+                    tmem_wait_ld(u);
+                    if (mine) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            reinterpret_cast<uint4 *>(dst + c)[q] =
+                                none ? make_uint4(0, 0, 0, 0) : make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (mine && half == 0)
+                    *reinterpret_cast<float2 *>(p.part_ml + at * 2) = none ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
+                if (pc.t0 == 0 && rank == 0 && tx == 0) {
+                    // the clusters that the item's tiles reach into
+                    const int64_t total = p.head->total;
+                    const int n = p.head->clusters;
+                    int64_t rest = it.n - pc.t1;
+                    int parts = 1;
+                    for (int k = cluster + 1; rest > 0 && k < n; ++k, ++parts) rest -= total * (k + 1) / n - total * k / n;
+                    p.split[cluster] = Split{it.row0, it.nrows, cluster, parts};
+                }
+            }
+            tc_fence_before();                                // O may be overwritten after the next P
+        }
+    }
+
+    __syncwarp();
+    if (*(volatile int32_t *)&ctl.abort_flag) {
+        // let copies in flight land before the shared memory goes
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 1000000ull) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    pdl_trigger();
+    cluster_sync_all();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc2(tmem, kTmemCols);
+    }
+}
+
+// One CTA: the items of the call, their costs, and where each cluster begins.
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ int plan_scan(int v, int &sum, int *sh) {   // exclusive prefix over the CTA
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int y = sh[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += z;
+        }
+        sh[32 + lane] = y;
+    }
+    __syncthreads();
+    sum = sh[63];
+    const int before = (warp ? sh[32 + warp - 1] : 0) + x - v;
+    __syncthreads();
+    return before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const Problem p, uint32_t *status, int max_items, int clusters,
+                                                                PlanHead *head, PlanItem *items, Start *start, int32_t *item0) {
+    __shared__ int sh[64];
+    pdl_wait();
+    const DevBatch &b = p.b;
+    int base = 0;                                             // items of the sequences before
+    for (int s0 = 0; s0 < b.B; s0 += kPlanThreads) {
+        const int s = s0 + (int)threadIdx.x;
+        int n = 0;
+        if (s < b.B) {
+            const int t0 = __ldg(b.cu_q + s), t1 = __ldg(b.cu_q + s + 1);
+            if (t0 < 0 || t1 < t0 || t1 > b.T) flag(status, DSA_DEV_BAD_POSITION);
+            else n = ((t1 - t0) * p.H + kRows - 1) / kRows;
+        }
+        int sum;
+        const int before = plan_scan(n, sum, sh);
+        if (s < b.B) item0[s] = base + before;
+        base += sum;
+    }
+    __syncthreads();
+    if (base > max_items) {                                   // only where cu_q falls somewhere
+        if (threadIdx.x == 0) flag(status, DSA_DEV_BAD_POSITION);
+        base = max_items;
+    }
+    int total = 0;
+    for (int i0 = 0; i0 < base; i0 += kPlanThreads) {
+        const int i = i0 + (int)threadIdx.x;
+        int cost = 0;
+        PlanItem pi{};
+        if (i < base) {
+            int lo = 0, hi = b.B;                             // item0[lo] <= i < item0[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (item0[mid] <= i) lo = mid; else hi = mid;
+            }
+            pi.seq = lo;
+            pi.row = (i - item0[lo]) * kRows;
+            const int t0 = __ldg(b.cu_q + lo), t1 = __ldg(b.cu_q + lo + 1);
+            const int row0 = t0 * p.H + pi.row, nrows = min(kRows, t1 * p.H - row0);
+            Item it;
+            it.seq = lo;
+            it.min_pos = INT32_MAX;
+            it.hi = -1;
+            for (int t = row0 / p.H; t <= (row0 + nrows - 1) / p.H; ++t) {
+                const int pos = __ldg(b.q_pos + t);
+                if (pos >= 0 && pos < b.max_kv) {
+                    it.min_pos = min(it.min_pos, pos);
+                    it.hi = max(it.hi, pos);
+                }
+            }
+            item_tiles(p, it);
+            cost = item_cost(it.n);
+        }
+        int sum;
+        const int before = plan_scan(cost, sum, sh);
+        if (i < base) {
+            pi.cost0 = total + before;
+            items[i] = pi;
+        }
+        total += sum;
+    }
+    __syncthreads();
+    const int n = min(clusters, total);
+    if (threadIdx.x == 0) *head = PlanHead{total, n};
+    for (int c = (int)threadIdx.x; c < n; c += kPlanThreads) {
+        const int at = (int)((int64_t)total * c / n);
+        int lo = 0, hi = base;                                // items[lo].cost0 <= at < items[hi].cost0
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (items[mid].cost0 <= at) lo = mid; else hi = mid;
+        }
+        start[c] = Start{lo, at - items[lo].cost0};
+    }
+    pdl_trigger();
+}
+
+// Joins the parts of an item that several clusters share: a warp a row.
+constexpr int kJoinRows = 8;
+
+__global__ void __launch_bounds__(32 * kJoinRows) mla_combine_kernel(const Split *split, const float *part_o, const float *part_ml,
+                                                                     void *out, int out_bf16, float *lse) {
+    pdl_wait();
+    const Split s = split[blockIdx.x];
+    const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= s.nrows) return;                               // 0 without a shared item
+    auto slot = [&](int k) { return ((int64_t)2 * (s.first + k) + (k == 0 ? 1 : 0)) * kRows + row; };
+    float M = -INFINITY;
+    for (int k = lane; k < s.parts; k += 32) M = fmaxf(M, part_ml[slot(k) * 2]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float L = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < s.parts; ++k) {
+        const int64_t at = slot(k);
+        const float2 ml = *reinterpret_cast<const float2 *>(part_ml + at * 2);
+        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        L += w * ml.y;
+        const float4 *src = reinterpret_cast<const float4 *>(part_o + at * D_L) + lane;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 v = src[32 * q];
+            acc[q].x += w * v.x; acc[q].y += w * v.y; acc[q].z += w * v.z; acc[q].w += w * v.w;
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t at = ((int64_t)s.row0 + row) * D_L + 4 * lane;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float4 v = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
+        if (out_bf16) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), c = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at + 128 * q) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(out) + at + 128 * q) = v;
+        }
+    }
+    if (lse && lane == 0) lse[(int64_t)s.row0 + row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// ---------------------------------------------------------------- host
+namespace {
+
+constexpr int kClusters = kSMs / 2;
+
+struct MlaLayout {
+    size_t head, start, split, ml, part, item0, items, total;
+    int64_t max_items;
+};
+MlaLayout mla_layout(int64_t T, int64_t B, int64_t H, size_t off) {
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = (off + bytes + 255) / 256 * 256;
+        return at;
+    };
+    MlaLayout L;
+    L.max_items = T * H / kRows + B;
+    L.head = take(sizeof(PlanHead));
+    L.start = take(kClusters * sizeof(Start));
+    L.split = take(kClusters * sizeof(Split));
+    L.ml = take((size_t)2 * kClusters * kRows * 2 * sizeof(float));
+    L.part = take((size_t)2 * kClusters * kRows * D_L * sizeof(float));
+    L.item0 = take((size_t)B * sizeof(int32_t));
+    L.items = take((size_t)L.max_items * sizeof(PlanItem));
+    L.total = off;
+    return L;
+}
+
+}  // namespace
+
+size_t mla_attn_workspace(int T, int B, int H) { return mla_layout(T, B, H, kStatusBytes).total; }
+
+bool mla_attn_countable(int T, int B, int H, int max_kv) {
+    // costs are 32-bit numbers
+    return mla_layout(T, B, H, kStatusBytes).max_items * ((int64_t)max_kv / kKeys + 2 + kItemCost) < INT32_MAX;
+}
+
+cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBatch &b, void *ws, cudaStream_t stream) {
+    const MlaLayout L = mla_layout(b.T, b.B, a.H, kStatusBytes);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    uint32_t *status = reinterpret_cast<uint32_t *>(w);
+    MlaParams p;
+    p.pr = Problem{b, a.H, a.window, a.n_sink, a.sink_pos0};
+    p.status = status;
+    PlanHead *head = reinterpret_cast<PlanHead *>(w + L.head);
+    PlanItem *items = reinterpret_cast<PlanItem *>(w + L.items);
+    Start *start = reinterpret_cast<Start *>(w + L.start);
+    p.head = head;
+    p.items = items;
+    p.start = start;
+    p.split = reinterpret_cast<Split *>(w + L.split);
+    p.part_o = reinterpret_cast<float *>(w + L.part);
+    p.part_ml = reinterpret_cast<float *>(w + L.ml);
+    p.out = a.out;
+    p.out_bf16 = a.out_bf16;
+    p.lse = a.lse;
+    p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+    p.tail = a.tail;
+    p.rows_per_box = !b.block_table || b.block_size % 64 == 0 ? 64 : b.block_size % 16 == 0 ? 16 : 0;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(mla_attn_kernel), 12, kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_k(mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, p.pr, status, (int)L.max_items, kClusters, head,
+                 items, start, reinterpret_cast<int32_t *>(w + L.item0));
+    if (e != cudaSuccess) return e;
+    e = launch_k(mla_attn_kernel, dim3(2 * kClusters), dim3(kThreads), kSmem, stream, true, p, maps.q_lat, maps.q_rope, maps.kv64,
+                 maps.kv16, maps.kv1);
+    if (e != cudaSuccess) return e;
+    return launch_k(mla_combine_kernel, dim3(kClusters, kRows / kJoinRows), dim3(32 * kJoinRows), 0, stream, true,
+                    (const Split *)p.split, (const float *)p.part_o, (const float *)p.part_ml, a.out, a.out_bf16, a.lse);
+}
+
+}  // namespace dsa

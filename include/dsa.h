@@ -101,7 +101,8 @@ enum {
     DSA_OP_TOPK = 2,
     DSA_OP_SPARSE_ATTN = 3,
     DSA_OP_DECODE = 4,
-    DSA_OP_KPOOL = 5          /* dsa_kpool_select and dsa_decode_kpool (k = top_k) */
+    DSA_OP_KPOOL = 5,         /* dsa_kpool_select and dsa_decode_kpool (k = top_k) */
+    DSA_OP_MLA_ATTN = 6       /* dsa_mla_attn and dsa_mla_attn_window (k is not read) */
 };
 
 /*
@@ -530,6 +531,48 @@ dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rop
                                     const float *scale, const dsa_batch_t *batch, const dsa_paging_t *paging,
                                     const int32_t *idx, int k, int H, float sm_scale, void *out, int out_dtype,
                                     float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Attention of every query head over all the latent rows that its token sees,
+ * nothing selected: contexts that fit a selection whole, layers without an
+ * indexer.  Token t attends to the positions s = 0..q_pos[t] of its sequence,
+ *   z_s      = sm_scale * (q_lat[t,h] . c_s[0:512] + q_rope[t,h] . c_s[512:576])
+ *   out[t,h] = sum_s softmax(z)_s c_s[0:512],  lse[t,h] = log(sum_s exp(z_s))
+ * with c_s the cache row of s.  One token per sequence (decode), chunks of any
+ * length, and several sequences of different lengths go through the same call.
+ *   q_lat [T,H,512] bf16, q_rope [T,H,64] bf16 and kv_cache [cache_rows,576] bf16 as
+ *   dsa_sparse_mla_attn; q_rope NULL: rows without a tail, kv_cache [cache_rows,512]
+ *   paging     NULL for contiguous caches; any block_size >= 1 (multiples of 64
+ *              are read in the largest pieces, then multiples of 16).  Only blocks
+ *              that hold a visible position are looked up.
+ *   out        [T,H,512] of out_dtype DSA_DT_F32 or DSA_DT_BF16; lse [T,H] or NULL
+ *   ws         dsa_workspace_size(DSA_OP_MLA_ATTN, batch, 1, H, 1)
+ * Operands are bf16, sums and the softmax float32; probabilities enter the value
+ * product as bf16.  Cache rows that no token of the call sees may hold anything.
+ * A token at position -1 is padding: out = 0, lse = -INFINITY.  One at any other
+ * position out of bounds, or in an unmapped block, gets the same and is flagged
+ * DSA_DEV_BAD_POSITION.  A visible position in an unmapped block is flagged
+ * DSA_DEV_BAD_INDEX; the outputs of the tokens that see it are unspecified.
+ * Errors: as dsa_sparse_mla_attn_q8 (paging as there); DSA_ERR_UNSUPPORTED where
+ * total_q * H exceeds 2^31 - 257 or the 128-position tiles of all rows 2^31.
+ */
+dsa_status_t dsa_mla_attn(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const dsa_bf16 *kv_cache, const dsa_batch_t *batch,
+                          const dsa_paging_t *paging, int H, float sm_scale, void *out, int out_dtype, float *lse, void *ws,
+                          size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * dsa_mla_attn through a sliding window: token t sees the last `window`
+ * positions q_pos[t] - window + 1 .. q_pos[t], and the first n_sink positions
+ * a_b .. a_b + n_sink - 1 up to its own (as in dsa_topk_sink: a_b = max(0,
+ * sink_pos0[b]), 0 when sink_pos0 is NULL).  Positions that are both count once.
+ * Blocks that hold no visible position may be unmapped or reused.
+ * Errors: as dsa_mla_attn; DSA_ERR_INVALID_ARGUMENT for window < 1 or n_sink < 0;
+ * DSA_ERR_MISALIGNED for sink_pos0 not 4-byte aligned.
+ */
+dsa_status_t dsa_mla_attn_window(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const dsa_bf16 *kv_cache,
+                                 const dsa_batch_t *batch, const dsa_paging_t *paging, int H, int window, int n_sink,
+                                 const int32_t *sink_pos0, float sm_scale, void *out, int out_dtype, float *lse, void *ws,
+                                 size_t ws_bytes, cudaStream_t stream);
 
 /*
  * Workspace bytes an operation needs for this batch (host only; batch
