@@ -58,14 +58,30 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kItemCost = 1;                  // what an item costs beside its tiles, in tiles
 
+// A piece of an item, for every warp of the CTA (Ctl::piece).
+struct Piece {
+    int32_t t0, t1;               // tiles of the item to do; t0 == t1: an item that sees nothing
+    int32_t n_first, first_tile, tile0;
+    int32_t lo, hi, s_lo, s_hi, min_pos;   // as in Item
+    int32_t row0, nrows, seq;
+    int32_t whole;                // all tiles of the item
+    int32_t rest;                 // tiles of the item behind t1
+    int32_t end;                  // no piece: there are no more
+    int32_t spare;                // a cache row that may be read for positions that no row sees
+    int64_t kv0;
+};
+constexpr int kPieces = 4;        // read ahead
+
 struct Ctl {
     uint64_t k_full[3], k_empty[3];
     uint64_t v_full[2], v_empty[2];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full, o_full;
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint32_t tmem_base;
     int32_t abort_flag;
     float red[2][kRows];
+    Piece piece[kPieces];
 };
 constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -108,23 +124,15 @@ __device__ __forceinline__ void tma2_gather4(uint32_t dst, const CUtensorMap *m,
         "l"(reinterpret_cast<uint64_t>(m)), "r"(col), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
         : "memory");
 }
+// Arrivals at a barrier of either CTA.  What they publish is read by the tensor
+// core alone, behind a proxy fence of the writer, or is a byte count: a release
+// over the cluster, which waits out every store of the thread, is not needed
+// (it cost 2700 clocks a tile).
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void arrive_expect_remote(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -179,16 +187,17 @@ __device__ __forceinline__ void item_tiles(const Problem &p, Item &it) {
     }
 }
 // Position of tile i's first key.
-__device__ __forceinline__ int tile_pos(const Item &it, int i) {
+__device__ __forceinline__ int tile_pos(const Piece &it, int i) {
     return (i < it.n_first ? it.first_tile + i : it.tile0 + i - it.n_first) * kKeys;
 }
-__device__ __forceinline__ bool seen_by_some(const Item &it, int pos) {
+__device__ __forceinline__ bool seen_by_some(const Piece &it, int pos) {
     return (pos >= it.lo && pos <= it.hi) || (pos >= it.s_lo && pos < it.s_hi);
 }
 // The tile's groups of 16 keys with a position that some row sees, one bit each.
-__device__ __forceinline__ uint32_t tile_groups(const Item &it, int p0) {
+__device__ __forceinline__ uint32_t tile_groups(const Piece &it, int p0) {
+    if (p0 >= it.lo && p0 + kKeys - 1 <= it.hi) return 0xffu;
     uint32_t m = 0;
-#pragma unroll
+#pragma unroll 1
     for (int g = 0; g < kKeys / kGroup; ++g) {
         const int a = p0 + g * kGroup, e = a + kGroup - 1;
         if ((e >= it.lo && a <= it.hi) || (e >= it.s_lo && a < it.s_hi)) m |= 1u << g;
@@ -229,12 +238,6 @@ __device__ __forceinline__ int token_pos(const DevBatch &b, int t, uint32_t *sta
     if (p != -1) flag(status, DSA_DEV_BAD_POSITION);
     return -1;
 }
-// The row of a position that a token holds, -1 if there is none.
-__device__ __forceinline__ int64_t own_row(const DevBatch &b, int seq, int64_t kv0, int pos) {
-    const int64_t r = kv0 < 0 ? -1 : cache_row(b, seq, kv0, pos);
-    return r >= 0 && r < b.cache_rows ? r : -1;
-}
-
 // Loads an item with a whole warp.
 __device__ __forceinline__ Item load_item(const MlaParams &p, int index, int lane) {
     const DevBatch &b = p.pr.b;
@@ -259,49 +262,14 @@ __device__ __forceinline__ Item load_item(const MlaParams &p, int index, int lan
     return it;
 }
 
-// The pieces of items that a cluster works on, in order.
-struct Pieces {
-    int item, off, left;          // next item, costs of it done, costs left to this cluster
-    int t0, t1;                   // tiles of the current piece
-    bool whole, first;            // all tiles of the item; the item's first tile is among them
-    Item it;
-    __device__ Pieces(const MlaParams &p, int cluster) {
-        const int64_t total = p.head->total;
-        const int n = p.head->clusters;
-        item = off = left = 0;
-        if (cluster >= n) return;
-        const Start s = p.start[cluster];
-        item = s.item;
-        off = s.off;
-        left = (int)(total * (cluster + 1) / n - total * cluster / n);
-    }
-    __device__ bool next(const MlaParams &p, int lane) {
-        while (left > 0) {
-            it = load_item(p, item, lane);
-            const int cost = item_cost(it.n), take = min(left, cost - off);
-            t0 = min(off, it.n);
-            t1 = min(off + take, it.n);
-            whole = t0 == 0 && t1 == it.n;
-            first = off == 0;
-            left -= take;
-            off += take;
-            if (off == cost) {
-                ++item;
-                off = 0;
-            }
-            if (t1 > t0 || (it.n == 0 && first)) return true;
-        }
-        return false;
-    }
-};
-
 // Bounded wait of a whole warp; the same answer in every lane.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
-    bool ok = try_wait_cluster(bar, parity);
+    bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
         const uint64_t t0 = global_ns();
+#pragma unroll 1
         while (!ok && !*(volatile int32_t *)&c.abort_flag) {
-            ok = try_wait_cluster(bar, parity);
+            ok = mbar_try_wait(bar, parity);
             if (!ok && global_ns() - t0 > limit_ns) {
                 *(volatile int32_t *)&c.abort_flag = 1;
                 flag(status, DSA_DEV_TIMEOUT);
@@ -311,28 +279,43 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, 
     return __all_sync(0xffffffffu, ok);
 }
 
-// Cache row of a position that some row of the item sees; `spare` (a row that is
-// there) for any other position, and for one in an unmapped block.
-__device__ __forceinline__ int32_t row_or_spare(const MlaParams &p, const Item &it, int64_t kv0, int pos, int32_t spare,
-                                                bool report) {
-    if (!seen_by_some(it, pos)) return spare;
-    const int64_t r = own_row(p.pr.b, it.seq, kv0, pos);
-    if (r >= 0) return (int32_t)r;
-    if (report) flag(p.status, DSA_DEV_BAD_INDEX);
-    return spare;
-}
+// The ring of pieces, as one warp reads it.
+struct Reader {
+    uint32_t n = 0;
+    __device__ __forceinline__ const Piece *next(Ctl &c, uint32_t *status, uint64_t limit) {
+        if (!wait_bar(smem_u32(&c.piece_full[n % kPieces]), (n / kPieces) & 1u, c, status, limit)) return nullptr;
+        return &c.piece[n % kPieces];
+    }
+    __device__ __forceinline__ void done(Ctl &c, int lane) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.piece_empty[n % kPieces]));
+        ++n;
+    }
+};
 
-// A row of the cache that may be read for positions that no row sees: the one of
-// the item's last position, row 0 if that has none (no row sees anything then).
-__device__ __forceinline__ int32_t spare_row(const MlaParams &p, const Item &it, int64_t kv0) {
-    const int64_t r = it.hi < 0 ? -1 : own_row(p.pr.b, it.seq, kv0, it.hi);
-    return r < 0 ? 0 : (int32_t)r;
+// Cache row of a position, whoever sees it: negative where there is none.
+__device__ __forceinline__ int32_t any_row(const DevBatch &b, int seq, int64_t kv0, int pos) {
+    int64_t r = kv0 + pos;
+    if (b.block_table) {
+        const int blk = pos / b.block_size;
+        const int e = blk < b.max_blocks ? __ldg(b.block_table + (int64_t)seq * b.max_blocks + blk) : -1;
+        r = e < 0 ? -1 : (int64_t)e * b.block_size + (pos - blk * b.block_size);
+    }
+    return r >= 0 && r < b.cache_rows ? (int32_t)r : -1;
+}
+// That of a position that some row of the piece sees, its spare one for any other.
+__device__ __noinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status, const Piece *pc, int pos) {
+    if (!seen_by_some(*pc, pos)) return pc->spare;
+    const int32_t r = any_row(b, pc->seq, pc->kv0, pos);
+    if (r >= 0) return r;
+    flag(status, DSA_DEV_BAD_INDEX);
+    return pc->spare;
 }
 
 }  // namespace
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    mla_attn_kernel(const MlaParams p, const __grid_constant__ CUtensorMap q_lat_map,
+    mla_attn_kernel(const __grid_constant__ MlaParams p, const __grid_constant__ CUtensorMap q_lat_map,
                     const __grid_constant__ CUtensorMap q_rope_map, const __grid_constant__ CUtensorMap kv64_map,
                     const __grid_constant__ CUtensorMap kv16_map, const __grid_constant__ CUtensorMap kv1_map) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -357,6 +340,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctl.v_empty[i]), 1);
             mbar_init(smem_u32(&ctl.s_full[i]), 1);
         }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(smem_u32(&ctl.piece_full[i]), 1);
+            mbar_init(smem_u32(&ctl.piece_empty[i]), kSoftmaxWarps + 2 + (rank == 0 ? 1 : 0));
+        }
         mbar_init(smem_u32(&ctl.q_full), 2);
         mbar_init(smem_u32(&ctl.q_empty), 1);
         mbar_init(smem_u32(&ctl.p_full), 2 * kSoftmaxWarps);
@@ -379,56 +366,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t limit = b.wait_ns;
     const int n_blocks = p.tail ? 9 : 8;
 
-    if (warp == kKWarp) {
-        // ---------------- keys: this CTA's 64 of each tile, in three groups of blocks
-        uint32_t g = 0;                                       // tiles so far
-        Pieces pc(p, cluster);
-        bool alive = true;
-        while (alive && pc.next(p, lane)) {
-            const int64_t kv0 = seq_base(b, pc.it.seq);
-            const int32_t spare = spare_row(p, pc.it, kv0);
-            for (int i = pc.t0; alive && i < pc.t1; ++i, ++g) {
-                const int pos = tile_pos(pc.it, i) + kHalf * (int)rank;
-                // rows of this lane's copies: one box of 64, four of 16, or quads of single
-                // rows.  Keys that nobody sees may be anything: their scores are masked.
-                int4 r = make_int4(0, 0, 0, 0);
-                const int step = p.rows_per_box ? p.rows_per_box : 4;   // keys of one copy
-                const int copies = kHalf / step;                       // of one block
-                const int mine = lane % copies;
-                if (p.rows_per_box) {
-                    // the box's first position; the rest of the box follows it
-                    const int a = pos + mine * step;
-                    int first = a;
-                    while (first < a + step && !seen_by_some(pc.it, first)) ++first;
-                    r.x = first < a + step ? row_or_spare(p, pc.it, kv0, first, spare + (first - a), true) - (first - a) : spare;
-                    r.x = max(r.x, 0);
-                } else {
-                    const int a = pos + mine * 4;
-                    r.x = row_or_spare(p, pc.it, kv0, a, spare, true);
-                    r.y = row_or_spare(p, pc.it, kv0, a + 1, spare, true);
-                    r.z = row_or_spare(p, pc.it, kv0, a + 2, spare, true);
-                    r.w = row_or_spare(p, pc.it, kv0, a + 3, spare, true);
+    if (warp == kQWarp) {
+        // ---------------- the cluster's pieces, a few ahead, and their queries
+        const int64_t total = p.head->total;
+        const int n_cl = p.head->clusters;
+        int item = 0, off = 0, left = 0;                      // next item, costs of it done, costs left to do
+        if (cluster < n_cl) {
+            const Start st = p.start[cluster];
+            item = st.item;
+            off = st.off;
+            left = (int)(total * (cluster + 1) / n_cl - total * cluster / n_cl);
+        }
+        uint32_t n = 0, nq = 0;
+        bool end = false;
+        while (!end) {
+            end = left <= 0;
+            Piece pc{};
+            pc.end = end;
+            if (!end) {
+                const Item it = load_item(p, item, lane);
+                const int cost = item_cost(it.n), take = min(left, cost - off);
+                pc.t0 = min(off, it.n);
+                pc.t1 = min(off + take, it.n);
+                const bool first = off == 0;
+                left -= take;
+                off += take;
+                if (off == cost) {
+                    ++item;
+                    off = 0;
                 }
+                if (pc.t1 == pc.t0 && !(it.n == 0 && first)) continue;
+                pc.n_first = it.n_first;
+                pc.first_tile = it.first_tile;
+                pc.tile0 = it.tile0;
+                pc.lo = it.lo;
+                pc.hi = it.hi;
+                pc.s_lo = it.s_lo;
+                pc.s_hi = it.s_hi;
+                pc.min_pos = it.min_pos;
+                pc.row0 = it.row0;
+                pc.nrows = it.nrows;
+                pc.seq = it.seq;
+                pc.whole = pc.t0 == 0 && pc.t1 == it.n;
+                pc.rest = it.n - pc.t1;
+                pc.kv0 = seq_base(b, it.seq);
+                // the row of the last position; row 0 if that has none (no row sees anything then)
+                pc.spare = it.hi < 0 || pc.kv0 < 0 ? 0 : max(0, any_row(b, it.seq, pc.kv0, it.hi));
+            }
+            if (!wait_bar(smem_u32(&ctl.piece_empty[n % kPieces]), ((n / kPieces) & 1u) ^ 1u, ctl, p.status, limit)) break;
+            if (lane == 0) {
+                ctl.piece[n % kPieces] = pc;
+                mbar_arrive(smem_u32(&ctl.piece_full[n % kPieces]));
+            }
+            __syncwarp();
+            ++n;
+            if (end || pc.t1 == pc.t0) continue;
+            if (!wait_bar(smem_u32(&ctl.q_empty), (nq & 1u) ^ 1u, ctl, p.status, limit)) break;
+            ++nq;
+            if (b.skip_copies) continue;
+            const uint32_t full = dsmem_map(smem_u32(&ctl.q_full), 0);
+            if (lane == 0) arrive_expect_remote(full, (uint32_t)(n_blocks * kBlock));
+            __syncwarp();
+            // rows past the sequence's are some other token's (or zero past the
+            // tensor): they only feed accumulator rows that are never stored
+            const int row = pc.row0 + kHalf * (int)rank;
+            if (lane < n_blocks)
+                tma2_load(s0 + kQOff + lane * kBlock, lane < 8 ? &q_lat_map : &q_rope_map, full, (lane & 7) * 64, row);
+            __syncwarp();
+        }
+    } else if (warp == kKWarp) {
+        // ---------------- keys: this CTA's 64 of each tile, in three groups of blocks.
+        // Keys that nobody sees may be anything: their scores are masked.
+        uint32_t g = 0;                                       // tiles so far
+        const int step = p.rows_per_box ? p.rows_per_box : 4; // keys of one copy
+        const int copies = kHalf / step;                      // of one block
+        const int mine = lane % copies;
+        bool alive = true;
+        Reader rd;
+        while (alive) {
+            const Piece *pc = rd.next(ctl, p.status, limit);
+            if (!pc || pc->end) break;
+            const int t1 = pc->t1, seq = pc->seq;
+            const int64_t kv0 = pc->kv0;
+            for (int i = pc->t0; alive && i < t1; ++i, ++g) {
+                const int a = tile_pos(*pc, i) + kHalf * (int)rank + mine * step;
+                int4 r;
+                r.x = max(0, any_row(b, seq, kv0, a));
+                if (!p.rows_per_box) {
+                    r.y = max(0, any_row(b, seq, kv0, a + 1));
+                    r.z = max(0, any_row(b, seq, kv0, a + 2));
+                    r.w = max(0, any_row(b, seq, kv0, a + 3));
+                }
+                const uint32_t dst = s0 + kKOff + mine * step * 128;
+#pragma unroll 1
                 for (int q = 0; q < 3; ++q) {
-                    if (!wait_bar(smem_u32(&ctl.k_empty[q]), (g & 1u) ^ 1u, ctl, p.status, limit)) {
-                        alive = false;
-                        break;
-                    }
+                    alive = wait_bar(smem_u32(&ctl.k_empty[q]), (g & 1u) ^ 1u, ctl, p.status, limit);
+                    if (!alive) break;
                     if (b.skip_copies) continue;
                     const int nb = min(3, n_blocks - 3 * q);
                     const uint32_t full = dsmem_map(smem_u32(&ctl.k_full[q]), 0);
                     if (lane == 0) arrive_expect_remote(full, (uint32_t)(nb * kBlock));
                     __syncwarp();
+                    // c % copies is lane % copies: copies divides 32
+#pragma unroll 1
                     for (int c = lane; c < nb * copies; c += 32) {
-                        // c % copies is lane % copies: copies divides 32
                         const int kb = 3 * q + c / copies;
-                        const uint32_t dst = s0 + kKOff + kb * kBlock + mine * step * 128;
-                        if (p.rows_per_box == 64) tma2_load(dst, &kv64_map, full, kb * 64, r.x);
-                        else if (p.rows_per_box) tma2_load(dst, &kv16_map, full, kb * 64, r.x);
-                        else tma2_gather4(dst, &kv1_map, full, kb * 64, r);
+                        if (p.rows_per_box) tma2_load(dst + kb * kBlock, p.rows_per_box == 64 ? &kv64_map : &kv16_map, full, kb * 64, r.x);
+                        else tma2_gather4(dst + kb * kBlock, &kv1_map, full, kb * 64, r);
                     }
+                    __syncwarp();
                 }
             }
+            rd.done(ctl, lane);
         }
     } else if (warp == kVWarp) {
         // ---------------- values: all keys of a tile, this CTA's 256 dims in two halves.
@@ -436,70 +485,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // group that is seen in part the other rows are the spare one's copies
         // (P is 0 there, and 0 times what an unused row may hold is not).
         uint32_t g = 0;
-        Pieces pc(p, cluster);
         bool alive = true;
-        while (alive && pc.next(p, lane)) {
-            const int64_t kv0 = seq_base(b, pc.it.seq);
-            const int32_t spare = spare_row(p, pc.it, kv0);
-            for (int i = pc.t0; alive && i < pc.t1; ++i, ++g) {
-                const int pos = tile_pos(pc.it, i), a = pos + 4 * lane;     // this lane's four keys
-                const uint32_t groups = tile_groups(pc.it, pos);
+        Reader rd;
+        while (alive) {
+            const Piece *pc = rd.next(ctl, p.status, limit);
+            if (!pc || pc->end) break;
+            const int t1 = pc->t1;
+            for (int i = pc->t0; alive && i < t1; ++i, ++g) {
+                const int pos = tile_pos(*pc, i), a = pos + 4 * lane;       // this lane's four keys
+                const uint32_t groups = tile_groups(*pc, pos);
                 int4 r;
-                r.x = row_or_spare(p, pc.it, kv0, a, spare, false);
-                r.y = row_or_spare(p, pc.it, kv0, a + 1, spare, false);
-                r.z = row_or_spare(p, pc.it, kv0, a + 2, spare, false);
-                r.w = row_or_spare(p, pc.it, kv0, a + 3, spare, false);
-                // groups whose 16 rows are all seen and lie together
-                const int32_t group_row = __shfl_sync(0xffffffffu, r.x, lane & ~3);
-                const bool run = r.y == r.x + 1 && r.z == r.x + 2 && r.w == r.x + 3 && r.x == group_row + 4 * (lane & 3);
-                const uint32_t runs = __ballot_sync(0xffffffffu, run);
-                const bool box16 = ((runs >> (lane & ~3)) & 0xfu) == 0xfu;
-                const int32_t half_row = __shfl_sync(0xffffffffu, r.x, lane & 16);
-                const bool in_half = box16 && r.x == half_row + 4 * (lane & 15);
-                const uint32_t halves = __ballot_sync(0xffffffffu, in_half);
-                const bool box64 = ((halves >> (lane & 16)) & 0xffffu) == 0xffffu;
+                bool box16 = true, box64 = true;
+                if (groups == 0xffu && p.rows_per_box == 64 && pos >= pc->lo && pos + kKeys - 1 <= pc->hi) {
+                    r.x = any_row(b, pc->seq, pc->kv0, pos + ((lane & 16) << 2));
+                    if (r.x < 0) {
+                        flag(p.status, DSA_DEV_BAD_INDEX);
+                        r.x = pc->spare;
+                    }
+                } else {
+                    r.x = row_or_spare(b, p.status, pc, a);
+                    r.y = row_or_spare(b, p.status, pc, a + 1);
+                    r.z = row_or_spare(b, p.status, pc, a + 2);
+                    r.w = row_or_spare(b, p.status, pc, a + 3);
+                    // groups whose 16 rows are all seen and lie together
+                    const int32_t group_row = __shfl_sync(0xffffffffu, r.x, lane & ~3);
+                    const bool run = r.y == r.x + 1 && r.z == r.x + 2 && r.w == r.x + 3 && r.x == group_row + 4 * (lane & 3);
+                    const uint32_t runs = __ballot_sync(0xffffffffu, run);
+                    box16 = ((runs >> (lane & ~3)) & 0xfu) == 0xfu;
+                    const int32_t half_row = __shfl_sync(0xffffffffu, r.x, lane & 16);
+                    const uint32_t halves = __ballot_sync(0xffffffffu, box16 && r.x == half_row + 4 * (lane & 15));
+                    box64 = ((halves >> (lane & 16)) & 0xffffu) == 0xffffu;
+                }
                 const bool on = (groups >> (lane >> 2)) & 1u;
                 const uint32_t bytes = (uint32_t)__popc(groups) * (kGroup * 128u) * 2u;
+#pragma unroll 1
                 for (int j = 0; j < 2; ++j) {
-                    if (!wait_bar(smem_u32(&ctl.v_empty[j]), (g & 1u) ^ 1u, ctl, p.status, limit)) {
-                        alive = false;
-                        break;
-                    }
+                    alive = wait_bar(smem_u32(&ctl.v_empty[j]), (g & 1u) ^ 1u, ctl, p.status, limit);
+                    if (!alive) break;
                     if (b.skip_copies) continue;
                     const uint32_t full = dsmem_map(smem_u32(&ctl.v_full[j]), 0);
                     if (lane == 0) arrive_expect_remote(full, bytes);
                     __syncwarp();
+#pragma unroll 1
                     for (int d = 0; d < 2; ++d) {
                         const uint32_t dst = s0 + kVOff + j * kVHalf + d * (kVHalf / 2) + lane * 4 * 128;
                         const int32_t col = 256 * (int)rank + 128 * j + 64 * d;
-                        if (box64) {
-                            if ((lane & 15) == 0) tma2_load(dst, &kv64_map, full, col, r.x);
-                        } else if (box16) {
-                            if ((lane & 3) == 0 && on) tma2_load(dst, &kv16_map, full, col, r.x);
+                        if (box16) {
+                            if ((lane & (box64 ? 15 : 3)) == 0 && on) tma2_load(dst, box64 ? &kv64_map : &kv16_map, full, col, r.x);
                         } else if (on) {
                             tma2_gather4(dst, &kv1_map, full, col, r);
                         }
                     }
+                    __syncwarp();
                 }
             }
-        }
-    } else if (warp == kQWarp) {
-        // ---------------- queries: this CTA's 64 rows of each piece's item
-        uint32_t n = 0;
-        Pieces pc(p, cluster);
-        while (pc.next(p, lane)) {
-            if (pc.t1 == pc.t0) continue;
-            if (!wait_bar(smem_u32(&ctl.q_empty), (n & 1u) ^ 1u, ctl, p.status, limit)) break;
-            ++n;
-            if (b.skip_copies) continue;
-            const uint32_t full = dsmem_map(smem_u32(&ctl.q_full), 0);
-            if (lane == 0) arrive_expect_remote(full, (uint32_t)(n_blocks * kBlock));
-            __syncwarp();
-            // rows past the sequence's are some other token's (or zero past the
-            // tensor): they only feed accumulator rows that are never stored
-            const int row = pc.it.row0 + kHalf * (int)rank;
-            if (lane < 8) tma2_load(s0 + kQOff + lane * kBlock, &q_lat_map, full, lane * 64, row);
-            else if (lane < n_blocks) tma2_load(s0 + kQOff + lane * kBlock, &q_rope_map, full, 0, row);
+            rd.done(ctl, lane);
         }
     } else if (warp == kMmaWarp) {
         // ---------------- MMA issuer: the even CTA's for both
@@ -509,24 +549,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t qd = sdesc_sw128(s0 + kQOff, 16, 1024), kd = sdesc_sw128(s0 + kKOff, 16, 1024);
             const uint64_t pd = sdesc_sw128(s0 + kPOff, 16, 1024), vd = sdesc_sw128(s0 + kVOff, kVHalf / 2, 1024);
             uint32_t gs = 0, go = 0, n = 0;                   // tiles scored and summed, pieces
-            Pieces pc(p, cluster);
             bool alive = true;
-            while (alive && pc.next(p, lane)) {
-                if (pc.t1 == pc.t0) continue;
-                if (!wait_bar(smem_u32(&ctl.q_full), n & 1u, ctl, p.status, limit)) break;
-                ++n;
-                for (int i = pc.t0; alive && i <= pc.t1; ++i) {
-                    if (i < pc.t1) {
+            Reader rd;
+            while (alive) {
+                const Piece *pc = rd.next(ctl, p.status, limit);
+                if (!pc || pc->end) break;
+                const int t0 = pc->t0, t1 = pc->t1;
+                if (t1 > t0) {
+                    alive = wait_bar(smem_u32(&ctl.q_full), n & 1u, ctl, p.status, limit);
+                    ++n;
+                }
+                for (int i = t0; alive && t1 > t0 && i <= t1; ++i) {
+                    if (i < t1) {
                         const uint32_t d_s = tmem + kColS + (gs & 1u) * (kKeys / 2);
+#pragma unroll 1
                         for (int q = 0; q < 3; ++q) {
-                            if (!wait_bar(smem_u32(&ctl.k_full[q]), gs & 1u, ctl, p.status, limit)) {
-                                alive = false;
-                                break;
-                            }
+                            alive = wait_bar(smem_u32(&ctl.k_full[q]), gs & 1u, ctl, p.status, limit);
+                            if (!alive) break;
                             tc_fence_after();
-                            const int nb = min(3, n_blocks - 3 * q);
                             if (elect_one()) {
-                                for (int kb = 3 * q; kb < 3 * q + nb; ++kb) {
+                                const int nb = min(3 * q + 3, n_blocks);
+#pragma unroll 1
+                                for (int kb = 3 * q; kb < nb; ++kb) {
                                     const uint64_t o = (uint64_t)(kb * (kBlock >> 4));
 #pragma unroll
                                     for (int ks = 0; ks < 4; ++ks)
@@ -534,34 +578,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 }
                                 commit2(smem_u32(&ctl.k_empty[q]));
                                 if (q == 2) commit2(smem_u32(&ctl.s_full[gs & 1u]));
-                                if (q == 2 && i == pc.t1 - 1) commit2(smem_u32(&ctl.q_empty));
+                                if (q == 2 && i == t1 - 1) commit2(smem_u32(&ctl.q_empty));
                             }
                             __syncwarp();
                         }
                         ++gs;
                     }
-                    if (!alive) break;
-                    if (i > pc.t0) {
-                        const uint32_t groups = tile_groups(pc.it, tile_pos(pc.it, i - 1));
-                        if (!wait_bar(smem_u32(&ctl.p_full), go & 1u, ctl, p.status, limit)) {
-                            alive = false;
-                            break;
-                        }
-                        for (int j = 0; j < 2; ++j) {
-                            if (!wait_bar(smem_u32(&ctl.v_full[j]), go & 1u, ctl, p.status, limit)) {
-                                alive = false;
-                                break;
-                            }
+                    if (alive && i > t0) {
+                        const uint32_t groups = tile_groups(*pc, tile_pos(*pc, i - 1));
+                        alive = wait_bar(smem_u32(&ctl.p_full), go & 1u, ctl, p.status, limit);
+#pragma unroll 1
+                        for (int j = 0; alive && j < 2; ++j) {
+                            alive = wait_bar(smem_u32(&ctl.v_full[j]), go & 1u, ctl, p.status, limit);
+                            if (!alive) break;
                             tc_fence_after();
                             if (elect_one()) {
-                                uint32_t acc = i - 1 > pc.t0 ? 1u : 0u;
-                                const uint64_t vj = vd + (uint64_t)(j * (kVHalf >> 4));
+                                uint32_t acc = i - 1 > t0 ? 1u : 0u;
+                                const uint32_t d_o = tmem + kColO + j * 128;
+#pragma unroll 1
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint64_t ph = pd + (uint64_t)(h * (kBlock >> 4));
+                                    const uint64_t vh = vd + (uint64_t)((j * kVHalf + h * kBlock) >> 4);
+                                    const uint32_t gh = groups >> (4 * h);
 #pragma unroll
-                                for (int ks = 0; ks < kKeys / kGroup; ++ks) {
-                                    if (groups >> ks & 1u) {
-                                        umma2_f16(tmem + kColO + j * 128, pd + (ks >> 2) * (kBlock >> 4) + 2 * (ks & 3),
-                                                  vj + ks * (kGroup * 128 >> 4), id_o, acc);
-                                        acc = 1u;
+                                    for (int ks = 0; ks < 4; ++ks) {
+                                        if (gh >> ks & 1u) {
+                                            umma2_f16(d_o, ph + 2 * ks, vh + ks * (kGroup * 128 >> 4), id_o, acc);
+                                            acc = 1u;
+                                        }
                                     }
                                 }
                                 commit2(smem_u32(&ctl.v_empty[j]));
@@ -572,80 +616,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ++go;
                     }
                 }
+                rd.done(ctl, lane);
             }
         }
     } else {
         // ---------------- softmax and output: TMEM lane tx holds row tx % 64 of
-        // this CTA's rows, keys (of S) or dims (of O) of half tx / 64
+        // this CTA's rows, keys (of S) or dims (of O) of half tx / 64.  The loops
+        // are kept small: unrolled over all 64 keys this kernel was bound by
+        // instruction fetches (120 KB of code; prefill 3.0 ms).
         const int tx = (int)threadIdx.x;
         const int half = tx >> 6, r = tx & 63;
-        const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
+        const uint32_t lane_tmem = tmem + ((uint32_t)(warp * 32) << 16);
         const uint32_t p_bar = dsmem_map(smem_u32(&ctl.p_full), 0);
-        uint8_t *prow = smem + kPOff + half * kBlock;
+        const int pair = 1 + (warp & 1);                      // named barrier of the two warps that share rows
+        uint8_t *prow = smem + kPOff + half * kBlock + (r >> 3) * 1024 + (r & 7) * 128;
+        const uint32_t swz = (uint32_t)(r & 7);
         if (rank == 0 && tx == 0) p.split[cluster] = Split{0, 0, 0, 0};
+        // A scale that is not positive is multiplied in where scores are masked.
+        const bool plain = p.scale_log2 > 0.f;
+        const float scale = plain ? p.scale_log2 : 1.f;
         uint32_t g = 0;                                       // tiles so far
-        Pieces pc(p, cluster);
-        // Every softmax thread runs the same sequence of named barriers whatever
+        // The two warps of a pair run the same sequence of named barriers whatever
         // happens; `alive` (the same in a warp) only gates work on tensor memory
         // and shared memory after a bounded wait gave up.
         bool alive = true;
-        while (pc.next(p, lane)) {
-            const Item &it = pc.it;
+        Reader rd;
+        while (true) {
+            const Piece *pc = rd.next(ctl, p.status, limit);
+            if (named_barrier_or(pair, 64, !pc)) break;
+            if (pc->end) break;
+            const int t0 = pc->t0, t1 = pc->t1;
             const int row = kHalf * (int)rank + r;
-            const bool mine = row < it.nrows;
-            const int64_t kv0 = seq_base(b, it.seq);
+            const bool mine = row < pc->nrows;
             int pos = -1;
             if (mine) {
-                pos = token_pos(b, (it.row0 + row) / p.pr.H, p.status);
-                if (pos >= 0 && own_row(b, it.seq, kv0, pos) < 0) {
+                pos = token_pos(b, (pc->row0 + row) / p.pr.H, p.status);
+                if (pos >= 0 && (pc->kv0 < 0 || any_row(b, pc->seq, pc->kv0, pos) < 0)) {
                     flag(p.status, DSA_DEV_BAD_POSITION);
                     pos = -1;
                 }
             }
-            const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);   // first of the window
             float m = -INFINITY, l = 0.f;
-            for (int i = pc.t0; i < pc.t1; ++i, ++g) {
-                const int p0 = tile_pos(it, i), kp = p0 + kHalf * half;
+            for (int i = t0; i < t1; ++i, ++g) {
+                const int p0 = tile_pos(*pc, i);
                 if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 1u]), (g >> 1) & 1u, ctl, p.status, limit);
-                float x[64];
+                tc_fence_after();
+                const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2);
+                // does every row of the item see every key of the tile?
+                if (!(plain && p0 + kKeys - 1 <= pc->min_pos && (int64_t)p0 > (int64_t)pc->hi - p.pr.window) && alive) {
+                    const int kp = p0 + kHalf * half;
+                    const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);   // first of the window
+                    const int s_lo = pc->s_lo, s_hi = min(pc->s_hi, pos + 1);
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t u[16];
+                        tmem_ld16(s_tmem + c, u);
+                        tmem_wait_ld(u);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int k = kp + c + e;
+                            const float x = __uint_as_float(u[e]) * (plain ? 1.f : p.scale_log2);
+                            u[e] = __float_as_uint((k >= from && k <= pos) || (k >= s_lo && k < s_hi) ? x : -INFINITY);
+                        }
+                        tmem_st16(s_tmem + c, u);
+                    }
+                    tmem_wait_st();
+                }
+                float top = -INFINITY;
                 if (alive) {
-                    tc_fence_after();
-                    uint32_t u[32], v[32];
-                    const uint32_t at = tmem + lane_addr + kColS + (g & 1u) * (kKeys / 2);
-                    tmem_ld32(at, u);
-                    tmem_ld32(at + 32, v);
-                    tmem_wait_ld(u, v);
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t u[32];
+                        tmem_ld32(s_tmem + c, u);
+                        tmem_wait_ld(u);
+                        float a0 = top, a1 = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        x[c] = __uint_as_float(u[c]) * p.scale_log2;
-                        x[32 + c] = __uint_as_float(v[c]) * p.scale_log2;
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) x[c] = -INFINITY;
-                }
-                // every row of the item sees every key of the tile?
-                if (!(p0 + kKeys - 1 <= it.min_pos && (int64_t)p0 > (int64_t)it.hi - p.pr.window)) {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        const int s = kp + c;
-                        const bool see = s <= pos && (s >= from || (s >= it.s_lo && s < it.s_hi));
-                        x[c] = see ? x[c] : -INFINITY;
+                        for (int e = 0; e < 32; e += 4) {
+                            a0 = fmaxf(fmaxf(a0, __uint_as_float(u[e])), __uint_as_float(u[e + 1]));
+                            a1 = fmaxf(fmaxf(a1, __uint_as_float(u[e + 2])), __uint_as_float(u[e + 3]));
+                        }
+                        top = fmaxf(a0, a1);
                     }
                 }
-                float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 64; c += 4) {
-                    t0 = fmaxf(t0, x[c]);
-                    t1 = fmaxf(t1, x[c + 1]);
-                    t2 = fmaxf(t2, x[c + 2]);
-                    t3 = fmaxf(t3, x[c + 3]);
-                }
-                const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
                 float *red = ctl.red[g & 1u];
                 red[tx] = top;
-                named_barrier(1 + (warp & 1), 64);            // the two warps that share these rows
-                const float mx = fmaxf(top, red[tx ^ 64]);
+                named_barrier(pair, 64);
+                const float mx = fmaxf(top, red[tx ^ 64]) * scale;
                 // The maximum is only raised by more than 2^8 at a time (the result
                 // is the same either way): O is rescaled seldom.
                 float al = 1.f;
@@ -653,40 +709,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     al = m == -INFINITY ? 0.f : ex2(m - mx);
                     m = mx;
                 }
-                const float mm = m == -INFINITY ? 0.f : m;
-                float l0 = 0.f, l1 = 0.f;
-                uint32_t pk[32];
-#pragma unroll
-                for (int c = 0; c < 64; c += 2) {
-                    const float a = ex2(x[c] - mm), e = ex2(x[c + 1] - mm);
-                    l0 += a;
-                    l1 += e;
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, e);
-                    pk[c / 2] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-                l = l * al + (l0 + l1);
                 // P's buffer and O are free once the product of the tile before is done
-                if (i > pc.t0) {
+                if (i > t0) {
                     if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (g - 1) & 1u, ctl, p.status, limit);
-                        if (__any_sync(0xffffffffu, al != 1.f) && alive) {
+                    if (__any_sync(0xffffffffu, al != 1.f) && alive) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 256; c += 32) {
-                            uint32_t u[32];
-                            tmem_ld32(tmem + lane_addr + kColO + c, u);
+                        for (int c = 0; c < 256; c += 16) {
+                            uint32_t u[16];
+                            tmem_ld16(lane_tmem + kColO + c, u);
                             tmem_wait_ld(u);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * al);
-                            tmem_st32(tmem + lane_addr + kColO + c, u);
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * al);
+                            tmem_st16(lane_tmem + kColO + c, u);
                         }
                         tmem_wait_st();
                     }
                 }
                 if (alive) {
+                    const float mm = m == -INFINITY ? 0.f : -m;
+                    uint64_t sum = f2(0.f, 0.f);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t u[16], w[8];
+                        tmem_ld16(s_tmem + 16 * c, u);
+                        tmem_wait_ld(u);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(prow + sw128_offset((uint32_t)r, (uint32_t)c)) =
-                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = ex2(fmaf(__uint_as_float(u[2 * e]), scale, mm));
+                            const float y = ex2(fmaf(__uint_as_float(u[2 * e + 1]), scale, mm));
+                            sum = f2_add(sum, f2(x, y));
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        *reinterpret_cast<uint4 *>(prow + (((2 * c) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(prow + (((2 * c + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                    const float2 s2 = f2_get(sum);
+                    l = l * al + (s2.x + s2.y);
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
@@ -694,82 +754,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- the piece's output
-            const bool empty = pc.t1 == pc.t0;
+            const bool empty = t1 == t0;
             if (!empty) {
                 if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (g - 1) & 1u, ctl, p.status, limit);
                 tc_fence_after();
-                named_barrier(1 + (warp & 1), 64);            // the last tile's maxima have been read
+                named_barrier(pair, 64);                      // the last tile's maxima have been read
                 ctl.red[0][tx] = l;
-                named_barrier(1 + (warp & 1), 64);
+                named_barrier(pair, 64);
                 l += ctl.red[0][tx ^ 64];
-                named_barrier(1 + (warp & 1), 64);
+                named_barrier(pair, 64);
             }
             const bool none = pos < 0 || l == 0.f;            // a sum of NaN is not none
-            if (alive && pc.whole) {
-                const float inv = 1.f / l;
-                const int64_t at = ((int64_t)it.row0 + row) * D_L + 256 * half;
+            if (alive) {
+                // a part goes to slot 2c where the item began in an earlier cluster, else to 2c + 1
+                const bool whole = pc->whole;
+                const int64_t out_row = (int64_t)pc->row0 + row;
+                const int64_t part_row = ((int64_t)2 * cluster + (t0 == 0 ? 1 : 0)) * kRows + row;
+                const float factor = whole ? 1.f / l : 1.f;
+                float *dst = whole ? static_cast<float *>(p.out) + out_row * D_L : p.part_o + part_row * D_L;
+                uint16_t *dst16 = static_cast<uint16_t *>(p.out) + out_row * D_L;
+                const bool narrow = whole && p.out_bf16;
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
-                    uint32_t u[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) u[e] = 0u;
+                for (int c = 0; c < 256; c += 16) {
+                    uint32_t u[16];
                     if (!empty) {
-                        tmem_ld32(tmem + lane_addr + kColO + c, u);
+                        tmem_ld16(lane_tmem + kColO + c, u);
                         tmem_wait_ld(u);
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) u[e] = none ? 0u : __float_as_uint(__uint_as_float(u[e]) * inv);
-                    if (mine && p.out_bf16) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at + c);
+                    for (int e = 0; e < 16; ++e) u[e] = none ? 0u : __float_as_uint(__uint_as_float(u[e]) * factor);
+                    if (mine) {
+                        const int at = 256 * half + c;
+                        if (narrow) {
+                            uint32_t w[8];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u[8 * q + 2 * e]),
-                                                                               __uint_as_float(u[8 * q + 2 * e + 1]));
+                            for (int e = 0; e < 8; ++e) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
                                 w[e] = *reinterpret_cast<const uint32_t *>(&h);
                             }
-                            dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>(dst16 + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>(dst16 + at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                reinterpret_cast<uint4 *>(dst + at)[q] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
                         }
-                    } else if (mine) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at + c);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) dst[q] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
                     }
                     __syncwarp();
                 }
-                if (p.lse && mine && half == 0) p.lse[(int64_t)it.row0 + row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
-            } else if (alive) {
-                // a part: to slot 2c where the item began in an earlier cluster, else 2c + 1
-                const int64_t at = ((int64_t)2 * cluster + (pc.t0 == 0 ? 1 : 0)) * kRows + row;
-                float *dst = p.part_o + at * D_L + 256 * half;
-#pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
-                    uint32_t u[32];
-                    tmem_ld32(tmem + lane_addr + kColO + c, u);
-                    tmem_wait_ld(u);
-                    if (mine) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            reinterpret_cast<uint4 *>(dst + c)[q] =
-                                none ? make_uint4(0, 0, 0, 0) : make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
-                    }
-                    __syncwarp();
+                if (mine && half == 0) {
+                    if (!whole) *reinterpret_cast<float2 *>(p.part_ml + part_row * 2) = none ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
+                    else if (p.lse) p.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
-                if (mine && half == 0)
-                    *reinterpret_cast<float2 *>(p.part_ml + at * 2) = none ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
-                if (pc.t0 == 0 && rank == 0 && tx == 0) {
+                if (!whole && t0 == 0 && rank == 0 && tx == 0) {
                     // the clusters that the item's tiles reach into
                     const int64_t total = p.head->total;
                     const int n = p.head->clusters;
-                    int64_t rest = it.n - pc.t1;
+                    int64_t rest = pc->rest;
                     int parts = 1;
                     for (int k = cluster + 1; rest > 0 && k < n; ++k, ++parts) rest -= total * (k + 1) / n - total * k / n;
-                    p.split[cluster] = Split{it.row0, it.nrows, cluster, parts};
+                    p.split[cluster] = Split{pc->row0, pc->nrows, cluster, parts};
                 }
             }
             tc_fence_before();                                // O may be overwritten after the next P
+            rd.done(ctl, lane);
         }
     }
 
