@@ -553,28 +553,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             Reader rd;
             while (alive) {
                 const Piece *pc = rd.next(ctl, p.status, limit);
-                if (!pc || pc->end) break;
-                const int t0 = pc->t0, t1 = pc->t1;
+                if (!pc) break;
+                // (reductions put what is the same in every lane into uniform
+                // registers, where the products take their descriptors from)
+                const int t0 = __reduce_max_sync(0xffffffffu, pc->t0), t1 = __reduce_max_sync(0xffffffffu, pc->t1);
+                if (__any_sync(0xffffffffu, pc->end)) break;
                 if (t1 > t0) {
                     alive = wait_bar(smem_u32(&ctl.q_full), n & 1u, ctl, p.status, limit);
                     ++n;
                 }
+                uint32_t groups = 0, next_groups = 0;         // of the tile before, of this one
+#pragma unroll 1
                 for (int i = t0; alive && t1 > t0 && i <= t1; ++i) {
                     if (i < t1) {
                         const uint32_t d_s = tmem + kColS + (gs & 1u) * (kKeys / 2);
-#pragma unroll 1
+#pragma unroll
                         for (int q = 0; q < 3; ++q) {
-                            alive = wait_bar(smem_u32(&ctl.k_full[q]), gs & 1u, ctl, p.status, limit);
+                            if (alive) alive = wait_bar(smem_u32(&ctl.k_full[q]), gs & 1u, ctl, p.status, limit);
                             if (!alive) break;
                             tc_fence_after();
                             if (elect_one()) {
-                                const int nb = min(3 * q + 3, n_blocks);
-#pragma unroll 1
-                                for (int kb = 3 * q; kb < nb; ++kb) {
-                                    const uint64_t o = (uint64_t)(kb * (kBlock >> 4));
+#pragma unroll
+                                for (int kb = 3 * q; kb < 3 * q + 3; ++kb) {
+                                    if (kb == 8 && !p.tail) continue;
 #pragma unroll
                                     for (int ks = 0; ks < 4; ++ks)
-                                        umma2_f16(d_s, qd + o + 2 * ks, kd + o + 2 * ks, id_s, (kb | ks) != 0);
+                                        umma2_f16(d_s, qd + (uint64_t)(kb * (kBlock >> 4) + 2 * ks),
+                                                  kd + (uint64_t)(kb * (kBlock >> 4) + 2 * ks), id_s, (kb | ks) != 0);
                                 }
                                 commit2(smem_u32(&ctl.k_empty[q]));
                                 if (q == 2) commit2(smem_u32(&ctl.s_full[gs & 1u]));
@@ -583,29 +588,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             __syncwarp();
                         }
                         ++gs;
+                        next_groups = __reduce_or_sync(0xffffffffu, tile_groups(*pc, tile_pos(*pc, i)));
                     }
                     if (alive && i > t0) {
-                        const uint32_t groups = tile_groups(*pc, tile_pos(*pc, i - 1));
                         alive = wait_bar(smem_u32(&ctl.p_full), go & 1u, ctl, p.status, limit);
-#pragma unroll 1
-                        for (int j = 0; alive && j < 2; ++j) {
-                            alive = wait_bar(smem_u32(&ctl.v_full[j]), go & 1u, ctl, p.status, limit);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (alive) alive = wait_bar(smem_u32(&ctl.v_full[j]), go & 1u, ctl, p.status, limit);
                             if (!alive) break;
                             tc_fence_after();
                             if (elect_one()) {
                                 uint32_t acc = i - 1 > t0 ? 1u : 0u;
-                                const uint32_t d_o = tmem + kColO + j * 128;
-#pragma unroll 1
-                                for (int h = 0; h < 2; ++h) {
-                                    const uint64_t ph = pd + (uint64_t)(h * (kBlock >> 4));
-                                    const uint64_t vh = vd + (uint64_t)((j * kVHalf + h * kBlock) >> 4);
-                                    const uint32_t gh = groups >> (4 * h);
 #pragma unroll
-                                    for (int ks = 0; ks < 4; ++ks) {
-                                        if (gh >> ks & 1u) {
-                                            umma2_f16(d_o, ph + 2 * ks, vh + ks * (kGroup * 128 >> 4), id_o, acc);
-                                            acc = 1u;
-                                        }
+                                for (int ks = 0; ks < kKeys / kGroup; ++ks) {
+                                    if (groups >> ks & 1u) {
+                                        umma2_f16(tmem + kColO + j * 128, pd + (uint64_t)((ks >> 2) * (kBlock >> 4) + 2 * (ks & 3)),
+                                                  vd + (uint64_t)((j * kVHalf + ks * kGroup * 128) >> 4), id_o, acc);
+                                        acc = 1u;
                                     }
                                 }
                                 commit2(smem_u32(&ctl.v_empty[j]));
@@ -615,6 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         ++go;
                     }
+                    groups = next_groups;
                 }
                 rd.done(ctl, lane);
             }
@@ -709,6 +709,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     al = m == -INFINITY ? 0.f : ex2(m - mx);
                     m = mx;
                 }
+                uint32_t w[32];
+                if (alive) {
+                    const float mm = m == -INFINITY ? 0.f : -m;
+                    uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t u[16];
+                        tmem_ld16(s_tmem + 16 * c, u);
+                        tmem_wait_ld(u);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = ex2(fmaf(__uint_as_float(u[2 * e]), scale, mm));
+                            const float y = ex2(fmaf(__uint_as_float(u[2 * e + 1]), scale, mm));
+                            sum = f2_add(sum, f2(x, y));
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                            w[8 * c + e] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                    }
+                    const float2 s2 = f2_get(sum);
+                    l = l * al + (s2.x + s2.y);
+                }
                 // P's buffer and O are free once the product of the tile before is done
                 if (i > t0) {
                     if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (g - 1) & 1u, ctl, p.status, limit);
@@ -727,26 +748,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (alive) {
-                    const float mm = m == -INFINITY ? 0.f : -m;
-                    uint64_t sum = f2(0.f, 0.f);
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t u[16], w[8];
-                        tmem_ld16(s_tmem + 16 * c, u);
-                        tmem_wait_ld(u);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float x = ex2(fmaf(__uint_as_float(u[2 * e]), scale, mm));
-                            const float y = ex2(fmaf(__uint_as_float(u[2 * e + 1]), scale, mm));
-                            sum = f2_add(sum, f2(x, y));
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-                            w[e] = *reinterpret_cast<const uint32_t *>(&h);
-                        }
-                        *reinterpret_cast<uint4 *>(prow + (((2 * c) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                        *reinterpret_cast<uint4 *>(prow + (((2 * c + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
-                    const float2 s2 = f2_get(sum);
-                    l = l * al + (s2.x + s2.y);
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(prow + ((c ^ swz) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
