@@ -45,13 +45,14 @@ constexpr int kGroup = 16;                    // keys of one MMA step of O
 constexpr int kBlock = kHalf * 128;           // 64 rows x 64 bf16: 8 KB
 constexpr int kQOff = 0;                      // nine blocks
 constexpr int kKOff = 9 * kBlock;             // nine blocks
-constexpr int kVOff = 18 * kBlock;            // [half j][64-dim block][128 keys]: eight blocks
+constexpr int kVOff = 18 * kBlock;            // [key half][64-dim block][64 keys]: eight blocks
 constexpr int kPOff = 26 * kBlock;            // two blocks
 constexpr int kCtlOff = 28 * kBlock;
 constexpr int kVHalf = 4 * kBlock;
-constexpr int kSoftmaxWarps = 4;
-constexpr int kMmaWarp = 4, kKWarp = 5, kVWarp = 6, kQWarp = 7;
-constexpr int kThreads = 256;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kQWarp = 11;
+constexpr int kThreads = 384;
+constexpr int kRowThreads = 128;              // softmax threads that share 32 rows
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr float kRescaleLog2 = 8.0f;
@@ -76,11 +77,11 @@ struct Ctl {
     uint64_t k_full[3], k_empty[3];
     uint64_t v_full[2], v_empty[2];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full, o_full;
+    uint64_t s_full[2], p_full[2];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint32_t tmem_base;
     int32_t abort_flag;
-    float red[2][kRows];
+    float red[2][4][kHalf];
     Piece piece[kPieces];
 };
 constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
@@ -262,15 +263,19 @@ __device__ __forceinline__ Item load_item(const MlaParams &p, int index, int lan
     return it;
 }
 
-// Bounded wait of a whole warp; the same answer in every lane.
+// Bounded wait of a whole warp; the same answer in every lane.  (Reading the
+// clock takes long: only every few tries, each of which waits for a while.)
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
-        const uint64_t t0 = global_ns();
+        uint64_t t0 = 0;
 #pragma unroll 1
-        while (!ok && !*(volatile int32_t *)&c.abort_flag) {
+        for (uint32_t n = 1; !ok; ++n) {
             ok = mbar_try_wait(bar, parity);
-            if (!ok && global_ns() - t0 > limit_ns) {
+            if (ok || n % 8 != 0) continue;
+            if (*(volatile int32_t *)&c.abort_flag) break;
+            if (t0 == 0) t0 = global_ns();
+            if (global_ns() - t0 > limit_ns) {
                 *(volatile int32_t *)&c.abort_flag = 1;
                 flag(status, DSA_DEV_TIMEOUT);
             }
@@ -346,8 +351,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         mbar_init(smem_u32(&ctl.q_full), 2);
         mbar_init(smem_u32(&ctl.q_empty), 1);
-        mbar_init(smem_u32(&ctl.p_full), 2 * kSoftmaxWarps);
-        mbar_init(smem_u32(&ctl.o_full), 1);
+        mbar_init(smem_u32(&ctl.p_full[0]), 2 * kSoftmaxWarps);
+        mbar_init(smem_u32(&ctl.p_full[1]), kSoftmaxWarps);
         ctl.abort_flag = 0;
         fence_mbar_init();
     }
@@ -441,6 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int step = p.rows_per_box ? p.rows_per_box : 4; // keys of one copy
         const int copies = kHalf / step;                      // of one block
         const int mine = lane % copies;
+        const uint32_t k_bar = dsmem_map(smem_u32(&ctl.k_full[0]), 0);
         bool alive = true;
         Reader rd;
         while (alive) {
@@ -458,20 +464,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     r.w = max(0, any_row(b, seq, kv0, a + 3));
                 }
                 const uint32_t dst = s0 + kKOff + mine * step * 128;
+                const int row = __reduce_max_sync(0xffffffffu, r.x);        // one box: the same in every lane
 #pragma unroll 1
                 for (int q = 0; q < 3; ++q) {
+                    const int nb = min(3, n_blocks - 3 * q);
+                    const uint32_t full = k_bar + q * 8;
                     alive = wait_bar(smem_u32(&ctl.k_empty[q]), (g & 1u) ^ 1u, ctl, p.status, limit);
                     if (!alive) break;
                     if (b.skip_copies) continue;
-                    const int nb = min(3, n_blocks - 3 * q);
-                    const uint32_t full = dsmem_map(smem_u32(&ctl.k_full[q]), 0);
+                    if (p.rows_per_box == 64) {
+                        if (elect_one()) {
+                            arrive_expect_remote(full, (uint32_t)(nb * kBlock));
+#pragma unroll
+                            for (int c = 0; c < 3; ++c)
+                                if (c < nb) tma2_load(s0 + kKOff + (3 * q + c) * kBlock, &kv64_map, full, (3 * q + c) * 64, row);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
                     if (lane == 0) arrive_expect_remote(full, (uint32_t)(nb * kBlock));
                     __syncwarp();
                     // c % copies is lane % copies: copies divides 32
 #pragma unroll 1
                     for (int c = lane; c < nb * copies; c += 32) {
                         const int kb = 3 * q + c / copies;
-                        if (p.rows_per_box) tma2_load(dst + kb * kBlock, p.rows_per_box == 64 ? &kv64_map : &kv16_map, full, kb * 64, r.x);
+                        if (p.rows_per_box) tma2_load(dst + kb * kBlock, &kv16_map, full, kb * 64, r.x);
                         else tma2_gather4(dst + kb * kBlock, &kv1_map, full, kb * 64, r);
                     }
                     __syncwarp();
@@ -480,12 +497,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             rd.done(ctl, lane);
         }
     } else if (warp == kVWarp) {
-        // ---------------- values: all keys of a tile, this CTA's 256 dims in two halves.
+        // ---------------- values: all keys of a tile in two halves, this CTA's 256 dims.
         // Groups of 16 keys that nobody sees are neither read nor multiplied; in a
         // group that is seen in part the other rows are the spare one's copies
         // (P is 0 there, and 0 times what an unused row may hold is not).
         uint32_t g = 0;
         bool alive = true;
+        const uint32_t v_bar = dsmem_map(smem_u32(&ctl.v_full[0]), 0);
         Reader rd;
         while (alive) {
             const Piece *pc = rd.next(ctl, p.status, limit);
@@ -496,7 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t groups = tile_groups(*pc, pos);
                 int4 r;
                 bool box16 = true, box64 = true;
-                if (groups == 0xffu && p.rows_per_box == 64 && pos >= pc->lo && pos + kKeys - 1 <= pc->hi) {
+                const bool simple = p.rows_per_box == 64 && pos >= pc->lo && pos + kKeys - 1 <= pc->hi;   // all seen
+                if (simple) {
                     r.x = any_row(b, pc->seq, pc->kv0, pos + ((lane & 16) << 2));
                     if (r.x < 0) {
                         flag(p.status, DSA_DEV_BAD_INDEX);
@@ -517,23 +536,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     box64 = ((halves >> (lane & 16)) & 0xffffu) == 0xffffu;
                 }
                 const bool on = (groups >> (lane >> 2)) & 1u;
-                const uint32_t bytes = (uint32_t)__popc(groups) * (kGroup * 128u) * 2u;
+                const bool boxes = __all_sync(0xffffffffu, box64);          // two of 64 rows
+                const int row0 = __reduce_min_sync(0xffffffffu, lane < 16 ? r.x : INT32_MAX);
+                const int row1 = __reduce_min_sync(0xffffffffu, lane < 16 ? INT32_MAX : r.x);
 #pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    alive = wait_bar(smem_u32(&ctl.v_empty[j]), (g & 1u) ^ 1u, ctl, p.status, limit);
+                for (int h = 0; h < 2; ++h) {
+                    alive = wait_bar(smem_u32(&ctl.v_empty[h]), (g & 1u) ^ 1u, ctl, p.status, limit);
                     if (!alive) break;
                     if (b.skip_copies) continue;
-                    const uint32_t full = dsmem_map(smem_u32(&ctl.v_full[j]), 0);
-                    if (lane == 0) arrive_expect_remote(full, bytes);
+                    const uint32_t full = v_bar + h * 8;
+                    if (boxes) {
+                        // the half's four blocks of this CTA's dims
+                        if (elect_one()) {
+                            arrive_expect_remote(full, kVHalf);
+#pragma unroll
+                            for (int d = 0; d < 4; ++d)
+                                tma2_load(s0 + kVOff + h * kVHalf + d * kBlock, &kv64_map, full, 256 * (int)rank + 64 * d, h ? row1 : row0);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                    if (lane == 0) arrive_expect_remote(full, (uint32_t)__popc((groups >> (4 * h)) & 0xfu) * (kGroup * 128u) * 4u);
                     __syncwarp();
+                    if ((lane >> 4) == h && on) {
+                        const uint32_t dst = s0 + kVOff + h * kVHalf + (lane & 15) * 4 * 128;
 #pragma unroll 1
-                    for (int d = 0; d < 2; ++d) {
-                        const uint32_t dst = s0 + kVOff + j * kVHalf + d * (kVHalf / 2) + lane * 4 * 128;
-                        const int32_t col = 256 * (int)rank + 128 * j + 64 * d;
-                        if (box16) {
-                            if ((lane & (box64 ? 15 : 3)) == 0 && on) tma2_load(dst, box64 ? &kv64_map : &kv16_map, full, col, r.x);
-                        } else if (on) {
-                            tma2_gather4(dst, &kv1_map, full, col, r);
+                        for (int d = 0; d < 4; ++d) {
+                            const int32_t col = 256 * (int)rank + 64 * d;
+                            if (box16) {
+                                if ((lane & (box64 ? 15 : 3)) == 0)
+                                    tma2_load(dst + d * kBlock, box64 ? &kv64_map : &kv16_map, full, col, r.x);
+                            } else {
+                                tma2_gather4(dst + d * kBlock, &kv1_map, full, col, r);
+                            }
                         }
                     }
                     __syncwarp();
@@ -547,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_s = idesc_f16(kRows, kKeys, true, false, false);
             constexpr uint32_t id_o = idesc_f16(kRows, 256, true, false, true);
             const uint64_t qd = sdesc_sw128(s0 + kQOff, 16, 1024), kd = sdesc_sw128(s0 + kKOff, 16, 1024);
-            const uint64_t pd = sdesc_sw128(s0 + kPOff, 16, 1024), vd = sdesc_sw128(s0 + kVOff, kVHalf / 2, 1024);
+            const uint64_t pd = sdesc_sw128(s0 + kPOff, 16, 1024), vd = sdesc_sw128(s0 + kVOff, kBlock, 1024);
             uint32_t gs = 0, go = 0, n = 0;                   // tiles scored and summed, pieces
             bool alive = true;
             Reader rd;
@@ -563,15 +598,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ++n;
                 }
                 uint32_t groups = 0, next_groups = 0;         // of the tile before, of this one
+                bool keys = false;                            // this tile's have been seen to be there
 #pragma unroll 1
                 for (int i = t0; alive && t1 > t0 && i <= t1; ++i) {
                     if (i < t1) {
                         const uint32_t d_s = tmem + kColS + (gs & 1u) * (kKeys / 2);
 #pragma unroll
                         for (int q = 0; q < 3; ++q) {
-                            if (alive) alive = wait_bar(smem_u32(&ctl.k_full[q]), gs & 1u, ctl, p.status, limit);
+                            if (alive && !keys) alive = wait_bar(smem_u32(&ctl.k_full[q]), gs & 1u, ctl, p.status, limit);
                             if (!alive) break;
-                            tc_fence_after();
+                            if (q == 0 || !keys) tc_fence_after();
                             if (elect_one()) {
 #pragma unroll
                                 for (int kb = 3 * q; kb < 3 * q + 3; ++kb) {
@@ -590,25 +626,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ++gs;
                         next_groups = __reduce_or_sync(0xffffffffu, tile_groups(*pc, tile_pos(*pc, i)));
                     }
+                    keys = false;
                     if (alive && i > t0) {
-                        alive = wait_bar(smem_u32(&ctl.p_full), go & 1u, ctl, p.status, limit);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (alive) alive = wait_bar(smem_u32(&ctl.v_full[j]), go & 1u, ctl, p.status, limit);
+                        for (int h = 0; h < 2; ++h) {
+                            if (alive) alive = wait_bar(smem_u32(&ctl.v_full[h]), go & 1u, ctl, p.status, limit);
+                            if (alive) alive = wait_bar(smem_u32(&ctl.p_full[h]), go & 1u, ctl, p.status, limit);
                             if (!alive) break;
+                            // the next tile's keys, asked for while there are products to run
+                            if (h == 1 && i + 1 < t1)
+                                keys = __all_sync(0xffffffffu, mbar_test(smem_u32(&ctl.k_full[0]), gs & 1u) &&
+                                                                   mbar_test(smem_u32(&ctl.k_full[1]), gs & 1u) &&
+                                                                   mbar_test(smem_u32(&ctl.k_full[2]), gs & 1u));
                             tc_fence_after();
                             if (elect_one()) {
-                                uint32_t acc = i - 1 > t0 ? 1u : 0u;
 #pragma unroll
-                                for (int ks = 0; ks < kKeys / kGroup; ++ks) {
-                                    if (groups >> ks & 1u) {
-                                        umma2_f16(tmem + kColO + j * 128, pd + (uint64_t)((ks >> 2) * (kBlock >> 4) + 2 * (ks & 3)),
-                                                  vd + (uint64_t)((j * kVHalf + ks * kGroup * 128) >> 4), id_o, acc);
-                                        acc = 1u;
+                                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                                    for (int ks = 0; ks < 4; ++ks) {
+                                        const int k = 4 * h + ks;
+                                        if (groups >> k & 1u)
+                                            umma2_f16(tmem + kColO + j * 128, pd + (uint64_t)(h * (kBlock >> 4) + 2 * ks),
+                                                      vd + (uint64_t)((h * kVHalf + j * 2 * kBlock + ks * kGroup * 128) >> 4), id_o,
+                                                      i - 1 > t0 || (groups & ((1u << k) - 1)) != 0);
                                     }
                                 }
-                                commit2(smem_u32(&ctl.v_empty[j]));
-                                if (j == 1) commit2(smem_u32(&ctl.o_full));
+                                commit2(smem_u32(&ctl.v_empty[h]));
                             }
                             __syncwarp();
                         }
@@ -620,30 +663,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        // ---------------- softmax and output: TMEM lane tx holds row tx % 64 of
-        // this CTA's rows, keys (of S) or dims (of O) of half tx / 64.  The loops
-        // are kept small: unrolled over all 64 keys this kernel was bound by
+        // ---------------- softmax and output.  TMEM lane L holds row L % 64 of this
+        // CTA's rows, keys (of S) or dims (of O) of half L / 64; two warps share
+        // each lane quarter and take half of its columns each.  The loops are kept
+        // small: unrolled over 64 keys in every role this kernel was bound by
         // instruction fetches (120 KB of code; prefill 3.0 ms).
         const int tx = (int)threadIdx.x;
-        const int half = tx >> 6, r = tx & 63;
-        const uint32_t lane_tmem = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t p_bar = dsmem_map(smem_u32(&ctl.p_full), 0);
-        const int pair = 1 + (warp & 1);                      // named barrier of the two warps that share rows
-        uint8_t *prow = smem + kPOff + half * kBlock + (r >> 3) * 1024 + (r & 7) * 128;
+        const int quarter = warp & 3, part = warp >> 2, half = quarter >> 1;
+        const int r = (warp & 1) * 32 + lane, c4 = half * 2 + part;
+        const uint32_t lane_tmem = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t p_bar0 = dsmem_map(smem_u32(&ctl.p_full[0]), 0), p_bar1 = dsmem_map(smem_u32(&ctl.p_full[1]), 0);
+        const int rows_bar = 1 + (warp & 1);                  // named barrier of the four warps that share rows
+        uint8_t *prow = smem + kPOff + half * kBlock + r * 128;
         const uint32_t swz = (uint32_t)(r & 7);
         if (rank == 0 && tx == 0) p.split[cluster] = Split{0, 0, 0, 0};
         // A scale that is not positive is multiplied in where scores are masked.
         const bool plain = p.scale_log2 > 0.f;
         const float scale = plain ? p.scale_log2 : 1.f;
         uint32_t g = 0;                                       // tiles so far
-        // The two warps of a pair run the same sequence of named barriers whatever
-        // happens; `alive` (the same in a warp) only gates work on tensor memory
+        // The softmax warps run the same sequence of named barriers whatever happens; `alive` (the same in a warp) only gates work on tensor memory
         // and shared memory after a bounded wait gave up.
         bool alive = true;
         Reader rd;
         while (true) {
             const Piece *pc = rd.next(ctl, p.status, limit);
-            if (named_barrier_or(pair, 64, !pc)) break;
+            // (all of them: their staging of the last output ends before any stores a P)
+            if (named_barrier_or(3, kSoftmaxWarps * 32, !pc)) break;
             if (pc->end) break;
             const int t0 = pc->t0, t1 = pc->t1;
             const int row = kHalf * (int)rank + r;
@@ -661,14 +706,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int p0 = tile_pos(*pc, i);
                 if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 1u]), (g >> 1) & 1u, ctl, p.status, limit);
                 tc_fence_after();
-                const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2);
+                const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2) + 32 * part;
                 // does every row of the item see every key of the tile?
                 if (!(plain && p0 + kKeys - 1 <= pc->min_pos && (int64_t)p0 > (int64_t)pc->hi - p.pr.window) && alive) {
-                    const int kp = p0 + kHalf * half;
+                    const int kp = p0 + kHalf * half + 32 * part;
                     const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);   // first of the window
                     const int s_lo = pc->s_lo, s_hi = min(pc->s_hi, pos + 1);
 #pragma unroll 1
-                    for (int c = 0; c < 64; c += 16) {
+                    for (int c = 0; c < 32; c += 16) {
                         uint32_t u[16];
                         tmem_ld16(s_tmem + c, u);
                         tmem_wait_ld(u);
@@ -682,26 +727,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tmem_wait_st();
                 }
-                float top = -INFINITY;
+                uint32_t u[32];
                 if (alive) {
-#pragma unroll 1
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t u[32];
-                        tmem_ld32(s_tmem + c, u);
-                        tmem_wait_ld(u);
-                        float a0 = top, a1 = -INFINITY;
+                    tmem_ld32(s_tmem, u);
+                    tmem_wait_ld(u);
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            a0 = fmaxf(fmaxf(a0, __uint_as_float(u[e])), __uint_as_float(u[e + 1]));
-                            a1 = fmaxf(fmaxf(a1, __uint_as_float(u[e + 2])), __uint_as_float(u[e + 3]));
-                        }
-                        top = fmaxf(a0, a1);
-                    }
+                    for (int e = 0; e < 32; ++e) u[e] = 0xff800000u;   // -infinity
                 }
-                float *red = ctl.red[g & 1u];
-                red[tx] = top;
-                named_barrier(pair, 64);
-                const float mx = fmaxf(top, red[tx ^ 64]) * scale;
+                float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    a0 = fmaxf(fmaxf(a0, __uint_as_float(u[e])), __uint_as_float(u[e + 1]));
+                    a1 = fmaxf(fmaxf(a1, __uint_as_float(u[e + 2])), __uint_as_float(u[e + 3]));
+                }
+                auto &red = ctl.red[g & 1u];
+                red[c4][r] = fmaxf(a0, a1);
+                named_barrier(rows_bar, kRowThreads);
+                const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r])) * scale;
                 // The maximum is only raised by more than 2^8 at a time (the result
                 // is the same either way): O is rescaled seldom.
                 float al = 1.f;
@@ -709,104 +752,122 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     al = m == -INFINITY ? 0.f : ex2(m - mx);
                     m = mx;
                 }
-                uint32_t w[32];
-                if (alive) {
-                    const float mm = m == -INFINITY ? 0.f : -m;
-                    uint64_t sum = f2(0.f, 0.f);
+                const float mm = m == -INFINITY ? 0.f : -m;
+                uint64_t sum = f2(0.f, 0.f);
+                uint32_t w[16];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t u[16];
-                        tmem_ld16(s_tmem + 16 * c, u);
-                        tmem_wait_ld(u);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float x = ex2(fmaf(__uint_as_float(u[2 * e]), scale, mm));
-                            const float y = ex2(fmaf(__uint_as_float(u[2 * e + 1]), scale, mm));
-                            sum = f2_add(sum, f2(x, y));
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-                            w[8 * c + e] = *reinterpret_cast<const uint32_t *>(&h);
-                        }
-                    }
-                    const float2 s2 = f2_get(sum);
-                    l = l * al + (s2.x + s2.y);
+                for (int e = 0; e < 16; ++e) {
+                    const float x = ex2(fmaf(__uint_as_float(u[2 * e]), scale, mm));
+                    const float y = ex2(fmaf(__uint_as_float(u[2 * e + 1]), scale, mm));
+                    sum = f2_add(sum, f2(x, y));
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                // P's buffer and O are free once the product of the tile before is done
-                if (i > t0) {
-                    if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (g - 1) & 1u, ctl, p.status, limit);
-                    if (__any_sync(0xffffffffu, al != 1.f) && alive) {
+                const float2 s2 = f2_get(sum);
+                l = l * al + (s2.x + s2.y);
+                // O may be rescaled once the product of the tile before is done
+                if (i > t0 && __any_sync(0xffffffffu, al != 1.f)) {
+                    if (alive) alive = wait_bar(smem_u32(&ctl.v_empty[1]), (g - 1) & 1u, ctl, p.status, limit);
+                    if (alive) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 256; c += 16) {
-                            uint32_t u[16];
-                            tmem_ld16(lane_tmem + kColO + c, u);
-                            tmem_wait_ld(u);
+                        for (int c = 0; c < 128; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(lane_tmem + kColO + 128 * part + c, o);
+                            tmem_wait_ld(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * al);
-                            tmem_st16(lane_tmem + kColO + c, u);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                            tmem_st16(lane_tmem + kColO + 128 * part + c, o);
                         }
                         tmem_wait_st();
                     }
                 }
+                // The product begins with the first half of the keys: of the second
+                // half's warps it only needs that O is as it should be.
+                if (half == 1 && alive) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote(p_bar0);
+                }
+                // and P's half is free once the same half of the product before is done
+                if (i > t0 && alive) alive = wait_bar(smem_u32(&ctl.v_empty[half]), (g - 1) & 1u, ctl, p.status, limit);
                 if (alive) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(prow + ((c ^ swz) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(prow + (((4 * part + c) ^ swz) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_remote(p_bar);
+                    if (lane == 0) arrive_remote(half ? p_bar1 : p_bar0);
                 }
             }
             // ---- the piece's output
             const bool empty = t1 == t0;
             if (!empty) {
-                if (alive) alive = wait_bar(smem_u32(&ctl.o_full), (g - 1) & 1u, ctl, p.status, limit);
+                if (alive) alive = wait_bar(smem_u32(&ctl.v_empty[1]), (g - 1) & 1u, ctl, p.status, limit);
                 tc_fence_after();
-                named_barrier(pair, 64);                      // the last tile's maxima have been read
-                ctl.red[0][tx] = l;
-                named_barrier(pair, 64);
-                l += ctl.red[0][tx ^ 64];
-                named_barrier(pair, 64);
+                named_barrier(rows_bar, kRowThreads);         // the last tile's maxima have been read
+                ctl.red[0][c4][r] = l;
+                named_barrier(rows_bar, kRowThreads);
+                l = (ctl.red[0][0][r] + ctl.red[0][1][r]) + (ctl.red[0][2][r] + ctl.red[0][3][r]);
+                named_barrier(rows_bar, kRowThreads);
             }
             const bool none = pos < 0 || l == 0.f;            // a sum of NaN is not none
             if (alive) {
-                // a part goes to slot 2c where the item began in an earlier cluster, else to 2c + 1
-                const bool whole = pc->whole;
+                // 64 bytes of each of the warp's 32 rows at a time, turned in the warp's
+                // share of P's buffer so that stores write whole sectors (a row a lane
+                // straight from the accumulator took 13,000 clocks).
+                // A part goes to slot 2c where the item began in an earlier cluster, else to 2c + 1.
+                const bool whole = pc->whole, narrow = whole && p.out_bf16;
                 const int64_t out_row = (int64_t)pc->row0 + row;
                 const int64_t part_row = ((int64_t)2 * cluster + (t0 == 0 ? 1 : 0)) * kRows + row;
-                const float factor = whole ? 1.f / l : 1.f;
-                float *dst = whole ? static_cast<float *>(p.out) + out_row * D_L : p.part_o + part_row * D_L;
-                uint16_t *dst16 = static_cast<uint16_t *>(p.out) + out_row * D_L;
-                const bool narrow = whole && p.out_bf16;
+                const float factor = none ? 0.f : whole ? 1.f / l : 1.f;
+                const int col0 = 256 * half + 128 * part, bytes = narrow ? 2 : 4;
+                const int rows_left = pc->nrows - (row - lane);            // of the warp's 32
+                uint8_t *stage = smem + kPOff + warp * 2048;
+                uint8_t *dst = (whole ? static_cast<uint8_t *>(p.out) + (out_row - lane) * D_L * bytes
+                                      : reinterpret_cast<uint8_t *>(p.part_o + (part_row - lane) * D_L)) + col0 * bytes;
+                const int step = 64 / bytes;
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 16) {
-                    uint32_t u[16];
-                    if (!empty) {
-                        tmem_ld16(lane_tmem + kColO + c, u);
-                        tmem_wait_ld(u);
+                for (int c = 0; c < 128; c += step) {
+                    uint32_t o[32];
+                    const uint32_t at = lane_tmem + kColO + 128 * part + c;
+                    if (empty) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    } else if (narrow) {
+                        tmem_ld32(at, o);
+                        tmem_wait_ld(o);
+                    } else {
+                        uint32_t v[16];
+                        tmem_ld16(at, v);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = v[e];
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) u[e] = none ? 0u : __float_as_uint(__uint_as_float(u[e]) * factor);
-                    if (mine) {
-                        const int at = 256 * half + c;
-                        if (narrow) {
-                            uint32_t w[8];
+                    for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * factor);
+                    if (narrow) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
-                                w[e] = *reinterpret_cast<const uint32_t *>(&h);
-                            }
-                            *reinterpret_cast<uint4 *>(dst16 + at) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4 *>(dst16 + at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                reinterpret_cast<uint4 *>(dst + at)[q] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+                        for (int e = 0; e < 16; ++e) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                            o[e] = *reinterpret_cast<const uint32_t *>(&h);
                         }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4 *>(stage + sw64_offset((uint32_t)lane, (uint32_t)q)) =
+                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int rr = 8 * q + (lane >> 2);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + sw64_offset((uint32_t)rr, (uint32_t)(lane & 3)));
+                        if (rr < rows_left) *reinterpret_cast<uint4 *>(dst + (int64_t)rr * D_L * bytes + c * bytes + 16 * (lane & 3)) = v;
                     }
                     __syncwarp();
                 }
-                if (mine && half == 0) {
+                if (mine && c4 == 0) {
                     if (!whole) *reinterpret_cast<float2 *>(p.part_ml + part_row * 2) = none ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
                     else if (p.lse) p.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
