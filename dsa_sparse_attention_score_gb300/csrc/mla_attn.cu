@@ -50,9 +50,9 @@ constexpr int kPOff = 26 * kBlock;            // two blocks
 constexpr int kCtlOff = 28 * kBlock;
 constexpr int kVHalf = 4 * kBlock;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kQWarp = 11;
+constexpr int kSWarp = 8, kOWarp = 9, kKWarp = 10, kVWarp = 11;
 constexpr int kThreads = 384;
-constexpr int kRowThreads = 128;              // softmax threads that share 32 rows
+constexpr int kSBufs = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256;
 constexpr float kRescaleLog2 = 8.0f;
@@ -71,17 +71,19 @@ struct Piece {
     int32_t spare;                // a cache row that may be read for positions that no row sees
     int64_t kv0;
 };
-constexpr int kPieces = 4;        // read ahead
+constexpr int kPieces = 3;        // read ahead
 
 struct Ctl {
-    uint64_t k_full[3], k_empty[3];
-    uint64_t v_full[2], v_empty[2];
+    uint64_t k_full[3], k_empty[2];
+    uint64_t v_full[2];
+    uint64_t o_done[2][2];        // by tile and half of the keys: a group of softmax warps waits for every other tile
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2];
+    uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[2];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint32_t tmem_base;
     int32_t abort_flag;
-    float red[2][4][kHalf];
+    float red[2][2][2][kHalf];    // a group's maxima by tile and half of the keys
+    float m[2][kHalf];            // running maxima by tile
     Piece piece[kPieces];
 };
 constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
@@ -136,6 +138,14 @@ __device__ __forceinline__ void arrive_expect_remote(uint32_t bar, uint32_t byte
     asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ void named_barrier_arrive(int id, int nthreads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -298,6 +308,23 @@ struct Reader {
     }
 };
 
+// Writes the cluster's pieces into the ring, one a call, with a whole warp.
+struct Scheduler {
+    int item = 0, off = 0, left = 0;   // next item, costs of it done, costs left to this cluster
+    uint32_t n = 0;
+    bool end = false;
+    __device__ __forceinline__ Scheduler(const MlaParams &p, int cluster) {
+        const int64_t total = p.head->total;
+        const int n_cl = p.head->clusters;
+        if (cluster >= n_cl) return;
+        const Start st = p.start[cluster];
+        item = st.item;
+        off = st.off;
+        left = (int)(total * (cluster + 1) / n_cl - total * cluster / n_cl);
+    }
+    __device__ __noinline__ bool write(const MlaParams &p, Ctl &ctl, int lane);
+};
+
 // Cache row of a position, whoever sees it: negative where there is none.
 __device__ __forceinline__ int32_t any_row(const DevBatch &b, int seq, int64_t kv0, int pos) {
     int64_t r = kv0 + pos;
@@ -315,6 +342,56 @@ __device__ __noinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status
     if (r >= 0) return r;
     flag(status, DSA_DEV_BAD_INDEX);
     return pc->spare;
+}
+
+__device__ __noinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int lane) {
+    while (!end) {
+        end = left <= 0;
+        Piece pc{};
+        pc.end = end;
+        if (!end) {
+            const Item it = load_item(p, item, lane);
+            const int cost = item_cost(it.n), take = min(left, cost - off);
+            pc.t0 = min(off, it.n);
+            pc.t1 = min(off + take, it.n);
+            const bool first = off == 0;
+            left -= take;
+            off += take;
+            if (off == cost) {
+                ++item;
+                off = 0;
+            }
+            if (pc.t1 == pc.t0 && !(it.n == 0 && first)) continue;
+            pc.n_first = it.n_first;
+            pc.first_tile = it.first_tile;
+            pc.tile0 = it.tile0;
+            pc.lo = it.lo;
+            pc.hi = it.hi;
+            pc.s_lo = it.s_lo;
+            pc.s_hi = it.s_hi;
+            pc.min_pos = it.min_pos;
+            pc.row0 = it.row0;
+            pc.nrows = it.nrows;
+            pc.seq = it.seq;
+            pc.whole = pc.t0 == 0 && pc.t1 == it.n;
+            pc.rest = it.n - pc.t1;
+            pc.kv0 = seq_base(p.pr.b, it.seq);
+            // the row of the last position; row 0 if that has none (no row sees anything then)
+            pc.spare = it.hi < 0 || pc.kv0 < 0 ? 0 : max(0, any_row(p.pr.b, it.seq, pc.kv0, it.hi));
+        }
+        if (!wait_bar(smem_u32(&ctl.piece_empty[n % kPieces]), ((n / kPieces) & 1u) ^ 1u, ctl, p.status, p.pr.b.wait_ns)) {
+            end = true;
+            return false;
+        }
+        if (lane == 0) {
+            ctl.piece[n % kPieces] = pc;
+            mbar_arrive(smem_u32(&ctl.piece_full[n % kPieces]));
+        }
+        __syncwarp();
+        ++n;
+        break;
+    }
+    return true;
 }
 
 }  // namespace
@@ -336,27 +413,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(smem_u32(&ctl.k_full[i]), 2);       // both CTAs' producers, and their bytes
-            mbar_init(smem_u32(&ctl.k_empty[i]), 1);
-        }
+        for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctl.k_full[i]), 2);   // both CTAs' producers, and their bytes
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl.k_empty[i]), 1);
             mbar_init(smem_u32(&ctl.v_full[i]), 2);
-            mbar_init(smem_u32(&ctl.v_empty[i]), 1);
+            mbar_init(smem_u32(&ctl.o_done[i][0]), 1);
+            mbar_init(smem_u32(&ctl.o_done[i][1]), 1);
+        }
+        for (int i = 0; i < kSBufs; ++i) {
             mbar_init(smem_u32(&ctl.s_full[i]), 1);
+            mbar_init(smem_u32(&ctl.s_empty[i]), kSoftmaxWarps);          // a group's in both CTAs
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_u32(&ctl.piece_full[i]), 1);
-            mbar_init(smem_u32(&ctl.piece_empty[i]), kSoftmaxWarps + 2 + (rank == 0 ? 1 : 0));
+            mbar_init(smem_u32(&ctl.piece_empty[i]), kSoftmaxWarps + 2 + (rank == 0 ? 2 : 0));
         }
         mbar_init(smem_u32(&ctl.q_full), 2);
         mbar_init(smem_u32(&ctl.q_empty), 1);
-        mbar_init(smem_u32(&ctl.p_full[0]), 2 * kSoftmaxWarps);
-        mbar_init(smem_u32(&ctl.p_full[1]), kSoftmaxWarps);
+        mbar_init(smem_u32(&ctl.p_full[0]), kSoftmaxWarps);
+        mbar_init(smem_u32(&ctl.p_full[1]), kSoftmaxWarps / 2);
         ctl.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) tmem_alloc2(smem_u32(&ctl.tmem_base), kTmemCols);
+    if (warp == kSWarp) tmem_alloc2(smem_u32(&ctl.tmem_base), kTmemCols);
     if (warp == kKWarp && lane == 0) {
         tma_prefetch_desc(&kv64_map);
         tma_prefetch_desc(&q_lat_map);
@@ -370,79 +449,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();
     const uint64_t limit = b.wait_ns;
     const int n_blocks = p.tail ? 9 : 8;
+    // waits for the value product of half h of tile t's keys
+    auto wait_o = [&](int h, uint32_t t) {
+        return wait_bar(smem_u32(&ctl.o_done[t & 1u][h]), (t >> 1) & 1u, ctl, p.status, limit);
+    };
 
-    if (warp == kQWarp) {
-        // ---------------- the cluster's pieces, a few ahead, and their queries
-        const int64_t total = p.head->total;
-        const int n_cl = p.head->clusters;
-        int item = 0, off = 0, left = 0;                      // next item, costs of it done, costs left to do
-        if (cluster < n_cl) {
-            const Start st = p.start[cluster];
-            item = st.item;
-            off = st.off;
-            left = (int)(total * (cluster + 1) / n_cl - total * cluster / n_cl);
-        }
-        uint32_t n = 0, nq = 0;
-        bool end = false;
-        while (!end) {
-            end = left <= 0;
-            Piece pc{};
-            pc.end = end;
-            if (!end) {
-                const Item it = load_item(p, item, lane);
-                const int cost = item_cost(it.n), take = min(left, cost - off);
-                pc.t0 = min(off, it.n);
-                pc.t1 = min(off + take, it.n);
-                const bool first = off == 0;
-                left -= take;
-                off += take;
-                if (off == cost) {
-                    ++item;
-                    off = 0;
-                }
-                if (pc.t1 == pc.t0 && !(it.n == 0 && first)) continue;
-                pc.n_first = it.n_first;
-                pc.first_tile = it.first_tile;
-                pc.tile0 = it.tile0;
-                pc.lo = it.lo;
-                pc.hi = it.hi;
-                pc.s_lo = it.s_lo;
-                pc.s_hi = it.s_hi;
-                pc.min_pos = it.min_pos;
-                pc.row0 = it.row0;
-                pc.nrows = it.nrows;
-                pc.seq = it.seq;
-                pc.whole = pc.t0 == 0 && pc.t1 == it.n;
-                pc.rest = it.n - pc.t1;
-                pc.kv0 = seq_base(b, it.seq);
-                // the row of the last position; row 0 if that has none (no row sees anything then)
-                pc.spare = it.hi < 0 || pc.kv0 < 0 ? 0 : max(0, any_row(b, it.seq, pc.kv0, it.hi));
-            }
-            if (!wait_bar(smem_u32(&ctl.piece_empty[n % kPieces]), ((n / kPieces) & 1u) ^ 1u, ctl, p.status, limit)) break;
-            if (lane == 0) {
-                ctl.piece[n % kPieces] = pc;
-                mbar_arrive(smem_u32(&ctl.piece_full[n % kPieces]));
-            }
-            __syncwarp();
-            ++n;
-            if (end || pc.t1 == pc.t0) continue;
-            if (!wait_bar(smem_u32(&ctl.q_empty), (nq & 1u) ^ 1u, ctl, p.status, limit)) break;
-            ++nq;
-            if (b.skip_copies) continue;
-            const uint32_t full = dsmem_map(smem_u32(&ctl.q_full), 0);
-            if (lane == 0) arrive_expect_remote(full, (uint32_t)(n_blocks * kBlock));
-            __syncwarp();
-            // rows past the sequence's are some other token's (or zero past the
-            // tensor): they only feed accumulator rows that are never stored
-            const int row = pc.row0 + kHalf * (int)rank;
-            if (lane < n_blocks)
-                tma2_load(s0 + kQOff + lane * kBlock, lane < 8 ? &q_lat_map : &q_rope_map, full, (lane & 7) * 64, row);
-            __syncwarp();
-        }
-    } else if (warp == kKWarp) {
+    if (warp == kKWarp) {
         // ---------------- keys: this CTA's 64 of each tile, in three groups of blocks.
         // Keys that nobody sees may be anything: their scores are masked.
-        uint32_t g = 0;                                       // tiles so far
+        uint32_t g = 0, nq = 0;                               // tiles and pieces so far
+        const uint32_t q_bar = dsmem_map(smem_u32(&ctl.q_full), 0);
         const int step = p.rows_per_box ? p.rows_per_box : 4; // keys of one copy
         const int copies = kHalf / step;                      // of one block
         const int mine = lane % copies;
@@ -452,9 +468,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (alive) {
             const Piece *pc = rd.next(ctl, p.status, limit);
             if (!pc || pc->end) break;
-            const int t1 = pc->t1, seq = pc->seq;
+            const int t0 = pc->t0, t1 = pc->t1, seq = pc->seq;
             const int64_t kv0 = pc->kv0;
-            for (int i = pc->t0; alive && i < t1; ++i, ++g) {
+            for (int i = t0; alive && i < t1; ++i, ++g) {
                 const int a = tile_pos(*pc, i) + kHalf * (int)rank + mine * step;
                 int4 r;
                 r.x = max(0, any_row(b, seq, kv0, a));
@@ -469,8 +485,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int q = 0; q < 3; ++q) {
                     const int nb = min(3, n_blocks - 3 * q);
                     const uint32_t full = k_bar + q * 8;
-                    alive = wait_bar(smem_u32(&ctl.k_empty[q]), (g & 1u) ^ 1u, ctl, p.status, limit);
+                    // the last group is free once the tile before is scored
+                    if (q < 2) alive = wait_bar(smem_u32(&ctl.k_empty[q]), (g & 1u) ^ 1u, ctl, p.status, limit);
+                    else if (g > 0) alive = wait_bar(smem_u32(&ctl.s_full[(g - 1) & 3u]), ((g - 1) >> 2) & 1u, ctl, p.status, limit);
                     if (!alive) break;
+                    if (q == 2 && i == t0) {
+                        // the queries of this CTA's 64 rows.  Rows past the sequence's are some
+                        // other token's (or zero past the tensor): they only feed accumulator
+                        // rows that are never stored.
+                        alive = wait_bar(smem_u32(&ctl.q_empty), (nq & 1u) ^ 1u, ctl, p.status, limit);
+                        if (!alive) break;
+                        ++nq;
+                        const int q_row = __reduce_max_sync(0xffffffffu, pc->row0) + kHalf * (int)rank;
+                        if (!b.skip_copies && elect_one()) {
+                            arrive_expect_remote(q_bar, (uint32_t)(n_blocks * kBlock));
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) tma2_load(s0 + kQOff + c * kBlock, &q_lat_map, q_bar, c * 64, q_row);
+                            if (p.tail) tma2_load(s0 + kQOff + 8 * kBlock, &q_rope_map, q_bar, 0, q_row);
+                        }
+                        __syncwarp();
+                    }
                     if (b.skip_copies) continue;
                     if (p.rows_per_box == 64) {
                         if (elect_one()) {
@@ -541,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int row1 = __reduce_min_sync(0xffffffffu, lane < 16 ? INT32_MAX : r.x);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    alive = wait_bar(smem_u32(&ctl.v_empty[h]), (g & 1u) ^ 1u, ctl, p.status, limit);
+                    if (g > 0) alive = wait_o(h, g - 1);
                     if (!alive) break;
                     if (b.skip_copies) continue;
                     const uint32_t full = v_bar + h * 8;
@@ -576,38 +610,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             rd.done(ctl, lane);
         }
-    } else if (warp == kMmaWarp) {
-        // ---------------- MMA issuer: the even CTA's for both
-        if (rank == 0) {
-            constexpr uint32_t id_s = idesc_f16(kRows, kKeys, true, false, false);
-            constexpr uint32_t id_o = idesc_f16(kRows, 256, true, false, true);
-            const uint64_t qd = sdesc_sw128(s0 + kQOff, 16, 1024), kd = sdesc_sw128(s0 + kKOff, 16, 1024);
-            const uint64_t pd = sdesc_sw128(s0 + kPOff, 16, 1024), vd = sdesc_sw128(s0 + kVOff, kBlock, 1024);
-            uint32_t gs = 0, go = 0, n = 0;                   // tiles scored and summed, pieces
-            bool alive = true;
+    } else if (warp == kSWarp || warp == kOWarp) {
+        // ---------------- MMA issuers, the even CTA's for both: one for S, one for O.
+        // The tensor core's queue is short, a wait or a commit takes the issuer 50 to
+        // 150 clocks: while one issuer is at them the other's products run.
+        // O's issuers, which wait for the first P of a piece, also write the pieces
+        // down for all warps of their CTA, one ahead.
+        Scheduler sched(p, cluster);
+        bool alive = true;
+        if (warp == kOWarp) alive = sched.write(p, ctl, lane);
+        if (rank == 1) {
+            while (warp == kOWarp && alive && !sched.end) alive = sched.write(p, ctl, lane);
+        } else {
+            uint32_t g = 0, n = 0;                            // tiles and pieces so far
             Reader rd;
             while (alive) {
+                if (warp == kOWarp) alive = sched.write(p, ctl, lane);
+                if (!alive) break;
                 const Piece *pc = rd.next(ctl, p.status, limit);
                 if (!pc) break;
                 // (reductions put what is the same in every lane into uniform
                 // registers, where the products take their descriptors from)
                 const int t0 = __reduce_max_sync(0xffffffffu, pc->t0), t1 = __reduce_max_sync(0xffffffffu, pc->t1);
                 if (__any_sync(0xffffffffu, pc->end)) break;
-                if (t1 > t0) {
-                    alive = wait_bar(smem_u32(&ctl.q_full), n & 1u, ctl, p.status, limit);
-                    ++n;
-                }
-                uint32_t groups = 0, next_groups = 0;         // of the tile before, of this one
-                bool keys = false;                            // this tile's have been seen to be there
+                if (warp == kSWarp) {
+                    constexpr uint32_t id_s = idesc_f16(kRows, kKeys, true, false, false);
+                    const uint64_t qd = sdesc_sw128(s0 + kQOff, 16, 1024), kd = sdesc_sw128(s0 + kKOff, 16, 1024);
+                    if (t1 > t0) {
+                        alive = wait_bar(smem_u32(&ctl.q_full), n & 1u, ctl, p.status, limit);
+                        ++n;
+                    }
 #pragma unroll 1
-                for (int i = t0; alive && t1 > t0 && i <= t1; ++i) {
-                    if (i < t1) {
-                        const uint32_t d_s = tmem + kColS + (gs & 1u) * (kKeys / 2);
+                    for (int i = t0; alive && i < t1; ++i, ++g) {
+                        const uint32_t d_s = tmem + kColS + (g & 3u) * (kKeys / 2);
+                        alive = wait_bar(smem_u32(&ctl.s_empty[g & 3u]), ((g >> 2) & 1u) ^ 1u, ctl, p.status, limit);
 #pragma unroll
                         for (int q = 0; q < 3; ++q) {
-                            if (alive && !keys) alive = wait_bar(smem_u32(&ctl.k_full[q]), gs & 1u, ctl, p.status, limit);
+                            if (alive) alive = wait_bar(smem_u32(&ctl.k_full[q]), g & 1u, ctl, p.status, limit);
                             if (!alive) break;
-                            if (q == 0 || !keys) tc_fence_after();
+                            tc_fence_after();
                             if (elect_one()) {
 #pragma unroll
                                 for (int kb = 3 * q; kb < 3 * q + 3; ++kb) {
@@ -617,27 +658,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                         umma2_f16(d_s, qd + (uint64_t)(kb * (kBlock >> 4) + 2 * ks),
                                                   kd + (uint64_t)(kb * (kBlock >> 4) + 2 * ks), id_s, (kb | ks) != 0);
                                 }
-                                commit2(smem_u32(&ctl.k_empty[q]));
-                                if (q == 2) commit2(smem_u32(&ctl.s_full[gs & 1u]));
+                                commit2(q < 2 ? smem_u32(&ctl.k_empty[q]) : smem_u32(&ctl.s_full[g & 3u]));
                                 if (q == 2 && i == t1 - 1) commit2(smem_u32(&ctl.q_empty));
                             }
                             __syncwarp();
                         }
-                        ++gs;
-                        next_groups = __reduce_or_sync(0xffffffffu, tile_groups(*pc, tile_pos(*pc, i)));
                     }
-                    keys = false;
-                    if (alive && i > t0) {
+                } else {
+                    constexpr uint32_t id_o = idesc_f16(kRows, 256, true, false, true);
+                    const uint64_t pd = sdesc_sw128(s0 + kPOff, 16, 1024), vd = sdesc_sw128(s0 + kVOff, kBlock, 1024);
+#pragma unroll 1
+                    for (int i = t0; alive && i < t1; ++i, ++g) {
+                        const uint32_t groups = __reduce_or_sync(0xffffffffu, tile_groups(*pc, tile_pos(*pc, i)));
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            if (alive) alive = wait_bar(smem_u32(&ctl.v_full[h]), go & 1u, ctl, p.status, limit);
-                            if (alive) alive = wait_bar(smem_u32(&ctl.p_full[h]), go & 1u, ctl, p.status, limit);
+                            if (alive) alive = wait_bar(smem_u32(&ctl.v_full[h]), g & 1u, ctl, p.status, limit);
+                            if (alive) alive = wait_bar(smem_u32(&ctl.p_full[h]), g & 1u, ctl, p.status, limit);
                             if (!alive) break;
-                            // the next tile's keys, asked for while there are products to run
-                            if (h == 1 && i + 1 < t1)
-                                keys = __all_sync(0xffffffffu, mbar_test(smem_u32(&ctl.k_full[0]), gs & 1u) &&
-                                                                   mbar_test(smem_u32(&ctl.k_full[1]), gs & 1u) &&
-                                                                   mbar_test(smem_u32(&ctl.k_full[2]), gs & 1u));
                             tc_fence_after();
                             if (elect_one()) {
 #pragma unroll
@@ -648,32 +685,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                         if (groups >> k & 1u)
                                             umma2_f16(tmem + kColO + j * 128, pd + (uint64_t)(h * (kBlock >> 4) + 2 * ks),
                                                       vd + (uint64_t)((h * kVHalf + j * 2 * kBlock + ks * kGroup * 128) >> 4), id_o,
-                                                      i - 1 > t0 || (groups & ((1u << k) - 1)) != 0);
+                                                      i > t0 || (groups & ((1u << k) - 1)) != 0);
                                     }
                                 }
-                                commit2(smem_u32(&ctl.v_empty[h]));
+                                commit2(smem_u32(&ctl.o_done[g & 1u][h]));
                             }
                             __syncwarp();
                         }
-                        ++go;
                     }
-                    groups = next_groups;
                 }
                 rd.done(ctl, lane);
             }
         }
     } else {
         // ---------------- softmax and output.  TMEM lane L holds row L % 64 of this
-        // CTA's rows, keys (of S) or dims (of O) of half L / 64; two warps share
-        // each lane quarter and take half of its columns each.  The loops are kept
-        // small: unrolled over 64 keys in every role this kernel was bound by
-        // instruction fetches (120 KB of code; prefill 3.0 ms).
+        // CTA's rows, keys (of S) or dims (of O) of half L / 64.  Two groups of four
+        // warps take the tiles in turn, so that one's loads, maxima and barriers run
+        // beside the other's exponentials; the running maximum of a row goes from
+        // group to group.  (All eight warps on one tile took 3300 clocks a tile.)
         const int tx = (int)threadIdx.x;
-        const int quarter = warp & 3, part = warp >> 2, half = quarter >> 1;
-        const int r = (warp & 1) * 32 + lane, c4 = half * 2 + part;
+        const int quarter = warp & 3, group = warp >> 2, half = quarter >> 1;
+        const int r = (warp & 1) * 32 + lane;
         const uint32_t lane_tmem = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t p_bar0 = dsmem_map(smem_u32(&ctl.p_full[0]), 0), p_bar1 = dsmem_map(smem_u32(&ctl.p_full[1]), 0);
-        const int rows_bar = 1 + (warp & 1);                  // named barrier of the four warps that share rows
+        const uint32_t s_bar = dsmem_map(smem_u32(&ctl.s_empty[0]), 0);
+        // Named barriers: 1..4 the two warps of a group that share rows, 5 and 6 from
+        // one group to the other, 7 all.
+        const int rows_bar = 1 + 2 * group + (warp & 1);
         uint8_t *prow = smem + kPOff + half * kBlock + r * 128;
         const uint32_t swz = (uint32_t)(r & 7);
         if (rank == 0 && tx == 0) p.split[cluster] = Split{0, 0, 0, 0};
@@ -681,16 +719,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool plain = p.scale_log2 > 0.f;
         const float scale = plain ? p.scale_log2 : 1.f;
         uint32_t g = 0;                                       // tiles so far
-        // The softmax warps run the same sequence of named barriers whatever happens; `alive` (the same in a warp) only gates work on tensor memory
-        // and shared memory after a bounded wait gave up.
+        // The softmax warps run the same sequence of named barriers whatever happens;
+        // `alive` (the same in a warp) only gates work on tensor memory and shared
+        // memory after a bounded wait gave up.
         bool alive = true;
         Reader rd;
         while (true) {
             const Piece *pc = rd.next(ctl, p.status, limit);
             // (all of them: their staging of the last output ends before any stores a P)
-            if (named_barrier_or(3, kSoftmaxWarps * 32, !pc)) break;
+            if (named_barrier_or(7, kSoftmaxWarps * 32, !pc)) break;
             if (pc->end) break;
-            const int t0 = pc->t0, t1 = pc->t1;
+            const int t0 = pc->t0, t1 = pc->t1, n_first = pc->n_first;
             const int row = kHalf * (int)rank + r;
             const bool mine = row < pc->nrows;
             int pos = -1;
@@ -701,19 +740,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     pos = -1;
                 }
             }
-            float m = -INFINITY, l = 0.f;
+            // Every row of the item sees every key of the tiles [clear0, clear1).
+            const int64_t open = (int64_t)pc->hi - p.pr.window + 1;      // the last token's window begins here
+            const int clear0 = n_first + (open <= 0 ? 0 : (int)((open + kKeys - 1) / kKeys)) - pc->tile0;
+            const int clear1 = plain ? n_first + (pc->min_pos + 1) / kKeys - pc->tile0 : 0;
+            float m = -INFINITY, l = 0.f;                     // m: as of this group's last tile
             for (int i = t0; i < t1; ++i, ++g) {
-                const int p0 = tile_pos(*pc, i);
-                if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 1u]), (g >> 1) & 1u, ctl, p.status, limit);
+                if ((int)(g & 1u) != group) continue;
+                if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 3u]), (g >> 2) & 1u, ctl, p.status, limit);
                 tc_fence_after();
-                const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2) + 32 * part;
-                // does every row of the item see every key of the tile?
-                if (!(plain && p0 + kKeys - 1 <= pc->min_pos && (int64_t)p0 > (int64_t)pc->hi - p.pr.window) && alive) {
-                    const int kp = p0 + kHalf * half + 32 * part;
+                const uint32_t s_tmem = lane_tmem + kColS + (g & 3u) * (kKeys / 2);
+                if ((i < max(clear0, n_first) || i >= clear1) && alive) {
+                    const int kp = tile_pos(*pc, i) + kHalf * half;
                     const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);   // first of the window
                     const int s_lo = pc->s_lo, s_hi = min(pc->s_hi, pos + 1);
 #pragma unroll 1
-                    for (int c = 0; c < 32; c += 16) {
+                    for (int c = 0; c < 64; c += 16) {
                         uint32_t u[16];
                         tmem_ld16(s_tmem + c, u);
                         tmem_wait_ld(u);
@@ -727,90 +769,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tmem_wait_st();
                 }
-                uint32_t u[32];
+                float top = -INFINITY;
                 if (alive) {
-                    tmem_ld32(s_tmem, u);
-                    tmem_wait_ld(u);
-                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t u[32];
+                        tmem_ld32(s_tmem + c, u);
+                        tmem_wait_ld(u);
+                        float a0 = top, a1 = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) u[e] = 0xff800000u;   // -infinity
+                        for (int e = 0; e < 32; e += 4) {
+                            a0 = fmaxf(fmaxf(a0, __uint_as_float(u[e])), __uint_as_float(u[e + 1]));
+                            a1 = fmaxf(fmaxf(a1, __uint_as_float(u[e + 2])), __uint_as_float(u[e + 3]));
+                        }
+                        top = fmaxf(a0, a1);
+                    }
                 }
-                float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    a0 = fmaxf(fmaxf(a0, __uint_as_float(u[e])), __uint_as_float(u[e + 1]));
-                    a1 = fmaxf(fmaxf(a1, __uint_as_float(u[e + 2])), __uint_as_float(u[e + 3]));
+                auto &red = ctl.red[group][(g >> 1) & 1u];
+                red[half][r] = top;
+                named_barrier(rows_bar, 64);
+                const float mx = fmaxf(top, red[half ^ 1][r]) * scale;
+                float mo = -INFINITY;                         // as of the tile before
+                if (i > t0) {
+                    named_barrier(5 + (group ^ 1), kSoftmaxWarps * 32);
+                    mo = ctl.m[(g - 1) & 1u][r];
                 }
-                auto &red = ctl.red[g & 1u];
-                red[c4][r] = fmaxf(a0, a1);
-                named_barrier(rows_bar, kRowThreads);
-                const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r])) * scale;
                 // The maximum is only raised by more than 2^8 at a time (the result
                 // is the same either way): O is rescaled seldom.
-                float al = 1.f;
-                if (mx > m + kRescaleLog2 || (m == -INFINITY && mx != -INFINITY)) {
-                    al = m == -INFINITY ? 0.f : ex2(m - mx);
-                    m = mx;
+                const bool raise = mx > mo + kRescaleLog2 || (mo == -INFINITY && mx != -INFINITY);
+                const float mn = raise ? mx : mo;
+                if (i + 1 < t1) {
+                    if (half == 0) ctl.m[g & 1u][r] = mn;
+                    named_barrier_arrive(5 + group, kSoftmaxWarps * 32);
                 }
-                const float mm = m == -INFINITY ? 0.f : -m;
+                const float al = raise && mo != -INFINITY ? ex2(mo - mn) : raise ? 0.f : 1.f;
+                l *= m == -INFINITY ? 0.f : ex2(m - mn);      // (1 where the maximum stayed)
+                m = mn;
+                const float mm = mn == -INFINITY ? 0.f : -mn;
                 uint64_t sum = f2(0.f, 0.f);
-                uint32_t w[16];
+                if (alive) {
+                    // P in pairs of bf16 over the first half of S's own columns, until
+                    // its place in shared memory is free
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t u[16], w[8];
+                        tmem_ld16(s_tmem + 16 * c, u);
+                        tmem_wait_ld(u);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float x = ex2(fmaf(__uint_as_float(u[2 * e]), scale, mm));
-                    const float y = ex2(fmaf(__uint_as_float(u[2 * e + 1]), scale, mm));
-                    sum = f2_add(sum, f2(x, y));
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = ex2(fmaf(__uint_as_float(u[2 * e]), scale, mm));
+                            const float y = ex2(fmaf(__uint_as_float(u[2 * e + 1]), scale, mm));
+                            sum = f2_add(sum, f2(x, y));
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        tmem_st8(s_tmem + 8 * c, w);
+                    }
+                    tmem_wait_st();
                 }
                 const float2 s2 = f2_get(sum);
-                l = l * al + (s2.x + s2.y);
+                l += s2.x + s2.y;
                 // O may be rescaled once the product of the tile before is done
                 if (i > t0 && __any_sync(0xffffffffu, al != 1.f)) {
-                    if (alive) alive = wait_bar(smem_u32(&ctl.v_empty[1]), (g - 1) & 1u, ctl, p.status, limit);
+                    if (alive) alive = wait_o(1, g - 1);
                     if (alive) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 128; c += 16) {
+                        for (int c = 0; c < 256; c += 16) {
                             uint32_t o[16];
-                            tmem_ld16(lane_tmem + kColO + 128 * part + c, o);
+                            tmem_ld16(lane_tmem + kColO + c, o);
                             tmem_wait_ld(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                            tmem_st16(lane_tmem + kColO + 128 * part + c, o);
+                            tmem_st16(lane_tmem + kColO + c, o);
                         }
                         tmem_wait_st();
                     }
                 }
                 // The product begins with the first half of the keys: of the second
-                // half's warps it only needs that O is as it should be.
+                // half's warps it only needs that O is as it should be (said once the
+                // product before has begun, or its own count would be taken for this one's).
+                // P's half is free once the same half of the product before is done.
+                if (i > t0 && alive) alive = wait_o(0, g - 1);
                 if (half == 1 && alive) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_remote(p_bar0);
                 }
-                // and P's half is free once the same half of the product before is done
-                if (i > t0 && alive) alive = wait_bar(smem_u32(&ctl.v_empty[half]), (g - 1) & 1u, ctl, p.status, limit);
+                if (i > t0 && half == 1 && alive) alive = wait_o(1, g - 1);
                 if (alive) {
+                    uint32_t w[32];
+                    tmem_ld32(s_tmem, w);
+                    tmem_wait_ld(w);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        *reinterpret_cast<uint4 *>(prow + (((4 * part + c) ^ swz) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(prow + ((c ^ swz) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_remote(half ? p_bar1 : p_bar0);
+                    if (lane == 0) {
+                        arrive_remote(half ? p_bar1 : p_bar0);
+                        arrive_remote(s_bar + (g & 3u) * 8);  // the next S but three may come
+                    }
                 }
             }
             // ---- the piece's output
             const bool empty = t1 == t0;
             if (!empty) {
-                if (alive) alive = wait_bar(smem_u32(&ctl.v_empty[1]), (g - 1) & 1u, ctl, p.status, limit);
+                if (alive) alive = wait_o(1, g - 1);
                 tc_fence_after();
-                named_barrier(rows_bar, kRowThreads);         // the last tile's maxima have been read
-                ctl.red[0][c4][r] = l;
-                named_barrier(rows_bar, kRowThreads);
-                l = (ctl.red[0][0][r] + ctl.red[0][1][r]) + (ctl.red[0][2][r] + ctl.red[0][3][r]);
-                named_barrier(rows_bar, kRowThreads);
+                if ((int)((g - 1) & 1u) == group && half == 0) ctl.m[0][r] = m;
+                named_barrier(7, kSoftmaxWarps * 32);
+                const float mn = ctl.m[0][r];
+                auto &sums = ctl.red[0];                      // nobody is at a tile now
+                sums[group][half][r] = m == -INFINITY ? 0.f : l * ex2(m - mn);
+                m = mn;
+                named_barrier(7, kSoftmaxWarps * 32);
+                l = (sums[0][0][r] + sums[0][1][r]) + (sums[1][0][r] + sums[1][1][r]);
             }
             const bool none = pos < 0 || l == 0.f;            // a sum of NaN is not none
             if (alive) {
@@ -822,7 +897,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int64_t out_row = (int64_t)pc->row0 + row;
                 const int64_t part_row = ((int64_t)2 * cluster + (t0 == 0 ? 1 : 0)) * kRows + row;
                 const float factor = none ? 0.f : whole ? 1.f / l : 1.f;
-                const int col0 = 256 * half + 128 * part, bytes = narrow ? 2 : 4;
+                const int col0 = 256 * half + 128 * group, bytes = narrow ? 2 : 4;
                 const int rows_left = pc->nrows - (row - lane);            // of the warp's 32
                 uint8_t *stage = smem + kPOff + warp * 2048;
                 uint8_t *dst = (whole ? static_cast<uint8_t *>(p.out) + (out_row - lane) * D_L * bytes
@@ -831,7 +906,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < 128; c += step) {
                     uint32_t o[32];
-                    const uint32_t at = lane_tmem + kColO + 128 * part + c;
+                    const uint32_t at = lane_tmem + kColO + 128 * group + c;
                     if (empty) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0u;
@@ -867,7 +942,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (mine && c4 == 0) {
+                if (mine && half == 0 && group == 0) {
                     if (!whole) *reinterpret_cast<float2 *>(p.part_ml + part_row * 2) = none ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
                     else if (p.lse) p.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
                 }
@@ -897,7 +972,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     pdl_trigger();
     cluster_sync_all();
-    if (warp == kMmaWarp) {
+    if (warp == kSWarp) {
         tc_fence_after();
         tmem_dealloc2(tmem, kTmemCols);
     }
