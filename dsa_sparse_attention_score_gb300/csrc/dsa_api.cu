@@ -971,6 +971,7 @@ static dsa_status_t mla_attn_impl(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope,
         !make_map(&m.kv1, bf16, kv_cache, width, rows, 64, 1))
         return DSA_ERR_CUDA;
     MlaLaunch a;
+    a.q_lat = q_lat;
     a.H = H;
     a.tail = tail;
     a.window = window;

@@ -219,6 +219,7 @@ cudaError_t launch_sparse_attn_q8(const AttnQ8Launch &a, const DevBatch &b, uint
 // Attention over all visible rows of the latent cache, or those of a window and
 // the first ones (mla_attn.cu): two or three launches.
 struct MlaLaunch {
+    const uint16_t *q_lat;            // bf16 [T, H, 512]
     int H, tail;                      // tail 0: 512-wide rows
     int window;                       // INT32_MAX: every position up to the token's
     int n_sink;

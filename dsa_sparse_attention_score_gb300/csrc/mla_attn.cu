@@ -43,18 +43,19 @@ constexpr int kHalf = 64;                     // rows and keys of one CTA
 constexpr int kKeys = 128;                    // positions of a tile
 constexpr int kGroup = 16;                    // keys of one MMA step of O
 constexpr int kBlock = kHalf * 128;           // 64 rows x 64 bf16: 8 KB
-constexpr int kQOff = 0;                      // nine blocks
-constexpr int kKOff = 9 * kBlock;             // nine blocks
-constexpr int kVOff = 18 * kBlock;            // [key half][64-dim block][64 keys]: eight blocks
+constexpr int kQTmem = 4;                     // blocks of the queries in tensor memory
+constexpr int kQOff = 0;                      // the other five
+constexpr int kKOff = 5 * kBlock;             // nine blocks
+constexpr int kVOff = 14 * kBlock;            // three halves of a tile's keys: [64-dim block][64 keys]
 constexpr int kPOff = 26 * kBlock;            // two blocks
 constexpr int kCtlOff = 28 * kBlock;
 constexpr int kVHalf = 4 * kBlock;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSWarp = 8, kOWarp = 9, kKWarp = 10, kVWarp = 11;
 constexpr int kThreads = 384;
-constexpr int kSBufs = 4;
+constexpr int kSBufs = 2, kVBufs = 3;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0, kColS = 256;
+constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kItemCost = 1;                  // what an item costs beside its tiles, in tiles
@@ -75,9 +76,9 @@ constexpr int kPieces = 3;        // read ahead
 
 struct Ctl {
     uint64_t k_full[3], k_empty[2];
-    uint64_t v_full[2];
+    uint64_t v_full[kVBufs];
     uint64_t o_done[2][2];        // by tile and half of the keys: a group of softmax warps waits for every other tile
-    uint64_t q_full, q_empty;
+    uint64_t q_full, q_empty, q_tmem;
     uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[2];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint32_t tmem_base;
@@ -103,6 +104,16 @@ __device__ __forceinline__ void umma2_f16(uint32_t d, uint64_t a, uint64_t b, ui
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// The same with A in tensor memory: row r of the CTA's 64 in lanes r and r + 64, two
+// values a column.
+__device__ __forceinline__ void umma2_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 // One arrival at the same barrier of both CTAs once the MMAs issued so far are done.
@@ -231,6 +242,7 @@ struct MlaParams {
     const PlanHead *head;
     const PlanItem *items;
     const Start *start;
+    const uint16_t *q_lat;        // bf16 [T * H, 512]
     Split *split;                 // [clusters]
     float *part_o;                // [2 * clusters, 128, 512]
     float *part_ml;               // [2 * clusters, 128, 2]
@@ -275,23 +287,26 @@ __device__ __forceinline__ Item load_item(const MlaParams &p, int index, int lan
 
 // Bounded wait of a whole warp; the same answer in every lane.  (Reading the
 // clock takes long: only every few tries, each of which waits for a while.)
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        uint64_t t0 = 0;
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int32_t *abort_flag, uint32_t *status, uint64_t limit_ns) {
+    bool ok = false;
+    uint64_t t0 = 0;
 #pragma unroll 1
-        for (uint32_t n = 1; !ok; ++n) {
-            ok = mbar_try_wait(bar, parity);
-            if (ok || n % 8 != 0) continue;
-            if (*(volatile int32_t *)&c.abort_flag) break;
-            if (t0 == 0) t0 = global_ns();
-            if (global_ns() - t0 > limit_ns) {
-                *(volatile int32_t *)&c.abort_flag = 1;
-                flag(status, DSA_DEV_TIMEOUT);
-            }
+    for (uint32_t n = 1; !ok; ++n) {
+        ok = mbar_try_wait(bar, parity);
+        if (ok || n % 8 != 0) continue;
+        if (*(volatile int32_t *)abort_flag) break;
+        const uint64_t t = global_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit_ns) {
+            *(volatile int32_t *)abort_flag = 1;
+            flag(status, DSA_DEV_TIMEOUT);
         }
     }
     return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl &c, uint32_t *status, uint64_t limit_ns) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_long(bar, parity, &c.abort_flag, status, limit_ns);
 }
 
 // The ring of pieces, as one warp reads it.
@@ -394,6 +409,40 @@ __device__ __noinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int 
     return true;
 }
 
+// Copies of rows that do not lie together 64 at a time, out of the usual path:
+// copies / block pieces of the keys (c = lane, lane + 32...; each lane's rows are
+// those of its piece of every block), and the values' groups that some row sees.
+__device__ __noinline__ void copy_keys(uint32_t dst, const CUtensorMap *kv16, const CUtensorMap *kv1, uint32_t full, int kb0, int n,
+                                       int copies, int4 r, int lane) {
+#pragma unroll 1
+    for (int c = lane; c < n * copies; c += 32) {             // copies divides 32
+        const int kb = kb0 + c / copies;
+        if (copies == 4) tma2_load(dst + kb * kBlock, kv16, full, kb * 64, r.x);
+        else tma2_gather4(dst + kb * kBlock, kv1, full, kb * 64, r);
+    }
+    __syncwarp();
+}
+__device__ __noinline__ void copy_values(uint32_t dst, const CUtensorMap *kv64, const CUtensorMap *kv16, const CUtensorMap *kv1,
+                                         uint32_t full, int col, int4 r, int box, int lane) {
+#pragma unroll 1
+    for (int d = 0; d < 4; ++d) {
+        if (box) {
+            if ((lane & (box - 1)) == 0) tma2_load(dst + d * kBlock, box == 16 ? kv64 : kv16, full, col + 64 * d, r.x);
+        } else {
+            tma2_gather4(dst + d * kBlock, kv1, full, col + 64 * d, r);
+        }
+    }
+}
+// The rows of the four keys from `pos` on.
+__device__ __noinline__ int4 four_rows(const DevBatch &b, uint32_t *status, const Piece *pc, int pos) {
+    return make_int4(row_or_spare(b, status, pc, pos), row_or_spare(b, status, pc, pos + 1), row_or_spare(b, status, pc, pos + 2),
+                     row_or_spare(b, status, pc, pos + 3));
+}
+__device__ __noinline__ int4 four_any_rows(const DevBatch &b, const Piece *pc, int pos) {
+    return make_int4(max(0, any_row(b, pc->seq, pc->kv0, pos)), max(0, any_row(b, pc->seq, pc->kv0, pos + 1)),
+                     max(0, any_row(b, pc->seq, pc->kv0, pos + 2)), max(0, any_row(b, pc->seq, pc->kv0, pos + 3)));
+}
+
 }  // namespace
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -416,7 +465,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctl.k_full[i]), 2);   // both CTAs' producers, and their bytes
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl.k_empty[i]), 1);
-            mbar_init(smem_u32(&ctl.v_full[i]), 2);
             mbar_init(smem_u32(&ctl.o_done[i][0]), 1);
             mbar_init(smem_u32(&ctl.o_done[i][1]), 1);
         }
@@ -428,6 +476,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctl.piece_full[i]), 1);
             mbar_init(smem_u32(&ctl.piece_empty[i]), kSoftmaxWarps + 2 + (rank == 0 ? 2 : 0));
         }
+        for (int i = 0; i < kVBufs; ++i) mbar_init(smem_u32(&ctl.v_full[i]), 2);
+        mbar_init(smem_u32(&ctl.q_tmem), kSoftmaxWarps);                      // a group's in both CTAs
         mbar_init(smem_u32(&ctl.q_full), 2);
         mbar_init(smem_u32(&ctl.q_empty), 1);
         mbar_init(smem_u32(&ctl.p_full[0]), kSoftmaxWarps);
@@ -472,13 +522,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t kv0 = pc->kv0;
             for (int i = t0; alive && i < t1; ++i, ++g) {
                 const int a = tile_pos(*pc, i) + kHalf * (int)rank + mine * step;
-                int4 r;
-                r.x = max(0, any_row(b, seq, kv0, a));
-                if (!p.rows_per_box) {
-                    r.y = max(0, any_row(b, seq, kv0, a + 1));
-                    r.z = max(0, any_row(b, seq, kv0, a + 2));
-                    r.w = max(0, any_row(b, seq, kv0, a + 3));
-                }
+                int4 r = make_int4(0, 0, 0, 0);
+                if (p.rows_per_box) r.x = max(0, any_row(b, seq, kv0, a));
+                else r = four_any_rows(b, pc, a);
                 const uint32_t dst = s0 + kKOff + mine * step * 128;
                 const int row = __reduce_max_sync(0xffffffffu, r.x);        // one box: the same in every lane
 #pragma unroll 1
@@ -487,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint32_t full = k_bar + q * 8;
                     // the last group is free once the tile before is scored
                     if (q < 2) alive = wait_bar(smem_u32(&ctl.k_empty[q]), (g & 1u) ^ 1u, ctl, p.status, limit);
-                    else if (g > 0) alive = wait_bar(smem_u32(&ctl.s_full[(g - 1) & 3u]), ((g - 1) >> 2) & 1u, ctl, p.status, limit);
+                    else if (g > 0) alive = wait_bar(smem_u32(&ctl.s_full[(g - 1) & 1u]), ((g - 1) >> 1) & 1u, ctl, p.status, limit);
                     if (!alive) break;
                     if (q == 2 && i == t0) {
                         // the queries of this CTA's 64 rows.  Rows past the sequence's are some
@@ -498,10 +544,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ++nq;
                         const int q_row = __reduce_max_sync(0xffffffffu, pc->row0) + kHalf * (int)rank;
                         if (!b.skip_copies && elect_one()) {
-                            arrive_expect_remote(q_bar, (uint32_t)(n_blocks * kBlock));
+                            arrive_expect_remote(q_bar, (uint32_t)((n_blocks - kQTmem) * kBlock));
 #pragma unroll 1
-                            for (int c = 0; c < 8; ++c) tma2_load(s0 + kQOff + c * kBlock, &q_lat_map, q_bar, c * 64, q_row);
-                            if (p.tail) tma2_load(s0 + kQOff + 8 * kBlock, &q_rope_map, q_bar, 0, q_row);
+                            for (int c = kQTmem; c < 8; ++c) tma2_load(s0 + kQOff + (c - kQTmem) * kBlock, &q_lat_map, q_bar, c * 64, q_row);
+                            if (p.tail) tma2_load(s0 + kQOff + (8 - kQTmem) * kBlock, &q_rope_map, q_bar, 0, q_row);
                         }
                         __syncwarp();
                     }
@@ -518,14 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     if (lane == 0) arrive_expect_remote(full, (uint32_t)(nb * kBlock));
                     __syncwarp();
-                    // c % copies is lane % copies: copies divides 32
-#pragma unroll 1
-                    for (int c = lane; c < nb * copies; c += 32) {
-                        const int kb = 3 * q + c / copies;
-                        if (p.rows_per_box) tma2_load(dst + kb * kBlock, &kv16_map, full, kb * 64, r.x);
-                        else tma2_gather4(dst + kb * kBlock, &kv1_map, full, kb * 64, r);
-                    }
-                    __syncwarp();
+                    copy_keys(dst, &kv16_map, &kv1_map, full, 3 * q, nb, copies, r, lane);
                 }
             }
             rd.done(ctl, lane);
@@ -535,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // Groups of 16 keys that nobody sees are neither read nor multiplied; in a
         // group that is seen in part the other rows are the spare one's copies
         // (P is 0 there, and 0 times what an unused row may hold is not).
-        uint32_t g = 0;
+        uint32_t g = 0, buf = 0;                              // tiles so far, the next half's place
         bool alive = true;
         const uint32_t v_bar = dsmem_map(smem_u32(&ctl.v_full[0]), 0);
         Reader rd;
@@ -556,10 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         r.x = pc->spare;
                     }
                 } else {
-                    r.x = row_or_spare(b, p.status, pc, a);
-                    r.y = row_or_spare(b, p.status, pc, a + 1);
-                    r.z = row_or_spare(b, p.status, pc, a + 2);
-                    r.w = row_or_spare(b, p.status, pc, a + 3);
+                    r = four_rows(b, p.status, pc, a);
                     // groups whose 16 rows are all seen and lie together
                     const int32_t group_row = __shfl_sync(0xffffffffu, r.x, lane & ~3);
                     const bool run = r.y == r.x + 1 && r.z == r.x + 2 && r.w == r.x + 3 && r.x == group_row + 4 * (lane & 3);
@@ -575,17 +611,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int row1 = __reduce_min_sync(0xffffffffu, lane < 16 ? INT32_MAX : r.x);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    if (g > 0) alive = wait_o(h, g - 1);
+                    const uint32_t n = 2 * g + h;                           // halves so far
+                    if (n >= kVBufs) alive = wait_o((n - kVBufs) & 1u, (n - kVBufs) >> 1);
                     if (!alive) break;
+                    const uint32_t at = s0 + kVOff + buf * kVHalf, full = v_bar + buf * 8;
+                    buf = buf + 1 == kVBufs ? 0 : buf + 1;
                     if (b.skip_copies) continue;
-                    const uint32_t full = v_bar + h * 8;
                     if (boxes) {
                         // the half's four blocks of this CTA's dims
                         if (elect_one()) {
                             arrive_expect_remote(full, kVHalf);
 #pragma unroll
                             for (int d = 0; d < 4; ++d)
-                                tma2_load(s0 + kVOff + h * kVHalf + d * kBlock, &kv64_map, full, 256 * (int)rank + 64 * d, h ? row1 : row0);
+                                tma2_load(at + d * kBlock, &kv64_map, full, 256 * (int)rank + 64 * d, h ? row1 : row0);
                         }
                         __syncwarp();
                         continue;
@@ -593,17 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (lane == 0) arrive_expect_remote(full, (uint32_t)__popc((groups >> (4 * h)) & 0xfu) * (kGroup * 128u) * 4u);
                     __syncwarp();
                     if ((lane >> 4) == h && on) {
-                        const uint32_t dst = s0 + kVOff + h * kVHalf + (lane & 15) * 4 * 128;
-#pragma unroll 1
-                        for (int d = 0; d < 4; ++d) {
-                            const int32_t col = 256 * (int)rank + 64 * d;
-                            if (box16) {
-                                if ((lane & (box64 ? 15 : 3)) == 0)
-                                    tma2_load(dst + d * kBlock, box64 ? &kv64_map : &kv16_map, full, col, r.x);
-                            } else {
-                                tma2_gather4(dst + d * kBlock, &kv1_map, full, col, r);
-                            }
-                        }
+                        const uint32_t dst = at + (lane & 15) * 4 * 128;
+                        copy_values(dst, &kv64_map, &kv16_map, &kv1_map, full, 256 * (int)rank, r, box64 ? 16 : box16 ? 4 : 0, lane);
                     }
                     __syncwarp();
                 }
@@ -623,6 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             while (warp == kOWarp && alive && !sched.end) alive = sched.write(p, ctl, lane);
         } else {
             uint32_t g = 0, n = 0;                            // tiles and pieces so far
+            uint32_t buf = 0, v_parity = 0;                   // the next half of a tile's values
             Reader rd;
             while (alive) {
                 if (warp == kOWarp) alive = sched.write(p, ctl, lane);
@@ -637,28 +667,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     constexpr uint32_t id_s = idesc_f16(kRows, kKeys, true, false, false);
                     const uint64_t qd = sdesc_sw128(s0 + kQOff, 16, 1024), kd = sdesc_sw128(s0 + kKOff, 16, 1024);
                     if (t1 > t0) {
-                        alive = wait_bar(smem_u32(&ctl.q_full), n & 1u, ctl, p.status, limit);
+                        alive = wait_bar(smem_u32(&ctl.q_tmem), n & 1u, ctl, p.status, limit);
+                        if (alive) alive = wait_bar(smem_u32(&ctl.q_full), n & 1u, ctl, p.status, limit);
                         ++n;
                     }
 #pragma unroll 1
                     for (int i = t0; alive && i < t1; ++i, ++g) {
-                        const uint32_t d_s = tmem + kColS + (g & 3u) * (kKeys / 2);
-                        alive = wait_bar(smem_u32(&ctl.s_empty[g & 3u]), ((g >> 2) & 1u) ^ 1u, ctl, p.status, limit);
-#pragma unroll
+                        const uint32_t d_s = tmem + kColS + (g & 1u) * (kKeys / 2);
+                        alive = wait_bar(smem_u32(&ctl.s_empty[g & 1u]), ((g >> 1) & 1u) ^ 1u, ctl, p.status, limit);
+#pragma unroll 1
                         for (int q = 0; q < 3; ++q) {
                             if (alive) alive = wait_bar(smem_u32(&ctl.k_full[q]), g & 1u, ctl, p.status, limit);
                             if (!alive) break;
                             tc_fence_after();
                             if (elect_one()) {
+                                const int kb1 = min(3 * q + 3, n_blocks);
+#pragma unroll 1
+                                for (int kb = 3 * q; kb < kb1; ++kb) {
+                                    const uint64_t kk = kd + (uint64_t)(kb * (kBlock >> 4));
+                                    if (kb < kQTmem) {
 #pragma unroll
-                                for (int kb = 3 * q; kb < 3 * q + 3; ++kb) {
-                                    if (kb == 8 && !p.tail) continue;
+                                        for (int ks = 0; ks < 4; ++ks)
+                                            umma2_f16_ts(d_s, tmem + kColQ + kb * 32 + ks * 8, kk + 2 * ks, id_s, (kb | ks) != 0);
+                                    } else {
+                                        const uint64_t qq = qd + (uint64_t)((kb - kQTmem) * (kBlock >> 4));
 #pragma unroll
-                                    for (int ks = 0; ks < 4; ++ks)
-                                        umma2_f16(d_s, qd + (uint64_t)(kb * (kBlock >> 4) + 2 * ks),
-                                                  kd + (uint64_t)(kb * (kBlock >> 4) + 2 * ks), id_s, (kb | ks) != 0);
+                                        for (int ks = 0; ks < 4; ++ks) umma2_f16(d_s, qq + 2 * ks, kk + 2 * ks, id_s, 1u);
+                                    }
                                 }
-                                commit2(q < 2 ? smem_u32(&ctl.k_empty[q]) : smem_u32(&ctl.s_full[g & 3u]));
+                                commit2(q < 2 ? smem_u32(&ctl.k_empty[q]) : smem_u32(&ctl.s_full[g & 1u]));
                                 if (q == 2 && i == t1 - 1) commit2(smem_u32(&ctl.q_empty));
                             }
                             __syncwarp();
@@ -670,27 +707,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int i = t0; alive && i < t1; ++i, ++g) {
                         const uint32_t groups = __reduce_or_sync(0xffffffffu, tile_groups(*pc, tile_pos(*pc, i)));
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
-                            if (alive) alive = wait_bar(smem_u32(&ctl.v_full[h]), g & 1u, ctl, p.status, limit);
+                            alive = wait_bar(smem_u32(&ctl.v_full[buf]), v_parity, ctl, p.status, limit);
                             if (alive) alive = wait_bar(smem_u32(&ctl.p_full[h]), g & 1u, ctl, p.status, limit);
                             if (!alive) break;
                             tc_fence_after();
+                            const uint64_t vb = vd + (uint64_t)(buf * (kVHalf >> 4)), pb = pd + (uint64_t)(h * (kBlock >> 4));
+                            const uint32_t on = groups >> (4 * h);
+                            const bool begun = i > t0 || (h && (groups & 0xfu));
                             if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
                                 for (int j = 0; j < 2; ++j) {
+                                    const uint64_t vj = vb + (uint64_t)((j * 2 * kBlock) >> 4);
 #pragma unroll
-                                    for (int ks = 0; ks < 4; ++ks) {
-                                        const int k = 4 * h + ks;
-                                        if (groups >> k & 1u)
-                                            umma2_f16(tmem + kColO + j * 128, pd + (uint64_t)(h * (kBlock >> 4) + 2 * ks),
-                                                      vd + (uint64_t)((h * kVHalf + j * 2 * kBlock + ks * kGroup * 128) >> 4), id_o,
-                                                      i > t0 || (groups & ((1u << k) - 1)) != 0);
-                                    }
+                                    for (int ks = 0; ks < 4; ++ks)
+                                        if (on >> ks & 1u)
+                                            umma2_f16(tmem + kColO + j * 128, pb + 2 * ks, vj + (uint64_t)(ks * kGroup * 128 >> 4), id_o,
+                                                      begun || (on & ((1u << ks) - 1)) != 0);
                                 }
                                 commit2(smem_u32(&ctl.o_done[g & 1u][h]));
                             }
                             __syncwarp();
+                            if (++buf == kVBufs) {
+                                buf = 0;
+                                v_parity ^= 1u;
+                            }
                         }
                     }
                 }
@@ -724,6 +766,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // memory after a bounded wait gave up.
         bool alive = true;
         Reader rd;
+        // The first 256 dims of the queries of piece n, by one group: row r into lanes r
+        // and r + 64.  The products that read the piece before's are done.
+        const uint32_t q_bar = dsmem_map(smem_u32(&ctl.q_tmem), 0);
+        auto load_queries = [&](uint32_t n) {
+            if (!wait_bar(smem_u32(&ctl.piece_full[n % kPieces]), (n / kPieces) & 1u, ctl, p.status, limit)) return;
+            const Piece *pc = &ctl.piece[n % kPieces];
+            if (pc->end || pc->t0 == pc->t1) return;
+            const int64_t row = (int64_t)pc->row0 + kHalf * (int)rank + r;
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * D_L);
+            const bool there = row < (int64_t)b.T * p.pr.H;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kQTmem; ++c) {
+                uint32_t u[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint4 x = there ? __ldg(src + 8 * c + e) : make_uint4(0, 0, 0, 0);
+                    u[4 * e] = x.x;
+                    u[4 * e + 1] = x.y;
+                    u[4 * e + 2] = x.z;
+                    u[4 * e + 3] = x.w;
+                }
+                tmem_st32(lane_tmem + kColQ + 32 * c, u);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_remote(q_bar);
+        };
+        if (group == 1) load_queries(0);
         while (true) {
             const Piece *pc = rd.next(ctl, p.status, limit);
             // (all of them: their staging of the last output ends before any stores a P)
@@ -747,9 +819,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;                     // m: as of this group's last tile
             for (int i = t0; i < t1; ++i, ++g) {
                 if ((int)(g & 1u) != group) continue;
-                if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 3u]), (g >> 2) & 1u, ctl, p.status, limit);
+                if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 1u]), (g >> 1) & 1u, ctl, p.status, limit);
                 tc_fence_after();
-                const uint32_t s_tmem = lane_tmem + kColS + (g & 3u) * (kKeys / 2);
+                const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2);
                 if ((i < max(clear0, n_first) || i >= clear1) && alive) {
                     const int kp = tile_pos(*pc, i) + kHalf * half;
                     const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);   // first of the window
@@ -869,12 +941,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) {
                         arrive_remote(half ? p_bar1 : p_bar0);
-                        arrive_remote(s_bar + (g & 3u) * 8);  // the next S but three may come
+                        arrive_remote(s_bar + (g & 1u) * 8);  // the next S but one may come
                     }
                 }
             }
-            // ---- the piece's output
+            // ---- the next piece's queries, by the group that is done first, once the
+            // last tile is scored
             const bool empty = t1 == t0;
+            if (empty ? group == 0 : (int)((g - 1) & 1u) != group) {
+                if (alive && !empty) alive = wait_bar(smem_u32(&ctl.s_full[(g - 1) & 1u]), ((g - 1) >> 1) & 1u, ctl, p.status, limit);
+                if (alive) load_queries(rd.n + 1);
+            }
+            // ---- the piece's output
             if (!empty) {
                 if (alive) alive = wait_o(1, g - 1);
                 tc_fence_after();
@@ -1174,6 +1252,7 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     MlaParams p;
     p.pr = Problem{b, a.H, a.window, a.n_sink, a.sink_pos0};
     p.status = status;
+    p.q_lat = a.q_lat;
     PlanHead *head = reinterpret_cast<PlanHead *>(w + L.head);
     PlanItem *items = reinterpret_cast<PlanItem *>(w + L.items);
     Start *start = reinterpret_cast<Start *>(w + L.start);
