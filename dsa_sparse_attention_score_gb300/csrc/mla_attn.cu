@@ -254,6 +254,13 @@ struct MlaParams {
     int rows_per_box;             // 64, 16 or 0: rows that lie together for certain (pages)
 };
 
+// Bits [lo, hi) of 64.
+__device__ __forceinline__ uint64_t key_bits(int lo, int hi) {
+    lo = max(lo, 0);
+    hi = min(hi, 64);
+    return lo < hi ? (~0ull >> (64 - (hi - lo))) << lo : 0ull;
+}
+
 // Token position if the token is in order, else -1 (flagged unless it is padding).
 __device__ __forceinline__ int token_pos(const DevBatch &b, int t, uint32_t *status) {
     const int p = __ldg(b.q_pos + t);
@@ -401,6 +408,11 @@ __device__ __noinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int 
         if (lane == 0) {
             ctl.piece[n % kPieces] = pc;
             mbar_arrive(smem_u32(&ctl.piece_full[n % kPieces]));
+            if (pc.t1 > pc.t0) {
+                // this CTA's query rows, wanted when the piece before is scored
+                const int64_t row = (int64_t)pc.row0 + kHalf * (int)cluster_rank(), rows = (int64_t)p.pr.b.T * p.pr.H - row;
+                if (rows > 0) prefetch_l2_bulk(p.q_lat + row * D_L, (uint32_t)min(rows, (int64_t)kHalf) * (D_L * 2));
+            }
         }
         __syncwarp();
         ++n;
@@ -576,18 +588,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (P is 0 there, and 0 times what an unused row may hold is not).
         uint32_t g = 0, buf = 0;                              // tiles so far, the next half's place
         bool alive = true;
+        const bool quads = !b.block_table || b.block_size % 4 == 0;
         const uint32_t v_bar = dsmem_map(smem_u32(&ctl.v_full[0]), 0);
         Reader rd;
         while (alive) {
             const Piece *pc = rd.next(ctl, p.status, limit);
             if (!pc || pc->end) break;
-            const int t1 = pc->t1;
+            const int t1 = pc->t1, lo = pc->lo, hi = pc->hi, s_lo = pc->s_lo, s_hi = pc->s_hi;
             for (int i = pc->t0; alive && i < t1; ++i, ++g) {
                 const int pos = tile_pos(*pc, i), a = pos + 4 * lane;       // this lane's four keys
                 const uint32_t groups = tile_groups(*pc, pos);
                 int4 r;
                 bool box16 = true, box64 = true;
-                const bool simple = p.rows_per_box == 64 && pos >= pc->lo && pos + kKeys - 1 <= pc->hi;   // all seen
+                const bool simple = p.rows_per_box == 64 && pos >= lo && pos + kKeys - 1 <= hi;   // all seen
                 if (simple) {
                     r.x = any_row(b, pc->seq, pc->kv0, pos + ((lane & 16) << 2));
                     if (r.x < 0) {
@@ -595,7 +608,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         r.x = pc->spare;
                     }
                 } else {
-                    r = four_rows(b, p.status, pc, a);
+                    if (quads) {
+                        // the four lie together: one lookup
+                        const int spare = pc->spare;
+                        auto seen = [&](int q) { return (q >= lo && q <= hi) || (q >= s_lo && q < s_hi); };
+                        const bool s0_ = seen(a), s1_ = seen(a + 1), s2_ = seen(a + 2), s3_ = seen(a + 3);
+                        int row = 0;
+                        if (s0_ || s1_ || s2_ || s3_) row = any_row(b, pc->seq, pc->kv0, a);
+                        if (row < 0) flag(p.status, DSA_DEV_BAD_INDEX);
+                        r.x = s0_ && row >= 0 ? row : spare;
+                        r.y = s1_ && row >= 0 ? row + 1 : spare;
+                        r.z = s2_ && row >= 0 ? row + 2 : spare;
+                        r.w = s3_ && row >= 0 ? row + 3 : spare;
+                    } else {
+                        r = four_rows(b, p.status, pc, a);
+                    }
                     // groups whose 16 rows are all seen and lie together
                     const int32_t group_row = __shfl_sync(0xffffffffu, r.x, lane & ~3);
                     const bool run = r.y == r.x + 1 && r.z == r.x + 2 && r.w == r.x + 3 && r.x == group_row + 4 * (lane & 3);
@@ -778,24 +805,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool there = row < (int64_t)b.T * p.pr.H;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kQTmem; ++c) {
-                uint32_t u[32];
+            for (int c = 0; c < kQTmem; c += 2) {
+                uint32_t u[32], v[32];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint4 x = there ? __ldg(src + 8 * c + e) : make_uint4(0, 0, 0, 0);
-                    u[4 * e] = x.x;
-                    u[4 * e + 1] = x.y;
-                    u[4 * e + 2] = x.z;
-                    u[4 * e + 3] = x.w;
+                    const uint4 y = there ? __ldg(src + 8 * c + 8 + e) : make_uint4(0, 0, 0, 0);
+                    u[4 * e] = x.x, u[4 * e + 1] = x.y, u[4 * e + 2] = x.z, u[4 * e + 3] = x.w;
+                    v[4 * e] = y.x, v[4 * e + 1] = y.y, v[4 * e + 2] = y.z, v[4 * e + 3] = y.w;
                 }
                 tmem_st32(lane_tmem + kColQ + 32 * c, u);
+                tmem_st32(lane_tmem + kColQ + 32 * c + 32, v);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_remote(q_bar);
         };
+        // The position of this thread's row in piece n, -1 without one.
+        auto row_pos = [&](const Piece *pc) {
+            const int row = kHalf * (int)rank + r;
+            if (row >= pc->nrows) return -1;
+            const int pos = token_pos(b, (pc->row0 + row) / p.pr.H, p.status);
+            if (pos >= 0 && (pc->kv0 < 0 || any_row(b, pc->seq, pc->kv0, pos) < 0)) {
+                flag(p.status, DSA_DEV_BAD_POSITION);
+                return -1;
+            }
+            return pos;
+        };
         if (group == 1) load_queries(0);
+        int pos = -1, next_pos = -1;
+        bool known = false;                                   // next_pos is the next piece's
         while (true) {
             const Piece *pc = rd.next(ctl, p.status, limit);
             // (all of them: their staging of the last output ends before any stores a P)
@@ -804,14 +844,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int t0 = pc->t0, t1 = pc->t1, n_first = pc->n_first;
             const int row = kHalf * (int)rank + r;
             const bool mine = row < pc->nrows;
-            int pos = -1;
-            if (mine) {
-                pos = token_pos(b, (pc->row0 + row) / p.pr.H, p.status);
-                if (pos >= 0 && (pc->kv0 < 0 || any_row(b, pc->seq, pc->kv0, pos) < 0)) {
-                    flag(p.status, DSA_DEV_BAD_POSITION);
-                    pos = -1;
-                }
-            }
+            pos = known ? next_pos : row_pos(pc);
             // Every row of the item sees every key of the tiles [clear0, clear1).
             const int64_t open = (int64_t)pc->hi - p.pr.window + 1;      // the last token's window begins here
             const int clear0 = n_first + (open <= 0 ? 0 : (int)((open + kKeys - 1) / kKeys)) - pc->tile0;
@@ -823,20 +856,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2);
                 if ((i < max(clear0, n_first) || i >= clear1) && alive) {
+                    // one bit a key of this half: the window's and the first ones'
                     const int kp = tile_pos(*pc, i) + kHalf * half;
-                    const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);   // first of the window
-                    const int s_lo = pc->s_lo, s_hi = min(pc->s_hi, pos + 1);
+                    const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);
+                    const uint64_t see = key_bits(from - kp, pos + 1 - kp) | key_bits(pc->s_lo - kp, min(pc->s_hi, pos + 1) - kp);
+                    const float factor = plain ? 1.f : p.scale_log2;
 #pragma unroll 1
                     for (int c = 0; c < 64; c += 16) {
+                        const uint32_t bits = (uint32_t)(see >> c);
                         uint32_t u[16];
                         tmem_ld16(s_tmem + c, u);
                         tmem_wait_ld(u);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int k = kp + c + e;
-                            const float x = __uint_as_float(u[e]) * (plain ? 1.f : p.scale_log2);
-                            u[e] = __float_as_uint((k >= from && k <= pos) || (k >= s_lo && k < s_hi) ? x : -INFINITY);
-                        }
+                        for (int e = 0; e < 16; ++e) u[e] = bits & (1u << e) ? __float_as_uint(__uint_as_float(u[e]) * factor) : 0xff800000u;
                         tmem_st16(s_tmem + c, u);
                     }
                     tmem_wait_st();
@@ -952,6 +984,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (alive && !empty) alive = wait_bar(smem_u32(&ctl.s_full[(g - 1) & 1u]), ((g - 1) >> 1) & 1u, ctl, p.status, limit);
                 if (alive) load_queries(rd.n + 1);
             }
+            // its positions, asked for before they are wanted
+            known = mbar_test(smem_u32(&ctl.piece_full[(rd.n + 1) % kPieces]), ((rd.n + 1) / kPieces) & 1u);
+            if (known) {
+                const Piece *nx = &ctl.piece[(rd.n + 1) % kPieces];
+                next_pos = nx->end ? -1 : row_pos(nx);
+            }
             // ---- the piece's output
             if (!empty) {
                 if (alive) alive = wait_o(1, g - 1);
@@ -974,50 +1012,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool whole = pc->whole, narrow = whole && p.out_bf16;
                 const int64_t out_row = (int64_t)pc->row0 + row;
                 const int64_t part_row = ((int64_t)2 * cluster + (t0 == 0 ? 1 : 0)) * kRows + row;
-                const float factor = none ? 0.f : whole ? 1.f / l : 1.f;
+                const float factor = whole ? 1.f / l : 1.f;
                 const int col0 = 256 * half + 128 * group, bytes = narrow ? 2 : 4;
                 const int rows_left = pc->nrows - (row - lane);            // of the warp's 32
                 uint8_t *stage = smem + kPOff + warp * 2048;
                 uint8_t *dst = (whole ? static_cast<uint8_t *>(p.out) + (out_row - lane) * D_L * bytes
-                                      : reinterpret_cast<uint8_t *>(p.part_o + (part_row - lane) * D_L)) + col0 * bytes;
+                                      : reinterpret_cast<uint8_t *>(p.part_o + (part_row - lane) * D_L)) +
+                               col0 * bytes + (int64_t)(lane >> 2) * D_L * bytes + 16 * (lane & 3);
+                const uint32_t o_tmem = lane_tmem + kColO + 128 * group;
                 const int step = 64 / bytes;
 #pragma unroll 1
                 for (int c = 0; c < 128; c += step) {
-                    uint32_t o[32];
-                    const uint32_t at = lane_tmem + kColO + 128 * group + c;
-                    if (empty) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
-                    } else if (narrow) {
-                        tmem_ld32(at, o);
+                    uint32_t w[16];
+                    if (narrow && !empty) {
+                        uint32_t o[32];
+                        tmem_ld32(o_tmem + c, o);
                         tmem_wait_ld(o);
-                    } else {
-                        uint32_t v[16];
-                        tmem_ld16(at, v);
-                        tmem_wait_ld(v);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = v[e];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * factor);
-                    if (narrow) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-                            o[e] = *reinterpret_cast<const uint32_t *>(&h);
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * factor, __uint_as_float(o[2 * e + 1]) * factor);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&h);
                         }
+                    } else if (!empty) {
+                        tmem_ld16(o_tmem + c, w);
+                        tmem_wait_ld(w);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * factor);
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         *reinterpret_cast<uint4 *>(stage + sw64_offset((uint32_t)lane, (uint32_t)q)) =
-                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                            none ? make_uint4(0, 0, 0, 0) : make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
                     __syncwarp();
+                    uint4 v[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int rr = 8 * q + (lane >> 2);
-                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + sw64_offset((uint32_t)rr, (uint32_t)(lane & 3)));
-                        if (rr < rows_left) *reinterpret_cast<uint4 *>(dst + (int64_t)rr * D_L * bytes + c * bytes + 16 * (lane & 3)) = v;
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        v[q] = *reinterpret_cast<const uint4 *>(stage + sw64_offset((uint32_t)(8 * q + (lane >> 2)), (uint32_t)(lane & 3)));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (8 * q + (lane >> 2) < rows_left) *reinterpret_cast<uint4 *>(dst + (int64_t)(8 * q) * D_L * bytes + c * bytes) = v[q];
                     __syncwarp();
                 }
                 if (mine && half == 0 && group == 0) {
