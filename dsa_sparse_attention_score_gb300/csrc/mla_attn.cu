@@ -56,7 +56,7 @@ constexpr int kThreads = 384;
 constexpr int kSBufs = 2, kVBufs = 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kRescaleLog2 = 20.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kItemCost = 1;                  // what an item costs beside its tiles, in tiles
 
@@ -151,11 +151,6 @@ __device__ __forceinline__ void arrive_expect_remote(uint32_t bar, uint32_t byte
 
 __device__ __forceinline__ void named_barrier_arrive(int id, int nthreads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -898,8 +893,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     named_barrier(5 + (group ^ 1), kSoftmaxWarps * 32);
                     mo = ctl.m[(g - 1) & 1u][r];
                 }
-                // The maximum is only raised by more than 2^8 at a time (the result
-                // is the same either way): O is rescaled seldom.
+                // The maximum is only raised by more than 2^20 at a time: the result is
+                // the same either way, P's and O's exponents have room, and O is
+                // rescaled seldom (with 2^8, rows whose first tile shows them a few keys
+                // made every other tile of a windowed prefill wait for it).
                 const bool raise = mx > mo + kRescaleLog2 || (mo == -INFINITY && mx != -INFINITY);
                 const float mn = raise ? mx : mo;
                 if (i + 1 < t1) {
@@ -915,19 +912,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // P in pairs of bf16 over the first half of S's own columns, until
                     // its place in shared memory is free
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t u[16], w[8];
-                        tmem_ld16(s_tmem + 16 * c, u);
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t u[32], w[16];
+                        tmem_ld32(s_tmem + 32 * c, u);
                         tmem_wait_ld(u);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const float x = ex2(fmaf(__uint_as_float(u[2 * e]), scale, mm));
                             const float y = ex2(fmaf(__uint_as_float(u[2 * e + 1]), scale, mm));
                             sum = f2_add(sum, f2(x, y));
                             const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
                             w[e] = *reinterpret_cast<const uint32_t *>(&h);
                         }
-                        tmem_st8(s_tmem + 8 * c, w);
+                        tmem_st16(s_tmem + 16 * c, w);
                     }
                     tmem_wait_st();
                 }
@@ -939,13 +936,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (alive) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 256; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(lane_tmem + kColO + c, o);
+                        for (int c = 0; c < 256; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_tmem + kColO + c, o);
                             tmem_wait_ld(o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                            tmem_st16(lane_tmem + kColO + c, o);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                            tmem_st32(lane_tmem + kColO + c, o);
                         }
                         tmem_wait_st();
                     }
