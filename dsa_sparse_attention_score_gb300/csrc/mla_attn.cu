@@ -38,6 +38,7 @@ namespace dsa {
 
 namespace {
 
+constexpr int kClusters = kSMs / 2;           // pairs of CTAs in the grid
 constexpr int kRows = 128;                    // query rows of an item
 constexpr int kHalf = 64;                     // rows and keys of one CTA
 constexpr int kKeys = 128;                    // positions of a tile
@@ -59,36 +60,6 @@ constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
 constexpr float kRescaleLog2 = 20.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kItemCost = 1;                  // what an item costs beside its tiles, in tiles
-
-// A piece of an item, for every warp of the CTA (Ctl::piece).
-struct Piece {
-    int32_t t0, t1;               // tiles of the item to do; t0 == t1: an item that sees nothing
-    int32_t n_first, first_tile, tile0;
-    int32_t lo, hi, s_lo, s_hi, min_pos;   // as in Item
-    int32_t row0, nrows, seq;
-    int32_t whole;                // all tiles of the item
-    int32_t rest;                 // tiles of the item behind t1
-    int32_t end;                  // no piece: there are no more
-    int32_t spare;                // a cache row that may be read for positions that no row sees
-    int64_t kv0;
-};
-constexpr int kPieces = 3;        // read ahead
-
-struct Ctl {
-    uint64_t k_full[3], k_empty[2];
-    uint64_t v_full[kVBufs];
-    uint64_t o_done[2][2];        // by tile and half of the keys: a group of softmax warps waits for every other tile
-    uint64_t q_full, q_empty, q_tmem;
-    uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[2];
-    uint64_t piece_full[kPieces], piece_empty[kPieces];
-    uint32_t tmem_base;
-    int32_t abort_flag;
-    float red[2][2][2][kHalf];    // a group's maxima by tile and half of the keys
-    float m[2][kHalf];            // running maxima by tile
-    Piece piece[kPieces];
-};
-constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
-static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 // ---------------------------------------------------------------- pairs of CTAs
 __device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t n) {
@@ -170,13 +141,17 @@ struct Problem {
 };
 
 // Up to 128 query rows of one sequence and the positions some of them see:
-// [lo, hi] and the first ones [s_lo, s_hi), as tiles of the grid of 128.
-struct Item {
-    int seq, row0, nrows;         // flat rows (token * H + head)
-    int lo, hi, s_lo, s_hi;       // hi < 0: nothing
-    int min_pos;                  // the least position of its tokens (those that see anything)
-    int first_tile, n_first;      // tiles of the first positions before those of [lo, hi]
-    int tile0, n;                 // first tile of [lo, hi]; all tiles
+// [lo, hi] and the first ones [s_lo, s_hi), as tiles of the grid of 128.  The plan
+// writes them into the workspace.
+struct __align__(16) Item {
+    int32_t seq, row0, nrows;         // flat rows (token * H + head)
+    int32_t cost0;                    // costs of the items before
+    int32_t lo, hi, s_lo, s_hi;       // hi < 0: nothing
+    int32_t min_pos;                  // the least position of its tokens (those that see anything)
+    int32_t first_tile, n_first;      // tiles of the first positions before those of [lo, hi]
+    int32_t tile0, n;                 // first tile of [lo, hi]; all tiles
+    int32_t spare;                    // a cache row that may be read for positions that no row sees
+    int64_t kv0;
 };
 
 __device__ __forceinline__ int item_cost(int n) { return n + kItemCost; }
@@ -203,6 +178,48 @@ __device__ __forceinline__ void item_tiles(const Problem &p, Item &it) {
         }
     }
 }
+// The plan of a call, in the workspace.
+struct PlanHead {
+    int32_t total;                // costs of all items
+    int32_t clusters;             // clusters with work: every one has some
+};
+struct Start { int32_t item, off; };                 // a cluster's first item and the costs of it done before
+struct Split { int32_t row0, nrows, first, parts; }; // an item that begins in a cluster and ends in a later one
+
+// A piece of an item, for every warp of the CTA (Ctl::piece).
+struct Piece {
+    int32_t t0, t1;               // tiles of the item to do; t0 == t1: an item that sees nothing
+    int32_t n_first, first_tile, tile0;
+    int32_t lo, hi, s_lo, s_hi, min_pos;   // as in Item
+    int32_t row0, nrows, seq;
+    int32_t whole;                // all tiles of the item
+    int32_t rest;                 // tiles of the item behind t1
+    int32_t end;                  // no piece: there are no more
+    int32_t spare;                // a cache row that may be read for positions that no row sees
+    int64_t kv0;
+};
+constexpr int kPieces = 3;        // read ahead
+
+struct Ctl {
+    uint64_t k_full[3], k_empty[2];
+    uint64_t v_full[kVBufs];
+    uint64_t o_done[2][2];        // by tile and half of the keys: a group of softmax warps waits for every other tile
+    uint64_t q_full, q_empty, q_tmem;
+    uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[2];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    float red[2][2][2][kHalf];    // a group's maxima by tile and half of the keys
+    alignas(16) float m[2][kHalf];   // running maxima by tile
+    // The first item of a plan made here, read before the first maximum is written.
+    __device__ __forceinline__ Item &first() { return *reinterpret_cast<Item *>(&m[0][0]); }
+    PlanHead head;                // the plan, and where this cluster begins
+    Start start;
+    Piece piece[kPieces];
+};
+constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+
 // Position of tile i's first key.
 __device__ __forceinline__ int tile_pos(const Piece &it, int i) {
     return (i < it.n_first ? it.first_tile + i : it.tile0 + i - it.n_first) * kKeys;
@@ -222,24 +239,15 @@ __device__ __forceinline__ uint32_t tile_groups(const Piece &it, int p0) {
     return m;
 }
 
-// The plan of a call, in the workspace.
-struct PlanHead {
-    int32_t total;                // costs of all items
-    int32_t clusters;             // clusters with work: every one has some
-};
-struct PlanItem { int32_t seq, row, cost0, pad; };   // row within the sequence; costs before it
-struct Start { int32_t item, off; };                 // a cluster's first item and the costs of it done before
-struct Split { int32_t row0, nrows, first, parts; }; // an item that begins in a cluster and ends in a later one
-
 struct MlaParams {
     Problem pr;
     uint32_t *status;
     const PlanHead *head;
-    const PlanItem *items;
+    const Item *items;
     const Start *start;
     const uint16_t *q_lat;        // bf16 [T * H, 512]
     Split *split;                 // [clusters]
-    float *part_o;                // [2 * clusters, 128, 512]
+    void *part_o;                 // [2 * clusters, 128, 512] of the output's type, unnormalised
     float *part_ml;               // [2 * clusters, 128, 2]
     void *out;
     int out_bf16;
@@ -263,30 +271,6 @@ __device__ __forceinline__ int token_pos(const DevBatch &b, int t, uint32_t *sta
     if (p != -1) flag(status, DSA_DEV_BAD_POSITION);
     return -1;
 }
-// Loads an item with a whole warp.
-__device__ __forceinline__ Item load_item(const MlaParams &p, int index, int lane) {
-    const DevBatch &b = p.pr.b;
-    Item it;
-    const PlanItem pi = p.items[index];
-    it.seq = pi.seq;
-    const int t0 = __ldg(b.cu_q + pi.seq), t1 = __ldg(b.cu_q + pi.seq + 1);
-    it.row0 = t0 * p.pr.H + pi.row;
-    it.nrows = min(kRows, t1 * p.pr.H - it.row0);
-    const int ta = it.row0 / p.pr.H, tb = (it.row0 + it.nrows - 1) / p.pr.H;
-    int lo = INT32_MAX, hi = -1;
-    for (int t = ta + lane; t <= tb; t += 32) {
-        const int pos = __ldg(b.q_pos + t);
-        if (pos >= 0 && pos < b.max_kv) {
-            lo = min(lo, pos);
-            hi = max(hi, pos);
-        }
-    }
-    it.min_pos = __reduce_min_sync(0xffffffffu, lo);
-    it.hi = __reduce_max_sync(0xffffffffu, hi);
-    item_tiles(p.pr, it);
-    return it;
-}
-
 // Bounded wait of a whole warp; the same answer in every lane.  (Reading the
 // clock takes long: only every few tries, each of which waits for a while.)
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int32_t *abort_flag, uint32_t *status, uint64_t limit_ns) {
@@ -325,23 +309,6 @@ struct Reader {
     }
 };
 
-// Writes the cluster's pieces into the ring, one a call, with a whole warp.
-struct Scheduler {
-    int item = 0, off = 0, left = 0;   // next item, costs of it done, costs left to this cluster
-    uint32_t n = 0;
-    bool end = false;
-    __device__ __forceinline__ Scheduler(const MlaParams &p, int cluster) {
-        const int64_t total = p.head->total;
-        const int n_cl = p.head->clusters;
-        if (cluster >= n_cl) return;
-        const Start st = p.start[cluster];
-        item = st.item;
-        off = st.off;
-        left = (int)(total * (cluster + 1) / n_cl - total * cluster / n_cl);
-    }
-    __device__ __noinline__ bool write(const MlaParams &p, Ctl &ctl, int lane);
-};
-
 // Cache row of a position, whoever sees it: negative where there is none.
 __device__ __forceinline__ int32_t any_row(const DevBatch &b, int seq, int64_t kv0, int pos) {
     int64_t r = kv0 + pos;
@@ -352,6 +319,54 @@ __device__ __forceinline__ int32_t any_row(const DevBatch &b, int seq, int64_t k
     }
     return r >= 0 && r < b.cache_rows ? (int32_t)r : -1;
 }
+// The rest of an item whose sequence and rows are set.
+__device__ __forceinline__ void item_fill(const Problem &p, Item &it) {
+    const DevBatch &b = p.b;
+    it.kv0 = seq_base(b, it.seq);
+    it.min_pos = INT32_MAX;
+    it.hi = -1;
+    for (int t = it.row0 / p.H; t <= (it.row0 + it.nrows - 1) / p.H; ++t) {
+        const int pos = __ldg(b.q_pos + t);
+        if (pos >= 0 && pos < b.max_kv) {
+            it.min_pos = min(it.min_pos, pos);
+            it.hi = max(it.hi, pos);
+        }
+    }
+    // the row of the last position; row 0 if that has none (no row sees anything then)
+    it.spare = it.hi < 0 || it.kv0 < 0 ? 0 : max(0, any_row(b, it.seq, it.kv0, it.hi));
+    item_tiles(p, it);
+}
+// The item of a sequence that has at most one (false: it has no rows).
+__device__ __forceinline__ bool item_of(const Problem &p, int seq, uint32_t *status, Item &it) {
+    const DevBatch &b = p.b;
+    const int t0 = __ldg(b.cu_q + seq), t1 = __ldg(b.cu_q + seq + 1);
+    if (t0 < 0 || t1 < t0 || t1 > b.T || (t1 - t0) * p.H > kRows) {
+        flag(status, DSA_DEV_BAD_POSITION);
+        return false;
+    }
+    if (t1 == t0) return false;
+    it.seq = seq;
+    it.row0 = t0 * p.H;
+    it.nrows = (t1 - t0) * p.H;
+    item_fill(p, it);
+    return true;
+}
+
+// Writes the cluster's pieces into the ring, one a call, with a whole warp.
+struct Scheduler {
+    int item = 0, off = 0, left = 0;   // next item, costs of it done, costs left to this cluster
+    uint32_t n = 0;
+    bool end = false, begun = false;
+    __device__ __forceinline__ Scheduler(const PlanHead &head, Start st, int cluster) {
+        const int64_t total = head.total;
+        if (cluster >= head.clusters) return;
+        item = st.item;
+        off = st.off;
+        left = (int)(total * (cluster + 1) / head.clusters - total * cluster / head.clusters);
+    }
+    __device__ __noinline__ bool write(const MlaParams &p, Ctl &ctl, int lane);
+};
+
 // That of a position that some row of the piece sees, its spare one for any other.
 __device__ __noinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status, const Piece *pc, int pos) {
     if (!seen_by_some(*pc, pos)) return pc->spare;
@@ -367,7 +382,16 @@ __device__ __noinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int 
         Piece pc{};
         pc.end = end;
         if (!end) {
-            const Item it = load_item(p, item, lane);
+            Item it;
+            if (p.items) {
+                it = p.items[item];
+            } else if (!begun) {
+                it = ctl.first();
+                begun = true;
+            } else if (!item_of(p.pr, item, p.status, it)) {  // no rows: no costs
+                ++item;
+                continue;
+            }
             const int cost = item_cost(it.n), take = min(left, cost - off);
             pc.t0 = min(off, it.n);
             pc.t1 = min(off + take, it.n);
@@ -392,9 +416,8 @@ __device__ __noinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int 
             pc.seq = it.seq;
             pc.whole = pc.t0 == 0 && pc.t1 == it.n;
             pc.rest = it.n - pc.t1;
-            pc.kv0 = seq_base(p.pr.b, it.seq);
-            // the row of the last position; row 0 if that has none (no row sees anything then)
-            pc.spare = it.hi < 0 || pc.kv0 < 0 ? 0 : max(0, any_row(p.pr.b, it.seq, pc.kv0, it.hi));
+            pc.kv0 = it.kv0;
+            pc.spare = it.spare;
         }
         if (!wait_bar(smem_u32(&ctl.piece_empty[n % kPieces]), ((n / kPieces) & 1u) ^ 1u, ctl, p.status, p.pr.b.wait_ns)) {
             end = true;
@@ -448,6 +471,54 @@ __device__ __noinline__ int4 four_rows(const DevBatch &b, uint32_t *status, cons
 __device__ __noinline__ int4 four_any_rows(const DevBatch &b, const Piece *pc, int pos) {
     return make_int4(max(0, any_row(b, pc->seq, pc->kv0, pos)), max(0, any_row(b, pc->seq, pc->kv0, pos + 1)),
                      max(0, any_row(b, pc->seq, pc->kv0, pos + 2)), max(0, any_row(b, pc->seq, pc->kv0, pos + 3)));
+}
+
+// Exclusive prefix over a CTA of N threads, and the sum; sh: 64 words.
+template <int N>
+__device__ __forceinline__ int plan_scan(int v, int &sum, int *sh) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int y = lane < N / 32 ? sh[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += z;
+        }
+        sh[32 + lane] = y;
+    }
+    __syncthreads();
+    sum = sh[63];
+    const int before = (warp ? sh[32 + warp - 1] : 0) + x - v;
+    __syncthreads();
+    return before;
+}
+
+// The plan of a call with at most one item a sequence and no more sequences than
+// threads, made by every CTA for itself (a launch less: 4 us).
+__device__ __noinline__ void plan_here(const MlaParams &p, Ctl &ctl, int cluster) {
+    const int seq = (int)threadIdx.x;
+    Item it{};
+    int cost = 0;
+    if (seq < p.pr.b.B && item_of(p.pr, seq, p.status, it)) cost = item_cost(it.n);
+    int total;
+    const int before = plan_scan<kThreads>(cost, total, reinterpret_cast<int *>(&ctl.red[0][0][0][0]));
+    const int n = min((int)gridDim.x / 2, total);
+    if (seq == 0) ctl.head = PlanHead{total, n};
+    if (cluster < n) {
+        const int at = (int)((int64_t)total * cluster / n);
+        if (at >= before && at < before + cost) {
+            ctl.start = Start{seq, at - before};
+            ctl.first() = it;
+        }
+    }
 }
 
 }  // namespace
@@ -504,6 +575,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
     pdl_wait();
+    if (p.items) {
+        if (threadIdx.x == 0) {
+            ctl.head = *p.head;
+            ctl.start = p.start[cluster];                     // (written for clusters with work)
+        }
+    } else {
+        plan_here(p, ctl, cluster);
+    }
+    __syncthreads();
     const uint64_t limit = b.wait_ns;
     const int n_blocks = p.tail ? 9 : 8;
     // waits for the value product of half h of tile t's keys
@@ -575,6 +655,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             rd.done(ctl, lane);
+        }
+        // the last arrivals at this CTA's barriers, before it ends
+        if (alive && g > 0) {
+            for (int q = 0; q < 2; ++q) wait_bar(smem_u32(&ctl.k_empty[q]), (g - 1) & 1u, ctl, p.status, limit);
+            wait_bar(smem_u32(&ctl.q_empty), (nq - 1) & 1u, ctl, p.status, limit);
         }
     } else if (warp == kVWarp) {
         // ---------------- values: all keys of a tile in two halves, this CTA's 256 dims.
@@ -667,7 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // 150 clocks: while one issuer is at them the other's products run.
         // O's issuers, which wait for the first P of a piece, also write the pieces
         // down for all warps of their CTA, one ahead.
-        Scheduler sched(p, cluster);
+        Scheduler sched(ctl.head, ctl.start, cluster);
         bool alive = true;
         if (warp == kOWarp) alive = sched.write(p, ctl, lane);
         if (rank == 1) {
@@ -1006,16 +1091,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // share of P's buffer so that stores write whole sectors (a row a lane
                 // straight from the accumulator took 13,000 clocks).
                 // A part goes to slot 2c where the item began in an earlier cluster, else to 2c + 1.
-                const bool whole = pc->whole, narrow = whole && p.out_bf16;
+                const bool whole = pc->whole, narrow = p.out_bf16;
                 const int64_t out_row = (int64_t)pc->row0 + row;
                 const int64_t part_row = ((int64_t)2 * cluster + (t0 == 0 ? 1 : 0)) * kRows + row;
                 const float factor = whole ? 1.f / l : 1.f;
                 const int col0 = 256 * half + 128 * group, bytes = narrow ? 2 : 4;
                 const int rows_left = pc->nrows - (row - lane);            // of the warp's 32
                 uint8_t *stage = smem + kPOff + warp * 2048;
-                uint8_t *dst = (whole ? static_cast<uint8_t *>(p.out) + (out_row - lane) * D_L * bytes
-                                      : reinterpret_cast<uint8_t *>(p.part_o + (part_row - lane) * D_L)) +
-                               col0 * bytes + (int64_t)(lane >> 2) * D_L * bytes + 16 * (lane & 3);
+                uint8_t *dst = static_cast<uint8_t *>(whole ? p.out : p.part_o) +
+                               (((whole ? out_row : part_row) - lane + (lane >> 2)) * D_L + col0) * bytes + 16 * (lane & 3);
                 const uint32_t o_tmem = lane_tmem + kColO + 128 * group;
                 const int step = 64 / bytes;
 #pragma unroll 1
@@ -1056,8 +1140,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (!whole && t0 == 0 && rank == 0 && tx == 0) {
                     // the clusters that the item's tiles reach into
-                    const int64_t total = p.head->total;
-                    const int n = p.head->clusters;
+                    const int64_t total = ctl.head.total;
+                    const int n = ctl.head.clusters;
                     int64_t rest = pc->rest;
                     int parts = 1;
                     for (int k = cluster + 1; rest > 0 && k < n; ++k, ++parts) rest -= total * (k + 1) / n - total * k / n;
@@ -1089,34 +1173,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // One CTA: the items of the call, their costs, and where each cluster begins.
 constexpr int kPlanThreads = 1024;
 
-__device__ __forceinline__ int plan_scan(int v, int &sum, int *sh) {   // exclusive prefix over the CTA
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 31) sh[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int y = sh[lane];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, d);
-            if (lane >= d) y += z;
-        }
-        sh[32 + lane] = y;
-    }
-    __syncthreads();
-    sum = sh[63];
-    const int before = (warp ? sh[32 + warp - 1] : 0) + x - v;
-    __syncthreads();
-    return before;
-}
-
 __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const Problem p, uint32_t *status, int max_items, int clusters,
-                                                                PlanHead *head, PlanItem *items, Start *start, int32_t *item0) {
+                                                                PlanHead *head, Item *items, Start *start, int32_t *item0) {
     __shared__ int sh[64];
     pdl_wait();
     const DevBatch &b = p.b;
@@ -1130,7 +1188,7 @@ __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const Problem p,
             else n = ((t1 - t0) * p.H + kRows - 1) / kRows;
         }
         int sum;
-        const int before = plan_scan(n, sum, sh);
+        const int before = plan_scan<kPlanThreads>(n, sum, sh);
         if (s < b.B) item0[s] = base + before;
         base += sum;
     }
@@ -1143,36 +1201,25 @@ __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const Problem p,
     for (int i0 = 0; i0 < base; i0 += kPlanThreads) {
         const int i = i0 + (int)threadIdx.x;
         int cost = 0;
-        PlanItem pi{};
+        Item it{};
         if (i < base) {
             int lo = 0, hi = b.B;                             // item0[lo] <= i < item0[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (item0[mid] <= i) lo = mid; else hi = mid;
             }
-            pi.seq = lo;
-            pi.row = (i - item0[lo]) * kRows;
             const int t0 = __ldg(b.cu_q + lo), t1 = __ldg(b.cu_q + lo + 1);
-            const int row0 = t0 * p.H + pi.row, nrows = min(kRows, t1 * p.H - row0);
-            Item it;
             it.seq = lo;
-            it.min_pos = INT32_MAX;
-            it.hi = -1;
-            for (int t = row0 / p.H; t <= (row0 + nrows - 1) / p.H; ++t) {
-                const int pos = __ldg(b.q_pos + t);
-                if (pos >= 0 && pos < b.max_kv) {
-                    it.min_pos = min(it.min_pos, pos);
-                    it.hi = max(it.hi, pos);
-                }
-            }
-            item_tiles(p, it);
+            it.row0 = t0 * p.H + (i - item0[lo]) * kRows;
+            it.nrows = min(kRows, t1 * p.H - it.row0);
+            item_fill(p, it);
             cost = item_cost(it.n);
         }
         int sum;
-        const int before = plan_scan(cost, sum, sh);
+        const int before = plan_scan<kPlanThreads>(cost, sum, sh);
         if (i < base) {
-            pi.cost0 = total + before;
-            items[i] = pi;
+            it.cost0 = total + before;
+            items[i] = it;
         }
         total += sum;
     }
@@ -1191,57 +1238,88 @@ __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const Problem p,
     pdl_trigger();
 }
 
-// Joins the parts of an item that several clusters share: a warp a row.
-constexpr int kJoinRows = 8;
+// Joins the parts of an item that several clusters share: a row's 512 dims over as
+// many threads as there are 16-byte pieces, as many parts at a time as there are
+// loads in flight.  Parts have the output's type: bf16 parts are off by no more
+// than the output's own rounding, and halve what is written and read.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinLoads = 8;
+template <bool kBf16> constexpr int kJoinRows = kBf16 ? kJoinThreads / 64 : kJoinThreads / 128;
 
-__global__ void __launch_bounds__(32 * kJoinRows) mla_combine_kernel(const Split *split, const float *part_o, const float *part_ml,
-                                                                     void *out, int out_bf16, float *lse) {
+template <bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads) mla_combine_kernel(const Split *split, const void *part_o, const float *part_ml,
+                                                                   void *out, float *lse) {
+    constexpr int kPer = kBf16 ? 8 : 4;                       // dims a thread
+    constexpr int kRowThreads = D_L / kPer;
+    __shared__ float wgt[kJoinRows<kBf16>][kClusters];
     pdl_wait();
     const Split s = split[blockIdx.x];
-    const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= s.nrows) return;                               // 0 without a shared item
-    auto slot = [&](int k) { return ((int64_t)2 * (s.first + k) + (k == 0 ? 1 : 0)) * kRows + row; };
-    float M = -INFINITY;
+    const int mine = threadIdx.x / kRowThreads, tx = threadIdx.x % kRowThreads, lane = threadIdx.x & 31;
+    const int row = blockIdx.y * kJoinRows<kBf16> + mine;
+    if (blockIdx.y * kJoinRows<kBf16> >= s.nrows) return;     // 0 rows without a shared item
+    const bool there = row < s.nrows;
+    auto slot = [&](int k) { return ((int64_t)2 * (s.first + k) + (k == 0 ? 1 : 0)) * kRows + (there ? row : 0); };
+    // every warp of the row has all maxima and sums; one lets the others have the weights
+    float M = -INFINITY, L = 0.f;
     for (int k = lane; k < s.parts; k += 32) M = fmaxf(M, part_ml[slot(k) * 2]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    float L = 0.f;
-    float4 acc[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < s.parts; ++k) {
-        const int64_t at = slot(k);
-        const float2 ml = *reinterpret_cast<const float2 *>(part_ml + at * 2);
+    for (int k = lane; k < s.parts; k += 32) {
+        const float2 ml = *reinterpret_cast<const float2 *>(part_ml + slot(k) * 2);
         const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
         L += w * ml.y;
-        const float4 *src = reinterpret_cast<const float4 *>(part_o + at * D_L) + lane;
+        if (tx < 32) wgt[mine][k] = w;
+    }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float4 v = src[32 * q];
-            acc[q].x += w * v.x; acc[q].y += w * v.y; acc[q].z += w * v.z; acc[q].w += w * v.w;
+    for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    __syncthreads();
+    float acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < s.parts; k0 += kJoinLoads) {
+        uint4 v[kJoinLoads];
+#pragma unroll
+        for (int q = 0; q < kJoinLoads; ++q)
+            if (k0 + q < s.parts)
+                v[q] = *(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(part_o) + slot(k0 + q) * (D_L * (kBf16 ? 2 : 4))) + tx);
+#pragma unroll
+        for (int q = 0; q < kJoinLoads; ++q) {
+            if (k0 + q < s.parts) {
+                const float w = wgt[mine][k0 + q];
+                const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (kBf16) {
+                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e]));
+                        acc[2 * e] += w * f.x;
+                        acc[2 * e + 1] += w * f.y;
+                    } else {
+                        acc[e] += w * __uint_as_float(u[e]);
+                    }
+                }
+            }
         }
     }
+    if (!there) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t at = ((int64_t)s.row0 + row) * D_L + 4 * lane;
+    const int64_t at = ((int64_t)s.row0 + row) * D_L + kPer * tx;
+    uint32_t u[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float4 v = make_float4(acc[q].x * inv, acc[q].y * inv, acc[q].z * inv, acc[q].w * inv);
-        if (out_bf16) {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), c = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at + 128 * q) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (kBf16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+            u[e] = *reinterpret_cast<const uint32_t *>(&h);
         } else {
-            *reinterpret_cast<float4 *>(static_cast<float *>(out) + at + 128 * q) = v;
+            u[e] = __float_as_uint(acc[e] * inv);
         }
     }
-    if (lse && lane == 0) lse[(int64_t)s.row0 + row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(out) + at * (kBf16 ? 2 : 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+    if (lse && tx == 0) lse[(int64_t)s.row0 + row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ---------------------------------------------------------------- host
 namespace {
 
-constexpr int kClusters = kSMs / 2;
 
 struct MlaLayout {
     size_t head, start, split, ml, part, item0, items, total;
@@ -1261,7 +1339,7 @@ MlaLayout mla_layout(int64_t T, int64_t B, int64_t H, size_t off) {
     L.ml = take((size_t)2 * kClusters * kRows * 2 * sizeof(float));
     L.part = take((size_t)2 * kClusters * kRows * D_L * sizeof(float));
     L.item0 = take((size_t)B * sizeof(int32_t));
-    L.items = take((size_t)L.max_items * sizeof(PlanItem));
+    L.items = take((size_t)L.max_items * sizeof(Item));
     L.total = off;
     return L;
 }
@@ -1279,18 +1357,20 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     const MlaLayout L = mla_layout(b.T, b.B, a.H, kStatusBytes);
     uint8_t *w = static_cast<uint8_t *>(ws);
     uint32_t *status = reinterpret_cast<uint32_t *>(w);
-    MlaParams p;
+    MlaParams p{};
     p.pr = Problem{b, a.H, a.window, a.n_sink, a.sink_pos0};
     p.status = status;
     p.q_lat = a.q_lat;
     PlanHead *head = reinterpret_cast<PlanHead *>(w + L.head);
-    PlanItem *items = reinterpret_cast<PlanItem *>(w + L.items);
+    Item *items = reinterpret_cast<Item *>(w + L.items);
     Start *start = reinterpret_cast<Start *>(w + L.start);
     p.head = head;
-    p.items = items;
+    // One item a sequence, a thread for each: the kernel plans for itself.
+    const bool here = (int64_t)b.max_q * a.H <= kRows && b.B <= kThreads;
+    p.items = here ? nullptr : items;
     p.start = start;
     p.split = reinterpret_cast<Split *>(w + L.split);
-    p.part_o = reinterpret_cast<float *>(w + L.part);
+    p.part_o = w + L.part;
     p.part_ml = reinterpret_cast<float *>(w + L.ml);
     p.out = a.out;
     p.out_bf16 = a.out_bf16;
@@ -1300,14 +1380,16 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     p.rows_per_box = !b.block_table || b.block_size % 64 == 0 ? 64 : b.block_size % 16 == 0 ? 16 : 0;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(mla_attn_kernel), 12, kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_k(mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, p.pr, status, (int)L.max_items, kClusters, head,
+    if (!here) e = launch_k(mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, p.pr, status, (int)L.max_items, kClusters, head,
                  items, start, reinterpret_cast<int32_t *>(w + L.item0));
     if (e != cudaSuccess) return e;
     e = launch_k(mla_attn_kernel, dim3(2 * kClusters), dim3(kThreads), kSmem, stream, true, p, maps.q_lat, maps.q_rope, maps.kv64,
                  maps.kv16, maps.kv1);
     if (e != cudaSuccess) return e;
-    return launch_k(mla_combine_kernel, dim3(kClusters, kRows / kJoinRows), dim3(32 * kJoinRows), 0, stream, true,
-                    (const Split *)p.split, (const float *)p.part_o, (const float *)p.part_ml, a.out, a.out_bf16, a.lse);
+    const int rows = a.out_bf16 ? kJoinRows<true> : kJoinRows<false>;
+    return launch_k(a.out_bf16 ? mla_combine_kernel<true> : mla_combine_kernel<false>, dim3(kClusters, kRows / rows),
+                    dim3(kJoinThreads), 0, stream, true, (const Split *)p.split, (const void *)p.part_o, (const float *)p.part_ml,
+                    a.out, a.lse);
 }
 
 }  // namespace dsa
