@@ -101,6 +101,8 @@ SIGNATURES = {
     "dsa_kv_append_q8": (_I, [_P, _I64, _P, _I64, _I, _BP, _P, _P, _P, _P, _P, _SZ, _P]),
     "dsa_kv_read_q8": (_I, [_P, _P, _I, _BP, _P, _P, _I, _I64, _P, _SZ, _P]),
     "dsa_sparse_mla_attn_q8": (_I, [_P, _P, _P, _P, _BP, _P, _P, _I, _I, _F, _P, _I, _P, _P, _SZ, _P]),
+    "dsa_rms_norm": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I, _F, _P, _I64, _I, _I, _I, _P]),
+    "dsa_rms_norm_q8": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I, _F, _P, _P, _I, _I, _I, _I, _P]),
     "dsa_mla_attn": (_I, [_P, _P, _P, _BP, _P, _I, _F, _P, _I, _P, _P, _SZ, _P]),
     "dsa_mla_attn_window": (_I, [_P, _P, _P, _BP, _P, _I, _I, _I, _P, _F, _P, _I, _P, _P, _SZ, _P]),
     "dsa_version": (_I, []),
@@ -716,6 +718,52 @@ def dsa_sparse_mla_attn_q8(q_lat, q_rope, codes, scale, batch: Batch, idx, sm_sc
           q_rope.data_ptr() if q_rope is not None else None, codes.data_ptr(), scale.data_ptr(),
           C.byref(_batch_desc(batch, dev)), _paging(block_table, block_size, batch, dev), idx.data_ptr(), k, H, sm_scale,
           out.data_ptr(), dt, lse.data_ptr() if lse is not None else None, *_workspace_arg(ws, dev))
+
+
+def _norm_args(x, residual, sum, weight, dev):
+    """Checked arguments of the norms, up to the weight; x's dtype and shape."""
+    dt, kind, shape = _dt(x, "x"), x.dtype, x.shape
+    if len(shape) != 2:
+        raise TypeError(f"x: expected rows [T, dim], got shape {tuple(shape)}")
+    args = [x.data_ptr(), _rows(x, "x", kind, shape, dev)]
+    for t, name in ((residual, "residual"), (sum, "sum")):
+        args += [None, 0] if t is None else [t.data_ptr(), _rows(t, name, kind, shape, dev)]
+    if weight is None:
+        return args + [None, dt], dt, shape
+    wt = weight.dtype
+    if wt is not kind and wt is not _t_f32:
+        raise TypeError(f"weight: expected {kind} or torch.float32, got {wt}")
+    _shaped(weight, "weight", wt, (shape[1],), dev)
+    return args + [weight.data_ptr(), _DT[wt]], dt, shape
+
+
+def dsa_rms_norm(x, residual, sum, weight, eps: float, out, stream=None):
+    """out = h / sqrt(mean(h^2) + eps) * weight over the rows of h = x + residual
+    (rounded to x's dtype; stored in sum).  x, residual, sum, out: [T, dim] of one
+    dtype (float32, float16, bfloat16), any row strides; residual, sum and weight may
+    be None; weight [dim] of x's dtype or float32.  sum and out may be x or residual."""
+    if not _DT:
+        _bind()
+    dev = _cuda(x, "x")
+    args, dt, shape = _norm_args(x, residual, sum, weight, dev)
+    stride = _rows(out, "out", x.dtype, shape, dev)
+    _call("dsa_rms_norm", dev, stream, lib().dsa_rms_norm, *args, eps, out.data_ptr(), stride, dt, shape[0], shape[1])
+
+
+def dsa_rms_norm_q8(x, residual, sum, weight, eps: float, codes, scale, stream=None):
+    """dsa_rms_norm with e4m3 codes (uint8 [T, dim]) and one float32 scale per
+    group as output; scale [T, dim / group] gives the group: 32, 64, 128 or dim."""
+    if not _DT:
+        _bind()
+    dev = _cuda(x, "x")
+    args, dt, (T, dim) = _norm_args(x, residual, sum, weight, dev)
+    _shaped(codes, "codes", _t_u8, (T, dim), dev)
+    groups = scale.shape[-1]
+    _shaped(scale, "scale", _t_f32, (T, groups), dev)
+    if groups < 1 or dim % groups:
+        raise TypeError(f"scale: {groups} groups do not divide rows of {dim}")
+    _call("dsa_rms_norm_q8", dev, stream, lib().dsa_rms_norm_q8, *args, eps, codes.data_ptr(), scale.data_ptr(),
+          dim // groups, dt, T, dim)
 
 
 def _mla_args(q_lat, q_rope, kv_cache, batch: Batch, out, lse, ws, block_table, block_size, dev):

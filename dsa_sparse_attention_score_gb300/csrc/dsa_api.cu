@@ -25,6 +25,7 @@ int g_skip_copies = 0;
 constexpr int kMaxHeads = 128;        // query heads: one or two groups of 64 per token
 constexpr int kMaxSplit = 128;        // split partials the combine kernel merges
 constexpr int kMaxRotDim = 512;       // values of a head that rotary positions turn
+constexpr int kMaxNormDim = 16384;    // values of a row that a norm keeps in registers
 constexpr int kKpoolMaxTopK = 4096;   // kpool: 1024 pools per token (the expansion's slots)
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -999,6 +1000,67 @@ dsa_status_t dsa_mla_attn_window(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, 
     if (window < 1 || n_sink < 0) return DSA_ERR_INVALID_ARGUMENT;
     return mla_attn_impl(q_lat, q_rope, kv_cache, batch, paging, H, window, n_sink, sink_pos0, sm_scale, out, out_dtype, lse,
                          ws, ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------- norms
+
+// May rows of y (written) and of x (read before they are) lie where they are?
+// The same rows, rows without a byte in common, or slices of the same wider rows.
+static bool rows_apart(const void *x, int64_t xs, const void *y, int64_t ys, int64_t n, int64_t dim, int64_t e, bool same_allowed) {
+    if (!x || !y) return true;
+    if (n == 1) xs = ys = dim;
+    const uintptr_t xb = reinterpret_cast<uintptr_t>(x), yb = reinterpret_cast<uintptr_t>(y);
+    if (xb == yb && xs == ys) return same_allowed;
+    const uintptr_t xe = xb + (uintptr_t)(((n - 1) * xs + dim) * e), ye = yb + (uintptr_t)(((n - 1) * ys + dim) * e);
+    if (xe <= yb || ye <= xb) return true;
+    return xs == ys && slices_apart((int64_t)(xb > yb ? xb - yb : yb - xb) / e, dim, n, xs, 1, 0);
+}
+
+static dsa_status_t rms_norm_impl(NormLaunch a, cudaStream_t stream) {
+    if (!a.x || !float_dtype(a.dtype) || a.n < 1 || a.dim < 1) return DSA_ERR_INVALID_ARGUMENT;
+    if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return DSA_ERR_INVALID_ARGUMENT;
+    if (a.dim > kMaxNormDim) return DSA_ERR_UNSUPPORTED;
+    constexpr int64_t kFar = int64_t(1) << 40;
+    struct { const void *p; int64_t *s; bool written; } rows[] = {{a.x, &a.x_stride, false}, {a.residual, &a.residual_stride, false},
+                                                                {a.sum, &a.sum_stride, true}, {a.out, &a.out_stride, true}};
+    const int64_t e = dtype_bytes(a.dtype);
+    for (auto &r : rows) {
+        if (!r.p || a.n == 1) *r.s = a.dim;                             // addresses nothing
+        if (*r.s < (r.written ? a.dim : 0) || *r.s > kFar / a.n) return DSA_ERR_INVALID_ARGUMENT;
+        if (!aligned(r.p, (size_t)e)) return DSA_ERR_MISALIGNED;
+    }
+    if (!aligned(a.weight, a.weight_f32 ? 4 : (size_t)e)) return DSA_ERR_MISALIGNED;
+    // a row's sum and output are written after all of it has been read
+    for (const void *w : {static_cast<const void *>(a.sum), static_cast<const void *>(a.out)}) {
+        const int64_t ws = w == a.sum ? a.sum_stride : a.out_stride;
+        if (!rows_apart(a.x, a.x_stride, w, ws, a.n, a.dim, e, true) ||
+            !rows_apart(a.residual, a.residual_stride, w, ws, a.n, a.dim, e, true))
+            return DSA_ERR_INVALID_ARGUMENT;
+    }
+    if (!rows_apart(a.sum, a.sum_stride, a.out, a.out_stride, a.n, a.dim, e, false)) return DSA_ERR_INVALID_ARGUMENT;
+    DSA_TRY_CUDA(launch_rms_norm(a, stream));
+    return DSA_OK;
+}
+
+dsa_status_t dsa_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, void *sum,
+                          int64_t sum_stride, const void *weight, int weight_dtype, float eps, void *out, int64_t out_stride,
+                          int dtype, int n_tokens, int dim, cudaStream_t stream) {
+    if (!out || (weight && weight_dtype != dtype && weight_dtype != DSA_DT_F32)) return DSA_ERR_INVALID_ARGUMENT;
+    NormLaunch a{x, residual, sum, weight, weight && weight_dtype == DSA_DT_F32, out, nullptr, nullptr, x_stride, residual_stride,
+                 sum_stride, out_stride, dtype, n_tokens, dim, 0, eps};
+    return rms_norm_impl(a, stream);
+}
+
+dsa_status_t dsa_rms_norm_q8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, void *sum,
+                             int64_t sum_stride, const void *weight, int weight_dtype, float eps, uint8_t *codes, float *scale,
+                             int group, int dtype, int n_tokens, int dim, cudaStream_t stream) {
+    if (!codes || !scale || (weight && weight_dtype != dtype && weight_dtype != DSA_DT_F32)) return DSA_ERR_INVALID_ARGUMENT;
+    if (dim < 1 || group < 1 || dim % group) return DSA_ERR_INVALID_ARGUMENT;
+    if (dim % 16 || (group != dim && group != 32 && group != 64 && group != 128)) return DSA_ERR_UNSUPPORTED;
+    if (!aligned(codes, 16) || !aligned(scale, 4)) return DSA_ERR_MISALIGNED;
+    NormLaunch a{x, residual, sum, weight, weight && weight_dtype == DSA_DT_F32, nullptr, codes, scale, x_stride, residual_stride,
+                 sum_stride, 0, dtype, n_tokens, dim, group, eps};
+    return rms_norm_impl(a, stream);
 }
 
 }  // extern "C"

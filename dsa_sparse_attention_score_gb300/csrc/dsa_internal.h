@@ -237,6 +237,21 @@ size_t mla_attn_workspace(int T, int B, int H);
 bool mla_attn_countable(int T, int B, int H, int max_kv);   // do the plan's counts fit
 cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBatch &b, void *ws, cudaStream_t stream);
 
+// Root-mean-square norm of rows (norm.cu): plain outputs, or e4m3 codes.
+struct NormLaunch {
+    const void *x, *residual;         // [n, dim] rows of dtype; residual null: none
+    void *sum;                        // x + residual, or null
+    const void *weight;               // [dim] of dtype, or float32 with weight_f32; null: 1
+    int weight_f32;
+    void *out;                        // or null, with
+    uint8_t *codes;                   // [n, dim] and
+    float *scale;                     // [n, dim / group]
+    int64_t x_stride, residual_stride, sum_stride, out_stride;
+    int dtype, n, dim, group;
+    float eps;
+};
+cudaError_t launch_rms_norm(const NormLaunch &a, cudaStream_t stream);
+
 // Sets a kernel's dynamic shared-memory limit once per device; `slot`
 // (0..kSmemAttrSlots-1) names the kernel instance.
 constexpr int kSmemAttrSlots = 13;

@@ -1,0 +1,244 @@
+// norm.cu -- root-mean-square norm of rows, with the residual's addition in
+// front and, in place of plain outputs, e4m3 codes with one scale per group:
+//     h = x + residual (rounded to the rows' type, as it is stored),
+//     y = h / sqrt(mean(h^2) + eps) * weight,
+//     scale = max(max |y| / 448, 2^-40),  code = e4m3(y / scale)  per group.
+//
+// Bound by HBM: a row's values are read once, kept in registers over the one
+// reduction that the row needs, and written once.  A row belongs to a run of
+// threads of one CTA (several short rows share a CTA), each of which holds up to
+// V units of W values; a unit is 16 bytes where the rows allow it.  Few rows get
+// many threads each (latency), many rows four units a thread, which keeps enough
+// loads in flight for the memory.
+#include <algorithm>
+
+#include "dsa_common.cuh"
+#include "dsa_internal.h"
+#include "quant8.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr float kLeastScale = 9.094947017729282e-13f;   // 2^-40, as in the 8-bit cache
+constexpr float kTop = 448.f;                           // the largest e4m3 value
+
+struct NormParams {
+    const void *x, *residual;      // residual null: none
+    void *sum;                     // null: not stored
+    const void *weight;            // null: 1
+    int weight_f32;
+    void *out;
+    uint8_t *codes;                // [n, dim]
+    float *scale;                  // [n, groups]
+    int64_t xs, rs, ss, os;        // values between rows
+    int n, dim, group;
+    float eps;
+};
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T, int W> struct alignas(W * sizeof(T) >= 16 ? 16 : sizeof(T)) Unit { T v[W]; };
+
+template <typename T, int W, bool kAligned> __device__ __forceinline__ Unit<T, W> load_unit(const T *p) {
+    if constexpr (kAligned || W == 1) return *reinterpret_cast<const Unit<T, W> *>(p);
+    Unit<T, W> u;
+#pragma unroll
+    for (int e = 0; e < W; ++e) u.v[e] = p[e];
+    return u;
+}
+template <typename T, int W, bool kAligned> __device__ __forceinline__ void store_unit(T *p, const Unit<T, W> &u) {
+    if constexpr (kAligned || W == 1) {
+        *reinterpret_cast<Unit<T, W> *>(p) = u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e) p[e] = u.v[e];
+    }
+}
+
+// Reduction over the threads of a row (blockDim.x of them, whole warps).
+template <typename Op, typename V> __device__ __forceinline__ V row_reduce(V v, Op op, V *sh) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, d));
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    V *row = sh + threadIdx.y * warps;
+    __syncthreads();                                     // an earlier reduction has been read
+    if ((threadIdx.x & 31) == 0) row[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = row[0];
+    for (int w = 1; w < warps; ++w) v = op(v, row[w]);   // the same order in every thread
+    return v;
+}
+
+}  // namespace
+
+template <typename T, int W, int V, bool kAligned, bool kCodes>
+__global__ void __launch_bounds__(W *V <= 16 ? 1024 : 512) rms_norm_kernel(const NormParams p) {
+    __shared__ uint32_t sh[32];
+    const int row = blockIdx.x * blockDim.y + threadIdx.y;
+    const bool live = row < p.n;
+    const int tx = threadIdx.x, step = blockDim.x;
+    const T *x = static_cast<const T *>(p.x) + row * p.xs;
+    pdl_wait();
+    float h[V][W];
+    {
+        Unit<T, W> a[V], r[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = (tx + k * step) * W;
+            if (live && at < p.dim) {
+                a[k] = load_unit<T, W, kAligned>(x + at);
+                if (p.residual) r[k] = load_unit<T, W, kAligned>(static_cast<const T *>(p.residual) + row * p.rs + at);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = (tx + k * step) * W;
+            const bool on = live && at < p.dim;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                if (on && p.residual) a[k].v[e] = from_f<T>(to_f(a[k].v[e]) + to_f(r[k].v[e]));
+                h[k][e] = on ? to_f(a[k].v[e]) : 0.f;
+            }
+            if (on && p.sum) store_unit<T, W, kAligned>(static_cast<T *>(p.sum) + row * p.ss + at, a[k]);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < W; ++e) ss = fmaf(h[k][e], h[k][e], ss);
+    ss = row_reduce(ss, [](float a, float b) { return a + b; }, reinterpret_cast<float *>(sh));
+    const float rstd = 1.f / sqrtf(ss / (float)p.dim + p.eps);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int at = (tx + k * step) * W;
+        if (at < p.dim) {
+            if (!p.weight) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) h[k][e] *= rstd;
+            } else if (p.weight_f32) {
+                const float *w = static_cast<const float *>(p.weight) + at;
+#pragma unroll
+                for (int e = 0; e < W; ++e) h[k][e] = h[k][e] * rstd * __ldg(w + e);
+            } else {
+                const Unit<T, W> w = load_unit<T, W, kAligned>(static_cast<const T *>(p.weight) + at);
+#pragma unroll
+                for (int e = 0; e < W; ++e) h[k][e] = h[k][e] * rstd * to_f(w.v[e]);
+            }
+        }
+    }
+    if constexpr (!kCodes) {
+        if (!live) return;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = (tx + k * step) * W;
+            if (at < p.dim) {
+                Unit<T, W> u;
+#pragma unroll
+                for (int e = 0; e < W; ++e) u.v[e] = from_f<T>(h[k][e]);
+                store_unit<T, W, kAligned>(static_cast<T *>(p.out) + row * p.os + at, u);
+            }
+        }
+    } else {
+        // Magnitudes compare as their bits do, NaN above infinity above all numbers.
+        uint32_t top[V], all = 0;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            top[k] = 0;
+#pragma unroll
+            for (int e = 0; e < W; ++e) top[k] = max(top[k], __float_as_uint(h[k][e]) & 0x7fffffffu);
+            all = max(all, top[k]);
+        }
+        const bool whole = p.group == p.dim;             // one scale a row
+        if (whole) all = row_reduce(all, [](uint32_t a, uint32_t b) { return max(a, b); }, sh);
+        const int lanes = p.group / W;                   // of one group (a power of two up to 32 otherwise)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = (tx + k * step) * W;
+            uint32_t t = whole ? all : top[k];
+            if (!whole)
+                for (int d = 1; d < lanes; d <<= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, d));
+            if (!live || at >= p.dim) continue;
+            const bool bad = t >= 0x7f800000u;
+            const float scale = bad ? __int_as_float(0x7fffffff) : fmaxf(__uint_as_float(t) / kTop, kLeastScale);
+            const float inv = 1.f / scale;
+            uint32_t c[W / 4];
+#pragma unroll
+            for (int e = 0; e < W; e += 4)
+                c[e / 4] = bad ? 0u : e4m3x2(h[k][e] * inv, h[k][e + 1] * inv) | e4m3x2(h[k][e + 2] * inv, h[k][e + 3] * inv) << 16;
+            uint8_t *dst = p.codes + (int64_t)row * p.dim + at;
+            if constexpr (W == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0], c[1]);
+            else *reinterpret_cast<uint32_t *>(dst) = c[0];
+            if (whole ? at == 0 : at % p.group == 0) p.scale[(int64_t)row * (p.dim / p.group) + at / p.group] = scale;
+        }
+    }
+}
+
+namespace {
+
+template <typename T, int W, int V, bool kAligned, bool kCodes>
+cudaError_t launch_norm_as(const NormParams &p, cudaStream_t stream) {
+    const int units = (p.dim + W - 1) / W;
+    const int threads = std::max(32, ((units + V - 1) / V + 31) / 32 * 32), rows = std::max(1, 128 / threads);
+    return launch_k(rms_norm_kernel<T, W, V, kAligned, kCodes>, dim3((unsigned)((p.n + rows - 1) / rows)),
+                    dim3((unsigned)threads, (unsigned)rows), 0, stream, true, p);
+}
+
+// Units a thread: one where that leaves no more than a wave of CTAs (two of
+// 1024 threads an SM) -- the row's latency is then its one load's --, else four.
+template <typename T, int W, bool kAligned, bool kCodes>
+cudaError_t launch_norm_units(const NormParams &p, cudaStream_t stream) {
+    const int units = (p.dim + W - 1) / W;
+    if (units <= 1024 && (int64_t)p.n * units <= 2048 * kSMs) return launch_norm_as<T, W, 1, kAligned, kCodes>(p, stream);
+    if (units <= 4 * (W * 4 <= 16 ? 1024 : 512)) return launch_norm_as<T, W, 4, kAligned, kCodes>(p, stream);
+    if constexpr (W == 1) return launch_norm_as<T, W, 16, kAligned, kCodes>(p, stream);
+    return cudaErrorInvalidValue;
+}
+
+template <typename T> cudaError_t launch_norm_t(const NormParams &p, cudaStream_t stream) {
+    constexpr int W = 16 / sizeof(T);
+    const auto bits = [](const void *q) { return reinterpret_cast<uintptr_t>(q); };
+    const bool aligned = ((bits(p.x) | bits(p.residual) | bits(p.sum) | bits(p.out) | (p.weight_f32 ? 0 : bits(p.weight))) & 15) == 0 &&
+                         (p.xs | p.rs | p.ss | p.os) % W == 0;
+    if (p.codes) return aligned ? launch_norm_units<T, W, true, true>(p, stream) : launch_norm_units<T, W, false, true>(p, stream);
+    if (p.dim % W == 0) return aligned ? launch_norm_units<T, W, true, false>(p, stream) : launch_norm_units<T, W, false, false>(p, stream);
+    return launch_norm_units<T, 1, true, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const NormLaunch &a, cudaStream_t stream) {
+    NormParams p;
+    p.x = a.x;
+    p.residual = a.residual;
+    p.sum = a.sum;
+    p.weight = a.weight;
+    p.weight_f32 = a.weight_f32;
+    p.out = a.out;
+    p.codes = a.codes;
+    p.scale = a.scale;
+    p.xs = a.x_stride;
+    p.rs = a.residual ? a.residual_stride : 0;
+    p.ss = a.sum ? a.sum_stride : 0;
+    p.os = a.out ? a.out_stride : 0;
+    p.n = a.n;
+    p.dim = a.dim;
+    p.group = a.group;
+    p.eps = a.eps;
+    switch (a.dtype) {
+        case DSA_DT_F32: return launch_norm_t<float>(p, stream);
+        case DSA_DT_F16: return launch_norm_t<__half>(p, stream);
+        default: return launch_norm_t<__nv_bfloat16>(p, stream);
+    }
+}
+
+}  // namespace dsa

@@ -533,6 +533,40 @@ dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rop
                                     float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Root-mean-square norm of rows, with the residual's addition in front:
+ *   h = x + residual     rounded to the element type (x itself without one)
+ *   sum = h              the new residual stream (sum may be residual or x; NULL:
+ *                        not stored)
+ *   out = h / sqrt(mean(h^2) + eps) * weight
+ * computed in float32 from the rounded h and rounded once.  dsa_rms_norm_q8 gives
+ * e4m3 codes and one float32 scale per group of values instead of out:
+ *   scale = max(max |y| / 448, 2^-40),  code = e4m3(y / scale)
+ * with y the norm's unrounded float32 values (round to nearest even).  A group
+ * with a value that is not finite gets the scale NaN and codes 0.
+ *   x, residual, sum, out   n_tokens rows of dim values of dtype DSA_DT_*,
+ *                *_stride values apart (>= 0; >= dim where rows are written; that of
+ *                a single row does not count); residual, sum and weight may be NULL
+ *   weight       [dim] of dtype, or float32 (weight_dtype)
+ *   codes        uint8 [n_tokens, dim], 16-byte aligned; scale float32
+ *                [n_tokens, dim / group], group 32, 64, 128 or dim
+ * out and sum may be x or residual with the same strides, but not each other;
+ * otherwise rows written must not share values with others, except as column
+ * slices of wider rows.  h^2 has to stay finite in float32 (and eps > 0 where all
+ * of a row may be 0).  No workspace.
+ * Errors: DSA_ERR_INVALID_ARGUMENT for null pointers, sizes below 1, a negative or
+ * not finite eps, strides outside the above, rows that overlap, dim not a multiple
+ * of group; DSA_ERR_UNSUPPORTED for dim > 16384, and with codes for dim not a
+ * multiple of 16 or another group; DSA_ERR_MISALIGNED for pointers not aligned to
+ * their elements.
+ */
+dsa_status_t dsa_rms_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, void *sum,
+                          int64_t sum_stride, const void *weight, int weight_dtype, float eps, void *out, int64_t out_stride,
+                          int dtype, int n_tokens, int dim, cudaStream_t stream);
+dsa_status_t dsa_rms_norm_q8(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride, void *sum,
+                             int64_t sum_stride, const void *weight, int weight_dtype, float eps, uint8_t *codes, float *scale,
+                             int group, int dtype, int n_tokens, int dim, cudaStream_t stream);
+
+/*
  * Attention of every query head over all the latent rows that its token sees,
  * nothing selected: contexts that fit a selection whole, layers without an
  * indexer.  Token t attends to the positions s = 0..q_pos[t] of its sequence,
