@@ -721,20 +721,22 @@ def dsa_sparse_mla_attn_q8(q_lat, q_rope, codes, scale, batch: Batch, idx, sm_sc
 
 
 def _norm_args(x, residual, sum, weight, dev):
-    """Checked arguments of the norms, up to the weight; x's dtype and shape."""
-    dt, kind, shape = _dt(x, "x"), x.dtype, x.shape
+    """Checked arguments of the norms up to the weight, x's DSA_DT_* and shape."""
+    kind, shape = x.dtype, x.shape
+    dt = _dt(x, "x")
     if len(shape) != 2:
         raise TypeError(f"x: expected rows [T, dim], got shape {tuple(shape)}")
-    args = [x.data_ptr(), _rows(x, "x", kind, shape, dev)]
-    for t, name in ((residual, "residual"), (sum, "sum")):
-        args += [None, 0] if t is None else [t.data_ptr(), _rows(t, name, kind, shape, dev)]
-    if weight is None:
-        return args + [None, dt], dt, shape
-    wt = weight.dtype
-    if wt is not kind and wt is not _t_f32:
-        raise TypeError(f"weight: expected {kind} or torch.float32, got {wt}")
-    _shaped(weight, "weight", wt, (shape[1],), dev)
-    return args + [weight.data_ptr(), _DT[wt]], dt, shape
+    xs, rp, rs, sp, ss, wp, wt = _rows(x, "x", kind, shape, dev), None, 0, None, 0, None, dt
+    if residual is not None:
+        rp, rs = residual.data_ptr(), _rows(residual, "residual", kind, shape, dev)
+    if sum is not None:
+        sp, ss = sum.data_ptr(), _rows(sum, "sum", kind, shape, dev)
+    if weight is not None:
+        if weight.dtype is not kind:
+            wt = DSA_DT_F32
+        _shaped(weight, "weight", kind if wt == dt else _t_f32, shape[1:], dev)
+        wp = weight.data_ptr()
+    return (x.data_ptr(), xs, rp, rs, sp, ss, wp, wt), dt, shape
 
 
 def dsa_rms_norm(x, residual, sum, weight, eps: float, out, stream=None):
@@ -756,8 +758,9 @@ def dsa_rms_norm_q8(x, residual, sum, weight, eps: float, codes, scale, stream=N
     if not _DT:
         _bind()
     dev = _cuda(x, "x")
-    args, dt, (T, dim) = _norm_args(x, residual, sum, weight, dev)
-    _shaped(codes, "codes", _t_u8, (T, dim), dev)
+    args, dt, shape = _norm_args(x, residual, sum, weight, dev)
+    T, dim = shape
+    _shaped(codes, "codes", _t_u8, shape, dev)
     groups = scale.shape[-1]
     _shaped(scale, "scale", _t_f32, (T, groups), dev)
     if groups < 1 or dim % groups:
