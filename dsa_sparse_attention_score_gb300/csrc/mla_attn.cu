@@ -150,7 +150,6 @@ struct __align__(16) Item {
     int32_t min_pos;                  // the least position of its tokens (those that see anything)
     int32_t first_tile, n_first;      // tiles of the first positions before those of [lo, hi]
     int32_t tile0, n;                 // first tile of [lo, hi]; all tiles
-    int32_t spare;                    // a cache row that may be read for positions that no row sees
     int64_t kv0;
 };
 
@@ -195,7 +194,6 @@ struct Piece {
     int32_t whole;                // all tiles of the item
     int32_t rest;                 // tiles of the item behind t1
     int32_t end;                  // no piece: there are no more
-    int32_t spare;                // a cache row that may be read for positions that no row sees
     int64_t kv0;
 };
 constexpr int kPieces = 3;        // read ahead
@@ -211,10 +209,8 @@ struct Ctl {
     int32_t abort_flag;
     float red[2][2][2][kHalf];    // a group's maxima by tile and half of the keys
     alignas(16) float m[2][kHalf];   // running maxima by tile
-    // The first item of a plan made here, read before the first maximum is written.
-    __device__ __forceinline__ Item &first() { return *reinterpret_cast<Item *>(&m[0][0]); }
-    PlanHead head;                // the plan, and where this cluster begins
-    Start start;
+    PlanHead head;                // the plan, and what is left of it behind the first piece:
+    int32_t todo[4];              // a Todo
     Piece piece[kPieces];
 };
 constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
@@ -332,14 +328,16 @@ __device__ __forceinline__ void item_fill(const Problem &p, Item &it) {
             it.hi = max(it.hi, pos);
         }
     }
-    // the row of the last position; row 0 if that has none (no row sees anything then)
-    it.spare = it.hi < 0 || it.kv0 < 0 ? 0 : max(0, any_row(b, it.seq, it.kv0, it.hi));
     item_tiles(p, it);
 }
-// The item of a sequence that has at most one (false: it has no rows).
+// The item of a sequence that has at most one (false: it has no rows).  Where every
+// sequence has one token (decode) its position is loaded beside the offsets, not
+// behind them.
 __device__ __forceinline__ bool item_of(const Problem &p, int seq, uint32_t *status, Item &it) {
     const DevBatch &b = p.b;
+    const int guess = __ldg(b.q_pos + min(seq, b.T - 1));
     const int t0 = __ldg(b.cu_q + seq), t1 = __ldg(b.cu_q + seq + 1);
+    it.kv0 = seq_base(b, seq);
     if (t0 < 0 || t1 < t0 || t1 > b.T || (t1 - t0) * p.H > kRows) {
         flag(status, DSA_DEV_BAD_POSITION);
         return false;
@@ -348,92 +346,108 @@ __device__ __forceinline__ bool item_of(const Problem &p, int seq, uint32_t *sta
     it.seq = seq;
     it.row0 = t0 * p.H;
     it.nrows = (t1 - t0) * p.H;
-    item_fill(p, it);
+    it.min_pos = INT32_MAX;
+    it.hi = -1;
+    for (int t = t0; t < t1; ++t) {
+        const int pos = t == seq ? guess : __ldg(b.q_pos + t);
+        if (pos >= 0 && pos < b.max_kv) {
+            it.min_pos = min(it.min_pos, pos);
+            it.hi = max(it.hi, pos);
+        }
+    }
+    item_tiles(p, it);
     return true;
+}
+
+// What a cluster has still to do.
+struct Todo {
+    int32_t item, off, left;      // next item, costs of it done, costs left to this cluster
+    int32_t written;              // pieces in the ring
+    // The next piece, of item `it`; false: costs that stand for no tile.
+    __device__ __forceinline__ bool take(const Item &it, Piece &pc) {
+        const int cost = item_cost(it.n), n = min(left, cost - off);
+        pc.t0 = min(off, it.n);
+        pc.t1 = min(off + n, it.n);
+        const bool first = off == 0;
+        left -= n;
+        off += n;
+        if (off == cost) {
+            ++item;
+            off = 0;
+        }
+        pc.n_first = it.n_first;
+        pc.first_tile = it.first_tile;
+        pc.tile0 = it.tile0;
+        pc.lo = it.lo;
+        pc.hi = it.hi;
+        pc.s_lo = it.s_lo;
+        pc.s_hi = it.s_hi;
+        pc.min_pos = it.min_pos;
+        pc.row0 = it.row0;
+        pc.nrows = it.nrows;
+        pc.seq = it.seq;
+        pc.whole = pc.t0 == 0 && pc.t1 == it.n;
+        pc.rest = it.n - pc.t1;
+        pc.kv0 = it.kv0;
+        pc.end = 0;
+        return pc.t1 > pc.t0 || (it.n == 0 && first);
+    }
+};
+// This CTA's query rows of a piece into L2, long before they are wanted.
+__device__ __forceinline__ void ask_for_queries(const MlaParams &p, const Piece &pc) {
+    if (pc.t1 == pc.t0) return;
+    const int64_t row = (int64_t)pc.row0 + kHalf * (int)cluster_rank(), rows = (int64_t)p.pr.b.T * p.pr.H - row;
+    if (rows > 0) prefetch_l2_bulk(p.q_lat + row * D_L, (uint32_t)min(rows, (int64_t)kHalf) * (D_L * 2));
 }
 
 // Writes the cluster's pieces into the ring, one a call, with a whole warp.
 struct Scheduler {
-    int item = 0, off = 0, left = 0;   // next item, costs of it done, costs left to this cluster
-    uint32_t n = 0;
-    bool end = false, begun = false;
-    __device__ __forceinline__ Scheduler(const PlanHead &head, Start st, int cluster) {
-        const int64_t total = head.total;
-        if (cluster >= head.clusters) return;
-        item = st.item;
-        off = st.off;
-        left = (int)(total * (cluster + 1) / head.clusters - total * cluster / head.clusters);
-    }
+    Todo todo;
+    bool end = false;
     __device__ __noinline__ bool write(const MlaParams &p, Ctl &ctl, int lane);
 };
 
 // That of a position that some row of the piece sees, its spare one for any other.
-__device__ __noinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status, const Piece *pc, int pos) {
-    if (!seen_by_some(*pc, pos)) return pc->spare;
+__device__ __noinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
+    if (!seen_by_some(*pc, pos)) return spare;
     const int32_t r = any_row(b, pc->seq, pc->kv0, pos);
     if (r >= 0) return r;
     flag(status, DSA_DEV_BAD_INDEX);
-    return pc->spare;
+    return spare;
+}
+// The row of a piece's last position, which may be read for positions that no row
+// sees; row 0 if that has none (no row sees anything then).
+__device__ __forceinline__ int32_t spare_row(const DevBatch &b, const Piece *pc) {
+    return pc->hi < 0 || pc->kv0 < 0 ? 0 : max(0, any_row(b, pc->seq, pc->kv0, pc->hi));
 }
 
 __device__ __noinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int lane) {
     while (!end) {
-        end = left <= 0;
+        end = todo.left <= 0;
         Piece pc{};
         pc.end = end;
         if (!end) {
             Item it;
             if (p.items) {
-                it = p.items[item];
-            } else if (!begun) {
-                it = ctl.first();
-                begun = true;
-            } else if (!item_of(p.pr, item, p.status, it)) {  // no rows: no costs
-                ++item;
+                it = p.items[todo.item];
+            } else if (!item_of(p.pr, todo.item, p.status, it)) {   // no rows: no costs
+                ++todo.item;
                 continue;
             }
-            const int cost = item_cost(it.n), take = min(left, cost - off);
-            pc.t0 = min(off, it.n);
-            pc.t1 = min(off + take, it.n);
-            const bool first = off == 0;
-            left -= take;
-            off += take;
-            if (off == cost) {
-                ++item;
-                off = 0;
-            }
-            if (pc.t1 == pc.t0 && !(it.n == 0 && first)) continue;
-            pc.n_first = it.n_first;
-            pc.first_tile = it.first_tile;
-            pc.tile0 = it.tile0;
-            pc.lo = it.lo;
-            pc.hi = it.hi;
-            pc.s_lo = it.s_lo;
-            pc.s_hi = it.s_hi;
-            pc.min_pos = it.min_pos;
-            pc.row0 = it.row0;
-            pc.nrows = it.nrows;
-            pc.seq = it.seq;
-            pc.whole = pc.t0 == 0 && pc.t1 == it.n;
-            pc.rest = it.n - pc.t1;
-            pc.kv0 = it.kv0;
-            pc.spare = it.spare;
+            if (!todo.take(it, pc)) continue;
         }
-        if (!wait_bar(smem_u32(&ctl.piece_empty[n % kPieces]), ((n / kPieces) & 1u) ^ 1u, ctl, p.status, p.pr.b.wait_ns)) {
+        const uint32_t n = (uint32_t)todo.written, slot = n % kPieces;
+        if (!wait_bar(smem_u32(&ctl.piece_empty[slot]), ((n / kPieces) & 1u) ^ 1u, ctl, p.status, p.pr.b.wait_ns)) {
             end = true;
             return false;
         }
         if (lane == 0) {
-            ctl.piece[n % kPieces] = pc;
-            mbar_arrive(smem_u32(&ctl.piece_full[n % kPieces]));
-            if (pc.t1 > pc.t0) {
-                // this CTA's query rows, wanted when the piece before is scored
-                const int64_t row = (int64_t)pc.row0 + kHalf * (int)cluster_rank(), rows = (int64_t)p.pr.b.T * p.pr.H - row;
-                if (rows > 0) prefetch_l2_bulk(p.q_lat + row * D_L, (uint32_t)min(rows, (int64_t)kHalf) * (D_L * 2));
-            }
+            ctl.piece[slot] = pc;
+            mbar_arrive(smem_u32(&ctl.piece_full[slot]));
+            ask_for_queries(p, pc);
         }
         __syncwarp();
-        ++n;
+        ++todo.written;
         break;
     }
     return true;
@@ -464,9 +478,9 @@ __device__ __noinline__ void copy_values(uint32_t dst, const CUtensorMap *kv64, 
     }
 }
 // The rows of the four keys from `pos` on.
-__device__ __noinline__ int4 four_rows(const DevBatch &b, uint32_t *status, const Piece *pc, int pos) {
-    return make_int4(row_or_spare(b, status, pc, pos), row_or_spare(b, status, pc, pos + 1), row_or_spare(b, status, pc, pos + 2),
-                     row_or_spare(b, status, pc, pos + 3));
+__device__ __noinline__ int4 four_rows(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
+    return make_int4(row_or_spare(b, status, pc, pos, spare), row_or_spare(b, status, pc, pos + 1, spare),
+                     row_or_spare(b, status, pc, pos + 2, spare), row_or_spare(b, status, pc, pos + 3, spare));
 }
 __device__ __noinline__ int4 four_any_rows(const DevBatch &b, const Piece *pc, int pos) {
     return make_int4(max(0, any_row(b, pc->seq, pc->kv0, pos)), max(0, any_row(b, pc->seq, pc->kv0, pos + 1)),
@@ -501,24 +515,43 @@ __device__ __forceinline__ int plan_scan(int v, int &sum, int *sh) {
     return before;
 }
 
+// A cluster's first piece into the ring, by the one thread that knows its first
+// item: the other warps begin with it right away.
+__device__ __forceinline__ void begin(const MlaParams &p, Ctl &ctl, int cluster, PlanHead head, int item, int off, const Item &it) {
+    const int64_t total = head.total;
+    Todo todo{item, off, (int)(total * (cluster + 1) / head.clusters - total * cluster / head.clusters), 0};
+    Piece pc;
+    if (todo.take(it, pc)) {
+        ctl.piece[0] = pc;
+        mbar_arrive(smem_u32(&ctl.piece_full[0]));
+        ask_for_queries(p, pc);
+        todo.written = 1;
+    }
+    *reinterpret_cast<Todo *>(ctl.todo) = todo;
+}
 // The plan of a call with at most one item a sequence and no more sequences than
 // threads, made by every CTA for itself (a launch less: 4 us).
 __device__ __noinline__ void plan_here(const MlaParams &p, Ctl &ctl, int cluster) {
     const int seq = (int)threadIdx.x;
-    Item it{};
+    Item it;
     int cost = 0;
     if (seq < p.pr.b.B && item_of(p.pr, seq, p.status, it)) cost = item_cost(it.n);
     int total;
     const int before = plan_scan<kThreads>(cost, total, reinterpret_cast<int *>(&ctl.red[0][0][0][0]));
-    const int n = min((int)gridDim.x / 2, total);
-    if (seq == 0) ctl.head = PlanHead{total, n};
-    if (cluster < n) {
-        const int at = (int)((int64_t)total * cluster / n);
-        if (at >= before && at < before + cost) {
-            ctl.start = Start{seq, at - before};
-            ctl.first() = it;
-        }
+    const PlanHead head{total, min((int)gridDim.x / 2, total)};
+    if (seq == 0) ctl.head = head;
+    if (cluster < head.clusters) {
+        const int at = (int)((int64_t)total * cluster / head.clusters);
+        if (at >= before && at < before + cost) begin(p, ctl, cluster, head, seq, at - before, it);
     }
+}
+// The same from the plan kernel's, by one thread.
+__device__ __noinline__ void plan_read(const MlaParams &p, Ctl &ctl, int cluster) {
+    const PlanHead head = *p.head;
+    ctl.head = head;
+    if (cluster >= head.clusters) return;
+    const Start st = p.start[cluster];
+    begin(p, ctl, cluster, head, st.item, st.off, p.items[st.item]);
 }
 
 }  // namespace
@@ -550,6 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctl.s_full[i]), 1);
             mbar_init(smem_u32(&ctl.s_empty[i]), kSoftmaxWarps);          // a group's in both CTAs
         }
+        for (int i = 0; i < 4; ++i) ctl.todo[i] = 0;          // what a cluster without work has to do
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_u32(&ctl.piece_full[i]), 1);
             mbar_init(smem_u32(&ctl.piece_empty[i]), kSoftmaxWarps + 2 + (rank == 0 ? 2 : 0));
@@ -575,14 +609,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
     pdl_wait();
-    if (p.items) {
-        if (threadIdx.x == 0) {
-            ctl.head = *p.head;
-            ctl.start = p.start[cluster];                     // (written for clusters with work)
-        }
-    } else {
-        plan_here(p, ctl, cluster);
-    }
+    if (!p.items) plan_here(p, ctl, cluster);
+    else if (threadIdx.x == 0) plan_read(p, ctl, cluster);
     __syncthreads();
     const uint64_t limit = b.wait_ns;
     const int n_blocks = p.tail ? 9 : 8;
@@ -675,6 +703,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Piece *pc = rd.next(ctl, p.status, limit);
             if (!pc || pc->end) break;
             const int t1 = pc->t1, lo = pc->lo, hi = pc->hi, s_lo = pc->s_lo, s_hi = pc->s_hi;
+            int32_t spare = -1;                               // not looked up yet
             for (int i = pc->t0; alive && i < t1; ++i, ++g) {
                 const int pos = tile_pos(*pc, i), a = pos + 4 * lane;       // this lane's four keys
                 const uint32_t groups = tile_groups(*pc, pos);
@@ -685,12 +714,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     r.x = any_row(b, pc->seq, pc->kv0, pos + ((lane & 16) << 2));
                     if (r.x < 0) {
                         flag(p.status, DSA_DEV_BAD_INDEX);
-                        r.x = pc->spare;
+                        r.x = spare_row(b, pc);
                     }
                 } else {
+                    if (spare < 0) spare = spare_row(b, pc);
                     if (quads) {
                         // the four lie together: one lookup
-                        const int spare = pc->spare;
                         auto seen = [&](int q) { return (q >= lo && q <= hi) || (q >= s_lo && q < s_hi); };
                         const bool s0_ = seen(a), s1_ = seen(a + 1), s2_ = seen(a + 2), s3_ = seen(a + 3);
                         int row = 0;
@@ -701,7 +730,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         r.z = s2_ && row >= 0 ? row + 2 : spare;
                         r.w = s3_ && row >= 0 ? row + 3 : spare;
                     } else {
-                        r = four_rows(b, p.status, pc, a);
+                        r = four_rows(b, p.status, pc, a, spare);
                     }
                     // groups whose 16 rows are all seen and lie together
                     const int32_t group_row = __shfl_sync(0xffffffffu, r.x, lane & ~3);
@@ -752,9 +781,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // 150 clocks: while one issuer is at them the other's products run.
         // O's issuers, which wait for the first P of a piece, also write the pieces
         // down for all warps of their CTA, one ahead.
-        Scheduler sched(ctl.head, ctl.start, cluster);
+        Scheduler sched;
+        sched.todo = *reinterpret_cast<const Todo *>(ctl.todo);
         bool alive = true;
-        if (warp == kOWarp) alive = sched.write(p, ctl, lane);
+        if (warp == kOWarp && sched.todo.written == 0) alive = sched.write(p, ctl, lane);
         if (rank == 1) {
             while (warp == kOWarp && alive && !sched.end) alive = sched.write(p, ctl, lane);
         } else {
@@ -886,16 +916,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kQTmem; c += 2) {
-                uint32_t u[32], v[32];
+                uint32_t u[2][32];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < 16; ++e) {
                     const uint4 x = there ? __ldg(src + 8 * c + e) : make_uint4(0, 0, 0, 0);
-                    const uint4 y = there ? __ldg(src + 8 * c + 8 + e) : make_uint4(0, 0, 0, 0);
-                    u[4 * e] = x.x, u[4 * e + 1] = x.y, u[4 * e + 2] = x.z, u[4 * e + 3] = x.w;
-                    v[4 * e] = y.x, v[4 * e + 1] = y.y, v[4 * e + 2] = y.z, v[4 * e + 3] = y.w;
+                    u[e / 8][4 * (e % 8)] = x.x, u[e / 8][4 * (e % 8) + 1] = x.y, u[e / 8][4 * (e % 8) + 2] = x.z, u[e / 8][4 * (e % 8) + 3] = x.w;
                 }
-                tmem_st32(lane_tmem + kColQ + 32 * c, u);
-                tmem_st32(lane_tmem + kColQ + 32 * c + 32, v);
+                tmem_st32(lane_tmem + kColQ + 32 * c, u[0]);
+                tmem_st32(lane_tmem + kColQ + 32 * c + 32, u[1]);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -1086,7 +1114,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 l = (sums[0][0][r] + sums[0][1][r]) + (sums[1][0][r] + sums[1][1][r]);
             }
             const bool none = pos < 0 || l == 0.f;            // a sum of NaN is not none
-            if (alive) {
+            if (alive && row - lane < pc->nrows) {
                 // 64 bytes of each of the warp's 32 rows at a time, turned in the warp's
                 // share of P's buffer so that stores write whole sectors (a row a lane
                 // straight from the accumulator took 13,000 clocks).
@@ -1259,16 +1287,30 @@ __global__ void __launch_bounds__(kJoinThreads) mla_combine_kernel(const Split *
     if (blockIdx.y * kJoinRows<kBf16> >= s.nrows) return;     // 0 rows without a shared item
     const bool there = row < s.nrows;
     auto slot = [&](int k) { return ((int64_t)2 * (s.first + k) + (k == 0 ? 1 : 0)) * kRows + (there ? row : 0); };
+    uint4 v[kJoinLoads];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int q = 0; q < kJoinLoads; ++q)
+            if (k0 + q < s.parts)
+                v[q] = *(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(part_o) + slot(k0 + q) * (D_L * (kBf16 ? 2 : 4))) + tx);
+    };
+    load(0);                                                  // beside the statistics, not behind them
     // every warp of the row has all maxima and sums; one lets the others have the weights
     float M = -INFINITY, L = 0.f;
-    for (int k = lane; k < s.parts; k += 32) M = fmaxf(M, part_ml[slot(k) * 2]);
+    float2 ml[(kClusters + 31) / 32];
+#pragma unroll
+    for (int i = 0; i < (kClusters + 31) / 32; ++i) {
+        const int k = lane + 32 * i;
+        ml[i] = k < s.parts ? *reinterpret_cast<const float2 *>(part_ml + slot(k) * 2) : make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, ml[i].x);
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    for (int k = lane; k < s.parts; k += 32) {
-        const float2 ml = *reinterpret_cast<const float2 *>(part_ml + slot(k) * 2);
-        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        L += w * ml.y;
-        if (tx < 32) wgt[mine][k] = w;
+#pragma unroll
+    for (int i = 0; i < (kClusters + 31) / 32; ++i) {
+        const float w = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - M);
+        L += w * ml[i].y;
+        if (tx < 32 && lane + 32 * i < s.parts) wgt[mine][lane + 32 * i] = w;
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
@@ -1277,11 +1319,7 @@ __global__ void __launch_bounds__(kJoinThreads) mla_combine_kernel(const Split *
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
     for (int k0 = 0; k0 < s.parts; k0 += kJoinLoads) {
-        uint4 v[kJoinLoads];
-#pragma unroll
-        for (int q = 0; q < kJoinLoads; ++q)
-            if (k0 + q < s.parts)
-                v[q] = *(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(part_o) + slot(k0 + q) * (D_L * (kBf16 ? 2 : 4))) + tx);
+        if (k0) load(k0);
 #pragma unroll
         for (int q = 0; q < kJoinLoads; ++q) {
             if (k0 + q < s.parts) {

@@ -50,10 +50,13 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 template <typename T, int W> struct alignas(W * sizeof(T) >= 16 ? 16 : sizeof(T)) Unit { T v[W]; };
 
 template <typename T, int W, bool kAligned> __device__ __forceinline__ Unit<T, W> load_unit(const T *p) {
-    if constexpr (kAligned || W == 1) return *reinterpret_cast<const Unit<T, W> *>(p);
     Unit<T, W> u;
+    if constexpr (kAligned || W == 1) {
+        u = *reinterpret_cast<const Unit<T, W> *>(p);
+    } else {
 #pragma unroll
-    for (int e = 0; e < W; ++e) u.v[e] = p[e];
+        for (int e = 0; e < W; ++e) u.v[e] = p[e];
+    }
     return u;
 }
 template <typename T, int W, bool kAligned> __device__ __forceinline__ void store_unit(T *p, const Unit<T, W> &u) {
