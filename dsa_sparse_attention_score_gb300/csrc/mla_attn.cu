@@ -243,7 +243,11 @@ struct MlaParams {
     const Start *start;
     const uint16_t *q_lat;        // bf16 [T * H, 512]
     Split *split;                 // [clusters]
-    void *part_o;                 // [2 * clusters, 128, 512] of the output's type, unnormalised
+    // Parts of items, unnormalised: float32 [2 * clusters, 128, 512] with float32 outputs;
+    // with bf16 ones fp16, 32 dims of a row times a power of two (part_unit holds
+    // 1 over it): 11 bits, which the output's own 8 hide, at half the bytes.
+    void *part_o;
+    float *part_unit;             // [2 * clusters, 128, 16]
     float *part_ml;               // [2 * clusters, 128, 2]
     void *out;
     int out_bf16;
@@ -1137,10 +1141,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         uint32_t o[32];
                         tmem_ld32(o_tmem + c, o);
                         tmem_wait_ld(o);
+                        if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * factor, __uint_as_float(o[2 * e + 1]) * factor);
-                            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                            for (int e = 0; e < 16; ++e) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * factor, __uint_as_float(o[2 * e + 1]) * factor);
+                                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                        } else {
+                            float top = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(o[e])));
+                            const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+                            const float unit = __int_as_float((127 - ex) << 23);      // values below 2 after it
+                            if (mine) p.part_unit[part_row * 16 + ((col0 + c) >> 5)] = __int_as_float((127 + ex) << 23);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const __half2 h = __floats2half2_rn(__uint_as_float(o[2 * e]) * unit, __uint_as_float(o[2 * e + 1]) * unit);
+                                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
                         }
                     } else if (!empty) {
                         tmem_ld16(o_tmem + c, w);
@@ -1268,15 +1286,14 @@ __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const Problem p,
 
 // Joins the parts of an item that several clusters share: a row's 512 dims over as
 // many threads as there are 16-byte pieces, as many parts at a time as there are
-// loads in flight.  Parts have the output's type: bf16 parts are off by no more
-// than the output's own rounding, and halve what is written and read.
+// loads in flight.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinLoads = 8;
 template <bool kBf16> constexpr int kJoinRows = kBf16 ? kJoinThreads / 64 : kJoinThreads / 128;
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads) mla_combine_kernel(const Split *split, const void *part_o, const float *part_ml,
-                                                                   void *out, float *lse) {
+__global__ void __launch_bounds__(kJoinThreads) mla_combine_kernel(const Split *split, const void *part_o, const float *part_unit,
+                                                                   const float *part_ml, void *out, float *lse) {
     constexpr int kPer = kBf16 ? 8 : 4;                       // dims a thread
     constexpr int kRowThreads = D_L / kPer;
     __shared__ float wgt[kJoinRows<kBf16>][kClusters];
@@ -1288,7 +1305,11 @@ __global__ void __launch_bounds__(kJoinThreads) mla_combine_kernel(const Split *
     const bool there = row < s.nrows;
     auto slot = [&](int k) { return ((int64_t)2 * (s.first + k) + (k == 0 ? 1 : 0)) * kRows + (there ? row : 0); };
     uint4 v[kJoinLoads];
+    float unit[kJoinLoads];
     auto load = [&](int k0) {
+#pragma unroll
+        for (int q = 0; q < kJoinLoads; ++q)
+            if (k0 + q < s.parts) unit[q] = kBf16 ? part_unit[slot(k0 + q) * 16 + tx / 4] : 1.f;
 #pragma unroll
         for (int q = 0; q < kJoinLoads; ++q)
             if (k0 + q < s.parts)
@@ -1323,12 +1344,12 @@ __global__ void __launch_bounds__(kJoinThreads) mla_combine_kernel(const Split *
 #pragma unroll
         for (int q = 0; q < kJoinLoads; ++q) {
             if (k0 + q < s.parts) {
-                const float w = wgt[mine][k0 + q];
+                const float w = wgt[mine][k0 + q] * unit[q];
                 const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (kBf16) {
-                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e]));
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[e]));
                         acc[2 * e] += w * f.x;
                         acc[2 * e + 1] += w * f.y;
                     } else {
@@ -1360,7 +1381,7 @@ namespace {
 
 
 struct MlaLayout {
-    size_t head, start, split, ml, part, item0, items, total;
+    size_t head, start, split, ml, part, unit, item0, items, total;
     int64_t max_items;
 };
 MlaLayout mla_layout(int64_t T, int64_t B, int64_t H, size_t off) {
@@ -1376,6 +1397,7 @@ MlaLayout mla_layout(int64_t T, int64_t B, int64_t H, size_t off) {
     L.split = take(kClusters * sizeof(Split));
     L.ml = take((size_t)2 * kClusters * kRows * 2 * sizeof(float));
     L.part = take((size_t)2 * kClusters * kRows * D_L * sizeof(float));
+    L.unit = take((size_t)2 * kClusters * kRows * 16 * sizeof(float));
     L.item0 = take((size_t)B * sizeof(int32_t));
     L.items = take((size_t)L.max_items * sizeof(Item));
     L.total = off;
@@ -1409,6 +1431,7 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     p.start = start;
     p.split = reinterpret_cast<Split *>(w + L.split);
     p.part_o = w + L.part;
+    p.part_unit = reinterpret_cast<float *>(w + L.unit);
     p.part_ml = reinterpret_cast<float *>(w + L.ml);
     p.out = a.out;
     p.out_bf16 = a.out_bf16;
@@ -1426,8 +1449,8 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     if (e != cudaSuccess) return e;
     const int rows = a.out_bf16 ? kJoinRows<true> : kJoinRows<false>;
     return launch_k(a.out_bf16 ? mla_combine_kernel<true> : mla_combine_kernel<false>, dim3(kClusters, kRows / rows),
-                    dim3(kJoinThreads), 0, stream, true, (const Split *)p.split, (const void *)p.part_o, (const float *)p.part_ml,
-                    a.out, a.lse);
+                    dim3(kJoinThreads), 0, stream, true, (const Split *)p.split, (const void *)p.part_o, (const float *)p.part_unit,
+                    (const float *)p.part_ml,                    a.out, a.lse);
 }
 
 }  // namespace dsa

@@ -64,7 +64,7 @@ def test_attention_workspace(L):
     assert size()[0] == dsa.DSA_OK and size()[1] % 256 == 0
     assert size(H=129)[0] == UNSUPPORTED
     # parts of 152 pieces of 128 rows in float32, and what the plan needs
-    parts = 2 * 76 * 128 * (512 + 2) * 4
+    parts = 2 * 76 * 128 * (512 + 16 + 2) * 4
     assert parts < size()[1] < parts + (1 << 16)
     assert size(total_q=4096, max_q_per_seq=4096)[1] < parts + (1 << 20)
     assert size(max_kv=1 << 20)[1] == size()[1]          # independent of the context
