@@ -457,29 +457,16 @@ __device__ __noinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int 
     return true;
 }
 
-// Copies of rows that do not lie together 64 at a time, out of the usual path:
-// copies / block pieces of the keys (c = lane, lane + 32...; each lane's rows are
-// those of its piece of every block), and the values' groups that some row sees.
-__device__ __noinline__ void copy_keys(uint32_t dst, const CUtensorMap *kv16, const CUtensorMap *kv1, uint32_t full, int kb0, int n,
-                                       int copies, int4 r, int lane) {
+// Copies of rows that do not lie together, out of the usual path: four keys a lane
+// of n blocks (lanes 0..15 and 16..31 of alternate ones), and four rows of values.
+__device__ __noinline__ void copy_keys(uint32_t dst, const CUtensorMap *kv1, uint32_t full, int kb0, int n, int4 r, int lane) {
 #pragma unroll 1
-    for (int c = lane; c < n * copies; c += 32) {             // copies divides 32
-        const int kb = kb0 + c / copies;
-        if (copies == 4) tma2_load(dst + kb * kBlock, kv16, full, kb * 64, r.x);
-        else tma2_gather4(dst + kb * kBlock, kv1, full, kb * 64, r);
-    }
+    for (int c = lane; c < n * 16; c += 32) tma2_gather4(dst + (kb0 + c / 16) * kBlock, kv1, full, (kb0 + c / 16) * 64, r);
     __syncwarp();
 }
-__device__ __noinline__ void copy_values(uint32_t dst, const CUtensorMap *kv64, const CUtensorMap *kv16, const CUtensorMap *kv1,
-                                         uint32_t full, int col, int4 r, int box, int lane) {
+__device__ __noinline__ void copy_values(uint32_t dst, const CUtensorMap *kv1, uint32_t full, int col, int4 r) {
 #pragma unroll 1
-    for (int d = 0; d < 4; ++d) {
-        if (box) {
-            if ((lane & (box - 1)) == 0) tma2_load(dst + d * kBlock, box == 16 ? kv64 : kv16, full, col + 64 * d, r.x);
-        } else {
-            tma2_gather4(dst + d * kBlock, kv1, full, col + 64 * d, r);
-        }
-    }
+    for (int d = 0; d < 4; ++d) tma2_gather4(dst + d * kBlock, kv1, full, col + 64 * d, r);
 }
 // The rows of the four keys from `pos` on.
 __device__ __noinline__ int4 four_rows(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
@@ -645,7 +632,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (p.rows_per_box) r.x = max(0, any_row(b, seq, kv0, a));
                 else r = four_any_rows(b, pc, a);
                 const uint32_t dst = s0 + kKOff + mine * step * 128;
-                const int row = __reduce_max_sync(0xffffffffu, r.x);        // one box: the same in every lane
+                // the boxes' rows in uniform registers: issued by one lane from there a copy takes
+                // 12 clocks, by several lanes from their own registers 130 each
+                int row[4];
+                if (copies <= 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) row[j] = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.x, j));
+                }
 #pragma unroll 1
                 for (int q = 0; q < 3; ++q) {
                     const int nb = min(3, n_blocks - 3 * q);
@@ -676,14 +669,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             arrive_expect_remote(full, (uint32_t)(nb * kBlock));
 #pragma unroll
                             for (int c = 0; c < 3; ++c)
-                                if (c < nb) tma2_load(s0 + kKOff + (3 * q + c) * kBlock, &kv64_map, full, (3 * q + c) * 64, row);
+                                if (c < nb) tma2_load(s0 + kKOff + (3 * q + c) * kBlock, &kv64_map, full, (3 * q + c) * 64, row[0]);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                    if (p.rows_per_box == 16) {
+                        if (elect_one()) {
+                            arrive_expect_remote(full, (uint32_t)(nb * kBlock));
+#pragma unroll 1
+                            for (int c = 3 * q; c < 3 * q + nb; ++c)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    tma2_load(s0 + kKOff + c * kBlock + j * 2048, &kv16_map, full, c * 64, row[j]);
                         }
                         __syncwarp();
                         continue;
                     }
                     if (lane == 0) arrive_expect_remote(full, (uint32_t)(nb * kBlock));
                     __syncwarp();
-                    copy_keys(dst, &kv16_map, &kv1_map, full, 3 * q, nb, copies, r, lane);
+                    copy_keys(dst, &kv1_map, full, 3 * q, nb, r, lane);
                 }
             }
             rd.done(ctl, lane);
@@ -713,13 +718,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t groups = tile_groups(*pc, pos);
                 int4 r;
                 bool box16 = true, box64 = true;
-                const bool simple = p.rows_per_box == 64 && pos >= lo && pos + kKeys - 1 <= hi;   // all seen
+                // every key seen, in boxes of 64 or 16: lane j looks box j up
+                const bool simple = p.rows_per_box && pos >= lo && pos + kKeys - 1 <= hi;
                 if (simple) {
-                    r.x = any_row(b, pc->seq, pc->kv0, pos + ((lane & 16) << 2));
+                    r.x = any_row(b, pc->seq, pc->kv0, pos + (p.rows_per_box == 64 ? (lane & 1) * 64 : (lane & 7) * 16));
                     if (r.x < 0) {
                         flag(p.status, DSA_DEV_BAD_INDEX);
                         r.x = spare_row(b, pc);
                     }
+                    box64 = p.rows_per_box == 64;
                 } else {
                     if (spare < 0) spare = spare_row(b, pc);
                     if (quads) {
@@ -747,8 +754,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 const bool on = (groups >> (lane >> 2)) & 1u;
                 const bool boxes = __all_sync(0xffffffffu, box64);          // two of 64 rows
-                const int row0 = __reduce_min_sync(0xffffffffu, lane < 16 ? r.x : INT32_MAX);
-                const int row1 = __reduce_min_sync(0xffffffffu, lane < 16 ? INT32_MAX : r.x);
+                // otherwise by groups: those that are one box, and the others by fours of rows
+                const uint32_t grouped = __ballot_sync(0xffffffffu, box16 && on);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t n = 2 * g + h;                           // halves so far
@@ -759,21 +766,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (b.skip_copies) continue;
                     if (boxes) {
                         // the half's four blocks of this CTA's dims
+                        const int row = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.x, simple ? h : 16 * h));
                         if (elect_one()) {
                             arrive_expect_remote(full, kVHalf);
 #pragma unroll
                             for (int d = 0; d < 4; ++d)
-                                tma2_load(at + d * kBlock, &kv64_map, full, 256 * (int)rank + 64 * d, h ? row1 : row0);
+                                tma2_load(at + d * kBlock, &kv64_map, full, 256 * (int)rank + 64 * d, row);
                         }
                         __syncwarp();
                         continue;
                     }
-                    if (lane == 0) arrive_expect_remote(full, (uint32_t)__popc((groups >> (4 * h)) & 0xfu) * (kGroup * 128u) * 4u);
-                    __syncwarp();
-                    if ((lane >> 4) == h && on) {
-                        const uint32_t dst = at + (lane & 15) * 4 * 128;
-                        copy_values(dst, &kv64_map, &kv16_map, &kv1_map, full, 256 * (int)rank, r, box64 ? 16 : box16 ? 4 : 0, lane);
+                    int row[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        row[j] = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.x, simple ? 4 * h + j : 16 * h + 4 * j));
+                    const uint32_t mine = __reduce_or_sync(0xffffffffu, grouped >> (16 * h));
+                    if (elect_one()) {
+                        arrive_expect_remote(full, (uint32_t)__popc((groups >> (4 * h)) & 0xfu) * (kGroup * 128u) * 4u);
+#pragma unroll 1
+                        for (int d = 0; d < 4; ++d)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (mine >> (4 * j) & 1u)
+                                    tma2_load(at + d * kBlock + j * 2048, &kv16_map, full, 256 * (int)rank + 64 * d, row[j]);
                     }
+                    __syncwarp();
+                    if ((lane >> 4) == h && on && !box16)
+                        copy_values(at + (lane & 15) * 4 * 128, &kv1_map, full, 256 * (int)rank, r);
                     __syncwarp();
                 }
             }
