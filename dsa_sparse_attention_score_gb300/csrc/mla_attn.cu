@@ -224,15 +224,12 @@ __device__ __forceinline__ bool seen_by_some(const Piece &it, int pos) {
     return (pos >= it.lo && pos <= it.hi) || (pos >= it.s_lo && pos < it.s_hi);
 }
 // The tile's groups of 16 keys with a position that some row sees, one bit each.
+__device__ __forceinline__ uint32_t groups_of(int lo, int hi) {   // from the tile's first key on, both included
+    const int g0 = max(lo, 0) / kGroup, g1 = min(hi, kKeys - 1) / kGroup;
+    return hi < 0 || g0 > g1 ? 0u : (0xffu << g0) & (0xffu >> (kKeys / kGroup - 1 - g1));
+}
 __device__ __forceinline__ uint32_t tile_groups(const Piece &it, int p0) {
-    if (p0 >= it.lo && p0 + kKeys - 1 <= it.hi) return 0xffu;
-    uint32_t m = 0;
-#pragma unroll 1
-    for (int g = 0; g < kKeys / kGroup; ++g) {
-        const int a = p0 + g * kGroup, e = a + kGroup - 1;
-        if ((e >= it.lo && a <= it.hi) || (e >= it.s_lo && a < it.s_hi)) m |= 1u << g;
-    }
-    return m;
+    return groups_of(it.lo - p0, it.hi - p0) | groups_of(it.s_lo - p0, it.s_hi - 1 - p0);
 }
 
 struct MlaParams {
@@ -408,11 +405,11 @@ __device__ __forceinline__ void ask_for_queries(const MlaParams &p, const Piece 
 struct Scheduler {
     Todo todo;
     bool end = false;
-    __device__ __noinline__ bool write(const MlaParams &p, Ctl &ctl, int lane);
+    __device__ __forceinline__ bool write(const MlaParams &p, Ctl &ctl, int lane);
 };
 
 // That of a position that some row of the piece sees, its spare one for any other.
-__device__ __noinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
+__device__ __forceinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
     if (!seen_by_some(*pc, pos)) return spare;
     const int32_t r = any_row(b, pc->seq, pc->kv0, pos);
     if (r >= 0) return r;
@@ -425,7 +422,7 @@ __device__ __forceinline__ int32_t spare_row(const DevBatch &b, const Piece *pc)
     return pc->hi < 0 || pc->kv0 < 0 ? 0 : max(0, any_row(b, pc->seq, pc->kv0, pc->hi));
 }
 
-__device__ __noinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int lane) {
+__device__ __forceinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int lane) {
     while (!end) {
         end = todo.left <= 0;
         Piece pc{};
@@ -464,16 +461,29 @@ __device__ __noinline__ void copy_keys(uint32_t dst, const CUtensorMap *kv1, uin
     for (int c = lane; c < n * 16; c += 32) tma2_gather4(dst + (kb0 + c / 16) * kBlock, kv1, full, (kb0 + c / 16) * 64, r);
     __syncwarp();
 }
-__device__ __noinline__ void copy_values(uint32_t dst, const CUtensorMap *kv1, uint32_t full, int col, int4 r) {
+// A group's 16 rows of values, four of them in each of the lanes from `lane0` on; one
+// lane issues the copies from uniform registers (a lane's own take 130 clocks each, not 12).
+__device__ __noinline__ void copy_values(uint32_t dst, const CUtensorMap *kv1, uint32_t full, int col, int4 r, int lane0) {
 #pragma unroll 1
-    for (int d = 0; d < 4; ++d) tma2_gather4(dst + d * kBlock, kv1, full, col + 64 * d, r);
+    for (int m = 0; m < 4; ++m) {
+        int4 u;
+        u.x = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.x, lane0 + m));
+        u.y = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.y, lane0 + m));
+        u.z = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.z, lane0 + m));
+        u.w = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.w, lane0 + m));
+        if (elect_one()) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) tma2_gather4(dst + m * 512 + d * kBlock, kv1, full, col + 64 * d, u);
+        }
+        __syncwarp();
+    }
 }
 // The rows of the four keys from `pos` on.
-__device__ __noinline__ int4 four_rows(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
+__device__ __forceinline__ int4 four_rows(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
     return make_int4(row_or_spare(b, status, pc, pos, spare), row_or_spare(b, status, pc, pos + 1, spare),
                      row_or_spare(b, status, pc, pos + 2, spare), row_or_spare(b, status, pc, pos + 3, spare));
 }
-__device__ __noinline__ int4 four_any_rows(const DevBatch &b, const Piece *pc, int pos) {
+__device__ __forceinline__ int4 four_any_rows(const DevBatch &b, const Piece *pc, int pos) {
     return make_int4(max(0, any_row(b, pc->seq, pc->kv0, pos)), max(0, any_row(b, pc->seq, pc->kv0, pos + 1)),
                      max(0, any_row(b, pc->seq, pc->kv0, pos + 2)), max(0, any_row(b, pc->seq, pc->kv0, pos + 3)));
 }
@@ -522,7 +532,7 @@ __device__ __forceinline__ void begin(const MlaParams &p, Ctl &ctl, int cluster,
 }
 // The plan of a call with at most one item a sequence and no more sequences than
 // threads, made by every CTA for itself (a launch less: 4 us).
-__device__ __noinline__ void plan_here(const MlaParams &p, Ctl &ctl, int cluster) {
+__device__ __forceinline__ void plan_here(const MlaParams &p, Ctl &ctl, int cluster) {
     const int seq = (int)threadIdx.x;
     Item it;
     int cost = 0;
@@ -537,7 +547,7 @@ __device__ __noinline__ void plan_here(const MlaParams &p, Ctl &ctl, int cluster
     }
 }
 // The same from the plan kernel's, by one thread.
-__device__ __noinline__ void plan_read(const MlaParams &p, Ctl &ctl, int cluster) {
+__device__ __forceinline__ void plan_read(const MlaParams &p, Ctl &ctl, int cluster) {
     const PlanHead head = *p.head;
     ctl.head = head;
     if (cluster >= head.clusters) return;
@@ -705,7 +715,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (P is 0 there, and 0 times what an unused row may hold is not).
         uint32_t g = 0, buf = 0;                              // tiles so far, the next half's place
         bool alive = true;
-        const bool quads = !b.block_table || b.block_size % 4 == 0;
         const uint32_t v_bar = dsmem_map(smem_u32(&ctl.v_full[0]), 0);
         Reader rd;
         while (alive) {
@@ -714,48 +723,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int t1 = pc->t1, lo = pc->lo, hi = pc->hi, s_lo = pc->s_lo, s_hi = pc->s_hi;
             int32_t spare = -1;                               // not looked up yet
             for (int i = pc->t0; alive && i < t1; ++i, ++g) {
-                const int pos = tile_pos(*pc, i), a = pos + 4 * lane;       // this lane's four keys
+                const int pos = tile_pos(*pc, i);
                 const uint32_t groups = tile_groups(*pc, pos);
-                int4 r;
-                bool box16 = true, box64 = true;
-                // every key seen, in boxes of 64 or 16: lane j looks box j up
-                const bool simple = p.rows_per_box && pos >= lo && pos + kKeys - 1 <= hi;
-                if (simple) {
-                    r.x = any_row(b, pc->seq, pc->kv0, pos + (p.rows_per_box == 64 ? (lane & 1) * 64 : (lane & 7) * 16));
-                    if (r.x < 0) {
-                        flag(p.status, DSA_DEV_BAD_INDEX);
-                        r.x = spare_row(b, pc);
+                // where a group's 16 rows lie together, lane j looks group j up; one that is
+                // seen in full is a box
+                int32_t first = -1;
+                uint32_t ones = 0;
+                if (p.rows_per_box) {
+                    const int a = pos + kGroup * (lane & 7), e = a + kGroup - 1;
+                    if (groups >> (lane & 7) & 1u) {
+                        first = any_row(b, pc->seq, pc->kv0, a);
+                        if (first < 0) flag(p.status, DSA_DEV_BAD_INDEX);
                     }
-                    box64 = p.rows_per_box == 64;
-                } else {
+                    ones = __ballot_sync(0xffffffffu, first >= 0 && ((a >= lo && e <= hi) || (a >= s_lo && e < s_hi))) & 0xffu;
+                }
+                // the other groups' rows, four a lane
+                int4 r = make_int4(0, 0, 0, 0);
+                if (groups & ~ones) {
                     if (spare < 0) spare = spare_row(b, pc);
-                    if (quads) {
-                        // the four lie together: one lookup
-                        auto seen = [&](int q) { return (q >= lo && q <= hi) || (q >= s_lo && q < s_hi); };
-                        const bool s0_ = seen(a), s1_ = seen(a + 1), s2_ = seen(a + 2), s3_ = seen(a + 3);
-                        int row = 0;
-                        if (s0_ || s1_ || s2_ || s3_) row = any_row(b, pc->seq, pc->kv0, a);
-                        if (row < 0) flag(p.status, DSA_DEV_BAD_INDEX);
-                        r.x = s0_ && row >= 0 ? row : spare;
-                        r.y = s1_ && row >= 0 ? row + 1 : spare;
-                        r.z = s2_ && row >= 0 ? row + 2 : spare;
-                        r.w = s3_ && row >= 0 ? row + 3 : spare;
+                    const int a = pos + 4 * lane;
+                    if (p.rows_per_box) {
+                        const int32_t row = __shfl_sync(0xffffffffu, first, lane >> 2), at = row + 4 * (lane & 3);
+                        r.x = row >= 0 && seen_by_some(*pc, a) ? at : spare;
+                        r.y = row >= 0 && seen_by_some(*pc, a + 1) ? at + 1 : spare;
+                        r.z = row >= 0 && seen_by_some(*pc, a + 2) ? at + 2 : spare;
+                        r.w = row >= 0 && seen_by_some(*pc, a + 3) ? at + 3 : spare;
                     } else {
                         r = four_rows(b, p.status, pc, a, spare);
                     }
-                    // groups whose 16 rows are all seen and lie together
-                    const int32_t group_row = __shfl_sync(0xffffffffu, r.x, lane & ~3);
-                    const bool run = r.y == r.x + 1 && r.z == r.x + 2 && r.w == r.x + 3 && r.x == group_row + 4 * (lane & 3);
-                    const uint32_t runs = __ballot_sync(0xffffffffu, run);
-                    box16 = ((runs >> (lane & ~3)) & 0xfu) == 0xfu;
-                    const int32_t half_row = __shfl_sync(0xffffffffu, r.x, lane & 16);
-                    const uint32_t halves = __ballot_sync(0xffffffffu, box16 && r.x == half_row + 4 * (lane & 15));
-                    box64 = ((halves >> (lane & 16)) & 0xffffu) == 0xffffu;
                 }
-                const bool on = (groups >> (lane >> 2)) & 1u;
-                const bool boxes = __all_sync(0xffffffffu, box64);          // two of 64 rows
-                // otherwise by groups: those that are one box, and the others by fours of rows
-                const uint32_t grouped = __ballot_sync(0xffffffffu, box16 && on);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t n = 2 * g + h;                           // halves so far
@@ -764,36 +760,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint32_t at = s0 + kVOff + buf * kVHalf, full = v_bar + buf * 8;
                     buf = buf + 1 == kVBufs ? 0 : buf + 1;
                     if (b.skip_copies) continue;
-                    if (boxes) {
+                    const uint32_t mine = __reduce_or_sync(0xffffffffu, ones >> (4 * h) & 0xfu);
+                    int row[4];
+                    row[0] = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, first, 4 * h));
+                    if (p.rows_per_box == 64 && mine == 0xfu) {
                         // the half's four blocks of this CTA's dims
-                        const int row = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.x, simple ? h : 16 * h));
                         if (elect_one()) {
                             arrive_expect_remote(full, kVHalf);
 #pragma unroll
                             for (int d = 0; d < 4; ++d)
-                                tma2_load(at + d * kBlock, &kv64_map, full, 256 * (int)rank + 64 * d, row);
+                                tma2_load(at + d * kBlock, &kv64_map, full, 256 * (int)rank + 64 * d, row[0]);
                         }
                         __syncwarp();
                         continue;
                     }
-                    int row[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        row[j] = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, r.x, simple ? 4 * h + j : 16 * h + 4 * j));
-                    const uint32_t mine = __reduce_or_sync(0xffffffffu, grouped >> (16 * h));
+                    for (int j = 1; j < 4; ++j) row[j] = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, first, 4 * h + j));
                     if (elect_one()) {
                         arrive_expect_remote(full, (uint32_t)__popc((groups >> (4 * h)) & 0xfu) * (kGroup * 128u) * 4u);
 #pragma unroll 1
                         for (int d = 0; d < 4; ++d)
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                if (mine >> (4 * j) & 1u)
+                                if (mine >> j & 1u)
                                     tma2_load(at + d * kBlock + j * 2048, &kv16_map, full, 256 * (int)rank + 64 * d, row[j]);
                     }
                     __syncwarp();
-                    if ((lane >> 4) == h && on && !box16)
-                        copy_values(at + (lane & 15) * 4 * 128, &kv1_map, full, 256 * (int)rank, r);
-                    __syncwarp();
+                    for (uint32_t rest = (groups & ~ones) >> (4 * h) & 0xfu; rest; rest &= rest - 1)
+                        copy_values(at + (__ffs(rest) - 1) * 2048, &kv1_map, full, 256 * (int)rank, r, 16 * h + 4 * (__ffs(rest) - 1));
                 }
             }
             rd.done(ctl, lane);
@@ -807,7 +801,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Scheduler sched;
         sched.todo = *reinterpret_cast<const Todo *>(ctl.todo);
         bool alive = true;
-        if (warp == kOWarp && sched.todo.written == 0) alive = sched.write(p, ctl, lane);
         if (rank == 1) {
             while (warp == kOWarp && alive && !sched.end) alive = sched.write(p, ctl, lane);
         } else {
@@ -815,7 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t buf = 0, v_parity = 0;                   // the next half of a tile's values
             Reader rd;
             while (alive) {
-                if (warp == kOWarp) alive = sched.write(p, ctl, lane);
+                while (warp == kOWarp && alive && !sched.end && sched.todo.written < (int)rd.n + 2) alive = sched.write(p, ctl, lane);
                 if (!alive) break;
                 const Piece *pc = rd.next(ctl, p.status, limit);
                 if (!pc) break;
