@@ -87,6 +87,19 @@ __device__ __forceinline__ void umma2_f16_ts(uint32_t d, uint32_t a, uint64_t b,
         "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
+// 64 columns of 16 lanes: thread t holds columns 8 j + 2 (t % 4) and the next one of
+// lane t / 4 in u[4 j], u[4 j + 1] and of lane t / 4 + 8 in u[4 j + 2], u[4 j + 3].
+__device__ __forceinline__ void tmem_st_16x256_x8(uint32_t taddr, const uint32_t (&u)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+        "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
+        "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]),
+        "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+        : "memory");
+}
 // One arrival at the same barrier of both CTAs once the MMAs issued so far are done.
 __device__ __forceinline__ void commit2(uint32_t bar) {
     asm volatile(
@@ -926,20 +939,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!wait_bar(smem_u32(&ctl.piece_full[n % kPieces]), (n / kPieces) & 1u, ctl, p.status, limit)) return;
             const Piece *pc = &ctl.piece[n % kPieces];
             if (pc->end || pc->t0 == pc->t1) return;
-            const int64_t row = (int64_t)pc->row0 + kHalf * (int)rank + r;
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.q_lat + row * D_L);
-            const bool there = row < (int64_t)b.T * p.pr.H;
+            // four threads a row: 32 bytes of eight rows a load (a row a thread, 16 bytes
+            // each, kept the load unit busy for 4900 clocks)
+            const int64_t row = (int64_t)pc->row0 + kHalf * (int)rank + (warp & 1) * 32 + (lane >> 2);
+            const int64_t rows = (int64_t)b.T * p.pr.H;
+            const uint2 *src = reinterpret_cast<const uint2 *>(p.q_lat + row * D_L) + (lane & 3);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kQTmem; c += 2) {
-                uint32_t u[2][32];
+            for (int c = 0; c < 128; c += 64) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint4 x = there ? __ldg(src + 8 * c + e) : make_uint4(0, 0, 0, 0);
-                    u[e / 8][4 * (e % 8)] = x.x, u[e / 8][4 * (e % 8) + 1] = x.y, u[e / 8][4 * (e % 8) + 2] = x.z, u[e / 8][4 * (e % 8) + 3] = x.w;
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t u[32];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int of = 16 * k + 8 * (e & 1);
+                        const uint2 x = row + of < rows ? __ldg(src + of * (D_L / 4) + c / 2 + 4 * (e >> 1)) : make_uint2(0, 0);
+                        u[2 * e] = x.x, u[2 * e + 1] = x.y;
+                    }
+                    tmem_st_16x256_x8(lane_tmem + ((uint32_t)(16 * k) << 16) + kColQ + c, u);
                 }
-                tmem_st32(lane_tmem + kColQ + 32 * c, u[0]);
-                tmem_st32(lane_tmem + kColQ + 32 * c + 32, u[1]);
             }
             tmem_wait_st();
             tc_fence_before();
