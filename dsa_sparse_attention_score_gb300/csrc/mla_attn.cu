@@ -935,7 +935,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // The first 256 dims of the queries of piece n, by one group: row r into lanes r
         // and r + 64.  The products that read the piece before's are done.
         const uint32_t q_bar = dsmem_map(smem_u32(&ctl.q_tmem), 0);
-        auto load_queries = [&](uint32_t n) {
+        auto load_queries = [&](uint32_t n, bool empty) {
             if (!wait_bar(smem_u32(&ctl.piece_full[n % kPieces]), (n / kPieces) & 1u, ctl, p.status, limit)) return;
             const Piece *pc = &ctl.piece[n % kPieces];
             if (pc->end || pc->t0 == pc->t1) return;
@@ -944,20 +944,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t row = (int64_t)pc->row0 + kHalf * (int)rank + (warp & 1) * 32 + (lane >> 2);
             const int64_t rows = (int64_t)b.T * p.pr.H;
             const uint2 *src = reinterpret_cast<const uint2 *>(p.q_lat + row * D_L) + (lane & 3);
-            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 128; c += 64) {
+                uint32_t u[2][32];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t u[32];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int of = 16 * k + 8 * (e & 1);
-                        const uint2 x = row + of < rows ? __ldg(src + of * (D_L / 4) + c / 2 + 4 * (e >> 1)) : make_uint2(0, 0);
-                        u[2 * e] = x.x, u[2 * e + 1] = x.y;
-                    }
-                    tmem_st_16x256_x8(lane_tmem + ((uint32_t)(16 * k) << 16) + kColQ + c, u);
+                for (int e = 0; e < 32; ++e) {
+                    const int of = 8 * (e >> 3);              // rows of lane, lane + 8, + 16 and + 24
+                    const uint2 x = row + of < rows ? __ldg(src + of * (D_L / 4) + c / 2 + 4 * (e & 7)) : make_uint2(0, 0);
+                    const int at = 4 * (e & 7) + 2 * (e >> 3 & 1);
+                    u[e >> 4][at] = x.x, u[e >> 4][at + 1] = x.y;
                 }
+                if (c == 0) {
+                    // the loads are under way: now the scores of the last tile have to be there
+                    if (!empty && !wait_bar(smem_u32(&ctl.s_full[(g - 1) & 1u]), ((g - 1) >> 1) & 1u, ctl, p.status, limit)) return;
+                    tc_fence_after();
+                }
+                tmem_st_16x256_x8(lane_tmem + kColQ + c, u[0]);
+                tmem_st_16x256_x8(lane_tmem + (16u << 16) + kColQ + c, u[1]);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -975,28 +978,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             return pos;
         };
-        if (group == 1) load_queries(0);
+        if (group == 1) load_queries(0, true);
         int pos = -1, next_pos = -1;
         bool known = false;                                   // next_pos is the next piece's
+        // A piece's output waits for its last products: until those are done it is
+        // owed, and the next piece is looked up.
+        const Piece *owed = nullptr;
+        float m_owed = 0.f, l_owed = 0.f;                     // as m and l below
+        int pos_owed = -1;
         while (true) {
             const Piece *pc = rd.next(ctl, p.status, limit);
-            // (all of them: their staging of the last output ends before any stores a P)
             if (named_barrier_or(7, kSoftmaxWarps * 32, !pc)) break;
-            if (pc->end) break;
+            if (pc->end && !owed) break;
             const int t0 = pc->t0, t1 = pc->t1, n_first = pc->n_first;
-            const int row = kHalf * (int)rank + r;
-            const bool mine = row < pc->nrows;
-            pos = known ? next_pos : row_pos(pc);
+            if (!pc->end) pos = known ? next_pos : row_pos(pc);
             // Every row of the item sees every key of the tiles [clear0, clear1).
             const int64_t open = (int64_t)pc->hi - p.pr.window + 1;      // the last token's window begins here
             const int clear0 = n_first + (open <= 0 ? 0 : (int)((open + kKeys - 1) / kKeys)) - pc->tile0;
             const int clear1 = plain ? n_first + (pc->min_pos + 1) / kKeys - pc->tile0 : 0;
             float m = -INFINITY, l = 0.f;                     // m: as of this group's last tile
-            for (int i = t0; i < t1; ++i, ++g) {
-                if ((int)(g & 1u) != group) continue;
+            const uint32_t g0 = g;                            // of the piece's first tile
+            if (owed) {
+                // ---- the output of the piece before
+                const bool empty = owed->t1 == owed->t0;
+                const int row = kHalf * (int)rank + r;
+                const bool mine = row < owed->nrows;
+                if (!empty) {
+                    // its last tile was g0 - 1.  That tile's group has not been at another
+                    // since, and the maxima of its tile before are not wanted any more.
+                    const int last = (int)((g0 - 1) & 1u);
+                    if (alive) alive = wait_o(1, g0 - 1);
+                    tc_fence_after();
+                    float *const m_last = ctl.red[last][(((g0 - 1) >> 1) & 1u) ^ 1u][0];
+                    if (last == group && half == 0) m_last[r] = m_owed;
+                    named_barrier(7, kSoftmaxWarps * 32);
+                    const float mn = m_last[r];
+                    auto &sums = ctl.red[last ^ 1];               // read by all of its group
+                    sums[group][half][r] = m_owed == -INFINITY ? 0.f : l_owed * ex2(m_owed - mn);
+                    m_owed = mn;
+                    named_barrier(7, kSoftmaxWarps * 32);
+                    l_owed = (sums[0][0][r] + sums[0][1][r]) + (sums[1][0][r] + sums[1][1][r]);
+                }
+                const bool none = pos_owed < 0 || l_owed == 0.f;  // a sum of NaN is not none
+                if (alive && row - lane < owed->nrows) {
+                    // 64 bytes of each of the warp's 32 rows at a time, turned in the warp's
+                    // share of P's buffer so that stores write whole sectors (a row a lane
+                    // straight from the accumulator took 13,000 clocks).
+                    // A part goes to slot 2c where the item began in an earlier cluster, else to 2c + 1.
+                    const bool whole = owed->whole, narrow = p.out_bf16;
+                    const int64_t out_row = (int64_t)owed->row0 + row;
+                    const int64_t part_row = ((int64_t)2 * cluster + (owed->t0 == 0 ? 1 : 0)) * kRows + row;
+                    const float factor = whole ? 1.f / l_owed : 1.f;
+                    const int col0 = 256 * half + 128 * group, bytes = narrow ? 2 : 4;
+                    const int rows_left = owed->nrows - (row - lane);            // of the warp's 32
+                    uint8_t *stage = smem + kPOff + warp * 2048;
+                    uint8_t *dst = static_cast<uint8_t *>(whole ? p.out : p.part_o) +
+                                   (((whole ? out_row : part_row) - lane + (lane >> 2)) * D_L + col0) * bytes + 16 * (lane & 3);
+                    const uint32_t o_tmem = lane_tmem + kColO + 128 * group;
+                    const int step = 64 / bytes;
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += step) {
+                        uint32_t w[16];
+                        if (narrow && !empty) {
+                            uint32_t o[32];
+                            tmem_ld32(o_tmem + c, o);
+                            tmem_wait_ld(o);
+                            if (whole) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * factor, __uint_as_float(o[2 * e + 1]) * factor);
+                                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                                }
+                            } else {
+                                float top = 0.f;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(o[e])));
+                                const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+                                const float unit = __int_as_float((127 - ex) << 23);      // values below 2 after it
+                                if (mine) p.part_unit[part_row * 16 + ((col0 + c) >> 5)] = __int_as_float((127 + ex) << 23);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const __half2 h = __floats2half2_rn(__uint_as_float(o[2 * e]) * unit, __uint_as_float(o[2 * e + 1]) * unit);
+                                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                                }
+                            }
+                        } else if (!empty) {
+                            tmem_ld16(o_tmem + c, w);
+                            tmem_wait_ld(w);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * factor);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<uint4 *>(stage + sw64_offset((uint32_t)lane, (uint32_t)q)) =
+                                none ? make_uint4(0, 0, 0, 0) : make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                        __syncwarp();
+                        uint4 v[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            v[q] = *reinterpret_cast<const uint4 *>(stage + sw64_offset((uint32_t)(8 * q + (lane >> 2)), (uint32_t)(lane & 3)));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (8 * q + (lane >> 2) < rows_left) *reinterpret_cast<uint4 *>(dst + (int64_t)(8 * q) * D_L * bytes + c * bytes) = v[q];
+                        __syncwarp();
+                    }
+                    if (mine && half == 0 && group == 0) {
+                        if (!whole) *reinterpret_cast<float2 *>(p.part_ml + part_row * 2) = none ? make_float2(-INFINITY, 0.f) : make_float2(m_owed, l_owed);
+                        else if (p.lse) p.lse[out_row] = none ? -INFINITY : (m_owed + log2f(l_owed)) * kLn2;
+                    }
+                    if (!whole && owed->t0 == 0 && rank == 0 && tx == 0) {
+                        // the clusters that the item's tiles reach into
+                        const int64_t total = ctl.head.total;
+                        const int n = ctl.head.clusters;
+                        int64_t rest = owed->rest;
+                        int parts = 1;
+                        for (int k = cluster + 1; rest > 0 && k < n; ++k, ++parts) rest -= total * (k + 1) / n - total * k / n;
+                        p.split[cluster] = Split{owed->row0, owed->nrows, cluster, parts};
+                    }
+                }
+                tc_fence_before();                                // O may be overwritten after the next P
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.piece_empty[(rd.n - 1) % kPieces]));
+                owed = nullptr;
+                named_barrier(7, kSoftmaxWarps * 32);             // all have read O, and their staging ends, before any stores a P
+            }
+            if (pc->end) break;
+            for (int i = t0 + ((int)(g0 & 1u) ^ group); i < t1; i += 2) {
+                g = g0 + (uint32_t)(i - t0);
+                const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2);
                 if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 1u]), (g >> 1) & 1u, ctl, p.status, limit);
                 tc_fence_after();
-                const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2);
                 if ((i < max(clear0, n_first) || i >= clear1) && alive) {
                     // one bit a key of this half: the window's and the first ones'
                     const int kp = tile_pos(*pc, i) + kHalf * half;
@@ -1121,12 +1232,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            g = g0 + (uint32_t)(t1 - t0);
             // ---- the next piece's queries, by the group that is done first, once the
             // last tile is scored
             const bool empty = t1 == t0;
             if (empty ? group == 0 : (int)((g - 1) & 1u) != group) {
-                if (alive && !empty) alive = wait_bar(smem_u32(&ctl.s_full[(g - 1) & 1u]), ((g - 1) >> 1) & 1u, ctl, p.status, limit);
-                if (alive) load_queries(rd.n + 1);
+                if (alive) load_queries(rd.n + 1, empty);
             }
             // its positions, asked for before they are wanted
             known = mbar_test(smem_u32(&ctl.piece_full[(rd.n + 1) % kPieces]), ((rd.n + 1) / kPieces) & 1u);
@@ -1134,98 +1245,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const Piece *nx = &ctl.piece[(rd.n + 1) % kPieces];
                 next_pos = nx->end ? -1 : row_pos(nx);
             }
-            // ---- the piece's output
-            if (!empty) {
-                if (alive) alive = wait_o(1, g - 1);
-                tc_fence_after();
-                if ((int)((g - 1) & 1u) == group && half == 0) ctl.m[0][r] = m;
-                named_barrier(7, kSoftmaxWarps * 32);
-                const float mn = ctl.m[0][r];
-                auto &sums = ctl.red[0];                      // nobody is at a tile now
-                sums[group][half][r] = m == -INFINITY ? 0.f : l * ex2(m - mn);
-                m = mn;
-                named_barrier(7, kSoftmaxWarps * 32);
-                l = (sums[0][0][r] + sums[0][1][r]) + (sums[1][0][r] + sums[1][1][r]);
-            }
-            const bool none = pos < 0 || l == 0.f;            // a sum of NaN is not none
-            if (alive && row - lane < pc->nrows) {
-                // 64 bytes of each of the warp's 32 rows at a time, turned in the warp's
-                // share of P's buffer so that stores write whole sectors (a row a lane
-                // straight from the accumulator took 13,000 clocks).
-                // A part goes to slot 2c where the item began in an earlier cluster, else to 2c + 1.
-                const bool whole = pc->whole, narrow = p.out_bf16;
-                const int64_t out_row = (int64_t)pc->row0 + row;
-                const int64_t part_row = ((int64_t)2 * cluster + (t0 == 0 ? 1 : 0)) * kRows + row;
-                const float factor = whole ? 1.f / l : 1.f;
-                const int col0 = 256 * half + 128 * group, bytes = narrow ? 2 : 4;
-                const int rows_left = pc->nrows - (row - lane);            // of the warp's 32
-                uint8_t *stage = smem + kPOff + warp * 2048;
-                uint8_t *dst = static_cast<uint8_t *>(whole ? p.out : p.part_o) +
-                               (((whole ? out_row : part_row) - lane + (lane >> 2)) * D_L + col0) * bytes + 16 * (lane & 3);
-                const uint32_t o_tmem = lane_tmem + kColO + 128 * group;
-                const int step = 64 / bytes;
-#pragma unroll 1
-                for (int c = 0; c < 128; c += step) {
-                    uint32_t w[16];
-                    if (narrow && !empty) {
-                        uint32_t o[32];
-                        tmem_ld32(o_tmem + c, o);
-                        tmem_wait_ld(o);
-                        if (whole) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * factor, __uint_as_float(o[2 * e + 1]) * factor);
-                                w[e] = *reinterpret_cast<const uint32_t *>(&h);
-                            }
-                        } else {
-                            float top = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(o[e])));
-                            const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
-                            const float unit = __int_as_float((127 - ex) << 23);      // values below 2 after it
-                            if (mine) p.part_unit[part_row * 16 + ((col0 + c) >> 5)] = __int_as_float((127 + ex) << 23);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const __half2 h = __floats2half2_rn(__uint_as_float(o[2 * e]) * unit, __uint_as_float(o[2 * e + 1]) * unit);
-                                w[e] = *reinterpret_cast<const uint32_t *>(&h);
-                            }
-                        }
-                    } else if (!empty) {
-                        tmem_ld16(o_tmem + c, w);
-                        tmem_wait_ld(w);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * factor);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4 *>(stage + sw64_offset((uint32_t)lane, (uint32_t)q)) =
-                            none ? make_uint4(0, 0, 0, 0) : make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-                    __syncwarp();
-                    uint4 v[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        v[q] = *reinterpret_cast<const uint4 *>(stage + sw64_offset((uint32_t)(8 * q + (lane >> 2)), (uint32_t)(lane & 3)));
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (8 * q + (lane >> 2) < rows_left) *reinterpret_cast<uint4 *>(dst + (int64_t)(8 * q) * D_L * bytes + c * bytes) = v[q];
-                    __syncwarp();
-                }
-                if (mine && half == 0 && group == 0) {
-                    if (!whole) *reinterpret_cast<float2 *>(p.part_ml + part_row * 2) = none ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
-                    else if (p.lse) p.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
-                }
-                if (!whole && t0 == 0 && rank == 0 && tx == 0) {
-                    // the clusters that the item's tiles reach into
-                    const int64_t total = ctl.head.total;
-                    const int n = ctl.head.clusters;
-                    int64_t rest = pc->rest;
-                    int parts = 1;
-                    for (int k = cluster + 1; rest > 0 && k < n; ++k, ++parts) rest -= total * (k + 1) / n - total * k / n;
-                    p.split[cluster] = Split{pc->row0, pc->nrows, cluster, parts};
-                }
-            }
-            tc_fence_before();                                // O may be overwritten after the next P
-            rd.done(ctl, lane);
+            owed = pc;
+            m_owed = m, l_owed = l, pos_owed = pos;
+            ++rd.n;
         }
     }
 
