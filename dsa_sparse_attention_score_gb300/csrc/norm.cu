@@ -11,7 +11,9 @@
 // GB300, 16,384 rows of 7168 bf16 values with residual and sum (939 MB): two units
 // a thread 158 us (5.9 TB/s), one 182, four 244 (fewer threads an SM); taking rows
 // in turn with the next one's loads ahead 216 (registers).  8191 rows of 4096 fp16
-// values to codes (236 MB): 54 us.
+// values to codes (236 MB): 48 us with 40 registers a thread and the weights loaded
+// behind the reduction (54 with 60 registers: fewer threads an SM; plain outputs
+// lose by it, 158 -> 167 us).
 #include <algorithm>
 
 #include "dsa_common.cuh"
@@ -35,6 +37,7 @@ struct NormParams {
     float *scale;                  // [n, groups]
     int64_t xs, rs, ss, os;        // values between rows
     int n, dim, group;
+    int groups, group_log2;        // of a row; of one group's values where a row has several
     float eps;
 };
 
@@ -86,7 +89,7 @@ template <typename Op, typename V> __device__ __forceinline__ V row_reduce(V v, 
 }  // namespace
 
 template <typename T, int W, int V, bool kAligned, bool kCodes>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
+__global__ void __maxnreg__(kCodes ? 40 : 64) rms_norm_kernel(const NormParams p) {
     __shared__ uint32_t sh[32];
     const int row = blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = row < p.n;
@@ -120,19 +123,23 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         }
     }
     const bool own_weight = p.weight && !p.weight_f32;
-    if (own_weight) {
+    auto load_weight = [&] {
+        if (!own_weight) return;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int at = (tx + k * step) * W;
             if (at < p.dim) w[k] = load_unit<T, W, kAligned>(static_cast<const T *>(p.weight) + at);
         }
-    }
+    };
+    constexpr bool late = kCodes && V > 1;               // registers before latency
+    if (!late) load_weight();
     float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
         for (int e = 0; e < W; ++e) ss = fmaf(to_f(h[k].v[e]), to_f(h[k].v[e]), ss);
     ss = row_reduce(ss, [](float a, float b) { return a + b; }, reinterpret_cast<float *>(sh));
+    if (late) load_weight();
     const float rstd = 1.f / sqrtf(ss / (float)p.dim + p.eps);
     // the W values of unit k
     auto values = [&](int k, float (&y)[W]) {
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
                 uint8_t *dst = p.codes + (int64_t)row * p.dim + at;
                 if constexpr (W == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0], c[1]);
                 else *reinterpret_cast<uint32_t *>(dst) = c[0];
-                if (whole ? at == 0 : at % p.group == 0) p.scale[(int64_t)row * (p.dim / p.group) + at / p.group] = scale;
+                if (whole ? at == 0 : (at & (p.group - 1)) == 0) p.scale[(int64_t)row * p.groups + (whole ? 0 : at >> p.group_log2)] = scale;
             }
         }
     }
@@ -249,7 +256,7 @@ template <typename T> cudaError_t launch_norm_t(const NormParams &p, cudaStream_
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormLaunch &a, cudaStream_t stream) {
-    NormParams p;
+    NormParams p{};
     p.x = a.x;
     p.residual = a.residual;
     p.sum = a.sum;
@@ -265,6 +272,8 @@ cudaError_t launch_rms_norm(const NormLaunch &a, cudaStream_t stream) {
     p.n = a.n;
     p.dim = a.dim;
     p.group = a.group;
+    p.groups = a.group ? a.dim / a.group : 0;
+    while ((1 << p.group_log2) < a.group) ++p.group_log2;
     p.eps = a.eps;
     switch (a.dtype) {
         case DSA_DT_F32: return launch_norm_t<float>(p, stream);
