@@ -195,6 +195,11 @@ struct PlanHead {
     int32_t total;                // costs of all items
     int32_t clusters;             // clusters with work: every one has some
 };
+// floor(total * c / n), the costs before cluster c of n, in 32 bits.
+__device__ __forceinline__ int share(int total, int c, int n) {
+    const int each = total / n;
+    return each * c + (total - each * n) * c / n;
+}
 struct Start { int32_t item, off; };                 // a cluster's first item and the costs of it done before
 struct Split { int32_t row0, nrows, first, parts; }; // an item that begins in a cluster and ends in a later one
 
@@ -532,8 +537,8 @@ __device__ __forceinline__ int plan_scan(int v, int &sum, int *sh) {
 // A cluster's first piece into the ring, by the one thread that knows its first
 // item: the other warps begin with it right away.
 __device__ __forceinline__ void begin(const MlaParams &p, Ctl &ctl, int cluster, PlanHead head, int item, int off, const Item &it) {
-    const int64_t total = head.total;
-    Todo todo{item, off, (int)(total * (cluster + 1) / head.clusters - total * cluster / head.clusters), 0};
+    const int left = share(head.total, cluster + 1, head.clusters) - share(head.total, cluster, head.clusters);
+    Todo todo{item, off, left, 0};
     Piece pc;
     if (todo.take(it, pc)) {
         ctl.piece[0] = pc;
@@ -555,7 +560,7 @@ __device__ __forceinline__ void plan_here(const MlaParams &p, Ctl &ctl, int clus
     const PlanHead head{total, min((int)gridDim.x / 2, total)};
     if (seq == 0) ctl.head = head;
     if (cluster < head.clusters) {
-        const int at = (int)((int64_t)total * cluster / head.clusters);
+        const int at = share(total, cluster, head.clusters);
         if (at >= before && at < before + cost) begin(p, ctl, cluster, head, seq, at - before, it);
     }
 }
@@ -1088,11 +1093,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     if (!whole && owed->t0 == 0 && rank == 0 && tx == 0) {
                         // the clusters that the item's tiles reach into
-                        const int64_t total = ctl.head.total;
-                        const int n = ctl.head.clusters;
-                        int64_t rest = owed->rest;
-                        int parts = 1;
-                        for (int k = cluster + 1; rest > 0 && k < n; ++k, ++parts) rest -= total * (k + 1) / n - total * k / n;
+                        const int total = ctl.head.total, n = ctl.head.clusters;
+                        int rest = owed->rest, parts = 1;
+                        for (int k = cluster + 1; rest > 0 && k < n; ++k, ++parts) rest -= share(total, k + 1, n) - share(total, k, n);
                         p.split[cluster] = Split{owed->row0, owed->nrows, cluster, parts};
                     }
                 }
@@ -1325,7 +1328,7 @@ __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const Problem p,
     const int n = min(clusters, total);
     if (threadIdx.x == 0) *head = PlanHead{total, n};
     for (int c = (int)threadIdx.x; c < n; c += kPlanThreads) {
-        const int at = (int)((int64_t)total * c / n);
+        const int at = share(total, c, n);
         int lo = 0, hi = base;                                // items[lo].cost0 <= at < items[hi].cost0
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
