@@ -248,3 +248,47 @@ def test_a_wait_that_runs_out_is_reported():
     out, lse = c.run(dsa, ws=ws)
     assert dsa.dsa_read_device_status(ws) == 0
     check(out, lse, ref)
+
+
+@pytest.mark.parametrize("B,H", [(384, 128), (385, 16), (1100, 3)])
+def test_many_decoding_sequences(B, H):
+    """Up to one thread a sequence the kernel plans for itself; beyond that a plan goes ahead of it."""
+    lens = [1 + (37 * b) % 300 for b in range(B)]
+    run_and_check(Case(*chunk(lens, [1] * B), H).cuda())
+
+
+def test_more_items_than_the_plan_has_threads():
+    c = Case(*chunk([1300], [1300]), 128).cuda()
+    ref = c.reference(window=70)
+    out, lse = c.run(dsa, window=70)
+    assert dsa.dsa_read_device_status(c.ws) == 0
+    check(out, lse, ref)
+
+
+def test_scale_of_zero_gives_the_mean():
+    c = Case(*chunk([130, 64], [2, 1]), 16, block=16).cuda()
+    c.sm = 0.0
+    run_and_check(c)
+
+
+def test_queries_of_padding_may_be_anything():
+    c = Case([0, 4], [-1, 700, -1, 701], 24).cuda()
+    c.q_lat[0], c.q_rope[0] = float("nan"), float("inf")
+    c.q_lat[2] = float("-inf")
+    run_and_check(c)
+
+
+def test_sequence_offsets_that_fall_are_flagged():
+    c = Case([0, 2, 3], [40, 41, 9], 16, lens=[42, 10]).cuda()
+    ref = c.reference()
+    b, lse = c.batch(dsa), torch.empty(3, 16, device="cuda")
+    ws = dsa.workspace(dsa.DSA_OP_MLA_ATTN, b, H=16)
+    for most in (2, 300):                                     # without and with a plan ahead
+        out = torch.full((3, 16, 512), 7.0, device="cuda")
+        bad = dsa.Batch(torch.tensor([0, 2, 1], dtype=torch.int32, device="cuda"), c.q_pos, c.kv_off, most, c.max_kv, c.rows)
+        dsa.dsa_mla_attn(c.q_lat, c.q_rope, c.kv, bad, c.sm, out, lse, ws)
+        assert dsa.dsa_read_device_status(ws) == dsa.DSA_DEV_BAD_POSITION
+        check(out[:2], lse[:2], tuple(x[:2] for x in ref))
+        assert (out[2] == 7).all()
+    dsa.dsa_mla_attn(c.q_lat, c.q_rope, c.kv, b, c.sm, out, lse, ws)
+    check(out, lse, ref)
