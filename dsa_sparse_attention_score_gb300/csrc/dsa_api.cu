@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
@@ -945,6 +946,12 @@ dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rop
 
 // ---------------------------------------------------------------- attention over all visible rows
 
+// Have two arrays (either may be null) no byte in common?
+static bool apart(const void *x, uint64_t x_bytes, const void *y, uint64_t y_bytes) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return !x || !y || a + x_bytes <= b || b + y_bytes <= a;
+}
+
 static dsa_status_t mla_attn_impl(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const dsa_bf16 *kv_cache,
                                   const dsa_batch_t *batch, const dsa_paging_t *paging, int H, int window, int n_sink,
                                   const int32_t *sink_pos0, float sm_scale, void *out, int out_dtype, float *lse, void *ws,
@@ -963,6 +970,13 @@ static dsa_status_t mla_attn_impl(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope,
     if ((s = check_ws(ws, ws_bytes, layout(DSA_OP_MLA_ATTN, batch, H, 1).total)) != DSA_OK) return s;
     const int tail = q_rope ? 1 : 0;
     const uint64_t qrows = (uint64_t)batch->total_q * H, rows = (uint64_t)batch->cache_rows, width = tail ? D_ROW : D_L;
+    // rows are stored while others are still being read
+    const uint64_t out_bytes = qrows * D_L * (out_dtype == DSA_DT_BF16 ? 2 : 4);
+    for (const auto &y : {std::pair<const void *, uint64_t>{out, out_bytes}, {lse, qrows * 4}})
+        if (!apart(q_lat, qrows * D_L * 2, y.first, y.second) || !apart(q_rope, qrows * D_R * 2, y.first, y.second) ||
+            !apart(kv_cache, rows * width * 2, y.first, y.second))
+            return DSA_ERR_INVALID_ARGUMENT;
+    if (!apart(out, out_bytes, lse, qrows * 4)) return DSA_ERR_INVALID_ARGUMENT;
     const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     MlaMaps m;
     // without a tail the kernel never reads the tail queries' map (it gets the latent one)
@@ -1038,6 +1052,14 @@ static dsa_status_t rms_norm_impl(NormLaunch a, cudaStream_t stream) {
             return DSA_ERR_INVALID_ARGUMENT;
     }
     if (!rows_apart(a.sum, a.sum_stride, a.out, a.out_stride, a.n, a.dim, e, false)) return DSA_ERR_INVALID_ARGUMENT;
+    if (a.codes) {
+        const uint64_t code_bytes = (uint64_t)a.n * a.dim, scale_bytes = (uint64_t)a.n * (a.dim / a.group) * 4;
+        for (auto &r : rows) {
+            const uint64_t bytes = ((uint64_t)(a.n - 1) * *r.s + a.dim) * e;
+            if (!apart(r.p, bytes, a.codes, code_bytes) || !apart(r.p, bytes, a.scale, scale_bytes)) return DSA_ERR_INVALID_ARGUMENT;
+        }
+        if (!apart(a.codes, code_bytes, a.scale, scale_bytes)) return DSA_ERR_INVALID_ARGUMENT;
+    }
     DSA_TRY_CUDA(launch_rms_norm(a, stream));
     return DSA_OK;
 }

@@ -551,7 +551,7 @@ dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rop
  *                [n_tokens, dim / group], group 32, 64, 128 or dim
  * out and sum may be x or residual with the same strides, but not each other;
  * otherwise rows written must not share values with others, except as column
- * slices of wider rows.  h^2 has to stay finite in float32 (and eps > 0 where all
+ * slices of wider rows; codes and scale share no byte with anything.  h^2 has to stay finite in float32 (and eps > 0 where all
  * of a row may be 0).  No workspace.
  * Errors: DSA_ERR_INVALID_ARGUMENT for null pointers, sizes below 1, a negative or
  * not finite eps, strides outside the above, rows that overlap, dim not a multiple
@@ -577,17 +577,21 @@ dsa_status_t dsa_rms_norm_q8(const void *x, int64_t x_stride, const void *residu
  *   q_lat [T,H,512] bf16, q_rope [T,H,64] bf16 and kv_cache [cache_rows,576] bf16 as
  *   dsa_sparse_mla_attn; q_rope NULL: rows without a tail, kv_cache [cache_rows,512]
  *   paging     NULL for contiguous caches; any block_size >= 1 (multiples of 64
- *              are read in the largest pieces, then multiples of 16).  Only blocks
- *              that hold a visible position are looked up.
- *   out        [T,H,512] of out_dtype DSA_DT_F32 or DSA_DT_BF16; lse [T,H] or NULL
+ *              are read in the largest pieces, then multiples of 16).  Entries of
+ *              blocks without a visible position may hold anything.
+ *   out        [T,H,512] of out_dtype DSA_DT_F32 or DSA_DT_BF16; lse [T,H] or NULL;
+ *              neither shares a byte with the other or with an input
  *   ws         dsa_workspace_size(DSA_OP_MLA_ATTN, batch, 1, H, 1)
  * Operands are bf16, sums and the softmax float32; probabilities enter the value
- * product as bf16.  Cache rows that no token of the call sees may hold anything.
+ * product as bf16.  Rows whose positions are divided among several parts of the GPU
+ * are joined from float32 parts (float32 out) or fp16 ones with a power of two for 32
+ * dims (bf16 out).  The results of a call do not change from run to run.  Cache rows that no token of the call sees may hold anything.
  * A token at position -1 is padding: out = 0, lse = -INFINITY.  One at any other
  * position out of bounds, or in an unmapped block, gets the same and is flagged
  * DSA_DEV_BAD_POSITION.  A visible position in an unmapped block is flagged
  * DSA_DEV_BAD_INDEX; the outputs of the tokens that see it are unspecified.
- * Errors: as dsa_sparse_mla_attn_q8 (paging as there); DSA_ERR_UNSUPPORTED where
+ * Errors: as dsa_sparse_mla_attn_q8 (paging as there), DSA_ERR_INVALID_ARGUMENT for
+ * out or lse in an input; DSA_ERR_UNSUPPORTED where
  * total_q * H exceeds 2^31 - 257 or the 128-position tiles of all rows 2^31.
  */
 dsa_status_t dsa_mla_attn(const dsa_bf16 *q_lat, const dsa_bf16 *q_rope, const dsa_bf16 *kv_cache, const dsa_batch_t *batch,

@@ -100,6 +100,17 @@ def test_norm_q8_refusals(L):
         assert _norm8(L, **kw) == MISALIGNED, kw
 
 
+def test_outputs_that_share_memory_are_refused(L):
+    # 2 tokens x 64 heads: q_lat and a bf16 out 131,072 bytes, q_rope 16,384, the cache 200 x 1152, lse 512
+    far = dict(q=0x100000, r=0x200000, kv=0x300000, out=0x400000, lse=0x500000)
+    for kw in (dict(out=0x100000), dict(out=0x100000 + 131072 - 16), dict(out=0x200000 + 16384 - 16), dict(out=0x300000 + 200 * 1152 - 16),
+               dict(lse=0x100000), dict(lse=0x300000 + 4), dict(lse=0x400000 + 131072 - 4), dict(out=0x100000 - 131072 + 16)):
+        assert _attn(L, **dict(far, **kw)) == INVALID, kw
+    for kw in (dict(codes=X), dict(codes=X + 4 * 1024 - 16), dict(codes=0x1000000 - 16), dict(scale=X + 8), dict(scale=0x1000000),
+               dict(scale=0x2000000 + 4 * 512 - 4)):
+        assert _norm8(L, **kw) == INVALID, kw
+
+
 def test_binding_refuses_tensors_that_are_not_on_a_gpu():
     torch = pytest.importorskip("torch")
     x = torch.zeros(4, 512, dtype=torch.bfloat16)
