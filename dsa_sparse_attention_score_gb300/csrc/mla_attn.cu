@@ -10,27 +10,41 @@
 //     O[row, dim] += P[row, s] . C[s, dim]             (M=128, N=2x256, K=128)
 // An O of 128 rows and 512 dims would fill the tensor memory of one SM.  With
 // M=128 over a pair of SMs each holds 64 rows, a row's first N / 2 columns in
-// lane r and the rest in lane r + 64: O takes 256 columns, two S buffers take 128.
+// lane r and the rest in lane r + 64: O takes 256 columns, two S buffers take 128,
+// and the other 128 hold the first 256 dims of the queries (as A in tensor memory).
 // Measured on GB300, this form runs at 4093 multiply-adds a clock and SM (all
 // the tensor core has), also while 64 bytes a clock come in through TMA.
 // Each CTA's shared memory holds
-//   its 64 query rows                                  72 KB
-//   its 64 of the tile's keys, nine 64-column blocks   72 KB   (B of S)
-//   all 128 rows of its 256 of the output dims         64 KB   (B of O)
-//   P of its 64 rows                                   16 KB
+//   the other dims of its 64 query rows                 40 KB
+//   its 64 of the tile's keys, nine 64-column blocks    72 KB   (B of S)
+//   three halves of 64 keys for its 256 output dims     96 KB   (B of O)
+//   P of its 64 rows                                    16 KB
 // The value rows are read a second time from L2 because a pair's B operand lies
 // at one address in both CTAs: S wants a CTA's own keys there, O all keys.
 //
-// Per tile S takes 1152 clocks and O 1024.  The tensor core runs S(i+1), O(i),
-// S(i+2), O(i+1)...: the softmax of tile i+1 has the time of O(i) and S(i+2).
-// Keys are refilled in three groups of blocks and values in two halves, each as
-// soon as the product that read it is done, which leaves every copy more than
-// 1600 clocks to land.
+// Per tile S takes 1152 clocks and O 1024, and 136 KB come into an SM.  S(i+1),
+// O(i), S(i+2), O(i+1)... follow each other on the tensor core, and the softmax of a
+// tile has the time of one O and one S.  Keys are refilled in three groups of blocks
+// and values in halves of a tile, each as soon as the product that read it is done.
+// Warps 0-7 are softmax and output, in two groups that take the tiles in turn; one
+// warp each issues S's and O's products and copies keys and values.
+// Measured: 2048 tokens of 64 heads after 6144 positions 1.26 ms (1.62 PFLOP/s, 86%
+// of the card's measured rate: 2450 clocks a tile, the tensor pipe 86% busy); 32
+// sequences of 4k-64k positions, 128 heads, one token each 0.26 ms (5.0 TB/s: 3700
+// clocks a tile, what HBM takes to deliver it being 2800); 8 of 8192, 64 heads 31 us (HBM's
+// share is 11: the first S comes 6 us after the launch, the output of the last
+// piece takes 2.5 and the join 5).  What bounds calls with many short items is the
+// change of pieces, 7000 clocks in which the tensor core waits for an output.
 //
 // The work is cut by tiles, not by items: the tiles of all items in a row are
 // divided evenly among the clusters.  An item that several clusters share gets
 // its parts (unnormalised O, running maximum, sum) into the workspace, and
 // mla_combine_kernel joins them.
+//
+// Code that only some calls or tiles reach is kept out of the loops: an instruction
+// that is not in the SM's cache takes a round trip to L2, and what every warp runs
+// in a tile has to stay there (tiles fell from 7500 misses an SM to 790, a prefill
+// from 1.55 to 1.27 ms).
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 
@@ -944,8 +958,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!wait_bar(smem_u32(&ctl.piece_full[n % kPieces]), (n / kPieces) & 1u, ctl, p.status, limit)) return;
             const Piece *pc = &ctl.piece[n % kPieces];
             if (pc->end || pc->t0 == pc->t1) return;
-            // four threads a row: 32 bytes of eight rows a load (a row a thread, 16 bytes
-            // each, kept the load unit busy for 4900 clocks)
+            // four threads a row: 32 bytes of eight rows a load (with a row a thread, 16 bytes
+            // each, a windowed prefill took 283 us instead of 271)
             const int64_t row = (int64_t)pc->row0 + kHalf * (int)rank + (warp & 1) * 32 + (lane >> 2);
             const int64_t rows = (int64_t)b.T * p.pr.H;
             const uint2 *src = reinterpret_cast<const uint2 *>(p.q_lat + row * D_L) + (lane & 3);
@@ -1434,7 +1448,6 @@ __global__ void __launch_bounds__(kJoinThreads) mla_combine_kernel(const Split *
 // ---------------------------------------------------------------- host
 namespace {
 
-
 struct MlaLayout {
     size_t head, start, split, ml, part, unit, item0, items, total;
     int64_t max_items;
@@ -1496,16 +1509,18 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     p.rows_per_box = !b.block_table || b.block_size % 64 == 0 ? 64 : b.block_size % 16 == 0 ? 16 : 0;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(mla_attn_kernel), 12, kSmem);
     if (e != cudaSuccess) return e;
-    if (!here) e = launch_k(mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, p.pr, status, (int)L.max_items, kClusters, head,
-                 items, start, reinterpret_cast<int32_t *>(w + L.item0));
-    if (e != cudaSuccess) return e;
+    if (!here) {
+        e = launch_k(mla_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, p.pr, status, (int)L.max_items, kClusters, head,
+                     items, start, reinterpret_cast<int32_t *>(w + L.item0));
+        if (e != cudaSuccess) return e;
+    }
     e = launch_k(mla_attn_kernel, dim3(2 * kClusters), dim3(kThreads), kSmem, stream, true, p, maps.q_lat, maps.q_rope, maps.kv64,
                  maps.kv16, maps.kv1);
     if (e != cudaSuccess) return e;
     const int rows = a.out_bf16 ? kJoinRows<true> : kJoinRows<false>;
     return launch_k(a.out_bf16 ? mla_combine_kernel<true> : mla_combine_kernel<false>, dim3(kClusters, kRows / rows),
                     dim3(kJoinThreads), 0, stream, true, (const Split *)p.split, (const void *)p.part_o, (const float *)p.part_unit,
-                    (const float *)p.part_ml,                    a.out, a.lse);
+                    (const float *)p.part_ml, a.out, a.lse);
 }
 
 }  // namespace dsa
