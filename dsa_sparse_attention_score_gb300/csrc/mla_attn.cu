@@ -242,7 +242,7 @@ struct Ctl {
     float red[2][2][2][kHalf];    // a group's maxima by tile and half of the keys
     alignas(16) float m[2][kHalf];   // running maxima by tile
     PlanHead head;                // the plan, and what is left of it behind the first piece:
-    int32_t todo[4];              // a Todo
+    int32_t todo[5];              // a Todo
     Piece piece[kPieces];
 };
 constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
@@ -283,6 +283,7 @@ struct MlaParams {
     float *lse;
     float scale_log2;
     int tail;                     // rows of 576 (1) or 512 (0)
+    bool one;                     // without a plan ahead (items null): at most one item a sequence
     int rows_per_box;             // 64, 16 or 0: rows that lie together for certain (pages)
 };
 
@@ -363,25 +364,26 @@ __device__ __forceinline__ void item_fill(const Problem &p, Item &it) {
     }
     item_tiles(p, it);
 }
-// The item of a sequence that has at most one (false: it has no rows).  Where every
-// sequence has one token (decode) its position is loaded beside the offsets, not
-// behind them.
-__device__ __forceinline__ bool item_of(const Problem &p, int seq, uint32_t *status, Item &it) {
+// Item `part` of a sequence (false: it has no such rows).  Where every sequence has
+// one token (decode) its position is loaded beside the offsets, not behind them.
+__device__ __forceinline__ bool item_of(const Problem &p, int seq, int part, bool one, uint32_t *status, Item &it) {
     const DevBatch &b = p.b;
     const int guess = __ldg(b.q_pos + min(seq, b.T - 1));
     const int t0 = __ldg(b.cu_q + seq), t1 = __ldg(b.cu_q + seq + 1);
     it.kv0 = seq_base(b, seq);
-    if (t0 < 0 || t1 < t0 || t1 > b.T || (t1 - t0) * p.H > kRows) {
+    if (t0 < 0 || t1 < t0 || t1 > b.T || (one && (t1 - t0) * p.H > kRows)) {
         flag(status, DSA_DEV_BAD_POSITION);
         return false;
     }
-    if (t1 == t0) return false;
     it.seq = seq;
-    it.row0 = t0 * p.H;
-    it.nrows = (t1 - t0) * p.H;
+    it.row0 = t0 * p.H + part * kRows;
+    it.nrows = min(kRows, t1 * p.H - it.row0);
+    if (it.nrows <= 0) return false;
     it.min_pos = INT32_MAX;
     it.hi = -1;
-    for (int t = t0; t < t1; ++t) {
+    const int last = (it.row0 + it.nrows - 1) / p.H;
+#pragma unroll 4
+    for (int t = it.row0 / p.H; t <= last; ++t) {
         const int pos = t == seq ? guess : __ldg(b.q_pos + t);
         if (pos >= 0 && pos < b.max_kv) {
             it.min_pos = min(it.min_pos, pos);
@@ -394,10 +396,11 @@ __device__ __forceinline__ bool item_of(const Problem &p, int seq, uint32_t *sta
 
 // What a cluster has still to do.
 struct Todo {
-    int32_t item, off, left;      // next item, costs of it done, costs left to this cluster
+    int32_t seq, item;            // next item (of the sequence; of all with a plan ahead)
+    int32_t off, left;            // costs of it done, costs left to this cluster
     int32_t written;              // pieces in the ring
     // The next piece, of item `it`; false: costs that stand for no tile.
-    __device__ __forceinline__ bool take(const Item &it, Piece &pc) {
+    __device__ __forceinline__ bool take(const Item &it, Piece &pc, bool by_seq) {
         const int cost = item_cost(it.n), n = min(left, cost - off);
         pc.t0 = min(off, it.n);
         pc.t1 = min(off + n, it.n);
@@ -405,7 +408,7 @@ struct Todo {
         left -= n;
         off += n;
         if (off == cost) {
-            ++item;
+            ++(by_seq ? seq : item);
             off = 0;
         }
         pc.n_first = it.n_first;
@@ -426,6 +429,7 @@ struct Todo {
         return pc.t1 > pc.t0 || (it.n == 0 && first);
     }
 };
+static_assert(sizeof(Todo) == sizeof(Ctl::todo), "a Todo's place");
 // This CTA's query rows of a piece into L2, long before they are wanted.
 __device__ __forceinline__ void ask_for_queries(const MlaParams &p, const Piece &pc) {
     if (pc.t1 == pc.t0) return;
@@ -463,11 +467,13 @@ __device__ __forceinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, i
             Item it;
             if (p.items) {
                 it = p.items[todo.item];
-            } else if (!item_of(p.pr, todo.item, p.status, it)) {   // no rows: no costs
-                ++todo.item;
-                continue;
+            } else if (!item_of(p.pr, todo.seq, todo.item, p.one, p.status, it)) {
+                end = ++todo.seq >= p.pr.b.B;                 // the next sequence's first
+                todo.item = 0;
+                if (!end) continue;
+                pc.end = true;
             }
-            if (!todo.take(it, pc)) continue;
+            if (!end && !todo.take(it, pc, p.one && !p.items)) continue;
         }
         const uint32_t n = (uint32_t)todo.written, slot = n % kPieces;
         if (!wait_bar(smem_u32(&ctl.piece_empty[slot]), ((n / kPieces) & 1u) ^ 1u, ctl, p.status, p.pr.b.wait_ns)) {
@@ -550,11 +556,11 @@ __device__ __forceinline__ int plan_scan(int v, int &sum, int *sh) {
 
 // A cluster's first piece into the ring, by the one thread that knows its first
 // item: the other warps begin with it right away.
-__device__ __forceinline__ void begin(const MlaParams &p, Ctl &ctl, int cluster, PlanHead head, int item, int off, const Item &it) {
+__device__ __forceinline__ void begin(const MlaParams &p, Ctl &ctl, int cluster, PlanHead head, int seq, int item, int off, const Item &it) {
     const int left = share(head.total, cluster + 1, head.clusters) - share(head.total, cluster, head.clusters);
-    Todo todo{item, off, left, 0};
+    Todo todo{seq, item, off, left, 0};
     Piece pc;
-    if (todo.take(it, pc)) {
+    if (todo.take(it, pc, p.one && !p.items)) {
         ctl.piece[0] = pc;
         mbar_arrive(smem_u32(&ctl.piece_full[0]));
         ask_for_queries(p, pc);
@@ -562,20 +568,44 @@ __device__ __forceinline__ void begin(const MlaParams &p, Ctl &ctl, int cluster,
     }
     *reinterpret_cast<Todo *>(ctl.todo) = todo;
 }
-// The plan of a call with at most one item a sequence and no more sequences than
-// threads, made by every CTA for itself (a launch less: 4 us).
+// The plan of a call with no more sequences and items than threads, made by every CTA
+// for itself: 8 us less than with a plan kernel ahead (decode 42.6 -> 34.5 us).
 __device__ __forceinline__ void plan_here(const MlaParams &p, Ctl &ctl, int cluster) {
-    const int seq = (int)threadIdx.x;
+    const DevBatch &b = p.pr.b;
+    int *const sh = reinterpret_cast<int *>(&ctl.red[0][0][0][0]);
+    int seq = (int)threadIdx.x, item = 0;                     // of this thread
+    bool there = seq < b.B;
+    if (!p.one) {
+        // items of the sequences before each, and from there this thread's
+        int n = 0, items;
+        if (there) {
+            const int t0 = __ldg(b.cu_q + seq), t1 = __ldg(b.cu_q + seq + 1);
+            if (t0 >= 0 && t1 >= t0 && t1 <= b.T) n = ((t1 - t0) * p.pr.H + kRows - 1) / kRows;
+            else flag(p.status, DSA_DEV_BAD_POSITION);
+        }
+        const int before = plan_scan<kThreads>(n, items, sh);
+        int *const first = sh + 64;
+        if (there) first[seq] = before;
+        __syncthreads();
+        if (items > kThreads && threadIdx.x == 0) flag(p.status, DSA_DEV_BAD_POSITION);   // only where cu_q falls somewhere
+        there = (int)threadIdx.x < items;
+        int hi = b.B;
+        for (seq = 0; hi - seq > 1;) {                        // first[seq] <= threadIdx.x < first[hi]
+            const int mid = (seq + hi) >> 1;
+            if (first[mid] <= (int)threadIdx.x) seq = mid; else hi = mid;
+        }
+        item = (int)threadIdx.x - first[seq];
+    }
     Item it;
     int cost = 0;
-    if (seq < p.pr.b.B && item_of(p.pr, seq, p.status, it)) cost = item_cost(it.n);
+    if (there && item_of(p.pr, seq, item, p.one, p.status, it)) cost = item_cost(it.n);
     int total;
-    const int before = plan_scan<kThreads>(cost, total, reinterpret_cast<int *>(&ctl.red[0][0][0][0]));
+    const int before = plan_scan<kThreads>(cost, total, sh);
     const PlanHead head{total, min((int)gridDim.x / 2, total)};
-    if (seq == 0) ctl.head = head;
+    if (threadIdx.x == 0) ctl.head = head;
     if (cluster < head.clusters) {
         const int at = share(total, cluster, head.clusters);
-        if (at >= before && at < before + cost) begin(p, ctl, cluster, head, seq, at - before, it);
+        if (at >= before && at < before + cost) begin(p, ctl, cluster, head, seq, item, at - before, it);
     }
 }
 // The same from the plan kernel's, by one thread.
@@ -584,7 +614,7 @@ __device__ __forceinline__ void plan_read(const MlaParams &p, Ctl &ctl, int clus
     ctl.head = head;
     if (cluster >= head.clusters) return;
     const Start st = p.start[cluster];
-    begin(p, ctl, cluster, head, st.item, st.off, p.items[st.item]);
+    begin(p, ctl, cluster, head, 0, st.item, st.off, p.items[st.item]);
 }
 
 }  // namespace
@@ -616,7 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctl.s_full[i]), 1);
             mbar_init(smem_u32(&ctl.s_empty[i]), kSoftmaxWarps);          // a group's in both CTAs
         }
-        for (int i = 0; i < 4; ++i) ctl.todo[i] = 0;          // what a cluster without work has to do
+        for (int32_t &x : ctl.todo) x = 0;                    // what a cluster without work has to do
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_u32(&ctl.piece_full[i]), 1);
             mbar_init(smem_u32(&ctl.piece_empty[i]), kSoftmaxWarps + 2 + (rank == 0 ? 2 : 0));
@@ -1493,8 +1523,10 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     Item *items = reinterpret_cast<Item *>(w + L.items);
     Start *start = reinterpret_cast<Start *>(w + L.start);
     p.head = head;
-    // One item a sequence, a thread for each: the kernel plans for itself.
-    const bool here = (int64_t)b.max_q * a.H <= kRows && b.B <= kThreads;
+    // No more sequences and items than threads: the kernel plans for itself.  Each
+    // thread goes through its item's tokens; with fewer than 8 heads there are many.
+    p.one = (int64_t)b.max_q * a.H <= kRows;
+    const bool here = b.B <= kThreads && (p.one || (L.max_items <= kThreads && a.H >= 8));
     p.items = here ? nullptr : items;
     p.start = start;
     p.split = reinterpret_cast<Split *>(w + L.split);

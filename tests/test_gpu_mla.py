@@ -278,13 +278,14 @@ def test_queries_of_padding_may_be_anything():
     run_and_check(c)
 
 
-def test_sequence_offsets_that_fall_are_flagged():
-    c = Case([0, 2, 3], [40, 41, 9], 16, lens=[42, 10]).cuda()
+@pytest.mark.parametrize("H", [16, 3])
+def test_sequence_offsets_that_fall_are_flagged(H):
+    c = Case([0, 2, 3], [40, 41, 9], H, lens=[42, 10]).cuda()
     ref = c.reference()
-    b, lse = c.batch(dsa), torch.empty(3, 16, device="cuda")
-    ws = dsa.workspace(dsa.DSA_OP_MLA_ATTN, b, H=16)
-    for most in (2, 300):                                     # without and with a plan ahead
-        out = torch.full((3, 16, 512), 7.0, device="cuda")
+    b, lse = c.batch(dsa), torch.empty(3, H, device="cuda")
+    ws = dsa.workspace(dsa.DSA_OP_MLA_ATTN, b, H=H)
+    for most in (2, 300):                                     # as decode, and as chunks
+        out = torch.full((3, H, 512), 7.0, device="cuda")
         bad = dsa.Batch(torch.tensor([0, 2, 1], dtype=torch.int32, device="cuda"), c.q_pos, c.kv_off, most, c.max_kv, c.rows)
         dsa.dsa_mla_attn(c.q_lat, c.q_rope, c.kv, bad, c.sm, out, lse, ws)
         assert dsa.dsa_read_device_status(ws) == dsa.DSA_DEV_BAD_POSITION
@@ -292,3 +293,16 @@ def test_sequence_offsets_that_fall_are_flagged():
         assert (out[2] == 7).all()
     dsa.dsa_mla_attn(c.q_lat, c.q_rope, c.kv, b, c.sm, out, lse, ws)
     check(out, lse, ref)
+
+
+@pytest.mark.parametrize("H", [7, 8, 64])
+def test_a_few_tokens_a_sequence(H):
+    """Sequences of several items each, some without tokens, few enough for the kernel's own plan."""
+    lens, per = [300, 5, 0, 513, 40, 0, 129], [9, 5, 0, 4, 1, 0, 20]
+    run_and_check(Case(*chunk(lens, per), H).cuda())
+    run_and_check(Case(*chunk(lens, per), H, block=16).cuda(), window=100, n_sink=2)
+
+
+def test_as_many_items_as_threads():
+    for tokens in (382, 383, 384):                            # 382 items and their sequence, to 385
+        run_and_check(Case(*chunk([tokens, 3], [tokens, 1]), 128).cuda(), window=33, n_sink=1)
