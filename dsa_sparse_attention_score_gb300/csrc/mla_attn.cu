@@ -165,6 +165,7 @@ struct Problem {
     int window;                   // INT32_MAX: every position
     int n_sink;
     const int32_t *sink_pos0;     // null: 0
+    int align;                    // of a tile's first position
 };
 
 // Up to 128 query rows of one sequence and the positions some of them see:
@@ -175,8 +176,8 @@ struct __align__(16) Item {
     int32_t cost0;                    // costs of the items before
     int32_t lo, hi, s_lo, s_hi;       // hi < 0: nothing
     int32_t min_pos;                  // the least position of its tokens (those that see anything)
-    int32_t first_tile, n_first;      // tiles of the first positions before those of [lo, hi]
-    int32_t tile0, n;                 // first tile of [lo, hi]; all tiles
+    int32_t first_pos, n_first;       // tiles of the first positions before pos0, from first_pos on
+    int32_t pos0, n;                  // first position of the tiles of [lo, hi]; all tiles
     int64_t kv0;
 };
 
@@ -186,20 +187,24 @@ __device__ __forceinline__ void item_tiles(const Problem &p, Item &it) {
     it.n = it.n_first = 0;
     it.s_lo = it.s_hi = 0;
     it.lo = 0;
-    it.tile0 = it.first_tile = 0;
+    it.pos0 = it.first_pos = 0;
     if (it.hi < 0) return;
     // 64 bits: a window near 2^31 must not wrap
     it.lo = (int)max((int64_t)0, (int64_t)it.min_pos - p.window + 1);
-    it.tile0 = it.lo / kKeys;
-    it.n = it.hi / kKeys - it.tile0 + 1;
+    // Tiles begin where the rows of a box may: a window of 1000 takes 8 of them, from a
+    // grid of 128 on mostly 9 (a prefill through it 269 -> @@ us).  (The last tile of positions
+    // close to 2^31 must not wrap.)
+    const int align = it.hi > INT32_MAX - 2 * kKeys ? kKeys : p.align;
+    it.pos0 = it.lo / align * align;
+    it.n = (it.hi - it.pos0) / kKeys + 1;
     if (p.n_sink > 0) {
         const int a = p.sink_pos0 ? max(0, __ldg(p.sink_pos0 + it.seq)) : 0;
         const int e = (int)min((int64_t)a + p.n_sink, (int64_t)it.hi + 1);
         if (a < e) {
             it.s_lo = a;
             it.s_hi = e;
-            it.first_tile = a / kKeys;
-            it.n_first = max(0, min((e - 1) / kKeys + 1, it.tile0) - it.first_tile);
+            it.first_pos = a / align * align;
+            it.n_first = a < it.pos0 ? (min(e, it.pos0) - it.first_pos + kKeys - 1) / kKeys : 0;
             it.n += it.n_first;
         }
     }
@@ -220,7 +225,7 @@ struct Split { int32_t row0, nrows, first, parts; }; // an item that begins in a
 // A piece of an item, for every warp of the CTA (Ctl::piece).
 struct Piece {
     int32_t t0, t1;               // tiles of the item to do; t0 == t1: an item that sees nothing
-    int32_t n_first, first_tile, tile0;
+    int32_t n_first, first_pos, pos0;
     int32_t lo, hi, s_lo, s_hi, min_pos;   // as in Item
     int32_t row0, nrows, seq;
     int32_t whole;                // all tiles of the item
@@ -250,7 +255,7 @@ static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 // Position of tile i's first key.
 __device__ __forceinline__ int tile_pos(const Piece &it, int i) {
-    return (i < it.n_first ? it.first_tile + i : it.tile0 + i - it.n_first) * kKeys;
+    return i < it.n_first ? it.first_pos + i * kKeys : it.pos0 + (i - it.n_first) * kKeys;
 }
 __device__ __forceinline__ bool seen_by_some(const Piece &it, int pos) {
     return (pos >= it.lo && pos <= it.hi) || (pos >= it.s_lo && pos < it.s_hi);
@@ -412,8 +417,8 @@ struct Todo {
             off = 0;
         }
         pc.n_first = it.n_first;
-        pc.first_tile = it.first_tile;
-        pc.tile0 = it.tile0;
+        pc.first_pos = it.first_pos;
+        pc.pos0 = it.pos0;
         pc.lo = it.lo;
         pc.hi = it.hi;
         pc.s_lo = it.s_lo;
@@ -1043,8 +1048,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!pc->end) pos = known ? next_pos : row_pos(pc);
             // Every row of the item sees every key of the tiles [clear0, clear1).
             const int64_t open = (int64_t)pc->hi - p.pr.window + 1;      // the last token's window begins here
-            const int clear0 = n_first + (open <= 0 ? 0 : (int)((open + kKeys - 1) / kKeys)) - pc->tile0;
-            const int clear1 = plain ? n_first + (pc->min_pos + 1) / kKeys - pc->tile0 : 0;
+            const int clear0 = n_first + (open <= pc->pos0 ? 0 : (int)(open - pc->pos0 + kKeys - 1) / kKeys);
+            const int clear1 = plain ? n_first + (pc->min_pos + 1 - pc->pos0) / kKeys : 0;
             float m = -INFINITY, l = 0.f;                     // m: as of this group's last tile
             const uint32_t g0 = g;                            // of the piece's first tile
             if (owed) {
@@ -1155,11 +1160,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t s_tmem = lane_tmem + kColS + (g & 1u) * (kKeys / 2);
                 if (alive) alive = wait_bar(smem_u32(&ctl.s_full[g & 1u]), (g >> 1) & 1u, ctl, p.status, limit);
                 tc_fence_after();
-                if ((i < max(clear0, n_first) || i >= clear1) && alive) {
+                if ((i < clear0 || i >= clear1) && alive) {
                     // one bit a key of this half: the window's and the first ones'
                     const int kp = tile_pos(*pc, i) + kHalf * half;
                     const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);
-                    const uint64_t see = key_bits(from - kp, pos + 1 - kp) | key_bits(pc->s_lo - kp, min(pc->s_hi, pos + 1) - kp);
+                    // (keys of the first tiles from pos0 on are those of the others)
+                    const uint64_t see = (key_bits(from - kp, pos + 1 - kp) | key_bits(pc->s_lo - kp, min(pc->s_hi, pos + 1) - kp)) &
+                                         key_bits(0, i < n_first ? pc->pos0 - kp : kHalf);
                     const float factor = plain ? 1.f : p.scale_log2;
 #pragma unroll 1
                     for (int c = 0; c < 64; c += 16) {
@@ -1508,7 +1515,7 @@ size_t mla_attn_workspace(int T, int B, int H) { return mla_layout(T, B, H, kSta
 
 bool mla_attn_countable(int T, int B, int H, int max_kv) {
     // costs are 32-bit numbers
-    return mla_layout(T, B, H, kStatusBytes).max_items * ((int64_t)max_kv / kKeys + 2 + kItemCost) < INT32_MAX;
+    return mla_layout(T, B, H, kStatusBytes).max_items * ((int64_t)max_kv / kKeys + 3 + kItemCost) < INT32_MAX;
 }
 
 cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBatch &b, void *ws, cudaStream_t stream) {
@@ -1516,7 +1523,6 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     uint8_t *w = static_cast<uint8_t *>(ws);
     uint32_t *status = reinterpret_cast<uint32_t *>(w);
     MlaParams p{};
-    p.pr = Problem{b, a.H, a.window, a.n_sink, a.sink_pos0};
     p.status = status;
     p.q_lat = a.q_lat;
     PlanHead *head = reinterpret_cast<PlanHead *>(w + L.head);
@@ -1539,6 +1545,8 @@ cudaError_t launch_mla_attn(const MlaLaunch &a, const MlaMaps &maps, const DevBa
     p.scale_log2 = a.sm_scale * 1.4426950408889634f;
     p.tail = a.tail;
     p.rows_per_box = !b.block_table || b.block_size % 64 == 0 ? 64 : b.block_size % 16 == 0 ? 16 : 0;
+    // (a box must not pass the end of a page)
+    p.pr = Problem{b, a.H, a.window, a.n_sink, a.sink_pos0, b.block_table && p.rows_per_box ? p.rows_per_box : 1};
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(mla_attn_kernel), 12, kSmem);
     if (e != cudaSuccess) return e;
     if (!here) {

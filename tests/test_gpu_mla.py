@@ -306,3 +306,12 @@ def test_a_few_tokens_a_sequence(H):
 def test_as_many_items_as_threads():
     for tokens in (382, 383, 384):                            # 382 items and their sequence, to 385
         run_and_check(Case(*chunk([tokens, 3], [tokens, 1]), 128).cuda(), window=33, n_sink=1)
+
+
+@pytest.mark.parametrize("window,sinks", [(130, 0), (37, 150), (300, 17), (257, 300)])
+@pytest.mark.parametrize("block", [0, 7, 16, 48, 64, 100, 128])
+def test_windows_over_pages_of_any_size(window, sinks, block):
+    """Windows and first positions that begin and end inside pages, and meet or not."""
+    c = Case(*chunk([777, 300, 520], [5, 2, 3]), 33, block=block).cuda()
+    a = torch.tensor([0, 5, 130], dtype=torch.int32, device="cuda")
+    run_and_check(c, window=window, n_sink=sinks, sink_pos0=a)
