@@ -29,7 +29,7 @@
 // Warps 0-7 are softmax and output, in two groups that take the tiles in turn; one
 // warp each issues S's and O's products and copies keys and values.
 // Measured: 2048 tokens of 64 heads after 6144 positions 1.26 ms (1.62 PFLOP/s, 86%
-// of the card's measured rate: 2450 clocks a tile, the tensor pipe 86% busy); 32
+// of the card's measured rate: 2450 clocks a tile, the tensor pipe 85% busy); 32
 // sequences of 4k-64k positions, 128 heads, one token each 0.26 ms (5.0 TB/s: 3700
 // clocks a tile, what HBM takes to deliver it being 2800); 8 of 8192, 64 heads 31 us (HBM's
 // share is 11: the first S comes 6 us after the launch, the output of the last
@@ -178,6 +178,7 @@ struct __align__(16) Item {
     int32_t min_pos;                  // the least position of its tokens (those that see anything)
     int32_t first_pos, n_first;       // tiles of the first positions before pos0, from first_pos on
     int32_t pos0, n;                  // first position of the tiles of [lo, hi]; all tiles
+    int32_t wrap;                     // the last tile's keys from here on are positions from first_pos on (128: none)
     int64_t kv0;
 };
 
@@ -188,11 +189,12 @@ __device__ __forceinline__ void item_tiles(const Problem &p, Item &it) {
     it.s_lo = it.s_hi = 0;
     it.lo = 0;
     it.pos0 = it.first_pos = 0;
+    it.wrap = kKeys;
     if (it.hi < 0) return;
     // 64 bits: a window near 2^31 must not wrap
     it.lo = (int)max((int64_t)0, (int64_t)it.min_pos - p.window + 1);
     // Tiles begin where the rows of a box may: a window of 1000 takes 8 of them, from a
-    // grid of 128 on mostly 9 (a prefill through it 269 -> @@ us).  (The last tile of positions
+    // grid of 128 on mostly 9 (a prefill through it 270 -> 259 us).  (The last tile of positions
     // close to 2^31 must not wrap.)
     const int align = it.hi > INT32_MAX - 2 * kKeys ? kKeys : p.align;
     it.pos0 = it.lo / align * align;
@@ -204,7 +206,12 @@ __device__ __forceinline__ void item_tiles(const Problem &p, Item &it) {
             it.s_lo = a;
             it.s_hi = e;
             it.first_pos = a / align * align;
-            it.n_first = a < it.pos0 ? (min(e, it.pos0) - it.first_pos + kKeys - 1) / kKeys : 0;
+            // Those before pos0 behind the last tile's own keys, if there is room (259 -> 241 us),
+            // else in tiles of their own.
+            const int more = a < it.pos0 ? min(e, it.pos0) - it.first_pos : 0;
+            const int used = ((it.hi - it.pos0) % kKeys / kGroup + 1) * kGroup;
+            if (more > 0 && used + more <= kKeys) it.wrap = used;
+            else it.n_first = (more + kKeys - 1) / kKeys;
             it.n += it.n_first;
         }
     }
@@ -222,10 +229,24 @@ __device__ __forceinline__ int share(int total, int c, int n) {
 struct Start { int32_t item, off; };                 // a cluster's first item and the costs of it done before
 struct Split { int32_t row0, nrows, first, parts; }; // an item that begins in a cluster and ends in a later one
 
+// Where an item's tiles are: n_first of the first positions, from first_pos on, then
+// those of the others, from pos0 on; the last one's keys from `wrap` on are first
+// positions again (128: none).
+struct Grid {
+    int32_t n_first, first_pos, pos0, last, wrap;
+    // position of tile i's first key, and of one of its keys
+    __device__ __forceinline__ int tile(int i) const { return i < n_first ? first_pos + i * kKeys : pos0 + (i - n_first) * kKeys; }
+    __device__ __forceinline__ int key(int i, int k) const {
+        int pos = tile(i) + k;
+        if (i == last && k >= wrap) pos = first_pos + k - wrap;
+        return pos;
+    }
+};
+
 // A piece of an item, for every warp of the CTA (Ctl::piece).
 struct Piece {
     int32_t t0, t1;               // tiles of the item to do; t0 == t1: an item that sees nothing
-    int32_t n_first, first_pos, pos0;
+    Grid grid;
     int32_t lo, hi, s_lo, s_hi, min_pos;   // as in Item
     int32_t row0, nrows, seq;
     int32_t whole;                // all tiles of the item
@@ -253,10 +274,6 @@ struct Ctl {
 constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
-// Position of tile i's first key.
-__device__ __forceinline__ int tile_pos(const Piece &it, int i) {
-    return i < it.n_first ? it.first_pos + i * kKeys : it.pos0 + (i - it.n_first) * kKeys;
-}
 __device__ __forceinline__ bool seen_by_some(const Piece &it, int pos) {
     return (pos >= it.lo && pos <= it.hi) || (pos >= it.s_lo && pos < it.s_hi);
 }
@@ -265,8 +282,15 @@ __device__ __forceinline__ uint32_t groups_of(int lo, int hi) {   // from the ti
     const int g0 = max(lo, 0) / kGroup, g1 = min(hi, kKeys - 1) / kGroup;
     return hi < 0 || g0 > g1 ? 0u : (0xffu << g0) & (0xffu >> (kKeys / kGroup - 1 - g1));
 }
-__device__ __forceinline__ uint32_t tile_groups(const Piece &it, int p0) {
-    return groups_of(it.lo - p0, it.hi - p0) | groups_of(it.s_lo - p0, it.s_hi - 1 - p0);
+__device__ __forceinline__ uint32_t tile_groups(const Piece &it, const Grid &grid, int i) {
+    const int p0 = grid.tile(i);
+    if (p0 >= it.lo && p0 + kKeys - 1 <= it.hi) return 0xffu;
+    uint32_t m = groups_of(it.lo - p0, it.hi - p0) | groups_of(it.s_lo - p0, it.s_hi - 1 - p0);
+    if (i == grid.last && grid.wrap < kKeys) {
+        const int p1 = grid.first_pos - grid.wrap;
+        m |= groups_of(it.s_lo - p1, min(it.s_hi, grid.pos0) - 1 - p1);
+    }
+    return m;
 }
 
 struct MlaParams {
@@ -416,9 +440,7 @@ struct Todo {
             ++(by_seq ? seq : item);
             off = 0;
         }
-        pc.n_first = it.n_first;
-        pc.first_pos = it.first_pos;
-        pc.pos0 = it.pos0;
+        pc.grid = Grid{it.n_first, it.first_pos, it.pos0, it.n - 1, it.wrap};
         pc.lo = it.lo;
         pc.hi = it.hi;
         pc.s_lo = it.s_lo;
@@ -703,8 +725,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!pc || pc->end) break;
             const int t0 = pc->t0, t1 = pc->t1, seq = pc->seq;
             const int64_t kv0 = pc->kv0;
+            const Grid grid = pc->grid;
             for (int i = t0; alive && i < t1; ++i, ++g) {
-                const int a = tile_pos(*pc, i) + kHalf * (int)rank + mine * step;
+                // (a half with keys of two places: boxes of 16)
+                const bool mixed = i == grid.last && grid.wrap < kHalf * ((int)rank + 1) && p.rows_per_box == 64;
+                const int a = grid.key(i, kHalf * (int)rank + (mixed ? (lane & 3) * kGroup : mine * step));
                 int4 r = make_int4(0, 0, 0, 0);
                 if (p.rows_per_box) r.x = max(0, any_row(b, seq, kv0, a));
                 else r = four_any_rows(b, pc, a);
@@ -741,7 +766,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         __syncwarp();
                     }
                     if (b.skip_copies) continue;
-                    if (p.rows_per_box == 64) {
+                    if (p.rows_per_box == 64 && !mixed) {
                         if (elect_one()) {
                             arrive_expect_remote(full, (uint32_t)(nb * kBlock));
 #pragma unroll
@@ -751,7 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         continue;
                     }
-                    if (p.rows_per_box == 16) {
+                    if (p.rows_per_box) {
                         if (elect_one()) {
                             arrive_expect_remote(full, (uint32_t)(nb * kBlock));
 #pragma unroll 1
@@ -788,16 +813,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Piece *pc = rd.next(ctl, p.status, limit);
             if (!pc || pc->end) break;
             const int t1 = pc->t1, lo = pc->lo, hi = pc->hi, s_lo = pc->s_lo, s_hi = pc->s_hi;
+            const Grid grid = pc->grid;
             int32_t spare = -1;                               // not looked up yet
             for (int i = pc->t0; alive && i < t1; ++i, ++g) {
-                const int pos = tile_pos(*pc, i);
-                const uint32_t groups = tile_groups(*pc, pos);
+                const uint32_t groups = tile_groups(*pc, grid, i);
                 // where a group's 16 rows lie together, lane j looks group j up; one that is
                 // seen in full is a box
                 int32_t first = -1;
                 uint32_t ones = 0;
                 if (p.rows_per_box) {
-                    const int a = pos + kGroup * (lane & 7), e = a + kGroup - 1;
+                    const int a = grid.key(i, kGroup * (lane & 7)), e = a + kGroup - 1;
                     if (groups >> (lane & 7) & 1u) {
                         first = any_row(b, pc->seq, pc->kv0, a);
                         if (first < 0) flag(p.status, DSA_DEV_BAD_INDEX);
@@ -808,7 +833,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 int4 r = make_int4(0, 0, 0, 0);
                 if (groups & ~ones) {
                     if (spare < 0) spare = spare_row(b, pc);
-                    const int a = pos + 4 * lane;
+                    const int a = grid.key(i, 4 * lane);
                     if (p.rows_per_box) {
                         const int32_t row = __shfl_sync(0xffffffffu, first, lane >> 2), at = row + 4 * (lane & 3);
                         r.x = row >= 0 && seen_by_some(*pc, a) ? at : spare;
@@ -830,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint32_t mine = __reduce_or_sync(0xffffffffu, ones >> (4 * h) & 0xfu);
                     int row[4];
                     row[0] = __reduce_max_sync(0xffffffffu, __shfl_sync(0xffffffffu, first, 4 * h));
-                    if (p.rows_per_box == 64 && mine == 0xfu) {
+                    if (p.rows_per_box == 64 && mine == 0xfu && (i < grid.last || grid.wrap >= 64 * (h + 1))) {
                         // the half's four blocks of this CTA's dims
                         if (elect_one()) {
                             arrive_expect_remote(full, kVHalf);
@@ -926,7 +951,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint64_t pd = sdesc_sw128(s0 + kPOff, 16, 1024), vd = sdesc_sw128(s0 + kVOff, kBlock, 1024);
 #pragma unroll 1
                     for (int i = t0; alive && i < t1; ++i, ++g) {
-                        const uint32_t groups = __reduce_or_sync(0xffffffffu, tile_groups(*pc, tile_pos(*pc, i)));
+                        const uint32_t groups = __reduce_or_sync(0xffffffffu, tile_groups(*pc, pc->grid, i));
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
                             alive = wait_bar(smem_u32(&ctl.v_full[buf]), v_parity, ctl, p.status, limit);
@@ -1044,12 +1069,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Piece *pc = rd.next(ctl, p.status, limit);
             if (named_barrier_or(7, kSoftmaxWarps * 32, !pc)) break;
             if (pc->end && !owed) break;
-            const int t0 = pc->t0, t1 = pc->t1, n_first = pc->n_first;
+            const int t0 = pc->t0, t1 = pc->t1, n_first = pc->grid.n_first;
             if (!pc->end) pos = known ? next_pos : row_pos(pc);
             // Every row of the item sees every key of the tiles [clear0, clear1).
             const int64_t open = (int64_t)pc->hi - p.pr.window + 1;      // the last token's window begins here
-            const int clear0 = n_first + (open <= pc->pos0 ? 0 : (int)(open - pc->pos0 + kKeys - 1) / kKeys);
-            const int clear1 = plain ? n_first + (pc->min_pos + 1 - pc->pos0) / kKeys : 0;
+            const int clear0 = n_first + (open <= pc->grid.pos0 ? 0 : (int)(open - pc->grid.pos0 + kKeys - 1) / kKeys);
+            const int clear1 = plain ? n_first + (pc->min_pos + 1 - pc->grid.pos0) / kKeys : 0;
             float m = -INFINITY, l = 0.f;                     // m: as of this group's last tile
             const uint32_t g0 = g;                            // of the piece's first tile
             if (owed) {
@@ -1162,11 +1187,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if ((i < clear0 || i >= clear1) && alive) {
                     // one bit a key of this half: the window's and the first ones'
-                    const int kp = tile_pos(*pc, i) + kHalf * half;
+                    const int kp = pc->grid.tile(i) + kHalf * half;
                     const int from = (int)max((int64_t)0, (int64_t)pos - p.pr.window + 1);
                     // (keys of the first tiles from pos0 on are those of the others)
-                    const uint64_t see = (key_bits(from - kp, pos + 1 - kp) | key_bits(pc->s_lo - kp, min(pc->s_hi, pos + 1) - kp)) &
-                                         key_bits(0, i < n_first ? pc->pos0 - kp : kHalf);
+                    uint64_t see = (key_bits(from - kp, pos + 1 - kp) | key_bits(pc->s_lo - kp, min(pc->s_hi, pos + 1) - kp)) &
+                                   key_bits(0, i < n_first ? pc->grid.pos0 - kp : kHalf);
+                    if (i == pc->grid.last && pc->grid.wrap < kKeys) {
+                        const int cut = pc->grid.wrap - kHalf * half, ks = pc->grid.first_pos - cut;
+                        see = (see & key_bits(0, cut)) | key_bits(pc->s_lo - ks, min(min(pc->s_hi, pc->grid.pos0), pos + 1) - ks);
+                    }
                     const float factor = plain ? 1.f : p.scale_log2;
 #pragma unroll 1
                     for (int c = 0; c < 64; c += 16) {
