@@ -1073,7 +1073,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!pc->end) pos = known ? next_pos : row_pos(pc);
             // Every row of the item sees every key of the tiles [clear0, clear1).
             const int64_t open = (int64_t)pc->hi - p.pr.window + 1;      // the last token's window begins here
-            const int clear0 = n_first + (open <= pc->grid.pos0 ? 0 : (int)(open - pc->grid.pos0 + kKeys - 1) / kKeys);
+            const int clear0 = n_first + (open <= pc->grid.pos0 ? 0 : (int)((open - pc->grid.pos0 + kKeys - 1) / kKeys));
             const int clear1 = plain ? n_first + (pc->min_pos + 1 - pc->grid.pos0) / kKeys : 0;
             float m = -INFINITY, l = 0.f;                     // m: as of this group's last tile
             const uint32_t g0 = g;                            // of the piece's first tile
