@@ -28,13 +28,14 @@
 // and values in halves of a tile, each as soon as the product that read it is done.
 // Warps 0-7 are softmax and output, in two groups that take the tiles in turn; one
 // warp each issues S's and O's products and copies keys and values.
-// Measured: 2048 tokens of 64 heads after 6144 positions 1.26 ms (1.62 PFLOP/s, 86%
-// of the card's measured rate: 2450 clocks a tile, the tensor pipe 85% busy); 32
-// sequences of 4k-64k positions, 128 heads, one token each 0.26 ms (5.0 TB/s: 3700
-// clocks a tile, what HBM takes to deliver it being 2800); 8 of 8192, 64 heads 31 us (HBM's
-// share is 11: the first S comes 6 us after the launch, the output of the last
-// piece takes 2.5 and the join 5).  What bounds calls with many short items is the
-// change of pieces, 7000 clocks in which the tensor core waits for an output.
+// Measured: 2048 tokens of 64 heads after 6144 positions 1.26 ms in a row of calls
+// (1.62 PFLOP/s, 95% of the sustained rate of the card's library products; the power
+// cap holds the clock at 1.6 GHz, one kernel at 2.07 GHz takes 1.09 ms): 2450 clocks a
+// tile, the tensor pipe 85% busy.  32 sequences of 4k-64k positions, 128 heads, one
+// token each 0.26 ms (5.0 TB/s: 3700 clocks a tile; HBM delivers one in 2800).  8 of
+// 8192, 64 heads 31 us (HBM's share is 11: the first S comes 6 us after the launch, the
+// output of the last piece takes 2.5 and the join 5).  What bounds calls of many short
+// items is the change of pieces, 7000 clocks in which the tensor core waits for an output.
 //
 // The work is cut by tiles, not by items: the tiles of all items in a row are
 // divided evenly among the clusters.  An item that several clusters share gets
