@@ -275,10 +275,8 @@ struct Ctl {
 constexpr size_t kSmem = kCtlOff + sizeof(Ctl);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
-__device__ __forceinline__ bool seen_by_some(const Piece &it, int pos) {
-    return (pos >= it.lo && pos <= it.hi) || (pos >= it.s_lo && pos < it.s_hi);
-}
-// The tile's groups of 16 keys with a position that some row sees, one bit each.
+// The tile's groups of 16 keys with a position between the first and the last that some
+// row sees, one bit each.
 __device__ __forceinline__ uint32_t groups_of(int lo, int hi) {   // from the tile's first key on, both included
     const int g0 = max(lo, 0) / kGroup, g1 = min(hi, kKeys - 1) / kGroup;
     return hi < 0 || g0 > g1 ? 0u : (0xffu << g0) & (0xffu >> (kKeys / kGroup - 1 - g1));
@@ -472,14 +470,63 @@ struct Scheduler {
     __device__ __forceinline__ bool write(const MlaParams &p, Ctl &ctl, int lane);
 };
 
-// That of a position that some row of the piece sees, its spare one for any other.
-__device__ __forceinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
-    if (!seen_by_some(*pc, pos)) return spare;
-    const int32_t r = any_row(b, pc->seq, pc->kv0, pos);
-    if (r >= 0) return r;
-    flag(status, DSA_DEV_BAD_INDEX);
-    return spare;
+// Of rows that no token sees not even 0 times a value may come into a product, and their
+// blocks need not be there.  The tokens of a piece see all positions between its first
+// and its last one, unless their windows do not meet.  Those rare pieces are looked at
+// token by token, out of the usual path.  (Parameters by value: behind a reference they
+// are loaded through generic addresses.)
+struct Tokens {
+    const int32_t *q_pos;           // of the piece's first token
+    int32_t n, max_kv, window;
+};
+__device__ __forceinline__ Tokens tokens_of(const Problem &p, const Piece *pc) {
+    const DevBatch &b = p.b;
+    const int first = pc->row0 / p.H;
+    return Tokens{b.q_pos + first, (pc->row0 + pc->nrows - 1) / p.H - first + 1, b.max_kv, p.window};
 }
+// The position of token t of them if it is in bounds, else a negative number.
+__device__ __forceinline__ int position_in_order(const Tokens &k, int t) {
+    const int pos = t < k.n ? __ldg(k.q_pos + t) : -1;
+    return pos < k.max_kv ? pos : -1;
+}
+// Do tokens in order see all positions between the least one's window's begin and the last?
+__device__ __noinline__ bool all_between_seen(const Tokens k) {
+    const int lane = threadIdx.x & 31;
+    int before = -1;                                          // position of the last token in order so far
+    bool gaps = false;
+#pragma unroll 1
+    for (int t = 0; t < k.n; t += 32) {
+        const int pos = position_in_order(k, t + lane);
+        // windows that meet from token to token leave no gap, whatever the order
+        const uint32_t there = __ballot_sync(0xffffffffu, pos >= 0), ahead = there & ((1u << lane) - 1);
+        const int x = __shfl_sync(0xffffffffu, pos, ahead ? 31 - __clz(ahead) : 0), to = ahead ? x : before;
+        gaps |= pos >= 0 && to >= 0 && abs(pos - to) > k.window;
+        const int y = __shfl_sync(0xffffffffu, pos, there ? 31 - __clz(there) : 0);
+        if (there) before = y;
+    }
+    return !__any_sync(0xffffffffu, gaps);
+}
+// Which of the four positions from `a` on (its own of each lane) some token in order sees,
+// as bits; [s_lo, s_hi) are the first ones.
+__device__ __noinline__ uint32_t seen_token_by_token(const Tokens k, int s_lo, int s_hi, int a) {
+    const int lane = threadIdx.x & 31;
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int t = 0; t < k.n; t += 32) {
+        const int pos = position_in_order(k, t + lane);
+#pragma unroll 1
+        for (int j = 0; j < min(32, k.n - t); ++j) {
+            const int last = __shfl_sync(0xffffffffu, pos, j), before = last - k.window;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int x = a + e;
+                m |= (uint32_t)(x <= last && (x > before || (x >= s_lo && x < s_hi))) << e;
+            }
+        }
+    }
+    return m;
+}
+
 // The row of a piece's last position, which may be read for positions that no row
 // sees; row 0 if that has none (no row sees anything then).
 __device__ __forceinline__ int32_t spare_row(const DevBatch &b, const Piece *pc) {
@@ -544,10 +591,18 @@ __device__ __noinline__ void copy_values(uint32_t dst, const CUtensorMap *kv1, u
         __syncwarp();
     }
 }
-// The rows of the four keys from `pos` on.
-__device__ __forceinline__ int4 four_rows(const DevBatch &b, uint32_t *status, const Piece *pc, int pos, int32_t spare) {
-    return make_int4(row_or_spare(b, status, pc, pos, spare), row_or_spare(b, status, pc, pos + 1, spare),
-                     row_or_spare(b, status, pc, pos + 2, spare), row_or_spare(b, status, pc, pos + 3, spare));
+// That of a position, the spare one where nobody sees it.
+__device__ __forceinline__ int32_t row_or_spare(const DevBatch &b, uint32_t *status, const Piece *pc, bool seen, int pos, int32_t spare) {
+    if (!seen) return spare;
+    const int32_t r = any_row(b, pc->seq, pc->kv0, pos);
+    if (r >= 0) return r;
+    flag(status, DSA_DEV_BAD_INDEX);
+    return spare;
+}
+// The rows of the four keys from `pos` on, of which those in the bits `see` are seen.
+__device__ __forceinline__ int4 four_rows(const DevBatch &b, uint32_t *status, const Piece *pc, uint32_t see, int pos, int32_t spare) {
+    return make_int4(row_or_spare(b, status, pc, see & 1u, pos, spare), row_or_spare(b, status, pc, see & 2u, pos + 1, spare),
+                     row_or_spare(b, status, pc, see & 4u, pos + 2, spare), row_or_spare(b, status, pc, see & 8u, pos + 3, spare));
 }
 __device__ __forceinline__ int4 four_any_rows(const DevBatch &b, const Piece *pc, int pos) {
     return make_int4(max(0, any_row(b, pc->seq, pc->kv0, pos)), max(0, any_row(b, pc->seq, pc->kv0, pos + 1)),
@@ -803,9 +858,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kVWarp) {
         // ---------------- values: all keys of a tile in two halves, this CTA's 256 dims.
-        // Groups of 16 keys that nobody sees are neither read nor multiplied; in a
-        // group that is seen in part the other rows are the spare one's copies
-        // (P is 0 there, and 0 times what an unused row may hold is not).
+        // Groups of 16 keys before the first position that some token sees, or behind the
+        // last one, are neither read nor multiplied; in the others a row that nobody sees
+        // is a copy of one that somebody does (P is 0 there, and 0 times what an unused
+        // row may hold is not).
         uint32_t g = 0, buf = 0;                              // tiles so far, the next half's place
         bool alive = true;
         const uint32_t v_bar = dsmem_map(smem_u32(&ctl.v_full[0]), 0);
@@ -815,34 +871,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!pc || pc->end) break;
             const int t1 = pc->t1, lo = pc->lo, hi = pc->hi, s_lo = pc->s_lo, s_hi = pc->s_hi;
             const Grid grid = pc->grid;
+            // The last token sees all back to its window's begin, the least one's sees from lo on.
+            const bool odd = lo < (int64_t)hi - p.pr.window + 1 && hi - pc->min_pos > p.pr.window && !all_between_seen(tokens_of(p.pr, pc));
             int32_t spare = -1;                               // not looked up yet
             for (int i = pc->t0; alive && i < t1; ++i, ++g) {
                 const uint32_t groups = tile_groups(*pc, grid, i);
                 // where a group's 16 rows lie together, lane j looks group j up; one that is
                 // seen in full is a box
                 int32_t first = -1;
-                uint32_t ones = 0;
+                uint32_t ones = 0, see = 0;
+                if (odd) see = seen_token_by_token(tokens_of(p.pr, pc), s_lo, s_hi, grid.key(i, 4 * lane));
                 if (p.rows_per_box) {
                     const int a = grid.key(i, kGroup * (lane & 7)), e = a + kGroup - 1;
-                    if (groups >> (lane & 7) & 1u) {
+                    bool some = groups >> (lane & 7) & 1u, all = (a >= lo && e <= hi) || (a >= s_lo && e < s_hi);
+                    if (odd) {
+                        const uint32_t some4 = __ballot_sync(0xffffffffu, see != 0), all4 = __ballot_sync(0xffffffffu, see == 0xfu);
+                        some &= (some4 >> (4 * (lane & 7)) & 0xfu) != 0;
+                        all = (all4 >> (4 * (lane & 7)) & 0xfu) == 0xfu;
+                    }
+                    if (some) {
                         first = any_row(b, pc->seq, pc->kv0, a);
                         if (first < 0) flag(p.status, DSA_DEV_BAD_INDEX);
                     }
-                    ones = __ballot_sync(0xffffffffu, first >= 0 && ((a >= lo && e <= hi) || (a >= s_lo && e < s_hi))) & 0xffu;
+                    ones = __ballot_sync(0xffffffffu, first >= 0 && all) & 0xffu;
                 }
                 // the other groups' rows, four a lane
                 int4 r = make_int4(0, 0, 0, 0);
                 if (groups & ~ones) {
                     if (spare < 0) spare = spare_row(b, pc);
                     const int a = grid.key(i, 4 * lane);
+                    if (!odd) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            see |= (uint32_t)((a + e >= lo && a + e <= hi) || (a + e >= s_lo && a + e < s_hi)) << e;
+                    }
                     if (p.rows_per_box) {
                         const int32_t row = __shfl_sync(0xffffffffu, first, lane >> 2), at = row + 4 * (lane & 3);
-                        r.x = row >= 0 && seen_by_some(*pc, a) ? at : spare;
-                        r.y = row >= 0 && seen_by_some(*pc, a + 1) ? at + 1 : spare;
-                        r.z = row >= 0 && seen_by_some(*pc, a + 2) ? at + 2 : spare;
-                        r.w = row >= 0 && seen_by_some(*pc, a + 3) ? at + 3 : spare;
+                        r.x = row >= 0 && see & 1u ? at : spare;
+                        r.y = row >= 0 && see & 2u ? at + 1 : spare;
+                        r.z = row >= 0 && see & 4u ? at + 2 : spare;
+                        r.w = row >= 0 && see & 8u ? at + 3 : spare;
                     } else {
-                        r = four_rows(b, p.status, pc, a, spare);
+                        r = four_rows(b, p.status, pc, see, a, spare);
                     }
                 }
 #pragma unroll 1
