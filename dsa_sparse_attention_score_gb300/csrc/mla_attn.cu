@@ -472,31 +472,41 @@ struct Scheduler {
 
 // Of rows that no token sees not even 0 times a value may come into a product, and their
 // blocks need not be there.  The tokens of a piece see all positions between its first
-// and its last one, unless their windows do not meet.  Those rare pieces are looked at
-// token by token, out of the usual path.  (Parameters by value: behind a reference they
-// are loaded through generic addresses.)
+// and its last one, unless some are not in order or their windows do not meet.  Those
+// rare pieces are looked at token by token, out of the usual path.  (Parameters by value:
+// behind a reference they are loaded through generic addresses.)
 struct Tokens {
-    const int32_t *q_pos;           // of the piece's first token
-    int32_t n, max_kv, window;
+    const int32_t *q_pos, *table;   // of the piece's first token; the sequence's blocks (null: contiguous)
+    int64_t kv0, cache_rows;
+    int32_t n, max_kv, block_size, max_blocks, window;
 };
 __device__ __forceinline__ Tokens tokens_of(const Problem &p, const Piece *pc) {
     const DevBatch &b = p.b;
     const int first = pc->row0 / p.H;
-    return Tokens{b.q_pos + first, (pc->row0 + pc->nrows - 1) / p.H - first + 1, b.max_kv, p.window};
+    return Tokens{b.q_pos + first, b.block_table ? b.block_table + (int64_t)pc->seq * b.max_blocks : nullptr, pc->kv0, b.cache_rows,
+                  (pc->row0 + pc->nrows - 1) / p.H - first + 1, b.max_kv, b.block_size, b.max_blocks, p.window};
 }
-// The position of token t of them if it is in bounds, else a negative number.
+// The position of token t of them if it is in order, else -1.
 __device__ __forceinline__ int position_in_order(const Tokens &k, int t) {
     const int pos = t < k.n ? __ldg(k.q_pos + t) : -1;
-    return pos < k.max_kv ? pos : -1;
+    if (pos < 0 || pos >= k.max_kv || k.kv0 < 0) return -1;
+    int64_t r = k.kv0 + pos;
+    if (k.table) {
+        const int blk = pos / k.block_size, e = blk < k.max_blocks ? __ldg(k.table + blk) : -1;
+        r = e < 0 ? -1 : (int64_t)e * k.block_size + (pos - blk * k.block_size);
+    }
+    return r >= 0 && r < k.cache_rows ? pos : -1;
 }
-// Do tokens in order see all positions between the least one's window's begin and the last?
-__device__ __noinline__ bool all_between_seen(const Tokens k) {
+// x: do tokens in order see all positions between the first that a window from `least`
+// reaches back to, and `hi`?  y: the largest position in order (-1: none).
+__device__ __noinline__ int2 all_between_seen(const Tokens k, int least, int hi) {
     const int lane = threadIdx.x & 31;
-    int before = -1;                                          // position of the last token in order so far
+    int lo = INT32_MAX, last = -1, before = -1;               // before: the last token's in order so far
     bool gaps = false;
 #pragma unroll 1
     for (int t = 0; t < k.n; t += 32) {
         const int pos = position_in_order(k, t + lane);
+        if (pos >= 0) lo = min(lo, pos), last = max(last, pos);
         // windows that meet from token to token leave no gap, whatever the order
         const uint32_t there = __ballot_sync(0xffffffffu, pos >= 0), ahead = there & ((1u << lane) - 1);
         const int x = __shfl_sync(0xffffffffu, pos, ahead ? 31 - __clz(ahead) : 0), to = ahead ? x : before;
@@ -504,7 +514,9 @@ __device__ __noinline__ bool all_between_seen(const Tokens k) {
         const int y = __shfl_sync(0xffffffffu, pos, there ? 31 - __clz(there) : 0);
         if (there) before = y;
     }
-    return !__any_sync(0xffffffffu, gaps);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    last = __reduce_max_sync(0xffffffffu, last);
+    return make_int2(!__any_sync(0xffffffffu, gaps) && lo == least && last == hi, last);
 }
 // Which of the four positions from `a` on (its own of each lane) some token in order sees,
 // as bits; [s_lo, s_hi) are the first ones.
@@ -525,12 +537,6 @@ __device__ __noinline__ uint32_t seen_token_by_token(const Tokens k, int s_lo, i
         }
     }
     return m;
-}
-
-// The row of a piece's last position, which may be read for positions that no row
-// sees; row 0 if that has none (no row sees anything then).
-__device__ __forceinline__ int32_t spare_row(const DevBatch &b, const Piece *pc) {
-    return pc->hi < 0 || pc->kv0 < 0 ? 0 : max(0, any_row(b, pc->seq, pc->kv0, pc->hi));
 }
 
 __device__ __forceinline__ bool Scheduler::write(const MlaParams &p, Ctl &ctl, int lane) {
@@ -871,9 +877,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!pc || pc->end) break;
             const int t1 = pc->t1, lo = pc->lo, hi = pc->hi, s_lo = pc->s_lo, s_hi = pc->s_hi;
             const Grid grid = pc->grid;
-            // The last token sees all back to its window's begin, the least one's sees from lo on.
-            const bool odd = lo < (int64_t)hi - p.pr.window + 1 && hi - pc->min_pos > p.pr.window && !all_between_seen(tokens_of(p.pr, pc));
-            int32_t spare = -1;                               // not looked up yet
+            // If the last position has a row, its token is in order and sees all back to its
+            // window's begin; that of the least one, as far back as the piece goes.
+            bool odd = false;                                 // otherwise: look at each token
+            const int32_t row_of_end = hi < 0 || pc->kv0 < 0 ? -1 : any_row(b, pc->seq, pc->kv0, lane & 1 ? pc->min_pos : hi);
+            const uint32_t ends = __ballot_sync(0xffffffffu, row_of_end >= 0);
+            int32_t spare = __shfl_sync(0xffffffffu, row_of_end, 0);
+            if (!(ends & 1u) || (lo < (int64_t)hi - p.pr.window + 1 && (!(ends & 2u) || hi - pc->min_pos > p.pr.window))) {
+                const int2 x = all_between_seen(tokens_of(p.pr, pc), pc->min_pos, hi);
+                odd = !x.x;
+                spare = x.y < 0 ? 0 : max(0, any_row(b, pc->seq, pc->kv0, x.y));
+            }
             for (int i = pc->t0; alive && i < t1; ++i, ++g) {
                 const uint32_t groups = tile_groups(*pc, grid, i);
                 // where a group's 16 rows lie together, lane j looks group j up; one that is
@@ -898,7 +912,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // the other groups' rows, four a lane
                 int4 r = make_int4(0, 0, 0, 0);
                 if (groups & ~ones) {
-                    if (spare < 0) spare = spare_row(b, pc);
                     const int a = grid.key(i, 4 * lane);
                     if (!odd) {
 #pragma unroll
