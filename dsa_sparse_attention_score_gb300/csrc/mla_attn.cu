@@ -1177,7 +1177,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     named_barrier(7, kSoftmaxWarps * 32);
                     const float mn = m_last[r];
                     auto &sums = ctl.red[last ^ 1];               // read by all of its group
-                    sums[group][half][r] = m_owed == -INFINITY ? 0.f : l_owed * ex2(m_owed - mn);
+                    // (not by the maximum: scores of NaN leave it at -infinity, but not the sum at 0)
+                    sums[group][half][r] = l_owed == 0.f ? 0.f : l_owed * ex2(m_owed - mn);
                     m_owed = mn;
                     named_barrier(7, kSoftmaxWarps * 32);
                     l_owed = (sums[0][0][r] + sums[0][1][r]) + (sums[1][0][r] + sums[1][1][r]);
