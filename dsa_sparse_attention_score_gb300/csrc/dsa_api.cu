@@ -1030,6 +1030,18 @@ static bool rows_apart(const void *x, int64_t xs, const void *y, int64_t ys, int
     return xs == ys && slices_apart((int64_t)(xb > yb ? xb - yb : yb - xb) / e, dim, n, xs, 1, 0);
 }
 
+// The same of an array of `bytes` that all rows read, whole before rows, behind them or
+// between two of them.
+static bool array_apart(const void *x, int64_t bytes, const void *y, int64_t ys, int64_t n, int64_t dim, int64_t e) {
+    if (!x || !y) return true;
+    const uintptr_t xb = reinterpret_cast<uintptr_t>(x), yb = reinterpret_cast<uintptr_t>(y);
+    if (xb + (uintptr_t)bytes <= yb) return true;
+    if (xb < yb) return false;
+    const uint64_t row = (uint64_t)(ys * e), i = (xb - yb) / row, col = (xb - yb) % row;   // at row i's column (in bytes)
+    if (i >= (uint64_t)n) return true;
+    return col >= (uint64_t)(dim * e) && (i + 1 == (uint64_t)n || col + (uint64_t)bytes <= row);
+}
+
 static dsa_status_t rms_norm_impl(NormLaunch a, cudaStream_t stream) {
     if (!a.x || !float_dtype(a.dtype) || a.n < 1 || a.dim < 1) return DSA_ERR_INVALID_ARGUMENT;
     if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return DSA_ERR_INVALID_ARGUMENT;
@@ -1044,11 +1056,14 @@ static dsa_status_t rms_norm_impl(NormLaunch a, cudaStream_t stream) {
         if (!aligned(r.p, (size_t)e)) return DSA_ERR_MISALIGNED;
     }
     if (!aligned(a.weight, a.weight_f32 ? 4 : (size_t)e)) return DSA_ERR_MISALIGNED;
-    // a row's sum and output are written after all of it has been read
+    const int64_t weight_bytes = (int64_t)a.dim * (a.weight_f32 ? 4 : e);
+    // a row's sum and output are written after all of it has been read; the weight is read
+    // all along
     for (const void *w : {static_cast<const void *>(a.sum), static_cast<const void *>(a.out)}) {
         const int64_t ws = w == a.sum ? a.sum_stride : a.out_stride;
         if (!rows_apart(a.x, a.x_stride, w, ws, a.n, a.dim, e, true) ||
-            !rows_apart(a.residual, a.residual_stride, w, ws, a.n, a.dim, e, true))
+            !rows_apart(a.residual, a.residual_stride, w, ws, a.n, a.dim, e, true) ||
+            !array_apart(a.weight, weight_bytes, w, ws, a.n, a.dim, e))
             return DSA_ERR_INVALID_ARGUMENT;
     }
     if (!rows_apart(a.sum, a.sum_stride, a.out, a.out_stride, a.n, a.dim, e, false)) return DSA_ERR_INVALID_ARGUMENT;
@@ -1058,7 +1073,9 @@ static dsa_status_t rms_norm_impl(NormLaunch a, cudaStream_t stream) {
             const uint64_t bytes = ((uint64_t)(a.n - 1) * *r.s + a.dim) * e;
             if (!apart(r.p, bytes, a.codes, code_bytes) || !apart(r.p, bytes, a.scale, scale_bytes)) return DSA_ERR_INVALID_ARGUMENT;
         }
-        if (!apart(a.codes, code_bytes, a.scale, scale_bytes)) return DSA_ERR_INVALID_ARGUMENT;
+        if (!apart(a.codes, code_bytes, a.scale, scale_bytes) || !apart(a.weight, weight_bytes, a.codes, code_bytes) ||
+            !apart(a.weight, weight_bytes, a.scale, scale_bytes))
+            return DSA_ERR_INVALID_ARGUMENT;
     }
     DSA_TRY_CUDA(launch_rms_norm(a, stream));
     return DSA_OK;

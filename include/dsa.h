@@ -550,9 +550,9 @@ dsa_status_t dsa_sparse_mla_attn_q8(const dsa_bf16 *q_lat, const dsa_bf16 *q_rop
  *   codes        uint8 [n_tokens, dim], 16-byte aligned; scale float32
  *                [n_tokens, dim / group], group 32, 64, 128 or dim
  * out and sum may be x or residual with the same strides, but not each other;
- * otherwise rows written must not share values with others, except as column
- * slices of wider rows; codes and scale share no byte with anything.  h^2 has to stay finite in float32 (and eps > 0 where all
- * of a row may be 0).  No workspace.
+ * otherwise rows written must not share values with others or with weight, except as
+ * column slices of wider rows; codes and scale share no byte with anything.  h^2 has
+ * to stay finite in float32 (and eps > 0 where all of a row may be 0).  No workspace.
  * Errors: DSA_ERR_INVALID_ARGUMENT for null pointers, sizes below 1, a negative or
  * not finite eps, strides outside the above, rows that overlap, dim not a multiple
  * of group; DSA_ERR_UNSUPPORTED for dim > 16384, and with codes for dim not a
