@@ -102,8 +102,8 @@ template <typename Op, typename V> __device__ __forceinline__ V row_reduce(V v, 
 template <typename T, int W, int V, bool kAligned, bool kCodes>
 __global__ void __maxnreg__(kCodes ? 40 : 64) rms_norm_kernel(const NormParams p) {
     __shared__ uint32_t sh[32];
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
-    const bool live = row < p.n;
+    const uint32_t row = blockIdx.x * blockDim.y + threadIdx.y;   // up to 3 behind 2^31 - 1 rows
+    const bool live = row < (uint32_t)p.n;
     const int tx = threadIdx.x, step = blockDim.x;
     const T *x = static_cast<const T *>(p.x) + row * p.xs;
     pdl_wait();
@@ -240,7 +240,7 @@ template <typename T, int W, int V, bool kAligned, bool kCodes>
 cudaError_t launch_norm_as(const NormParams &p, cudaStream_t stream) {
     const int units = (p.dim + W - 1) / W;
     const int threads = std::max(32, ((units + V - 1) / V + 31) / 32 * 32), rows = std::max(1, 128 / threads);
-    return launch_k(rms_norm_kernel<T, W, V, kAligned, kCodes>, dim3((unsigned)((p.n + rows - 1) / rows)),
+    return launch_k(rms_norm_kernel<T, W, V, kAligned, kCodes>, dim3((unsigned)(((int64_t)p.n + rows - 1) / rows)),
                     dim3((unsigned)threads, (unsigned)rows), 0, stream, true, p);
 }
 
