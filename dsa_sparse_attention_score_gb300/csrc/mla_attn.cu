@@ -28,14 +28,16 @@
 // and values in halves of a tile, each as soon as the product that read it is done.
 // Warps 0-7 are softmax and output, in two groups that take the tiles in turn; one
 // warp each issues S's and O's products and copies keys and values.
-// Measured: 2048 tokens of 64 heads after 6144 positions 1.26 ms in a row of calls
-// (1.62 PFLOP/s, 95% of the sustained rate of the card's library products; the power
-// cap holds the clock at 1.6 GHz, one kernel at 2.07 GHz takes 1.09 ms): 2450 clocks a
-// tile, the tensor pipe 85% busy.  32 sequences of 4k-64k positions, 128 heads, one
-// token each 0.26 ms (5.0 TB/s: 3700 clocks a tile; HBM delivers one in 2800).  8 of
-// 8192, 64 heads 31 us (HBM's share is 11: the first S comes 6 us after the launch, the
-// output of the last piece takes 2.5 and the join 5).  What bounds calls of many short
-// items is the change of pieces, 7000 clocks in which the tensor core waits for an output.
+// Measured: 2048 tokens of 64 heads after 6144 positions 1.23 to 1.29 ms in a row of
+// calls (1.58 to 1.66 PFLOP/s, 92 to 97% of the sustained rate of the card's library
+// products; the power cap holds the clock at 1.6 GHz.  One launch under a profiler took
+// 1.09 to 1.15 ms at 1.9 to 1.8 GHz): 2.06 million clocks, 2710 a tile with changes of
+// pieces, begin and end, 2450 between two tiles of an item; the tensor pipe 85% busy.
+// 32 sequences of 4k-64k positions, 128 heads, one token each 0.25 to 0.27 ms (4.8 to
+// 5.2 TB/s: 3700 clocks a tile; HBM delivers one in 2800).  8 of 8192, 64 heads 31 us
+// (HBM's share is 11: the first S comes 6 us after the launch, the output of the last
+// piece takes 2.5 and the join 5).  What bounds calls of many short items is the change
+// of pieces, 7000 clocks in which the tensor core waits for an output.
 //
 // The work is cut by tiles, not by items: the tiles of all items in a row are
 // divided evenly among the clusters.  An item that several clusters share gets
@@ -473,7 +475,9 @@ struct Scheduler {
 // Of rows that no token sees not even 0 times a value may come into a product, and their
 // blocks need not be there.  The tokens of a piece see all positions between its first
 // and its last one, unless some are not in order or their windows do not meet.  Those
-// rare pieces are looked at token by token, out of the usual path.  (Parameters by value:
+// rare pieces are looked at token by token, out of the usual path, over all tiles between
+// their first and last position.  That this is looked up costs chunks over pages of 16
+// rows 3% (247 -> 254 us), other calls nothing that is measured.  (Parameters by value:
 // behind a reference they are loaded through generic addresses.)
 struct Tokens {
     const int32_t *q_pos, *table;   // of the piece's first token; the sequence's blocks (null: contiguous)
@@ -1336,7 +1340,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint64_t sum = f2(0.f, 0.f);
                 if (alive) {
                     // P in pairs of bf16 over the first half of S's own columns, until
-                    // its place in shared memory is free
+                    // its place in shared memory is free.  bf16, the values' type, is what
+                    // one product takes: P is off by up to 2^-8 of itself, outputs by 0.001
+                    // of their size (the sum is of P before it).  A second product of the
+                    // remainders would take O's clocks again, and their place in shared
+                    // memory is not there.
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         uint32_t u[32], w[16];

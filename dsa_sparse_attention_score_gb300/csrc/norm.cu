@@ -4,8 +4,9 @@
 //     y = h / sqrt(mean(h^2) + eps) * weight,
 //     scale = max(max |y| / 448, 2^-40),  code = e4m3(y / scale)  per group.
 //
-// Bound by HBM: a row's values are read once, kept in registers over the one
-// reduction that the row needs, and written once.  A row belongs to a run of
+// Bound by HBM, and with codes by instructions (8191 rows of 4096 fp16 values: 70% of what
+// an SM issues, DRAM at 51%): a row's values are read once, kept in registers over the
+// one reduction that the row needs, and written once.  A row belongs to a run of
 // threads of one CTA (several short rows share a CTA), each of which holds V
 // units of W values; a unit is 16 bytes where the rows allow it.  Measured on
 // GB300, 16,384 rows of 7168 bf16 values with residual and sum (939 MB): two units
@@ -13,7 +14,10 @@
 // in turn with the next one's loads ahead 216 (registers).  8191 rows of 4096 fp16
 // values to codes (236 MB): 48 us with 40 registers a thread and the weights loaded
 // behind the reduction (54 with 60 registers: fewer threads an SM; plain outputs
-// lose by it, 158 -> 167 us).
+// lose by it, 158 -> 167 us).  At 40 the forms of two units and more spill (fp16 40
+// bytes a thread, bf16 56, float32 132, rows that are not aligned 20 to 124): bf16 takes 55 us for
+// the same rows, float32 83.  Without a residual, at 3 bytes a value instead of 7, fp16
+// takes 40 us, bf16 44.
 #include <algorithm>
 
 #include "dsa_common.cuh"

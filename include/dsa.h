@@ -583,13 +583,14 @@ dsa_status_t dsa_rms_norm_q8(const void *x, int64_t x_stride, const void *residu
  *              neither shares a byte with the other or with an input
  *   ws         dsa_workspace_size(DSA_OP_MLA_ATTN, batch, 1, H, 1)
  * Operands are bf16, sums and the softmax float32; probabilities enter the value
- * product as bf16.  Rows whose positions are divided among several parts of the GPU
- * are joined from float32 parts (float32 out) or fp16 ones with a power of two for 32
- * dims (bf16 out).  The results of a call do not change from run to run.
- * Cache rows that no token of the call sees may hold anything.  A query row
- * that holds NaN gives NaN in its own outputs and lse alone.  Values of a cache row that
- * some token sees have to be finite: others may reach the outputs of all tokens of its
- * sequence, also of those that do not see the row.
+ * product as bf16, so that a float32 output too is off by about 0.001 of its size.
+ * Rows whose positions are divided among several parts of the GPU are joined from
+ * float32 parts (float32 out) or fp16 ones with a power of two for 32 dims (bf16 out).
+ * The results of a call do not change from run to run.
+ * Cache rows that no token of the call sees may hold anything.  A query row that holds
+ * NaN gives NaN in its own outputs and lse alone.  Values of a cache row that some token
+ * sees have to be finite: others may reach the outputs of all tokens of its sequence,
+ * also of those that do not see the row.
  * A token at position -1 is padding: out = 0, lse = -INFINITY.  One at any other
  * position out of bounds, or in an unmapped block, gets the same and is flagged
  * DSA_DEV_BAD_POSITION.  A visible position in an unmapped block is flagged
