@@ -304,7 +304,8 @@ struct MlaParams {
     Split *split;                 // [clusters]
     // Parts of items, unnormalised: float32 [2 * clusters, 128, 512] with float32 outputs;
     // with bf16 ones fp16, 32 dims of a row times a power of two (part_unit holds
-    // 1 over it): 11 bits, which the output's own 8 hide, at half the bytes.
+    // 1 over it): 11 bits, which the output's own 8 hide, at half the bytes, for dims
+    // down to 2^-29 of the largest of the 32.
     void *part_o;
     float *part_unit;             // [2 * clusters, 128, 16]
     float *part_ml;               // [2 * clusters, 128, 2]
@@ -1221,8 +1222,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 float top = 0.f;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(o[e])));
-                                const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
-                                const float unit = __int_as_float((127 - ex) << 23);      // values below 2 after it
+                                // values below 2^15 after it: those down to 2^-29 of the largest keep 11 bits
+                                const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -112), 127) - 14;
+                                const float unit = __int_as_float((127 - ex) << 23);
                                 if (mine) p.part_unit[part_row * 16 + ((col0 + c) >> 5)] = __int_as_float((127 + ex) << 23);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
