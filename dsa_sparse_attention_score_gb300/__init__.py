@@ -810,6 +810,8 @@ def dsa_mla_attn_window(q_lat, q_rope, kv_cache, batch: Batch, window: int, n_si
     a, z = _mla_args(q_lat, q_rope, kv_cache, batch, out, lse, ws, block_table, block_size, dev)
     if sink_pos0 is not None:
         _shaped(sink_pos0, "sink_pos0", _t_i32, (batch.B,), dev)
+    # beyond 32 bits: as many as there are, or refused
+    window, n_sink = max(-1, min(window, 2 ** 31 - 1)), max(-1, min(n_sink, 2 ** 31 - 1))
     _call("dsa_mla_attn_window", dev, stream, lib().dsa_mla_attn_window, *a, window, n_sink,
           sink_pos0.data_ptr() if sink_pos0 is not None else None, sm_scale, *z)
 
